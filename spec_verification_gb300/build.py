@@ -18,7 +18,8 @@ INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 LIB = BUILD / "libss.so"
 SOURCES = ["ss_api.cu", "ss_stage1.cu", "ss_stage1_f32.cu", "ss_stage1_bf16.cu", "ss_stage1_exact.cu",
-           "ss_stage2.cu", "ss_residual.cu", "ss_noalloc.cu"]
+           "ss_stage2.cu", "ss_residual.cu", "ss_noalloc.cu", "ss_kv_api.cu", "ss_kv_pages.cu", "ss_kv_rope.cu",
+           "ss_kv_attend_bf16.cu", "ss_kv_attend_f16.cu", "ss_kv_attend_bf16_e4m3.cu", "ss_kv_attend_f16_e4m3.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -41,7 +42,7 @@ def flags() -> list:
 def _stale(obj: Path, src: Path) -> bool:
     if not obj.exists():
         return True
-    deps = [src, INCLUDE / "ss.h", CSRC / "ss_common.cuh", CSRC / "ss_stage1.cuh", CSRC / "ss_stage2.cuh", Path(__file__)]
+    deps = [src, *INCLUDE.glob("*.h"), *CSRC.glob("*.cuh"), Path(__file__)]
     return any(d.exists() and d.stat().st_mtime > obj.stat().st_mtime for d in deps)
 
 
