@@ -27,23 +27,24 @@ namespace {
 
 constexpr int kNT = 256;
 
-__device__ __forceinline__ void unpack(uint32_t w, float& a, float& b, __nv_bfloat16) {
-  a = __uint_as_float(w << 16);
-  b = __uint_as_float(w & 0xffff0000u);
-}
-__device__ __forceinline__ void unpack(uint32_t w, float& a, float& b, __half) {
-  const float2 f = __half22float2(*reinterpret_cast<__half2*>(&w));
-  a = f.x;
-  b = f.y;
-}
-__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
+template <class T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 of(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+  static __device__ __forceinline__ uint32_t to(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+template <>
+struct Pair<__half> {
+  static __device__ __forceinline__ float2 of(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+  static __device__ __forceinline__ uint32_t to(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
 
 // (cos, sin) of position * f radians.  f = m64 * 2^(e - 63) with m64 its
 // mantissa at the top of 64 bits; f / (2 pi) * 2^64 = (m64 * K >> 64) * 2^(e + 1),
@@ -89,174 +90,219 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | hi << 16;
 }
 
-// A CTA takes TB tokens (blockIdx.x) and every gridDim.y-th item (a head of q,
-// k or v) of them; D / 8 lanes work on one head, eight values each.
-template <class T, bool E4M3, int D, int TB>
-__global__ void __launch_bounds__(kNT) rope_kernel(const RopeParams P) {
+// Eight values of a head that one thread holds: four pairs (a, b).
+struct Eight {
+  float a[4], b[4];
+};
+// Where they are in the head: values at, at + 1, .. at + 3 and then, .., then + 3.  "half" pairs: the first four are
+// a, the others b.  Otherwise (interleaved pairs, values past the rotated ones) then = at + 4, and neighbours pair.
+template <class T>
+__device__ __forceinline__ Eight spread(const uint2 lo, const uint2 hi, bool halves) {
+  const float2 p = Pair<T>::of(lo.x), q = Pair<T>::of(lo.y), r = Pair<T>::of(hi.x), s = Pair<T>::of(hi.y);
+  return halves ? Eight{{p.x, p.y, q.x, q.y}, {r.x, r.y, s.x, s.y}} : Eight{{p.x, q.x, r.x, s.x}, {p.y, q.y, r.y, s.y}};
+}
+__device__ __forceinline__ void gathered(const Eight& e, bool halves, float (&y)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[halves ? i : 2 * i] = e.a[i];
+    y[halves ? 4 + i : 2 * i + 1] = e.b[i];
+  }
+}
+
+// A CTA takes TB tokens (blockIdx.x) and every gridDim.y-th group of their heads; D / 8 lanes work on one head.  A
+// thread holds both values of each of its pairs, so no lane needs another's; cos and sin of its four pairs are in
+// registers, multiplied with the norm's weights, and a head costs two 8-byte loads, its sum of squares over the
+// lanes, 24 multiplications and additions, and two stores.
+// `Order` says what is known of the pairs at compile time: kNeighbours in every lane, kHalves in every lane (all of
+// the head is rotated), or kMixed ("half" pairs in the first lanes).
+enum Order { kNeighbours, kHalves, kMixed };
+template <class T, bool E4M3, int D, int TB, Order kOrder>
+__global__ void __launch_bounds__(kNT, 4) rope_kernel(const RopeParams P) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kNT / kLanes / TB;  // heads of one token at a time
-  constexpr int kAhead = 2;                   // heads whose loads are in flight together
+  constexpr int kAhead = TB > 1 ? 2 : 1;      // heads to a batch; the next batch's loads are in flight over a batch
   __shared__ float2 turns[TB][D / 2];
   const int tid = threadIdx.x, lane = tid % kLanes, group = tid / kLanes;
-  const int tl = group % TB, g = group / TB;
-  const int t0 = blockIdx.x * TB;
+  const int tl = group % TB;
+  const int t0 = blockIdx.x * TB, t = min(t0 + tl, P.T - 1);
+  const bool live = t0 + tl < P.T;
   const int half = P.rot >> 1;
+  const bool turned = kOrder == kHalves || lane * 8 < P.rot;
+  const bool halves = kOrder == kHalves || (kOrder == kMixed && turned);
+  const int at = halves ? lane * 4 : lane * 8, then = halves ? half + lane * 4 : at + 4;
+  const int h0 = blockIdx.y * kGroups + group / TB, step = kGroups * gridDim.y;
+
+  // batches of heads: those of q, then those of k, the same number in every lane
+  const int nq = (P.hq + step * kAhead - 1) / (step * kAhead), nk = (P.hkv + step * kAhead - 1) / (step * kAhead);
+  struct Raw {
+    uint2 lo[kAhead], hi[kAhead];
+  };
+  auto load = [&](int b, Raw& r) {
+    const bool is_q = b < nq;
+    const T* src = is_q ? static_cast<const T*>(P.q) + t * P.q_stride : static_cast<const T*>(P.k) + t * P.k_stride;
+    const int first = h0 + (is_q ? b : b - nq) * step * kAhead, last = (is_q ? P.hq : P.hkv) - 1;
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      const T* p = src + min(first + n * step, last) * D;
+      r.lo[n] = __ldcs(reinterpret_cast<const uint2*>(p + at));
+      r.hi[n] = __ldcs(reinterpret_cast<const uint2*>(p + then));
+    }
+  };
+  Raw raw;
+  load(0, raw);
+
   for (int i = tid; i < TB * half; i += kNT) {
-    const int t = i / half, f = i - t * half;
-    if (t0 + t < P.T) {
-      const float2 cs = turn_of(P.inv_freq[f], P.positions[t0 + t]);
-      turns[t][f] = make_float2(cs.x * P.rope_scale, cs.y * P.rope_scale);
+    const int n = i / half, f = i - n * half;
+    if (t0 + n < P.T) {
+      const float2 cs = turn_of(P.inv_freq[f], P.positions[t0 + n]);
+      turns[n][f] = make_float2(cs.x * P.rope_scale, cs.y * P.rope_scale);
     }
   }
-  const int t = t0 + tl;
-  const bool live = t < P.T;
-  long long place = -1;
-  if (live) {
-    const int slot = P.slots[t];
-    if (slot >= 0 && slot < P.num_slots)
-      place = (long long)(slot >> P.page_shift) * P.page_stride + (long long)(slot & ((1 << P.page_shift) - 1)) * P.token_stride;
-  }
+  const int slot = live ? P.slots[t] : -1;
+  const long long place = (long long)(slot >> P.page_shift) * P.page_stride + (long long)(slot & ((1 << P.page_shift) - 1)) * P.token_stride;
+  const bool stored = slot >= 0 && slot < P.num_slots;
   __syncthreads();
 
-  // this thread's values: 8 * lane .. 8 * lane + 7; their partners are inside ("interleaved") or in another lane
-  const int at = lane * 8;
-  const bool turned = at < P.rot;
-  float c[8], s[8];
+  // batches [b0, b1), the heads of one of q and k: norm, rotation, then `put`
+  auto rotate = [&](int b0, int b1, int heads, const void* weight, auto put) {
+    Eight w = {{1.0f, 1.0f, 1.0f, 1.0f}, {1.0f, 1.0f, 1.0f, 1.0f}};
+    if (weight != nullptr) {
+      const T* p = static_cast<const T*>(weight);
+      w = spread<T>(*reinterpret_cast<const uint2*>(p + at), *reinterpret_cast<const uint2*>(p + then), halves);
+    }
+    Eight cw, sw;  // a -> a cw.a - b sw.b, b -> b cw.b + a sw.a
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c[i] = 1.0f;
-    s[i] = 0.0f;
-  }
-  if (turned && live) {
-    if (P.interleaved) {
+    for (int i = 0; i < 4; ++i) {
+      const float2 cs = turned ? turns[tl][lane * 4 + i] : make_float2(1.0f, 0.0f);
+      cw.a[i] = cs.x * w.a[i];
+      cw.b[i] = cs.x * w.b[i];
+      sw.a[i] = cs.y * w.a[i];
+      sw.b[i] = cs.y * w.b[i];
+    }
+    for (int b = b0; b < b1; ++b) {
+      const Raw now = raw;
+      if (b + 1 < nq + nk) load(b + 1, raw);
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) {
+        const int h = h0 + ((b - b0) * kAhead + n) * step;
+        const Eight x = spread<T>(now.lo[n], now.hi[n], halves);
+        float r = 1.0f;
+        if (weight != nullptr) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum = fmaf(x.a[i], x.a[i], fmaf(x.b[i], x.b[i], sum));
+#pragma unroll
+          for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          const float m = fmaf(sum, 1.0f / D, P.eps);
+          r = rsqrtf(m);
+          r = fmaf(r * fmaf(-m * r, r, 1.0f), 0.5f, r);  // a Newton step: to about a rounding
+        }
+        Eight y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y.a[i] = fmaf(x.a[i], cw.a[i], -x.b[i] * sw.b[i]) * r;
+          y.b[i] = fmaf(x.b[i], cw.b[i], x.a[i] * sw.a[i]) * r;
+        }
+        if (!turned) {  // nothing of a neighbour may reach these (sw is 0, but 0 * infinity is not)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y.a[i] = x.a[i] * cw.a[i] * r;
+            y.b[i] = x.b[i] * cw.b[i] * r;
+          }
+        }
+        if (h < heads) put(h, y);
+      }
+    }
+  };
+  auto pack = [&](const float (&y)[8], uint2& lo, uint2& hi) {
+    lo = make_uint2(Pair<T>::to(y[0], y[1]), Pair<T>::to(y[2], y[3]));
+    hi = make_uint2(Pair<T>::to(y[4], y[5]), Pair<T>::to(y[6], y[7]));
+  };
+  // y[0..3] at `at`, y[4..7] at `then` of a head of the cache, divided by the head's factor
+  auto hold = [&](void* cache, const float* scales, int h, float (&y)[8]) {
+    const long long off = place + h * P.head_stride;
+    if (E4M3) {
+      if (scales != nullptr) {
+        const float sc = scales[h], inv = 1.0f / sc;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = divide(y[i], sc, inv);
+      }
+      unsigned char* p = static_cast<unsigned char*>(cache) + off;
+      *reinterpret_cast<uint32_t*>(p + at) = e4m3x4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint32_t*>(p + then) = e4m3x4(y[4], y[5], y[6], y[7]);
+    } else {
+      T* p = static_cast<T*>(cache) + off;
+      uint2 lo, hi;
+      pack(y, lo, hi);
+      *reinterpret_cast<uint2*>(p + at) = lo;
+      *reinterpret_cast<uint2*>(p + then) = hi;
+    }
+  };
+
+  rotate(0, nq, P.hq, P.qw, [&](int h, const Eight& e) {
+    if (!live) return;
+    float y[8];
+    gathered(e, halves, y);
+    uint2 lo, hi;
+    pack(y, lo, hi);
+    T* p = static_cast<T*>(P.q_out) + t * P.qo_stride + h * D;
+    *reinterpret_cast<uint2*>(p + at) = lo;
+    *reinterpret_cast<uint2*>(p + then) = hi;
+  });
+  rotate(nq, nq + nk, P.hkv, P.kw, [&](int h, const Eight& e) {
+    if (!stored) return;
+    float y[8];
+    gathered(e, halves, y);
+    hold(P.k_cache, P.k_scale, h, y);
+  });
+  if (!stored) return;
+  const T* v = static_cast<const T*>(P.v) + t * P.v_stride + lane * 8;
+  for (int h = h0; h < P.hkv; h += step) {
+    const uint4 x = __ldcs(reinterpret_cast<const uint4*>(v + h * D));
+    const long long off = place + h * P.head_stride + lane * 8;
+    if (E4M3) {
+      const float sc = P.v_scale ? P.v_scale[h] : 1.0f, inv = 1.0f / sc;
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      float y[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 cs = turns[tl][at / 2 + i];
-        c[2 * i] = c[2 * i + 1] = cs.x;
-        s[2 * i] = -cs.y;
-        s[2 * i + 1] = cs.y;
+        const float2 f = Pair<T>::of(w[i]);
+        y[2 * i] = divide(f.x, sc, inv);
+        y[2 * i + 1] = divide(f.y, sc, inv);
       }
+      *reinterpret_cast<uint2*>(static_cast<unsigned char*>(P.v_cache) + off) =
+          make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
     } else {
-      const bool low = at < half;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 cs = turns[tl][(low ? at : at - half) + i];
-        c[i] = cs.x;
-        s[i] = low ? -cs.y : cs.y;
-      }
-    }
-  }
-  // lane that holds this thread's partners ("half" pairs)
-  const int apart = P.rot >> 4;
-  const int partner = (tid & 31) - lane + (turned ? (at < half ? lane + apart : lane - apart) : lane);
-
-  const int heads = P.hq + 2 * P.hkv;
-  const int step = kGroups * gridDim.y;
-  const int rounds = (heads + step - 1) / step;
-  for (int r0 = 0; r0 < rounds; r0 += kAhead) {
-    uint4 raw[kAhead];
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int h = (r0 + a) * step + blockIdx.y * kGroups + g;
-      raw[a] = make_uint4(0u, 0u, 0u, 0u);
-      if (live && h < heads) {
-        const T* src = h < P.hq ? static_cast<const T*>(P.q) + t * P.q_stride + h * D
-                       : h < P.hq + P.hkv ? static_cast<const T*>(P.k) + t * P.k_stride + (h - P.hq) * D
-                                          : static_cast<const T*>(P.v) + t * P.v_stride + (h - P.hq - P.hkv) * D;
-        raw[a] = *reinterpret_cast<const uint4*>(src + at);
-      }
-    }
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int h = (r0 + a) * step + blockIdx.y * kGroups + g;
-      const bool is_q = h < P.hq, is_v = h >= P.hq + P.hkv;
-      float x[8];
-      unpack(raw[a].x, x[0], x[1], T());
-      unpack(raw[a].y, x[2], x[3], T());
-      unpack(raw[a].z, x[4], x[5], T());
-      unpack(raw[a].w, x[6], x[7], T());
-      const void* weight = is_q ? P.qw : P.kw;
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
-#pragma unroll
-      for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (weight != nullptr && !is_v) {
-        const float r = 1.0f / sqrtf(sum * (1.0f / D) + P.eps);
-        const uint4 wr = *reinterpret_cast<const uint4*>(static_cast<const T*>(weight) + at);
-        float w[8];
-        unpack(wr.x, w[0], w[1], T());
-        unpack(wr.y, w[2], w[3], T());
-        unpack(wr.z, w[4], w[5], T());
-        unpack(wr.w, w[6], w[7], T());
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-      }
-      float y[8];
-      if (P.interleaved) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i ^ 1], s[i], x[i] * c[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fmaf(__shfl_sync(0xffffffffu, x[i], partner), s[i], x[i] * c[i]);
-      }
-      if (!turned || is_v) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i];
-      }
-      if (!live || h >= heads) continue;
-      if (is_q) {
-        uint4 o;
-        o.x = pack2(y[0], y[1], T());
-        o.y = pack2(y[2], y[3], T());
-        o.z = pack2(y[4], y[5], T());
-        o.w = pack2(y[6], y[7], T());
-        *reinterpret_cast<uint4*>(static_cast<T*>(P.q_out) + t * P.qo_stride + h * D + at) = o;
-      } else if (place >= 0) {
-        const int kh = is_v ? h - P.hq - P.hkv : h - P.hq;
-        const long long off = place + kh * P.head_stride + at;
-        void* cache = is_v ? P.v_cache : P.k_cache;
-        if (E4M3) {
-          const float* scales = is_v ? P.v_scale : P.k_scale;
-          if (scales != nullptr) {
-            const float sc = scales[kh], inv = 1.0f / sc;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = divide(y[i], sc, inv);
-          }
-          *reinterpret_cast<uint2*>(static_cast<unsigned char*>(cache) + off) =
-              make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
-        } else {
-          uint4 o;
-          o.x = is_v ? raw[a].x : pack2(y[0], y[1], T());
-          o.y = is_v ? raw[a].y : pack2(y[2], y[3], T());
-          o.z = is_v ? raw[a].z : pack2(y[4], y[5], T());
-          o.w = is_v ? raw[a].w : pack2(y[6], y[7], T());
-          *reinterpret_cast<uint4*>(static_cast<T*>(cache) + off) = o;
-        }
-      }
+      *reinterpret_cast<uint4*>(static_cast<T*>(P.v_cache) + off) = x;
     }
   }
 }
 
-template <class T, bool E4M3, int D>
+template <class T, bool E4M3, int D, Order kOrder>
 cudaError_t launch(const RopeParams& P, int sms, cudaStream_t st) {
   constexpr int kTokens = 4;
-  const int heads = P.hq + 2 * P.hkv;
-  if (P.T >= 4 * sms * kTokens) {
-    rope_kernel<T, E4M3, D, kTokens><<<dim3((P.T + kTokens - 1) / kTokens, 1), kNT, 0, st>>>(P);
+  const int heads = std::max(P.hq, P.hkv);
+  if (P.T >= 2 * sms) {
+    rope_kernel<T, E4M3, D, kTokens, kOrder><<<dim3((P.T + kTokens - 1) / kTokens, 1), kNT, 0, st>>>(P);
   } else {
     // few tokens: one a CTA, and its heads over several CTAs until the GPU has about two CTAs an SM
     const int per = kNT / (D / 8);
     const int most = (heads + per - 1) / per;
     const int split = std::min(most, std::max(1, 2 * sms / P.T));
-    rope_kernel<T, E4M3, D, 1><<<dim3(P.T, split), kNT, 0, st>>>(P);
+    rope_kernel<T, E4M3, D, 1, kOrder><<<dim3(P.T, split), kNT, 0, st>>>(P);
   }
   return cudaGetLastError();
 }
 
+template <class T, bool E4M3, int D>
+cudaError_t by_order(const RopeParams& P, int sms, cudaStream_t st) {
+  if (P.interleaved || P.rot == 0) return launch<T, E4M3, D, kNeighbours>(P, sms, st);
+  return P.rot == D ? launch<T, E4M3, D, kHalves>(P, sms, st) : launch<T, E4M3, D, kMixed>(P, sms, st);
+}
+
 template <class T, bool E4M3>
 cudaError_t by_dim(const RopeParams& P, int d, int sms, cudaStream_t st) {
-  return d == 64 ? launch<T, E4M3, 64>(P, sms, st) : d == 128 ? launch<T, E4M3, 128>(P, sms, st) : launch<T, E4M3, 256>(P, sms, st);
+  return d == 64 ? by_order<T, E4M3, 64>(P, sms, st) : d == 128 ? by_order<T, E4M3, 128>(P, sms, st) : by_order<T, E4M3, 256>(P, sms, st);
 }
 
 }  // namespace

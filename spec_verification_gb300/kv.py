@@ -7,6 +7,7 @@ from __future__ import annotations
 import ctypes as C
 
 import numpy as np
+import torch
 
 from . import native
 
@@ -14,6 +15,8 @@ SS_F16, SS_E4M3 = 2, 3
 DTYPES = {"bf16": native.SS_BF16, "f16": SS_F16, "e4m3": SS_E4M3}
 # row status bits (beside those of native.py)
 ST_KV_POOL, ST_KV_TABLE, ST_KV_PAGE = 1 << 11, 1 << 12, 1 << 13
+
+_TORCH = {"bf16": torch.bfloat16, "f16": torch.float16, "e4m3": torch.float8_e4m3fn}
 
 _p, _i32, _i64, _f32 = C.c_void_p, C.c_int32, C.c_int64, C.c_float
 
@@ -63,6 +66,7 @@ def library() -> C.CDLL:
     L.ss_kv_plan_destroy.restype = None
     L.ss_kv_workspace_bytes.argtypes = [_p]
     L.ss_kv_workspace_bytes.restype = C.c_size_t
+    # a struct may be passed where its pointer is wanted: ctypes takes its address
     L.ss_kv_append.argtypes = [C.POINTER(Pool), _p, _p, _p, _p, _p]
     L.ss_kv_commit.argtypes = [C.POINTER(Pool), _p, _p, _i32, _p]
     L.ss_rope_store.argtypes = [C.POINTER(RopeBatch), C.POINTER(Cache)]
@@ -88,7 +92,9 @@ class Plan:
         self.handle = self._p.value
         self.page_size, self.num_pages, self.max_blocks = page_size, num_pages, max_blocks
         self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
-        self.dtype, self.cache_dtype = dtype, cache_dtype or dtype
+        self.dtype, self.cache_dtype, self.device = dtype, cache_dtype or dtype, device
+        self.type, self.cache_type = _TORCH[self.dtype], _TORCH[self.cache_dtype]
+        self.cache_shape = torch.Size((num_pages, page_size, kv_heads, head_dim))
         self.workspace_bytes = L.ss_kv_workspace_bytes(self._p)
 
     def __del__(self):
@@ -100,77 +106,94 @@ class Plan:
             pass
 
 
+# The calls below are made once per layer and step, so their host time counts: element types are compared as objects,
+# structs are filled by position, and the current stream is asked for by its raw handle.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, plan):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(plan.device)
+    return torch.cuda.current_stream(plan.device).cuda_stream
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _check_type(name, t, dtype):
-    """Tensors whose element type the library could not see for itself."""
-    got = str(t.dtype)
-    want = {"bf16": "torch.bfloat16", "f16": "torch.float16", "e4m3": "torch.float8_e4m3fn", "i32": "torch.int32",
-            "f32": "torch.float32", "f64": "torch.float64"}[dtype]
-    if got != want:
-        raise native.SSError(-1, f"{name} must be {want}, got {got}")
+def _bad(msg):
+    return native.SSError(-1, msg)
+
+
+def _type(name, t, want):
+    if t.dtype is not want:
+        raise _bad(f"{name} must be {want}, got {t.dtype}")
 
 
 def _cache(plan, k_cache, v_cache, k_scale, v_scale):
     """k_cache and v_cache seen as [pages, page_size, kv_heads, head_dim], in any memory order of the first three."""
-    want = (plan.num_pages, plan.page_size, plan.kv_heads, plan.head_dim)
-    if k_cache.shape != want or v_cache.shape != want:
-        raise native.SSError(-1, f"caches must be seen as [pages, page_size, kv_heads, head_dim] = {list(want)}, got "
-                                 f"{list(k_cache.shape)} and {list(v_cache.shape)}")
+    if k_cache.shape != plan.cache_shape or v_cache.shape != plan.cache_shape:
+        raise _bad(f"caches must be seen as [pages, page_size, kv_heads, head_dim] = {list(plan.cache_shape)}, got "
+                   f"{list(k_cache.shape)} and {list(v_cache.shape)}")
+    if k_cache.dtype is not plan.cache_type or v_cache.dtype is not plan.cache_type:
+        raise _bad(f"caches must be {plan.cache_type}, got {k_cache.dtype} and {v_cache.dtype}")
     st = k_cache.stride()
     if st != v_cache.stride() or st[3] != 1:
-        raise native.SSError(-1, "both caches must have the same strides, and a head's values must be contiguous")
-    _check_type("k_cache", k_cache, plan.cache_dtype)
-    _check_type("v_cache", v_cache, plan.cache_dtype)
+        raise _bad("both caches must have the same strides, and a head's values must be contiguous")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is not None and (t.dtype is not torch.float32 or t.numel() != plan.kv_heads or not t.is_contiguous()):
+            raise _bad(f"{name} must be {plan.kv_heads} contiguous float32 values")
     return Cache(k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], _ptr(k_scale), _ptr(v_scale))
 
 
 def _tokens(name, t, heads, plan):
     """[tokens, heads, head_dim] with contiguous heads -> stride between tokens."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != plan.head_dim or t.stride(2) != 1 or \
-            (heads > 1 and t.stride(1) != plan.head_dim):
-        raise native.SSError(-1, f"{name} must be [tokens, {heads}, {plan.head_dim}] with contiguous heads, got "
-                                 f"{list(t.shape)} with strides {list(t.stride())}")
-    _check_type(name, t, plan.dtype)
-    return t.stride(0) if t.shape[0] > 1 else heads * plan.head_dim
+    shape, st, d = t.shape, t.stride(), plan.head_dim
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or st[2] != 1 or (heads > 1 and st[1] != d):
+        raise _bad(f"{name} must be [tokens, {heads}, {d}] with contiguous heads, got {list(shape)} with strides {list(st)}")
+    if t.dtype is not plan.type:
+        raise _bad(f"{name} must be {plan.type}, got {t.dtype}")
+    if st[0] % 8:
+        raise native.SSError(-2, f"{name}: token strides must be multiples of 8 elements, got {st[0]}")
+    return st[0] if shape[0] > 1 else heads * d
 
 
-def _ints(**tensors):
-    for name, t in tensors.items():
-        if t is not None:
-            _check_type(name, t, "i32")
-            if not t.is_contiguous():
-                raise native.SSError(-1, f"{name} must be contiguous")
+def _int(name, t, least):
+    """Address of an int32 tensor of at least `least` entries."""
+    if t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() < least:
+        raise _bad(f"{name} must be contiguous int32 with at least {least} entries, got {t.dtype}, {list(t.shape)}")
+    return t.data_ptr()
 
 
 def _pool(plan, block_table, kv_len, free_pages, free_count, B, stream):
-    _ints(block_table=block_table, kv_len=kv_len, free_pages=free_pages, free_count=free_count)
-    B = kv_len.shape[0] if B is None else B
-    if block_table.dim() != 2 or block_table.shape[0] < B or block_table.shape[1] != plan.max_blocks:
-        raise native.SSError(-1, f"block_table must be [rows, {plan.max_blocks}], got {list(block_table.shape)}")
-    if free_pages.numel() < plan.num_pages:
-        raise native.SSError(-1, "free_pages must have num_pages entries")
-    return Pool(B, block_table.data_ptr(), kv_len.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
-                native._stream_ptr(stream), plan.handle)
+    return Pool(B, _int("block_table", block_table, B * plan.max_blocks), _int("kv_len", kv_len, B),
+                _int("free_pages", free_pages, plan.num_pages), _int("free_count", free_count, 1), _stream(stream, plan),
+                plan.handle)
 
 
 def ss_kv_append(plan: Plan, block_table, kv_len, free_pages, free_count, cu_new, *, slots, positions, seq_len,
                  row_status, B=None, stream=None):
-    """ss_kv_append on int32 tensors: pages, slots and positions of each row's new tokens."""
-    _ints(cu_new=cu_new, slots=slots, positions=positions, seq_len=seq_len, row_status=row_status)
+    """ss_kv_append on int32 tensors: pages, slots and positions of each row's new tokens.  slots and positions hold at
+    least as many entries as there are tokens."""
+    B = kv_len.shape[0] if B is None else B
     pool = _pool(plan, block_table, kv_len, free_pages, free_count, B, stream)
-    native._check(library().ss_kv_append(C.byref(pool), cu_new.data_ptr(), slots.data_ptr(), positions.data_ptr(),
-                                         seq_len.data_ptr(), row_status.data_ptr()))
+    code = _lib.ss_kv_append(pool, _int("cu_new", cu_new, B + 1), _int("slots", slots, 1), _int("positions", positions, 1),
+                             _int("seq_len", seq_len, B), _int("row_status", row_status, B))
+    if code:
+        native._check(code)
 
 
 def ss_kv_commit(plan: Plan, block_table, kv_len, free_pages, free_count, seq_len, *, counts=None, plus=0, finished=None,
                  B=None, stream=None):
     """ss_kv_commit on int32 tensors: lengths move past what is kept, other pages go back to the pool."""
-    _ints(seq_len=seq_len, counts=counts, finished=finished)
+    B = kv_len.shape[0] if B is None else B
     pool = _pool(plan, block_table, kv_len, free_pages, free_count, B, stream)
-    native._check(library().ss_kv_commit(C.byref(pool), seq_len.data_ptr(), _ptr(counts), plus, _ptr(finished)))
+    code = _lib.ss_kv_commit(pool, _int("seq_len", seq_len, B), None if counts is None else _int("counts", counts, B), plus,
+                             None if finished is None else _int("finished", finished, B))
+    if code:
+        native._check(code)
 
 
 def ss_rope_store(plan: Plan, q, k, v, k_cache, v_cache, inv_freq, positions, slots, *, q_out, q_weight=None,
@@ -182,19 +205,21 @@ def ss_rope_store(plan: Plan, q, k, v, k_cache, v_cache, inv_freq, positions, sl
     qs, ks = _tokens("q", q, plan.q_heads, plan), _tokens("k", k, plan.kv_heads, plan)
     vs, os = _tokens("v", v, plan.kv_heads, plan), _tokens("q_out", q_out, plan.q_heads, plan)
     if not (k.shape[0] == v.shape[0] == q_out.shape[0] == positions.shape[0] == slots.shape[0] == T):
-        raise native.SSError(-1, "q, k, v, q_out, positions and slots must have the same number of tokens")
-    _ints(positions=positions, slots=slots)
+        raise _bad("q, k, v, q_out, positions and slots must have the same number of tokens")
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _check_type(name, w, plan.dtype)
+        if w is not None and (w.dtype is not plan.type or w.numel() != plan.head_dim or not w.is_contiguous()):
+            raise _bad(f"{name} must be {plan.head_dim} contiguous {plan.type} values")
     rot = 0
     if inv_freq is not None:
-        _check_type("inv_freq", inv_freq, "f64")
+        if inv_freq.dtype is not torch.float64 or not inv_freq.is_contiguous():
+            raise _bad("inv_freq must be contiguous float64")
         rot = 2 * inv_freq.shape[0]
     b = RopeBatch(T, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(q_weight), _ptr(k_weight), eps, _ptr(inv_freq),
-                  rot, 1 if interleaved else 0, rope_scale, positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(), os,
-                  native._stream_ptr(stream), plan.handle)
-    native._check(library().ss_rope_store(C.byref(b), C.byref(cache)))
+                  rot, 1 if interleaved else 0, rope_scale, _int("positions", positions, T), _int("slots", slots, T),
+                  q_out.data_ptr(), os, _stream(stream, plan), plan.handle)
+    code = _lib.ss_rope_store(b, cache)
+    if code:
+        native._check(code)
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, *, factor: float = 1.0, original_len: int = 0,
@@ -208,14 +233,19 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, factor: float = 1.0
 
 def ss_attend(plan: Plan, q, k_cache, v_cache, block_table, seq_len, cu_new, *, out, row_status, workspace, scale,
               window=0, sinks=0, lse=None, k_scale=None, v_scale=None, B=None, stream=None):
-    """ss_attend: q, out [tokens, q_heads, head_dim]; caches seen as [pages, page_size, kv_heads, head_dim]."""
+    """ss_attend: q, out [tokens, q_heads, head_dim]; caches seen as [pages, page_size, kv_heads, head_dim]; lse float32
+    [tokens, q_heads] or None."""
+    B = seq_len.shape[0] if B is None else B
     cache = _cache(plan, k_cache, v_cache, k_scale, v_scale)
     qs, os = _tokens("q", q, plan.q_heads, plan), _tokens("out", out, plan.q_heads, plan)
-    _ints(block_table=block_table, seq_len=seq_len, cu_new=cu_new, row_status=row_status)
-    B = seq_len.shape[0] if B is None else B
-    if block_table.dim() != 2 or block_table.shape[0] < B or block_table.shape[1] != plan.max_blocks:
-        raise native.SSError(-1, f"block_table must be [rows, {plan.max_blocks}], got {list(block_table.shape)}")
-    b = AttendBatch(B, q.data_ptr(), qs, cu_new.data_ptr(), seq_len.data_ptr(), block_table.data_ptr(), scale, window, sinks,
-                    out.data_ptr(), os, _ptr(lse), row_status.data_ptr(), workspace.data_ptr(),
-                    workspace.numel() * workspace.element_size(), native._stream_ptr(stream), plan.handle)
-    native._check(library().ss_attend(C.byref(b), C.byref(cache)))
+    if out.shape[0] < q.shape[0]:
+        raise _bad("out must have as many tokens as q")
+    if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() < q.shape[0] * plan.q_heads):
+        raise _bad("lse must be contiguous float32 [tokens, q_heads]")
+    b = AttendBatch(B, q.data_ptr(), qs, _int("cu_new", cu_new, B + 1), _int("seq_len", seq_len, B),
+                    _int("block_table", block_table, B * plan.max_blocks), scale, window, sinks, out.data_ptr(), os, _ptr(lse),
+                    _int("row_status", row_status, B), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                    _stream(stream, plan), plan.handle)
+    code = _lib.ss_attend(b, cache)
+    if code:
+        native._check(code)
