@@ -76,7 +76,10 @@ ss_status encode(CUtensorMap* map, const ss_kv_plan* p, const ss_kv_cache* cache
   const cuuint64_t row = c.head_dim * el, atom = std::min<cuuint64_t>(row, 128);
   const cuuint64_t dims[5] = {atom / el, (cuuint64_t)c.page_size, row / atom, (cuuint64_t)c.kv_heads, (cuuint64_t)c.num_pages};
   const cuuint64_t strides[4] = {cache->token_stride * el, atom, cache->head_stride * el, cache->page_stride * el};
-  const cuuint32_t box[5] = {(cuuint32_t)(atom / el), (cuuint32_t)std::min(c.page_size, 64), (cuuint32_t)(row / atom), 1, 1};
+  // a copy of 64 tokens has every run of a tile, one of fewer (a smaller page) has one, so that in shared memory a
+  // tile is its runs of 64 tokens either way; the 8-bit kernel takes all runs of a page together
+  const cuuint32_t tokens = (cuuint32_t)std::min(c.page_size, 64);
+  const cuuint32_t box[5] = {(cuuint32_t)(atom / el), tokens, tokens == 64 || el == 1 ? (cuuint32_t)(row / atom) : 1, 1, 1};
   const cuuint32_t step[5] = {1, 1, 1, 1, 1};
   const CUresult r = encode_tiled()(map, el == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, base, dims, strides,
                                     box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -159,7 +162,7 @@ ss_status ss_kv_plan_create(ss_kv_plan** out, const ss_kv_config* config) {
   // the smallest row tile that holds a row's usual query rows: larger tiles waste products on rows that do not
   // exist, smaller ones read the keys once for each of several tiles
   const int64_t rows = (int64_t)c.max_new * group;
-  const int row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const int row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || c.cache_dtype == SS_E4M3 ? 64 : 128;
   const ss::AttendKernel k = attend_kernel(c, row_tile);
   int occ = 0;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
@@ -347,6 +350,9 @@ ss_status ss_attend(const ss_attend_batch* b, const ss_kv_cache* cache) {
   P.ml = reinterpret_cast<float2*>(w + p->off_ml);
   P.spin_limit = kSpin;
   const ss::AttendKernel k = attend_kernel(c, p->row_tile);
+  P.rows = p->row_tile;
+  P.slots = k.slots;
+  P.q_bufs = k.q_bufs;
   void* args[] = {&P, &mk, &mv};
   const Range range("ss_attend");
   const cudaError_t e = cudaLaunchKernel(k.fn, dim3(p->attend_grid), dim3(k.threads), args, k.smem, static_cast<cudaStream_t>(b->stream));

@@ -1,40 +1,39 @@
-// ss_attend: attention of a step's new tokens over the paged key-value cache.
+// ss_attend for 16-bit caches: attention of a step's new tokens over the paged
+// key-value cache, on the 5th-generation tensor cores.
 //
 // Mathematics.  For a query q at position p, o = sum_t w_t v_t / sum_t w_t
-// with w_t = 2^(c q.k_t - m), c = scale * log2 e, m the running maximum: one
-// pass over the keys, the running sum l and the output rescaled by
-// 2^(m_old - m_new) whenever m grows.  Two pieces (m, l, O) over disjoint keys
-// join as (max m, sum l 2^(m_i - m), sum O 2^(m_i - m)), so the keys of a row
-// can be split anywhere.
+// with w_t = 2^(c q.k_t - m), c = scale * log2 e and m any number near the
+// largest exponent: one pass over the keys.  m is the maximum of the first
+// tile that a row sees; when a later tile exceeds it by more than 2^8 the sum
+// and the output so far are scaled down and m moves (weights up to 2^8 lose
+// nothing in 16-bit floating point, and the output, which lives in tensor
+// memory, is hardly ever touched).  Pieces (m, l, O) over disjoint keys join as
+// (max m, sum l 2^(m_i - m), sum O 2^(m_i - m)), so the keys of a row can be
+// split anywhere.
 //
 // What bounds it.  A key and its value (2 * head_dim elements) are read once
 // for the n * group queries of a key head (n new tokens, group = q_heads /
 // kv_heads): 4 * head_dim * n * group operations on 4 * head_dim bytes, i.e.
-// 1 .. 64 operations a byte where the card's tensor rate over its HBM rate is
+// 1 .. 128 operations a byte where the card's tensor rate over its HBM rate is
 // about 280.  HBM bandwidth is the bound, and the kernel's one aim is to keep
-// enough loads in flight everywhere until the end.
+// loads in flight everywhere until the end.
 //
-// Layout of the work.
-//  - A unit is (row, key head, tile of MT query rows); query row i of a unit
-//    is token i / group, head i % group, so the heads that share a key head
-//    share its loads.  MT = 16, 32 or 64.  A unit's keys are tiles of 64.
-//  - The tiles of all units, in order, are cut into equal ranges, one per CTA
-//    of a grid that fills the GPU: the split follows from the lengths on the
-//    device, every CTA streams the same number of tiles whatever the rows'
-//    lengths are, and the launch never changes.  A unit that ends up in
-//    several CTAs is joined by the last of them to arrive (no CTA waits), in
-//    the order of the tiles, so results do not depend on timing.
-//  - One warp loads: TMA tiles of a page (or 64 tokens of it) of one head
-//    into a ring of swizzled key and value tiles, page ids read a batch
-//    ahead.  Four warps compute with 16 x 8 x 16 matrix instructions.  With
-//    MT = 16 every warp has all query rows and a quarter of a tile's keys,
-//    with its own maximum and sum, and the four join at the end of the unit,
-//    so that nothing synchronises the warps inside it; with MT = 64 a warp has
-//    its own 16 rows and all keys.
-//  - Tensor instructions: at these few query rows the 128-row tiles of the
-//    tcgen05 unit would be empty for the most part, and the softmax of their
-//    accumulators would sit on the few threads that own the live rows; the
-//    warp-wide instructions need no padding beyond 16 rows.
+// A CTA's warps (how the work is cut up: ss_kv_work.cuh):
+//  - load: walks the CTA's range, publishes its segments, gathers their query
+//    rows into shared memory and runs the ring of key and value tiles: TMA
+//    copies of a page (or 64 tokens of it), page ids read a batch ahead.
+//  - product: one thread issues S = Q K^T (128 x 64, both from shared memory)
+//    and O += P V (P from tensor memory) with tcgen05.mma; S of a tile is
+//    issued before the weights of the tile before it are ready.
+//  - four softmax warps: a thread owns a query row (a lane of tensor memory),
+//    so maxima and sums need no exchange; it reads its 64 scores, writes its
+//    weights over them and never waits for the products in between.
+//  Query rows past the live ones are whatever follows in shared memory: rows
+//  of a product do not mix, and nothing reads theirs.  Padding to 128 rows
+//  costs tensor time only (measured with one live row in eight it stays below
+//  the time of the loads), and a warp without live rows skips its part.
+//  - A unit that lies in several CTAs is joined by the last of them to arrive
+//    (none waits), in the order of its tiles: results do not depend on timing.
 #pragma once
 
 #include <cuda.h>
@@ -43,24 +42,26 @@
 
 #include <type_traits>
 
-#include "ss_kv_common.cuh"
+#include "ss_kv_work.cuh"
 #include "ss_stage1.cuh"
 
 namespace ss {
 namespace kv {
 
-constexpr int kTile = 64;         // keys of a tile
-constexpr int kWarps = 4;         // computing warps
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kSoftmaxWarps = 4;                 // warps 0 .. 3: a warp reaches the 32 lanes of its number modulo 4
+constexpr int kLoadWarp = 4, kProductWarp = 5;
+constexpr int kThreads = 192;
+constexpr int kMaxSlots = 16;                    // tiles of keys or values in the ring
+constexpr int kControl = 1536;                   // bytes of the control block, at most
 constexpr uint32_t kDrainPolls = 1u << 22;
-constexpr int kMaxSlots = 16;     // tiles of keys or values in the ring
-constexpr int kControl = 2048;    // bytes of the control block, at most
 
 // ------------------------------------------------------------------ types
 template <class T>
 struct Elem;
 template <>
 struct Elem<__nv_bfloat16> {
+  static constexpr uint32_t kFormat = 1;       // of tcgen05.mma's operands
+  static constexpr uint32_t kExponent = 0x7f80;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -68,257 +69,214 @@ struct Elem<__nv_bfloat16> {
   static __device__ __forceinline__ float2 unpack(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
-  // both halves with infinities and NaN replaced by 0
-  static __device__ __forceinline__ uint32_t finite(uint32_t w) {
-    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
-    return w;
-  }
 };
 template <>
 struct Elem<__half> {
+  static constexpr uint32_t kFormat = 0;
+  static constexpr uint32_t kExponent = 0x7c00;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
-  static __device__ __forceinline__ float2 unpack(uint32_t w) {
-    return __half22float2(*reinterpret_cast<__half2*>(&w));
-  }
-  static __device__ __forceinline__ uint32_t finite(uint32_t w) {
-    if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u;
-    if ((w & 0x7c000000u) == 0x7c000000u) w &= 0xffffu;
-    return w;
-  }
+  static __device__ __forceinline__ float2 unpack(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
 };
 
-template <class T>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
-template <>
-__device__ __forceinline__ void mma<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-template <>
-__device__ __forceinline__ void mma<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-// Two e4m3 values (the low 16 bits of w) as f16x2: exact.
-__device__ __forceinline__ uint32_t e4m3_f16(uint32_t w) {
-  uint32_t d;
-  asm("{\n .reg .b16 h;\n cvt.u16.u32 h, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(d) : "r"(w));
-  return d;
-}
+// ------------------------------------------------------------------ instructions
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ void mbar_init_n(unsigned long long* m, int n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(m)), "r"(n) : "memory");
+}
 __device__ __forceinline__ void arrive(unsigned long long* m) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(m)) : "memory");
 }
-__device__ __forceinline__ void bar_warps() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void expect(unsigned long long* m, int bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(m)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, unsigned long long* m, int token, int run, int head,
+                                         int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(token), "r"(run), "r"(head), "r"(page), "r"(smem_u32(m))
+      : "memory");
+}
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// arrives at m when every product issued so far by this thread is done
+__device__ __forceinline__ void commit(unsigned long long* m) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(m)) : "memory");
+}
+// D (+)= A B^T, A and B from shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a),
+               "l"(b), "r"(desc), "r"((uint32_t)add)
+               : "memory");
+}
+// D (+)= A B, A from tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a),
+               "l"(b), "r"(desc), "r"((uint32_t)add)
+               : "memory");
+}
+// Tensor memory: this warp's 32 lanes, a register for each of n columns from `at` on.
+__device__ __forceinline__ void tmem_load(uint32_t (&r)[32], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+        "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load(uint32_t (&r)[64], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+        "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
+        "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]),
+        "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]),
+        "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]),
+        "=r"(r[63])
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load(uint32_t (&r)[1], uint32_t at) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;" : "=r"(r[0]) : "r"(at) : "memory");
+}
+// Shared-memory operand of lines of 128 bytes, swizzled: 8 lines (1024 bytes) from one group of 8 to the next, `lead`
+// bytes from one run of 64 columns to the next where a product spans several.
+__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lead) {
+  return (uint64_t)((at & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
 
 // ------------------------------------------------------------------ shape of one instantiation
-template <class T, bool E4M3, int D, int MT>
+template <class T, int D>
 struct Shape {
-  using Mul = typename std::conditional<E4M3, __half, T>::type;  // what the products run in
-  static constexpr bool kScaleQ = E4M3 && std::is_same<T, __nv_bfloat16>::value;
-  static constexpr int kEl = E4M3 ? 1 : 2;
-  static constexpr int kRow = D * kEl;                       // bytes of a token
-  static constexpr int kAtom = kRow < 128 ? kRow : 128;      // swizzled run of bytes
-  static constexpr int kRuns = kRow / kAtom;
-  static constexpr int kSlot = kTile * kRow;                 // bytes of a key (or value) tile
+  static constexpr int kRuns = D / 64;                       // runs of 64 columns (128 bytes)
+  static constexpr int kRun = kTile * 128;                   // bytes of a run of a tile
+  static constexpr int kSlot = kRuns * kRun;                 // bytes of a tile of keys or of values
   static constexpr int kCtas = D <= 128 ? 2 : 1;             // CTAs per SM
-  static constexpr int kSmem = (228 * 1024 / kCtas - 1024) & ~127;  // an SM's share of shared memory
-  static constexpr int kWM = MT / 16, kWK = kWarps / kWM;    // warps along query rows, along keys
-  static constexpr int kKG = 4 / kWK;                        // 16-key groups of a warp
-  static constexpr int kQRow = D * 2 + 16;                   // padded: rows fall into different banks
-  static constexpr bool kQRegs = D <= 128 && MT < 64;        // query fragments stay in registers
-  // ring of tiles: as many as the room beside the queries and the control block holds
-  static constexpr int kFit = (kSmem - 1024 - kControl - MT * kQRow) / kSlot;
-  static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
+  static constexpr uint32_t kCols = D <= 128 ? 256 : 512;    // columns of tensor memory: two tiles of scores, the output
+  static constexpr uint32_t kOut = 128;
+  // instruction descriptors: 32-bit sums, both operands of type T, 128 rows; S: 64 columns; O: D columns, V as it lies
+  static constexpr uint32_t kCommon = 1u << 4 | Elem<T>::kFormat << 7 | Elem<T>::kFormat << 10 | (128u >> 4) << 24;
+  static constexpr uint32_t kScores = kCommon | (kTile >> 3) << 17;
+  static constexpr uint32_t kValues = kCommon | 1u << 16 | (uint32_t)(D >> 3) << 17;
 };
-
-// ------------------------------------------------------------------ the work
-struct Row {
-  int q0, n, len;
-  uint32_t status;
-};
-
-__device__ __forceinline__ Row row_info(const AttendParams& P, int r) {
-  Row w;
-  w.q0 = P.cu_new[r];
-  const int q1 = P.cu_new[r + 1];
-  w.n = q1 - w.q0;
-  w.len = P.seq_len[r];
-  w.status = 0;
-  if (w.q0 < 0 || q1 < w.q0 || q1 > P.max_tokens) {
-    w.n = 0;
-    w.status = SS_ST_CAPACITY;
-  }
-  if (w.len < 0 || w.len > P.max_blocks << P.page_shift) {
-    w.len = 0;
-    w.status |= SS_ST_BAD_PARAM;
-  }
-  return w;
-}
-
-// Key tiles of a unit: `sink` tiles from 0, then from `first` on.
-struct Unit {
-  int pos0, pos1;  // positions of its first and last token (may be negative)
-  int sink, first, tiles;
-};
-
-template <int MT>
-__device__ __forceinline__ Unit unit_info(const AttendParams& P, const Row& w, int mt) {
-  Unit u;
-  const int j0 = mt * MT / P.group;
-  const int j1 = min(w.n - 1, (mt * MT + MT - 1) / P.group);
-  u.pos0 = w.len - w.n + j0;
-  u.pos1 = w.len - w.n + j1;
-  u.sink = 0;
-  u.first = 0;
-  if (P.window > 0) {
-    u.first = max(0, u.pos0 - P.window + 1) / kTile;
-    u.sink = min((P.sinks + kTile - 1) / kTile, u.first);
-  }
-  // a unit without a visible key still has one (masked) tile: its output is written
-  u.tiles = u.pos1 < 0 ? 1 : u.sink + u.pos1 / kTile - u.first + 1;
-  return u;
-}
-
-template <int MT>
-__device__ __forceinline__ int row_units(const AttendParams& P, const Row& w) {  // of one key head
-  return (w.n * P.group + MT - 1) / MT;
-}
-template <int MT>
-__device__ __forceinline__ long long row_tiles(const AttendParams& P, const Row& w) {  // of one key head
-  long long s = 0;
-  for (int m = 0; m < row_units<MT>(P, w); ++m) s += unit_info<MT>(P, w, m).tiles;
-  return s;
-}
-
-// A place in the order of all tiles: tile `from` of unit (row, h, mt).
-struct Place {
-  int row, h, mt, from;
-};
-
-// A CTA's part of one unit.
-struct Segment {
-  int row, h, mt;
-  Row w;
-  Unit u;
-  int from, count;       // tiles [from, from + count) of the unit
-  long long unit_start;  // of all tiles
-};
-
-// Steps through the range [t, end) of all tiles; every warp runs its own.
-struct Walk {
-  long long t, end;
-  Place at;
-};
-
-template <int MT>
-__device__ __forceinline__ Segment next_segment(const AttendParams& P, Walk& k) {
-  Segment g;
-  g.w = row_info(P, k.at.row);
-  while (k.at.mt >= row_units<MT>(P, g.w)) {  // next key head, next row with work (the range ends before the rows do)
-    k.at.mt = 0;
-    if (g.w.n == 0 || ++k.at.h == P.hkv) {
-      k.at.h = 0;
-      g.w = row_info(P, ++k.at.row);
-    }
-  }
-  g.row = k.at.row;
-  g.h = k.at.h;
-  g.mt = k.at.mt;
-  g.u = unit_info<MT>(P, g.w, g.mt);
-  g.from = k.at.from;
-  g.count = (int)min((long long)(g.u.tiles - g.from), k.end - k.t);
-  g.unit_start = k.t - g.from;
-  k.t += g.count;
-  k.at.from = 0;  // a range goes on only past the end of a unit
-  ++k.at.mt;
-  return g;
-}
-
-__device__ __forceinline__ int tile_of(const Unit& u, int i) { return i < u.sink ? i : i - u.sink + u.first; }
 
 struct Control {
-  unsigned long long full[kMaxSlots], empty[kMaxSlots];
-  int bad[kMaxSlots];   // per tile of keys: its 16-key groups that lie on pages with a bad id
-  long long range_sums[kThreads / 32];
-  long long total;
-  Place start;
+  unsigned long long full[kMaxSlots], empty[kMaxSlots];  // ring: copies landed; products done with them
+  unsigned long long seg_full[2], seg_empty[2];          // segment published with its queries; done with by all
+  unsigned long long s_full[2], p_full[2], pv_done[2];   // scores there; weights there; added to the output
+  unsigned long long o_free, drained;                    // output read; all products done
+  Segment seg[2];
+  Range range;
+  long long sums[kThreads / 32];
+  int bad[kMaxSlots];  // per tile of keys: its 16-key groups that lie on pages with a bad id
+  int slow[2];         // the tile's values were added by the softmax warps
   int last;
-  float ml[kWarps][16][2];
-  float qinv[64];
+  uint32_t tmem;
 };
-
 static_assert(sizeof(Control) <= kControl, "control block");
 
 // A place in the ring: tiles of keys and of values take turns.
 struct Turn {
   int slot = 0;
   uint32_t parity = 0;
-  template <int N>
-  __device__ __forceinline__ void next() {
-    if (++slot == N) {
+  __device__ __forceinline__ void next(int slots) {
+    if (++slot == slots) {
       slot = 0;
       parity ^= 1;
     }
   }
 };
 
-template <class S>
-constexpr size_t smem_bytes(int MT) {
-  return 1024 + (size_t)S::kSlots * S::kSlot + (size_t)MT * S::kQRow + kControl;
+__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool any_softmax(bool x) {  // over the softmax warps, which it also brings together
+  uint32_t y;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+               : "=r"(y)
+               : "r"((uint32_t)x)
+               : "memory");
+  return y != 0;
 }
 
-// ------------------------------------------------------------------ loads
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, unsigned long long* mbar, int token, int head,
-                                         int page) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %2, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(0), "r"(token), "r"(head), "r"(page), "r"(smem_u32(mbar))
-      : "memory");
+// Is tile `base` of the unit seen in full by every live row?
+__device__ __forceinline__ bool partly(const AttendParams& P, const Unit& u, int base, int bad) {
+  return base + kTile - 1 > u.pos0 || bad != 0 || (P.window > 0 && base <= u.pos1 - P.window && base + kTile > P.sinks);
 }
-__device__ __forceinline__ void expect(unsigned long long* mbar, int bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(mbar)), "r"(bytes) : "memory");
+// Is a key visible from position p?
+__device__ __forceinline__ bool visible(const AttendParams& P, int key, int p) {
+  return key <= p && (P.window <= 0 || key > p - P.window || key < P.sinks);
 }
 
-template <class S, int MT>
-__device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CUtensorMap* mv, unsigned char* ring, Control& c,
-                          Walk k) {
+// ------------------------------------------------------------------ load warp
+template <class S, class T, int D>
+__device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t sq, uint32_t ring, Control& c) {
   const int lane = threadIdx.x & 31;
   const int box_shift = min(P.page_shift, 6);            // tokens of one copy
-  const int subs_shift = 6 - box_shift;                  // copies of a tile
+  const int subs_shift = 6 - box_shift;                  // copies of a run of a tile
+  const int runs = subs_shift ? S::kRuns : 1;            // a copy of 64 tokens has every run
   const int batch = 32 >> subs_shift;                    // tiles whose page ids one lane each holds
   const int sub = lane & ((1 << subs_shift) - 1), nth = lane >> subs_shift;
   const int page_mask = (1 << P.page_shift) - 1;
   const int groups = (1 << (1 << (box_shift - 4))) - 1;  // 16-key groups of a copy, as bits
+  const uint32_t q_bytes = (uint32_t)P.rows * D * 2;
   Turn turn;
-  int asked = 0;                                         // copies in flight or landed, at most kSlots
+  int asked = 0;                                         // copies in flight or landed, at most P.slots
   bool dead = false;
-  while (k.t < k.end && !dead) {
-    const Segment g = next_segment<MT>(P, k);
+  Range k = c.range;
+  Segment g;
+  int sg = 0;
+  bool more = true;
+  while (more && !dead) {
+    more = next_segment(P, k, g);
+    // the segment's place and query buffer: free once segment sg - 2 (or sg - 1) is done
+    const int prior = sg - P.q_bufs;
+    if (prior >= 0) dead = !__all_sync(0xffffffffu, mbar_wait(&c.seg_empty[prior & 1], (prior >> 1) & 1, P.spin_limit, 0u));
+    if (dead) break;
+    if (!more) g.count = 0;  // the end of the range
+    if (lane == 0) c.seg[sg & 1] = g;
+    if (more) {
+      const uint32_t to = sq + (P.q_bufs == 2 && (sg & 1) ? q_bytes : 0u);
+      for (int i = lane; i < g.live * (D / 8); i += 32) {
+        const int m = i / (D / 8), piece = i % (D / 8), f = g.mt * P.rows + m, j = f / P.group;
+        const T* src = static_cast<const T*>(P.q) + (g.q0 + j) * P.q_stride + (g.h * P.group + f - j * P.group) * D + piece * 8;
+        const uint32_t dst = to + (piece >> 3) * (P.rows * 128) + m * 128 + (((piece & 7) ^ (m & 7)) << 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+      }
+    }
+    bool published = false;
+    auto publish = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) arrive(&c.seg_full[sg & 1]);
+      published = true;
+    };
+    if (!more) publish();
+
     const int32_t* table = P.block_table + (long long)g.row * P.max_blocks;
-    const int used = (g.w.len + page_mask) >> P.page_shift;
+    const int used = (g.len + page_mask) >> P.page_shift;
     // The page of this lane's copy in the batch from tile i0 on: num_pages, past the cache, where nothing is held
     // (the copy reads zeros), -1 where the table's id is bad.
     auto fetch = [&](int i0) {
@@ -360,531 +318,419 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
           }
           __syncwarp();
           if (nth == j)
-            tma_load(smem_u32(ring) + turn.slot * S::kSlot + (sub << box_shift) * S::kRow, values ? mv : mk, &c.full[turn.slot], tok, g.h, id);
-          turn.next<S::kSlots>();
-          asked = min(asked + 1, S::kSlots);
+            for (int r = 0; r < runs; ++r)
+              tma_load(ring + turn.slot * S::kSlot + r * S::kRun + (sub << box_shift) * 128, values ? mv : mk, &c.full[turn.slot], tok, r,
+                       g.h, id);
+          turn.next(P.slots);
+          asked = min(asked + 1, P.slots);
         }
+        if (!published && !dead) publish();
       }
     }
+    if (!published) publish();
+    ++sg;
   }
   // no copy may be in flight when the CTA ends (all have landed unless a wait ran out)
+  asm volatile("cp.async.wait_all;" ::: "memory");
   for (; asked > 0; --asked) {
     if (--turn.slot < 0) {
-      turn.slot = S::kSlots - 1;
+      turn.slot = P.slots - 1;
       turn.parity ^= 1;
     }
     mbar_wait(&c.full[turn.slot], turn.parity, kDrainPolls, 0u);
   }
 }
 
-// ------------------------------------------------------------------ products
-// Byte offset in a tile of byte b of key `key`: copies of 2^box_shift keys, in each of them runs of kAtom bytes of
-// all keys, the 16-byte pieces of a 128-byte line permuted by the line's number (64-byte runs: by its half).
-template <class S>
-__device__ __forceinline__ uint32_t place_of(int key, int b, int box_shift) {
-  const int box = key >> box_shift, in = key & ((1 << box_shift) - 1);
-  const uint32_t off = (box << box_shift) * S::kRow + ((b / S::kAtom) << box_shift) * S::kAtom + in * S::kAtom + b % S::kAtom;
-  return off ^ ((off >> 3) & (S::kAtom == 128 ? 0x70 : 0x30));
-}
-
-template <class S, class T, bool E4M3, int D, int MT>
-__device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsigned char* sq, Control& c, Walk k, int ctas) {
-  using Mul = typename S::Mul;
-  using E = Elem<Mul>;
-  constexpr int kNT = S::kKG * 2;  // 8-key tiles of a warp
-  constexpr int kOT = D / 8;       // 8-column tiles of the output
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int wm = warp % S::kWM, wk = warp / S::kWM;
-  const int quad = lane & 3, r0 = lane >> 2;
-  const int box_shift = min(P.page_shift, 6);
-  const uint32_t ring_u = smem_u32(ring), sq_u = smem_u32(sq);
+// ------------------------------------------------------------------ product thread
+template <class S, class T, int D>
+__device__ void product_thread(const AttendParams& P, uint32_t sq, uint32_t ring, Control& c) {
+  const uint32_t tmem = c.tmem, q_bytes = (uint32_t)P.rows * D * 2, q_run = (uint32_t)P.rows * 128;
   Turn turn;
   bool dead = false;
-
-  // This lane's ldmatrix rows: byte `b` (a multiple of 32) of its key of a 16-key group is at group + run of b +
-  // row + ((b % kAtom) ^ x).  Keys: the two 16-byte pieces vary fastest over the matrices; values: the keys do.
-  const int k_key = ((lane >> 4) << 3) + (lane & 7), v_key = (((lane >> 3) & 1) << 3) + (lane & 7);
-  auto permuted = [](int key, int piece) { return (uint32_t)((piece << 4) ^ (S::kAtom == 128 ? (key & 7) << 4 : ((key >> 1) & 3) << 4)); };
-  const uint32_t k_x = permuted(k_key, (lane >> 3) & 1), v_x = permuted(v_key, lane >> 4);
-  const uint32_t run_bytes = (uint32_t)S::kAtom << box_shift;
-  uint32_t group_at[S::kKG];
+  auto wait = [&](unsigned long long* m, uint32_t parity) {
+    if (!dead) dead = !mbar_wait(m, parity, P.spin_limit, 0u);
+  };
+  uint32_t it = 0;  // tiles so far
+  int sg = 0;
+  // adds the weights of tile `tile` times its values to the output
+  auto values = [&](uint32_t tile, const Turn& at, bool first) {
+    const int b = tile & 1;
+    wait(&c.p_full[b], (tile >> 1) & 1);
+    wait(&c.full[at.slot], at.parity);
+    if (first) wait(&c.o_free, (sg & 1) ^ 1);
+    if (dead) return;
+    fence_after();
+    if (!c.slow[b]) {
 #pragma unroll
-  for (int i = 0; i < S::kKG; ++i) {
-    const int key = (wk * S::kKG + i) * 16;
-    group_at[i] = (key >> box_shift << box_shift) * S::kRow + (key & ((1 << box_shift) - 1)) * S::kAtom;
+      for (int k = 0; k < kTile / 16; ++k)
+        mma_ts(tmem + S::kOut, tmem + b * kTile + k * 8, operand(ring + at.slot * S::kSlot + k * 2048, S::kRun), S::kValues, !first || k);
+    }
+    commit(&c.empty[at.slot]);
+    commit(&c.pv_done[b]);
+  };
+  bool more = true;
+  while (more && !dead) {
+    wait(&c.seg_full[sg & 1], (sg >> 1) & 1);
+    const int count = dead ? 0 : c.seg[sg & 1].count;
+    more = count > 0;
+    if (!more) break;
+    const uint32_t q = sq + (P.q_bufs == 2 && (sg & 1) ? q_bytes : 0u);
+    Turn before;  // the values of the tile before
+    for (int i = 0; i < count && !dead; ++i, ++it) {
+      const int b = it & 1;
+      wait(&c.full[turn.slot], turn.parity);
+      wait(&c.pv_done[b], ((it >> 1) & 1) ^ 1);  // the weights of two tiles ago, in the same columns
+      if (dead) break;
+      fence_after();
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        mma_ss(tmem + b * kTile, operand(q + (k >> 2) * q_run + (k & 3) * 32, 0),
+               operand(ring + turn.slot * S::kSlot + (k >> 2) * S::kRun + (k & 3) * 32, 0), S::kScores, k != 0);
+      commit(&c.s_full[b]);
+      commit(&c.empty[turn.slot]);
+      turn.next(P.slots);
+      if (i > 0) values(it - 1, before, i == 1);
+      before = turn;
+      turn.next(P.slots);
+    }
+    if (!dead) values(it - 1, before, count == 1);
+    if (!dead) arrive(&c.seg_empty[sg & 1]);
+    ++sg;
   }
+  // nothing may be in flight when tensor memory is given back
+  commit(&c.drained);
+  mbar_wait(&c.drained, 0, kDrainPolls, 0u);
+}
 
-  while (k.t < k.end) {
-    const Segment g = next_segment<MT>(P, k);
-    const int rows_here = min(MT, g.w.n * P.group - g.mt * MT);
+// ------------------------------------------------------------------ softmax warps
+template <class S, class T, int D>
+__device__ void softmax_warps(const AttendParams& P, unsigned char* ring, Control& c) {
+  using E = Elem<T>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t lanes = c.tmem + ((uint32_t)warp << 21);  // this warp's lanes of tensor memory
+  const uint32_t out_at = lanes + S::kOut;
+  Turn turn;
+  bool dead = false;
+  auto wait = [&](unsigned long long* m, uint32_t parity) {
+    if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(m, parity, P.spin_limit, 0u));
+  };
+  auto added = [&](uint32_t tile) {  // the output holds everything up to this tile
+    wait(&c.pv_done[tile & 1], (tile >> 1) & 1);
+    fence_after();
+  };
+  uint32_t it = 0;
+  int sg = 0;
+  bool more = true;
+  while (more) {
+    wait(&c.seg_full[sg & 1], (sg >> 1) & 1);
+    dead = any_softmax(dead);  // all go on, or none: they meet at barriers
+    const Segment g = c.seg[sg & 1];
+    more = g.count > 0 && !dead;
+    if (!more) break;
+    const bool busy = warp * 32 < g.live;  // the warp has live rows
+    const bool live = tid < g.live;
+    const int f = g.mt * P.rows + tid, token = f / P.group;
+    const int p = live ? g.len - g.n + token : -1;
+    const float scale = P.scale_log2;
+    float mx = -INFINITY, l = 0.0f;
 
-    // queries into shared memory, rows past the end zero
-    bar_warps();
-    for (int i = threadIdx.x; i < MT * (D / 8); i += 32 * kWarps) {
-      const int m = i / (D / 8), piece = i % (D / 8);
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (m < rows_here) {
-        const int f = g.mt * MT + m, j = f / P.group;
-        x = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + (g.w.q0 + j) * P.q_stride +
-                                            (g.h * P.group + f - j * P.group) * D + piece * 8);
-      }
-      if (S::kScaleQ) {
-        // bf16 to f16: a row is scaled by a power of two that brings its largest value near 2^14, so every
-        // value keeps its bits unless it is below 2^-28 of the largest
-        const float2 a = Elem<__nv_bfloat16>::unpack(x.x), b = Elem<__nv_bfloat16>::unpack(x.y),
-                     d = Elem<__nv_bfloat16>::unpack(x.z), e = Elem<__nv_bfloat16>::unpack(x.w);
-        float top = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))),
-                          fmaxf(fmaxf(fabsf(d.x), fabsf(d.y)), fmaxf(fabsf(e.x), fabsf(e.y))));
-#pragma unroll
-        for (int o = D / 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 240);      // biased exponent
-        const float up = __uint_as_float((uint32_t)(127 + 14 + 127 - ex) << 23);  // 2^(14 - exponent)
-        if (piece == 0) c.qinv[m] = __uint_as_float((uint32_t)(ex - 14) << 23);
-        x = make_uint4(Elem<__half>::pack(a.x * up, a.y * up), Elem<__half>::pack(b.x * up, b.y * up),
-                       Elem<__half>::pack(d.x * up, d.y * up), Elem<__half>::pack(e.x * up, e.y * up));
-      }
-      *reinterpret_cast<uint4*>(sq + m * S::kQRow + piece * 16) = x;
-    }
-    bar_warps();
-
-    // a fragment of 16 query rows and 16 columns; with 8-bit keys the columns are permuted as the keys' bytes come
-    auto q_frag = [&](uint32_t (&a)[4], int ks) {
-      if (E4M3) {
-        const unsigned char* p = sq + (wm * 16 + r0) * S::kQRow + ks * 32 + quad * 8;
-        const uint2 x = *reinterpret_cast<const uint2*>(p), y = *reinterpret_cast<const uint2*>(p + 8 * S::kQRow);
-        a[0] = x.x;
-        a[1] = y.x;
-        a[2] = x.y;
-        a[3] = y.y;
-      } else {
-        ldsm(a, sq_u + (wm * 16 + (lane & 15)) * S::kQRow + ks * 32 + (lane >> 4) * 16);
-      }
-    };
-    uint32_t qf[S::kQRegs ? D / 16 : 1][4];
-    if (S::kQRegs) {
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) q_frag(qf[S::kQRegs ? ks : 0], ks);
-    }
-    // positions of this thread's two rows; rows past the end see nothing
-    const int m0 = wm * 16 + r0, m1 = m0 + 8;
-    const int p0 = m0 < rows_here ? g.w.len - g.w.n + (g.mt * MT + m0) / P.group : -1;
-    const int p1 = m1 < rows_here ? g.w.len - g.w.n + (g.mt * MT + m1) / P.group : -1;
-    float c0 = P.scale_log2, c1 = P.scale_log2;
-    if (E4M3 && P.k_scale) {
-      const float s = P.k_scale[g.h];
-      c0 *= s;
-      c1 *= s;
-    }
-    if (S::kScaleQ) {
-      c0 *= c.qinv[m0];
-      c1 *= c.qinv[m1];
-    }
-
-    float o[kOT][4];
-#pragma unroll
-    for (int i = 0; i < kOT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
-    float mx0 = -INFINITY, mx1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-
-    Turn keys, values;
-    for (int i = 0; i < g.count; ++i) {
-      keys = values = turn;
-      values.next<S::kSlots>();
-      const uint32_t kt = ring_u + keys.slot * S::kSlot + k_key * S::kAtom, vt = ring_u + values.slot * S::kSlot + v_key * S::kAtom;
+    for (int i = 0; i < g.count; ++i, ++it) {
+      const int b = it & 1;
       const int base = tile_of(g.u, g.from + i) * kTile;
-      if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&c.full[keys.slot], keys.parity, P.spin_limit, 0u));
-      const int bad = c.bad[keys.slot];
-      // does any live row not see all of the tile?
-      const bool part = base + kTile - 1 > g.u.pos0 || bad != 0 ||
-                        (P.window > 0 && base <= g.u.pos1 - P.window && base + kTile > P.sinks);
-
-      // scores
-      float s[kNT][4];
-#pragma unroll
-      for (int n = 0; n < kNT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-#pragma unroll
-      for (int b0 = 0; b0 < S::kRow; b0 += 32) {  // 32 bytes of every key: 16 columns, or 32 of 8 bits
-        constexpr int kSteps = E4M3 ? 2 : 1;
-        const int ks = b0 / 32 * kSteps;
-        uint32_t qa[kSteps][4];
-        if (!S::kQRegs) {
-#pragma unroll
-          for (int h = 0; h < kSteps; ++h) q_frag(qa[h], ks + h);
-        }
-#pragma unroll
-        for (int gk = 0; gk < S::kKG; ++gk) {
-          uint32_t b[4];
-          ldsm(b, kt + group_at[gk] + b0 / S::kAtom * run_bytes + ((b0 % S::kAtom) ^ k_x));
-#pragma unroll
-          for (int h = 0; h < kSteps; ++h) {
-            const uint32_t(&a)[4] = S::kQRegs ? qf[S::kQRegs ? ks + h : 0] : qa[h];
-            if (E4M3) {
-              mma<Mul>(s[2 * gk], a, e4m3_f16(b[h]), e4m3_f16(b[h] >> 16));
-              mma<Mul>(s[2 * gk + 1], a, e4m3_f16(b[2 + h]), e4m3_f16(b[2 + h] >> 16));
-            } else {
-              mma<Mul>(s[2 * gk], a, b[0], b[1]);
-              mma<Mul>(s[2 * gk + 1], a, b[2], b[3]);
-            }
-          }
-        }
-      }
-      const bool held = i + 1 == g.count;  // the last tile's room serves the join below
-      __syncwarp();
-      if (!held && lane == 0) arrive(&c.empty[keys.slot]);
-
-      // is key `in` of the tile visible from position p?
-      auto sees = [&](int in, int p) {
-        const int key = base + in;
-        return key <= p && (P.window <= 0 || key > p - P.window || key < P.sinks) && !((bad >> (in >> 4)) & 1);
-      };
+      const int k_slot = turn.slot;
+      turn.next(P.slots);
+      const Turn v_turn = turn;
+      turn.next(P.slots);
+      wait(&c.s_full[b], (it >> 1) & 1);
+      fence_after();
+      const int bad = c.bad[k_slot];
+      const bool part = partly(P, g.u, base, bad);
+      bool slow = false;
+      unsigned char* values = ring + v_turn.slot * S::kSlot;
       if (part) {
+        // Values of keys that no row sees must not reach the product (0 * infinity, and what was never written may be
+        // anything): they become zeros.  If a value that only some rows see is not finite, the tile goes the slow way.
+        wait(&c.full[v_turn.slot], v_turn.parity);
+        const int in = tid >> 1, key = base + in;
+        const bool good = !((bad >> (in >> 4)) & 1);
+        const bool some = good && key <= g.u.pos1 && (P.window <= 0 || key > g.u.pos0 - P.window || key < P.sinks);
+        const bool all = good && key <= g.u.pos0 && (P.window <= 0 || key > g.u.pos1 - P.window || key < P.sinks);
+        uint32_t wild = 0;
 #pragma unroll
-        for (int n = 0; n < kNT; ++n)
+        for (int r = 0; r < S::kRuns; ++r) {
+          uint4* line = reinterpret_cast<uint4*>(values + r * S::kRun + in * 128) + (tid & 1) * 4;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int in = wk * S::kKG * 16 + n * 8 + 2 * quad + e;
-            if (!sees(in, p0)) s[n][e] = -INFINITY;
-            if (!sees(in, p1)) s[n][2 + e] = -INFINITY;
-          }
-      }
-
-      // softmax of this warp's keys
-      float t0 = s[0][0], t1 = s[0][2];
-#pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        t0 = fmaxf(t0, fmaxf(s[n][0], s[n][1]));
-        t1 = fmaxf(t1, fmaxf(s[n][2], s[n][3]));
-      }
-      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
-      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
-      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
-      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
-      const float n0 = fmaxf(mx0, t0 * c0), n1 = fmaxf(mx1, t1 * c1);
-      const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
-      if (__any_sync(0xffffffffu, n0 != mx0 || n1 != mx1)) {
-        const float a0 = ex2(mx0 - z0), a1 = ex2(mx1 - z1);
-        l0 *= a0;
-        l1 *= a1;
-#pragma unroll
-        for (int d = 0; d < kOT; ++d) {
-          o[d][0] *= a0;
-          o[d][1] *= a0;
-          o[d][2] *= a1;
-          o[d][3] *= a1;
-        }
-        mx0 = n0;
-        mx1 = n1;
-      }
-#pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        s[n][0] = ex2(fmaf(s[n][0], c0, -z0));
-        s[n][1] = ex2(fmaf(s[n][1], c0, -z0));
-        s[n][2] = ex2(fmaf(s[n][2], c1, -z1));
-        s[n][3] = ex2(fmaf(s[n][3], c1, -z1));
-        l0 += s[n][0] + s[n][1];
-        l1 += s[n][2] + s[n][3];
-      }
-
-      // times the values
-      if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&c.full[values.slot], values.parity, P.spin_limit, 0u));
-      bool odd = false;  // a value of a partly visible tile is not finite
-      auto clean = [&](uint32_t& x) {
-        const uint32_t y = E::finite(x);
-        odd |= y != x;
-        x = y;
-      };
-#pragma unroll
-      for (int gk = 0; gk < S::kKG; ++gk) {
-        // weights are rounded to 16 bits for the product (half a step, 2^-9 or 2^-12 of each, random in sign);
-        // their sum is not
-        const uint32_t a[4] = {E::pack(s[2 * gk][0], s[2 * gk][1]), E::pack(s[2 * gk][2], s[2 * gk][3]),
-                               E::pack(s[2 * gk + 1][0], s[2 * gk + 1][1]), E::pack(s[2 * gk + 1][2], s[2 * gk + 1][3])};
-#pragma unroll
-        for (int b0 = 0; b0 < S::kRow; b0 += 32) {
-          const int d = b0 / 32;
-          uint32_t b[4];
-          ldsm_t(b, vt + group_at[gk] + b0 / S::kAtom * run_bytes + ((b0 % S::kAtom) ^ v_x));
-          if (!E4M3) {
-            if (part) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) clean(b[e]);
-            }
-            mma<Mul>(o[2 * d], a, b[0], b[1]);
-            mma<Mul>(o[2 * d + 1], a, b[2], b[3]);
-          } else {
-            // a register holds two neighbouring columns of two keys: even columns to one product, odd to the other
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t even = __byte_perm(b[2 * h], b[2 * h + 1], 0x6420), odds = __byte_perm(b[2 * h], b[2 * h + 1], 0x7531);
-              uint32_t f[4] = {e4m3_f16(even), e4m3_f16(even >> 16), e4m3_f16(odds), e4m3_f16(odds >> 16)};
-              if (part) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) clean(f[e]);
-              }
-              mma<Mul>(o[(4 * d + 2 * h) % kOT], a, f[0], f[1]);
-              mma<Mul>(o[(4 * d + 2 * h + 1) % kOT], a, f[2], f[3]);
+          for (int x = 0; x < 4; ++x) {
+            if (!some) {
+              line[x] = make_uint4(0u, 0u, 0u, 0u);
+            } else if (!all) {
+              const uint4 y = line[x];
+              for (const uint32_t w : {y.x, y.y, y.z, y.w})
+                wild |= (uint32_t)((w & E::kExponent) == E::kExponent) | (uint32_t)((w >> 16 & E::kExponent) == E::kExponent);
             }
           }
         }
+        proxy_fence();
+        slow = any_softmax(wild != 0);
       }
-      if (part && __any_sync(0xffffffffu, odd)) {
-        // Some value in the tile is not finite and was left out above; rows that see its key take it here, one
-        // key at a time (0 * infinity of a row that does not see it must not happen).
+      if (busy) {
+        uint32_t x[64];
+        tmem_load(x, lanes + b * kTile);
+        auto score = [&](int n) { return __uint_as_float(x[n]); };
+        if (part) {
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) {
+          for (int n = 0; n < 64; ++n)
+            if (!visible(P, base + n, p) || ((bad >> (n >> 4)) & 1)) x[n] = 0xff800000u;
+        }
+        float t0 = score(0), t1 = score(1), t2 = score(2), t3 = score(3);
+#pragma unroll
+        for (int n = 4; n < 64; n += 4) {
+          t0 = fmaxf(t0, score(n));
+          t1 = fmaxf(t1, score(n + 1));
+          t2 = fmaxf(t2, score(n + 2));
+          t3 = fmaxf(t3, score(n + 3));
+        }
+        const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * scale;
+        const bool grow = live && top > (mx == -INFINITY ? mx : mx + 8.0f);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float by = grow ? ex2(mx - top) : 1.0f;  // 0 if nothing was seen before
+          if (grow) mx = top;
+          l *= by;
+          if (i > 0) {
+            added(it - 1);
+#pragma unroll
+            for (int d = 0; d < D; d += 32) {
+              uint32_t o[32];
+              tmem_load(o, out_at + d);
+#pragma unroll
+              for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * by);
+              tmem_store(out_at + d, o);
+            }
+            store_wait();
+          }
+        }
+        const float z = mx == -INFINITY ? 0.0f : mx;
+        // weights are rounded to 16 bits for the product (half a step, 2^-9 or 2^-12 of each, random in sign); their
+        // sum is not
+        uint32_t w[32];
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int n = 0; n < 32; ++n) {
+          const float a = ex2(fmaf(score(2 * n), scale, -z)), e = ex2(fmaf(score(2 * n + 1), scale, -z));
+          s0 += a;
+          s1 += e;
+          w[n] = E::pack(a, e);
+        }
+        l += s0 + s1;
+        tmem_store(lanes + b * kTile, w);
+        store_wait();
+      }
+      if (part) {
+        if (slow && busy) {
+          // one key at a time, and only for the rows that see it
+          if (i > 0) added(it - 1);
 #pragma unroll 1
-          for (int src = 0; src < 8; ++src) {
-            const int from = (lane & ~3) + (src >> 1);
-            const float e0 = __shfl_sync(0xffffffffu, s[n][0], from), e1 = __shfl_sync(0xffffffffu, s[n][1], from);
-            const float e2 = __shfl_sync(0xffffffffu, s[n][2], from), e3 = __shfl_sync(0xffffffffu, s[n][3], from);
-            const float w0 = src & 1 ? e1 : e0, w1 = src & 1 ? e3 : e2;
-            const int in = wk * S::kKG * 16 + n * 8 + src;
-            const bool v0 = sees(in, p0), v1 = sees(in, p1);
+          for (int d = 0; d < D; d += 32) {
+            uint32_t o[32];
+            if (i > 0) tmem_load(o, out_at + d);
+            float acc[32];
 #pragma unroll
-            for (int d = 0; d < kOT; ++d)
+            for (int n = 0; n < 32; ++n) acc[n] = i > 0 ? __uint_as_float(o[n]) : 0.0f;
+#pragma unroll 1
+            for (int n = 0; n < kTile; ++n) {
+              uint32_t pair[1];
+              tmem_load(pair, lanes + b * kTile + (n >> 1));
+              const float2 ws = E::unpack(pair[0]);
+              const float wt = n & 1 ? ws.y : ws.x;
+              const bool sees = visible(P, base + n, p) && !((bad >> (n >> 4)) & 1);
+              const unsigned char* line = values + (d >> 6) * S::kRun + n * 128;
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const int col = E4M3 ? (d >> 1) * 16 + 4 * quad + 2 * x + (d & 1) : d * 8 + 2 * quad + x;
-                const unsigned char* at = ring + values.slot * S::kSlot + place_of<S>(in, col * S::kEl, box_shift);
-                const float v = E4M3 ? E::unpack(e4m3_f16(*at)).x : E::unpack(*reinterpret_cast<const unsigned short*>(at)).x;
-                if (!isfinite(v)) {
-                  if (v0) o[d][x] = fmaf(w0, v, o[d][x]);
-                  if (v1) o[d][2 + x] = fmaf(w1, v, o[d][2 + x]);
+              for (int q = 0; q < 4; ++q) {
+                const uint4 y = *reinterpret_cast<const uint4*>(line + ((((d >> 3) & 7) + q) ^ (n & 7)) * 16);
+                const uint32_t ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                  const float2 v = E::unpack(ys[h]);
+                  if (sees) {
+                    acc[q * 8 + h * 2] = fmaf(wt, v.x, acc[q * 8 + h * 2]);
+                    acc[q * 8 + h * 2 + 1] = fmaf(wt, v.y, acc[q * 8 + h * 2 + 1]);
+                  }
                 }
               }
+            }
+#pragma unroll
+            for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(acc[n]);
+            tmem_store(out_at + d, o);
           }
+          store_wait();
         }
       }
+      if (tid == 0) c.slow[b] = slow;
+      fence_before();
       __syncwarp();
-      if (!held && lane == 0) arrive(&c.empty[values.slot]);
-      turn = values;
-      turn.next<S::kSlots>();
+      if (lane == 0) arrive(&c.p_full[b]);
     }
     if (dead && lane == 0) atomicOr(&P.row_status[g.row], (uint32_t)SS_ST_COPY_TIMEOUT);
 
-    // ---- join: the warps of the unit, then the CTAs
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    // adds another piece
-    auto take = [&](float ym0, float ym1, float yl0, float yl1, const float4* at) {
-      const float n0 = fmaxf(mx0, ym0), n1 = fmaxf(mx1, ym1);
-      const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
-      const float a0 = ex2(mx0 - z0), a1 = ex2(mx1 - z1), b0 = ex2(ym0 - z0), b1 = ex2(ym1 - z1);
-      l0 = l0 * a0 + yl0 * b0;
-      l1 = l1 * a1 + yl1 * b1;
+    // ---- the unit's output, or this CTA's piece of it
+    added(it - 1);
+    const bool whole = g.ca == g.cb;
+    auto piece = [&](int x) { return (size_t)(2 * x + (x == g.ca ? 1 : 0)) * P.rows; };  // a range's last unit / its first
+    if (busy) {
+      const size_t mine = piece(blockIdx.x);
+      const int head = g.h * P.group + f - token * P.group;
+      const float r = l == 0.0f ? 0.0f : 1.0f / l;
+      T* to = static_cast<T*>(P.out) + (g.q0 + token) * P.out_stride + head * D;
+      float4* part_to = reinterpret_cast<float4*>(P.part + mine * D) + tid;
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        uint32_t o[32];
+        tmem_load(o, out_at + d);
+        auto val = [&](int n) { return __uint_as_float(o[n]); };
+        if (!live) continue;
+        if (whole) {
 #pragma unroll
-      for (int d = 0; d < kOT; ++d) {
-        const float4 y = at[d * 32];
-        o[d][0] = o[d][0] * a0 + y.x * b0;
-        o[d][1] = o[d][1] * a0 + y.y * b0;
-        o[d][2] = o[d][2] * a1 + y.z * b1;
-        o[d][3] = o[d][3] * a1 + y.w * b1;
-      }
-      mx0 = n0;
-      mx1 = n1;
-    };
-    auto join_warps = [&]() {
+          for (int n = 0; n < 32; n += 8)
+            *reinterpret_cast<uint4*>(to + d + n) =
+                make_uint4(E::pack(val(n) * r, val(n + 1) * r), E::pack(val(n + 2) * r, val(n + 3) * r),
+                           E::pack(val(n + 4) * r, val(n + 5) * r), E::pack(val(n + 6) * r, val(n + 7) * r));
+        } else {
 #pragma unroll
-      for (int half = S::kWK / 2; half > 0; half >>= 1) {
-        // warps [half, 2 half) along the keys hand their piece to warps [0, half)
-        bar_warps();
-        const int area = S::kWM == 1 ? wk % half : wm;  // at most two pieces at a time
-        float4* at = reinterpret_cast<float4*>(ring + (area ? values.slot : keys.slot) * S::kSlot) + lane;
-        if (wk >= half && wk < 2 * half) {
-#pragma unroll
-          for (int d = 0; d < kOT; ++d) at[d * 32] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
-          if (quad == 0) {
-            c.ml[warp][r0][0] = mx0;
-            c.ml[warp][r0][1] = l0;
-            c.ml[warp][r0 + 8][0] = mx1;
-            c.ml[warp][r0 + 8][1] = l1;
-          }
-        }
-        bar_warps();
-        if (wk < half) {
-          const int other = warp + half * S::kWM;
-          take(c.ml[other][r0][0], c.ml[other][r0 + 8][0], c.ml[other][r0][1], c.ml[other][r0 + 8][1], at);
+          for (int n = 0; n < 32; n += 4)
+            part_to[(size_t)((d + n) >> 2) * P.rows] = make_float4(val(n), val(n + 1), val(n + 2), val(n + 3));
         }
       }
-    };
-    join_warps();
-
-    bool write = true;
-    if (g.from != 0 || g.count != g.u.tiles) {
-      // owner of tile t: the largest c with c * total / ctas <= t
-      const long long total = c.total;
-      const int ca = (int)(((g.unit_start + 1) * ctas - 1) / total);
-      const int cb = (int)(((g.unit_start + g.u.tiles) * ctas - 1) / total);
-      auto piece = [&](int x) { return (size_t)(2 * x + (x == ca ? 1 : 0)) * MT; };  // a range's last unit / its first
-      if (wk == 0) {
-        const size_t mine = piece(blockIdx.x);
-        float4* to = reinterpret_cast<float4*>(P.part + mine * D) + wm * (16 * D / 4) + lane;
-#pragma unroll
-        for (int d = 0; d < kOT; ++d) to[d * 32] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
-        if (quad == 0) {
-          P.ml[mine + m0] = make_float2(mx0, l0);
-          P.ml[mine + m1] = make_float2(mx1, l1);
-        }
-      }
-      __threadfence();
-      bar_warps();
-      if (threadIdx.x == 0) {
-        const uint32_t before = atomicAdd(&P.counters[ca], 1u);
-        c.last = before == (uint32_t)(cb - ca);
-        if (c.last) P.counters[ca] = 0;
-      }
-      bar_warps();
-      write = c.last != 0;
-      if (write) {
-        __threadfence();
-        mx0 = mx1 = -INFINITY;
-        l0 = l1 = 0.0f;
-#pragma unroll
-        for (int d = 0; d < kOT; ++d)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
-        for (int x = ca + wk; x <= cb; x += S::kWK) {
-          const size_t its = piece(x);
-          const float2 y0 = P.ml[its + m0], y1 = P.ml[its + m1];
-          take(y0.x, y1.x, y0.y, y1.y, reinterpret_cast<const float4*>(P.part + its * D) + wm * (16 * D / 4) + lane);
-        }
-        join_warps();
+      if (live) {
+        if (!whole) P.ml[mine + tid] = make_float2(mx, l);
+        else if (P.lse) P.lse[(size_t)(g.q0 + token) * (P.group * P.hkv) + head] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
       }
     }
-
-    if (write && wk == 0) {
-      float f0 = l0 == 0.0f ? 0.0f : 1.0f / l0, f1 = l1 == 0.0f ? 0.0f : 1.0f / l1;
-      if (E4M3 && P.v_scale) {
-        f0 *= P.v_scale[g.h];
-        f1 *= P.v_scale[g.h];
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int m = x ? m1 : m0;
-        if (m < rows_here) {
-          const int f = g.mt * MT + m, j = f / P.group, head = g.h * P.group + f - j * P.group;
-          const float r = x ? f1 : f0;
-          T* to = static_cast<T*>(P.out) + (g.w.q0 + j) * P.out_stride + head * D;
-          if (E4M3) {
-#pragma unroll
-            for (int d = 0; d < kOT; d += 2)
-              *reinterpret_cast<uint2*>(to + d * 8 + quad * 4) =
-                  make_uint2(Elem<T>::pack(o[d][2 * x] * r, o[d + 1][2 * x] * r),
-                             Elem<T>::pack(o[d][2 * x + 1] * r, o[d + 1][2 * x + 1] * r));
-          } else {
-#pragma unroll
-            for (int d = 0; d < kOT; ++d)
-              *reinterpret_cast<uint32_t*>(to + d * 8 + quad * 2) = Elem<T>::pack(o[d][2 * x] * r, o[d][2 * x + 1] * r);
-          }
-          if (P.lse && quad == 0) {
-            const float l = x ? l1 : l0, mx = x ? mx1 : mx0;
-            P.lse[(size_t)(g.w.q0 + j) * (P.group * P.hkv) + head] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
-          }
-        }
-      }
-    }
-    // the room is given back to the loads
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    fence_before();
     __syncwarp();
     if (lane == 0) {
-      arrive(&c.empty[keys.slot]);
-      arrive(&c.empty[values.slot]);
+      arrive(&c.o_free);
+      arrive(&c.seg_empty[sg & 1]);
+    }
+    ++sg;
+    if (whole) continue;
+    __threadfence();
+    bar_softmax();
+    if (tid == 0) {
+      const uint32_t before = atomicAdd(&P.counters[g.ca], 1u);
+      c.last = before == (uint32_t)(g.cb - g.ca);
+      if (c.last) P.counters[g.ca] = 0;
+    }
+    bar_softmax();
+    if (!c.last) continue;
+    __threadfence();
+    // four columns of a row at a time, the pieces in order
+    for (int e = tid; e < P.rows * (D / 4); e += 32 * kSoftmaxWarps) {
+      const int m = e % P.rows, col = e / P.rows * 4;
+      if (m >= g.live) continue;
+      float top = -INFINITY, sum = 0.0f;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      auto add = [&](float2 ml, float4 y) {
+        const float n = fmaxf(top, ml.x), zn = n == -INFINITY ? 0.0f : n, a = ex2(top - zn), bb = ex2(ml.x - zn);
+        sum = sum * a + ml.y * bb;
+        o = make_float4(o.x * a + y.x * bb, o.y * a + y.y * bb, o.z * a + y.z * bb, o.w * a + y.w * bb);
+        top = n;
+      };
+      auto at = [&](int x) { return reinterpret_cast<const float4*>(P.part + piece(x) * D) + e; };
+      int x = g.ca;
+      for (; x + 4 <= g.cb + 1; x += 4) {
+        float2 ml[4];
+        float4 y[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          ml[n] = __ldcg(P.ml + piece(x + n) + m);
+          y[n] = __ldcg(at(x + n));
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) add(ml[n], y[n]);
+      }
+      for (; x <= g.cb; ++x) add(__ldcg(P.ml + piece(x) + m), __ldcg(at(x)));
+      const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const int fm = g.mt * P.rows + m, jm = fm / P.group, head = g.h * P.group + fm - jm * P.group;
+      *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + (g.q0 + jm) * P.out_stride + head * D + col) =
+          make_uint2(E::pack(o.x * r, o.y * r), E::pack(o.z * r, o.w * r));
+      if (P.lse && col == 0)
+        P.lse[(size_t)(g.q0 + jm) * (P.group * P.hkv) + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
     }
   }
 }
 
 // ------------------------------------------------------------------ kernel
-template <class T, bool E4M3, int D, int MT>
-__global__ void __launch_bounds__(kThreads, (Shape<T, E4M3, D, MT>::kCtas))
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas))
     attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-  using S = Shape<T, E4M3, D, MT>;
-  static_assert(S::kSlots >= 4, "ring length");
+  using S = Shape<T, D>;
   extern __shared__ unsigned char raw[];
-  unsigned char* ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  unsigned char* sq = ring + S::kSlots * S::kSlot;
-  Control& c = *reinterpret_cast<Control*>(sq + MT * S::kQRow);
+  __shared__ Control c;
+  // query buffers first: products read 128 rows from each of their runs, into the ring where fewer are live
+  unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  unsigned char* ring = base + P.q_bufs * P.rows * D * 2;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  find_range<kThreads>(P, c.sums, &c.range);
+  if (c.range.ctas == 0) return;
   if (tid == 0) {
-    for (int i = 0; i < S::kSlots; ++i) {
-      mbar_init(&c.full[i]);
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&c.empty[i])), "r"(kWarps) : "memory");
+    for (int i = 0; i < P.slots; ++i) {
+      mbar_init_n(&c.full[i], 1);
+      mbar_init_n(&c.empty[i], 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init_n(&c.seg_full[i], 1);
+      mbar_init_n(&c.seg_empty[i], kSoftmaxWarps + 1);
+      mbar_init_n(&c.s_full[i], 1);
+      mbar_init_n(&c.p_full[i], kSoftmaxWarps);
+      mbar_init_n(&c.pv_done[i], 1);
+      c.slow[i] = 0;
+    }
+    mbar_init_n(&c.o_free, kSoftmaxWarps);
+    mbar_init_n(&c.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kWarps && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &mv : &mk) : "memory");
-
-  // all tiles, and where this CTA's range of them starts: every thread sums a run of rows
-  const int run = (P.B + kThreads - 1) / kThreads;
-  const int ra = min(P.B, tid * run), rb = min(P.B, ra + run);
-  long long mine = 0;
-  for (int r = ra; r < rb; ++r) {
-    const Row w = row_info(P, r);
-    if (w.status && blockIdx.x == 0) atomicOr(&P.row_status[r], w.status);
-    mine += row_tiles<MT>(P, w) * P.hkv;
+  if (warp == kProductWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&c.tmem)), "r"(S::kCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  long long incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += y;
-  }
-  if (lane == 31) c.range_sums[warp] = incl;
+  if (warp == kLoadWarp && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &mv : &mk) : "memory");
+  fence_before();
   __syncthreads();
-  long long total = 0, before = incl - mine;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const long long y = c.range_sums[w];
-    if (w < warp) before += y;
-    total += y;
+  fence_after();
+  if (warp == kLoadWarp) {
+    load_warp<S, T, D>(P, &mk, &mv, smem_u32(base), smem_u32(ring), c);
+  } else if (warp == kProductWarp) {
+    if (lane == 0) product_thread<S, T, D>(P, smem_u32(base), smem_u32(ring), c);
+    __syncwarp();
+  } else {
+    softmax_warps<S, T, D>(P, ring, c);
   }
-  const int ctas = (int)min((long long)gridDim.x, total);
-  if ((int)blockIdx.x >= ctas) return;
-  const long long start = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
-  if (start >= before && start < before + mine) {
-    long long off = start - before, per_head = 0;
-    Place at = {ra, 0, 0, 0};
-    Row w;
-    for (; at.row < rb; ++at.row) {
-      w = row_info(P, at.row);
-      per_head = row_tiles<MT>(P, w);
-      if (off < per_head * P.hkv) break;
-      off -= per_head * P.hkv;
-    }
-    at.h = (int)(off / per_head);
-    off -= at.h * per_head;
-    for (int n = unit_info<MT>(P, w, 0).tiles; off >= n; n = unit_info<MT>(P, w, at.mt).tiles) {
-      off -= n;
-      ++at.mt;
-    }
-    at.from = (int)off;
-    c.start = at;
-    c.total = total;
-  }
+  fence_before();
   __syncthreads();
-  Walk k;
-  k.t = start;
-  k.end = end;
-  k.at = c.start;
-  if (warp == kWarps) load_warp<S, MT>(P, &mk, &mv, ring, c, k);
-  else compute_warps<S, T, E4M3, D, MT>(P, ring, sq, c, k, ctas);
+  if (warp == kProductWarp) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(c.tmem), "r"(S::kCols) : "memory");
+  }
 }
 
-template <class T, bool E4M3, int D, int MT>
-AttendKernel entry() {
-  return {reinterpret_cast<const void*>(&attend_kernel<T, E4M3, D, MT>), kThreads, smem_bytes<Shape<T, E4M3, D, MT>>(MT)};
+// The kernel for `rows` query rows of a unit, its ring length and shared memory.
+template <class T, int D>
+AttendKernel entry(int rows) {
+  using S = Shape<T, D>;
+  const int share = (228 * 1024 / S::kCtas - 1024 - kControl - 1024) & ~1023;  // a CTA's, without the control block
+  AttendKernel k;
+  k.fn = reinterpret_cast<const void*>(&attend_kernel<T, D>);
+  k.threads = kThreads;
+  k.q_bufs = rows <= 64 ? 2 : 1;  // a second buffer hides the gathering of the next segment's queries; 128 rows leave no room
+  const int q = k.q_bufs * rows * D * 2;
+  k.slots = (share - 1024 - q) / S::kSlot;
+  if (k.slots > kMaxSlots) k.slots = kMaxSlots;
+  k.smem = 1024 + (size_t)q + (size_t)k.slots * S::kSlot;
+  return k;
 }
-template <class T, bool E4M3, int D>
-AttendKernel by_rows(int mt) {
-  return mt == 16 ? entry<T, E4M3, D, 16>() : mt == 32 ? entry<T, E4M3, D, 32>() : entry<T, E4M3, D, 64>();
-}
-template <class T, bool E4M3>
-AttendKernel pick(int d, int mt) {
-  return d == 64 ? by_rows<T, E4M3, 64>(mt) : d == 128 ? by_rows<T, E4M3, 128>(mt) : by_rows<T, E4M3, 256>(mt);
+template <class T>
+AttendKernel pick(int d, int rows) {
+  return d == 64 ? entry<T, 64>(rows) : d == 128 ? entry<T, 128>(rows) : entry<T, 256>(rows);
 }
 
 }  // namespace kv

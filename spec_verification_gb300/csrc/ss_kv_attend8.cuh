@@ -1,0 +1,735 @@
+// ss_attend: attention of a step's new tokens over the paged key-value cache.
+//
+// Mathematics.  For a query q at position p, o = sum_t w_t v_t / sum_t w_t
+// with w_t = 2^(c q.k_t - m), c = scale * log2 e, m the running maximum: one
+// pass over the keys, the running sum l and the output rescaled by
+// 2^(m_old - m_new) whenever m grows.  Two pieces (m, l, O) over disjoint keys
+// join as (max m, sum l 2^(m_i - m), sum O 2^(m_i - m)), so the keys of a row
+// can be split anywhere.
+//
+// What bounds it.  A key and its value (2 * head_dim elements) are read once
+// for the n * group queries of a key head (n new tokens, group = q_heads /
+// kv_heads): 4 * head_dim * n * group operations on 4 * head_dim bytes, i.e.
+// 1 .. 64 operations a byte where the card's tensor rate over its HBM rate is
+// about 280.  HBM bandwidth is the bound, and the kernel's one aim is to keep
+// enough loads in flight everywhere until the end.
+//
+// Layout of the work.
+//  - A unit is (row, key head, tile of MT query rows); query row i of a unit
+//    is token i / group, head i % group, so the heads that share a key head
+//    share its loads.  MT = 16, 32 or 64.  A unit's keys are tiles of 64.
+//  - The tiles of all units, in order, are cut into equal ranges, one per CTA
+//    of a grid that fills the GPU: the split follows from the lengths on the
+//    device, every CTA streams the same number of tiles whatever the rows'
+//    lengths are, and the launch never changes.  A unit that ends up in
+//    several CTAs is joined by the last of them to arrive (no CTA waits), in
+//    the order of the tiles, so results do not depend on timing.
+//  - One warp loads: TMA tiles of a page (or 64 tokens of it) of one head
+//    into a ring of swizzled key and value tiles, page ids read a batch
+//    ahead.  Four warps compute with 16 x 8 x 16 matrix instructions.  With
+//    MT = 16 every warp has all query rows and a quarter of a tile's keys,
+//    with its own maximum and sum, and the four join at the end of the unit,
+//    so that nothing synchronises the warps inside it; with MT = 64 a warp has
+//    its own 16 rows and all keys.
+//  - Tensor instructions: at these few query rows the 128-row tiles of the
+//    tcgen05 unit would be empty for the most part, and the softmax of their
+//    accumulators would sit on the few threads that own the live rows; the
+//    warp-wide instructions need no padding beyond 16 rows.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "ss_kv_work.cuh"
+#include "ss_stage1.cuh"
+
+namespace ss {
+namespace kv8 {
+
+using namespace kv;
+
+constexpr int kWarps = 4;         // computing warps
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr uint32_t kDrainPolls = 1u << 22;
+constexpr int kMaxSlots = 16;     // tiles of keys or values in the ring
+constexpr int kControl = 2048;    // bytes of the control block, at most
+
+// ------------------------------------------------------------------ types
+template <class T>
+struct Elem;
+template <>
+struct Elem<__nv_bfloat16> {
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  // both halves with infinities and NaN replaced by 0
+  static __device__ __forceinline__ uint32_t finite(uint32_t w) {
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+    return w;
+  }
+};
+template <>
+struct Elem<__half> {
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    return __half22float2(*reinterpret_cast<__half2*>(&w));
+  }
+  static __device__ __forceinline__ uint32_t finite(uint32_t w) {
+    if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u;
+    if ((w & 0x7c000000u) == 0x7c000000u) w &= 0xffffu;
+    return w;
+  }
+};
+
+template <class T>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// Two e4m3 values (the low 16 bits of w) as f16x2: exact.
+__device__ __forceinline__ uint32_t e4m3_f16(uint32_t w) {
+  uint32_t d;
+  asm("{\n .reg .b16 h;\n cvt.u16.u32 h, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(d) : "r"(w));
+  return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void arrive(unsigned long long* m) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(m)) : "memory");
+}
+__device__ __forceinline__ void bar_warps() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// ------------------------------------------------------------------ shape of one instantiation
+template <class T, bool E4M3, int D, int MT>
+struct Shape {
+  using Mul = typename std::conditional<E4M3, __half, T>::type;  // what the products run in
+  static constexpr bool kScaleQ = E4M3 && std::is_same<T, __nv_bfloat16>::value;
+  static constexpr int kEl = E4M3 ? 1 : 2;
+  static constexpr int kRow = D * kEl;                       // bytes of a token
+  static constexpr int kAtom = kRow < 128 ? kRow : 128;      // swizzled run of bytes
+  static constexpr int kRuns = kRow / kAtom;
+  static constexpr int kSlot = kTile * kRow;                 // bytes of a key (or value) tile
+  static constexpr int kCtas = D <= 128 ? 2 : 1;             // CTAs per SM
+  static constexpr int kSmem = (228 * 1024 / kCtas - 1024) & ~127;  // an SM's share of shared memory
+  static constexpr int kWM = MT / 16, kWK = kWarps / kWM;    // warps along query rows, along keys
+  static constexpr int kKG = 4 / kWK;                        // 16-key groups of a warp
+  static constexpr int kQRow = D * 2 + 16;                   // padded: rows fall into different banks
+  static constexpr bool kQRegs = D <= 128 && MT < 64;        // query fragments stay in registers
+  // ring of tiles: as many as the room beside the queries and the control block holds
+  static constexpr int kFit = (kSmem - 1024 - kControl - MT * kQRow) / kSlot;
+  static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
+};
+
+// ------------------------------------------------------------------ control
+struct Control {
+  unsigned long long full[kMaxSlots], empty[kMaxSlots];
+  int bad[kMaxSlots];   // per tile of keys: its 16-key groups that lie on pages with a bad id
+  long long range_sums[kThreads / 32];
+  Range range;
+  int last;
+  float ml[kWarps][16][2];
+  float qinv[64];
+};
+
+static_assert(sizeof(Control) <= kControl, "control block");
+
+// A place in the ring: tiles of keys and of values take turns.
+struct Turn {
+  int slot = 0;
+  uint32_t parity = 0;
+  template <int N>
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+template <class S>
+constexpr size_t smem_bytes(int MT) {
+  return 1024 + (size_t)S::kSlots * S::kSlot + (size_t)MT * S::kQRow + kControl;
+}
+
+// ------------------------------------------------------------------ loads
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, unsigned long long* mbar, int token, int head,
+                                         int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %2, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(token), "r"(head), "r"(page), "r"(smem_u32(mbar))
+      : "memory");
+}
+__device__ __forceinline__ void expect(unsigned long long* mbar, int bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(mbar)), "r"(bytes) : "memory");
+}
+
+template <class S, int MT>
+__device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CUtensorMap* mv, unsigned char* ring, Control& c,
+                          Range k) {
+  const int lane = threadIdx.x & 31;
+  const int box_shift = min(P.page_shift, 6);            // tokens of one copy
+  const int subs_shift = 6 - box_shift;                  // copies of a tile
+  const int batch = 32 >> subs_shift;                    // tiles whose page ids one lane each holds
+  const int sub = lane & ((1 << subs_shift) - 1), nth = lane >> subs_shift;
+  const int page_mask = (1 << P.page_shift) - 1;
+  const int groups = (1 << (1 << (box_shift - 4))) - 1;  // 16-key groups of a copy, as bits
+  Turn turn;
+  int asked = 0;                                         // copies in flight or landed, at most kSlots
+  bool dead = false;
+  Segment g;
+  while (!dead && next_segment(P, k, g)) {
+    const int32_t* table = P.block_table + (long long)g.row * P.max_blocks;
+    const int used = (g.len + page_mask) >> P.page_shift;
+    // The page of this lane's copy in the batch from tile i0 on: num_pages, past the cache, where nothing is held
+    // (the copy reads zeros), -1 where the table's id is bad.
+    auto fetch = [&](int i0) {
+      const int i = i0 + nth;
+      int id = P.num_pages;
+      if (i < g.count) {
+        const int block = (tile_of(g.u, g.from + i) * kTile + (sub << box_shift)) >> P.page_shift;
+        if (block < used) {
+          id = __ldg(table + block);
+          if ((unsigned)id >= (unsigned)P.num_pages) id = -1;
+        }
+      }
+      return id;
+    };
+    int next = fetch(0);
+    for (int i0 = 0; i0 < g.count && !dead; i0 += batch) {
+      int id = next;
+      const uint32_t bad_lanes = __ballot_sync(0xffffffffu, id < 0);
+      if (id < 0) {
+        id = P.num_pages;
+        atomicOr(&P.row_status[g.row], (uint32_t)SS_ST_KV_PAGE);
+      }
+      next = fetch(i0 + batch);
+      const int n = min(batch, g.count - i0);
+      for (int j = 0; j < n && !dead; ++j) {
+        const int tok = (tile_of(g.u, g.from + i0 + j) * kTile + (sub << box_shift)) & page_mask;
+#pragma unroll
+        for (int values = 0; values < 2; ++values) {
+          dead = !__all_sync(0xffffffffu, mbar_wait(&c.empty[turn.slot], turn.parity ^ 1, P.spin_limit, 0u));
+          if (dead) break;
+          if (lane == 0) {
+            if (!values) {
+              int bits = 0;
+              for (int s = 0; s < 1 << subs_shift; ++s)
+                if ((bad_lanes >> ((j << subs_shift) + s)) & 1) bits |= groups << (s << (box_shift - 4));
+              c.bad[turn.slot] = bits;
+            }
+            expect(&c.full[turn.slot], S::kSlot);
+          }
+          __syncwarp();
+          if (nth == j)
+            tma_load(smem_u32(ring) + turn.slot * S::kSlot + (sub << box_shift) * S::kRow, values ? mv : mk, &c.full[turn.slot], tok, g.h, id);
+          turn.next<S::kSlots>();
+          asked = min(asked + 1, S::kSlots);
+        }
+      }
+    }
+  }
+  // no copy may be in flight when the CTA ends (all have landed unless a wait ran out)
+  for (; asked > 0; --asked) {
+    if (--turn.slot < 0) {
+      turn.slot = S::kSlots - 1;
+      turn.parity ^= 1;
+    }
+    mbar_wait(&c.full[turn.slot], turn.parity, kDrainPolls, 0u);
+  }
+}
+
+// ------------------------------------------------------------------ products
+// Byte offset in a tile of byte b of key `key`: copies of 2^box_shift keys, in each of them runs of kAtom bytes of
+// all keys, the 16-byte pieces of a 128-byte line permuted by the line's number (64-byte runs: by its half).
+template <class S>
+__device__ __forceinline__ uint32_t place_of(int key, int b, int box_shift) {
+  const int box = key >> box_shift, in = key & ((1 << box_shift) - 1);
+  const uint32_t off = (box << box_shift) * S::kRow + ((b / S::kAtom) << box_shift) * S::kAtom + in * S::kAtom + b % S::kAtom;
+  return off ^ ((off >> 3) & (S::kAtom == 128 ? 0x70 : 0x30));
+}
+
+template <class S, class T, bool E4M3, int D, int MT>
+__device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsigned char* sq, Control& c, Range k) {
+  using Mul = typename S::Mul;
+  using E = Elem<Mul>;
+  constexpr int kNT = S::kKG * 2;  // 8-key tiles of a warp
+  constexpr int kOT = D / 8;       // 8-column tiles of the output
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int wm = warp % S::kWM, wk = warp / S::kWM;
+  const int quad = lane & 3, r0 = lane >> 2;
+  const int box_shift = min(P.page_shift, 6);
+  const uint32_t ring_u = smem_u32(ring), sq_u = smem_u32(sq);
+  Turn turn;
+  bool dead = false;
+
+  // This lane's ldmatrix rows: byte `b` (a multiple of 32) of its key of a 16-key group is at group + run of b +
+  // row + ((b % kAtom) ^ x).  Keys: the two 16-byte pieces vary fastest over the matrices; values: the keys do.
+  const int k_key = ((lane >> 4) << 3) + (lane & 7), v_key = (((lane >> 3) & 1) << 3) + (lane & 7);
+  auto permuted = [](int key, int piece) { return (uint32_t)((piece << 4) ^ (S::kAtom == 128 ? (key & 7) << 4 : ((key >> 1) & 3) << 4)); };
+  const uint32_t k_x = permuted(k_key, (lane >> 3) & 1), v_x = permuted(v_key, lane >> 4);
+  const uint32_t run_bytes = (uint32_t)S::kAtom << box_shift;
+  uint32_t group_at[S::kKG];
+#pragma unroll
+  for (int i = 0; i < S::kKG; ++i) {
+    const int key = (wk * S::kKG + i) * 16;
+    group_at[i] = (key >> box_shift << box_shift) * S::kRow + (key & ((1 << box_shift) - 1)) * S::kAtom;
+  }
+
+  Segment g;
+  while (next_segment(P, k, g)) {
+    const int rows_here = g.live;
+
+    // queries into shared memory, rows past the end zero
+    bar_warps();
+    for (int i = threadIdx.x; i < MT * (D / 8); i += 32 * kWarps) {
+      const int m = i / (D / 8), piece = i % (D / 8);
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (m < rows_here) {
+        const int f = g.mt * MT + m, j = f / P.group;
+        x = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + (g.q0 + j) * P.q_stride +
+                                            (g.h * P.group + f - j * P.group) * D + piece * 8);
+      }
+      if (S::kScaleQ) {
+        // bf16 to f16: a row is scaled by a power of two that brings its largest value near 2^14, so every
+        // value keeps its bits unless it is below 2^-28 of the largest
+        const float2 a = Elem<__nv_bfloat16>::unpack(x.x), b = Elem<__nv_bfloat16>::unpack(x.y),
+                     d = Elem<__nv_bfloat16>::unpack(x.z), e = Elem<__nv_bfloat16>::unpack(x.w);
+        float top = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))),
+                          fmaxf(fmaxf(fabsf(d.x), fabsf(d.y)), fmaxf(fabsf(e.x), fabsf(e.y))));
+#pragma unroll
+        for (int o = D / 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 240);      // biased exponent
+        const float up = __uint_as_float((uint32_t)(127 + 14 + 127 - ex) << 23);  // 2^(14 - exponent)
+        if (piece == 0) c.qinv[m] = __uint_as_float((uint32_t)(ex - 14) << 23);
+        x = make_uint4(Elem<__half>::pack(a.x * up, a.y * up), Elem<__half>::pack(b.x * up, b.y * up),
+                       Elem<__half>::pack(d.x * up, d.y * up), Elem<__half>::pack(e.x * up, e.y * up));
+      }
+      *reinterpret_cast<uint4*>(sq + m * S::kQRow + piece * 16) = x;
+    }
+    bar_warps();
+
+    // a fragment of 16 query rows and 16 columns; with 8-bit keys the columns are permuted as the keys' bytes come
+    auto q_frag = [&](uint32_t (&a)[4], int ks) {
+      if (E4M3) {
+        const unsigned char* p = sq + (wm * 16 + r0) * S::kQRow + ks * 32 + quad * 8;
+        const uint2 x = *reinterpret_cast<const uint2*>(p), y = *reinterpret_cast<const uint2*>(p + 8 * S::kQRow);
+        a[0] = x.x;
+        a[1] = y.x;
+        a[2] = x.y;
+        a[3] = y.y;
+      } else {
+        ldsm(a, sq_u + (wm * 16 + (lane & 15)) * S::kQRow + ks * 32 + (lane >> 4) * 16);
+      }
+    };
+    uint32_t qf[S::kQRegs ? D / 16 : 1][4];
+    if (S::kQRegs) {
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) q_frag(qf[S::kQRegs ? ks : 0], ks);
+    }
+    // positions of this thread's two rows; rows past the end see nothing
+    const int m0 = wm * 16 + r0, m1 = m0 + 8;
+    const int p0 = m0 < rows_here ? g.len - g.n + (g.mt * MT + m0) / P.group : -1;
+    const int p1 = m1 < rows_here ? g.len - g.n + (g.mt * MT + m1) / P.group : -1;
+    float c0 = P.scale_log2, c1 = P.scale_log2;
+    if (E4M3 && P.k_scale) {
+      const float s = P.k_scale[g.h];
+      c0 *= s;
+      c1 *= s;
+    }
+    if (S::kScaleQ) {
+      c0 *= c.qinv[m0];
+      c1 *= c.qinv[m1];
+    }
+
+    float o[kOT][4];
+#pragma unroll
+    for (int i = 0; i < kOT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+    float mx0 = -INFINITY, mx1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+
+    Turn keys, values;
+    for (int i = 0; i < g.count; ++i) {
+      keys = values = turn;
+      values.next<S::kSlots>();
+      const uint32_t kt = ring_u + keys.slot * S::kSlot + k_key * S::kAtom, vt = ring_u + values.slot * S::kSlot + v_key * S::kAtom;
+      const int base = tile_of(g.u, g.from + i) * kTile;
+      if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&c.full[keys.slot], keys.parity, P.spin_limit, 0u));
+      const int bad = c.bad[keys.slot];
+      // does any live row not see all of the tile?
+      const bool part = base + kTile - 1 > g.u.pos0 || bad != 0 ||
+                        (P.window > 0 && base <= g.u.pos1 - P.window && base + kTile > P.sinks);
+
+      // scores
+      float s[kNT][4];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+#pragma unroll
+      for (int b0 = 0; b0 < S::kRow; b0 += 32) {  // 32 bytes of every key: 16 columns, or 32 of 8 bits
+        constexpr int kSteps = E4M3 ? 2 : 1;
+        const int ks = b0 / 32 * kSteps;
+        uint32_t qa[kSteps][4];
+        if (!S::kQRegs) {
+#pragma unroll
+          for (int h = 0; h < kSteps; ++h) q_frag(qa[h], ks + h);
+        }
+#pragma unroll
+        for (int gk = 0; gk < S::kKG; ++gk) {
+          uint32_t b[4];
+          ldsm(b, kt + group_at[gk] + b0 / S::kAtom * run_bytes + ((b0 % S::kAtom) ^ k_x));
+#pragma unroll
+          for (int h = 0; h < kSteps; ++h) {
+            const uint32_t(&a)[4] = S::kQRegs ? qf[S::kQRegs ? ks + h : 0] : qa[h];
+            if (E4M3) {
+              mma<Mul>(s[2 * gk], a, e4m3_f16(b[h]), e4m3_f16(b[h] >> 16));
+              mma<Mul>(s[2 * gk + 1], a, e4m3_f16(b[2 + h]), e4m3_f16(b[2 + h] >> 16));
+            } else {
+              mma<Mul>(s[2 * gk], a, b[0], b[1]);
+              mma<Mul>(s[2 * gk + 1], a, b[2], b[3]);
+            }
+          }
+        }
+      }
+      const bool held = i + 1 == g.count;  // the last tile's room serves the join below
+      __syncwarp();
+      if (!held && lane == 0) arrive(&c.empty[keys.slot]);
+
+      // is key `in` of the tile visible from position p?
+      auto sees = [&](int in, int p) {
+        const int key = base + in;
+        return key <= p && (P.window <= 0 || key > p - P.window || key < P.sinks) && !((bad >> (in >> 4)) & 1);
+      };
+      if (part) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int in = wk * S::kKG * 16 + n * 8 + 2 * quad + e;
+            if (!sees(in, p0)) s[n][e] = -INFINITY;
+            if (!sees(in, p1)) s[n][2 + e] = -INFINITY;
+          }
+      }
+
+      // softmax of this warp's keys
+      float t0 = s[0][0], t1 = s[0][2];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        t0 = fmaxf(t0, fmaxf(s[n][0], s[n][1]));
+        t1 = fmaxf(t1, fmaxf(s[n][2], s[n][3]));
+      }
+      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
+      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
+      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
+      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
+      const float n0 = fmaxf(mx0, t0 * c0), n1 = fmaxf(mx1, t1 * c1);
+      const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
+      if (__any_sync(0xffffffffu, n0 != mx0 || n1 != mx1)) {
+        const float a0 = ex2(mx0 - z0), a1 = ex2(mx1 - z1);
+        l0 *= a0;
+        l1 *= a1;
+#pragma unroll
+        for (int d = 0; d < kOT; ++d) {
+          o[d][0] *= a0;
+          o[d][1] *= a0;
+          o[d][2] *= a1;
+          o[d][3] *= a1;
+        }
+        mx0 = n0;
+        mx1 = n1;
+      }
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        s[n][0] = ex2(fmaf(s[n][0], c0, -z0));
+        s[n][1] = ex2(fmaf(s[n][1], c0, -z0));
+        s[n][2] = ex2(fmaf(s[n][2], c1, -z1));
+        s[n][3] = ex2(fmaf(s[n][3], c1, -z1));
+        l0 += s[n][0] + s[n][1];
+        l1 += s[n][2] + s[n][3];
+      }
+
+      // times the values
+      if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&c.full[values.slot], values.parity, P.spin_limit, 0u));
+      bool odd = false;  // a value of a partly visible tile is not finite
+      auto clean = [&](uint32_t& x) {
+        const uint32_t y = E::finite(x);
+        odd |= y != x;
+        x = y;
+      };
+#pragma unroll
+      for (int gk = 0; gk < S::kKG; ++gk) {
+        // weights are rounded to 16 bits for the product (half a step, 2^-9 or 2^-12 of each, random in sign);
+        // their sum is not
+        const uint32_t a[4] = {E::pack(s[2 * gk][0], s[2 * gk][1]), E::pack(s[2 * gk][2], s[2 * gk][3]),
+                               E::pack(s[2 * gk + 1][0], s[2 * gk + 1][1]), E::pack(s[2 * gk + 1][2], s[2 * gk + 1][3])};
+#pragma unroll
+        for (int b0 = 0; b0 < S::kRow; b0 += 32) {
+          const int d = b0 / 32;
+          uint32_t b[4];
+          ldsm_t(b, vt + group_at[gk] + b0 / S::kAtom * run_bytes + ((b0 % S::kAtom) ^ v_x));
+          if (!E4M3) {
+            if (part) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) clean(b[e]);
+            }
+            mma<Mul>(o[2 * d], a, b[0], b[1]);
+            mma<Mul>(o[2 * d + 1], a, b[2], b[3]);
+          } else {
+            // a register holds two neighbouring columns of two keys: even columns to one product, odd to the other
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t even = __byte_perm(b[2 * h], b[2 * h + 1], 0x6420), odds = __byte_perm(b[2 * h], b[2 * h + 1], 0x7531);
+              uint32_t f[4] = {e4m3_f16(even), e4m3_f16(even >> 16), e4m3_f16(odds), e4m3_f16(odds >> 16)};
+              if (part) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) clean(f[e]);
+              }
+              mma<Mul>(o[(4 * d + 2 * h) % kOT], a, f[0], f[1]);
+              mma<Mul>(o[(4 * d + 2 * h + 1) % kOT], a, f[2], f[3]);
+            }
+          }
+        }
+      }
+      if (part && __any_sync(0xffffffffu, odd)) {
+        // Some value in the tile is not finite and was left out above; rows that see its key take it here, one
+        // key at a time (0 * infinity of a row that does not see it must not happen).
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+#pragma unroll 1
+          for (int src = 0; src < 8; ++src) {
+            const int from = (lane & ~3) + (src >> 1);
+            const float e0 = __shfl_sync(0xffffffffu, s[n][0], from), e1 = __shfl_sync(0xffffffffu, s[n][1], from);
+            const float e2 = __shfl_sync(0xffffffffu, s[n][2], from), e3 = __shfl_sync(0xffffffffu, s[n][3], from);
+            const float w0 = src & 1 ? e1 : e0, w1 = src & 1 ? e3 : e2;
+            const int in = wk * S::kKG * 16 + n * 8 + src;
+            const bool v0 = sees(in, p0), v1 = sees(in, p1);
+#pragma unroll
+            for (int d = 0; d < kOT; ++d)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const int col = E4M3 ? (d >> 1) * 16 + 4 * quad + 2 * x + (d & 1) : d * 8 + 2 * quad + x;
+                const unsigned char* at = ring + values.slot * S::kSlot + place_of<S>(in, col * S::kEl, box_shift);
+                const float v = E4M3 ? E::unpack(e4m3_f16(*at)).x : E::unpack(*reinterpret_cast<const unsigned short*>(at)).x;
+                if (!isfinite(v)) {
+                  if (v0) o[d][x] = fmaf(w0, v, o[d][x]);
+                  if (v1) o[d][2 + x] = fmaf(w1, v, o[d][2 + x]);
+                }
+              }
+          }
+        }
+      }
+      __syncwarp();
+      if (!held && lane == 0) arrive(&c.empty[values.slot]);
+      turn = values;
+      turn.next<S::kSlots>();
+    }
+    if (dead && lane == 0) atomicOr(&P.row_status[g.row], (uint32_t)SS_ST_COPY_TIMEOUT);
+
+    // ---- join: the warps of the unit, then the CTAs
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    // adds another piece
+    auto take = [&](float ym0, float ym1, float yl0, float yl1, const float4* at) {
+      const float n0 = fmaxf(mx0, ym0), n1 = fmaxf(mx1, ym1);
+      const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
+      const float a0 = ex2(mx0 - z0), a1 = ex2(mx1 - z1), b0 = ex2(ym0 - z0), b1 = ex2(ym1 - z1);
+      l0 = l0 * a0 + yl0 * b0;
+      l1 = l1 * a1 + yl1 * b1;
+#pragma unroll
+      for (int d = 0; d < kOT; ++d) {
+        const float4 y = at[d * 32];
+        o[d][0] = o[d][0] * a0 + y.x * b0;
+        o[d][1] = o[d][1] * a0 + y.y * b0;
+        o[d][2] = o[d][2] * a1 + y.z * b1;
+        o[d][3] = o[d][3] * a1 + y.w * b1;
+      }
+      mx0 = n0;
+      mx1 = n1;
+    };
+    auto join_warps = [&]() {
+#pragma unroll
+      for (int half = S::kWK / 2; half > 0; half >>= 1) {
+        // warps [half, 2 half) along the keys hand their piece to warps [0, half)
+        bar_warps();
+        const int area = S::kWM == 1 ? wk % half : wm;  // at most two pieces at a time
+        float4* at = reinterpret_cast<float4*>(ring + (area ? values.slot : keys.slot) * S::kSlot) + lane;
+        if (wk >= half && wk < 2 * half) {
+#pragma unroll
+          for (int d = 0; d < kOT; ++d) at[d * 32] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
+          if (quad == 0) {
+            c.ml[warp][r0][0] = mx0;
+            c.ml[warp][r0][1] = l0;
+            c.ml[warp][r0 + 8][0] = mx1;
+            c.ml[warp][r0 + 8][1] = l1;
+          }
+        }
+        bar_warps();
+        if (wk < half) {
+          const int other = warp + half * S::kWM;
+          take(c.ml[other][r0][0], c.ml[other][r0 + 8][0], c.ml[other][r0][1], c.ml[other][r0 + 8][1], at);
+        }
+      }
+    };
+    join_warps();
+
+    bool write = true;
+    if (g.ca != g.cb) {
+      const int ca = g.ca, cb = g.cb;
+      auto piece = [&](int x) { return (size_t)(2 * x + (x == ca ? 1 : 0)) * MT; };  // a range's last unit / its first
+      if (wk == 0) {
+        const size_t mine = piece(blockIdx.x);
+        float4* to = reinterpret_cast<float4*>(P.part + mine * D) + wm * (16 * D / 4) + lane;
+#pragma unroll
+        for (int d = 0; d < kOT; ++d) to[d * 32] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
+        if (quad == 0) {
+          P.ml[mine + m0] = make_float2(mx0, l0);
+          P.ml[mine + m1] = make_float2(mx1, l1);
+        }
+      }
+      __threadfence();
+      bar_warps();
+      if (threadIdx.x == 0) {
+        const uint32_t before = atomicAdd(&P.counters[ca], 1u);
+        c.last = before == (uint32_t)(cb - ca);
+        if (c.last) P.counters[ca] = 0;
+      }
+      bar_warps();
+      write = c.last != 0;
+      if (write) {
+        __threadfence();
+        mx0 = mx1 = -INFINITY;
+        l0 = l1 = 0.0f;
+#pragma unroll
+        for (int d = 0; d < kOT; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
+        for (int x = ca + wk; x <= cb; x += S::kWK) {
+          const size_t its = piece(x);
+          const float2 y0 = P.ml[its + m0], y1 = P.ml[its + m1];
+          take(y0.x, y1.x, y0.y, y1.y, reinterpret_cast<const float4*>(P.part + its * D) + wm * (16 * D / 4) + lane);
+        }
+        join_warps();
+      }
+    }
+
+    if (write && wk == 0) {
+      float f0 = l0 == 0.0f ? 0.0f : 1.0f / l0, f1 = l1 == 0.0f ? 0.0f : 1.0f / l1;
+      if (E4M3 && P.v_scale) {
+        f0 *= P.v_scale[g.h];
+        f1 *= P.v_scale[g.h];
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int m = x ? m1 : m0;
+        if (m < rows_here) {
+          const int f = g.mt * MT + m, j = f / P.group, head = g.h * P.group + f - j * P.group;
+          const float r = x ? f1 : f0;
+          T* to = static_cast<T*>(P.out) + (g.q0 + j) * P.out_stride + head * D;
+          if (E4M3) {
+#pragma unroll
+            for (int d = 0; d < kOT; d += 2)
+              *reinterpret_cast<uint2*>(to + d * 8 + quad * 4) =
+                  make_uint2(Elem<T>::pack(o[d][2 * x] * r, o[d + 1][2 * x] * r),
+                             Elem<T>::pack(o[d][2 * x + 1] * r, o[d + 1][2 * x + 1] * r));
+          } else {
+#pragma unroll
+            for (int d = 0; d < kOT; ++d)
+              *reinterpret_cast<uint32_t*>(to + d * 8 + quad * 2) = Elem<T>::pack(o[d][2 * x] * r, o[d][2 * x + 1] * r);
+          }
+          if (P.lse && quad == 0) {
+            const float l = x ? l1 : l0, mx = x ? mx1 : mx0;
+            P.lse[(size_t)(g.q0 + j) * (P.group * P.hkv) + head] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
+          }
+        }
+      }
+    }
+    // the room is given back to the loads
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      arrive(&c.empty[keys.slot]);
+      arrive(&c.empty[values.slot]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+template <class T, bool E4M3, int D, int MT>
+__global__ void __launch_bounds__(kThreads, (Shape<T, E4M3, D, MT>::kCtas))
+    attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  using S = Shape<T, E4M3, D, MT>;
+  static_assert(S::kSlots >= 4, "ring length");
+  extern __shared__ unsigned char raw[];
+  unsigned char* ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  unsigned char* sq = ring + S::kSlots * S::kSlot;
+  Control& c = *reinterpret_cast<Control*>(sq + MT * S::kQRow);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(&c.full[i]);
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&c.empty[i])), "r"(kWarps) : "memory");
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kWarps && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &mv : &mk) : "memory");
+
+  find_range<kThreads>(P, c.range_sums, &c.range);
+  if (c.range.ctas == 0) return;
+  if (warp == kWarps) load_warp<S, MT>(P, &mk, &mv, ring, c, c.range);
+  else compute_warps<S, T, E4M3, D, MT>(P, ring, sq, c, c.range);
+}
+
+template <class T, bool E4M3, int D, int MT>
+AttendKernel entry() {
+  using S = Shape<T, E4M3, D, MT>;
+  return {reinterpret_cast<const void*>(&attend_kernel<T, E4M3, D, MT>), kThreads, S::kSlots, 1, smem_bytes<S>(MT)};
+}
+template <class T, bool E4M3, int D>
+AttendKernel by_rows(int mt) {
+  return mt == 16 ? entry<T, E4M3, D, 16>() : mt == 32 ? entry<T, E4M3, D, 32>() : entry<T, E4M3, D, 64>();
+}
+template <class T, bool E4M3>
+AttendKernel pick(int d, int mt) {
+  return d == 64 ? by_rows<T, E4M3, 64>(mt) : d == 128 ? by_rows<T, E4M3, 128>(mt) : by_rows<T, E4M3, 256>(mt);
+}
+
+}  // namespace kv8
+}  // namespace ss

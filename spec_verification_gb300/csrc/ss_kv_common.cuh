@@ -11,7 +11,7 @@ struct ss_kv_plan {
   ss_kv_config c;
   int page_shift;
   int sms;
-  int row_tile;         // query rows per unit of ss_attend: 16, 32 or 64
+  int row_tile;         // query rows per unit of ss_attend: 16, 32, 64 or (16-bit caches) 128
   int attend_grid;      // persistent CTAs of ss_attend
   size_t off_part, off_ml, ws_bytes;  // workspace: counters at 0, partial outputs, their (max, sum)
 };
@@ -58,15 +58,16 @@ struct AttendParams {
   const float *k_scale, *v_scale;
   float scale_log2;     // scale * log2(e)
   int B, hkv, group, max_blocks, num_pages, page_shift, max_tokens, window, sinks;
+  int rows, slots, q_bufs;  // query rows of a unit, tiles in the ring, query buffers
   uint32_t* counters;   // [grid] arrivals at the unit that a CTA's range ends in
   float* part;          // [2 * grid][row_tile][head_dim]
   float2* ml;           // [2 * grid][row_tile] (max in log2 units, sum)
   uint32_t spin_limit;
 };
-// The kernel of a head size, types and row tile, its block size and shared memory.
+// The kernel of a head size, types and row tile, its block size, ring, query buffers and shared memory.
 struct AttendKernel {
   const void* fn;
-  int threads;
+  int threads, slots, q_bufs;
   size_t smem;
 };
 AttendKernel kv_attend_bf16(int head_dim, int row_tile);       // bf16 activations, bf16 cache

@@ -1,0 +1,188 @@
+// How ss_attend's work is cut up: units, their key tiles, and the ranges of
+// tiles that the CTAs of its fixed grid take.
+//
+//  - A unit is (row, key head, tile of `rows` query rows); query row i of a
+//    unit is token i / group, head i % group, so the heads that share a key
+//    head share its loads.  A unit's keys are tiles of 64.
+//  - The units, in order, form one line in which a unit is as long as its tiles
+//    plus kUnitCost (what starting and ending one costs, in tiles).  The line
+//    is cut into equal parts, one per CTA: the split follows from the lengths
+//    on the device, every CTA has the same work whatever the rows' lengths
+//    are, and the launch never changes.  Tile i of a unit that starts at u is
+//    at u + kUnitCost + i and belongs to the CTA whose part that lies in.
+#pragma once
+
+#include "ss_kv_common.cuh"
+
+namespace ss {
+namespace kv {
+
+constexpr int kTile = 64;  // keys of a tile
+constexpr int kUnitCost = 2;
+
+struct Row {
+  int q0, n, len;
+  uint32_t status;
+};
+
+__device__ __forceinline__ Row row_info(const AttendParams& P, int r) {
+  Row w;
+  w.q0 = P.cu_new[r];
+  const int q1 = P.cu_new[r + 1];
+  w.n = q1 - w.q0;
+  w.len = P.seq_len[r];
+  w.status = 0;
+  if (w.q0 < 0 || q1 < w.q0 || q1 > P.max_tokens) {
+    w.n = 0;
+    w.status = SS_ST_CAPACITY;
+  }
+  if (w.len < 0 || w.len > P.max_blocks << P.page_shift) {
+    w.len = 0;
+    w.status |= SS_ST_BAD_PARAM;
+  }
+  return w;
+}
+
+// Key tiles of a unit: `sink` tiles from 0, then from `first` on.
+struct Unit {
+  int pos0, pos1;  // positions of its first and last token (may be negative)
+  int sink, first, tiles;
+};
+
+__device__ __forceinline__ Unit unit_info(const AttendParams& P, const Row& w, int mt) {
+  Unit u;
+  const int j0 = mt * P.rows / P.group;
+  const int j1 = min(w.n - 1, (mt * P.rows + P.rows - 1) / P.group);
+  u.pos0 = w.len - w.n + j0;
+  u.pos1 = w.len - w.n + j1;
+  u.sink = 0;
+  u.first = 0;
+  if (P.window > 0) {
+    u.first = max(0, u.pos0 - P.window + 1) / kTile;
+    u.sink = min((P.sinks + kTile - 1) / kTile, u.first);
+  }
+  // a unit without a visible key still has one (masked) tile: its output is written
+  u.tiles = u.pos1 < 0 ? 1 : u.sink + u.pos1 / kTile - u.first + 1;
+  return u;
+}
+__device__ __forceinline__ int tile_of(const Unit& u, int i) { return i < u.sink ? i : i - u.sink + u.first; }
+
+__device__ __forceinline__ int row_units(const AttendParams& P, const Row& w) {  // of one key head
+  return (w.n * P.group + P.rows - 1) / P.rows;
+}
+__device__ __forceinline__ long long row_length(const AttendParams& P, const Row& w) {  // of one key head, on the line
+  long long s = 0;
+  for (int m = 0; m < row_units(P, w); ++m) s += unit_info(P, w, m).tiles + kUnitCost;
+  return s;
+}
+
+// A CTA's part of the line and where it starts: `skip` tiles into unit (row, h, mt), which starts at `unit`.
+struct Range {
+  long long total, unit, end;
+  int ctas, row, h, mt, skip;
+};
+
+// A CTA's part of one unit.
+struct Segment {
+  Unit u;
+  int row, h, mt, q0, n, len;
+  int from, count;  // tiles [from, from + count) of the unit
+  int live;         // query rows
+  int ca, cb;       // first and last CTA that have tiles of the unit
+};
+
+// The next segment of the range; false at its end.
+__device__ __forceinline__ bool next_segment(const AttendParams& P, Range& k, Segment& g) {
+  if (k.unit >= k.end) return false;
+  Row w = row_info(P, k.row);
+  while (k.mt >= row_units(P, w)) {  // next key head, next row with work (the line ends before the rows do)
+    k.mt = 0;
+    if (w.n == 0 || ++k.h == P.hkv) {
+      k.h = 0;
+      w = row_info(P, ++k.row);
+    }
+  }
+  g.u = unit_info(P, w, k.mt);
+  g.row = k.row;
+  g.h = k.h;
+  g.mt = k.mt;
+  g.q0 = w.q0;
+  g.n = w.n;
+  g.len = w.len;
+  g.from = k.skip;
+  const long long at = k.unit + kUnitCost;  // of tile 0
+  g.count = (int)min((long long)g.u.tiles, k.end - at) - g.from;
+  if (g.count <= 0) return false;  // the part ends inside the unit's start
+  g.live = min(P.rows, w.n * P.group - k.mt * P.rows);
+  // owner of place t: the largest c with c * total / ctas <= t
+  g.ca = g.cb = blockIdx.x;
+  if (g.from != 0 || g.count != g.u.tiles) {
+    g.ca = (int)(((at + 1) * k.ctas - 1) / k.total);
+    g.cb = (int)(((at + g.u.tiles) * k.ctas - 1) / k.total);
+  }
+  k.unit = at + g.u.tiles;
+  k.skip = 0;
+  ++k.mt;
+  return true;
+}
+
+// This CTA's range, by all NT threads of the block: every thread sums a run of rows.  `sums` holds NT / 32 values,
+// `out` gets the range; row status bits of bad rows are set.  ctas == 0: nothing for this CTA.
+template <int NT>
+__device__ __forceinline__ void find_range(const AttendParams& P, long long* sums, Range* out) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int run = (P.B + NT - 1) / NT;
+  const int ra = min(P.B, tid * run), rb = min(P.B, ra + run);
+  long long mine = 0;
+  for (int r = ra; r < rb; ++r) {
+    const Row w = row_info(P, r);
+    if (w.status && blockIdx.x == 0) atomicOr(&P.row_status[r], w.status);
+    mine += row_length(P, w) * P.hkv;
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += y;
+  }
+  if (lane == 31) sums[warp] = incl;
+  if (tid == 0) out->ctas = 0;
+  __syncthreads();
+  long long total = 0, before = incl - mine;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    const long long y = sums[w];
+    if (w < warp) before += y;
+    total += y;
+  }
+  const int ctas = (int)min((long long)gridDim.x, total);
+  const long long start = ctas ? total * blockIdx.x / ctas : 0;
+  if ((int)blockIdx.x < ctas && start >= before && start < before + mine) {
+    long long off = start - before, per_head = 0;
+    Range k;
+    k.total = total;
+    k.ctas = ctas;
+    k.end = total * (blockIdx.x + 1) / ctas;
+    Row w;
+    for (k.row = ra; k.row < rb; ++k.row) {
+      w = row_info(P, k.row);
+      per_head = row_length(P, w);
+      if (off < per_head * P.hkv) break;
+      off -= per_head * P.hkv;
+    }
+    k.h = (int)(off / per_head);
+    off -= k.h * per_head;
+    k.mt = 0;
+    for (int n = unit_info(P, w, 0).tiles + kUnitCost; off >= n; n = unit_info(P, w, k.mt).tiles + kUnitCost) {
+      off -= n;
+      ++k.mt;
+    }
+    k.unit = start - off;
+    k.skip = max(0, (int)off - kUnitCost);
+    *out = k;
+  }
+  __syncthreads();
+}
+
+}  // namespace kv
+}  // namespace ss
