@@ -164,9 +164,7 @@ ss_status ss_kv_plan_create(ss_kv_plan** out, const ss_kv_config* config) {
   const int64_t rows = (int64_t)c.max_new * group;
   const int row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || c.cache_dtype == SS_E4M3 ? 64 : 128;
   const ss::AttendKernel k = attend_kernel(c, row_tile);
-  int occ = 0;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k.fn, k.threads, k.smem);
   if (e != cudaSuccess) return cuda_fail(e, "kernel attributes");
   ss_kv_plan* p = new (std::nothrow) ss_kv_plan();
   if (!p) return fail(SS_ERR_ARG, "out of host memory");
@@ -174,7 +172,7 @@ ss_status ss_kv_plan_create(ss_kv_plan** out, const ss_kv_config* config) {
   p->page_shift = __builtin_ctz((unsigned)c.page_size);
   p->sms = sms;
   p->row_tile = row_tile;
-  p->attend_grid = std::max(occ, 1) * sms;
+  p->attend_grid = k.ctas * sms;
   p->off_part = up256((size_t)p->attend_grid * 4);
   p->off_ml = p->off_part + up256((size_t)2 * p->attend_grid * row_tile * c.head_dim * 4);
   p->ws_bytes = p->off_ml + up256((size_t)2 * p->attend_grid * row_tile * 8);

@@ -721,6 +721,7 @@ AttendKernel entry(int rows) {
   AttendKernel k;
   k.fn = reinterpret_cast<const void*>(&attend_kernel<T, D>);
   k.threads = kThreads;
+  k.ctas = S::kCtas;
   k.q_bufs = rows <= 64 ? 2 : 1;  // a second buffer hides the gathering of the next segment's queries; 128 rows leave no room
   const int q = k.q_bufs * rows * D * 2;
   k.slots = (share - 1024 - q) / S::kSlot;

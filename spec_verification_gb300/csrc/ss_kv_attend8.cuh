@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, E4M3, D, MT>::kCtas))
 template <class T, bool E4M3, int D, int MT>
 AttendKernel entry() {
   using S = Shape<T, E4M3, D, MT>;
-  return {reinterpret_cast<const void*>(&attend_kernel<T, E4M3, D, MT>), kThreads, S::kSlots, 1, smem_bytes<S>(MT)};
+  return {reinterpret_cast<const void*>(&attend_kernel<T, E4M3, D, MT>), kThreads, S::kSlots, 1, S::kCtas, smem_bytes<S>(MT)};
 }
 template <class T, bool E4M3, int D>
 AttendKernel by_rows(int mt) {

@@ -67,7 +67,7 @@ struct AttendParams {
 // The kernel of a head size, types and row tile, its block size, ring, query buffers and shared memory.
 struct AttendKernel {
   const void* fn;
-  int threads, slots, q_bufs;
+  int threads, slots, q_bufs, ctas;  // ctas: per SM
   size_t smem;
 };
 AttendKernel kv_attend_bf16(int head_dim, int row_tile);       // bf16 activations, bf16 cache
