@@ -351,6 +351,8 @@ ss_status ss_attend(const ss_attend_batch* b, const ss_kv_cache* cache) {
   P.rows = p->row_tile;
   P.slots = k.slots;
   P.q_bufs = k.q_bufs;
+  while ((1u << P.group_shift) < (uint32_t)P.group) ++P.group_shift;
+  P.group_mul = (uint32_t)(((1ull << 32) * ((1ull << P.group_shift) - P.group)) / P.group + 1);
   void* args[] = {&P, &mk, &mv};
   const Range range("ss_attend");
   const cudaError_t e = cudaLaunchKernel(k.fn, dim3(p->attend_grid), dim3(k.threads), args, k.smem, static_cast<cudaStream_t>(b->stream));

@@ -256,25 +256,6 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
     if (dead) break;
     if (!more) g.count = 0;  // the end of the range
     if (lane == 0) c.seg[sg & 1] = g;
-    if (more) {
-      const uint32_t to = sq + (P.q_bufs == 2 && (sg & 1) ? q_bytes : 0u);
-      for (int i = lane; i < g.live * (D / 8); i += 32) {
-        const int m = i / (D / 8), piece = i % (D / 8), f = g.mt * P.rows + m, j = f / P.group;
-        const T* src = static_cast<const T*>(P.q) + (g.q0 + j) * P.q_stride + (g.h * P.group + f - j * P.group) * D + piece * 8;
-        const uint32_t dst = to + (piece >> 3) * (P.rows * 128) + m * 128 + (((piece & 7) ^ (m & 7)) << 4);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-      }
-    }
-    bool published = false;
-    auto publish = [&]() {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      proxy_fence();
-      __syncwarp();
-      if (lane == 0) arrive(&c.seg_full[sg & 1]);
-      published = true;
-    };
-    if (!more) publish();
-
     const int32_t* table = P.block_table + (long long)g.row * P.max_blocks;
     const int used = (g.len + page_mask) >> P.page_shift;
     // The page of this lane's copy in the batch from tile i0 on: num_pages, past the cache, where nothing is held
@@ -292,6 +273,24 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
       return id;
     };
     int next = fetch(0);
+    if (more) {
+      const uint32_t to = sq + (P.q_bufs == 2 && (sg & 1) ? q_bytes : 0u);
+      for (int i = lane; i < g.live * (D / 8); i += 32) {
+        const int m = i / (D / 8), piece = i % (D / 8), f = g.mt * P.rows + m, j = token_of(P, f);
+        const T* src = static_cast<const T*>(P.q) + (g.q0 + j) * P.q_stride + (g.h * P.group + f - j * P.group) * D + piece * 8;
+        const uint32_t dst = to + (piece >> 3) * (P.rows * 128) + m * 128 + (((piece & 7) ^ (m & 7)) << 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+      }
+    }
+    bool published = false;
+    auto publish = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) arrive(&c.seg_full[sg & 1]);
+      published = true;
+    };
+    if (!more) publish();
     for (int i0 = 0; i0 < g.count && !dead; i0 += batch) {
       int id = next;
       const uint32_t bad_lanes = __ballot_sync(0xffffffffu, id < 0);
@@ -429,7 +428,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* ring, Contro
     if (!more) break;
     const bool busy = warp * 32 < g.live;  // the warp has live rows
     const bool live = tid < g.live;
-    const int f = g.mt * P.rows + tid, token = f / P.group;
+    const int f = g.mt * P.rows + tid, token = token_of(P, f);
     const int p = live ? g.len - g.n + token : -1;
     const float scale = P.scale_log2;
     float mx = -INFINITY, l = 0.0f;
@@ -623,38 +622,50 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* ring, Contro
     bar_softmax();
     if (!c.last) continue;
     __threadfence();
-    // four columns of a row at a time, the pieces in order
-    for (int e = tid; e < P.rows * (D / 4); e += 32 * kSoftmaxWarps) {
-      const int m = e % P.rows, col = e / P.rows * 4;
-      if (m >= g.live) continue;
+    // Four columns of a row are an item; a thread's items are of one row (rows divides 128).  Loads of kPieces pieces
+    // of kItems items are in flight together; the pieces are added in order.
+    constexpr int kPieces = 4, kItems = 4;
+    const int jm = tid & (P.rows - 1);
+    if (jm >= g.live) continue;
+    const int fm = g.mt * P.rows + jm, tm = token_of(P, fm), head = g.h * P.group + fm - tm * P.group;
+    T* to = static_cast<T*>(P.out) + (g.q0 + tm) * P.out_stride + head * D;
+    const int items = P.rows * (D / 4);
+    for (int e0 = tid; e0 < items; e0 += 128 * kItems) {
       float top = -INFINITY, sum = 0.0f;
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      auto add = [&](float2 ml, float4 y) {
-        const float n = fmaxf(top, ml.x), zn = n == -INFINITY ? 0.0f : n, a = ex2(top - zn), bb = ex2(ml.x - zn);
-        sum = sum * a + ml.y * bb;
-        o = make_float4(o.x * a + y.x * bb, o.y * a + y.y * bb, o.z * a + y.z * bb, o.w * a + y.w * bb);
-        top = n;
-      };
-      auto at = [&](int x) { return reinterpret_cast<const float4*>(P.part + piece(x) * D) + e; };
-      int x = g.ca;
-      for (; x + 4 <= g.cb + 1; x += 4) {
-        float2 ml[4];
-        float4 y[4];
+      float4 o[kItems];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          ml[n] = __ldcg(P.ml + piece(x + n) + m);
-          y[n] = __ldcg(at(x + n));
+      for (int n = 0; n < kItems; ++n) o[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int x0 = g.ca; x0 <= g.cb; x0 += kPieces) {
+        float2 ml[kPieces];
+        float4 y[kPieces][kItems];
+#pragma unroll
+        for (int x = 0; x < kPieces; ++x) {
+          const size_t its = piece(min(x0 + x, g.cb));
+          ml[x] = __ldcg(P.ml + its + jm);
+#pragma unroll
+          for (int n = 0; n < kItems; ++n)
+            y[x][n] = __ldcg(reinterpret_cast<const float4*>(P.part + its * D) + min(e0 + 128 * n, items - 1));
         }
 #pragma unroll
-        for (int n = 0; n < 4; ++n) add(ml[n], y[n]);
+        for (int x = 0; x < kPieces; ++x) {
+          if (x0 + x > g.cb) break;
+          const float n = fmaxf(top, ml[x].x), zn = n == -INFINITY ? 0.0f : n, a = ex2(top - zn), b = ex2(ml[x].x - zn);
+          sum = sum * a + ml[x].y * b;
+          top = n;
+#pragma unroll
+          for (int q = 0; q < kItems; ++q)
+            o[q] = make_float4(o[q].x * a + y[x][q].x * b, o[q].y * a + y[x][q].y * b, o[q].z * a + y[x][q].z * b, o[q].w * a + y[x][q].w * b);
+        }
       }
-      for (; x <= g.cb; ++x) add(__ldcg(P.ml + piece(x) + m), __ldcg(at(x)));
       const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
-      const int fm = g.mt * P.rows + m, jm = fm / P.group, head = g.h * P.group + fm - jm * P.group;
-      *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + (g.q0 + jm) * P.out_stride + head * D + col) =
-          make_uint2(E::pack(o.x * r, o.y * r), E::pack(o.z * r, o.w * r));
-      if (P.lse && col == 0)
-        P.lse[(size_t)(g.q0 + jm) * (P.group * P.hkv) + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+#pragma unroll
+      for (int n = 0; n < kItems; ++n) {
+        const int e = e0 + 128 * n;
+        if (e < items)
+          *reinterpret_cast<uint2*>(to + e / P.rows * 4) = make_uint2(E::pack(o[n].x * r, o[n].y * r), E::pack(o[n].z * r, o[n].w * r));
+      }
+      if (P.lse && e0 < P.rows)
+        P.lse[(size_t)(g.q0 + tm) * (P.group * P.hkv) + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
     }
   }
 }
@@ -671,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas))
   unsigned char* ring = base + P.q_bufs * P.rows * D * 2;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   find_range<kThreads>(P, c.sums, &c.range);
-  if (c.range.ctas == 0) return;
+  if (c.range.cut.ctas == 0) return;
   if (tid == 0) {
     for (int i = 0; i < P.slots; ++i) {
       mbar_init_n(&c.full[i], 1);

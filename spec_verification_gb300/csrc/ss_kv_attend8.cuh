@@ -320,7 +320,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
       const int m = i / (D / 8), piece = i % (D / 8);
       uint4 x = make_uint4(0u, 0u, 0u, 0u);
       if (m < rows_here) {
-        const int f = g.mt * MT + m, j = f / P.group;
+        const int f = g.mt * MT + m, j = token_of(P, f);
         x = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + (g.q0 + j) * P.q_stride +
                                             (g.h * P.group + f - j * P.group) * D + piece * 8);
       }
@@ -363,8 +363,8 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
     }
     // positions of this thread's two rows; rows past the end see nothing
     const int m0 = wm * 16 + r0, m1 = m0 + 8;
-    const int p0 = m0 < rows_here ? g.len - g.n + (g.mt * MT + m0) / P.group : -1;
-    const int p1 = m1 < rows_here ? g.len - g.n + (g.mt * MT + m1) / P.group : -1;
+    const int p0 = m0 < rows_here ? g.len - g.n + token_of(P, g.mt * MT + m0) : -1;
+    const int p1 = m1 < rows_here ? g.len - g.n + token_of(P, g.mt * MT + m1) : -1;
     float c0 = P.scale_log2, c1 = P.scale_log2;
     if (E4M3 && P.k_scale) {
       const float s = P.k_scale[g.h];
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, E4M3, D, MT>::kCtas))
   if (warp == kWarps && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &mv : &mk) : "memory");
 
   find_range<kThreads>(P, c.range_sums, &c.range);
-  if (c.range.ctas == 0) return;
+  if (c.range.cut.ctas == 0) return;
   if (warp == kWarps) load_warp<S, MT>(P, &mk, &mv, ring, c, c.range);
   else compute_warps<S, T, E4M3, D, MT>(P, ring, sq, c, c.range);
 }

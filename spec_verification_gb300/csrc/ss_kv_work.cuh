@@ -19,6 +19,7 @@ namespace kv {
 
 constexpr int kTile = 64;  // keys of a tile
 constexpr int kUnitCost = 2;
+constexpr int kLeast = 1;  // least length of a part
 
 struct Row {
   int q0, n, len;
@@ -43,6 +44,11 @@ __device__ __forceinline__ Row row_info(const AttendParams& P, int r) {
   return w;
 }
 
+// Token of query row x of a row of requests: x / group.
+__device__ __forceinline__ int token_of(const AttendParams& P, int x) {
+  return (int)((__umulhi((uint32_t)x, P.group_mul) + (uint32_t)x) >> P.group_shift);
+}
+
 // Key tiles of a unit: `sink` tiles from 0, then from `first` on.
 struct Unit {
   int pos0, pos1;  // positions of its first and last token (may be negative)
@@ -51,8 +57,8 @@ struct Unit {
 
 __device__ __forceinline__ Unit unit_info(const AttendParams& P, const Row& w, int mt) {
   Unit u;
-  const int j0 = mt * P.rows / P.group;
-  const int j1 = min(w.n - 1, (mt * P.rows + P.rows - 1) / P.group);
+  const int j0 = token_of(P, mt * P.rows);
+  const int j1 = min(w.n - 1, token_of(P, mt * P.rows + P.rows - 1));
   u.pos0 = w.len - w.n + j0;
   u.pos1 = w.len - w.n + j1;
   u.sink = 0;
@@ -68,7 +74,7 @@ __device__ __forceinline__ Unit unit_info(const AttendParams& P, const Row& w, i
 __device__ __forceinline__ int tile_of(const Unit& u, int i) { return i < u.sink ? i : i - u.sink + u.first; }
 
 __device__ __forceinline__ int row_units(const AttendParams& P, const Row& w) {  // of one key head
-  return (w.n * P.group + P.rows - 1) / P.rows;
+  return (w.n * P.group + P.rows - 1) >> (31 - __clz(P.rows));
 }
 __device__ __forceinline__ long long row_length(const AttendParams& P, const Row& w) {  // of one key head, on the line
   long long s = 0;
@@ -76,10 +82,26 @@ __device__ __forceinline__ long long row_length(const AttendParams& P, const Row
   return s;
 }
 
+// The line cut into `ctas` parts: the first `longer` of them are base + 1 long, the others base.
+struct Cut {
+  long long base;
+  int longer, ctas;
+  __device__ __forceinline__ long long start(int c) const { return base * c + min(c, longer); }
+  // the part that place t lies in
+  __device__ __forceinline__ int owner(long long t) const {
+    const long long edge = (base + 1) * longer;
+    const bool first = t < edge;
+    const long long x = first ? t : t - edge, d = first ? base + 1 : base;
+    const int q = (x | d) >> 31 ? (int)(x / d) : (int)((uint32_t)x / (uint32_t)d);  // 32-bit divisions where they do
+    return first ? q : longer + q;
+  }
+};
+
 // A CTA's part of the line and where it starts: `skip` tiles into unit (row, h, mt), which starts at `unit`.
 struct Range {
-  long long total, unit, end;
-  int ctas, row, h, mt, skip;
+  Cut cut;
+  long long unit, end;
+  int row, h, mt, skip;
 };
 
 // A CTA's part of one unit.
@@ -114,12 +136,8 @@ __device__ __forceinline__ bool next_segment(const AttendParams& P, Range& k, Se
   g.count = (int)min((long long)g.u.tiles, k.end - at) - g.from;
   if (g.count <= 0) return false;  // the part ends inside the unit's start
   g.live = min(P.rows, w.n * P.group - k.mt * P.rows);
-  // owner of place t: the largest c with c * total / ctas <= t
-  g.ca = g.cb = blockIdx.x;
-  if (g.from != 0 || g.count != g.u.tiles) {
-    g.ca = (int)(((at + 1) * k.ctas - 1) / k.total);
-    g.cb = (int)(((at + g.u.tiles) * k.ctas - 1) / k.total);
-  }
+  g.ca = g.from != 0 ? k.cut.owner(at) : (int)blockIdx.x;
+  g.cb = g.from + g.count != g.u.tiles ? k.cut.owner(at + g.u.tiles - 1) : (int)blockIdx.x;
   k.unit = at + g.u.tiles;
   k.skip = 0;
   ++k.mt;
@@ -127,7 +145,7 @@ __device__ __forceinline__ bool next_segment(const AttendParams& P, Range& k, Se
 }
 
 // This CTA's range, by all NT threads of the block: every thread sums a run of rows.  `sums` holds NT / 32 values,
-// `out` gets the range; row status bits of bad rows are set.  ctas == 0: nothing for this CTA.
+// `out` gets the range; row status bits of bad rows are set.  cut.ctas == 0: nothing for this CTA.
 template <int NT>
 __device__ __forceinline__ void find_range(const AttendParams& P, long long* sums, Range* out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -146,7 +164,7 @@ __device__ __forceinline__ void find_range(const AttendParams& P, long long* sum
     if (lane >= d) incl += y;
   }
   if (lane == 31) sums[warp] = incl;
-  if (tid == 0) out->ctas = 0;
+  if (tid == 0) out->cut.ctas = 0;
   __syncthreads();
   long long total = 0, before = incl - mine;
 #pragma unroll
@@ -155,14 +173,17 @@ __device__ __forceinline__ void find_range(const AttendParams& P, long long* sum
     if (w < warp) before += y;
     total += y;
   }
-  const int ctas = (int)min((long long)gridDim.x, total);
-  const long long start = ctas ? total * blockIdx.x / ctas : 0;
-  if ((int)blockIdx.x < ctas && start >= before && start < before + mine) {
+  Cut cut;
+  const bool small = total < (1ll << 31);
+  cut.ctas = (int)min((long long)gridDim.x, small ? (long long)(((uint32_t)total + kLeast - 1) / kLeast) : total);
+  cut.base = cut.ctas == 0 ? 0 : small ? (long long)((uint32_t)total / (uint32_t)cut.ctas) : total / cut.ctas;
+  cut.longer = (int)(total - cut.base * cut.ctas);
+  const long long start = cut.start(blockIdx.x);
+  if ((int)blockIdx.x < cut.ctas && start >= before && start < before + mine) {
     long long off = start - before, per_head = 0;
     Range k;
-    k.total = total;
-    k.ctas = ctas;
-    k.end = total * (blockIdx.x + 1) / ctas;
+    k.cut = cut;
+    k.end = cut.start(blockIdx.x + 1);
     Row w;
     for (k.row = ra; k.row < rb; ++k.row) {
       w = row_info(P, k.row);
@@ -170,7 +191,7 @@ __device__ __forceinline__ void find_range(const AttendParams& P, long long* sum
       if (off < per_head * P.hkv) break;
       off -= per_head * P.hkv;
     }
-    k.h = (int)(off / per_head);
+    k.h = small ? (int)((uint32_t)off / (uint32_t)per_head) : (int)(off / per_head);
     off -= k.h * per_head;
     k.mt = 0;
     for (int n = unit_info(P, w, 0).tiles + kUnitCost; off >= n; n = unit_info(P, w, k.mt).tiles + kUnitCost) {
