@@ -681,8 +681,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas))
   unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   unsigned char* ring = base + P.q_bufs * P.rows * D * 2;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  find_range<kThreads>(P, c.sums, &c.range);
-  if (c.range.cut.ctas == 0) return;
   if (tid == 0) {
     for (int i = 0; i < P.slots; ++i) {
       mbar_init_n(&c.full[i], 1);
@@ -706,9 +704,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas))
   }
   if (warp == kLoadWarp && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &mv : &mk) : "memory");
   fence_before();
-  __syncthreads();
+  find_range<kThreads>(P, c.sums, &c.range);  // ends in a barrier
   fence_after();
-  if (warp == kLoadWarp) {
+  if (c.range.cut.ctas == 0) {
+    // no work: straight to the end
+  } else if (warp == kLoadWarp) {
     load_warp<S, T, D>(P, &mk, &mv, smem_u32(base), smem_u32(ring), c);
   } else if (warp == kProductWarp) {
     if (lane == 0) product_thread<S, T, D>(P, smem_u32(base), smem_u32(ring), c);

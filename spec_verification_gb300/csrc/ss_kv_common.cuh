@@ -59,6 +59,7 @@ struct AttendParams {
   float scale_log2;     // scale * log2(e)
   int B, hkv, group, max_blocks, num_pages, page_shift, max_tokens, window, sinks;
   int rows, slots, q_bufs;  // query rows of a unit, tiles in the ring, query buffers
+  int unit_cost;            // tiles' worth of time that starting and ending a unit takes
   uint32_t group_mul, group_shift;  // x / group = (umulhi(x, mul) + x) >> shift for x < 2^31
   uint32_t* counters;   // [grid] arrivals at the unit that a CTA's range ends in
   float* part;          // [2 * grid][row_tile][head_dim]

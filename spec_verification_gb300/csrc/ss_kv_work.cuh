@@ -5,11 +5,11 @@
 //    unit is token i / group, head i % group, so the heads that share a key
 //    head share its loads.  A unit's keys are tiles of 64.
 //  - The units, in order, form one line in which a unit is as long as its tiles
-//    plus kUnitCost (what starting and ending one costs, in tiles).  The line
+//    plus unit_cost (what starting and ending one costs, in tiles).  The line
 //    is cut into equal parts, one per CTA: the split follows from the lengths
 //    on the device, every CTA has the same work whatever the rows' lengths
 //    are, and the launch never changes.  Tile i of a unit that starts at u is
-//    at u + kUnitCost + i and belongs to the CTA whose part that lies in.
+//    at u + unit_cost + i and belongs to the CTA whose part that lies in.
 #pragma once
 
 #include "ss_kv_common.cuh"
@@ -18,8 +18,7 @@ namespace ss {
 namespace kv {
 
 constexpr int kTile = 64;  // keys of a tile
-constexpr int kUnitCost = 2;
-constexpr int kLeast = 1;  // least length of a part
+constexpr int kLeast = 2;  // least length of a part: shorter ones cost more in the join than they save
 
 struct Row {
   int q0, n, len;
@@ -78,7 +77,7 @@ __device__ __forceinline__ int row_units(const AttendParams& P, const Row& w) { 
 }
 __device__ __forceinline__ long long row_length(const AttendParams& P, const Row& w) {  // of one key head, on the line
   long long s = 0;
-  for (int m = 0; m < row_units(P, w); ++m) s += unit_info(P, w, m).tiles + kUnitCost;
+  for (int m = 0; m < row_units(P, w); ++m) s += unit_info(P, w, m).tiles + P.unit_cost;
   return s;
 }
 
@@ -132,7 +131,7 @@ __device__ __forceinline__ bool next_segment(const AttendParams& P, Range& k, Se
   g.n = w.n;
   g.len = w.len;
   g.from = k.skip;
-  const long long at = k.unit + kUnitCost;  // of tile 0
+  const long long at = k.unit + P.unit_cost;  // of tile 0
   g.count = (int)min((long long)g.u.tiles, k.end - at) - g.from;
   if (g.count <= 0) return false;  // the part ends inside the unit's start
   g.live = min(P.rows, w.n * P.group - k.mt * P.rows);
@@ -194,12 +193,12 @@ __device__ __forceinline__ void find_range(const AttendParams& P, long long* sum
     k.h = small ? (int)((uint32_t)off / (uint32_t)per_head) : (int)(off / per_head);
     off -= k.h * per_head;
     k.mt = 0;
-    for (int n = unit_info(P, w, 0).tiles + kUnitCost; off >= n; n = unit_info(P, w, k.mt).tiles + kUnitCost) {
+    for (int n = unit_info(P, w, 0).tiles + P.unit_cost; off >= n; n = unit_info(P, w, k.mt).tiles + P.unit_cost) {
       off -= n;
       ++k.mt;
     }
     k.unit = start - off;
-    k.skip = max(0, (int)off - kUnitCost);
+    k.skip = max(0, (int)off - P.unit_cost);
     *out = k;
   }
   __syncthreads();
