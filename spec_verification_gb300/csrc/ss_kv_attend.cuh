@@ -48,6 +48,7 @@
 namespace ss {
 namespace kv {
 
+constexpr int kTile = 64;                        // keys of a tile
 constexpr int kSoftmaxWarps = 4;                 // warps 0 .. 3: a warp reaches the 32 lanes of its number modulo 4
 constexpr int kLoadWarp = 4, kProductWarp = 5;
 constexpr int kThreads = 192;
@@ -733,6 +734,7 @@ AttendKernel entry(int rows) {
   k.fn = reinterpret_cast<const void*>(&attend_kernel<T, D>);
   k.threads = kThreads;
   k.ctas = S::kCtas;
+  k.tile = kTile;
   k.q_bufs = rows <= 64 ? 2 : 1;  // a second buffer hides the gathering of the next segment's queries; 128 rows leave no room
   const int q = k.q_bufs * rows * D * 2;
   k.slots = (share - 1024 - q) / S::kSlot;

@@ -1,40 +1,20 @@
-// ss_attend: attention of a step's new tokens over the paged key-value cache.
+// ss_attend for 8-bit caches (e4m3): attention of a step's new tokens over the
+// paged key-value cache.  The mathematics, the split of the work and the join
+// of its pieces are those of ss_kv_attend.cuh.
 //
-// Mathematics.  For a query q at position p, o = sum_t w_t v_t / sum_t w_t
-// with w_t = 2^(c q.k_t - m), c = scale * log2 e, m the running maximum: one
-// pass over the keys, the running sum l and the output rescaled by
-// 2^(m_old - m_new) whenever m grows.  Two pieces (m, l, O) over disjoint keys
-// join as (max m, sum l 2^(m_i - m), sum O 2^(m_i - m)), so the keys of a row
-// can be split anywhere.
-//
-// What bounds it.  A key and its value (2 * head_dim elements) are read once
-// for the n * group queries of a key head (n new tokens, group = q_heads /
-// kv_heads): 4 * head_dim * n * group operations on 4 * head_dim bytes, i.e.
-// 1 .. 64 operations a byte where the card's tensor rate over its HBM rate is
-// about 280.  HBM bandwidth is the bound, and the kernel's one aim is to keep
-// enough loads in flight everywhere until the end.
-//
-// Layout of the work.
-//  - A unit is (row, key head, tile of MT query rows); query row i of a unit
-//    is token i / group, head i % group, so the heads that share a key head
-//    share its loads.  MT = 16, 32 or 64.  A unit's keys are tiles of 64.
-//  - The tiles of all units, in order, are cut into equal ranges, one per CTA
-//    of a grid that fills the GPU: the split follows from the lengths on the
-//    device, every CTA streams the same number of tiles whatever the rows'
-//    lengths are, and the launch never changes.  A unit that ends up in
-//    several CTAs is joined by the last of them to arrive (no CTA waits), in
-//    the order of the tiles, so results do not depend on timing.
-//  - One warp loads: TMA tiles of a page (or 64 tokens of it) of one head
-//    into a ring of swizzled key and value tiles, page ids read a batch
-//    ahead.  Four warps compute with 16 x 8 x 16 matrix instructions.  With
-//    MT = 16 every warp has all query rows and a quarter of a tile's keys,
-//    with its own maximum and sum, and the four join at the end of the unit,
-//    so that nothing synchronises the warps inside it; with MT = 64 a warp has
-//    its own 16 rows and all keys.
-//  - Tensor instructions: at these few query rows the 128-row tiles of the
-//    tcgen05 unit would be empty for the most part, and the softmax of their
-//    accumulators would sit on the few threads that own the live rows; the
-//    warp-wide instructions need no padding beyond 16 rows.
+// What differs: the tensor cores multiply 8-bit keys only with 8-bit queries,
+// and splitting 16-bit queries and weights into several 8-bit terms costs two
+// to three products for every one (above the time of the loads, whose bytes
+// are halved).  Instead keys and values become f16 in registers (exactly) on
+// their way from shared memory to 16 x 8 x 16 warp-wide products, whose operand
+// layout makes that cheap: the bytes of a key may be taken in any order of
+// columns as long as the queries are taken in the same one, and a register of
+// transposed values holds two neighbouring columns of two keys, which one byte
+// permutation each sorts into an even and an odd column.  One warp runs the
+// ring of TMA copies, four compute.  With MT = 16 query rows every warp has all
+// of them and a quarter of a tile's keys, with its own maximum and sum, and the
+// four join at the end of the unit, so that nothing synchronises the warps
+// inside it; with MT = 64 a warp has its own 16 rows and all keys.
 #pragma once
 
 #include <cuda.h>
@@ -51,57 +31,34 @@ namespace kv8 {
 
 using namespace kv;
 
+constexpr int kTile = 128;        // keys of a tile
 constexpr int kWarps = 4;         // computing warps
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr uint32_t kDrainPolls = 1u << 22;
 constexpr int kMaxSlots = 16;     // tiles of keys or values in the ring
 constexpr int kControl = 2048;    // bytes of the control block, at most
 
-// ------------------------------------------------------------------ types
+// ------------------------------------------------------------------ instructions
 template <class T>
-struct Elem;
+__device__ __forceinline__ uint32_t pack(float a, float b);
 template <>
-struct Elem<__nv_bfloat16> {
-  static __device__ __forceinline__ uint32_t pack(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  static __device__ __forceinline__ float2 unpack(uint32_t w) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  }
-  // both halves with infinities and NaN replaced by 0
-  static __device__ __forceinline__ uint32_t finite(uint32_t w) {
-    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
-    return w;
-  }
-};
-template <>
-struct Elem<__half> {
-  static __device__ __forceinline__ uint32_t pack(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  static __device__ __forceinline__ float2 unpack(uint32_t w) {
-    return __half22float2(*reinterpret_cast<__half2*>(&w));
-  }
-  static __device__ __forceinline__ uint32_t finite(uint32_t w) {
-    if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u;
-    if ((w & 0x7c000000u) == 0x7c000000u) w &= 0xffffu;
-    return w;
-  }
-};
-
-template <class T>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
-template <>
-__device__ __forceinline__ void mma<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 template <>
-__device__ __forceinline__ void mma<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ uint32_t pack<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 bf16_pair(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+// both f16 halves with NaN (e4m3 has no infinities) replaced by 0
+__device__ __forceinline__ uint32_t finite(uint32_t w) {
+  if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u;
+  if ((w & 0x7c000000u) == 0x7c000000u) w &= 0xffffu;
+  return w;
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -135,19 +92,19 @@ __device__ __forceinline__ void arrive(unsigned long long* m) {
 __device__ __forceinline__ void bar_warps() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // ------------------------------------------------------------------ shape of one instantiation
-template <class T, bool E4M3, int D, int MT>
+template <class T, int D, int MT>
 struct Shape {
-  using Mul = typename std::conditional<E4M3, __half, T>::type;  // what the products run in
-  static constexpr bool kScaleQ = E4M3 && std::is_same<T, __nv_bfloat16>::value;
-  static constexpr int kEl = E4M3 ? 1 : 2;
-  static constexpr int kRow = D * kEl;                       // bytes of a token
+  static constexpr bool kScaleQ = std::is_same<T, __nv_bfloat16>::value;
+  static constexpr int kRow = D;                             // bytes of a token
   static constexpr int kAtom = kRow < 128 ? kRow : 128;      // swizzled run of bytes
   static constexpr int kRuns = kRow / kAtom;
   static constexpr int kSlot = kTile * kRow;                 // bytes of a key (or value) tile
   static constexpr int kCtas = D <= 128 ? 2 : 1;             // CTAs per SM
   static constexpr int kSmem = (228 * 1024 / kCtas - 1024) & ~127;  // an SM's share of shared memory
   static constexpr int kWM = MT / 16, kWK = kWarps / kWM;    // warps along query rows, along keys
-  static constexpr int kKG = 4 / kWK;                        // 16-key groups of a warp
+  static constexpr int kKeys = kTile / kWK < 64 ? kTile / kWK : 64;  // keys that a warp takes at a time
+  static constexpr int kKG = kKeys / 16;                     // their 16-key groups
+  static constexpr int kPasses = kTile / (kKeys * kWK);
   static constexpr int kQRow = D * 2 + 16;                   // padded: rows fall into different banks
   static constexpr bool kQRegs = D <= 128 && MT < 64;        // query fragments stay in registers
   // ring of tiles: as many as the room beside the queries and the control block holds
@@ -203,7 +160,7 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
                           Range k) {
   const int lane = threadIdx.x & 31;
   const int box_shift = min(P.page_shift, 6);            // tokens of one copy
-  const int subs_shift = 6 - box_shift;                  // copies of a tile
+  const int subs_shift = 7 - box_shift;                  // copies of a tile
   const int batch = 32 >> subs_shift;                    // tiles whose page ids one lane each holds
   const int sub = lane & ((1 << subs_shift) - 1), nth = lane >> subs_shift;
   const int page_mask = (1 << P.page_shift) - 1;
@@ -283,10 +240,8 @@ __device__ __forceinline__ uint32_t place_of(int key, int b, int box_shift) {
   return off ^ ((off >> 3) & (S::kAtom == 128 ? 0x70 : 0x30));
 }
 
-template <class S, class T, bool E4M3, int D, int MT>
+template <class S, class T, int D, int MT>
 __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsigned char* sq, Control& c, Range k) {
-  using Mul = typename S::Mul;
-  using E = Elem<Mul>;
   constexpr int kNT = S::kKG * 2;  // 8-key tiles of a warp
   constexpr int kOT = D / 8;       // 8-column tiles of the output
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -306,7 +261,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
   uint32_t group_at[S::kKG];
 #pragma unroll
   for (int i = 0; i < S::kKG; ++i) {
-    const int key = (wk * S::kKG + i) * 16;
+    const int key = wk * S::kKeys + i * 16;
     group_at[i] = (key >> box_shift << box_shift) * S::kRow + (key & ((1 << box_shift) - 1)) * S::kAtom;
   }
 
@@ -327,8 +282,8 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
       if (S::kScaleQ) {
         // bf16 to f16: a row is scaled by a power of two that brings its largest value near 2^14, so every
         // value keeps its bits unless it is below 2^-28 of the largest
-        const float2 a = Elem<__nv_bfloat16>::unpack(x.x), b = Elem<__nv_bfloat16>::unpack(x.y),
-                     d = Elem<__nv_bfloat16>::unpack(x.z), e = Elem<__nv_bfloat16>::unpack(x.w);
+        const float2 a = bf16_pair(x.x), b = bf16_pair(x.y),
+                     d = bf16_pair(x.z), e = bf16_pair(x.w);
         float top = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))),
                           fmaxf(fmaxf(fabsf(d.x), fabsf(d.y)), fmaxf(fabsf(e.x), fabsf(e.y))));
 #pragma unroll
@@ -336,25 +291,21 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
         const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 240);      // biased exponent
         const float up = __uint_as_float((uint32_t)(127 + 14 + 127 - ex) << 23);  // 2^(14 - exponent)
         if (piece == 0) c.qinv[m] = __uint_as_float((uint32_t)(ex - 14) << 23);
-        x = make_uint4(Elem<__half>::pack(a.x * up, a.y * up), Elem<__half>::pack(b.x * up, b.y * up),
-                       Elem<__half>::pack(d.x * up, d.y * up), Elem<__half>::pack(e.x * up, e.y * up));
+        x = make_uint4(pack<__half>(a.x * up, a.y * up), pack<__half>(b.x * up, b.y * up),
+                       pack<__half>(d.x * up, d.y * up), pack<__half>(e.x * up, e.y * up));
       }
       *reinterpret_cast<uint4*>(sq + m * S::kQRow + piece * 16) = x;
     }
     bar_warps();
 
-    // a fragment of 16 query rows and 16 columns; with 8-bit keys the columns are permuted as the keys' bytes come
+    // a fragment of 16 query rows and 16 columns, the columns in the order in which the keys' bytes come
     auto q_frag = [&](uint32_t (&a)[4], int ks) {
-      if (E4M3) {
-        const unsigned char* p = sq + (wm * 16 + r0) * S::kQRow + ks * 32 + quad * 8;
-        const uint2 x = *reinterpret_cast<const uint2*>(p), y = *reinterpret_cast<const uint2*>(p + 8 * S::kQRow);
-        a[0] = x.x;
-        a[1] = y.x;
-        a[2] = x.y;
-        a[3] = y.y;
-      } else {
-        ldsm(a, sq_u + (wm * 16 + (lane & 15)) * S::kQRow + ks * 32 + (lane >> 4) * 16);
-      }
+      const unsigned char* p = sq + (wm * 16 + r0) * S::kQRow + ks * 32 + quad * 8;
+      const uint2 x = *reinterpret_cast<const uint2*>(p), y = *reinterpret_cast<const uint2*>(p + 8 * S::kQRow);
+      a[0] = x.x;
+      a[1] = y.x;
+      a[2] = x.y;
+      a[3] = y.y;
     };
     uint32_t qf[S::kQRegs ? D / 16 : 1][4];
     if (S::kQRegs) {
@@ -366,7 +317,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
     const int p0 = m0 < rows_here ? g.len - g.n + token_of(P, g.mt * MT + m0) : -1;
     const int p1 = m1 < rows_here ? g.len - g.n + token_of(P, g.mt * MT + m1) : -1;
     float c0 = P.scale_log2, c1 = P.scale_log2;
-    if (E4M3 && P.k_scale) {
+    if (P.k_scale) {
       const float s = P.k_scale[g.h];
       c0 *= s;
       c1 *= s;
@@ -387,130 +338,122 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
     for (int i = 0; i < g.count; ++i) {
       keys = values = turn;
       values.next<S::kSlots>();
-      const uint32_t kt = ring_u + keys.slot * S::kSlot + k_key * S::kAtom, vt = ring_u + values.slot * S::kSlot + v_key * S::kAtom;
-      const int base = tile_of(g.u, g.from + i) * kTile;
-      if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&c.full[keys.slot], keys.parity, P.spin_limit, 0u));
-      const int bad = c.bad[keys.slot];
-      // does any live row not see all of the tile?
-      const bool part = base + kTile - 1 > g.u.pos0 || bad != 0 ||
-                        (P.window > 0 && base <= g.u.pos1 - P.window && base + kTile > P.sinks);
-
-      // scores
-      float s[kNT][4];
-#pragma unroll
-      for (int n = 0; n < kNT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-#pragma unroll
-      for (int b0 = 0; b0 < S::kRow; b0 += 32) {  // 32 bytes of every key: 16 columns, or 32 of 8 bits
-        constexpr int kSteps = E4M3 ? 2 : 1;
-        const int ks = b0 / 32 * kSteps;
-        uint32_t qa[kSteps][4];
-        if (!S::kQRegs) {
-#pragma unroll
-          for (int h = 0; h < kSteps; ++h) q_frag(qa[h], ks + h);
-        }
-#pragma unroll
-        for (int gk = 0; gk < S::kKG; ++gk) {
-          uint32_t b[4];
-          ldsm(b, kt + group_at[gk] + b0 / S::kAtom * run_bytes + ((b0 % S::kAtom) ^ k_x));
-#pragma unroll
-          for (int h = 0; h < kSteps; ++h) {
-            const uint32_t(&a)[4] = S::kQRegs ? qf[S::kQRegs ? ks + h : 0] : qa[h];
-            if (E4M3) {
-              mma<Mul>(s[2 * gk], a, e4m3_f16(b[h]), e4m3_f16(b[h] >> 16));
-              mma<Mul>(s[2 * gk + 1], a, e4m3_f16(b[2 + h]), e4m3_f16(b[2 + h] >> 16));
-            } else {
-              mma<Mul>(s[2 * gk], a, b[0], b[1]);
-              mma<Mul>(s[2 * gk + 1], a, b[2], b[3]);
-            }
-          }
-        }
-      }
+      turn = values;
+      turn.next<S::kSlots>();
       const bool held = i + 1 == g.count;  // the last tile's room serves the join below
-      __syncwarp();
-      if (!held && lane == 0) arrive(&c.empty[keys.slot]);
-
+      if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&c.full[keys.slot], keys.parity, P.spin_limit, 0u));
+      const int tile = tile_of(g.u, g.from + i) * kTile, bad = c.bad[keys.slot];
+      // does any live row not see all of the tile?
+      const bool part = tile + kTile - 1 > g.u.pos0 || bad != 0 ||
+                        (P.window > 0 && tile <= g.u.pos1 - P.window && tile + kTile > P.sinks);
       // is key `in` of the tile visible from position p?
       auto sees = [&](int in, int p) {
-        const int key = base + in;
+        const int key = tile + in;
         return key <= p && (P.window <= 0 || key > p - P.window || key < P.sinks) && !((bad >> (in >> 4)) & 1);
       };
-      if (part) {
+#pragma unroll 1
+      for (int pass = 0; pass < S::kPasses; ++pass) {
+        const int in0 = pass * S::kKeys * S::kWK + wk * S::kKeys;  // this warp's keys
+        const uint32_t skip = pass * S::kKeys * S::kWK * S::kRow;  // a pass is a multiple of 64 keys: whole copies
+        const uint32_t kt = ring_u + keys.slot * S::kSlot + skip + k_key * S::kAtom;
+        const uint32_t vt = ring_u + values.slot * S::kSlot + skip + v_key * S::kAtom;
+
+        // scores
+        float s[kNT][4];
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int in = wk * S::kKG * 16 + n * 8 + 2 * quad + e;
-            if (!sees(in, p0)) s[n][e] = -INFINITY;
-            if (!sees(in, p1)) s[n][2 + e] = -INFINITY;
+          for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+#pragma unroll
+        for (int b0 = 0; b0 < S::kRow; b0 += 32) {  // 32 columns of every key
+          const int ks = b0 / 16;
+          uint32_t qa[2][4];
+          if (!S::kQRegs) {
+            q_frag(qa[0], ks);
+            q_frag(qa[1], ks + 1);
           }
-      }
-
-      // softmax of this warp's keys
-      float t0 = s[0][0], t1 = s[0][2];
 #pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        t0 = fmaxf(t0, fmaxf(s[n][0], s[n][1]));
-        t1 = fmaxf(t1, fmaxf(s[n][2], s[n][3]));
-      }
-      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
-      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
-      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
-      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
-      const float n0 = fmaxf(mx0, t0 * c0), n1 = fmaxf(mx1, t1 * c1);
-      const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
-      if (__any_sync(0xffffffffu, n0 != mx0 || n1 != mx1)) {
-        const float a0 = ex2(mx0 - z0), a1 = ex2(mx1 - z1);
-        l0 *= a0;
-        l1 *= a1;
+          for (int gk = 0; gk < S::kKG; ++gk) {
+            uint32_t b[4];
+            ldsm(b, kt + group_at[gk] + b0 / S::kAtom * run_bytes + ((b0 % S::kAtom) ^ k_x));
 #pragma unroll
-        for (int d = 0; d < kOT; ++d) {
-          o[d][0] *= a0;
-          o[d][1] *= a0;
-          o[d][2] *= a1;
-          o[d][3] *= a1;
-        }
-        mx0 = n0;
-        mx1 = n1;
-      }
-#pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        s[n][0] = ex2(fmaf(s[n][0], c0, -z0));
-        s[n][1] = ex2(fmaf(s[n][1], c0, -z0));
-        s[n][2] = ex2(fmaf(s[n][2], c1, -z1));
-        s[n][3] = ex2(fmaf(s[n][3], c1, -z1));
-        l0 += s[n][0] + s[n][1];
-        l1 += s[n][2] + s[n][3];
-      }
-
-      // times the values
-      if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&c.full[values.slot], values.parity, P.spin_limit, 0u));
-      bool odd = false;  // a value of a partly visible tile is not finite
-      auto clean = [&](uint32_t& x) {
-        const uint32_t y = E::finite(x);
-        odd |= y != x;
-        x = y;
-      };
-#pragma unroll
-      for (int gk = 0; gk < S::kKG; ++gk) {
-        // weights are rounded to 16 bits for the product (half a step, 2^-9 or 2^-12 of each, random in sign);
-        // their sum is not
-        const uint32_t a[4] = {E::pack(s[2 * gk][0], s[2 * gk][1]), E::pack(s[2 * gk][2], s[2 * gk][3]),
-                               E::pack(s[2 * gk + 1][0], s[2 * gk + 1][1]), E::pack(s[2 * gk + 1][2], s[2 * gk + 1][3])};
-#pragma unroll
-        for (int b0 = 0; b0 < S::kRow; b0 += 32) {
-          const int d = b0 / 32;
-          uint32_t b[4];
-          ldsm_t(b, vt + group_at[gk] + b0 / S::kAtom * run_bytes + ((b0 % S::kAtom) ^ v_x));
-          if (!E4M3) {
-            if (part) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) clean(b[e]);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t(&a)[4] = S::kQRegs ? qf[S::kQRegs ? ks + h : 0] : qa[h];
+              mma(s[2 * gk], a, e4m3_f16(b[h]), e4m3_f16(b[h] >> 16));
+              mma(s[2 * gk + 1], a, e4m3_f16(b[2 + h]), e4m3_f16(b[2 + h] >> 16));
             }
-            mma<Mul>(o[2 * d], a, b[0], b[1]);
-            mma<Mul>(o[2 * d + 1], a, b[2], b[3]);
-          } else {
+          }
+        }
+        __syncwarp();
+        if (!held && pass + 1 == S::kPasses && lane == 0) arrive(&c.empty[keys.slot]);
+        if (part) {
+#pragma unroll
+          for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int in = in0 + n * 8 + 2 * quad + e;
+              if (!sees(in, p0)) s[n][e] = -INFINITY;
+              if (!sees(in, p1)) s[n][2 + e] = -INFINITY;
+            }
+        }
+
+        // softmax of this warp's keys; m moves only when a score exceeds it by more than 2^8
+        float t0 = s[0][0], t1 = s[0][2];
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+          t0 = fmaxf(t0, fmaxf(s[n][0], s[n][1]));
+          t1 = fmaxf(t1, fmaxf(s[n][2], s[n][3]));
+        }
+        t0 *= c0;
+        t1 *= c1;
+        if (__any_sync(0xffffffffu, t0 > mx0 + 8.0f || t1 > mx1 + 8.0f || (mx0 == -INFINITY && t0 > mx0) || (mx1 == -INFINITY && t1 > mx1))) {
+          t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
+          t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
+          t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
+          t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
+          const float n0 = fmaxf(mx0, t0), n1 = fmaxf(mx1, t1);
+          const float a0 = n0 == mx0 ? 1.0f : ex2(mx0 - n0), a1 = n1 == mx1 ? 1.0f : ex2(mx1 - n1);
+          l0 *= a0;
+          l1 *= a1;
+#pragma unroll
+          for (int d = 0; d < kOT; ++d) {
+            o[d][0] *= a0;
+            o[d][1] *= a0;
+            o[d][2] *= a1;
+            o[d][3] *= a1;
+          }
+          mx0 = n0;
+          mx1 = n1;
+        }
+        const float z0 = mx0 == -INFINITY ? 0.0f : mx0, z1 = mx1 == -INFINITY ? 0.0f : mx1;
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+          s[n][0] = ex2(fmaf(s[n][0], c0, -z0));
+          s[n][1] = ex2(fmaf(s[n][1], c0, -z0));
+          s[n][2] = ex2(fmaf(s[n][2], c1, -z1));
+          s[n][3] = ex2(fmaf(s[n][3], c1, -z1));
+          l0 += s[n][0] + s[n][1];
+          l1 += s[n][2] + s[n][3];
+        }
+
+        // times the values
+        if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&c.full[values.slot], values.parity, P.spin_limit, 0u));
+        bool odd = false;  // a value of a partly visible tile is not finite
+        auto clean = [&](uint32_t& x) {
+          const uint32_t y = finite(x);
+          odd |= y != x;
+          x = y;
+        };
+#pragma unroll
+        for (int gk = 0; gk < S::kKG; ++gk) {
+          // weights are rounded to f16 for the product (half a step, 2^-12 of each, random in sign); their sum is not
+          const uint32_t a[4] = {pack<__half>(s[2 * gk][0], s[2 * gk][1]), pack<__half>(s[2 * gk][2], s[2 * gk][3]),
+                                 pack<__half>(s[2 * gk + 1][0], s[2 * gk + 1][1]), pack<__half>(s[2 * gk + 1][2], s[2 * gk + 1][3])};
+#pragma unroll
+          for (int b0 = 0; b0 < S::kRow; b0 += 32) {
+            const int d = b0 / 8;
+            uint32_t b[4];
+            ldsm_t(b, vt + group_at[gk] + b0 / S::kAtom * run_bytes + ((b0 % S::kAtom) ^ v_x));
             // a register holds two neighbouring columns of two keys: even columns to one product, odd to the other
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -520,44 +463,41 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
 #pragma unroll
                 for (int e = 0; e < 4; ++e) clean(f[e]);
               }
-              mma<Mul>(o[(4 * d + 2 * h) % kOT], a, f[0], f[1]);
-              mma<Mul>(o[(4 * d + 2 * h + 1) % kOT], a, f[2], f[3]);
+              mma(o[d + 2 * h], a, f[0], f[1]);
+              mma(o[d + 2 * h + 1], a, f[2], f[3]);
             }
           }
         }
-      }
-      if (part && __any_sync(0xffffffffu, odd)) {
-        // Some value in the tile is not finite and was left out above; rows that see its key take it here, one
-        // key at a time (0 * infinity of a row that does not see it must not happen).
+        if (part && __any_sync(0xffffffffu, odd)) {
+          // Some value in the tile is not finite and was left out above; rows that see its key take it here, one
+          // key at a time (0 * NaN of a row that does not see it must not happen).
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) {
+          for (int n = 0; n < kNT; ++n) {
 #pragma unroll 1
-          for (int src = 0; src < 8; ++src) {
-            const int from = (lane & ~3) + (src >> 1);
-            const float e0 = __shfl_sync(0xffffffffu, s[n][0], from), e1 = __shfl_sync(0xffffffffu, s[n][1], from);
-            const float e2 = __shfl_sync(0xffffffffu, s[n][2], from), e3 = __shfl_sync(0xffffffffu, s[n][3], from);
-            const float w0 = src & 1 ? e1 : e0, w1 = src & 1 ? e3 : e2;
-            const int in = wk * S::kKG * 16 + n * 8 + src;
-            const bool v0 = sees(in, p0), v1 = sees(in, p1);
+            for (int src = 0; src < 8; ++src) {
+              const int from = (lane & ~3) + (src >> 1);
+              const float e0 = __shfl_sync(0xffffffffu, s[n][0], from), e1 = __shfl_sync(0xffffffffu, s[n][1], from);
+              const float e2 = __shfl_sync(0xffffffffu, s[n][2], from), e3 = __shfl_sync(0xffffffffu, s[n][3], from);
+              const float w0 = src & 1 ? e1 : e0, w1 = src & 1 ? e3 : e2;
+              const int in = in0 + n * 8 + src;
+              const bool v0 = sees(in, p0), v1 = sees(in, p1);
 #pragma unroll
-            for (int d = 0; d < kOT; ++d)
+              for (int d = 0; d < kOT; ++d)
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const int col = E4M3 ? (d >> 1) * 16 + 4 * quad + 2 * x + (d & 1) : d * 8 + 2 * quad + x;
-                const unsigned char* at = ring + values.slot * S::kSlot + place_of<S>(in, col * S::kEl, box_shift);
-                const float v = E4M3 ? E::unpack(e4m3_f16(*at)).x : E::unpack(*reinterpret_cast<const unsigned short*>(at)).x;
-                if (!isfinite(v)) {
-                  if (v0) o[d][x] = fmaf(w0, v, o[d][x]);
-                  if (v1) o[d][2 + x] = fmaf(w1, v, o[d][2 + x]);
+                for (int x = 0; x < 2; ++x) {
+                  const int col = (d >> 1) * 16 + 4 * quad + 2 * x + (d & 1);
+                  const float v = __half2float(__ushort_as_half((unsigned short)e4m3_f16(ring[values.slot * S::kSlot + place_of<S>(in, col, box_shift)])));
+                  if (!isfinite(v)) {
+                    if (v0) o[d][x] = fmaf(w0, v, o[d][x]);
+                    if (v1) o[d][2 + x] = fmaf(w1, v, o[d][2 + x]);
+                  }
                 }
-              }
+            }
           }
         }
       }
       __syncwarp();
       if (!held && lane == 0) arrive(&c.empty[values.slot]);
-      turn = values;
-      turn.next<S::kSlots>();
     }
     if (dead && lane == 0) atomicOr(&P.row_status[g.row], (uint32_t)SS_ST_COPY_TIMEOUT);
 
@@ -652,7 +592,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
 
     if (write && wk == 0) {
       float f0 = l0 == 0.0f ? 0.0f : 1.0f / l0, f1 = l1 == 0.0f ? 0.0f : 1.0f / l1;
-      if (E4M3 && P.v_scale) {
+      if (P.v_scale) {
         f0 *= P.v_scale[g.h];
         f1 *= P.v_scale[g.h];
       }
@@ -663,17 +603,10 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
           const int f = g.mt * MT + m, j = f / P.group, head = g.h * P.group + f - j * P.group;
           const float r = x ? f1 : f0;
           T* to = static_cast<T*>(P.out) + (g.q0 + j) * P.out_stride + head * D;
-          if (E4M3) {
 #pragma unroll
-            for (int d = 0; d < kOT; d += 2)
-              *reinterpret_cast<uint2*>(to + d * 8 + quad * 4) =
-                  make_uint2(Elem<T>::pack(o[d][2 * x] * r, o[d + 1][2 * x] * r),
-                             Elem<T>::pack(o[d][2 * x + 1] * r, o[d + 1][2 * x + 1] * r));
-          } else {
-#pragma unroll
-            for (int d = 0; d < kOT; ++d)
-              *reinterpret_cast<uint32_t*>(to + d * 8 + quad * 2) = Elem<T>::pack(o[d][2 * x] * r, o[d][2 * x + 1] * r);
-          }
+          for (int d = 0; d < kOT; d += 2)
+            *reinterpret_cast<uint2*>(to + d * 8 + quad * 4) = make_uint2(pack<T>(o[d][2 * x] * r, o[d + 1][2 * x] * r),
+                                                                          pack<T>(o[d][2 * x + 1] * r, o[d + 1][2 * x + 1] * r));
           if (P.lse && quad == 0) {
             const float l = x ? l1 : l0, mx = x ? mx1 : mx0;
             P.lse[(size_t)(g.q0 + j) * (P.group * P.hkv) + head] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
@@ -692,10 +625,10 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
 }
 
 // ------------------------------------------------------------------ kernel
-template <class T, bool E4M3, int D, int MT>
-__global__ void __launch_bounds__(kThreads, (Shape<T, E4M3, D, MT>::kCtas))
+template <class T, int D, int MT>
+__global__ void __launch_bounds__(kThreads, (Shape<T, D, MT>::kCtas))
     attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-  using S = Shape<T, E4M3, D, MT>;
+  using S = Shape<T, D, MT>;
   static_assert(S::kSlots >= 4, "ring length");
   extern __shared__ unsigned char raw[];
   unsigned char* ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -714,21 +647,21 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, E4M3, D, MT>::kCtas))
   find_range<kThreads>(P, c.range_sums, &c.range);
   if (c.range.cut.ctas == 0) return;
   if (warp == kWarps) load_warp<S, MT>(P, &mk, &mv, ring, c, c.range);
-  else compute_warps<S, T, E4M3, D, MT>(P, ring, sq, c, c.range);
+  else compute_warps<S, T, D, MT>(P, ring, sq, c, c.range);
 }
 
-template <class T, bool E4M3, int D, int MT>
+template <class T, int D, int MT>
 AttendKernel entry() {
-  using S = Shape<T, E4M3, D, MT>;
-  return {reinterpret_cast<const void*>(&attend_kernel<T, E4M3, D, MT>), kThreads, S::kSlots, 1, S::kCtas, smem_bytes<S>(MT)};
+  using S = Shape<T, D, MT>;
+  return {reinterpret_cast<const void*>(&attend_kernel<T, D, MT>), kThreads, S::kSlots, 1, S::kCtas, kTile, smem_bytes<S>(MT)};
 }
-template <class T, bool E4M3, int D>
+template <class T, int D>
 AttendKernel by_rows(int mt) {
-  return mt == 16 ? entry<T, E4M3, D, 16>() : mt == 32 ? entry<T, E4M3, D, 32>() : entry<T, E4M3, D, 64>();
+  return mt == 16 ? entry<T, D, 16>() : mt == 32 ? entry<T, D, 32>() : entry<T, D, 64>();
 }
-template <class T, bool E4M3>
+template <class T>
 AttendKernel pick(int d, int mt) {
-  return d == 64 ? by_rows<T, E4M3, 64>(mt) : d == 128 ? by_rows<T, E4M3, 128>(mt) : by_rows<T, E4M3, 256>(mt);
+  return d == 64 ? by_rows<T, 64>(mt) : d == 128 ? by_rows<T, 128>(mt) : by_rows<T, 256>(mt);
 }
 
 }  // namespace kv8

@@ -2,5 +2,5 @@
 #include "ss_kv_attend8.cuh"
 
 namespace ss {
-AttendKernel kv_attend_f16_e4m3(int head_dim, int row_tile) { return kv8::pick<__half, true>(head_dim, row_tile); }
+AttendKernel kv_attend_f16_e4m3(int head_dim, int row_tile) { return kv8::pick<__half>(head_dim, row_tile); }
 }  // namespace ss

@@ -3,7 +3,7 @@
 //
 //  - A unit is (row, key head, tile of `rows` query rows); query row i of a
 //    unit is token i / group, head i % group, so the heads that share a key
-//    head share its loads.  A unit's keys are tiles of 64.
+//    head share its loads.  A unit's keys are tiles of 64 or 128.
 //  - The units, in order, form one line in which a unit is as long as its tiles
 //    plus unit_cost (what starting and ending one costs, in tiles).  The line
 //    is cut into equal parts, one per CTA: the split follows from the lengths
@@ -17,7 +17,6 @@
 namespace ss {
 namespace kv {
 
-constexpr int kTile = 64;  // keys of a tile
 constexpr int kLeast = 2;  // least length of a part: shorter ones cost more in the join than they save
 
 struct Row {
@@ -63,11 +62,11 @@ __device__ __forceinline__ Unit unit_info(const AttendParams& P, const Row& w, i
   u.sink = 0;
   u.first = 0;
   if (P.window > 0) {
-    u.first = max(0, u.pos0 - P.window + 1) / kTile;
-    u.sink = min((P.sinks + kTile - 1) / kTile, u.first);
+    u.first = max(0, u.pos0 - P.window + 1)  >> P.tile_shift;
+    u.sink = min((P.sinks + (1 << P.tile_shift) - 1) >> P.tile_shift, u.first);
   }
   // a unit without a visible key still has one (masked) tile: its output is written
-  u.tiles = u.pos1 < 0 ? 1 : u.sink + u.pos1 / kTile - u.first + 1;
+  u.tiles = u.pos1 < 0 ? 1 : u.sink + (u.pos1 >> P.tile_shift) - u.first + 1;
   return u;
 }
 __device__ __forceinline__ int tile_of(const Unit& u, int i) { return i < u.sink ? i : i - u.sink + u.first; }
