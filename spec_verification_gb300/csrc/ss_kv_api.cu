@@ -17,6 +17,7 @@ void set_last_error(const char* msg);
 
 namespace {
 
+constexpr int kUnit8 = 128 << 10;
 constexpr uint32_t kSpin = 1u << 22;  // polls of a copy wait before the copy counts as lost
 
 ss_status fail(ss_status s, const char* msg) {
@@ -173,7 +174,7 @@ ss_status ss_kv_plan_create(ss_kv_plan** out, const ss_kv_config* config) {
   p->sms = sms;
   p->row_tile = row_tile;
   p->attend_grid = k.ctas * sms;
-  p->off_part = up256((size_t)p->attend_grid * 4);
+  p->off_part = up256((size_t)3 * p->attend_grid * 4);
   p->off_ml = p->off_part + up256((size_t)2 * p->attend_grid * row_tile * c.head_dim * 4);
   p->ws_bytes = p->off_ml + up256((size_t)2 * p->attend_grid * row_tile * 8);
   *out = p;
@@ -353,7 +354,7 @@ ss_status ss_attend(const ss_attend_batch* b, const ss_kv_cache* cache) {
   P.q_bufs = k.q_bufs;
   // About 2 us beside its tiles, which take the longer the more bytes they have: two tiles of 32 KB.
   // Measured (1, 2, 4 tiles): 64 x 1 rows of 32 KB tiles 101, 95.7, 96.3 us; 96 x 3 rows of 16 KB tiles 89, 82, 76 us.
-  P.unit_cost = std::max(1, (64 << 10) / (2 * k.tile * c.head_dim * (c.cache_dtype == SS_E4M3 ? 1 : 2)));
+  P.unit_cost = std::max(1, (c.cache_dtype == SS_E4M3 ? kUnit8 : 64 << 10) / (2 * k.tile * c.head_dim * (c.cache_dtype == SS_E4M3 ? 1 : 2)));
   P.tile_shift = k.tile == 64 ? 6 : 7;
   while ((1u << P.group_shift) < (uint32_t)P.group) ++P.group_shift;
   P.group_mul = (uint32_t)(((1ull << 32) * ((1ull << P.group_shift) - P.group)) / P.group + 1);

@@ -33,7 +33,7 @@
 //  costs tensor time only (measured with one live row in eight it stays below
 //  the time of the loads), and a warp without live rows skips its part.
 //  - A unit that lies in several CTAs is joined by the last of them to arrive
-//    (none waits), in the order of its tiles: results do not depend on timing.
+//    (ss_kv_join.cuh).
 #pragma once
 
 #include <cuda.h>
@@ -42,7 +42,7 @@
 
 #include <type_traits>
 
-#include "ss_kv_work.cuh"
+#include "ss_kv_join.cuh"
 #include "ss_stage1.cuh"
 
 namespace ss {
@@ -83,11 +83,6 @@ struct Elem<__half> {
 };
 
 // ------------------------------------------------------------------ instructions
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void mbar_init_n(unsigned long long* m, int n) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(m)), "r"(n) : "memory");
 }
@@ -575,13 +570,12 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* ring, Contro
     // ---- the unit's output, or this CTA's piece of it
     added(it - 1);
     const bool whole = g.ca == g.cb;
-    auto piece = [&](int x) { return (size_t)(2 * x + (x == g.ca ? 1 : 0)) * P.rows; };  // a range's last unit / its first
     if (busy) {
-      const size_t mine = piece(blockIdx.x);
+      const int mine = piece_of(g, blockIdx.x);
       const int head = g.h * P.group + f - token * P.group;
       const float r = l == 0.0f ? 0.0f : 1.0f / l;
       T* to = static_cast<T*>(P.out) + (g.q0 + token) * P.out_stride + head * D;
-      float4* part_to = reinterpret_cast<float4*>(P.part + mine * D) + tid;
+      float4* part_to = piece_out<D>(P, mine) + tid;
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         uint32_t o[32];
@@ -601,7 +595,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* ring, Contro
         }
       }
       if (live) {
-        if (!whole) P.ml[mine + tid] = make_float2(mx, l);
+        if (!whole) piece_ml(P, mine)[tid] = make_float2(mx, l);
         else if (P.lse) P.lse[(size_t)(g.q0 + token) * (P.group * P.hkv) + head] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
       }
     }
@@ -612,62 +606,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* ring, Contro
       arrive(&c.seg_empty[sg & 1]);
     }
     ++sg;
-    if (whole) continue;
-    __threadfence();
-    bar_softmax();
-    if (tid == 0) {
-      const uint32_t before = atomicAdd(&P.counters[g.ca], 1u);
-      c.last = before == (uint32_t)(g.cb - g.ca);
-      if (c.last) P.counters[g.ca] = 0;
-    }
-    bar_softmax();
-    if (!c.last) continue;
-    __threadfence();
-    // Four columns of a row are an item; a thread's items are of one row (rows divides 128).  Loads of kPieces pieces
-    // of kItems items are in flight together; the pieces are added in order.
-    constexpr int kPieces = 4, kItems = 4;
-    const int jm = tid & (P.rows - 1);
-    if (jm >= g.live) continue;
-    const int fm = g.mt * P.rows + jm, tm = token_of(P, fm), head = g.h * P.group + fm - tm * P.group;
-    T* to = static_cast<T*>(P.out) + (g.q0 + tm) * P.out_stride + head * D;
-    const int items = P.rows * (D / 4);
-    for (int e0 = tid; e0 < items; e0 += 128 * kItems) {
-      float top = -INFINITY, sum = 0.0f;
-      float4 o[kItems];
-#pragma unroll
-      for (int n = 0; n < kItems; ++n) o[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int x0 = g.ca; x0 <= g.cb; x0 += kPieces) {
-        float2 ml[kPieces];
-        float4 y[kPieces][kItems];
-#pragma unroll
-        for (int x = 0; x < kPieces; ++x) {
-          const size_t its = piece(min(x0 + x, g.cb));
-          ml[x] = __ldcg(P.ml + its + jm);
-#pragma unroll
-          for (int n = 0; n < kItems; ++n)
-            y[x][n] = __ldcg(reinterpret_cast<const float4*>(P.part + its * D) + min(e0 + 128 * n, items - 1));
-        }
-#pragma unroll
-        for (int x = 0; x < kPieces; ++x) {
-          if (x0 + x > g.cb) break;
-          const float n = fmaxf(top, ml[x].x), zn = n == -INFINITY ? 0.0f : n, a = ex2(top - zn), b = ex2(ml[x].x - zn);
-          sum = sum * a + ml[x].y * b;
-          top = n;
-#pragma unroll
-          for (int q = 0; q < kItems; ++q)
-            o[q] = make_float4(o[q].x * a + y[x][q].x * b, o[q].y * a + y[x][q].y * b, o[q].z * a + y[x][q].z * b, o[q].w * a + y[x][q].w * b);
-        }
-      }
-      const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-      for (int n = 0; n < kItems; ++n) {
-        const int e = e0 + 128 * n;
-        if (e < items)
-          *reinterpret_cast<uint2*>(to + e / P.rows * 4) = make_uint2(E::pack(o[n].x * r, o[n].y * r), E::pack(o[n].z * r, o[n].w * r));
-      }
-      if (P.lse && e0 < P.rows)
-        P.lse[(size_t)(g.q0 + tm) * (P.group * P.hkv) + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
-    }
+    if (!whole) join_unit<T, E, D, 32 * kSoftmaxWarps>(P, g, &c.last, bar_softmax);
   }
 }
 

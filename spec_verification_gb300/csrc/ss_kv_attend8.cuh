@@ -23,7 +23,7 @@
 
 #include <type_traits>
 
-#include "ss_kv_work.cuh"
+#include "ss_kv_join.cuh"
 #include "ss_stage1.cuh"
 
 namespace ss {
@@ -32,25 +32,27 @@ namespace kv8 {
 using namespace kv;
 
 constexpr int kTile = 128;        // keys of a tile
-constexpr int kWarps = 4;         // computing warps
-constexpr int kThreads = 32 * (kWarps + 1);
 constexpr uint32_t kDrainPolls = 1u << 22;
 constexpr int kMaxSlots = 16;     // tiles of keys or values in the ring
-constexpr int kControl = 2048;    // bytes of the control block, at most
+constexpr int kControl = 2304;    // bytes of the control block, at most
 
 // ------------------------------------------------------------------ instructions
 template <class T>
-__device__ __forceinline__ uint32_t pack(float a, float b);
+struct Pack;
 template <>
-__device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
+struct Pack<__nv_bfloat16> {
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
 template <>
-__device__ __forceinline__ uint32_t pack<__half>(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
+struct Pack<__half> {
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
 __device__ __forceinline__ float2 bf16_pair(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
 // both f16 halves with NaN (e4m3 has no infinities) replaced by 0
 __device__ __forceinline__ uint32_t finite(uint32_t w) {
@@ -81,15 +83,13 @@ __device__ __forceinline__ uint32_t e4m3_f16(uint32_t w) {
   asm("{\n .reg .b16 h;\n cvt.u16.u32 h, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(d) : "r"(w));
   return d;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void arrive(unsigned long long* m) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(m)) : "memory");
 }
-__device__ __forceinline__ void bar_warps() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bar_warps() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * N) : "memory");
+}
 
 // ------------------------------------------------------------------ shape of one instantiation
 template <class T, int D, int MT>
@@ -101,6 +101,8 @@ struct Shape {
   static constexpr int kSlot = kTile * kRow;                 // bytes of a key (or value) tile
   static constexpr int kCtas = D <= 128 ? 2 : 1;             // CTAs per SM
   static constexpr int kSmem = (228 * 1024 / kCtas - 1024) & ~127;  // an SM's share of shared memory
+  static constexpr int kWarps = 4;                           // computing warps
+  static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kWM = MT / 16, kWK = kWarps / kWM;    // warps along query rows, along keys
   static constexpr int kKeys = kTile / kWK < 64 ? kTile / kWK : 64;  // keys that a warp takes at a time
   static constexpr int kKG = kKeys / 16;                     // their 16-key groups
@@ -116,10 +118,10 @@ struct Shape {
 struct Control {
   unsigned long long full[kMaxSlots], empty[kMaxSlots];
   int bad[kMaxSlots];   // per tile of keys: its 16-key groups that lie on pages with a bad id
-  long long range_sums[kThreads / 32];
+  long long range_sums[9];
   Range range;
   int last;
-  float ml[kWarps][16][2];
+  float ml[8][16][2];
   float qinv[64];
 };
 
@@ -270,8 +272,8 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
     const int rows_here = g.live;
 
     // queries into shared memory, rows past the end zero
-    bar_warps();
-    for (int i = threadIdx.x; i < MT * (D / 8); i += 32 * kWarps) {
+    bar_warps<S::kWarps>();
+    for (int i = threadIdx.x; i < MT * (D / 8); i += 32 * S::kWarps) {
       const int m = i / (D / 8), piece = i % (D / 8);
       uint4 x = make_uint4(0u, 0u, 0u, 0u);
       if (m < rows_here) {
@@ -291,12 +293,12 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
         const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 240);      // biased exponent
         const float up = __uint_as_float((uint32_t)(127 + 14 + 127 - ex) << 23);  // 2^(14 - exponent)
         if (piece == 0) c.qinv[m] = __uint_as_float((uint32_t)(ex - 14) << 23);
-        x = make_uint4(pack<__half>(a.x * up, a.y * up), pack<__half>(b.x * up, b.y * up),
-                       pack<__half>(d.x * up, d.y * up), pack<__half>(e.x * up, e.y * up));
+        x = make_uint4(Pack<__half>::pack(a.x * up, a.y * up), Pack<__half>::pack(b.x * up, b.y * up),
+                       Pack<__half>::pack(d.x * up, d.y * up), Pack<__half>::pack(e.x * up, e.y * up));
       }
       *reinterpret_cast<uint4*>(sq + m * S::kQRow + piece * 16) = x;
     }
-    bar_warps();
+    bar_warps<S::kWarps>();
 
     // a fragment of 16 query rows and 16 columns, the columns in the order in which the keys' bytes come
     auto q_frag = [&](uint32_t (&a)[4], int ks) {
@@ -447,8 +449,8 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
 #pragma unroll
         for (int gk = 0; gk < S::kKG; ++gk) {
           // weights are rounded to f16 for the product (half a step, 2^-12 of each, random in sign); their sum is not
-          const uint32_t a[4] = {pack<__half>(s[2 * gk][0], s[2 * gk][1]), pack<__half>(s[2 * gk][2], s[2 * gk][3]),
-                                 pack<__half>(s[2 * gk + 1][0], s[2 * gk + 1][1]), pack<__half>(s[2 * gk + 1][2], s[2 * gk + 1][3])};
+          const uint32_t a[4] = {Pack<__half>::pack(s[2 * gk][0], s[2 * gk][1]), Pack<__half>::pack(s[2 * gk][2], s[2 * gk][3]),
+                                 Pack<__half>::pack(s[2 * gk + 1][0], s[2 * gk + 1][1]), Pack<__half>::pack(s[2 * gk + 1][2], s[2 * gk + 1][3])};
 #pragma unroll
           for (int b0 = 0; b0 < S::kRow; b0 += 32) {
             const int d = b0 / 8;
@@ -501,7 +503,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
     }
     if (dead && lane == 0) atomicOr(&P.row_status[g.row], (uint32_t)SS_ST_COPY_TIMEOUT);
 
-    // ---- join: the warps of the unit, then the CTAs
+    // ---- join: the warps of the unit
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
@@ -528,9 +530,9 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
 #pragma unroll
       for (int half = S::kWK / 2; half > 0; half >>= 1) {
         // warps [half, 2 half) along the keys hand their piece to warps [0, half)
-        bar_warps();
-        const int area = S::kWM == 1 ? wk % half : wm;  // at most two pieces at a time
-        float4* at = reinterpret_cast<float4*>(ring + (area ? values.slot : keys.slot) * S::kSlot) + lane;
+        bar_warps<S::kWarps>();
+        const int area = wk % half * S::kWM + wm;  // at most four pieces at a time, each half a tile long
+        float4* at = reinterpret_cast<float4*>(ring + (area >> 1 ? values.slot : keys.slot) * S::kSlot + (area & 1) * (S::kSlot / 2)) + lane;
         if (wk >= half && wk < 2 * half) {
 #pragma unroll
           for (int d = 0; d < kOT; ++d) at[d * 32] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
@@ -541,7 +543,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
             c.ml[warp][r0 + 8][1] = l1;
           }
         }
-        bar_warps();
+        bar_warps<S::kWarps>();
         if (wk < half) {
           const int other = warp + half * S::kWM;
           take(c.ml[other][r0][0], c.ml[other][r0 + 8][0], c.ml[other][r0][1], c.ml[other][r0 + 8][1], at);
@@ -550,67 +552,33 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
     };
     join_warps();
 
-    bool write = true;
-    if (g.ca != g.cb) {
-      const int ca = g.ca, cb = g.cb;
-      auto piece = [&](int x) { return (size_t)(2 * x + (x == ca ? 1 : 0)) * MT; };  // a range's last unit / its first
-      if (wk == 0) {
-        const size_t mine = piece(blockIdx.x);
-        float4* to = reinterpret_cast<float4*>(P.part + mine * D) + wm * (16 * D / 4) + lane;
-#pragma unroll
-        for (int d = 0; d < kOT; ++d) to[d * 32] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
-        if (quad == 0) {
-          P.ml[mine + m0] = make_float2(mx0, l0);
-          P.ml[mine + m1] = make_float2(mx1, l1);
-        }
-      }
-      __threadfence();
-      bar_warps();
-      if (threadIdx.x == 0) {
-        const uint32_t before = atomicAdd(&P.counters[ca], 1u);
-        c.last = before == (uint32_t)(cb - ca);
-        if (c.last) P.counters[ca] = 0;
-      }
-      bar_warps();
-      write = c.last != 0;
-      if (write) {
-        __threadfence();
-        mx0 = mx1 = -INFINITY;
-        l0 = l1 = 0.0f;
-#pragma unroll
-        for (int d = 0; d < kOT; ++d)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
-        for (int x = ca + wk; x <= cb; x += S::kWK) {
-          const size_t its = piece(x);
-          const float2 y0 = P.ml[its + m0], y1 = P.ml[its + m1];
-          take(y0.x, y1.x, y0.y, y1.y, reinterpret_cast<const float4*>(P.part + its * D) + wm * (16 * D / 4) + lane);
-        }
-        join_warps();
-      }
-    }
-
-    if (write && wk == 0) {
-      float f0 = l0 == 0.0f ? 0.0f : 1.0f / l0, f1 = l1 == 0.0f ? 0.0f : 1.0f / l1;
+    const bool whole = g.ca == g.cb;
+    if (wk == 0) {
+      float f0 = whole ? (l0 == 0.0f ? 0.0f : 1.0f / l0) : 1.0f, f1 = whole ? (l1 == 0.0f ? 0.0f : 1.0f / l1) : 1.0f;
       if (P.v_scale) {
         f0 *= P.v_scale[g.h];
         f1 *= P.v_scale[g.h];
       }
+      const int mine = piece_of(g, blockIdx.x);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int m = x ? m1 : m0;
-        if (m < rows_here) {
-          const int f = g.mt * MT + m, j = f / P.group, head = g.h * P.group + f - j * P.group;
-          const float r = x ? f1 : f0;
-          T* to = static_cast<T*>(P.out) + (g.q0 + j) * P.out_stride + head * D;
+        if (m >= rows_here) continue;
+        const int f = g.mt * MT + m, j = token_of(P, f), head = g.h * P.group + f - j * P.group;
+        const float r = x ? f1 : f0, l = x ? l1 : l0, mx = x ? mx1 : mx0;
+        T* to = static_cast<T*>(P.out) + (g.q0 + j) * P.out_stride + head * D;
 #pragma unroll
-          for (int d = 0; d < kOT; d += 2)
-            *reinterpret_cast<uint2*>(to + d * 8 + quad * 4) = make_uint2(pack<T>(o[d][2 * x] * r, o[d + 1][2 * x] * r),
-                                                                          pack<T>(o[d][2 * x + 1] * r, o[d + 1][2 * x + 1] * r));
-          if (P.lse && quad == 0) {
-            const float l = x ? l1 : l0, mx = x ? mx1 : mx0;
+        for (int d = 0; d < kOT; d += 2) {
+          const float4 y = make_float4(o[d][2 * x] * r, o[d + 1][2 * x] * r, o[d][2 * x + 1] * r, o[d + 1][2 * x + 1] * r);
+          if (whole)
+            *reinterpret_cast<uint2*>(to + d * 8 + quad * 4) = make_uint2(Pack<T>::pack(y.x, y.y), Pack<T>::pack(y.z, y.w));
+          else
+            piece_out<D>(P, mine)[(d * 2 + quad) * MT + m] = y;
+        }
+        if (quad == 0) {
+          if (!whole) piece_ml(P, mine)[m] = make_float2(mx, l);
+          else if (P.lse)
             P.lse[(size_t)(g.q0 + j) * (P.group * P.hkv) + head] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
-          }
         }
       }
     }
@@ -621,12 +589,13 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
       arrive(&c.empty[keys.slot]);
       arrive(&c.empty[values.slot]);
     }
+    if (!whole) join_unit<T, Pack<T>, D, 32 * S::kWarps>(P, g, &c.last, bar_warps<S::kWarps>);
   }
 }
 
 // ------------------------------------------------------------------ kernel
 template <class T, int D, int MT>
-__global__ void __launch_bounds__(kThreads, (Shape<T, D, MT>::kCtas))
+__global__ void __launch_bounds__((Shape<T, D, MT>::kThreads), (Shape<T, D, MT>::kCtas))
     attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   using S = Shape<T, D, MT>;
   static_assert(S::kSlots >= 4, "ring length");
@@ -638,22 +607,22 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, MT>::kCtas))
   if (tid == 0) {
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(&c.full[i]);
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&c.empty[i])), "r"(kWarps) : "memory");
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&c.empty[i])), "r"(S::kWarps) : "memory");
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kWarps && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &mv : &mk) : "memory");
+  if (warp == S::kWarps && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &mv : &mk) : "memory");
 
-  find_range<kThreads>(P, c.range_sums, &c.range);
+  find_range<S::kThreads>(P, c.range_sums, &c.range);
   if (c.range.cut.ctas == 0) return;
-  if (warp == kWarps) load_warp<S, MT>(P, &mk, &mv, ring, c, c.range);
+  if (warp == S::kWarps) load_warp<S, MT>(P, &mk, &mv, ring, c, c.range);
   else compute_warps<S, T, D, MT>(P, ring, sq, c, c.range);
 }
 
 template <class T, int D, int MT>
 AttendKernel entry() {
   using S = Shape<T, D, MT>;
-  return {reinterpret_cast<const void*>(&attend_kernel<T, D, MT>), kThreads, S::kSlots, 1, S::kCtas, kTile, smem_bytes<S>(MT)};
+  return {reinterpret_cast<const void*>(&attend_kernel<T, D, MT>), S::kThreads, S::kSlots, 1, S::kCtas, kTile, smem_bytes<S>(MT)};
 }
 template <class T, int D>
 AttendKernel by_rows(int mt) {
