@@ -28,6 +28,11 @@
 //  - four softmax warps: a thread owns a query row (a lane of tensor memory),
 //    so maxima and sums need no exchange; it reads its 64 scores, writes its
 //    weights over them and never waits for the products in between.
+//  - With 64 columns a tile's loads are short and one warp's 64 exponentials a
+//    row would take longer.  Where a unit has at most 64 (32) query rows they
+//    are there twice (four times), in lanes 64 (32) apart, and each copy weighs
+//    its half (quarter) of a tile's keys and zeros elsewhere; the copies' sums
+//    and outputs are added at the end of the unit.
 //  Query rows past the live ones are whatever follows in shared memory: rows
 //  of a product do not mix, and nothing reads theirs.  Padding to 128 rows
 //  costs tensor time only (measured with one live row in eight it stays below
@@ -53,7 +58,7 @@ constexpr int kSoftmaxWarps = 4;                 // warps 0 .. 3: a warp reaches
 constexpr int kLoadWarp = 4, kProductWarp = 5;
 constexpr int kThreads = 192;
 constexpr int kMaxSlots = 16;                    // tiles of keys or values in the ring
-constexpr int kControl = 1536;                   // bytes of the control block, at most
+constexpr int kControl = 2048;                   // bytes of the control block, at most
 constexpr uint32_t kDrainPolls = 1u << 22;
 
 // ------------------------------------------------------------------ types
@@ -155,6 +160,28 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32])
       "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_load(uint32_t (&r)[16], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_load(uint32_t (&r)[1], uint32_t at) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;" : "=r"(r[0]) : "r"(at) : "memory");
 }
@@ -165,8 +192,10 @@ __device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lead) {
 }
 
 // ------------------------------------------------------------------ shape of one instantiation
-template <class T, int D>
+template <class T, int D, int KEYS>
 struct Shape {
+  static constexpr int kCopies = kTile / KEYS;               // of the queries; a softmax thread weighs KEYS keys of a tile
+  static constexpr int kLanes = 128 / kCopies;               // lanes of a copy
   static constexpr int kRuns = D / 64;                       // runs of 64 columns (128 bytes)
   static constexpr int kRun = kTile * 128;                   // bytes of a run of a tile
   static constexpr int kSlot = kRuns * kRun;                 // bytes of a tile of keys or of values
@@ -191,8 +220,15 @@ struct Control {
   int slow[2];         // the tile's values were added by the softmax warps
   int last;
   uint32_t tmem;
+  float2 ml[128];      // of the copies of a row
 };
 static_assert(sizeof(Control) <= kControl, "control block");
+
+// Rows of a query buffer: where there are copies, all 128.
+template <class S>
+__device__ __forceinline__ uint32_t q_rows(const AttendParams& P) {
+  return S::kCopies > 1 ? 128u : (uint32_t)P.rows;
+}
 
 // A place in the ring: tiles of keys and of values take turns.
 struct Turn {
@@ -236,7 +272,7 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
   const int sub = lane & ((1 << subs_shift) - 1), nth = lane >> subs_shift;
   const int page_mask = (1 << P.page_shift) - 1;
   const int groups = (1 << (1 << (box_shift - 4))) - 1;  // 16-key groups of a copy, as bits
-  const uint32_t q_bytes = (uint32_t)P.rows * D * 2;
+  const uint32_t q_bytes = q_rows<S>(P) * D * 2;
   Turn turn;
   int asked = 0;                                         // copies in flight or landed, at most P.slots
   bool dead = false;
@@ -274,8 +310,10 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
       for (int i = lane; i < g.live * (D / 8); i += 32) {
         const int m = i / (D / 8), piece = i % (D / 8), f = g.mt * P.rows + m, j = token_of(P, f);
         const T* src = static_cast<const T*>(P.q) + (g.q0 + j) * P.q_stride + (g.h * P.group + f - j * P.group) * D + piece * 8;
-        const uint32_t dst = to + (piece >> 3) * (P.rows * 128) + m * 128 + (((piece & 7) ^ (m & 7)) << 4);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        const uint32_t dst = to + (piece >> 3) * (q_rows<S>(P) * 128) + m * 128 + (((piece & 7) ^ (m & 7)) << 4);
+#pragma unroll
+        for (int n = 0; n < S::kCopies; ++n)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + n * S::kLanes * 128), "l"(src) : "memory");
       }
     }
     bool published = false;
@@ -339,7 +377,7 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
 // ------------------------------------------------------------------ product thread
 template <class S, class T, int D>
 __device__ void product_thread(const AttendParams& P, uint32_t sq, uint32_t ring, Control& c) {
-  const uint32_t tmem = c.tmem, q_bytes = (uint32_t)P.rows * D * 2, q_run = (uint32_t)P.rows * 128;
+  const uint32_t tmem = c.tmem, q_bytes = q_rows<S>(P) * D * 2, q_run = q_rows<S>(P) * 128;
   Turn turn;
   bool dead = false;
   auto wait = [&](unsigned long long* m, uint32_t parity) {
@@ -398,12 +436,13 @@ __device__ void product_thread(const AttendParams& P, uint32_t sq, uint32_t ring
 }
 
 // ------------------------------------------------------------------ softmax warps
-template <class S, class T, int D>
-__device__ void softmax_warps(const AttendParams& P, unsigned char* ring, Control& c) {
+template <class S, class T, int D, int KEYS>
+__device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned char* ring, Control& c) {
   using E = Elem<T>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t lanes = c.tmem + ((uint32_t)warp << 21);  // this warp's lanes of tensor memory
   const uint32_t out_at = lanes + S::kOut;
+  const int copy = tid / S::kLanes, row = tid % S::kLanes, key0 = copy * KEYS;
   Turn turn;
   bool dead = false;
   auto wait = [&](unsigned long long* m, uint32_t parity) {
@@ -422,9 +461,9 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* ring, Contro
     const Segment g = c.seg[sg & 1];
     more = g.count > 0 && !dead;
     if (!more) break;
-    const bool busy = warp * 32 < g.live;  // the warp has live rows
-    const bool live = tid < g.live;
-    const int f = g.mt * P.rows + tid, token = token_of(P, f);
+    const bool busy = warp * 32 % S::kLanes < g.live;  // the warp has live rows
+    const bool live = row < g.live;
+    const int f = g.mt * P.rows + row, token = token_of(P, f);
     const int p = live ? g.len - g.n + token : -1;
     const float scale = P.scale_log2;
     float mx = -INFINITY, l = 0.0f;
@@ -469,17 +508,17 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* ring, Contro
         slow = any_softmax(wild != 0);
       }
       if (busy) {
-        uint32_t x[64];
-        tmem_load(x, lanes + b * kTile);
+        uint32_t x[KEYS];
+        tmem_load(x, lanes + b * kTile + key0);
         auto score = [&](int n) { return __uint_as_float(x[n]); };
         if (part) {
 #pragma unroll
-          for (int n = 0; n < 64; ++n)
-            if (!visible(P, base + n, p) || ((bad >> (n >> 4)) & 1)) x[n] = 0xff800000u;
+          for (int n = 0; n < KEYS; ++n)
+            if (!visible(P, base + key0 + n, p) || ((bad >> ((key0 + n) >> 4)) & 1)) x[n] = 0xff800000u;
         }
         float t0 = score(0), t1 = score(1), t2 = score(2), t3 = score(3);
 #pragma unroll
-        for (int n = 4; n < 64; n += 4) {
+        for (int n = 4; n < KEYS; n += 4) {
           t0 = fmaxf(t0, score(n));
           t1 = fmaxf(t1, score(n + 1));
           t2 = fmaxf(t2, score(n + 2));
@@ -507,17 +546,20 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* ring, Contro
         const float z = mx == -INFINITY ? 0.0f : mx;
         // weights are rounded to 16 bits for the product (half a step, 2^-9 or 2^-12 of each, random in sign); their
         // sum is not
-        uint32_t w[32];
+        uint32_t w[KEYS / 2];
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-        for (int n = 0; n < 32; ++n) {
+        for (int n = 0; n < KEYS / 2; ++n) {
           const float a = ex2(fmaf(score(2 * n), scale, -z)), e = ex2(fmaf(score(2 * n + 1), scale, -z));
           s0 += a;
           s1 += e;
           w[n] = E::pack(a, e);
         }
         l += s0 + s1;
-        tmem_store(lanes + b * kTile, w);
+        tmem_store(lanes + b * kTile + key0 / 2, w);
+        const uint32_t zeros[KEYS / 2] = {};
+#pragma unroll
+        for (int n = 1; n < S::kCopies; ++n) tmem_store(lanes + b * kTile + (copy + n) % S::kCopies * (KEYS / 2), zeros);
         store_wait();
       }
       if (part) {
@@ -537,7 +579,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* ring, Contro
               tmem_load(pair, lanes + b * kTile + (n >> 1));
               const float2 ws = E::unpack(pair[0]);
               const float wt = n & 1 ? ws.y : ws.x;
-              const bool sees = visible(P, base + n, p) && !((bad >> (n >> 4)) & 1);
+              const bool sees = visible(P, base + n, p) && !((bad >> (n >> 4)) & 1) && n / KEYS == copy;
               const unsigned char* line = values + (d >> 6) * S::kRun + n * 128;
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
@@ -570,34 +612,81 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* ring, Contro
     // ---- the unit's output, or this CTA's piece of it
     added(it - 1);
     const bool whole = g.ca == g.cb;
-    if (busy) {
-      const int mine = piece_of(g, blockIdx.x);
-      const int head = g.h * P.group + f - token * P.group;
-      const float r = l == 0.0f ? 0.0f : 1.0f / l;
-      T* to = static_cast<T*>(P.out) + (g.q0 + token) * P.out_stride + head * D;
-      float4* part_to = piece_out<D>(P, mine) + tid;
+    const int mine = piece_of(g, blockIdx.x), head = g.h * P.group + f - token * P.group;
+    auto write_sums = [&](float m, float sum) {  // of a live row
+      if (!whole) piece_ml(P, mine)[row] = make_float2(m, sum);
+      else if (P.lse)
+        P.lse[(size_t)(g.q0 + token) * (P.group * P.hkv) + head] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+    };
+    if constexpr (S::kCopies == 1) {
+      if (busy) {
+        const float r = l == 0.0f ? 0.0f : 1.0f / l;
+        T* to = static_cast<T*>(P.out) + (g.q0 + token) * P.out_stride + head * D;
+        float4* part_to = piece_out<D>(P, mine) + row;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          uint32_t o[32];
+          tmem_load(o, out_at + d);
+          auto val = [&](int n) { return __uint_as_float(o[n]); };
+          if (!live) continue;
+          if (whole) {
+#pragma unroll
+            for (int n = 0; n < 32; n += 8)
+              *reinterpret_cast<uint4*>(to + d + n) =
+                  make_uint4(E::pack(val(n) * r, val(n + 1) * r), E::pack(val(n + 2) * r, val(n + 3) * r),
+                             E::pack(val(n + 4) * r, val(n + 5) * r), E::pack(val(n + 6) * r, val(n + 7) * r));
+          } else {
+#pragma unroll
+            for (int n = 0; n < 32; n += 4)
+              part_to[(size_t)((d + n) >> 2) * P.rows] = make_float4(val(n), val(n + 1), val(n + 2), val(n + 3));
+          }
+        }
+        if (live) write_sums(mx, l);
+      }
+    } else {
+      // the copies' outputs are added by way of the segment's query buffer, whose products are done: 32 columns of
+      // 128 lanes at a time, every thread then adding four columns of a row
+      static_assert(128 * D * 2 >= 128 * 32 * 4, "room for 32 columns");
+      float4* room = reinterpret_cast<float4*>(sq + (P.q_bufs == 2 && (sg & 1) ? 128 * D * 2 : 0));
+      c.ml[tid] = make_float2(mx, l);
+      bar_softmax();
+      float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int n = 0; n < S::kCopies; ++n) top = fmaxf(top, c.ml[row + n * S::kLanes].x);
+      const float zero = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+      for (int n = 0; n < S::kCopies; ++n) sum += c.ml[row + n * S::kLanes].y * ex2(c.ml[row + n * S::kLanes].x - zero);
+      const float by = ex2(mx - zero) * (whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f);
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
-        uint32_t o[32];
-        tmem_load(o, out_at + d);
-        auto val = [&](int n) { return __uint_as_float(o[n]); };
-        if (!live) continue;
-        if (whole) {
+        if (busy) {
+          uint32_t o[32];
+          tmem_load(o, out_at + d);
+          auto val = [&](int n) { return __uint_as_float(o[n]) * by; };
+          if (live) {
 #pragma unroll
-          for (int n = 0; n < 32; n += 8)
-            *reinterpret_cast<uint4*>(to + d + n) =
-                make_uint4(E::pack(val(n) * r, val(n + 1) * r), E::pack(val(n + 2) * r, val(n + 3) * r),
-                           E::pack(val(n + 4) * r, val(n + 5) * r), E::pack(val(n + 6) * r, val(n + 7) * r));
-        } else {
-#pragma unroll
-          for (int n = 0; n < 32; n += 4)
-            part_to[(size_t)((d + n) >> 2) * P.rows] = make_float4(val(n), val(n + 1), val(n + 2), val(n + 3));
+            for (int n = 0; n < 32; n += 4) room[(n >> 2) * 128 + tid] = make_float4(val(n), val(n + 1), val(n + 2), val(n + 3));
+          }
         }
+        bar_softmax();
+        if (live) {
+          for (int n = copy; n < 8; n += S::kCopies) {
+            float4 y = room[n * 128 + row];
+#pragma unroll
+            for (int x = 1; x < S::kCopies; ++x) {
+              const float4 z = room[n * 128 + row + x * S::kLanes];
+              y = make_float4(y.x + z.x, y.y + z.y, y.z + z.z, y.w + z.w);
+            }
+            if (whole)
+              *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + (g.q0 + token) * P.out_stride + head * D + d + n * 4) =
+                  make_uint2(E::pack(y.x, y.y), E::pack(y.z, y.w));
+            else
+              piece_out<D>(P, mine)[(size_t)((d >> 2) + n) * P.rows + row] = y;
+          }
+        }
+        bar_softmax();
       }
-      if (live) {
-        if (!whole) piece_ml(P, mine)[tid] = make_float2(mx, l);
-        else if (P.lse) P.lse[(size_t)(g.q0 + token) * (P.group * P.hkv) + head] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
-      }
+      if (live && copy == 0) write_sums(top, sum);
     }
     fence_before();
     __syncwarp();
@@ -611,15 +700,15 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* ring, Contro
 }
 
 // ------------------------------------------------------------------ kernel
-template <class T, int D>
-__global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas))
+template <class T, int D, int KEYS>
+__global__ void __launch_bounds__(kThreads, (Shape<T, D, KEYS>::kCtas))
     attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-  using S = Shape<T, D>;
+  using S = Shape<T, D, KEYS>;
   extern __shared__ unsigned char raw[];
   __shared__ Control c;
   // query buffers first: products read 128 rows from each of their runs, into the ring where fewer are live
   unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  unsigned char* ring = base + P.q_bufs * P.rows * D * 2;
+  unsigned char* ring = base + P.q_bufs * q_rows<S>(P) * D * 2;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < P.slots; ++i) {
@@ -654,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas))
     if (lane == 0) product_thread<S, T, D>(P, smem_u32(base), smem_u32(ring), c);
     __syncwarp();
   } else {
-    softmax_warps<S, T, D>(P, ring, c);
+    softmax_warps<S, T, D, KEYS>(P, base, ring, c);
   }
   fence_before();
   __syncthreads();
@@ -665,17 +754,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas))
 }
 
 // The kernel for `rows` query rows of a unit, its ring length and shared memory.
-template <class T, int D>
+template <class T, int D, int KEYS = kTile>
 AttendKernel entry(int rows) {
-  using S = Shape<T, D>;
+  using S = Shape<T, D, KEYS>;
   const int share = (228 * 1024 / S::kCtas - 1024 - kControl - 1024) & ~1023;  // a CTA's, without the control block
   AttendKernel k;
-  k.fn = reinterpret_cast<const void*>(&attend_kernel<T, D>);
+  k.fn = reinterpret_cast<const void*>(&attend_kernel<T, D, KEYS>);
   k.threads = kThreads;
   k.ctas = S::kCtas;
   k.tile = kTile;
-  k.q_bufs = rows <= 64 ? 2 : 1;  // a second buffer hides the gathering of the next segment's queries; 128 rows leave no room
-  const int q = k.q_bufs * rows * D * 2;
+  // a second buffer hides the gathering of the next segment's queries; 128 rows of 128 columns leave no room for it
+  const int q_rows = S::kCopies > 1 ? 128 : rows;
+  k.q_bufs = q_rows * D <= 64 * 128 ? 2 : 1;
+  const int q = k.q_bufs * q_rows * D * 2;
   k.slots = (share - 1024 - q) / S::kSlot;
   if (k.slots > kMaxSlots) k.slots = kMaxSlots;
   k.smem = 1024 + (size_t)q + (size_t)k.slots * S::kSlot;
@@ -683,7 +774,8 @@ AttendKernel entry(int rows) {
 }
 template <class T>
 AttendKernel pick(int d, int rows) {
-  return d == 64 ? entry<T, 64>(rows) : d == 128 ? entry<T, 128>(rows) : entry<T, 256>(rows);
+  if (d == 64) return rows <= 32 ? entry<T, 64, 16>(rows) : rows == 64 ? entry<T, 64, 32>(rows) : entry<T, 64>(rows);
+  return d == 128 ? entry<T, 128>(rows) : entry<T, 256>(rows);
 }
 
 }  // namespace kv
