@@ -94,6 +94,16 @@ __device__ __forceinline__ void mbar_init_n(unsigned long long* m, int n) {
 __device__ __forceinline__ void arrive(unsigned long long* m) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(m)) : "memory");
 }
+// One look at a barrier's phase.  Looks at two barriers overlap, where one wait after the other would take twice the
+// time even if both phases are done.
+__device__ __forceinline__ bool done(unsigned long long* m, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(smem_u32(m)), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ void expect(unsigned long long* m, int bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(m)), "r"(bytes) : "memory");
 }
@@ -388,9 +398,10 @@ __device__ void product_thread(const AttendParams& P, uint32_t sq, uint32_t ring
   // adds the weights of tile `tile` times its values to the output
   auto values = [&](uint32_t tile, const Turn& at, bool first) {
     const int b = tile & 1;
-    wait(&c.p_full[b], (tile >> 1) & 1);
-    wait(&c.full[at.slot], at.parity);
+    const bool there = done(&c.full[at.slot], at.parity), weighed = done(&c.p_full[b], (tile >> 1) & 1);
     if (first) wait(&c.o_free, (sg & 1) ^ 1);
+    if (!there) wait(&c.full[at.slot], at.parity);
+    if (!weighed) wait(&c.p_full[b], (tile >> 1) & 1);
     if (dead) return;
     fence_after();
     if (!c.slow[b]) {
@@ -411,8 +422,10 @@ __device__ void product_thread(const AttendParams& P, uint32_t sq, uint32_t ring
     Turn before;  // the values of the tile before
     for (int i = 0; i < count && !dead; ++i, ++it) {
       const int b = it & 1;
-      wait(&c.full[turn.slot], turn.parity);
-      wait(&c.pv_done[b], ((it >> 1) & 1) ^ 1);  // the weights of two tiles ago, in the same columns
+      // the keys, and the weights of two tiles ago, which are in the same columns
+      const bool there = done(&c.full[turn.slot], turn.parity), used = done(&c.pv_done[b], ((it >> 1) & 1) ^ 1);
+      if (!there) wait(&c.full[turn.slot], turn.parity);
+      if (!used) wait(&c.pv_done[b], ((it >> 1) & 1) ^ 1);
       if (dead) break;
       fence_after();
 #pragma unroll
