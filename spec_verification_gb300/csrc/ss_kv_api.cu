@@ -70,22 +70,25 @@ ss::AttendKernel attend_kernel(const ss_kv_config& c, int row_tile) {
               : (low ? ss::kv_attend_f16_e4m3(c.head_dim, row_tile) : ss::kv_attend_f16(c.head_dim, row_tile));
 }
 
-// A cache as the copies see it: (run of 128 bytes, token, run number, head, page).
-ss_status encode(CUtensorMap* map, const ss_kv_plan* p, const ss_kv_cache* cache, void* base) {
+// A cache as a kernel's copies see it: (part of a head, token, number of the part, head, page).  Swizzled heads come in
+// parts of at most 128 bytes; a copy of 16-bit values has all parts of 64 tokens, or one part of fewer (a smaller page),
+// so that in shared memory a tile is its parts of 64 tokens either way; one of 8-bit values always has all.
+ss_status encode(CUtensorMap* map, const ss_kv_plan* p, const ss_kv_cache* cache, void* base, bool swizzled) {
   const ss_kv_config& c = p->c;
-  const cuuint64_t el = c.cache_dtype == SS_E4M3 ? 1 : 2;
-  const cuuint64_t row = c.head_dim * el, atom = std::min<cuuint64_t>(row, 128);
-  const cuuint64_t dims[5] = {atom / el, (cuuint64_t)c.page_size, row / atom, (cuuint64_t)c.kv_heads, (cuuint64_t)c.num_pages};
-  const cuuint64_t strides[4] = {cache->token_stride * el, atom, cache->head_stride * el, cache->page_stride * el};
-  // a copy of 64 tokens has every run of a tile, one of fewer (a smaller page) has one, so that in shared memory a
-  // tile is its runs of 64 tokens either way; the 8-bit kernel takes all runs of a page together
-  const cuuint32_t tokens = (cuuint32_t)std::min(c.page_size, 64);
-  const cuuint32_t box[5] = {(cuuint32_t)(atom / el), tokens, tokens == 64 || el == 1 ? (cuuint32_t)(row / atom) : 1, 1, 1};
+  const bool low = c.cache_dtype == SS_E4M3;
+  const cuuint32_t el = low ? 1 : 2, tokens = std::min(c.page_size, 64);
+  const cuuint32_t part = swizzled ? std::min<cuuint32_t>(c.head_dim, 128 / el) : c.head_dim, parts = c.head_dim / part;
+  const cuuint64_t dims[5] = {part, (cuuint64_t)c.page_size, parts, (cuuint64_t)c.kv_heads, (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[4] = {(cuuint64_t)cache->token_stride * el, (cuuint64_t)part * el, (cuuint64_t)cache->head_stride * el,
+                                 (cuuint64_t)cache->page_stride * el};
+  const cuuint32_t box[5] = {part, tokens, low || tokens == 64 ? parts : 1, 1, 1};
   const cuuint32_t step[5] = {1, 1, 1, 1, 1};
-  const CUresult r = encode_tiled()(map, el == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, base, dims, strides,
-                                    box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                    atom == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUtensorMapSwizzle swizzle = !swizzled          ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                     : part * el == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                        : CU_TENSOR_MAP_SWIZZLE_64B;
+  const CUresult r = encode_tiled()(map, low ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, base, dims, strides, box,
+                                    step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SS_ERR_CUDA, "cuTensorMapEncodeTiled refused the cache's layout");
   return SS_OK;
 }
@@ -163,7 +166,7 @@ ss_status ss_kv_plan_create(ss_kv_plan** out, const ss_kv_config* config) {
   // the smallest row tile that holds a row's usual query rows: larger tiles waste products on rows that do not
   // exist, smaller ones read the keys once for each of several tiles
   const int64_t rows = (int64_t)c.max_new * group;
-  const int row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || c.cache_dtype == SS_E4M3 ? 64 : 128;
+  const int row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   const ss::AttendKernel k = attend_kernel(c, row_tile);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
   if (e != cudaSuccess) return cuda_fail(e, "kernel attributes");
@@ -317,8 +320,9 @@ ss_status ss_attend(const ss_attend_batch* b, const ss_kv_cache* cache) {
   if (!aligned(b->workspace, 256)) return fail(SS_ERR_ALIGN, "workspace must be 256-byte aligned");
   const OnDevice on(c.device);
   CUtensorMap mk, mv;
-  s = encode(&mk, p, cache, cache->k);
-  if (s == SS_OK) s = encode(&mv, p, cache, cache->v);
+  const ss::AttendKernel k = attend_kernel(c, p->row_tile);
+  s = encode(&mk, p, cache, cache->k, k.swizzled);
+  if (s == SS_OK) s = encode(&mv, p, cache, cache->v, k.swizzled);
   if (s != SS_OK) return s;
   const int32_t longest = c.max_blocks * c.page_size;
   ss::AttendParams P = {};
@@ -348,9 +352,9 @@ ss_status ss_attend(const ss_attend_batch* b, const ss_kv_cache* cache) {
   P.part = reinterpret_cast<float*>(w + p->off_part);
   P.ml = reinterpret_cast<float2*>(w + p->off_ml);
   P.spin_limit = kSpin;
-  const ss::AttendKernel k = attend_kernel(c, p->row_tile);
   P.rows = p->row_tile;
   P.slots = k.slots;
+  P.raw_slots = k.raw_slots;
   P.q_bufs = k.q_bufs;
   // About 2 us beside its tiles, which take the longer the more bytes they have: two tiles of 32 KB.
   // Measured (1, 2, 4 tiles): 64 x 1 rows of 32 KB tiles 101, 95.7, 96.3 us; 96 x 3 rows of 16 KB tiles 89, 82, 76 us.

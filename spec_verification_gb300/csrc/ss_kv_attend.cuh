@@ -45,6 +45,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "ss_kv_join.cuh"
@@ -56,9 +57,9 @@ namespace kv {
 constexpr int kTile = 64;                        // keys of a tile
 constexpr int kSoftmaxWarps = 4;                 // warps 0 .. 3: a warp reaches the 32 lanes of its number modulo 4
 constexpr int kLoadWarp = 4, kProductWarp = 5;
-constexpr int kThreads = 192;
 constexpr int kMaxSlots = 16;                    // tiles of keys or values in the ring
-constexpr int kControl = 2048;                   // bytes of the control block, at most
+constexpr int kMaxRaw = 8;                       // 8-bit tiles in their ring
+constexpr int kControl = 3072;                   // bytes of the control block, at most
 constexpr uint32_t kDrainPolls = 1u << 22;
 
 // ------------------------------------------------------------------ types
@@ -202,8 +203,13 @@ __device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lead) {
 }
 
 // ------------------------------------------------------------------ shape of one instantiation
-template <class T, int D, int KEYS>
+template <class T, int D, int KEYS, bool LOW>
 struct Shape {
+  using Mul = typename std::conditional<LOW, __half, T>::type;  // what is multiplied: 8-bit values become f16
+  static constexpr bool kLow = LOW;
+  static constexpr bool kScaleQ = LOW && std::is_same<T, __nv_bfloat16>::value;
+  static constexpr int kThreads = LOW ? 320 : 192;           // 8 bits: four warps more, which convert
+  static constexpr int kRaw = kTile * D;                     // bytes of a tile of 8-bit values
   static constexpr int kCopies = kTile / KEYS;               // of the queries; a softmax thread weighs KEYS keys of a tile
   static constexpr int kLanes = 128 / kCopies;               // lanes of a copy
   static constexpr int kRuns = D / 64;                       // runs of 64 columns (128 bytes)
@@ -213,7 +219,7 @@ struct Shape {
   static constexpr uint32_t kCols = D <= 128 ? 256 : 512;    // columns of tensor memory: two tiles of scores, the output
   static constexpr uint32_t kOut = 128;
   // instruction descriptors: 32-bit sums, both operands of type T, 128 rows; S: 64 columns; O: D columns, V as it lies
-  static constexpr uint32_t kCommon = 1u << 4 | Elem<T>::kFormat << 7 | Elem<T>::kFormat << 10 | (128u >> 4) << 24;
+  static constexpr uint32_t kCommon = 1u << 4 | Elem<Mul>::kFormat << 7 | Elem<Mul>::kFormat << 10 | (128u >> 4) << 24;
   static constexpr uint32_t kScores = kCommon | (kTile >> 3) << 17;
   static constexpr uint32_t kValues = kCommon | 1u << 16 | (uint32_t)(D >> 3) << 17;
 };
@@ -222,12 +228,15 @@ struct Control {
   unsigned long long full[kMaxSlots], empty[kMaxSlots];  // ring: copies landed; products done with them
   unsigned long long seg_full[2], seg_empty[2];          // segment published with its queries; done with by all
   unsigned long long s_full[2], p_full[2], pv_done[2];   // scores there; weights there; added to the output
-  unsigned long long o_free, drained;                    // output read; all products done
+  unsigned long long o_free, q_free, drained;            // output read; last scores of a segment there; all products done
   Segment seg[2];
   Range range;
-  long long sums[kThreads / 32];
-  int bad[kMaxSlots];  // per tile of keys: its 16-key groups that lie on pages with a bad id
+  long long sums[10];
+  int bad[kMaxSlots];  // per place of a tile of keys in the ring: its 16-key groups that lie on pages with a bad id
+  int bad_mul[kMaxSlots];  // the same by its place in the ring of the products (8 bits)
   int slow[2];         // the tile's values were added by the softmax warps
+  unsigned long long raw_full[kMaxRaw], raw_empty[kMaxRaw];  // ring of 8-bit tiles: copies landed; converted
+  float q_back[2][128];  // per query row, what its f16 values were scaled by, undone
   int last;
   uint32_t tmem;
   float2 ml[128];      // of the copies of a row
@@ -273,18 +282,25 @@ __device__ __forceinline__ bool visible(const AttendParams& P, int key, int p) {
 
 // ------------------------------------------------------------------ load warp
 template <class S, class T, int D>
-__device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t sq, uint32_t ring, Control& c) {
+__device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t sq, uint32_t ring, uint32_t raw,
+                          Control& c) {
+  // the ring that the copies fill
+  unsigned long long* const full = S::kLow ? c.raw_full : c.full;
+  unsigned long long* const empty = S::kLow ? c.raw_empty : c.empty;
+  const int slots = S::kLow ? P.raw_slots : P.slots;
+  const uint32_t copies = S::kLow ? raw : ring;
+  constexpr int kBytes = S::kLow ? S::kRaw : S::kSlot;
   const int lane = threadIdx.x & 31;
   const int box_shift = min(P.page_shift, 6);            // tokens of one copy
   const int subs_shift = 6 - box_shift;                  // copies of a run of a tile
-  const int runs = subs_shift ? S::kRuns : 1;            // a copy of 64 tokens has every run
+  const int runs = S::kLow || !subs_shift ? 1 : S::kRuns;  // a copy of 64 tokens, or of 8-bit values, has every run
   const int batch = 32 >> subs_shift;                    // tiles whose page ids one lane each holds
   const int sub = lane & ((1 << subs_shift) - 1), nth = lane >> subs_shift;
   const int page_mask = (1 << P.page_shift) - 1;
   const int groups = (1 << (1 << (box_shift - 4))) - 1;  // 16-key groups of a copy, as bits
   const uint32_t q_bytes = q_rows<S>(P) * D * 2;
   Turn turn;
-  int asked = 0;                                         // copies in flight or landed, at most P.slots
+  int asked = 0;                                         // copies in flight or landed, at most `slots`
   bool dead = false;
   Range k = c.range;
   Segment g;
@@ -292,9 +308,10 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
   bool more = true;
   while (more && !dead) {
     more = next_segment(P, k, g);
-    // the segment's place and query buffer: free once segment sg - 2 (or sg - 1) is done
-    const int prior = sg - P.q_bufs;
-    if (prior >= 0) dead = !__all_sync(0xffffffffu, mbar_wait(&c.seg_empty[prior & 1], (prior >> 1) & 1, P.spin_limit, 0u));
+    // the segment's place is free once segment sg - 2 is done with; so is a second query buffer, and an only one once
+    // the last scores of segment sg - 1 are there
+    if (sg >= 2) dead = !__all_sync(0xffffffffu, mbar_wait(&c.seg_empty[sg & 1], ((sg >> 1) & 1) ^ 1, P.spin_limit, 0u));
+    if (sg >= 1 && P.q_bufs == 1 && !dead) dead = !__all_sync(0xffffffffu, mbar_wait(&c.q_free, (sg & 1) ^ 1, P.spin_limit, 0u));
     if (dead) break;
     if (!more) g.count = 0;  // the end of the range
     if (lane == 0) c.seg[sg & 1] = g;
@@ -317,13 +334,52 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
     int next = fetch(0);
     if (more) {
       const uint32_t to = sq + (P.q_bufs == 2 && (sg & 1) ? q_bytes : 0u);
-      for (int i = lane; i < g.live * (D / 8); i += 32) {
+      const int pieces = g.live * (D / 8);
+      auto source = [&](int i) {
         const int m = i / (D / 8), piece = i % (D / 8), f = g.mt * P.rows + m, j = token_of(P, f);
-        const T* src = static_cast<const T*>(P.q) + (g.q0 + j) * P.q_stride + (g.h * P.group + f - j * P.group) * D + piece * 8;
-        const uint32_t dst = to + (piece >> 3) * (q_rows<S>(P) * 128) + m * 128 + (((piece & 7) ^ (m & 7)) << 4);
+        return static_cast<const T*>(P.q) + (g.q0 + j) * P.q_stride + (g.h * P.group + f - j * P.group) * D + piece * 8;
+      };
+      auto place = [&](int i) {
+        const int m = i / (D / 8), piece = i % (D / 8);
+        return to + (piece >> 3) * (q_rows<S>(P) * 128) + m * 128 + (((piece & 7) ^ (m & 7)) << 4);
+      };
+      if constexpr (S::kScaleQ) {
+        // bf16 to f16: a row is scaled by a power of two that brings its largest value near 2^14, so every value keeps
+        // its bits unless it is below 2^-28 of the largest
+        constexpr int kBatch = 8;  // loads in flight
+        for (int i0 = lane; i0 - lane < pieces; i0 += 32 * kBatch) {
+          uint4 x[kBatch];
 #pragma unroll
-        for (int n = 0; n < S::kCopies; ++n)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + n * S::kLanes * 128), "l"(src) : "memory");
+          for (int n = 0; n < kBatch; ++n)
+            x[n] = i0 + 32 * n < pieces ? __ldg(reinterpret_cast<const uint4*>(source(i0 + 32 * n))) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int n = 0; n < kBatch; ++n) {
+            const int i = i0 + 32 * n;
+            using B = Elem<__nv_bfloat16>;
+            using H = Elem<__half>;
+            const float2 v0 = B::unpack(x[n].x), v1 = B::unpack(x[n].y), v2 = B::unpack(x[n].z), v3 = B::unpack(x[n].w);
+            float top = fmaxf(fmaxf(fmaxf(fabsf(v0.x), fabsf(v0.y)), fmaxf(fabsf(v1.x), fabsf(v1.y))),
+                              fmaxf(fmaxf(fabsf(v2.x), fabsf(v2.y)), fmaxf(fabsf(v3.x), fabsf(v3.y))));
+#pragma unroll
+            for (int o = D / 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 240);      // biased exponent
+            const float up = __uint_as_float((uint32_t)(127 + 14 + 127 - ex) << 23);  // 2^(14 - exponent)
+            if (i >= pieces) continue;
+            if (i % (D / 8) == 0) c.q_back[sg & 1][i / (D / 8)] = __uint_as_float((uint32_t)(ex - 14) << 23);
+            const uint32_t w0 = H::pack(v0.x * up, v0.y * up), w1 = H::pack(v1.x * up, v1.y * up), w2 = H::pack(v2.x * up, v2.y * up),
+                           w3 = H::pack(v3.x * up, v3.y * up);
+#pragma unroll
+            for (int y = 0; y < S::kCopies; ++y)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(place(i) + y * S::kLanes * 128), "r"(w0), "r"(w1), "r"(w2), "r"(w3)
+                           : "memory");
+          }
+        }
+      } else {
+        for (int i = lane; i < pieces; i += 32) {
+#pragma unroll
+          for (int n = 0; n < S::kCopies; ++n)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(place(i) + n * S::kLanes * 128), "l"(source(i)) : "memory");
+        }
       }
     }
     bool published = false;
@@ -348,24 +404,24 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
         const int tok = (tile_of(g.u, g.from + i0 + j) * kTile + (sub << box_shift)) & page_mask;
 #pragma unroll
         for (int values = 0; values < 2; ++values) {
-          dead = !__all_sync(0xffffffffu, mbar_wait(&c.empty[turn.slot], turn.parity ^ 1, P.spin_limit, 0u));
+          dead = !__all_sync(0xffffffffu, mbar_wait(&empty[turn.slot], turn.parity ^ 1, P.spin_limit, 0u));
           if (dead) break;
           if (lane == 0) {
             if (!values) {
               int bits = 0;
               for (int s = 0; s < 1 << subs_shift; ++s)
                 if ((bad_lanes >> ((j << subs_shift) + s)) & 1) bits |= groups << (s << (box_shift - 4));
-              c.bad[turn.slot] = bits;
+              c.bad[turn.slot] = bits;  // (8 bits: handed on by the converting warps)
             }
-            expect(&c.full[turn.slot], S::kSlot);
+            expect(&full[turn.slot], kBytes);
           }
           __syncwarp();
           if (nth == j)
             for (int r = 0; r < runs; ++r)
-              tma_load(ring + turn.slot * S::kSlot + r * S::kRun + (sub << box_shift) * 128, values ? mv : mk, &c.full[turn.slot], tok, r,
-                       g.h, id);
-          turn.next(P.slots);
-          asked = min(asked + 1, P.slots);
+              tma_load(copies + turn.slot * kBytes + r * S::kRun + (sub << box_shift) * (S::kLow ? D : 128), values ? mv : mk,
+                       &full[turn.slot], tok, r, g.h, id);
+          turn.next(slots);
+          asked = min(asked + 1, slots);
         }
         if (!published && !dead) publish();
       }
@@ -377,10 +433,69 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
   asm volatile("cp.async.wait_all;" ::: "memory");
   for (; asked > 0; --asked) {
     if (--turn.slot < 0) {
-      turn.slot = P.slots - 1;
+      turn.slot = slots - 1;
       turn.parity ^= 1;
     }
-    mbar_wait(&c.full[turn.slot], turn.parity, kDrainPolls, 0u);
+    mbar_wait(&full[turn.slot], turn.parity, kDrainPolls, 0u);
+  }
+}
+
+// ------------------------------------------------------------------ converting warps
+// Two e4m3 values (the low 16 bits of w) as f16x2: exact.
+__device__ __forceinline__ uint32_t e4m3_f16(uint32_t w) {
+  uint32_t d;
+  asm("{\n .reg .b16 h;\n cvt.u16.u32 h, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(d) : "r"(w));
+  return d;
+}
+
+// From the ring of 8-bit tiles (a token after the other, as the copies bring them) to that of the products (runs of
+// 64 columns, swizzled).  The load warp publishes segments; these warps follow their tile counts.
+template <class S, int D>
+__device__ void convert_warps(const AttendParams& P, const unsigned char* raw, unsigned char* ring, Control& c) {
+  const int tid = threadIdx.x - 32 * (kProductWarp + 1), lane = tid & 31;
+  Turn from, to;
+  bool dead = false;
+  auto wait = [&](unsigned long long* m, uint32_t parity) {
+    if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(m, parity, P.spin_limit, 0u));
+  };
+  int sg = 0;
+  bool more = true;
+  while (more) {
+    wait(&c.seg_full[sg & 1], (sg >> 1) & 1);
+    const int count = dead ? 0 : c.seg[sg & 1].count;
+    more = count > 0;
+    for (int i = 0; i < 2 * count && !dead; ++i) {
+      wait(&c.raw_full[from.slot], from.parity);
+      wait(&c.empty[to.slot], to.parity ^ 1);
+      if (dead) break;
+      const uint4* src = reinterpret_cast<const uint4*>(raw + from.slot * S::kRaw);
+      unsigned char* dst = ring + to.slot * S::kSlot;
+      uint4 x[D / 32];
+#pragma unroll
+      for (int n = 0; n < D / 32; ++n) x[n] = src[tid + 128 * n];
+#pragma unroll
+      for (int n = 0; n < D / 32; ++n) {
+        const int at = tid + 128 * n, token = at / (D / 16), piece = at % (D / 16);  // 16 columns
+        unsigned char* line = dst + (piece >> 2) * S::kRun + token * 128;
+        const uint4 lo = make_uint4(e4m3_f16(x[n].x), e4m3_f16(x[n].x >> 16), e4m3_f16(x[n].y), e4m3_f16(x[n].y >> 16));
+        const uint4 hi = make_uint4(e4m3_f16(x[n].z), e4m3_f16(x[n].z >> 16), e4m3_f16(x[n].w), e4m3_f16(x[n].w >> 16));
+        // every other run's second half first: neighbouring runs would meet in the same banks
+        const int swap = (piece >> 2) & 1, c0 = (piece & 3) * 2 + swap, c1 = (piece & 3) * 2 + 1 - swap;
+        *reinterpret_cast<uint4*>(line + ((c0 ^ (token & 7)) << 4)) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(line + ((c1 ^ (token & 7)) << 4)) = swap ? lo : hi;
+      }
+      if (tid == 0 && (i & 1) == 0) c.bad_mul[to.slot] = c.bad[from.slot];
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) {
+        arrive(&c.raw_empty[from.slot]);
+        arrive(&c.full[to.slot]);
+      }
+      from.next(P.raw_slots);
+      to.next(P.slots);
+    }
+    if (more && lane == 0) arrive(&c.seg_empty[sg & 1]);
+    ++sg;
   }
 }
 
@@ -434,6 +549,7 @@ __device__ void product_thread(const AttendParams& P, uint32_t sq, uint32_t ring
                operand(ring + turn.slot * S::kSlot + (k >> 2) * S::kRun + (k & 3) * 32, 0), S::kScores, k != 0);
       commit(&c.s_full[b]);
       commit(&c.empty[turn.slot]);
+      if (i + 1 == count) commit(&c.q_free);
       turn.next(P.slots);
       if (i > 0) values(it - 1, before, i == 1);
       before = turn;
@@ -451,7 +567,9 @@ __device__ void product_thread(const AttendParams& P, uint32_t sq, uint32_t ring
 // ------------------------------------------------------------------ softmax warps
 template <class S, class T, int D, int KEYS>
 __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned char* ring, Control& c) {
-  using E = Elem<T>;
+  using E = Elem<typename S::Mul>;
+  using Out = Elem<T>;
+  constexpr int kChunk = S::kLow && KEYS > 32 ? 32 : KEYS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t lanes = c.tmem + ((uint32_t)warp << 21);  // this warp's lanes of tensor memory
   const uint32_t out_at = lanes + S::kOut;
@@ -478,7 +596,9 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
     const bool live = row < g.live;
     const int f = g.mt * P.rows + row, token = token_of(P, f);
     const int p = live ? g.len - g.n + token : -1;
-    const float scale = P.scale_log2;
+    float scale = P.scale_log2;
+    if (S::kLow && P.k_scale) scale *= P.k_scale[g.h];
+    if (S::kScaleQ && live) scale *= c.q_back[sg & 1][row];
     float mx = -INFINITY, l = 0.0f;
 
     for (int i = 0; i < g.count; ++i, ++it) {
@@ -490,7 +610,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
       turn.next(P.slots);
       wait(&c.s_full[b], (it >> 1) & 1);
       fence_after();
-      const int bad = c.bad[k_slot];
+      const int bad = (S::kLow ? c.bad_mul : c.bad)[k_slot];
       const bool part = partly(P, g.u, base, bad);
       bool slow = false;
       unsigned char* values = ring + v_turn.slot * S::kSlot;
@@ -521,23 +641,27 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         slow = any_softmax(wild != 0);
       }
       if (busy) {
-        uint32_t x[KEYS];
-        tmem_load(x, lanes + b * kTile + key0);
-        auto score = [&](int n) { return __uint_as_float(x[n]); };
-        if (part) {
+        // this thread's scores, kChunk at a time: one chunk where registers allow, else each is read once for the
+        // maximum and once for its weights
+        auto scores = [&](uint32_t (&x)[kChunk], int at) {
+          tmem_load(x, lanes + b * kTile + key0 + at);
+          if (part) {
 #pragma unroll
-          for (int n = 0; n < KEYS; ++n)
-            if (!visible(P, base + key0 + n, p) || ((bad >> ((key0 + n) >> 4)) & 1)) x[n] = 0xff800000u;
-        }
-        float t0 = score(0), t1 = score(1), t2 = score(2), t3 = score(3);
+            for (int n = 0; n < kChunk; ++n) {
+              const int in = key0 + at + n;
+              if (!visible(P, base + in, p) || ((bad >> (in >> 4)) & 1)) x[n] = 0xff800000u;
+            }
+          }
+        };
+        uint32_t x[kChunk];
+        float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int n = 4; n < KEYS; n += 4) {
-          t0 = fmaxf(t0, score(n));
-          t1 = fmaxf(t1, score(n + 1));
-          t2 = fmaxf(t2, score(n + 2));
-          t3 = fmaxf(t3, score(n + 3));
+        for (int at = 0; at < KEYS; at += kChunk) {
+          scores(x, at);
+#pragma unroll
+          for (int n = 0; n < kChunk; ++n) t[n & 3] = fmaxf(t[n & 3], __uint_as_float(x[n]));
         }
-        const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * scale;
+        const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
         const bool grow = live && top > (mx == -INFINITY ? mx : mx + 8.0f);
         if (__any_sync(0xffffffffu, grow)) {
           const float by = grow ? ex2(mx - top) : 1.0f;  // 0 if nothing was seen before
@@ -545,7 +669,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
           l *= by;
           if (i > 0) {
             added(it - 1);
-#pragma unroll
+#pragma unroll 1
             for (int d = 0; d < D; d += 32) {
               uint32_t o[32];
               tmem_load(o, out_at + d);
@@ -559,17 +683,21 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         const float z = mx == -INFINITY ? 0.0f : mx;
         // weights are rounded to 16 bits for the product (half a step, 2^-9 or 2^-12 of each, random in sign); their
         // sum is not
-        uint32_t w[KEYS / 2];
-        float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-        for (int n = 0; n < KEYS / 2; ++n) {
-          const float a = ex2(fmaf(score(2 * n), scale, -z)), e = ex2(fmaf(score(2 * n + 1), scale, -z));
-          s0 += a;
-          s1 += e;
-          w[n] = E::pack(a, e);
+        for (int at = 0; at < KEYS; at += kChunk) {
+          if (KEYS > kChunk) scores(x, at);
+          uint32_t w[kChunk / 2];
+          float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+          for (int n = 0; n < kChunk / 2; ++n) {
+            const float a = ex2(fmaf(__uint_as_float(x[2 * n]), scale, -z)), e = ex2(fmaf(__uint_as_float(x[2 * n + 1]), scale, -z));
+            s0 += a;
+            s1 += e;
+            w[n] = E::pack(a, e);
+          }
+          l += s0 + s1;
+          tmem_store(lanes + b * kTile + (key0 + at) / 2, w);
         }
-        l += s0 + s1;
-        tmem_store(lanes + b * kTile + key0 / 2, w);
         const uint32_t zeros[KEYS / 2] = {};
 #pragma unroll
         for (int n = 1; n < S::kCopies; ++n) tmem_store(lanes + b * kTile + (copy + n) % S::kCopies * (KEYS / 2), zeros);
@@ -625,6 +753,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
     // ---- the unit's output, or this CTA's piece of it
     added(it - 1);
     const bool whole = g.ca == g.cb;
+    const float v_scale = S::kLow && P.v_scale ? P.v_scale[g.h] : 1.0f;
     const int mine = piece_of(g, blockIdx.x), head = g.h * P.group + f - token * P.group;
     auto write_sums = [&](float m, float sum) {  // of a live row
       if (!whole) piece_ml(P, mine)[row] = make_float2(m, sum);
@@ -633,7 +762,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
     };
     if constexpr (S::kCopies == 1) {
       if (busy) {
-        const float r = l == 0.0f ? 0.0f : 1.0f / l;
+        const float r = (whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f) * v_scale;
         T* to = static_cast<T*>(P.out) + (g.q0 + token) * P.out_stride + head * D;
         float4* part_to = piece_out<D>(P, mine) + row;
 #pragma unroll 1
@@ -646,12 +775,12 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
 #pragma unroll
             for (int n = 0; n < 32; n += 8)
               *reinterpret_cast<uint4*>(to + d + n) =
-                  make_uint4(E::pack(val(n) * r, val(n + 1) * r), E::pack(val(n + 2) * r, val(n + 3) * r),
-                             E::pack(val(n + 4) * r, val(n + 5) * r), E::pack(val(n + 6) * r, val(n + 7) * r));
+                  make_uint4(Out::pack(val(n) * r, val(n + 1) * r), Out::pack(val(n + 2) * r, val(n + 3) * r),
+                             Out::pack(val(n + 4) * r, val(n + 5) * r), Out::pack(val(n + 6) * r, val(n + 7) * r));
           } else {
 #pragma unroll
             for (int n = 0; n < 32; n += 4)
-              part_to[(size_t)((d + n) >> 2) * P.rows] = make_float4(val(n), val(n + 1), val(n + 2), val(n + 3));
+              part_to[(size_t)((d + n) >> 2) * P.rows] = make_float4(val(n) * r, val(n + 1) * r, val(n + 2) * r, val(n + 3) * r);
           }
         }
         if (live) write_sums(mx, l);
@@ -669,7 +798,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
       const float zero = top == -INFINITY ? 0.0f : top;
 #pragma unroll
       for (int n = 0; n < S::kCopies; ++n) sum += c.ml[row + n * S::kLanes].y * ex2(c.ml[row + n * S::kLanes].x - zero);
-      const float by = ex2(mx - zero) * (whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f);
+      const float by = ex2(mx - zero) * (whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f) * v_scale;
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         if (busy) {
@@ -692,7 +821,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
             }
             if (whole)
               *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + (g.q0 + token) * P.out_stride + head * D + d + n * 4) =
-                  make_uint2(E::pack(y.x, y.y), E::pack(y.z, y.w));
+                  make_uint2(Out::pack(y.x, y.y), Out::pack(y.z, y.w));
             else
               piece_out<D>(P, mine)[(size_t)((d >> 2) + n) * P.rows + row] = y;
           }
@@ -708,35 +837,43 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
       arrive(&c.seg_empty[sg & 1]);
     }
     ++sg;
-    if (!whole) join_unit<T, E, D, 32 * kSoftmaxWarps>(P, g, &c.last, bar_softmax);
+    if (!whole) join_unit<T, Out, D, 32 * kSoftmaxWarps>(P, g, &c.last, bar_softmax);
   }
 }
 
 // ------------------------------------------------------------------ kernel
-template <class T, int D, int KEYS>
-__global__ void __launch_bounds__(kThreads, (Shape<T, D, KEYS>::kCtas))
+template <class T, int D, int KEYS, bool LOW>
+__global__ void __launch_bounds__((Shape<T, D, KEYS, LOW>::kThreads), (Shape<T, D, KEYS, LOW>::kCtas))
     attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-  using S = Shape<T, D, KEYS>;
+  using S = Shape<T, D, KEYS, LOW>;
   extern __shared__ unsigned char raw[];
   __shared__ Control c;
   // query buffers first: products read 128 rows from each of their runs, into the ring where fewer are live
   unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   unsigned char* ring = base + P.q_bufs * q_rows<S>(P) * D * 2;
+  unsigned char* raw_ring = ring + P.slots * S::kSlot;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
+    if (LOW) {
+      for (int i = 0; i < P.raw_slots; ++i) {
+        mbar_init_n(&c.raw_full[i], 1);
+        mbar_init_n(&c.raw_empty[i], 4);
+      }
+    }
     for (int i = 0; i < P.slots; ++i) {
-      mbar_init_n(&c.full[i], 1);
+      mbar_init_n(&c.full[i], LOW ? 4 : 1);
       mbar_init_n(&c.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init_n(&c.seg_full[i], 1);
-      mbar_init_n(&c.seg_empty[i], kSoftmaxWarps + 1);
+      mbar_init_n(&c.seg_empty[i], kSoftmaxWarps + 1 + (LOW ? 4 : 0));
       mbar_init_n(&c.s_full[i], 1);
       mbar_init_n(&c.p_full[i], kSoftmaxWarps);
       mbar_init_n(&c.pv_done[i], 1);
       c.slow[i] = 0;
     }
     mbar_init_n(&c.o_free, kSoftmaxWarps);
+    mbar_init_n(&c.q_free, 1);
     mbar_init_n(&c.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -746,17 +883,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, KEYS>::kCtas))
   }
   if (warp == kLoadWarp && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &mv : &mk) : "memory");
   fence_before();
-  find_range<kThreads>(P, c.sums, &c.range);  // ends in a barrier
+  find_range<S::kThreads>(P, c.sums, &c.range);  // ends in a barrier
   fence_after();
   if (c.range.cut.ctas == 0) {
     // no work: straight to the end
+  } else if (warp < kSoftmaxWarps) {
+    softmax_warps<S, T, D, KEYS>(P, base, ring, c);
   } else if (warp == kLoadWarp) {
-    load_warp<S, T, D>(P, &mk, &mv, smem_u32(base), smem_u32(ring), c);
+    load_warp<S, T, D>(P, &mk, &mv, smem_u32(base), smem_u32(ring), smem_u32(raw_ring), c);
   } else if (warp == kProductWarp) {
     if (lane == 0) product_thread<S, T, D>(P, smem_u32(base), smem_u32(ring), c);
     __syncwarp();
-  } else {
-    softmax_warps<S, T, D, KEYS>(P, base, ring, c);
+  } else if constexpr (LOW) {
+    convert_warps<S, D>(P, raw_ring, ring, c);
   }
   fence_before();
   __syncthreads();
@@ -766,29 +905,33 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, KEYS>::kCtas))
   }
 }
 
-// The kernel for `rows` query rows of a unit, its ring length and shared memory.
-template <class T, int D, int KEYS = kTile>
+// The kernel for `rows` query rows of a unit, its rings and shared memory.
+template <class T, int D, int KEYS, bool LOW>
 AttendKernel entry(int rows) {
-  using S = Shape<T, D, KEYS>;
+  using S = Shape<T, D, KEYS, LOW>;
   const int share = (228 * 1024 / S::kCtas - 1024 - kControl - 1024) & ~1023;  // a CTA's, without the control block
   AttendKernel k;
-  k.fn = reinterpret_cast<const void*>(&attend_kernel<T, D, KEYS>);
-  k.threads = kThreads;
+  k.fn = reinterpret_cast<const void*>(&attend_kernel<T, D, KEYS, LOW>);
+  k.threads = S::kThreads;
   k.ctas = S::kCtas;
   k.tile = kTile;
+  k.swizzled = !LOW;
   // a second buffer hides the gathering of the next segment's queries; 128 rows of 128 columns leave no room for it
   const int q_rows = S::kCopies > 1 ? 128 : rows;
   k.q_bufs = q_rows * D <= 64 * 128 ? 2 : 1;
   const int q = k.q_bufs * q_rows * D * 2;
-  k.slots = (share - 1024 - q) / S::kSlot;
-  if (k.slots > kMaxSlots) k.slots = kMaxSlots;
-  k.smem = 1024 + (size_t)q + (size_t)k.slots * S::kSlot;
+  // the loads fill the ring of products, or (8 bits) that of the copies: half a tile's bytes for each of its tiles
+  const int room = share - 1024 - q;
+  k.slots = std::min(LOW ? room / (S::kSlot + S::kRaw) : room / S::kSlot, kMaxSlots);
+  k.raw_slots = LOW ? std::min((room - k.slots * S::kSlot) / S::kRaw, kMaxRaw) : 0;
+  k.smem = 1024 + (size_t)q + (size_t)k.slots * S::kSlot + (size_t)k.raw_slots * S::kRaw;
   return k;
 }
-template <class T>
+// With 64 columns few query rows are copied (see above).
+template <class T, bool LOW>
 AttendKernel pick(int d, int rows) {
-  if (d == 64) return rows <= 32 ? entry<T, 64, 16>(rows) : rows == 64 ? entry<T, 64, 32>(rows) : entry<T, 64>(rows);
-  return d == 128 ? entry<T, 128>(rows) : entry<T, 256>(rows);
+  if (d == 64) return rows <= 32 ? entry<T, 64, 16, LOW>(rows) : rows == 64 ? entry<T, 64, 32, LOW>(rows) : entry<T, 64, kTile, LOW>(rows);
+  return d == 128 ? entry<T, 128, kTile, LOW>(rows) : entry<T, 256, kTile, LOW>(rows);
 }
 
 }  // namespace kv

@@ -622,7 +622,7 @@ __global__ void __launch_bounds__((Shape<T, D, MT>::kThreads), (Shape<T, D, MT>:
 template <class T, int D, int MT>
 AttendKernel entry() {
   using S = Shape<T, D, MT>;
-  return {reinterpret_cast<const void*>(&attend_kernel<T, D, MT>), S::kThreads, S::kSlots, 1, S::kCtas, kTile, smem_bytes<S>(MT)};
+  return {reinterpret_cast<const void*>(&attend_kernel<T, D, MT>), S::kThreads, S::kSlots, 0, 1, S::kCtas, kTile, smem_bytes<S>(MT), true};
 }
 template <class T, int D>
 AttendKernel by_rows(int mt) {

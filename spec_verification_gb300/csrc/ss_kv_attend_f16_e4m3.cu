@@ -1,6 +1,10 @@
 // ss_attend for f16 activations and an e4m3 cache.
+#include "ss_kv_attend.cuh"
 #include "ss_kv_attend8.cuh"
 
 namespace ss {
-AttendKernel kv_attend_f16_e4m3(int head_dim, int row_tile) { return kv8::pick<__half>(head_dim, row_tile); }
+constexpr int kFew = 16;
+AttendKernel kv_attend_f16_e4m3(int head_dim, int row_tile) {
+  return head_dim <= 128 && row_tile <= kFew ? kv8::pick<__half>(head_dim, row_tile) : kv::pick<__half, true>(head_dim, row_tile);
+}
 }  // namespace ss

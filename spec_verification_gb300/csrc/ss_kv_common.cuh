@@ -58,7 +58,7 @@ struct AttendParams {
   const float *k_scale, *v_scale;
   float scale_log2;     // scale * log2(e)
   int B, hkv, group, max_blocks, num_pages, page_shift, max_tokens, window, sinks;
-  int rows, slots, q_bufs;  // query rows of a unit, tiles in the ring, query buffers
+  int rows, slots, raw_slots, q_bufs;  // query rows of a unit, tiles in the rings, query buffers
   int tile_shift;           // log2 of a tile's keys
   int unit_cost;            // tiles' worth of time that starting and ending a unit takes
   uint32_t group_mul, group_shift;  // x / group = (umulhi(x, mul) + x) >> shift for x < 2^31
@@ -70,8 +70,9 @@ struct AttendParams {
 // The kernel of a head size, types and row tile, its block size, ring, query buffers and shared memory.
 struct AttendKernel {
   const void* fn;
-  int threads, slots, q_bufs, ctas, tile;  // ctas: per SM; tile: keys of a tile
+  int threads, slots, raw_slots, q_bufs, ctas, tile;  // ctas: per SM; tile: keys of a tile
   size_t smem;
+  bool swizzled;  // how the copies lay tiles out in shared memory
 };
 AttendKernel kv_attend_bf16(int head_dim, int row_tile);       // bf16 activations, bf16 cache
 AttendKernel kv_attend_f16(int head_dim, int row_tile);        // f16, f16
