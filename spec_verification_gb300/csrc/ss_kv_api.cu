@@ -17,7 +17,6 @@ void set_last_error(const char* msg);
 
 namespace {
 
-constexpr int kUnit8 = 128 << 10;
 constexpr uint32_t kSpin = 1u << 22;  // polls of a copy wait before the copy counts as lost
 
 ss_status fail(ss_status s, const char* msg) {
@@ -356,9 +355,7 @@ ss_status ss_attend(const ss_attend_batch* b, const ss_kv_cache* cache) {
   P.slots = k.slots;
   P.raw_slots = k.raw_slots;
   P.q_bufs = k.q_bufs;
-  // About 2 us beside its tiles, which take the longer the more bytes they have: two tiles of 32 KB.
-  // Measured (1, 2, 4 tiles): 64 x 1 rows of 32 KB tiles 101, 95.7, 96.3 us; 96 x 3 rows of 16 KB tiles 89, 82, 76 us.
-  P.unit_cost = std::max(1, (c.cache_dtype == SS_E4M3 ? kUnit8 : 64 << 10) / (2 * k.tile * c.head_dim * (c.cache_dtype == SS_E4M3 ? 1 : 2)));
+  P.unit_cost = k.unit_cost;
   P.tile_shift = k.tile == 64 ? 6 : 7;
   while ((1u << P.group_shift) < (uint32_t)P.group) ++P.group_shift;
   P.group_mul = (uint32_t)(((1ull << 32) * ((1ull << P.group_shift) - P.group)) / P.group + 1);

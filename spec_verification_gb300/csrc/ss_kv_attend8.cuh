@@ -1,20 +1,25 @@
-// ss_attend for 8-bit caches (e4m3): attention of a step's new tokens over the
-// paged key-value cache.  The mathematics, the split of the work and the join
-// of its pieces are those of ss_kv_attend.cuh.
+// ss_attend for 8-bit caches (e4m3) and at most 16 query rows to a unit.  The
+// mathematics, the split of the work and the join of its pieces are those of
+// ss_kv_attend.cuh.
 //
 // What differs: the tensor cores multiply 8-bit keys only with 8-bit queries,
 // and splitting 16-bit queries and weights into several 8-bit terms costs two
 // to three products for every one (above the time of the loads, whose bytes
-// are halved).  Instead keys and values become f16 in registers (exactly) on
-// their way from shared memory to 16 x 8 x 16 warp-wide products, whose operand
-// layout makes that cheap: the bytes of a key may be taken in any order of
+// are halved).  Where few query rows share a key, its conversion to f16 (exact)
+// is best done in registers, on the way from shared memory to 16 x 8 x 16
+// warp-wide products: converting into shared memory writes and reads every key
+// twice more there, which costs more than these products do.  Their operand
+// layout makes it cheap: the bytes of a key may be taken in any order of
 // columns as long as the queries are taken in the same one, and a register of
 // transposed values holds two neighbouring columns of two keys, which one byte
-// permutation each sorts into an even and an odd column.  One warp runs the
-// ring of TMA copies, four compute.  With MT = 16 query rows every warp has all
-// of them and a quarter of a tile's keys, with its own maximum and sum, and the
-// four join at the end of the unit, so that nothing synchronises the warps
-// inside it; with MT = 64 a warp has its own 16 rows and all keys.
+// permutation each sorts into an even and an odd column.
+//
+// One warp runs the ring of TMA copies, four compute.  Each has all query rows
+// and a quarter of a tile's 128 keys, with its own maximum and sum; the four
+// join at the end of the unit, so that nothing synchronises them inside it.
+// Measured: 32 rows x 4 tokens x 4 query heads over up to 32000 tokens 161 us,
+// 4.6 TB/s; what bounds it is the latency of its chains (two warps to a
+// scheduler, 36 % of issue slots, 20 % of the tensor pipe).
 #pragma once
 
 #include <cuda.h>
@@ -32,9 +37,12 @@ namespace kv8 {
 using namespace kv;
 
 constexpr int kTile = 128;        // keys of a tile
+constexpr int kRows = 16;         // query rows of a unit
+constexpr int kWarps = 4;         // computing warps
+constexpr int kThreads = 32 * (kWarps + 1);
 constexpr uint32_t kDrainPolls = 1u << 22;
 constexpr int kMaxSlots = 16;     // tiles of keys or values in the ring
-constexpr int kControl = 2304;    // bytes of the control block, at most
+constexpr int kControl = 2048;    // bytes of the control block, at most
 
 // ------------------------------------------------------------------ instructions
 template <class T>
@@ -92,25 +100,18 @@ __device__ __forceinline__ void bar_warps() {
 }
 
 // ------------------------------------------------------------------ shape of one instantiation
-template <class T, int D, int MT>
+template <class T, int D>
 struct Shape {
   static constexpr bool kScaleQ = std::is_same<T, __nv_bfloat16>::value;
-  static constexpr int kRow = D;                             // bytes of a token
-  static constexpr int kAtom = kRow < 128 ? kRow : 128;      // swizzled run of bytes
-  static constexpr int kRuns = kRow / kAtom;
-  static constexpr int kSlot = kTile * kRow;                 // bytes of a key (or value) tile
-  static constexpr int kCtas = D <= 128 ? 2 : 1;             // CTAs per SM
+  static_assert(D <= 128, "a head is one swizzled run");
+  static constexpr int kSlot = kTile * D;                    // bytes of a key (or value) tile
+  static constexpr int kCtas = 2;                            // CTAs per SM
   static constexpr int kSmem = (228 * 1024 / kCtas - 1024) & ~127;  // an SM's share of shared memory
-  static constexpr int kWarps = 4;                           // computing warps
-  static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kWM = MT / 16, kWK = kWarps / kWM;    // warps along query rows, along keys
-  static constexpr int kKeys = kTile / kWK < 64 ? kTile / kWK : 64;  // keys that a warp takes at a time
+  static constexpr int kKeys = kTile / kWarps;               // keys of a warp
   static constexpr int kKG = kKeys / 16;                     // their 16-key groups
-  static constexpr int kPasses = kTile / (kKeys * kWK);
   static constexpr int kQRow = D * 2 + 16;                   // padded: rows fall into different banks
-  static constexpr bool kQRegs = D <= 128 && MT < 64;        // query fragments stay in registers
   // ring of tiles: as many as the room beside the queries and the control block holds
-  static constexpr int kFit = (kSmem - 1024 - kControl - MT * kQRow) / kSlot;
+  static constexpr int kFit = (kSmem - 1024 - kControl - kRows * kQRow) / kSlot;
   static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
 };
 
@@ -118,11 +119,11 @@ struct Shape {
 struct Control {
   unsigned long long full[kMaxSlots], empty[kMaxSlots];
   int bad[kMaxSlots];   // per tile of keys: its 16-key groups that lie on pages with a bad id
-  long long range_sums[9];
+  long long range_sums[kThreads / 32];
   Range range;
   int last;
-  float ml[8][16][2];
-  float qinv[64];
+  float ml[kWarps][16][2];
+  float qinv[kRows];
 };
 
 static_assert(sizeof(Control) <= kControl, "control block");
@@ -141,8 +142,8 @@ struct Turn {
 };
 
 template <class S>
-constexpr size_t smem_bytes(int MT) {
-  return 1024 + (size_t)S::kSlots * S::kSlot + (size_t)MT * S::kQRow + kControl;
+constexpr size_t smem_bytes() {
+  return 1024 + (size_t)S::kSlots * S::kSlot + (size_t)kRows * S::kQRow + kControl;
 }
 
 // ------------------------------------------------------------------ loads
@@ -157,7 +158,7 @@ __device__ __forceinline__ void expect(unsigned long long* mbar, int bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(mbar)), "r"(bytes) : "memory");
 }
 
-template <class S, int MT>
+template <class S>
 __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CUtensorMap* mv, unsigned char* ring, Control& c,
                           Range k) {
   const int lane = threadIdx.x & 31;
@@ -215,7 +216,7 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
           }
           __syncwarp();
           if (nth == j)
-            tma_load(smem_u32(ring) + turn.slot * S::kSlot + (sub << box_shift) * S::kRow, values ? mv : mk, &c.full[turn.slot], tok, g.h, id);
+            tma_load(smem_u32(ring) + turn.slot * S::kSlot + (sub << box_shift) * (S::kSlot / kTile), values ? mv : mk, &c.full[turn.slot], tok, g.h, id);
           turn.next<S::kSlots>();
           asked = min(asked + 1, S::kSlots);
         }
@@ -233,51 +234,42 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
 }
 
 // ------------------------------------------------------------------ products
-// Byte offset in a tile of byte b of key `key`: copies of 2^box_shift keys, in each of them runs of kAtom bytes of
-// all keys, the 16-byte pieces of a 128-byte line permuted by the line's number (64-byte runs: by its half).
-template <class S>
-__device__ __forceinline__ uint32_t place_of(int key, int b, int box_shift) {
-  const int box = key >> box_shift, in = key & ((1 << box_shift) - 1);
-  const uint32_t off = (box << box_shift) * S::kRow + ((b / S::kAtom) << box_shift) * S::kAtom + in * S::kAtom + b % S::kAtom;
-  return off ^ ((off >> 3) & (S::kAtom == 128 ? 0x70 : 0x30));
+// Byte offset in a tile of byte b of key `key`: its 16-byte pieces are permuted by the number of its 128-byte line (a
+// half line: by its half).
+template <int D>
+__device__ __forceinline__ uint32_t place_of(int key, int b) {
+  const uint32_t off = key * D + b;
+  return off ^ ((off >> 3) & (D == 128 ? 0x70 : 0x30));
 }
 
-template <class S, class T, int D, int MT>
+template <class S, class T, int D>
 __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsigned char* sq, Control& c, Range k) {
   constexpr int kNT = S::kKG * 2;  // 8-key tiles of a warp
   constexpr int kOT = D / 8;       // 8-column tiles of the output
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int wm = warp % S::kWM, wk = warp / S::kWM;
   const int quad = lane & 3, r0 = lane >> 2;
-  const int box_shift = min(P.page_shift, 6);
   const uint32_t ring_u = smem_u32(ring), sq_u = smem_u32(sq);
   Turn turn;
   bool dead = false;
 
-  // This lane's ldmatrix rows: byte `b` (a multiple of 32) of its key of a 16-key group is at group + run of b +
-  // row + ((b % kAtom) ^ x).  Keys: the two 16-byte pieces vary fastest over the matrices; values: the keys do.
+  // This lane's ldmatrix rows: byte `b` (a multiple of 32) of its key is at row + (b ^ x).  Keys: the two 16-byte pieces
+  // vary fastest over the matrices; values: the keys do.
   const int k_key = ((lane >> 4) << 3) + (lane & 7), v_key = (((lane >> 3) & 1) << 3) + (lane & 7);
-  auto permuted = [](int key, int piece) { return (uint32_t)((piece << 4) ^ (S::kAtom == 128 ? (key & 7) << 4 : ((key >> 1) & 3) << 4)); };
+  auto permuted = [](int key, int piece) { return (uint32_t)((piece << 4) ^ (D == 128 ? (key & 7) << 4 : ((key >> 1) & 3) << 4)); };
   const uint32_t k_x = permuted(k_key, (lane >> 3) & 1), v_x = permuted(v_key, lane >> 4);
-  const uint32_t run_bytes = (uint32_t)S::kAtom << box_shift;
-  uint32_t group_at[S::kKG];
-#pragma unroll
-  for (int i = 0; i < S::kKG; ++i) {
-    const int key = wk * S::kKeys + i * 16;
-    group_at[i] = (key >> box_shift << box_shift) * S::kRow + (key & ((1 << box_shift) - 1)) * S::kAtom;
-  }
+  const int in0 = warp * S::kKeys;  // this warp's keys of a tile
 
   Segment g;
   while (next_segment(P, k, g)) {
     const int rows_here = g.live;
 
     // queries into shared memory, rows past the end zero
-    bar_warps<S::kWarps>();
-    for (int i = threadIdx.x; i < MT * (D / 8); i += 32 * S::kWarps) {
+    bar_warps<kWarps>();
+    for (int i = threadIdx.x; i < kRows * (D / 8); i += 32 * kWarps) {
       const int m = i / (D / 8), piece = i % (D / 8);
       uint4 x = make_uint4(0u, 0u, 0u, 0u);
       if (m < rows_here) {
-        const int f = g.mt * MT + m, j = token_of(P, f);
+        const int f = g.mt * kRows + m, j = token_of(P, f);
         x = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + (g.q0 + j) * P.q_stride +
                                             (g.h * P.group + f - j * P.group) * D + piece * 8);
       }
@@ -298,26 +290,24 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
       }
       *reinterpret_cast<uint4*>(sq + m * S::kQRow + piece * 16) = x;
     }
-    bar_warps<S::kWarps>();
+    bar_warps<kWarps>();
 
     // a fragment of 16 query rows and 16 columns, the columns in the order in which the keys' bytes come
     auto q_frag = [&](uint32_t (&a)[4], int ks) {
-      const unsigned char* p = sq + (wm * 16 + r0) * S::kQRow + ks * 32 + quad * 8;
+      const unsigned char* p = sq + r0 * S::kQRow + ks * 32 + quad * 8;
       const uint2 x = *reinterpret_cast<const uint2*>(p), y = *reinterpret_cast<const uint2*>(p + 8 * S::kQRow);
       a[0] = x.x;
       a[1] = y.x;
       a[2] = x.y;
       a[3] = y.y;
     };
-    uint32_t qf[S::kQRegs ? D / 16 : 1][4];
-    if (S::kQRegs) {
+    uint32_t qf[D / 16][4];
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) q_frag(qf[S::kQRegs ? ks : 0], ks);
-    }
+    for (int ks = 0; ks < D / 16; ++ks) q_frag(qf[ks], ks);
     // positions of this thread's two rows; rows past the end see nothing
-    const int m0 = wm * 16 + r0, m1 = m0 + 8;
-    const int p0 = m0 < rows_here ? g.len - g.n + token_of(P, g.mt * MT + m0) : -1;
-    const int p1 = m1 < rows_here ? g.len - g.n + token_of(P, g.mt * MT + m1) : -1;
+    const int m0 = r0, m1 = r0 + 8;
+    const int p0 = m0 < rows_here ? g.len - g.n + token_of(P, g.mt * kRows + m0) : -1;
+    const int p1 = m1 < rows_here ? g.len - g.n + token_of(P, g.mt * kRows + m1) : -1;
     float c0 = P.scale_log2, c1 = P.scale_log2;
     if (P.k_scale) {
       const float s = P.k_scale[g.h];
@@ -353,148 +343,138 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
         const int key = tile + in;
         return key <= p && (P.window <= 0 || key > p - P.window || key < P.sinks) && !((bad >> (in >> 4)) & 1);
       };
-#pragma unroll 1
-      for (int pass = 0; pass < S::kPasses; ++pass) {
-        const int in0 = pass * S::kKeys * S::kWK + wk * S::kKeys;  // this warp's keys
-        const uint32_t skip = pass * S::kKeys * S::kWK * S::kRow;  // a pass is a multiple of 64 keys: whole copies
-        const uint32_t kt = ring_u + keys.slot * S::kSlot + skip + k_key * S::kAtom;
-        const uint32_t vt = ring_u + values.slot * S::kSlot + skip + v_key * S::kAtom;
+      const uint32_t kt = ring_u + keys.slot * S::kSlot + (in0 + k_key) * D;
+      const uint32_t vt = ring_u + values.slot * S::kSlot + (in0 + v_key) * D;
 
-        // scores
-        float s[kNT][4];
+      // scores
+      float s[kNT][4];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+#pragma unroll
+      for (int b0 = 0; b0 < D; b0 += 32) {  // 32 columns of every key
+        const int ks = b0 / 16;
+#pragma unroll
+        for (int gk = 0; gk < S::kKG; ++gk) {
+          uint32_t b[4];
+          ldsm(b, kt + gk * 16 * D + (b0 ^ k_x));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t(&a)[4] = qf[ks + h];
+            mma(s[2 * gk], a, e4m3_f16(b[h]), e4m3_f16(b[h] >> 16));
+            mma(s[2 * gk + 1], a, e4m3_f16(b[2 + h]), e4m3_f16(b[2 + h] >> 16));
+          }
+        }
+      }
+      __syncwarp();
+      if (!held && lane == 0) arrive(&c.empty[keys.slot]);
+      if (part) {
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-#pragma unroll
-        for (int b0 = 0; b0 < S::kRow; b0 += 32) {  // 32 columns of every key
-          const int ks = b0 / 16;
-          uint32_t qa[2][4];
-          if (!S::kQRegs) {
-            q_frag(qa[0], ks);
-            q_frag(qa[1], ks + 1);
+          for (int e = 0; e < 2; ++e) {
+            const int in = in0 + n * 8 + 2 * quad + e;
+            if (!sees(in, p0)) s[n][e] = -INFINITY;
+            if (!sees(in, p1)) s[n][2 + e] = -INFINITY;
           }
-#pragma unroll
-          for (int gk = 0; gk < S::kKG; ++gk) {
-            uint32_t b[4];
-            ldsm(b, kt + group_at[gk] + b0 / S::kAtom * run_bytes + ((b0 % S::kAtom) ^ k_x));
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t(&a)[4] = S::kQRegs ? qf[S::kQRegs ? ks + h : 0] : qa[h];
-              mma(s[2 * gk], a, e4m3_f16(b[h]), e4m3_f16(b[h] >> 16));
-              mma(s[2 * gk + 1], a, e4m3_f16(b[2 + h]), e4m3_f16(b[2 + h] >> 16));
-            }
-          }
-        }
-        __syncwarp();
-        if (!held && pass + 1 == S::kPasses && lane == 0) arrive(&c.empty[keys.slot]);
-        if (part) {
-#pragma unroll
-          for (int n = 0; n < kNT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int in = in0 + n * 8 + 2 * quad + e;
-              if (!sees(in, p0)) s[n][e] = -INFINITY;
-              if (!sees(in, p1)) s[n][2 + e] = -INFINITY;
-            }
-        }
+      }
 
-        // softmax of this warp's keys; m moves only when a score exceeds it by more than 2^8
-        float t0 = s[0][0], t1 = s[0][2];
+      // softmax of this warp's keys; m moves only when a score exceeds it by more than 2^8
+      float t0 = s[0][0], t1 = s[0][2];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        t0 = fmaxf(t0, fmaxf(s[n][0], s[n][1]));
+        t1 = fmaxf(t1, fmaxf(s[n][2], s[n][3]));
+      }
+      t0 *= c0;
+      t1 *= c1;
+      if (__any_sync(0xffffffffu, t0 > mx0 + 8.0f || t1 > mx1 + 8.0f || (mx0 == -INFINITY && t0 > mx0) || (mx1 == -INFINITY && t1 > mx1))) {
+        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
+        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
+        const float n0 = fmaxf(mx0, t0), n1 = fmaxf(mx1, t1);
+        const float a0 = n0 == mx0 ? 1.0f : ex2(mx0 - n0), a1 = n1 == mx1 ? 1.0f : ex2(mx1 - n1);
+        l0 *= a0;
+        l1 *= a1;
+#pragma unroll
+        for (int d = 0; d < kOT; ++d) {
+          o[d][0] *= a0;
+          o[d][1] *= a0;
+          o[d][2] *= a1;
+          o[d][3] *= a1;
+        }
+        mx0 = n0;
+        mx1 = n1;
+      }
+      const float z0 = mx0 == -INFINITY ? 0.0f : mx0, z1 = mx1 == -INFINITY ? 0.0f : mx1;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        s[n][0] = ex2(fmaf(s[n][0], c0, -z0));
+        s[n][1] = ex2(fmaf(s[n][1], c0, -z0));
+        s[n][2] = ex2(fmaf(s[n][2], c1, -z1));
+        s[n][3] = ex2(fmaf(s[n][3], c1, -z1));
+        l0 += s[n][0] + s[n][1];
+        l1 += s[n][2] + s[n][3];
+      }
+
+      // times the values
+      if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&c.full[values.slot], values.parity, P.spin_limit, 0u));
+      bool odd = false;  // a value of a partly visible tile is not finite
+      auto clean = [&](uint32_t& x) {
+        const uint32_t y = finite(x);
+        odd |= y != x;
+        x = y;
+      };
+#pragma unroll
+      for (int gk = 0; gk < S::kKG; ++gk) {
+        // weights are rounded to f16 for the product (half a step, 2^-12 of each, random in sign); their sum is not
+        const uint32_t a[4] = {Pack<__half>::pack(s[2 * gk][0], s[2 * gk][1]), Pack<__half>::pack(s[2 * gk][2], s[2 * gk][3]),
+                               Pack<__half>::pack(s[2 * gk + 1][0], s[2 * gk + 1][1]), Pack<__half>::pack(s[2 * gk + 1][2], s[2 * gk + 1][3])};
+#pragma unroll
+        for (int b0 = 0; b0 < D; b0 += 32) {
+          const int d = b0 / 8;
+          uint32_t b[4];
+          ldsm_t(b, vt + gk * 16 * D + (b0 ^ v_x));
+          // a register holds two neighbouring columns of two keys: even columns to one product, odd to the other
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t even = __byte_perm(b[2 * h], b[2 * h + 1], 0x6420), odds = __byte_perm(b[2 * h], b[2 * h + 1], 0x7531);
+            uint32_t f[4] = {e4m3_f16(even), e4m3_f16(even >> 16), e4m3_f16(odds), e4m3_f16(odds >> 16)};
+            if (part) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) clean(f[e]);
+            }
+            mma(o[d + 2 * h], a, f[0], f[1]);
+            mma(o[d + 2 * h + 1], a, f[2], f[3]);
+          }
+        }
+      }
+      if (part && __any_sync(0xffffffffu, odd)) {
+        // Some value in the tile is not finite and was left out above; rows that see its key take it here, one
+        // key at a time (0 * NaN of a row that does not see it must not happen).
 #pragma unroll
         for (int n = 0; n < kNT; ++n) {
-          t0 = fmaxf(t0, fmaxf(s[n][0], s[n][1]));
-          t1 = fmaxf(t1, fmaxf(s[n][2], s[n][3]));
-        }
-        t0 *= c0;
-        t1 *= c1;
-        if (__any_sync(0xffffffffu, t0 > mx0 + 8.0f || t1 > mx1 + 8.0f || (mx0 == -INFINITY && t0 > mx0) || (mx1 == -INFINITY && t1 > mx1))) {
-          t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
-          t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
-          t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
-          t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
-          const float n0 = fmaxf(mx0, t0), n1 = fmaxf(mx1, t1);
-          const float a0 = n0 == mx0 ? 1.0f : ex2(mx0 - n0), a1 = n1 == mx1 ? 1.0f : ex2(mx1 - n1);
-          l0 *= a0;
-          l1 *= a1;
-#pragma unroll
-          for (int d = 0; d < kOT; ++d) {
-            o[d][0] *= a0;
-            o[d][1] *= a0;
-            o[d][2] *= a1;
-            o[d][3] *= a1;
-          }
-          mx0 = n0;
-          mx1 = n1;
-        }
-        const float z0 = mx0 == -INFINITY ? 0.0f : mx0, z1 = mx1 == -INFINITY ? 0.0f : mx1;
-#pragma unroll
-        for (int n = 0; n < kNT; ++n) {
-          s[n][0] = ex2(fmaf(s[n][0], c0, -z0));
-          s[n][1] = ex2(fmaf(s[n][1], c0, -z0));
-          s[n][2] = ex2(fmaf(s[n][2], c1, -z1));
-          s[n][3] = ex2(fmaf(s[n][3], c1, -z1));
-          l0 += s[n][0] + s[n][1];
-          l1 += s[n][2] + s[n][3];
-        }
-
-        // times the values
-        if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&c.full[values.slot], values.parity, P.spin_limit, 0u));
-        bool odd = false;  // a value of a partly visible tile is not finite
-        auto clean = [&](uint32_t& x) {
-          const uint32_t y = finite(x);
-          odd |= y != x;
-          x = y;
-        };
-#pragma unroll
-        for (int gk = 0; gk < S::kKG; ++gk) {
-          // weights are rounded to f16 for the product (half a step, 2^-12 of each, random in sign); their sum is not
-          const uint32_t a[4] = {Pack<__half>::pack(s[2 * gk][0], s[2 * gk][1]), Pack<__half>::pack(s[2 * gk][2], s[2 * gk][3]),
-                                 Pack<__half>::pack(s[2 * gk + 1][0], s[2 * gk + 1][1]), Pack<__half>::pack(s[2 * gk + 1][2], s[2 * gk + 1][3])};
-#pragma unroll
-          for (int b0 = 0; b0 < S::kRow; b0 += 32) {
-            const int d = b0 / 8;
-            uint32_t b[4];
-            ldsm_t(b, vt + group_at[gk] + b0 / S::kAtom * run_bytes + ((b0 % S::kAtom) ^ v_x));
-            // a register holds two neighbouring columns of two keys: even columns to one product, odd to the other
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t even = __byte_perm(b[2 * h], b[2 * h + 1], 0x6420), odds = __byte_perm(b[2 * h], b[2 * h + 1], 0x7531);
-              uint32_t f[4] = {e4m3_f16(even), e4m3_f16(even >> 16), e4m3_f16(odds), e4m3_f16(odds >> 16)};
-              if (part) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) clean(f[e]);
-              }
-              mma(o[d + 2 * h], a, f[0], f[1]);
-              mma(o[d + 2 * h + 1], a, f[2], f[3]);
-            }
-          }
-        }
-        if (part && __any_sync(0xffffffffu, odd)) {
-          // Some value in the tile is not finite and was left out above; rows that see its key take it here, one
-          // key at a time (0 * NaN of a row that does not see it must not happen).
-#pragma unroll
-          for (int n = 0; n < kNT; ++n) {
 #pragma unroll 1
-            for (int src = 0; src < 8; ++src) {
-              const int from = (lane & ~3) + (src >> 1);
-              const float e0 = __shfl_sync(0xffffffffu, s[n][0], from), e1 = __shfl_sync(0xffffffffu, s[n][1], from);
-              const float e2 = __shfl_sync(0xffffffffu, s[n][2], from), e3 = __shfl_sync(0xffffffffu, s[n][3], from);
-              const float w0 = src & 1 ? e1 : e0, w1 = src & 1 ? e3 : e2;
-              const int in = in0 + n * 8 + src;
-              const bool v0 = sees(in, p0), v1 = sees(in, p1);
+          for (int src = 0; src < 8; ++src) {
+            const int from = (lane & ~3) + (src >> 1);
+            const float e0 = __shfl_sync(0xffffffffu, s[n][0], from), e1 = __shfl_sync(0xffffffffu, s[n][1], from);
+            const float e2 = __shfl_sync(0xffffffffu, s[n][2], from), e3 = __shfl_sync(0xffffffffu, s[n][3], from);
+            const float w0 = src & 1 ? e1 : e0, w1 = src & 1 ? e3 : e2;
+            const int in = in0 + n * 8 + src;
+            const bool v0 = sees(in, p0), v1 = sees(in, p1);
 #pragma unroll
-              for (int d = 0; d < kOT; ++d)
+            for (int d = 0; d < kOT; ++d)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  const int col = (d >> 1) * 16 + 4 * quad + 2 * x + (d & 1);
-                  const float v = __half2float(__ushort_as_half((unsigned short)e4m3_f16(ring[values.slot * S::kSlot + place_of<S>(in, col, box_shift)])));
-                  if (!isfinite(v)) {
-                    if (v0) o[d][x] = fmaf(w0, v, o[d][x]);
-                    if (v1) o[d][2 + x] = fmaf(w1, v, o[d][2 + x]);
-                  }
+              for (int x = 0; x < 2; ++x) {
+                const int col = (d >> 1) * 16 + 4 * quad + 2 * x + (d & 1);
+                const float v = __half2float(__ushort_as_half((unsigned short)e4m3_f16(ring[values.slot * S::kSlot + place_of<D>(in, col)])));
+                if (!isfinite(v)) {
+                  if (v0) o[d][x] = fmaf(w0, v, o[d][x]);
+                  if (v1) o[d][2 + x] = fmaf(w1, v, o[d][2 + x]);
                 }
-            }
+              }
           }
         }
       }
@@ -528,12 +508,12 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
     };
     auto join_warps = [&]() {
 #pragma unroll
-      for (int half = S::kWK / 2; half > 0; half >>= 1) {
+      for (int half = kWarps / 2; half > 0; half >>= 1) {
         // warps [half, 2 half) along the keys hand their piece to warps [0, half)
-        bar_warps<S::kWarps>();
-        const int area = wk % half * S::kWM + wm;  // at most four pieces at a time, each half a tile long
-        float4* at = reinterpret_cast<float4*>(ring + (area >> 1 ? values.slot : keys.slot) * S::kSlot + (area & 1) * (S::kSlot / 2)) + lane;
-        if (wk >= half && wk < 2 * half) {
+        bar_warps<kWarps>();
+        const int area = warp % half;  // at most two pieces at a time
+        float4* at = reinterpret_cast<float4*>(ring + (area ? values.slot : keys.slot) * S::kSlot) + lane;
+        if (warp >= half && warp < 2 * half) {
 #pragma unroll
           for (int d = 0; d < kOT; ++d) at[d * 32] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
           if (quad == 0) {
@@ -543,9 +523,9 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
             c.ml[warp][r0 + 8][1] = l1;
           }
         }
-        bar_warps<S::kWarps>();
-        if (wk < half) {
-          const int other = warp + half * S::kWM;
+        bar_warps<kWarps>();
+        if (warp < half) {
+          const int other = warp + half;
           take(c.ml[other][r0][0], c.ml[other][r0 + 8][0], c.ml[other][r0][1], c.ml[other][r0 + 8][1], at);
         }
       }
@@ -553,7 +533,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
     join_warps();
 
     const bool whole = g.ca == g.cb;
-    if (wk == 0) {
+    if (warp == 0) {
       float f0 = whole ? (l0 == 0.0f ? 0.0f : 1.0f / l0) : 1.0f, f1 = whole ? (l1 == 0.0f ? 0.0f : 1.0f / l1) : 1.0f;
       if (P.v_scale) {
         f0 *= P.v_scale[g.h];
@@ -564,7 +544,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
       for (int x = 0; x < 2; ++x) {
         const int m = x ? m1 : m0;
         if (m >= rows_here) continue;
-        const int f = g.mt * MT + m, j = token_of(P, f), head = g.h * P.group + f - j * P.group;
+        const int f = g.mt * kRows + m, j = token_of(P, f), head = g.h * P.group + f - j * P.group;
         const float r = x ? f1 : f0, l = x ? l1 : l0, mx = x ? mx1 : mx0;
         T* to = static_cast<T*>(P.out) + (g.q0 + j) * P.out_stride + head * D;
 #pragma unroll
@@ -573,7 +553,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
           if (whole)
             *reinterpret_cast<uint2*>(to + d * 8 + quad * 4) = make_uint2(Pack<T>::pack(y.x, y.y), Pack<T>::pack(y.z, y.w));
           else
-            piece_out<D>(P, mine)[(d * 2 + quad) * MT + m] = y;
+            piece_out<D>(P, mine)[(d * 2 + quad) * kRows + m] = y;
         }
         if (quad == 0) {
           if (!whole) piece_ml(P, mine)[m] = make_float2(mx, l);
@@ -589,48 +569,44 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
       arrive(&c.empty[keys.slot]);
       arrive(&c.empty[values.slot]);
     }
-    if (!whole) join_unit<T, Pack<T>, D, 32 * S::kWarps>(P, g, &c.last, bar_warps<S::kWarps>);
+    if (!whole) join_unit<T, Pack<T>, D, 32 * kWarps>(P, g, &c.last, bar_warps<kWarps>);
   }
 }
 
 // ------------------------------------------------------------------ kernel
-template <class T, int D, int MT>
-__global__ void __launch_bounds__((Shape<T, D, MT>::kThreads), (Shape<T, D, MT>::kCtas))
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas))
     attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-  using S = Shape<T, D, MT>;
+  using S = Shape<T, D>;
   static_assert(S::kSlots >= 4, "ring length");
   extern __shared__ unsigned char raw[];
   unsigned char* ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   unsigned char* sq = ring + S::kSlots * S::kSlot;
-  Control& c = *reinterpret_cast<Control*>(sq + MT * S::kQRow);
+  Control& c = *reinterpret_cast<Control*>(sq + kRows * S::kQRow);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(&c.full[i]);
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&c.empty[i])), "r"(S::kWarps) : "memory");
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&c.empty[i])), "r"(kWarps) : "memory");
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == S::kWarps && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &mv : &mk) : "memory");
+  if (warp == kWarps && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &mv : &mk) : "memory");
 
-  find_range<S::kThreads>(P, c.range_sums, &c.range);
+  find_range<kThreads>(P, c.range_sums, &c.range);
   if (c.range.cut.ctas == 0) return;
-  if (warp == S::kWarps) load_warp<S, MT>(P, &mk, &mv, ring, c, c.range);
-  else compute_warps<S, T, D, MT>(P, ring, sq, c, c.range);
+  if (warp == kWarps) load_warp<S>(P, &mk, &mv, ring, c, c.range);
+  else compute_warps<S, T, D>(P, ring, sq, c, c.range);
 }
 
-template <class T, int D, int MT>
-AttendKernel entry() {
-  using S = Shape<T, D, MT>;
-  return {reinterpret_cast<const void*>(&attend_kernel<T, D, MT>), S::kThreads, S::kSlots, 0, 1, S::kCtas, kTile, smem_bytes<S>(MT), true};
-}
 template <class T, int D>
-AttendKernel by_rows(int mt) {
-  return mt == 16 ? entry<T, D, 16>() : mt == 32 ? entry<T, D, 32>() : entry<T, D, 64>();
+AttendKernel entry() {
+  using S = Shape<T, D>;
+  return {reinterpret_cast<const void*>(&attend_kernel<T, D>), kThreads, S::kSlots, 0, 1, S::kCtas, kTile, smem_bytes<S>(), D == 128 ? 4 : 2, true};
 }
 template <class T>
-AttendKernel pick(int d, int mt) {
-  return d == 64 ? by_rows<T, 64>(mt) : d == 128 ? by_rows<T, 128>(mt) : by_rows<T, 256>(mt);
+AttendKernel pick(int d) {
+  return d == 64 ? entry<T, 64>() : entry<T, 128>();
 }
 
 }  // namespace kv8

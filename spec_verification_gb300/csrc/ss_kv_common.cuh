@@ -72,6 +72,7 @@ struct AttendKernel {
   const void* fn;
   int threads, slots, raw_slots, q_bufs, ctas, tile;  // ctas: per SM; tile: keys of a tile
   size_t smem;
+  int unit_cost;  // see ss_kv_work.cuh
   bool swizzled;  // how the copies lay tiles out in shared memory
 };
 AttendKernel kv_attend_bf16(int head_dim, int row_tile);       // bf16 activations, bf16 cache
