@@ -192,7 +192,10 @@ typedef struct {
  * zeros and lse -inf.  Values of tokens that a query does not see never reach
  * its result, whatever they hold.  A row whose cu_new passes max_tokens or
  * decreases is left out (SS_ST_CAPACITY); one whose seq_len is negative or
- * passes its table row gives zeros (SS_ST_BAD_PARAM). */
+ * passes its table row gives zeros (SS_ST_BAD_PARAM).  An infinite value that
+ * a query does see may give NaN in its column.  Every wait inside the kernel
+ * is bounded: should one run out (not expected), the rows concerned report
+ * SS_ST_COPY_TIMEOUT, and the workspace is to be zeroed before its next use. */
 ss_status ss_attend(const ss_attend_batch* batch, const ss_kv_cache* cache);
 
 #ifdef __cplusplus

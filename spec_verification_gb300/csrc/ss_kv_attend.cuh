@@ -839,6 +839,11 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
     ++sg;
     if (!whole) join_unit<T, Out, D, 32 * kSoftmaxWarps>(P, g, &c.last, bar_softmax);
   }
+  if (dead && tid == 0) {  // a wait ran out: no row of the range is to be trusted
+    Range k = c.range;
+    Segment g;
+    while (next_segment(P, k, g)) atomicOr(&P.row_status[g.row], (uint32_t)SS_ST_COPY_TIMEOUT);
+  }
 }
 
 // ------------------------------------------------------------------ kernel
