@@ -6,8 +6,10 @@
 
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 #include <new>
 #include <string>
+#include <vector>
 
 #include "ss_kv_common.cuh"
 
@@ -61,6 +63,31 @@ EncodeTiled encode_tiled() {
     return reinterpret_cast<EncodeTiled>(p);
   }();
   return fn;
+}
+
+// Shared-memory limits of the plans' kernels: set once per device and kernel (and size, for kernels with several).
+cudaError_t configure(int device, const ss::AttendKernel& k) {
+  struct Done {
+    int device;
+    const void* fn;
+    size_t smem;
+  };
+  static std::mutex mu;
+  static std::vector<Done> done;
+  const std::lock_guard<std::mutex> lock(mu);
+  bool pages = false;
+  size_t most = 0;
+  for (const Done& d : done) {
+    if (d.device != device) continue;
+    pages = true;
+    if (d.fn == k.fn) most = std::max(most, d.smem);
+  }
+  cudaError_t e = pages ? cudaSuccess : ss::kv_pages_configure();
+  if (e == cudaSuccess && most < k.smem) {
+    e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
+    if (e == cudaSuccess) done.push_back({device, k.fn, k.smem});
+  }
+  return e;
 }
 
 ss::AttendKernel attend_kernel(const ss_kv_config& c, int row_tile) {
@@ -161,13 +188,12 @@ ss_status ss_kv_plan_create(ss_kv_plan** out, const ss_kv_config* config) {
   const OnDevice on(c.device);
   int sms = 0;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c.device);
-  if (e == cudaSuccess) e = ss::kv_pages_configure();
   // the smallest row tile that holds a row's usual query rows: larger tiles waste products on rows that do not
   // exist, smaller ones read the keys once for each of several tiles
   const int64_t rows = (int64_t)c.max_new * group;
   const int row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   const ss::AttendKernel k = attend_kernel(c, row_tile);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
+  if (e == cudaSuccess) e = configure(c.device, k);
   if (e != cudaSuccess) return cuda_fail(e, "kernel attributes");
   ss_kv_plan* p = new (std::nothrow) ss_kv_plan();
   if (!p) return fail(SS_ERR_ARG, "out of host memory");
@@ -175,7 +201,10 @@ ss_status ss_kv_plan_create(ss_kv_plan** out, const ss_kv_config* config) {
   p->page_shift = __builtin_ctz((unsigned)c.page_size);
   p->sms = sms;
   p->row_tile = row_tile;
-  p->attend_grid = k.ctas * sms;
+  // a CTA for every place that the GPU has, or, for a small plan, for every two tiles there can be (ss_kv_work.cuh)
+  const int64_t units = std::min<int64_t>((int64_t)c.max_tokens * group, c.max_rows + (int64_t)c.max_tokens * group / row_tile) * c.kv_heads;
+  const int64_t line = units * ((int64_t)c.max_blocks * c.page_size / k.tile + 1 + k.unit_cost);
+  p->attend_grid = (int)std::min<int64_t>((int64_t)k.ctas * sms, std::max<int64_t>(1, (line + 1) / 2));
   p->off_part = up256((size_t)3 * p->attend_grid * 4);
   p->off_ml = p->off_part + up256((size_t)2 * p->attend_grid * row_tile * c.head_dim * 4);
   p->ws_bytes = p->off_ml + up256((size_t)2 * p->attend_grid * row_tile * 8);
