@@ -11,6 +11,9 @@
  * "ss_verify", and one per launch: stage 1, stage 2, the residual pass) for
  * profilers that record them.
  *
+ * The calls of a serving step around ss_verify (page bookkeeping, rotary store
+ * and attention over a paged key-value cache) are declared in ss_kv.h.
+ *
  * What is computed (page titles and sections of the source material):
  *  - "SonicSampler: unified tile-aware kernels for LLM sampling and
  *    speculative verification", 3.1 Background: logits processing (grammar
