@@ -175,33 +175,25 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
   while (!dead && next_segment(P, k, g)) {
     const int32_t* table = P.block_table + (long long)g.row * P.max_blocks;
     const int used = (g.len + page_mask) >> P.page_shift;
-    // The page of this lane's copy in the batch from tile i0 on: num_pages, past the cache, where nothing is held
-    // (the copy reads zeros), -1 where the table's id is bad.
-    auto fetch = [&](int i0) {
-      const int i = i0 + nth;
-      int id = P.num_pages;
-      if (i < g.count) {
-        const int block = (tile_of(g.u, g.from + i) * kTile + (sub << box_shift)) >> P.page_shift;
-        if (block < used) {
-          id = __ldg(table + block);
-          if ((unsigned)id >= (unsigned)P.num_pages) id = -1;
-        }
-      }
-      return id;
-    };
+    // Whether this lane's copy in the batch from tile i0 on is of tokens that the row holds, and its page: read a batch
+    // ahead and looked at only then.  Where nothing is held the copy is from past the cache and reads zeros.
+    auto block_of = [&](int i0) { return (tile_of(g.u, g.from + i0 + nth) * kTile + (sub << box_shift)) >> P.page_shift; };
+    auto holds = [&](int i0) { return i0 + nth < g.count && block_of(i0) < used; };
+    auto fetch = [&](int i0) { return holds(i0) ? __ldg(table + block_of(i0)) : P.num_pages; };
     int next = fetch(0);
     for (int i0 = 0; i0 < g.count && !dead; i0 += batch) {
       int id = next;
-      const uint32_t bad_lanes = __ballot_sync(0xffffffffu, id < 0);
-      if (id < 0) {
+      next = fetch(i0 + batch);
+      const bool is_bad = holds(i0) && (unsigned)id >= (unsigned)P.num_pages;
+      const uint32_t bad_lanes = __ballot_sync(0xffffffffu, is_bad);
+      if (is_bad) {
         id = P.num_pages;
         atomicOr(&P.row_status[g.row], (uint32_t)SS_ST_KV_PAGE);
       }
-      next = fetch(i0 + batch);
       const int n = min(batch, g.count - i0);
       for (int j = 0; j < n && !dead; ++j) {
         const int tok = (tile_of(g.u, g.from + i0 + j) * kTile + (sub << box_shift)) & page_mask;
-#pragma unroll
+#pragma unroll 1
         for (int values = 0; values < 2; ++values) {
           dead = !__all_sync(0xffffffffu, mbar_wait(&c.empty[turn.slot], turn.parity ^ 1, P.spin_limit, 0u));
           if (dead) break;

@@ -100,6 +100,7 @@ struct Range {
   Cut cut;
   long long unit, end;
   int row, h, mt, skip;
+  Row w;  // of `row`
 };
 
 // A CTA's part of one unit.
@@ -114,14 +115,14 @@ struct Segment {
 // The next segment of the range; false at its end.
 __device__ __forceinline__ bool next_segment(const AttendParams& P, Range& k, Segment& g) {
   if (k.unit >= k.end) return false;
-  Row w = row_info(P, k.row);
-  while (k.mt >= row_units(P, w)) {  // next key head, next row with work (the line ends before the rows do)
+  while (k.mt >= row_units(P, k.w)) {  // next key head, next row with work (the line ends before the rows do)
     k.mt = 0;
-    if (w.n == 0 || ++k.h == P.hkv) {
+    if (k.w.n == 0 || ++k.h == P.hkv) {
       k.h = 0;
-      w = row_info(P, ++k.row);
+      k.w = row_info(P, ++k.row);
     }
   }
+  const Row& w = k.w;
   g.u = unit_info(P, w, k.mt);
   g.row = k.row;
   g.h = k.h;
@@ -149,11 +150,13 @@ __device__ __forceinline__ void find_range(const AttendParams& P, long long* sum
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (P.B + NT - 1) / NT;
   const int ra = min(P.B, tid * run), rb = min(P.B, ra + run);
-  long long mine = 0;
-  for (int r = ra; r < rb; ++r) {
-    const Row w = row_info(P, r);
+  long long mine = 0, per_head = 0;  // per_head, w: of the first row, mostly the only one
+  Row w = {0, 0, 0, 0};
+  for (int r = rb - 1; r >= ra; --r) {
+    w = row_info(P, r);
     if (w.status && blockIdx.x == 0) atomicOr(&P.row_status[r], w.status);
-    mine += row_length(P, w) * P.hkv;
+    per_head = row_length(P, w);
+    mine += per_head * P.hkv;
   }
   long long incl = mine;
 #pragma unroll
@@ -178,17 +181,16 @@ __device__ __forceinline__ void find_range(const AttendParams& P, long long* sum
   cut.longer = (int)(total - cut.base * cut.ctas);
   const long long start = cut.start(blockIdx.x);
   if ((int)blockIdx.x < cut.ctas && start >= before && start < before + mine) {
-    long long off = start - before, per_head = 0;
+    long long off = start - before;
     Range k;
     k.cut = cut;
     k.end = cut.start(blockIdx.x + 1);
-    Row w;
-    for (k.row = ra; k.row < rb; ++k.row) {
-      w = row_info(P, k.row);
-      per_head = row_length(P, w);
-      if (off < per_head * P.hkv) break;
+    for (k.row = ra; off >= per_head * P.hkv;) {
       off -= per_head * P.hkv;
+      w = row_info(P, ++k.row);
+      per_head = row_length(P, w);
     }
+    k.w = w;
     k.h = small ? (int)((uint32_t)off / (uint32_t)per_head) : (int)(off / per_head);
     off -= k.h * per_head;
     k.mt = 0;
