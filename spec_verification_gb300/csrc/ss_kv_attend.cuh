@@ -394,7 +394,7 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
       const int n = min(batch, g.count - i0);
       for (int j = 0; j < n && !dead; ++j) {
         const int tok = (tile_of(g.u, g.from + i0 + j) * kTile + (sub << box_shift)) & page_mask;
-#pragma unroll 1
+#pragma unroll(S::kLow ? 1 : 2)
         for (int values = 0; values < 2; ++values) {
           dead = !__all_sync(0xffffffffu, mbar_wait(&empty[turn.slot], turn.parity ^ 1, P.spin_limit, 0u));
           if (dead) break;
