@@ -382,6 +382,114 @@ def test_attend(new, length, hq, hkv, dim, kind, cache, layout, page, window, si
     assert torch.equal(first.view(torch.int16), b.out.view(torch.int16))
 
 
+ATTEND_8BIT = [
+    # the 8-bit kernels by query rows and columns: one buffer of 128 query rows, copies of 64, all columns at once
+    ([9, 4], [700, 130], 16, 2, 128, "bf16", "e4m3", "hnd", 16),
+    ([8, 1, 3], [500, 64, 65], 8, 1, 128, "f16", "e4m3", "nhd", 128),
+    ([40, 30], [300, 30], 8, 2, 128, "bf16", "e4m3", "hnd", 32),
+    ([8, 5], [900, 77], 16, 2, 64, "bf16", "e4m3", "nhd", 64),
+    ([30, 2], [200, 1000], 16, 2, 64, "f16", "e4m3", "hnd", 16),
+    ([2, 1], [333, 2000], 16, 2, 256, "f16", "e4m3", "hnd", 512),
+    ([20, 1], [400, 100], 16, 2, 256, "bf16", "e4m3", "nhd", 16),
+]
+
+
+@pytest.mark.parametrize("new,length,hq,hkv,dim,kind,cache,layout,page", ATTEND_8BIT)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 5)])
+def test_attend_8_bit(new, length, hq, hkv, dim, kind, cache, layout, page, window, sinks):
+    b = Batch(new, length, hq, hkv, dim, kind, cache, layout, page, seed=len(new) + dim)
+    b.run(window, sinks)
+    b.check(window, sinks)
+    assert b.status.tolist() == [0] * len(new)
+
+
+def test_attend_caches_inside_one_tensor_and_strided_output():
+    """Keys and values of a page next to each other, and an output with gaps between its tokens."""
+    kv = _kv()
+    b = Batch([3, 1], [100, 40], 8, 2, 128, "bf16", "bf16", "nhd", 16)
+    both = torch.full((b.pages, 2, 16, 2, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+    both[:, 0], both[:, 1] = b.kc, b.vc
+    wide = torch.full((4, 8 * 128 + 24), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = wide[:, :1024].view(4, 8, 128)
+    kv.ss_attend(b.plan, b.q, both[:, 0], both[:, 1], b.table, _i32(b.length), b.cu, out=out, row_status=b.status, workspace=b.workspace,
+                 scale=b.scale, lse=b.lse)
+    b.out[:4] = out
+    b.check()
+    assert torch.all(wide[:, 1024:] == 7.0)
+
+
+def test_far_pages_of_a_large_cache():
+    """Pages whose offset passes 2^32 elements: stored by ss_rope_store and read by ss_attend there and nowhere else."""
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GB of free device memory")
+    kv = _kv()
+    page, hkv, dim, tokens = 64, 8, 128, 130
+    pages = 2 ** 32 // (page * hkv * dim) + 4
+    kc, vc = (torch.empty(pages, hkv, page, dim, dtype=torch.bfloat16, device="cuda").transpose(1, 2) for _ in range(2))
+    mine = [pages - 1, 3, pages - 2]
+    for p in mine:
+        kc[p], vc[p] = math.nan, math.nan
+    g = torch.Generator(device="cuda").manual_seed(9)
+    q, k, v = (torch.randn(tokens, h, dim, generator=g, device="cuda").bfloat16() for h in (16, hkv, hkv))
+    plan = _plan(1, tokens, page, pages, 3, q_heads=16, kv_heads=hkv, head_dim=dim, max_new=4)
+    positions = torch.arange(tokens, device="cuda", dtype=torch.int32)
+    slots = _i32([mine[t // page] * page + t % page for t in range(tokens)])
+    assert int(slots.max()) * hkv * dim > 2 ** 32
+    inv = torch.tensor(kv.rope_frequencies(dim), device="cuda")
+    turned = torch.empty_like(q)
+    kv.ss_rope_store(plan, q, k, v, kc, vc, inv, positions, slots, q_out=turned)
+    out, status = torch.empty(4, 16, dim, dtype=torch.bfloat16, device="cuda"), _i32([0])
+    workspace = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    kv.ss_attend(plan, turned[-4:], kc, vc, _i32([mine]), _i32([tokens]), _i32([0, 4]), out=out, row_status=status, workspace=workspace,
+                 scale=dim ** -0.5)
+    torch.cuda.synchronize()
+    held_k = torch.stack([kc[mine[t // page], t % page] for t in range(tokens)])
+    held_v = torch.stack([vc[mine[t // page], t % page] for t in range(tokens)])
+    assert torch.equal(held_v, v)
+    want = ref.rope(k, None, positions, inv, False)
+    assert torch.all((held_k.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -16)
+    want, _, weighted, _, _ = ref.attend(turned[-4:].double(), held_k.double(), held_v.double(), tokens - 4, dim ** -0.5)
+    assert torch.all((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -16) * weighted + 2.0 ** -20)
+    assert status.tolist() == [0]
+
+
+def test_guard_bands_around_what_is_written():
+    """Outputs, log-sum-exps, workspace, slots, positions and tables sit between bands that must not change."""
+    kv = _kv()
+    guard = 4096
+
+    def banded(shape, dtype, fill=0):
+        n = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+        raw = torch.full((n + 2 * guard,), 0xA5, dtype=torch.uint8, device="cuda")
+        t = raw[guard:guard + n].view(dtype).view(shape)
+        t.fill_(fill)
+        bands.append((raw, n))
+        return t
+
+    bands = []
+    b = Batch([5, 1, 9, 1], [700, 3, 9, 2500], 12, 2, 64, "f16", "f16", "hnd", 16)
+    b.out, b.lse, b.status = banded((16, 12, 64), torch.float16), banded((16, 12), torch.float32), banded((4,), torch.int32)
+    b.workspace = banded((b.plan.workspace_bytes,), torch.uint8)
+    for window in (0, 33):
+        b.run(window, 2)
+    plan = _plan(3, 40, 16, 60, 5)
+    table, slots, positions = banded((3, 5), torch.int32, -1), banded((40,), torch.int32), banded((40,), torch.int32)
+    seq, status, kv_len = banded((3,), torch.int32), banded((3,), torch.int32), banded((3,), torch.int32)
+    free, count = banded((60,), torch.int32), banded((1,), torch.int32, 60)
+    free.copy_(torch.arange(60))
+    for _ in range(2):
+        kv.ss_kv_append(plan, table, kv_len, free, count, _i32([0, 20, 21, 40]), slots=slots, positions=positions, seq_len=seq, row_status=status)
+        kv.ss_kv_commit(plan, table, kv_len, free, count, seq, counts=_i32([18, 0, 5]), finished=_i32([0, 0, 1]))
+    cache = banded((2, 60, 2, 16, 64), torch.bfloat16)
+    q = torch.randn(40, 4, 64, device="cuda").bfloat16()
+    q_out = banded((40, 4, 64), torch.bfloat16)
+    kv.ss_rope_store(plan, q, q[:, :2].contiguous(), q[:, 2:].contiguous(), cache[0].transpose(1, 2), cache[1].transpose(1, 2),
+                     torch.tensor(kv.rope_frequencies(64), device="cuda"), positions, slots, q_out=q_out)
+    torch.cuda.synchronize()
+    for raw, n in bands:
+        assert torch.all(raw[:guard] == 0xA5) and torch.all(raw[guard + n:] == 0xA5)
+
+
 def test_attend_sharp_scores():
     """Scores of some hundreds: the running maximum moves, weights underflow."""
     b = Batch([3, 1], [900, 70], 8, 2, 128, "bf16", "bf16", "hnd", 16, spread=30.0)
