@@ -757,21 +757,22 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         const float r = (whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f) * v_scale;
         T* to = static_cast<T*>(P.out) + (g.q0 + token) * P.out_stride + head * D;
         float4* part_to = piece_out<D>(P, mine) + row;
+        constexpr int kCols = S::kLow ? 32 : 64;
 #pragma unroll 1
-        for (int d = 0; d < D; d += 32) {
-          uint32_t o[32];
+        for (int d = 0; d < D; d += kCols) {
+          uint32_t o[kCols];
           tmem_load(o, out_at + d);
           auto val = [&](int n) { return __uint_as_float(o[n]); };
           if (!live) continue;
           if (whole) {
 #pragma unroll
-            for (int n = 0; n < 32; n += 8)
+            for (int n = 0; n < kCols; n += 8)
               *reinterpret_cast<uint4*>(to + d + n) =
                   make_uint4(Out::pack(val(n) * r, val(n + 1) * r), Out::pack(val(n + 2) * r, val(n + 3) * r),
                              Out::pack(val(n + 4) * r, val(n + 5) * r), Out::pack(val(n + 6) * r, val(n + 7) * r));
           } else {
 #pragma unroll
-            for (int n = 0; n < 32; n += 4)
+            for (int n = 0; n < kCols; n += 4)
               part_to[(size_t)((d + n) >> 2) * P.rows] = make_float4(val(n) * r, val(n + 1) * r, val(n + 2) * r, val(n + 3) * r);
           }
         }
@@ -880,7 +881,7 @@ __global__ void __launch_bounds__((Shape<T, D, KEYS, LOW>::kThreads), (Shape<T, 
   }
   if (warp == kLoadWarp && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &mv : &mk) : "memory");
   fence_before();
-  find_range<S::kThreads>(P, c.sums, &c.range);  // ends in a barrier
+  find_range<S::kThreads, kProductWarp>(P, c.sums, &c.range);  // ends in a barrier
   fence_after();
   if (c.range.cut.ctas == 0) {
     // no work: straight to the end

@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas))
   }
   if (warp == kWarps && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &mv : &mk) : "memory");
 
-  find_range<kThreads>(P, c.range_sums, &c.range);
+  find_range<kThreads, kWarps>(P, c.range_sums, &c.range);
   if (c.range.cut.ctas == 0) return;
   if (warp == kWarps) load_warp<S>(P, &mk, &mv, ring, c, c.range);
   else compute_warps<S, T, D>(P, ring, sq, c, c.range);

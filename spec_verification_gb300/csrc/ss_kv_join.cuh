@@ -98,17 +98,18 @@ template <class T, class Pack, int D, int NT, class Bar>
 __device__ __forceinline__ void join_unit(const AttendParams& P, const Segment& g, int* flag, Bar bar) {
   const int cta = blockIdx.x, first = g.ca + (cta - g.ca) / kGroup * kGroup;
   const int members = min(kGroup, g.cb - first + 1), groups = (g.cb - g.ca) / kGroup + 1;
-  auto last = [&](uint32_t* counter, int of) {  // counts in; true for the last of `of`, which leaves the counter at zero
-    __threadfence();
+  // Counts in; true for the last of `of`, which leaves the counter at zero.  One thread's fences stand for all: the
+  // barrier orders the others' writes before them, and their reads (from L2) after.
+  auto last = [&](uint32_t* counter, int of) {
     bar();
     if (threadIdx.x == 0) {
+      __threadfence();
       *flag = atomicAdd(counter, 1u) + 1 == (uint32_t)of;
       if (*flag) *counter = 0;
+      __threadfence();
     }
     bar();
-    const bool yes = *flag != 0;
-    if (yes) __threadfence();
-    return yes;
+    return *flag != 0;
   };
   if (!last(P.counters + piece_of(g, first), members)) return;
   if (groups > 1) {

@@ -143,13 +143,14 @@ __device__ __forceinline__ bool next_segment(const AttendParams& P, Range& k, Se
   return true;
 }
 
-// This CTA's range, by all NT threads of the block: every thread sums a run of rows.  `sums` holds NT / 32 values,
+// This CTA's range, by all NT threads of the block: every thread sums a run of rows, but for those of warp kBusy, which
+// come later than the others.  `sums` holds NT / 32 values,
 // `out` gets the range; row status bits of bad rows are set.  cut.ctas == 0: nothing for this CTA.
-template <int NT>
+template <int NT, int kBusy>
 __device__ __forceinline__ void find_range(const AttendParams& P, long long* sums, Range* out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int run = (P.B + NT - 1) / NT;
-  const int ra = min(P.B, tid * run), rb = min(P.B, ra + run);
+  const int run = (P.B + NT - 33) / (NT - 32), nth = warp > kBusy ? tid - 32 : tid;
+  const int ra = min(P.B, nth * run), rb = warp == kBusy ? ra : min(P.B, ra + run);
   long long mine = 0, per_head = 0;  // per_head, w: of the first row, mostly the only one
   Row w = {0, 0, 0, 0};
   for (int r = rb - 1; r >= ra; --r) {
