@@ -557,6 +557,13 @@ __device__ void product_thread(const AttendParams& P, uint32_t sq, uint32_t ring
 }
 
 // ------------------------------------------------------------------ softmax warps
+// A wait ran out: no row of the range is to be trusted.  (Out of line: it is not expected to run.)
+static __device__ __noinline__ void report_range(const AttendParams& P, const Range* range) {
+  Range k = *range;
+  Segment g;
+  while (next_segment(P, k, g)) atomicOr(&P.row_status[g.row], (uint32_t)SS_ST_COPY_TIMEOUT);
+}
+
 template <class S, class T, int D, int KEYS>
 __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned char* ring, Control& c) {
   using E = Elem<typename S::Mul>;
@@ -832,11 +839,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
     ++sg;
     if (!whole) join_unit<T, Out, D, 32 * kSoftmaxWarps>(P, g, &c.last, bar_softmax);
   }
-  if (dead && tid == 0) {  // a wait ran out: no row of the range is to be trusted
-    Range k = c.range;
-    Segment g;
-    while (next_segment(P, k, g)) atomicOr(&P.row_status[g.row], (uint32_t)SS_ST_COPY_TIMEOUT);
-  }
+  if (dead && tid == 0) report_range(P, &c.range);
 }
 
 // ------------------------------------------------------------------ kernel
