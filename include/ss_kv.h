@@ -187,7 +187,8 @@ typedef struct {
  * window, t > p - window or t < sinks.  Query head h reads key head
  * h / (q_heads / kv_heads).  Scores, softmax sums and outputs are fp32,
  * rounded once at the end (the softmax weights are rounded to the cache's
- * 16-bit type, f16 for SS_E4M3, before the product with the values).  A query
+ * 16-bit type, f16 for SS_E4M3, before the product with the values; the sum
+ * that divides is then that of the rounded bf16 weights).  A query
  * that sees no token (a position below 0), or only scores of -inf, gives
  * zeros and lse -inf.  Values of tokens that a query does not see never reach
  * its result, whatever they hold.  A row whose cu_new passes max_tokens or

@@ -207,7 +207,7 @@ ss_status ss_kv_plan_create(ss_kv_plan** out, const ss_kv_config* config) {
   p->attend_grid = (int)std::min<int64_t>((int64_t)k.ctas * sms, std::max<int64_t>(1, (line + 1) / 2));
   p->off_part = up256((size_t)3 * p->attend_grid * 4);
   p->off_ml = p->off_part + up256((size_t)2 * p->attend_grid * row_tile * c.head_dim * 4);
-  p->ws_bytes = p->off_ml + up256((size_t)2 * p->attend_grid * row_tile * 8);
+  p->ws_bytes = p->off_ml + up256((size_t)2 * p->attend_grid * row_tile * 16);
   *out = p;
   return SS_OK;
 }
@@ -378,7 +378,7 @@ ss_status ss_attend(const ss_attend_batch* b, const ss_kv_cache* cache) {
   char* w = static_cast<char*>(b->workspace);
   P.counters = reinterpret_cast<uint32_t*>(w);
   P.part = reinterpret_cast<float*>(w + p->off_part);
-  P.ml = reinterpret_cast<float2*>(w + p->off_ml);
+  P.ml = reinterpret_cast<float4*>(w + p->off_ml);
   P.spin_limit = kSpin;
   P.rows = p->row_tile;
   P.slots = k.slots;

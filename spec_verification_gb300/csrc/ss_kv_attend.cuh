@@ -59,7 +59,7 @@ constexpr int kSoftmaxWarps = 4;                 // warps 0 .. 3: a warp reaches
 constexpr int kLoadWarp = 4, kProductWarp = 5;
 constexpr int kMaxSlots = 16;                    // tiles of keys or values in the ring
 constexpr int kMaxRaw = 8;                       // 8-bit tiles in their ring
-constexpr int kControl = 3200;                   // bytes of the control block, at most
+constexpr int kControl = 4096;                   // bytes of the control block, at most
 constexpr uint32_t kDrainPolls = 1u << 22;
 
 // ------------------------------------------------------------------ types
@@ -239,7 +239,7 @@ struct Control {
   float q_back[2][128];  // per query row, what its f16 values were scaled by, undone
   int last;
   uint32_t tmem;
-  float2 ml[128];      // of the copies of a row
+  float4 ml[128];      // of the copies of a row, as in a piece
 };
 static_assert(sizeof(Control) <= kControl, "control block");
 
@@ -598,7 +598,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
     float scale = P.scale_log2;
     if (S::kLow && P.k_scale) scale *= P.k_scale[g.h];
     if (S::kScaleQ && live) scale *= c.q_back[sg & 1][row];
-    float mx = -INFINITY, l = 0.0f;
+    float mx = -INFINITY, l = 0.0f, exact = 0.0f;  // m, the sum that divides, the sum of the weights
 
     for (int i = 0; i < g.count; ++i, ++it) {
       const int b = it & 1;
@@ -666,6 +666,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
           const float by = grow ? ex2(mx - top) : 1.0f;  // 0 if nothing was seen before
           if (grow) mx = top;
           l *= by;
+          exact *= by;
           if (i > 0) {
             added(it - 1);
 #pragma unroll 1
@@ -680,21 +681,29 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
           }
         }
         const float z = mx == -INFINITY ? 0.0f : mx;
-        // weights are rounded to 16 bits for the product (half a step, 2^-9 or 2^-12 of each, random in sign); their
-        // sum is not
+        // Weights are rounded to 16 bits for the product (half a step, 2^-9 or 2^-12 of each, random in sign).  To bf16
+        // the divisor is the sum of the rounded ones, so that the error of a weight that dominates its row cancels; the
+        // log-sum-exp has the sum before rounding.
+        constexpr bool kTwo = std::is_same<typename S::Mul, __nv_bfloat16>::value;
 #pragma unroll
         for (int at = 0; at < KEYS; at += kChunk) {
           if (KEYS > kChunk) scores(x, at);
           uint32_t w[kChunk / 2];
-          float s0 = 0.0f, s1 = 0.0f;
+          float s0 = 0.0f, s1 = 0.0f, e0 = 0.0f, e1 = 0.0f;
 #pragma unroll
           for (int n = 0; n < kChunk / 2; ++n) {
             const float a = ex2(fmaf(__uint_as_float(x[2 * n]), scale, -z)), e = ex2(fmaf(__uint_as_float(x[2 * n + 1]), scale, -z));
-            s0 += a;
-            s1 += e;
             w[n] = E::pack(a, e);
+            const float2 r = kTwo ? E::unpack(w[n]) : make_float2(a, e);
+            s0 += r.x;
+            s1 += r.y;
+            if (kTwo) {
+              e0 += a;
+              e1 += e;
+            }
           }
           l += s0 + s1;
+          exact += kTwo ? e0 + e1 : s0 + s1;
           tmem_store(lanes + b * kTile + (key0 + at) / 2, w);
         }
         const uint32_t zeros[KEYS / 2] = {};
@@ -754,10 +763,10 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
     const bool whole = g.ca == g.cb;
     const float v_scale = S::kLow && P.v_scale ? P.v_scale[g.h] : 1.0f;
     const int mine = piece_of(g, blockIdx.x), head = g.h * P.group + f - token * P.group;
-    auto write_sums = [&](float m, float sum) {  // of a live row
-      if (!whole) piece_ml(P, mine)[row] = make_float2(m, sum);
+    auto write_sums = [&](float m, float sum, float weights) {  // of a live row
+      if (!whole) piece_ml(P, mine)[row] = make_float4(m, sum, weights, 0.0f);
       else if (P.lse)
-        P.lse[(size_t)(g.q0 + token) * (P.group * P.hkv) + head] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+        P.lse[(size_t)(g.q0 + token) * (P.group * P.hkv) + head] = weights == 0.0f ? -INFINITY : (m + log2f(weights)) * 0.69314718055994531f;
     };
     if constexpr (S::kCopies == 1) {
       if (busy) {
@@ -783,21 +792,26 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
               part_to[(size_t)((d + n) >> 2) * P.rows] = make_float4(val(n) * r, val(n + 1) * r, val(n + 2) * r, val(n + 3) * r);
           }
         }
-        if (live) write_sums(mx, l);
+        if (live) write_sums(mx, l, exact);
       }
     } else {
       // the copies' outputs are added by way of the segment's query buffer, whose products are done: 32 columns of
       // 128 lanes at a time, every thread then adding four columns of a row
       static_assert(128 * D * 2 >= 128 * 32 * 4, "room for 32 columns");
       float4* room = reinterpret_cast<float4*>(sq + (P.q_bufs == 2 && (sg & 1) ? 128 * D * 2 : 0));
-      c.ml[tid] = make_float2(mx, l);
+      c.ml[tid] = make_float4(mx, l, exact, 0.0f);
       bar_softmax();
-      float top = -INFINITY, sum = 0.0f;
+      float top = -INFINITY, sum = 0.0f, weights = 0.0f;
 #pragma unroll
       for (int n = 0; n < S::kCopies; ++n) top = fmaxf(top, c.ml[row + n * S::kLanes].x);
       const float zero = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-      for (int n = 0; n < S::kCopies; ++n) sum += c.ml[row + n * S::kLanes].y * ex2(c.ml[row + n * S::kLanes].x - zero);
+      for (int n = 0; n < S::kCopies; ++n) {
+        const float4 its = c.ml[row + n * S::kLanes];
+        const float share = ex2(its.x - zero);
+        sum += its.y * share;
+        weights += its.z * share;
+      }
       const float by = ex2(mx - zero) * (whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f) * v_scale;
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
@@ -828,7 +842,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         }
         bar_softmax();
       }
-      if (live && copy == 0) write_sums(top, sum);
+      if (live && copy == 0) write_sums(top, sum, weights);
     }
     fence_before();
     __syncwarp();

@@ -548,7 +548,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
             piece_out<D>(P, mine)[(d * 2 + quad) * kRows + m] = y;
         }
         if (quad == 0) {
-          if (!whole) piece_ml(P, mine)[m] = make_float2(mx, l);
+          if (!whole) piece_ml(P, mine)[m] = make_float4(mx, l, l, 0.0f);
           else if (P.lse)
             P.lse[(size_t)(g.q0 + j) * (P.group * P.hkv) + head] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
         }

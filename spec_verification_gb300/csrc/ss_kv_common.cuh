@@ -64,7 +64,7 @@ struct AttendParams {
   uint32_t group_mul, group_shift;  // x / group = (umulhi(x, mul) + x) >> shift for x < 2^31
   uint32_t* counters;   // [3 * grid] arrivals at groups of pieces, then at units (ss_kv_join.cuh)
   float* part;          // [2 * grid][head_dim / 4][row_tile][4] outputs of pieces
-  float2* ml;           // [2 * grid][row_tile] their maximum (of log2) and sum
+  float4* ml;           // [2 * grid][row_tile] their maximum (of log2), the sum that divides and the sum of the weights
   uint32_t spin_limit;
 };
 // The kernel of a head size, types and row tile, its block size, ring, query buffers and shared memory.

@@ -25,8 +25,9 @@ __device__ __forceinline__ float ex2(float x) {
 
 // A CTA has at most two pieces: of the unit that its range ends in (which starts in it), and of the one it begins in.
 __device__ __forceinline__ int piece_of(const Segment& g, int x) { return 2 * x + (x == g.ca ? 1 : 0); }
-// Piece p: (m, l) of row r, and four columns of row r, column 4 * c, at (c * rows + r).
-__device__ __forceinline__ float2* piece_ml(const AttendParams& P, int p) { return P.ml + (size_t)p * P.rows; }
+// Piece p: of row r, (m, the sum that O is divided by, the sum of the weights); four columns of row r, from column 4 * c
+// on, are at (c * rows + r).
+__device__ __forceinline__ float4* piece_ml(const AttendParams& P, int p) { return P.ml + (size_t)p * P.rows; }
 template <int D>
 __device__ __forceinline__ float4* piece_out(const AttendParams& P, int p) {
   return reinterpret_cast<float4*>(P.part + (size_t)p * P.rows * D);
@@ -41,16 +42,16 @@ __device__ __forceinline__ void add_pieces(const AttendParams& P, const Segment&
   const bool live = m < g.live;
   const int f = g.mt * P.rows + m, token = token_of(P, f), head = g.h * P.group + f - token * P.group;
   T* to = static_cast<T*>(P.out) + (g.q0 + token) * P.out_stride + head * D;
-  float top = -INFINITY, sum = 0.0f;
+  float top = -INFINITY, sum = 0.0f, weights = 0.0f;
   if (live) {
     for (int e0 = tid; e0 < items; e0 += NT * kItems) {
       top = -INFINITY;
-      sum = 0.0f;
+      sum = weights = 0.0f;
       float4 o[kItems];
 #pragma unroll
       for (int n = 0; n < kItems; ++n) o[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       for (int x0 = 0; x0 < count; x0 += kPieces) {
-        float2 ml[kPieces];
+        float4 ml[kPieces];
         float4 y[kPieces][kItems];
 #pragma unroll
         for (int x = 0; x < kPieces; ++x) {
@@ -64,6 +65,7 @@ __device__ __forceinline__ void add_pieces(const AttendParams& P, const Segment&
           if (x0 + x >= count) break;
           const float n = fmaxf(top, ml[x].x), zn = n == -INFINITY ? 0.0f : n, a = ex2(top - zn), b = ex2(ml[x].x - zn);
           sum = sum * a + ml[x].y * b;
+          weights = weights * a + ml[x].z * b;
           top = n;
 #pragma unroll
           for (int q = 0; q < kItems; ++q)
@@ -86,9 +88,9 @@ __device__ __forceinline__ void add_pieces(const AttendParams& P, const Segment&
   if (!to_out) bar();  // everyone has read the (m, l) of `first`
   if (live && tid < P.rows) {
     if (!to_out)
-      piece_ml(P, piece_of(g, first))[m] = make_float2(top, sum);
+      piece_ml(P, piece_of(g, first))[m] = make_float4(top, sum, weights, 0.0f);
     else if (P.lse)
-      P.lse[(size_t)(g.q0 + token) * (P.group * P.hkv) + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+      P.lse[(size_t)(g.q0 + token) * (P.group * P.hkv) + head] = weights == 0.0f ? -INFINITY : (top + log2f(weights)) * 0.69314718055994531f;
   }
 }
 
