@@ -17,8 +17,8 @@
 // One warp runs the ring of TMA copies, four compute.  Each has all query rows
 // and a quarter of a tile's 128 keys, with its own maximum and sum; the four
 // join at the end of the unit, so that nothing synchronises them inside it.
-// Measured: 32 rows x 4 tokens x 4 query heads over up to 32000 tokens 161 us,
-// 4.6 TB/s; what bounds it is the latency of its chains (two warps to a
+// Measured: 32 rows x 4 tokens x 4 query heads over up to 32000 tokens 154 us,
+// 4.8 TB/s; what bounds it is the latency of its chains (two warps to a
 // scheduler, 36 % of issue slots, 20 % of the tensor pipe).
 #pragma once
 
