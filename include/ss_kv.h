@@ -91,6 +91,7 @@ typedef struct {
  * too) before the commit. */
 typedef struct {
   int32_t B;             /* rows of this call, 1 .. max_rows */
+  int32_t tokens;        /* ss_kv_append: entries of slots and positions (those past max_tokens are not used) */
   int32_t* block_table;  /* [B, max_blocks]; entries past a row's pages are not read */
   int32_t* kv_len;       /* [B] tokens held */
   int32_t* free_pages;   /* [num_pages], the first *free_count are free; the last of them goes first */
@@ -106,9 +107,9 @@ typedef struct {
  * is not served: its tokens get slot -1 and its seq_len stays kv_len.  kv_len,
  * free_pages and free_count are not changed.
  * cu_new:     [B+1] prefix sums, cu_new[0] = 0.  A row with a negative count,
- *             a negative kv_len or a token past max_tokens is not served
- *             (SS_ST_BAD_PARAM).
- * slots:      [tokens]
+ *             a negative kv_len or a token past max_tokens or pool->tokens is
+ *             not served (SS_ST_BAD_PARAM).
+ * slots:      [tokens] (it and positions may be NULL if pool->tokens is 0)
  * positions:  [tokens] kv_len + index of the token in its row
  * seq_len:    [B] kv_len + n_r (kv_len if not served)
  * row_status: [B] written (0 or bits). */
@@ -164,6 +165,7 @@ ss_status ss_rope_frequencies(double* inv_freq, int32_t rot_dim, double base, do
 /* New tokens' queries and where their keys are. */
 typedef struct {
   int32_t B;
+  int32_t tokens;         /* that q, out and lse hold (those past max_tokens are not used); 0: nothing is done */
   const void* q;          /* [tokens, q_heads, head_dim], heads contiguous; 16-byte aligned */
   int64_t q_stride;       /* between tokens, in elements: a multiple of 8 */
   const int32_t* cu_new;  /* [B+1] prefix sums of the rows' new tokens */
@@ -191,12 +193,13 @@ typedef struct {
  * that divides is then that of the rounded bf16 weights).  A query
  * that sees no token (a position below 0), or only scores of -inf, gives
  * zeros and lse -inf.  Values of tokens that a query does not see never reach
- * its result, whatever they hold.  A row whose cu_new passes max_tokens or
- * decreases is left out (SS_ST_CAPACITY); one whose seq_len is negative or
- * passes its table row gives zeros (SS_ST_BAD_PARAM).  An infinite value that
- * a query does see may give NaN in its column.  Every wait inside the kernel
- * is bounded: should one run out (not expected), the rows concerned report
- * SS_ST_COPY_TIMEOUT, and the workspace is to be zeroed before its next use. */
+ * its result, whatever they hold.  A row whose cu_new passes tokens or
+ * max_tokens, or decreases, is left out (SS_ST_CAPACITY); one whose seq_len is
+ * negative or passes its table row gives zeros (SS_ST_BAD_PARAM).  An infinite
+ * value that a query does see may give NaN in its column.  Every wait inside
+ * the kernel is bounded: should one run out (not expected), the rows concerned
+ * report SS_ST_COPY_TIMEOUT, and the workspace is to be zeroed before its next
+ * use. */
 ss_status ss_attend(const ss_attend_batch* batch, const ss_kv_cache* cache);
 
 #ifdef __cplusplus

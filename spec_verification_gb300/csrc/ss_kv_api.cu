@@ -145,7 +145,7 @@ ss::PagesParams pages_params(const ss_kv_pool* pool) {
   const ss_kv_plan* p = pool->plan;
   ss::PagesParams P = {};
   P.B = pool->B;
-  P.max_tokens = p->c.max_tokens;
+  P.max_tokens = std::min(pool->tokens, p->c.max_tokens);
   P.max_blocks = p->c.max_blocks;
   P.num_pages = p->c.num_pages;
   P.page_shift = p->page_shift;
@@ -220,7 +220,8 @@ ss_status ss_kv_append(const ss_kv_pool* pool, const int32_t* cu_new, int32_t* s
                        uint32_t* row_status) {
   const ss_status s = check_pool(pool);
   if (s != SS_OK) return s;
-  if (!cu_new || !slots || !positions || !seq_len || !row_status)
+  if (pool->tokens < 0) return fail(SS_ERR_ARG, "tokens must be >= 0");
+  if (!cu_new || !seq_len || !row_status || (pool->tokens > 0 && (!slots || !positions)))
     return fail(SS_ERR_ARG, "cu_new, slots, positions, seq_len and row_status are required");
   ss::PagesParams P = pages_params(pool);
   P.cu_new = cu_new;
@@ -333,9 +334,11 @@ ss_status ss_attend(const ss_attend_batch* b, const ss_kv_cache* cache) {
   const ss_kv_plan* p = b->plan;
   const ss_kv_config& c = p->c;
   if (b->B < 1 || b->B > c.max_rows) return fail(SS_ERR_ARG, "B must be in [1, max_rows]");
+  if (b->tokens < 0) return fail(SS_ERR_ARG, "tokens must be >= 0");
+  if (b->tokens == 0) return SS_OK;
   if (!b->q || !b->cu_new || !b->seq_len || !b->block_table || !b->out || !b->row_status)
     return fail(SS_ERR_ARG, "q, cu_new, seq_len, block_table, out and row_status are required");
-  if (!(b->scale > 0.0f) || !std::isfinite(b->scale)) return fail(SS_ERR_ARG, "scale must be positive and finite");
+  if (!(b->scale > 0.0f) || !std::isfinite(b->scale * 1.4426951f)) return fail(SS_ERR_ARG, "scale must be positive and finite");
   if (b->window < 0 || b->sinks < 0) return fail(SS_ERR_ARG, "window and sinks must be >= 0");
   const int64_t wq = (int64_t)c.q_heads * c.head_dim;
   if (b->q_stride < wq || b->out_stride < wq) return fail(SS_ERR_ARG, "a token stride is smaller than its heads");
@@ -372,7 +375,7 @@ ss_status ss_attend(const ss_attend_batch* b, const ss_kv_cache* cache) {
   P.max_blocks = c.max_blocks;
   P.num_pages = c.num_pages;
   P.page_shift = p->page_shift;
-  P.max_tokens = c.max_tokens;
+  P.max_tokens = std::min(b->tokens, c.max_tokens);
   P.window = b->window >= longest ? 0 : b->window;  // a window that reaches every token is none
   P.sinks = P.window ? std::min(b->sinks, longest) : 0;
   char* w = static_cast<char*>(b->workspace);

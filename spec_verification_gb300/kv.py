@@ -34,7 +34,7 @@ class Cache(C.Structure):
 
 
 class Pool(C.Structure):
-    _fields_ = [("B", _i32), ("block_table", _p), ("kv_len", _p), ("free_pages", _p), ("free_count", _p),
+    _fields_ = [("B", _i32), ("tokens", _i32), ("block_table", _p), ("kv_len", _p), ("free_pages", _p), ("free_count", _p),
                 ("stream", _p), ("plan", _p)]
 
 
@@ -46,16 +46,16 @@ class RopeBatch(C.Structure):
 
 
 class AttendBatch(C.Structure):
-    _fields_ = [("B", _i32), ("q", _p), ("q_stride", _i64), ("cu_new", _p), ("seq_len", _p), ("block_table", _p),
+    _fields_ = [("B", _i32), ("tokens", _i32), ("q", _p), ("q_stride", _i64), ("cu_new", _p), ("seq_len", _p), ("block_table", _p),
                 ("scale", _f32), ("window", _i32), ("sinks", _i32), ("out", _p), ("out_stride", _i64), ("lse", _p),
                 ("row_status", _p), ("workspace", _p), ("workspace_bytes", C.c_size_t), ("stream", _p), ("plan", _p)]
 
 
 # The same layouts as native struct formats: packing one takes a fifth of the time that filling a ctypes structure does.
 _CACHE = struct.Struct("@PPqqqPP")
-_POOL = struct.Struct("@iPPPPPP")
+_POOL = struct.Struct("@iiPPPPPP")
 _ROPE = struct.Struct("@iPPPqqqPPfPiifPPPqPP")
-_ATTEND = struct.Struct("@iPqPPPfiiPqPPPNPP")
+_ATTEND = struct.Struct("@iiPqPPPfiiPqPPPNPP")
 assert [_CACHE.size, _POOL.size, _ROPE.size, _ATTEND.size] == [C.sizeof(c) for c in (Cache, Pool, RopeBatch, AttendBatch)]
 
 EXPORTS = ["ss_kv_plan_create", "ss_kv_plan_destroy", "ss_kv_workspace_bytes", "ss_kv_append", "ss_kv_commit",
@@ -172,19 +172,19 @@ def _int(name, t, least):
     return t.data_ptr()
 
 
-def _pool(plan, block_table, kv_len, free_pages, free_count, B, stream):
-    return _POOL.pack(B, _int("block_table", block_table, B * plan.max_blocks), _int("kv_len", kv_len, B),
+def _pool(plan, block_table, kv_len, free_pages, free_count, B, tokens, stream):
+    return _POOL.pack(B, tokens, _int("block_table", block_table, B * plan.max_blocks), _int("kv_len", kv_len, B),
                       _int("free_pages", free_pages, plan.num_pages), _int("free_count", free_count, 1), _stream(stream, plan),
                       plan.handle)
 
 
 def ss_kv_append(plan: Plan, block_table, kv_len, free_pages, free_count, cu_new, *, slots, positions, seq_len,
                  row_status, B=None, stream=None):
-    """ss_kv_append on int32 tensors: pages, slots and positions of each row's new tokens.  slots and positions hold at
-    least as many entries as there are tokens."""
+    """ss_kv_append on int32 tensors: pages, slots and positions of each row's new tokens.  A row with a token past the
+    entries of slots or positions is not served."""
     B = kv_len.shape[0] if B is None else B
-    pool = _pool(plan, block_table, kv_len, free_pages, free_count, B, stream)
-    code = _lib.ss_kv_append(pool, _int("cu_new", cu_new, B + 1), _int("slots", slots, 1), _int("positions", positions, 1),
+    pool = _pool(plan, block_table, kv_len, free_pages, free_count, B, min(slots.numel(), positions.numel()), stream)
+    code = _lib.ss_kv_append(pool, _int("cu_new", cu_new, B + 1), _int("slots", slots, 0), _int("positions", positions, 0),
                              _int("seq_len", seq_len, B), _int("row_status", row_status, B))
     if code:
         native._check(code)
@@ -194,7 +194,7 @@ def ss_kv_commit(plan: Plan, block_table, kv_len, free_pages, free_count, seq_le
                  B=None, stream=None):
     """ss_kv_commit on int32 tensors: lengths move past what is kept, other pages go back to the pool."""
     B = kv_len.shape[0] if B is None else B
-    pool = _pool(plan, block_table, kv_len, free_pages, free_count, B, stream)
+    pool = _pool(plan, block_table, kv_len, free_pages, free_count, B, 0, stream)
     code = _lib.ss_kv_commit(pool, _int("seq_len", seq_len, B), None if counts is None else _int("counts", counts, B), plus,
                              None if finished is None else _int("finished", finished, B))
     if code:
@@ -239,7 +239,7 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, factor: float = 1.0
 def ss_attend(plan: Plan, q, k_cache, v_cache, block_table, seq_len, cu_new, *, out, row_status, workspace, scale,
               window=0, sinks=0, lse=None, k_scale=None, v_scale=None, B=None, stream=None):
     """ss_attend: q, out [tokens, q_heads, head_dim]; caches seen as [pages, page_size, kv_heads, head_dim]; lse float32
-    [tokens, q_heads] or None."""
+    [tokens, q_heads] or None.  A row with a token past those of q is left out."""
     B = seq_len.shape[0] if B is None else B
     cache = _cache(plan, k_cache, v_cache, k_scale, v_scale)
     qs, os = _tokens("q", q, plan.q_heads, plan), _tokens("out", out, plan.q_heads, plan)
@@ -247,7 +247,7 @@ def ss_attend(plan: Plan, q, k_cache, v_cache, block_table, seq_len, cu_new, *, 
         raise _bad("out must have as many tokens as q")
     if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() < q.shape[0] * plan.q_heads):
         raise _bad("lse must be contiguous float32 [tokens, q_heads]")
-    b = _ATTEND.pack(B, q.data_ptr(), qs, _int("cu_new", cu_new, B + 1), _int("seq_len", seq_len, B),
+    b = _ATTEND.pack(B, q.shape[0], q.data_ptr(), qs, _int("cu_new", cu_new, B + 1), _int("seq_len", seq_len, B),
                     _int("block_table", block_table, B * plan.max_blocks), scale, window, sinks, out.data_ptr(), os, _ptr(lse),
                     _int("row_status", row_status, B), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                     _stream(stream, plan), plan.handle)

@@ -615,6 +615,47 @@ def test_attend_long_rows_are_split():
     assert torch.all((got - want).abs() <= tol)
 
 
+# ------------------------------------------------------------------ prefix sums that pass the buffers
+def test_append_leaves_out_rows_past_its_buffers():
+    kv = _kv()
+    plan = _plan(3, 40, 16, 60, 5)
+    for entries in (40, 39, 20, 19, 0):
+        room = _i32([99] * 2 * 64)
+        slots, positions = room[:entries], room[64:64 + min(40, entries + 1)]
+        seq, status = _i32([99] * 3), _i32([99] * 3)
+        table = _i32([[-1] * 5] * 3)
+        kv.ss_kv_append(plan, table, _i32([0, 0, 0]), _i32(list(range(60))), _i32([60]), _i32([0, 20, 21, 40]), slots=slots,
+                        positions=positions, seq_len=seq, row_status=status)
+        torch.cuda.synchronize()
+        served = sum(t <= entries for t in (20, 21, 40))
+        new = [20, 1, 19]
+        assert status.tolist() == [0] * served + [1 << 4] * (3 - served)
+        assert seq.tolist() == new[:served] + [0] * (3 - served)
+        assert torch.all(room[entries:64] == 99) and torch.all(room[64 + entries:] == 99)
+        tokens = sum(new[:served])
+        assert torch.all(slots[:tokens] >= 0) and torch.all(slots[tokens:] == -1)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_attend_leaves_out_rows_past_its_queries(cache):
+    b = Batch([2, 1, 3], [500, 40, 77], 8, 2, 128, "bf16", cache, "hnd", 16)
+    b.q = b.q[:4]
+    b.run()
+    torch.cuda.synchronize()
+    assert b.status.tolist() == [0, 0, 1 << 9]
+    assert torch.all(b.out[3:] == 7.0) and torch.all(b.lse[3:] == 7.0)
+    got, got_lse = b.out[:3].clone(), b.lse[:3].clone()
+    b.q = b.q[:0]  # nothing to do
+    b.run()
+    whole = Batch([2, 1, 3], [500, 40, 77], 8, 2, 128, "bf16", cache, "hnd", 16)
+    whole.run()
+    whole.check()
+    assert torch.equal(b.out[:3], got)
+    # another cut of the work: the same sums in another order, each within the bounds above (scores stay below 30)
+    assert torch.all((got_lse - whole.lse[:3]).abs() <= 2.0 ** -12)
+    assert torch.all((got.double() - whole.out[:3].double()).abs() <= 2.0 ** -7 * whole.out[:3].double().abs() + 2.0 ** -7)
+
+
 # ------------------------------------------------------------------ refusals with a plan
 def test_calls_refuse_wrong_arguments():
     from spec_verification_gb300 import native
