@@ -35,7 +35,8 @@ extern "C" {
 
 /* Element types of activations (SS_BF16, SS_F16) and of the cache (the
  * activations' type, or SS_E4M3: 8-bit values with one fp32 factor per key
- * head; the value held is x / factor, rounded to nearest, at most 448). */
+ * head; the value held is x / factor, rounded to nearest, infinities and all
+ * beyond 448 as 448 with their sign, NaN as NaN). */
 enum { SS_F16 = 2, SS_E4M3 = 3 };
 
 /* Row status bits of these calls, beside those of ss.h. */
@@ -81,7 +82,7 @@ typedef struct {
   void* k;
   void* v;
   int64_t page_stride, token_stride, head_stride;
-  const float* k_scale; /* [kv_heads] factors of an SS_E4M3 cache, > 0; NULL = 1 (NULL for other caches) */
+  const float* k_scale; /* [kv_heads] factors of an SS_E4M3 cache, normal numbers > 0; NULL = 1 (NULL for other caches) */
   const float* v_scale;
 } ss_kv_cache;
 

@@ -78,10 +78,10 @@ __device__ __forceinline__ float2 turn_of(double f, int position) {
 }
 
 // x / s correctly rounded in all but rare cases: a multiplication by 1 / s
-// and one correction of the remainder.
+// and one correction of the remainder; infinities stay what they are.
 __device__ __forceinline__ float divide(float x, float s, float inv) {
   const float y = x * inv;
-  return fmaf(fmaf(-y, s, x), inv, y);
+  return fabsf(y) < INFINITY ? fmaf(fmaf(-y, s, x), inv, y) : y;
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {

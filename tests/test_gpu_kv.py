@@ -260,6 +260,30 @@ def test_rope_in_place_and_special_values():
     assert torch.equal(q[..., 32:][~wild[..., 32:]], before[..., 32:][~wild[..., 32:]])
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("scaled", [False, True])
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_rope_store_8_bits_of_special_values(kind, scaled, dim):
+    """Infinities and values beyond the range are held as 448 with their sign, NaN as NaN; nothing is rotated here."""
+    kv = _kv()
+    plan = _plan(1, 8, 16, 4, 1, q_heads=2, kv_heads=2, head_dim=dim, dtype=kind, cache_dtype="e4m3")
+    wild = torch.tensor([math.inf, -math.inf, math.nan, 60000.0, -60000.0, 0.0, 449.0, 2.0], device="cuda").repeat(dim // 8).to(TYPES[kind])
+    q, k, v = (torch.zeros(8, 2, dim, device="cuda", dtype=TYPES[kind]) for _ in range(3))
+    k[3, 1], v[5, 0] = wild, wild
+    factors = torch.tensor([0.5, 0.25], device="cuda") if scaled else None
+    kc, vc = _cache("e4m3", "hnd", 4, 16, 2, dim, 0.0), _cache("e4m3", "hnd", 4, 16, 2, dim, 0.0)
+    places = torch.arange(8, device="cuda", dtype=torch.int32)
+    kv.ss_rope_store(plan, q, k, v, kc, vc, None, places, places, q_out=q, k_scale=factors, v_scale=factors)
+    torch.cuda.synchronize()
+    for cache, token, head in ((kc, 3, 1), (vc, 5, 0)):
+        got = cache.float()
+        two = 2.0 / (factors[head].item() if scaled else 1.0)
+        want = torch.tensor([448.0, -448.0, math.nan, 448.0, -448.0, 0.0, 448.0, two], device="cuda").repeat(dim // 8)
+        assert torch.equal(torch.nan_to_num(got[0, token, head], nan=-1.0), torch.nan_to_num(want, nan=-1.0))
+        got[0, token, head] = 0.0
+        assert torch.all(got == 0.0)
+
+
 # ------------------------------------------------------------------ attention
 def _held(x, kind, scale):
     """Values as the cache holds them, and in 64 bits."""
