@@ -6,10 +6,9 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdio>
 #include <mutex>
 #include <new>
-#include <string>
-#include <vector>
 
 #include "ss_kv_common.cuh"
 
@@ -26,7 +25,9 @@ ss_status fail(ss_status s, const char* msg) {
   return s;
 }
 ss_status cuda_fail(cudaError_t e, const char* where) {
-  ss::set_last_error((std::string(where) + ": " + cudaGetErrorString(e)).c_str());
+  char msg[256];
+  std::snprintf(msg, sizeof msg, "%s: %s", where, cudaGetErrorString(e));
+  ss::set_last_error(msg);
   return SS_ERR_CUDA;
 }
 bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -73,19 +74,20 @@ cudaError_t configure(int device, const ss::AttendKernel& k) {
     size_t smem;
   };
   static std::mutex mu;
-  static std::vector<Done> done;
+  static Done done[256];  // 16 kernels with at most a few sizes each; past that they are set again each time
+  static int count = 0;
   const std::lock_guard<std::mutex> lock(mu);
   bool pages = false;
   size_t most = 0;
-  for (const Done& d : done) {
-    if (d.device != device) continue;
+  for (const Done* d = done; d != done + count; ++d) {
+    if (d->device != device) continue;
     pages = true;
-    if (d.fn == k.fn) most = std::max(most, d.smem);
+    if (d->fn == k.fn) most = std::max(most, d->smem);
   }
   cudaError_t e = pages ? cudaSuccess : ss::kv_pages_configure();
   if (e == cudaSuccess && most < k.smem) {
     e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
-    if (e == cudaSuccess) done.push_back({device, k.fn, k.smem});
+    if (e == cudaSuccess && count < 256) done[count++] = {device, k.fn, k.smem};
   }
   return e;
 }

@@ -734,3 +734,29 @@ def test_calls_refuse_wrong_arguments():
     kv.ss_attend(**base)  # and the call itself is fine
     kv.ss_rope_store(**rbase)
     torch.cuda.synchronize()
+
+
+def test_calls_refuse_host_tensors():
+    """A host address never reaches a kernel: rope_frequencies' result, for one, is a host array."""
+    from spec_verification_gb300 import native
+    kv = _kv()
+    b = Batch([1], [20], 4, 2, 64, "bf16", "e4m3", "hnd", 16)
+    attend = dict(plan=b.plan, q=b.q, k_cache=b.kc, v_cache=b.vc, block_table=b.table, seq_len=_i32([20]), cu_new=b.cu, out=b.out[:1],
+                  row_status=b.status, workspace=b.workspace, scale=b.scale, lse=b.lse, k_scale=b.ks, v_scale=b.vs)
+    k = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    weight = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    rope = dict(plan=b.plan, q=b.q, k=k, v=k, k_cache=b.kc, v_cache=b.vc, inv_freq=torch.tensor(kv.rope_frequencies(64), device="cuda"),
+                positions=_i32([3]), slots=_i32([-1]), q_out=b.out[:1], q_weight=weight, k_weight=weight, k_scale=b.ks, v_scale=b.vs)
+    pool = dict(plan=b.plan, block_table=b.table, kv_len=_i32([20]), free_pages=_i32([0] * b.pages), free_count=_i32([0]), seq_len=_i32([20]))
+    append = dict(pool, cu_new=_i32([0, 0]), slots=_i32([]), positions=_i32([]), row_status=_i32([0]))
+    commit = dict(pool, counts=_i32([0]), finished=_i32([0]))
+    for call, args in ((kv.ss_attend, attend), (kv.ss_rope_store, rope), (kv.ss_kv_append, append), (kv.ss_kv_commit, commit)):
+        for name, value in args.items():
+            if torch.is_tensor(value):
+                with pytest.raises(native.SSError) as e:
+                    call(**{**args, name: value.cpu()})
+                assert e.value.code == -1 and "host" in str(e.value), name
+        call(**args)
+    with pytest.raises(native.SSError):
+        kv.ss_attend(**{**attend, "scale": 3e38})  # finite, but not in powers of two
+    torch.cuda.synchronize()
