@@ -309,9 +309,11 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
   while (more && !dead) {
     more = next_segment(P, k, g);
     // the segment's place is free once segment sg - 2 is done with; so is a second query buffer, and an only one once
-    // the last scores of segment sg - 1 are there
+    // the last scores of segment sg - 1 are there, or, where its output goes by way of that buffer (copies), all of it
     if (sg >= 2) dead = !__all_sync(0xffffffffu, mbar_wait(&c.seg_empty[sg & 1], ((sg >> 1) & 1) ^ 1, P.spin_limit, 0u));
-    if (sg >= 1 && P.q_bufs == 1 && !dead) dead = !__all_sync(0xffffffffu, mbar_wait(&c.q_free, (sg & 1) ^ 1, P.spin_limit, 0u));
+    if (sg >= 1 && P.q_bufs == 1 && !dead)
+      dead = !__all_sync(0xffffffffu, S::kCopies > 1 ? mbar_wait(&c.seg_empty[(sg - 1) & 1], ((sg - 1) >> 1) & 1, P.spin_limit, 0u)
+                                                     : mbar_wait(&c.q_free, (sg & 1) ^ 1, P.spin_limit, 0u));
     if (dead) break;
     if (!more) g.count = 0;  // the end of the range
     if (lane == 0) c.seg[sg & 1] = g;
@@ -935,21 +937,25 @@ AttendKernel entry(int rows) {
   // 128 columns with 1, 2, 4: 101, 95.7, 96.3; 96 x 3 rows of 64 columns: 89, 82, 76; 8 bits, 32 x 8 rows of 128
   // columns with 2, 4, 8: 135, 112, 96; 64 x 8 rows of 64 columns with 4, 8, 16: 58, 61, 67.
   k.unit_cost = LOW ? (D == 128 ? 8 : 4) : 256 / D;
-  // a second buffer hides the gathering of the next segment's queries; 128 rows of 128 columns leave no room for it
+  // a second buffer hides the gathering of the next segment's queries; 128 rows of 128 columns leave no room for it, and
+  // with 8 bits the rings need it more (16 x 16 rows x 4 query heads of 128 columns: 101 us with it, 98 without)
   const int q_rows = S::kCopies > 1 ? 128 : rows;
-  k.q_bufs = q_rows * D <= 64 * 128 ? 2 : 1;
+  k.q_bufs = q_rows * D <= 64 * 128 && !(LOW && D == 128) ? 2 : 1;
   const int q = k.q_bufs * q_rows * D * 2;
-  // the loads fill the ring of products, or (8 bits) that of the copies: half a tile's bytes for each of its tiles
+  // the loads fill the ring of products, or (8 bits) that of the copies, which has at least three places
   const int room = share - 1024 - q;
-  k.slots = std::min(LOW ? room / (S::kSlot + S::kRaw) : room / S::kSlot, kMaxSlots);
+  k.slots = std::min((room - (LOW ? 3 * S::kRaw : 0)) / S::kSlot, kMaxSlots);
   k.raw_slots = LOW ? std::min((room - k.slots * S::kSlot) / S::kRaw, kMaxRaw) : 0;
   k.smem = 1024 + (size_t)q + (size_t)k.slots * S::kSlot + (size_t)k.raw_slots * S::kRaw;
   return k;
 }
-// With 64 columns few query rows are copied (see above).
+// With 64 columns few query rows are copied (see above); so are at most 32 of 128 columns in 8 bits, where the softmax
+// shares its issue slots with the conversion (32 x 4 rows x 8 query heads: 84 us without copies, 76 with four; 64 rows
+// with two: no gain, 98 us; in 16 bits the larger query buffer costs the ring more: 64 x 1 90 -> 103 us).
 template <class T, bool LOW>
 AttendKernel pick(int d, int rows) {
   if (d == 64) return rows <= 32 ? entry<T, 64, 16, LOW>(rows) : rows == 64 ? entry<T, 64, 32, LOW>(rows) : entry<T, 64, kTile, LOW>(rows);
+  if (LOW && d == 128 && rows <= 32) return entry<T, 128, LOW ? 16 : kTile, LOW>(rows);
   return d == 128 ? entry<T, 128, kTile, LOW>(rows) : entry<T, 256, kTile, LOW>(rows);
 }
 
