@@ -1,7 +1,7 @@
 // How the pieces of a unit that lies in several CTAs become its output.
 //
 // Every CTA that has tiles of the unit writes its piece, (m, l) and O of each
-// query row, to the workspace and counts itself in; the last of kGroup
+// query row, to the workspace and counts itself in; the last of a group of
 // neighbouring CTAs to do so joins their pieces, and the last of the groups
 // joins what the groups left.  Nobody waits.  Which pieces meet is fixed by the
 // split, and they are added in its order, so the result does not depend on who
@@ -15,7 +15,10 @@
 namespace ss {
 namespace kv {
 
-constexpr int kGroup = 8;
+// Pieces of a group, of n: as many as there are groups, so that the fewest are read one after the other; one group where
+// that costs less than meeting twice.  Measured (us, groups of 8 / of about sqrt n): 16 query rows of 128 columns, 6
+// pieces 12.4 / 13.7, about 10 75.4 / 73.5; 64 of 128, 8 pieces 57.5 / 52.4; 64 columns, 13 rows of 128 69.3 / 65.4.
+__device__ __forceinline__ int group_of(int n, bool large) { return n <= (large ? 3 : 8) ? n : (int)ceilf(sqrtf((float)n)); }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -98,8 +101,8 @@ __device__ __forceinline__ void add_pieces(const AttendParams& P, const Segment&
 // `bar`: brings them together.  The output's factors (8-bit values) must be in the pieces already.
 template <class T, class Pack, int D, int NT, class Bar>
 __device__ __forceinline__ void join_unit(const AttendParams& P, const Segment& g, int* flag, Bar bar) {
-  const int cta = blockIdx.x, first = g.ca + (cta - g.ca) / kGroup * kGroup;
-  const int members = min(kGroup, g.cb - first + 1), groups = (g.cb - g.ca) / kGroup + 1;
+  const int cta = blockIdx.x, size = group_of(g.cb - g.ca + 1, P.rows * D > 32 * 128), first = g.ca + (cta - g.ca) / size * size;
+  const int members = min(size, g.cb - first + 1), groups = (g.cb - g.ca) / size + 1;
   // Counts in; true for the last of `of`, which leaves the counter at zero.  One thread's fences stand for all: the
   // barrier orders the others' writes before them, and their reads (from L2) after.
   auto last = [&](uint32_t* counter, int of) {
@@ -118,7 +121,7 @@ __device__ __forceinline__ void join_unit(const AttendParams& P, const Segment& 
     add_pieces<T, Pack, D, NT>(P, g, first, 1, members, false, bar);
     if (!last(P.counters + 2 * gridDim.x + g.ca, groups)) return;
   }
-  add_pieces<T, Pack, D, NT>(P, g, g.ca, groups > 1 ? kGroup : 1, groups > 1 ? groups : members, true, bar);
+  add_pieces<T, Pack, D, NT>(P, g, g.ca, groups > 1 ? size : 1, groups > 1 ? groups : members, true, bar);
 }
 
 }  // namespace kv

@@ -17,7 +17,14 @@
 namespace ss {
 namespace kv {
 
-constexpr int kLeast = 2;  // least length of a part: shorter ones cost more in the join than they save
+// Least length of a part: shorter ones cost more in the join than they save, the more the larger the pieces are.
+// Measured (us) with 2, 4, 8, 12: 16 query rows of 128 columns, 700 tokens 12.4, 13.8, 20.5, 20.6; 32 of 256, 2 x 2237
+// 25.8, 27.6, 27.9, 34; 128 of 64, 1 x 11550 44, 37, 33, 34; 128 of 256, 13 x 9308 75.5, 75.6, 68, 74.  But not longer
+// than a row's units are on average: those want a CTA each (128 query rows, 77 rows of 4 tokens, 308 units of 3: with 8
+// 24.6, with 2 18.2).
+__device__ __forceinline__ int least_part(const AttendParams& P, uint32_t total) {
+  return P.rows == 128 ? (int)min(8u, max(2u, total / (uint32_t)(P.B * P.hkv))) : 2;
+}
 
 struct Row {
   int q0, n, len;
@@ -177,7 +184,8 @@ __device__ __forceinline__ void find_range(const AttendParams& P, long long* sum
   }
   Cut cut;
   const bool small = total < (1ll << 31);
-  cut.ctas = (int)min((long long)gridDim.x, small ? (long long)(((uint32_t)total + kLeast - 1) / kLeast) : total);
+  const int least = least_part(P, (uint32_t)total);  // (of no use to long lines)
+  cut.ctas = (int)min((long long)gridDim.x, small ? (long long)(((uint32_t)total + least - 1) / least) : total);
   cut.base = cut.ctas == 0 ? 0 : small ? (long long)((uint32_t)total / (uint32_t)cut.ctas) : total / cut.ctas;
   cut.longer = (int)(total - cut.base * cut.ctas);
   const long long start = cut.start(blockIdx.x);
