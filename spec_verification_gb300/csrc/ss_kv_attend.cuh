@@ -275,9 +275,17 @@ __device__ __forceinline__ bool any_softmax(bool x) {  // over the softmax warps
 __device__ __forceinline__ bool partly(const AttendParams& P, const Unit& u, int base, int bad) {
   return base + kTile - 1 > u.pos0 || bad != 0 || (P.window > 0 && base <= u.pos1 - P.window && base + kTile > P.sinks);
 }
-// Is a key visible from position p?
-__device__ __forceinline__ bool visible(const AttendParams& P, int key, int p) {
-  return key <= p && (P.window <= 0 || key > p - P.window || key < P.sinks);
+// As bits, the keys of tile `base` that are visible from position p.
+__device__ __forceinline__ uint64_t visible_keys(const AttendParams& P, int base, int p, int bad) {
+  auto below = [&](int key) {  // keys before `key`
+    const int n = key - base;
+    return n <= 0 ? 0ull : n >= kTile ? ~0ull : (1ull << n) - 1;
+  };
+  uint64_t seen = below(p + 1);  // (positions stay below 2^31 - 1)
+  if (P.window > 0) seen &= ~below(p - P.window + 1) | below(P.sinks);
+  for (int n = 0; bad != 0 && n < kTile / 16; ++n)
+    if ((bad >> n) & 1) seen &= ~(0xffffull << (16 * n));
+  return seen;
 }
 
 // ------------------------------------------------------------------ load warp
@@ -613,34 +621,9 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
       fence_after();
       const int bad = (S::kLow ? c.bad_mul : c.bad)[k_slot];
       const bool part = partly(P, g.u, base, bad);
-      bool slow = false;
+      // as bits, the tile's keys that this thread's row sees
+      const uint64_t seen = part ? visible_keys(P, base, p, bad) : ~0ull;
       unsigned char* values = ring + v_turn.slot * S::kSlot;
-      if (part) {
-        // Values of keys that no row sees must not reach the product (0 * infinity, and what was never written may be
-        // anything): they become zeros.  If a value that only some rows see is not finite, the tile goes the slow way.
-        wait(&c.full[v_turn.slot], v_turn.parity);
-        const int in = tid >> 1, key = base + in;
-        const bool good = !((bad >> (in >> 4)) & 1);
-        const bool some = good && key <= g.u.pos1 && (P.window <= 0 || key > g.u.pos0 - P.window || key < P.sinks);
-        const bool all = good && key <= g.u.pos0 && (P.window <= 0 || key > g.u.pos1 - P.window || key < P.sinks);
-        uint32_t wild = 0;
-#pragma unroll
-        for (int r = 0; r < S::kRuns; ++r) {
-          uint4* line = reinterpret_cast<uint4*>(values + r * S::kRun + in * 128) + (tid & 1) * 4;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if (!some) {
-              line[x] = make_uint4(0u, 0u, 0u, 0u);
-            } else if (!all) {
-              const uint4 y = line[x];
-              for (const uint32_t w : {y.x, y.y, y.z, y.w})
-                wild |= (uint32_t)((w & E::kExponent) == E::kExponent) | (uint32_t)((w >> 16 & E::kExponent) == E::kExponent);
-            }
-          }
-        }
-        proxy_fence();
-        slow = any_softmax(wild != 0);
-      }
       if (busy) {
         // this thread's scores, kChunk at a time: one chunk where registers allow, else each is read once for the
         // maximum and once for its weights
@@ -648,10 +631,8 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
           tmem_load(x, lanes + b * kTile + key0 + at);
           if (part) {
 #pragma unroll
-            for (int n = 0; n < kChunk; ++n) {
-              const int in = key0 + at + n;
-              if (!visible(P, base + in, p) || ((bad >> (in >> 4)) & 1)) x[n] = 0xff800000u;
-            }
+            for (int n = 0; n < kChunk; ++n)
+              if (!((uint32_t)(seen >> (key0 + at + (n & 32))) >> (n & 31) & 1)) x[n] = 0xff800000u;
           }
         };
         uint32_t x[kChunk];
@@ -713,7 +694,33 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         for (int n = 1; n < S::kCopies; ++n) tmem_store(lanes + b * kTile + (copy + n) % S::kCopies * (KEYS / 2), zeros);
         store_wait();
       }
+      bool slow = false;
       if (part) {
+        // Values of keys that no row sees must not reach the product (0 * infinity, and what was never written may be
+        // anything): they become zeros.  If a value that only some rows see is not finite, the tile goes the slow way.
+        // (After the weights, which do not wait for the values.)
+        wait(&c.full[v_turn.slot], v_turn.parity);
+        const int in = tid >> 1, key = base + in;
+        const bool good = !((bad >> (in >> 4)) & 1);
+        const bool some = good && key <= g.u.pos1 && (P.window <= 0 || key > max(0, g.u.pos0) - P.window || key < P.sinks);
+        const bool all = good && key <= g.u.pos0 && (P.window <= 0 || key > g.u.pos1 - P.window || key < P.sinks);
+        uint32_t wild = 0;  // bits 15 and 31: an exponent of ones, plus one, carries into the sign's place
+        constexpr uint32_t kOnes = E::kExponent * 0x10001u, kOne = kOnes & ~(kOnes << 1);
+#pragma unroll
+        for (int r = 0; r < S::kRuns; ++r) {
+          uint4* line = reinterpret_cast<uint4*>(values + r * S::kRun + in * 128) + (tid & 1) * 4;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if (!some) {
+              line[x] = make_uint4(0u, 0u, 0u, 0u);
+            } else if (!all) {
+              const uint4 y = line[x];
+              for (const uint32_t w : {y.x, y.y, y.z, y.w}) wild |= (w & kOnes) + kOne;
+            }
+          }
+        }
+        proxy_fence();
+        slow = any_softmax((wild & 0x80008000u) != 0);
         if (slow && busy) {
           // one key at a time, and only for the rows that see it
           if (i > 0) added(it - 1);
@@ -730,7 +737,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
               tmem_load(pair, lanes + b * kTile + (n >> 1));
               const float2 ws = E::unpack(pair[0]);
               const float wt = n & 1 ? ws.y : ws.x;
-              const bool sees = visible(P, base + n, p) && !((bad >> (n >> 4)) & 1) && n / KEYS == copy;
+              const bool sees = (seen >> n & 1) && n / KEYS == copy;
               const unsigned char* line = values + (d >> 6) * S::kRun + n * 128;
 #pragma unroll
               for (int q = 0; q < 4; ++q) {

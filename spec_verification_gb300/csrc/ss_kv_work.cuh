@@ -69,7 +69,7 @@ __device__ __forceinline__ Unit unit_info(const AttendParams& P, const Row& w, i
   u.sink = 0;
   u.first = 0;
   if (P.window > 0) {
-    u.first = max(0, u.pos0 - P.window + 1)  >> P.tile_shift;
+    u.first = max(0, max(0, u.pos0) - P.window + 1) >> P.tile_shift;
     u.sink = min((P.sinks + (1 << P.tile_shift) - 1) >> P.tile_shift, u.first);
   }
   // a unit without a visible key still has one (masked) tile: its output is written
