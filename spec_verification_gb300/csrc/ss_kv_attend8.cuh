@@ -297,7 +297,8 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
     }
   };
   fetch(0, 0);
-  for (int sg = 0;; ++sg) {
+  bool more = true;
+  for (int sg = 0; more; ++sg) {
     // the segment's fields are read from shared memory where registers are better used otherwise
     const Segment& g = c.seg[sg & 1];
     const int rows_here = dead ? 0 : g.live;
@@ -325,7 +326,8 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
       *reinterpret_cast<uint4*>(sq + m * S::kQRow + piece * 16) = x;
     }
     dead = any_warp(dead);  // all go on, or none: they meet at barriers
-    if (dead || g.count == 0) break;
+    more = !dead && g.count > 0;
+    if (!more) break;
     const Unit u = g.u;
     const int count = g.count, from = g.from;
 
