@@ -9,7 +9,8 @@
 //    is cut into equal parts, one per CTA: the split follows from the lengths
 //    on the device, every CTA has the same work whatever the rows' lengths
 //    are, and the launch never changes.  Tile i of a unit that starts at u is
-//    at u + unit_cost + i and belongs to the CTA whose part that lies in.
+//    at u + unit_cost + i and belongs to the CTA whose part that lies in; all
+//    tiles of a short unit belong to the CTA that has the first.
 #pragma once
 
 #include "ss_kv_common.cuh"
@@ -24,6 +25,14 @@ namespace kv {
 // 24.6, with 2 18.2).
 __device__ __forceinline__ int least_part(const AttendParams& P, uint32_t total) {
   return P.rows == 128 ? (int)min(8u, max(2u, total / (uint32_t)(P.B * P.hkv))) : 2;
+}
+
+// Tiles of a unit that is not worth cutting: the join of its pieces would take longer.  Measured (us) with none, 2 and 4
+// of 64 keys and 128 columns: 256 x 1 rows of at most 200 tokens 48.3, 47.6, 44.4; 213 x 8, window 68, 45.5, 45.9, 43.9; 64
+// columns, 256 x 1, with none, 4, 8: 21.8, 20.5, 20.5.  128 keys, with none, 3, 6: one row of 300 13, 12.3, 12.2, but
+// 4 x 1 rows of at most 3000 17, 17, 19.3.
+__device__ __forceinline__ int longest_uncut(const AttendParams& P) {
+  return P.tile_shift == 6 ? min(2 * P.unit_cost, 4) : P.unit_cost;
 }
 
 struct Row {
@@ -121,33 +130,37 @@ struct Segment {
 
 // The next segment of the range; false at its end.
 __device__ __forceinline__ bool next_segment(const AttendParams& P, Range& k, Segment& g) {
-  if (k.unit >= k.end) return false;
-  while (k.mt >= row_units(P, k.w)) {  // next key head, next row with work (the line ends before the rows do)
-    k.mt = 0;
-    if (k.w.n == 0 || ++k.h == P.hkv) {
-      k.h = 0;
-      k.w = row_info(P, ++k.row);
+  while (k.unit < k.end) {
+    while (k.mt >= row_units(P, k.w)) {  // next key head, next row with work (the line ends before the rows do)
+      k.mt = 0;
+      if (k.w.n == 0 || ++k.h == P.hkv) {
+        k.h = 0;
+        k.w = row_info(P, ++k.row);
+      }
     }
+    const Row& w = k.w;
+    g.u = unit_info(P, w, k.mt);
+    const bool uncut = g.u.tiles <= longest_uncut(P);
+    const long long at = k.unit + P.unit_cost;  // of tile 0
+    g.row = k.row;
+    g.h = k.h;
+    g.mt = k.mt;
+    g.q0 = w.q0;
+    g.n = w.n;
+    g.len = w.len;
+    g.from = k.skip;
+    g.count = uncut ? (at < k.end ? g.u.tiles : 0) : (int)min((long long)g.u.tiles, k.end - at) - g.from;
+    if (g.count <= 0) return false;  // the part ends inside the unit's start
+    g.live = min(P.rows, w.n * P.group - k.mt * P.rows);
+    g.ca = g.from != 0 ? k.cut.owner(at) : (int)blockIdx.x;
+    g.cb = g.from + g.count != g.u.tiles ? k.cut.owner(at + g.u.tiles - 1) : (int)blockIdx.x;
+    const bool ours = !uncut || k.skip == 0;
+    k.unit = at + g.u.tiles;
+    k.skip = 0;
+    ++k.mt;
+    if (ours) return true;
   }
-  const Row& w = k.w;
-  g.u = unit_info(P, w, k.mt);
-  g.row = k.row;
-  g.h = k.h;
-  g.mt = k.mt;
-  g.q0 = w.q0;
-  g.n = w.n;
-  g.len = w.len;
-  g.from = k.skip;
-  const long long at = k.unit + P.unit_cost;  // of tile 0
-  g.count = (int)min((long long)g.u.tiles, k.end - at) - g.from;
-  if (g.count <= 0) return false;  // the part ends inside the unit's start
-  g.live = min(P.rows, w.n * P.group - k.mt * P.rows);
-  g.ca = g.from != 0 ? k.cut.owner(at) : (int)blockIdx.x;
-  g.cb = g.from + g.count != g.u.tiles ? k.cut.owner(at + g.u.tiles - 1) : (int)blockIdx.x;
-  k.unit = at + g.u.tiles;
-  k.skip = 0;
-  ++k.mt;
-  return true;
+  return false;
 }
 
 // This CTA's range, by all NT threads of the block: every thread sums a run of rows, but for those of warp kBusy, which
