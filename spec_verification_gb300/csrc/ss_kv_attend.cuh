@@ -59,6 +59,7 @@ constexpr int kSoftmaxWarps = 4;                 // warps 0 .. 3: a warp reaches
 constexpr int kLoadWarp = 4, kProductWarp = 5;
 constexpr int kMaxSlots = 16;                    // tiles of keys or values in the ring
 constexpr int kMaxRaw = 8;                       // 8-bit tiles in their ring
+constexpr int kBadTiles = 16;                    // tiles whose unreadable keys are kept
 constexpr int kControl = 4096;                   // bytes of the control block, at most
 constexpr uint32_t kDrainPolls = 1u << 22;
 
@@ -232,8 +233,9 @@ struct Control {
   Segment seg[2];
   Range range;
   long long sums[10];
-  int bad[kMaxSlots];  // per place of a tile of keys in the ring: its 16-key groups that lie on pages with a bad id
-  int bad_mul[kMaxSlots];  // the same by its place in the ring of the products (8 bits)
+  // Per tile, by its number in the CTA's range modulo kBadTiles: its 16-key groups that lie on pages with a bad id.  Not
+  // by its place in the ring: that is free as soon as the scores are there, before the softmax warps have looked.
+  int bad[kBadTiles];
   int slow[2];         // the tile's values were added by the softmax warps
   unsigned long long raw_full[kMaxRaw], raw_empty[kMaxRaw];  // ring of 8-bit tiles: copies landed; converted
   float q_back[2][128];  // per query row, what its f16 values were scaled by, undone
@@ -242,6 +244,10 @@ struct Control {
   float4 ml[128];      // of the copies of a row, as in a piece
 };
 static_assert(sizeof(Control) <= kControl, "control block");
+// The load warp writes the word of tile t once the place of its keys is free, so with all places of the ring(s) before it
+// given back; among them is that of the values of tile t - (places + 2) / 2 at the latest, which took the weights of
+// every softmax warp.
+static_assert((kMaxSlots + kMaxRaw + 2) / 2 <= kBadTiles && (kBadTiles & (kBadTiles - 1)) == 0, "tiles ahead of the softmax");
 
 // Rows of a query buffer: where there are copies, all 128.
 template <class S>
@@ -309,6 +315,7 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
   const uint32_t q_bytes = q_rows<S>(P) * D * 2;
   Turn turn;
   int asked = 0;                                         // copies in flight or landed, at most `slots`
+  uint32_t it = 0;                                       // tiles so far
   bool dead = false;
   Range k = c.range;
   Segment g;
@@ -413,7 +420,7 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
               int bits = 0;
               for (int s = 0; s < 1 << subs_shift; ++s)
                 if ((bad_lanes >> ((j << subs_shift) + s)) & 1) bits |= groups << (s << (box_shift - 4));
-              c.bad[turn.slot] = bits;  // (8 bits: handed on by the converting warps)
+              c.bad[it++ & (kBadTiles - 1)] = bits;
             }
             expect(&full[turn.slot], kBytes);
           }
@@ -486,7 +493,6 @@ __device__ void convert_warps(const AttendParams& P, const unsigned char* raw, u
         *reinterpret_cast<uint4*>(line + ((c0 ^ (token & 7)) << 4)) = swap ? hi : lo;
         *reinterpret_cast<uint4*>(line + ((c1 ^ (token & 7)) << 4)) = swap ? lo : hi;
       }
-      if (tid == 0 && (i & 1) == 0) c.bad_mul[to.slot] = c.bad[from.slot];
       proxy_fence();
       __syncwarp();
       if (lane == 0) {
@@ -613,13 +619,12 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
     for (int i = 0; i < g.count; ++i, ++it) {
       const int b = it & 1;
       const int base = tile_of(g.u, g.from + i) * kTile;
-      const int k_slot = turn.slot;
       turn.next(P.slots);
       const Turn v_turn = turn;
       turn.next(P.slots);
       wait(&c.s_full[b], (it >> 1) & 1);
       fence_after();
-      const int bad = (S::kLow ? c.bad_mul : c.bad)[k_slot];
+      const int bad = c.bad[it & (kBadTiles - 1)];
       const bool part = partly(P, g.u, base, bad);
       // as bits, the tile's keys that this thread's row sees
       const uint64_t seen = part ? visible_keys(P, base, p, bad) : ~0ull;
