@@ -277,9 +277,10 @@ __device__ __forceinline__ bool any_softmax(bool x) {  // over the softmax warps
   return y != 0;
 }
 
-// Is tile `base` of the unit seen in full by every live row?
-__device__ __forceinline__ bool partly(const AttendParams& P, const Unit& u, int base, int bad) {
-  return base + kTile - 1 > u.pos0 || bad != 0 || (P.window > 0 && base <= u.pos1 - P.window && base + kTile > P.sinks);
+// Does the diagonal or a window's edge cut tile `base` of the unit for some live row?  It follows from the segment alone,
+// so that the softmax warps, which meet at a barrier in such tiles, agree on it even when one of them has lost a wait.
+__device__ __forceinline__ bool partly(const AttendParams& P, const Unit& u, int base) {
+  return base + kTile - 1 > u.pos0 || (P.window > 0 && base <= u.pos1 - P.window && base + kTile > P.sinks);
 }
 // As bits, the keys of tile `base` that are visible from position p.
 __device__ __forceinline__ uint64_t visible_keys(const AttendParams& P, int base, int p, int bad) {
@@ -625,7 +626,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
       wait(&c.s_full[b], (it >> 1) & 1);
       fence_after();
       const int bad = c.bad[it & (kBadTiles - 1)];
-      const bool part = partly(P, g.u, base, bad);
+      const bool cut = partly(P, g.u, base), part = cut || bad != 0;
       // as bits, the tile's keys that this thread's row sees
       const uint64_t seen = part ? visible_keys(P, base, p, bad) : ~0ull;
       unsigned char* values = ring + v_turn.slot * S::kSlot;
@@ -700,15 +701,15 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         store_wait();
       }
       bool slow = false;
-      if (part) {
+      if (cut) {
         // Values of keys that no row sees must not reach the product (0 * infinity, and what was never written may be
-        // anything): they become zeros.  If a value that only some rows see is not finite, the tile goes the slow way.
+        // anything): they become zeros, as those on unreadable pages are already (their copies read past the cache).
+        // If a value that only some rows see is not finite, the tile goes the slow way.
         // (After the weights, which do not wait for the values.)
         wait(&c.full[v_turn.slot], v_turn.parity);
         const int in = tid >> 1, key = base + in;
-        const bool good = !((bad >> (in >> 4)) & 1);
-        const bool some = good && key <= g.u.pos1 && (P.window <= 0 || key > max(0, g.u.pos0) - P.window || key < P.sinks);
-        const bool all = good && key <= g.u.pos0 && (P.window <= 0 || key > g.u.pos1 - P.window || key < P.sinks);
+        const bool some = key <= g.u.pos1 && (P.window <= 0 || key > max(0, g.u.pos0) - P.window || key < P.sinks);
+        const bool all = key <= g.u.pos0 && (P.window <= 0 || key > g.u.pos1 - P.window || key < P.sinks);
         uint32_t wild = 0;  // bits 15 and 31: an exponent of ones, plus one, carries into the sign's place
         constexpr uint32_t kOnes = E::kExponent * 0x10001u, kOne = kOnes & ~(kOnes << 1);
 #pragma unroll
