@@ -97,7 +97,7 @@ class Decoder:
         hq, hkv, d = m.q_heads, m.kv_heads, m.head_dim
         for layer, (k_cache, v_cache) in zip(m.layers, self.caches):
             qkv = m.norm(x) @ layer["qkv"].T
-            q, k, v = (part.view(n, -1, d) for part in qkv.split([hq * d, hkv * d, hkv * d], 1))
+            q, k, v = (part.view(n, heads, d) for part, heads in zip(qkv.split([hq * d, hkv * d, hkv * d], 1), (hq, hkv, hkv)))
             out = torch.empty(n, hq, d, dtype=x.dtype, device=dev)
             kv.ss_rope_store(self.plan, q, k, v, k_cache, v_cache, m.inv_freq, positions, slots, q_out=q, q_weight=layer["q_norm"],
                              k_weight=layer["k_norm"])
