@@ -107,9 +107,17 @@ class Decoder:
             x = m.feed_forward(layer, x)
         return m.norm(x), cu
 
+    @staticmethod
+    def _check(status):
+        bad = status.tolist()
+        if any(bad):
+            raise RuntimeError(f"row status {[hex(b) for b in bad]}")
+
     def prompt(self, prompts: list):
-        """Caches all tokens of the prompts but the last of each, which the first step takes."""
+        """Caches all tokens of the prompts but the last of each, which the first step takes.  Where a prompt does not fit
+        its table row or the free pages, nothing is kept of any."""
         self.forward([p[:-1] for p in prompts])
+        self._check(self.status)  # the next append writes it anew
         kv.ss_kv_commit(self.plan, self.block_table, self.kv_len, self.free_pages, self.free_count, self.seq_len)
 
     def step(self, last: list, drafts: list, finished=None) -> list:
@@ -128,9 +136,7 @@ class Decoder:
         done = None if finished is None else torch.tensor(finished, dtype=torch.int32, device=dev)
         kv.ss_kv_commit(self.plan, self.block_table, self.kv_len, self.free_pages, self.free_count, self.seq_len, counts=self.accepted,
                         plus=1, finished=done)
-        bad = (self.status | self.verify_status).tolist()
-        if any(bad):
-            raise RuntimeError(f"row status {[hex(b) for b in bad]}")
+        self._check(self.status | self.verify_status)
         return [row[:n + 1] for row, n in zip(self.tokens.tolist(), self.accepted.tolist())]
 
 
