@@ -151,7 +151,9 @@ typedef struct {
 /* For every head x of q and k: x * rsqrt(mean(x^2) + eps) * weight where a
  * weight is given, then (a, b) -> (a cos - b sin, b cos + a sin) for its
  * pairs, angle = position * inv_freq taken modulo a turn in 64-bit fixed
- * point (exact for every 32-bit position); everything in fp32, rounded once.
+ * point (exact for every 32-bit position); everything in fp32, rounded once
+ * (the mean of squares that pass its range is taken of scaled values; beside an
+ * infinite value the others of a normed head become 0, and it and its pair NaN).
  * Queries go to q_out, keys and (unchanged) values to the slots. */
 ss_status ss_rope_store(const ss_rope_batch* batch, const ss_kv_cache* cache);
 

@@ -19,6 +19,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ss_kv_common.cuh"
 
@@ -113,7 +114,7 @@ __device__ __forceinline__ void gathered(const Eight& e, bool halves, float (&y)
 // thread holds both values of each of its pairs, so no lane needs another's; cos and sin of its four pairs are in
 // registers, multiplied with the norm's weights, and a head costs two 8-byte loads, its sum of squares over the
 // lanes, 24 multiplications and additions, and two stores.  Ten CTAs of 128 threads an SM keep enough loads in flight
-// (eight: 71 us where ten take 65): 16384 tokens of 48 heads of 128, with norms, 65 us, 6.2 TB/s.
+// (eight: 71 us where ten take 65): 16384 tokens of 48 heads of 128, with norms, 65.7 us, 6.1 TB/s.
 // `Order` says what is known of the pairs at compile time: kNeighbours in every lane, kHalves in every lane (all of
 // the head is rotated), or kMixed ("half" pairs in the first lanes).
 enum Order { kNeighbours, kHalves, kMixed };
@@ -186,17 +187,40 @@ __global__ void __launch_bounds__(kNT, 10) rope_kernel(const RopeParams P) {
 #pragma unroll
       for (int n = 0; n < kAhead; ++n) {
         const int h = h0 + ((b - b0) * kAhead + n) * step;
-        const Eight x = spread<T>(now.lo[n], now.hi[n], halves);
+        Eight x = spread<T>(now.lo[n], now.hi[n], halves);
         float r = 1.0f;
         if (weight != nullptr) {
-          float sum = 0.0f;
+          float sum = 0.0f, eps = P.eps;
+          auto squares = [&]() {
+            sum = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sum = fmaf(x.a[i], x.a[i], fmaf(x.b[i], x.b[i], sum));
+            for (int i = 0; i < 4; ++i) sum = fmaf(x.a[i], x.a[i], fmaf(x.b[i], x.b[i], sum));
+          };
+          squares();
+          if (std::is_same<T, __nv_bfloat16>::value) {
+            // bf16 values whose squares come near the ends of 32 bits, or pass them: once more with the head scaled by a
+            // power of two, which the norm takes out.  (Asked before the sum over the lanes, beside which the vote costs
+            // least: 16384 tokens 64.8 -> 65.7 us.  Leaving such heads out for a second pass: 66.3.)
+            const bool tiny = P.eps < 0x1p-100f;  // nothing else keeps the root from the small end
+            if (__any_sync(0xffffffffu, sum > 0x1p100f || (tiny && sum < 0x1p-100f))) {
+#pragma unroll
+              for (int d = kLanes / 2; d > 0; d >>= 1) sum = fmaxf(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+              const float f = sum > 0x1p100f ? 0x1p-70f : tiny && sum < 0x1p-100f ? 0x1p70f : 1.0f;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                x.a[i] *= f;
+                x.b[i] *= f;
+              }
+              eps = eps * f * f;
+              squares();
+            }
+          }
 #pragma unroll
           for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-          const float m = fmaf(sum, 1.0f / D, P.eps);
+          const float m = fmaf(sum, 1.0f / D, eps);
           r = rsqrtf(m);
-          r = fmaf(r * fmaf(-m * r, r, 1.0f), 0.5f, r);  // a Newton step: to about a rounding
+          // a Newton step: to about a rounding (an infinite value leaves 0 of the others, as in the formula)
+          if (m < INFINITY) r = fmaf(r * fmaf(-m * r, r, 1.0f), 0.5f, r);
         }
         Eight y;
 #pragma unroll

@@ -73,3 +73,47 @@ def test_bad_pages_of_some_of_many_rows(rows, most, longest, hq, hkv, dim, kind,
     if not window:
         assert all(status[r] == 1 << 13 for r in hidden)
     assert int(_counters(b).abs().sum()) == 0
+
+
+# ------------------------------------------------------------------ rotary store
+@pytest.mark.parametrize("tokens", [9, 400, 2600])  # one, two and four tokens to a CTA
+@pytest.mark.parametrize("dim,rot,inter,kind,cache", [(64, 64, False, "bf16", "bf16"), (128, 48, False, "bf16", "e4m3"),
+                                                       (128, 0, False, "bf16", "bf16"), (256, 256, True, "bf16", "bf16"),
+                                                       (128, 128, False, "f16", "f16"), (64, 32, True, "f16", "e4m3")])
+def test_norms_of_heads_whose_squares_pass_32_bits(tokens, dim, rot, inter, kind, cache):
+    """Against 64 bits: squares whose sum overflows or vanishes in 32, an infinite value (the others are 0), NaN."""
+    kv = _kv()
+    g = torch.Generator(device="cuda").manual_seed(tokens + dim)
+    plan = _plan(1, tokens, 16, -(-tokens // 16), 1, q_heads=4, kv_heads=2, head_dim=dim, dtype=kind, cache_dtype=cache)
+    q, k = (torch.randn(tokens, h, dim, generator=g, device="cuda") for h in (4, 2))
+    for x in (q, k):
+        if kind == "bf16":
+            x[0] *= 1e25
+            x[1, 0, 5], x[tokens - 1, 1, dim - 2] = 3e38, -2e20
+            x[2, 1] = x[2, 1].sign() * 3e38
+            x[3] *= 1e-25
+            x[4, 0] *= 1e-37
+        x[5, 1, 3], x[6, 0, dim - 1], x[7, 1, 0] = math.inf, -math.inf, math.nan
+    q, k, v = q.to(TYPES[kind]), k.to(TYPES[kind]), torch.zeros(tokens, 2, dim, device="cuda", dtype=TYPES[kind])
+    qw, kw = (1 + 0.3 * torch.randn(2, dim, generator=g, device="cuda")).to(TYPES[kind])
+    positions, slots = (torch.arange(tokens, device="cuda", dtype=torch.int32) + 1), torch.arange(tokens, device="cuda", dtype=torch.int32)
+    inv = torch.tensor(kv.rope_frequencies(rot), device="cuda") if rot else None
+    kc, vc = (_cache(cache, "hnd", -(-tokens // 16), 16, 2, dim, 0.0) for _ in range(2))
+    out = torch.empty_like(q)
+    for eps in (0.0, 1e-6):
+        kv.ss_rope_store(plan, q, k, v, kc, vc, inv, positions, slots, q_out=out, q_weight=qw, k_weight=kw, eps=eps, interleaved=inter)
+        held = kc[slots.long() // 16, slots.long() % 16].double() if cache != "e4m3" else kc.double().reshape(-1, 2, dim)[:tokens]
+        for got, x, w, low in ((out.double(), q, qw, False), (held, k, kw, cache == "e4m3")):
+            want = ref.rope(x, w, positions, inv, inter, eps=eps)
+            size = want.abs()
+            if rot:
+                a, b = (slice(0, rot, 2), slice(1, rot, 2)) if inter else (slice(0, rot // 2), slice(rot // 2, rot))
+                size[..., a] = size[..., b] = size[..., a] + size[..., b]
+            tol = (16 * 2.0 ** -24 + 2.0 ** -22) * 1.5 * size + 2.0 ** -25
+            if low:
+                want = want.clamp(-448, 448)
+                tol = tol * (1 + U["e4m3"]) + 2.0 ** -10
+            tol = tol + U["e4m3" if low else kind] * want.abs()
+            assert torch.equal(torch.isnan(got), torch.isnan(want))
+            assert torch.all(((got - want).abs() <= tol) | torch.isnan(want)), (eps, (got - want).abs().nan_to_num(0).max())
+            assert torch.all(torch.isfinite(got[0]))
