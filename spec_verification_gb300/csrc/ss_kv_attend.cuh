@@ -4,10 +4,13 @@
 // Mathematics.  For a query q at position p, o = sum_t w_t v_t / sum_t w_t
 // with w_t = 2^(c q.k_t - m), c = scale * log2 e and m any number near the
 // largest exponent: one pass over the keys.  m is the maximum of the first
-// tile that a row sees; when a later tile exceeds it by more than 2^8 the sum
-// and the output so far are scaled down and m moves (weights up to 2^8 lose
-// nothing in 16-bit floating point, and the output, which lives in tensor
-// memory, is hardly ever touched).  Pieces (m, l, O) over disjoint keys join as
+// tile that a row sees, less 7 where weights are f16; when a later tile makes
+// weights 2^8 times as large as that tile's the sum and the output so far are
+// scaled down and m moves (bf16 weights up to 2^8 and f16 weights up to 2^15
+// lose nothing, and the output, which lives in tensor memory, is hardly ever
+// touched).  The 7 are for f16's short lower end: weights below 2^-25 are held
+// as 0, which the divisor does not know of; beside one dominant key that would
+// be 1 % of a row of 400000 faint ones, and is 1 in 10000 at 2^-32.  Pieces (m, l, O) over disjoint keys join as
 // (max m, sum l 2^(m_i - m), sum O 2^(m_i - m)), so the keys of a row can be
 // split anywhere.
 //
@@ -70,6 +73,7 @@ template <>
 struct Elem<__nv_bfloat16> {
   static constexpr uint32_t kFormat = 1;       // of tcgen05.mma's operands
   static constexpr uint32_t kExponent = 0x7f80;
+  static constexpr float kLift = 0.0f;         // of weights, in powers of two (see above)
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -82,6 +86,7 @@ template <>
 struct Elem<__half> {
   static constexpr uint32_t kFormat = 0;
   static constexpr uint32_t kExponent = 0x7c00;
+  static constexpr float kLift = 7.0f;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -649,7 +654,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
 #pragma unroll
           for (int n = 0; n < kChunk; ++n) t[n & 3] = fmaxf(t[n & 3], __uint_as_float(x[n]));
         }
-        const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
+        const float top = fmaf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), scale, -E::kLift);
         const bool grow = live && top > (mx == -INFINITY ? mx : mx + 8.0f);
         if (__any_sync(0xffffffffu, grow)) {
           const float by = grow ? ex2(mx - top) : 1.0f;  // 0 if nothing was seen before
@@ -670,8 +675,8 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
           }
         }
         const float z = mx == -INFINITY ? 0.0f : mx;
-        // Weights are rounded to 16 bits for the product (half a step, 2^-9 or 2^-12 of each, random in sign).  To bf16
-        // the divisor is the sum of the rounded ones, so that the error of a weight that dominates its row cancels; the
+        // Weights are rounded to 16 bits for the product (half a step, 2^-9 or 2^-12 of each, random in sign; f16 weights
+        // below 2^-14, 2^-21 of the first tile's largest, by up to 2^-25).  To bf16 the divisor is the sum of the rounded ones, so that the error of a weight that dominates its row cancels; the
         // log-sum-exp has the sum before rounding.
         constexpr bool kTwo = std::is_same<typename S::Mul, __nv_bfloat16>::value;
 #pragma unroll

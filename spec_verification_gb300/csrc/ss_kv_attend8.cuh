@@ -419,15 +419,16 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
           }
       }
 
-      // softmax of this warp's keys; m moves only when a score exceeds it by more than 2^8
+      // softmax of this warp's keys; m is 7 below the largest score (weights start at 2^7) and moves only when a score
+      // makes weights more than 2^8 times as large
       float t0 = s[0][0], t1 = s[0][2];
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
         t0 = fmaxf(t0, fmaxf(s[n][0], s[n][1]));
         t1 = fmaxf(t1, fmaxf(s[n][2], s[n][3]));
       }
-      t0 *= c0;
-      t1 *= c1;
+      t0 = fmaf(t0, c0, -Elem<__half>::kLift);
+      t1 = fmaf(t1, c1, -Elem<__half>::kLift);
       if (__any_sync(0xffffffffu, t0 > mx0 + 8.0f || t1 > mx1 + 8.0f || (mx0 == -INFINITY && t0 > mx0) || (mx1 == -INFINITY && t1 > mx1))) {
         t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
@@ -468,7 +469,8 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
       };
 #pragma unroll
       for (int gk = 0; gk < S::kKG; ++gk) {
-        // weights are rounded to f16 for the product (half a step, 2^-12 of each, random in sign); their sum is not
+        // weights are rounded to f16 for the product (half a step, 2^-12 of each, random in sign; those below 2^-14, 2^-21
+        // of the largest, by up to 2^-25); their sum is not
         const uint32_t a[4] = {Pack<__half>::pack(s[2 * gk][0], s[2 * gk][1]), Pack<__half>::pack(s[2 * gk][2], s[2 * gk][3]),
                                Pack<__half>::pack(s[2 * gk + 1][0], s[2 * gk + 1][1]), Pack<__half>::pack(s[2 * gk + 1][2], s[2 * gk + 1][3])};
 #pragma unroll

@@ -117,3 +117,74 @@ def test_norms_of_heads_whose_squares_pass_32_bits(tokens, dim, rot, inter, kind
             assert torch.equal(torch.isnan(got), torch.isnan(want))
             assert torch.all(((got - want).abs() <= tol) | torch.isnan(want)), (eps, (got - want).abs().nan_to_num(0).max())
             assert torch.all(torch.isfinite(got[0]))
+
+
+# ------------------------------------------------------------------ attention: weights and scores at the ends of their types
+class Row:
+    """One row over given keys and values [tokens, hkv, dim] in scattered pages, `times` times in a batch."""
+
+    def __init__(self, q, k, v, kind, cache, page=64, k_scale=None, v_scale=None, times=1):
+        kv = _kv()
+        n, hq, self.dim = q.shape
+        tokens, hkv = k.shape[:2]
+        blocks = -(-tokens // page)
+        g = torch.Generator(device="cuda").manual_seed(tokens)
+        ids = torch.randperm(blocks + 2, generator=g, device="cuda")[:blocks]
+        self.q, self.tokens, self.kind, self.product = q.to(TYPES[kind]).contiguous(), tokens, kind, "f16" if cache == "e4m3" else kind
+        self.ks, self.vs, self.scale = k_scale, v_scale, self.dim ** -0.5
+
+        def held(x, scale):
+            y = (x if scale is None else (x / scale[:, None]).clamp(-448, 448)).to(TYPES[cache])
+            full = torch.zeros(blocks * page, hkv, self.dim, dtype=y.dtype, device="cuda").view(torch.uint8)
+            full[:tokens] = y.view(torch.uint8)
+            c = _cache(cache, "nhd", blocks + 2, page, hkv, self.dim, math.nan)
+            c.view(torch.uint8)[ids] = full.view(blocks, page, hkv, -1)
+            return c, y.double() * (1.0 if scale is None else scale.double()[:, None])
+
+        (self.kc, self.k), (self.vc, self.v) = held(k, k_scale), held(v, v_scale)
+        self.plan = kv.Plan(max_rows=times, max_tokens=n * times, max_new=n, q_heads=hq, kv_heads=hkv, head_dim=self.dim, page_size=page,
+                            num_pages=blocks + 2, max_blocks=blocks, dtype=kind, cache_dtype=cache)
+        self.times, self.table, self.status = times, ids.to(torch.int32).repeat(times, 1), _i32([0] * times)
+        self.workspace = torch.zeros(self.plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+
+    def run(self, **kw):
+        """Outputs [times, n, hq, dim] and log-sum-exps."""
+        n, hq, d = self.q.shape
+        q = self.q.repeat(self.times, 1, 1)
+        out, lse = torch.empty_like(q), torch.empty(n * self.times, hq, device="cuda")
+        _kv().ss_attend(self.plan, q, self.kc, self.vc, self.table, _i32([self.tokens] * self.times), _i32(list(range(0, n * self.times + 1, n))),
+                        out=out, row_status=self.status, workspace=self.workspace, scale=self.scale, lse=lse, k_scale=self.ks, v_scale=self.vs, **kw)
+        torch.cuda.synchronize()
+        assert self.status.tolist() == [0] * self.times
+        return out.double().view(self.times, n, hq, d), lse.double().view(self.times, n, hq)
+
+
+# query rows, columns, type, cache: every kernel whose weights are f16
+F16_WEIGHTS = [(4, 64, "f16", "f16"), (64, 64, "f16", "f16"), (16, 128, "f16", "f16"), (128, 128, "f16", "f16"), (8, 256, "f16", "f16"),
+               (4, 64, "bf16", "e4m3"), (16, 128, "f16", "e4m3"), (32, 128, "bf16", "e4m3"), (64, 128, "f16", "e4m3"),
+               (128, 64, "bf16", "e4m3"), (8, 256, "bf16", "e4m3")]
+
+
+@pytest.mark.parametrize("rows,dim,kind,cache", F16_WEIGHTS)
+@pytest.mark.parametrize("times,first", [(1, 0), (80, 0), (80, 128 * 100)])
+def test_faint_keys_beside_dominant_ones(rows, dim, kind, cache, times, first):
+    """60000 keys at about 2^-25.7 of eight (one for every 16 keys of a tile): each weight is held to 2^-11 of itself or to
+    2^-32 of the largest.  80 rows are enough that a CTA has some 60000 keys, one row is split over all CTAs."""
+    g = torch.Generator(device="cuda").manual_seed(rows + dim)
+    tokens, hkv, group = 60000, 4, 4
+    n = rows // group
+    factors = (0.02 + 0.02 * torch.rand(hkv, generator=g, device="cuda")) if cache == "e4m3" else None
+    one = torch.randn(hkv, dim, generator=g, device="cuda")  # all queries of a key head
+    q = one.repeat_interleave(group, 0).expand(n, hkv * group, dim)
+    k = 0.01 * torch.randn(tokens, hkv, dim, generator=g, device="cuda")
+    v = 1 + 0.1 * torch.randn(tokens, hkv, dim, generator=g, device="cuda")
+    k[first:first + 128:16] = one * (17.8 * dim ** 0.5 / one.square().sum(-1, keepdim=True))
+    v[first:first + 128:16] = 0.0
+    row = Row(q, k, v, kind, cache, k_scale=factors, v_scale=factors, times=times)
+    got, got_lse = row.run()
+    want, lse, weighted, plain, size = ref.attend(row.q.double(), row.k, row.v, tokens - n, row.scale)
+    assert 2e-5 < want.min() and want.max() < 1e-3
+    off = (dim * 2.0 ** -23 * size + 2.0 ** -20)[..., None]
+    tol = U[kind] * want.abs() * (1 + 2.0 ** -10) + (U["f16"] + 2 * off) * weighted + 2.0 ** -32 * plain * (1 + 2.0 ** -10) + 2.0 ** -25
+    assert torch.all((got - want).abs() <= tol), ((got - want).abs() / tol).max().item()
+    assert torch.all((got_lse - lse).abs() <= 2 * off[..., 0] + 2.0 ** -22 * lse.abs())
