@@ -49,6 +49,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "ss_kv_join.cuh"
@@ -620,6 +621,9 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
     float scale = P.scale_log2;
     if (S::kLow && P.k_scale) scale *= P.k_scale[g.h];
     if (S::kScaleQ && live) scale *= c.q_back[sg & 1][row];
+    // A product of factors may vanish (a query of zeros comes with 2^-126), and -inf, the score of a hidden key, times 0 is
+    // NaN.  Products of the held values are below 2^33, so with factors this small every score is 0 either way.
+    if (S::kLow) scale = fmaxf(scale, FLT_MIN);
     float mx = -INFINITY, l = 0.0f, exact = 0.0f;  // m, the sum that divides, the sum of the weights
 
     for (int i = 0; i < g.count; ++i, ++it) {

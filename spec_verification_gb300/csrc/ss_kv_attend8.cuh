@@ -30,6 +30,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cfloat>
 #include <type_traits>
 
 #include "ss_kv_attend.cuh"
@@ -357,6 +358,8 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
       c0 *= c.qinv[m0];
       c1 *= c.qinv[m1];
     }
+    c0 = fmaxf(c0, FLT_MIN);  // see softmax_warps
+    c1 = fmaxf(c1, FLT_MIN);
 
     float o[kOT][4];
 #pragma unroll

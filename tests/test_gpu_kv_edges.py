@@ -188,3 +188,25 @@ def test_faint_keys_beside_dominant_ones(rows, dim, kind, cache, times, first):
     tol = U[kind] * want.abs() * (1 + 2.0 ** -10) + (U["f16"] + 2 * off) * weighted + 2.0 ** -32 * plain * (1 + 2.0 ** -10) + 2.0 ** -25
     assert torch.all((got - want).abs() <= tol), ((got - want).abs() / tol).max().item()
     assert torch.all((got_lse - lse).abs() <= 2 * off[..., 0] + 2.0 ** -22 * lse.abs())
+
+
+@pytest.mark.parametrize("rows,dim,kind", [(8, 64, "bf16"), (8, 128, "bf16"), (16, 128, "f16"), (24, 128, "bf16"), (64, 128, "bf16"),
+                                           (128, 64, "bf16"), (64, 64, "f16"), (8, 256, "bf16")])
+@pytest.mark.parametrize("factor", [3e-7, 1e-30, 2.0 ** -126])
+def test_queries_of_zeros_and_small_factors_over_8_bits(rows, dim, kind, factor):
+    """Every score is 0: the mean of the values that a query sees, in tiles that it sees in part too."""
+    g = torch.Generator(device="cuda").manual_seed(rows + dim)
+    tokens, hkv, group = 300, 2, 4
+    n = rows // group
+    q = torch.randn(n, hkv * group, dim, generator=g, device="cuda")
+    q[:, 1::2] = 0.0
+    k, v = torch.randn(2, tokens, hkv, dim, generator=g, device="cuda")
+    ones = torch.ones(hkv, device="cuda")
+    row = Row(q, k * factor, v, kind, "e4m3", k_scale=factor * ones, v_scale=ones)
+    for kw in ({}, {"window": 40, "sinks": 3}):
+        got, got_lse = row.run(**kw)
+        want, lse, weighted, plain, _ = ref.attend(row.q.double(), row.k, row.v, tokens - n, row.scale, **kw)
+        # scores and weights are exact, but for 2^x (2^-20) and what scores of 2^-12 are rounded to
+        tol = U[kind] * want.abs() * (1 + 2.0 ** -10) + (U["f16"] + 2.0 ** -19) * weighted + 2.0 ** -25
+        assert torch.all((got - want).abs() <= tol)
+        assert torch.all((got_lse - lse).abs() <= 2.0 ** -18)
