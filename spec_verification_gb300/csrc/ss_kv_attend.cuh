@@ -286,7 +286,7 @@ __device__ __forceinline__ bool any_softmax(bool x) {  // over the softmax warps
 // Does the diagonal or a window's edge cut tile `base` of the unit for some live row?  It follows from the segment alone,
 // so that the softmax warps, which meet at a barrier in such tiles, agree on it even when one of them has lost a wait.
 __device__ __forceinline__ bool partly(const AttendParams& P, const Unit& u, int base) {
-  return base + kTile - 1 > u.pos0 || (P.window > 0 && base <= u.pos1 - P.window && base + kTile > P.sinks);
+  return base + kTile - 1 > u.pos0 || (P.window > 0 && base <= u.pos1 - P.window && base > P.sinks - kTile);
 }
 // As bits, the keys of tile `base` that are visible from position p.
 __device__ __forceinline__ uint64_t visible_keys(const AttendParams& P, int base, int p, int bad) {

@@ -379,7 +379,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
       const int tile = tile_of(u, from + i) * kTile, bad = c.bad[keys.slot];
       // does any live row not see all of the tile?
       const bool part = tile + kTile - 1 > u.pos0 || bad != 0 ||
-                        (P.window > 0 && tile <= u.pos1 - P.window && tile + kTile > P.sinks);
+                        (P.window > 0 && tile <= u.pos1 - P.window && tile > P.sinks - kTile);
       // is key `in` of the tile visible from position p?
       auto sees = [&](int in, int p) {
         const int key = tile + in;

@@ -79,7 +79,7 @@ __device__ __forceinline__ Unit unit_info(const AttendParams& P, const Row& w, i
   u.first = 0;
   if (P.window > 0) {
     u.first = max(0, max(0, u.pos0) - P.window + 1) >> P.tile_shift;
-    u.sink = min((P.sinks + (1 << P.tile_shift) - 1) >> P.tile_shift, u.first);
+    u.sink = min(((P.sinks - 1) >> P.tile_shift) + 1, u.first);  // (no sum that could pass 2^31)
   }
   // a unit without a visible key still has one (masked) tile: its output is written
   u.tiles = u.pos1 < 0 ? 1 : u.sink + (u.pos1 >> P.tile_shift) - u.first + 1;

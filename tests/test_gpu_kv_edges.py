@@ -210,3 +210,21 @@ def test_queries_of_zeros_and_small_factors_over_8_bits(rows, dim, kind, factor)
         tol = U[kind] * want.abs() * (1 + 2.0 ** -10) + (U["f16"] + 2.0 ** -19) * weighted + 2.0 ** -25
         assert torch.all((got - want).abs() <= tol)
         assert torch.all((got_lse - lse).abs() <= 2.0 ** -18)
+
+
+@pytest.mark.parametrize("cache,page", [("bf16", 16), ("e4m3", 64)])  # tiles of 64 and of 128 keys
+def test_sinks_near_two_to_the_31(cache, page):
+    """The largest table row there is, and as many first tokens visible: a window that hides nothing."""
+    kv = _kv()
+    b = Batch([3, 2], [300, 1000], 8, 2, 64, "bf16", cache, "hnd", page)
+    blocks = (2 ** 31 - 1) // page
+    b.plan = kv.Plan(max_rows=2, max_tokens=5, max_new=3, q_heads=8, kv_heads=2, head_dim=64, page_size=page, num_pages=b.pages,
+                     max_blocks=blocks, dtype="bf16", cache_dtype=cache)
+    b.workspace = torch.zeros(b.plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    table = torch.empty(2, blocks, dtype=torch.int32, device="cuda")
+    table[:, :b.table.shape[1]] = b.table
+    b.table = table
+    for sinks in (2 ** 31 - 1, blocks * page - 1, 2 ** 30):
+        b.run(window=70, sinks=sinks)
+        b.check()
+    assert b.status.tolist() == [0, 0]
