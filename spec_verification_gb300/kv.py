@@ -136,7 +136,10 @@ def _bad(msg):
     return native.SSError(-1, msg)
 
 
-def _host(name):
+def _elsewhere(name, t, plan):
+    """The refusal of a tensor that is not on the plan's device."""
+    if t.is_cuda:
+        return _bad(f"{name} is on {t.device}, its plan on cuda:{plan.device}")
     return _bad(f"{name} is on the host: a device tensor is needed")
 
 
@@ -145,8 +148,9 @@ def _cache(plan, k_cache, v_cache, k_scale, v_scale):
     if k_cache.shape != plan.cache_shape or v_cache.shape != plan.cache_shape:
         raise _bad(f"caches must be seen as [pages, page_size, kv_heads, head_dim] = {list(plan.cache_shape)}, got "
                    f"{list(k_cache.shape)} and {list(v_cache.shape)}")
-    if not (k_cache.is_cuda and v_cache.is_cuda):
-        raise _host("the cache")
+    for t in (k_cache, v_cache):
+        if t.get_device() != plan.device:
+            raise _elsewhere("the cache", t, plan)
     if k_cache.dtype is not plan.cache_type or v_cache.dtype is not plan.cache_type:
         raise _bad(f"caches must be {plan.cache_type}, got {k_cache.dtype} and {v_cache.dtype}")
     st = k_cache.stride()
@@ -156,8 +160,8 @@ def _cache(plan, k_cache, v_cache, k_scale, v_scale):
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is not None and (t.dtype is not torch.float32 or t.numel() != plan.kv_heads or not t.is_contiguous()):
                 raise _bad(f"{name} must be {plan.kv_heads} contiguous float32 values")
-            if t is not None and not t.is_cuda:
-                raise _host(name)
+            if t is not None and t.get_device() != plan.device:
+                raise _elsewhere(name, t, plan)
     return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], _ptr(k_scale), _ptr(v_scale))
 
 
@@ -168,25 +172,25 @@ def _tokens(name, t, heads, plan):
         raise _bad(f"{name} must be [tokens, {heads}, {d}] with contiguous heads, got {list(shape)} with strides {list(st)}")
     if t.dtype is not plan.type:
         raise _bad(f"{name} must be {plan.type}, got {t.dtype}")
-    if not t.is_cuda:
-        raise _host(name)
+    if t.get_device() != plan.device:
+        raise _elsewhere(name, t, plan)
     if st[0] % 8:
         raise native.SSError(-2, f"{name}: token strides must be multiples of 8 elements, got {st[0]}")
     return st[0] if shape[0] > 1 else heads * d
 
 
-def _int(name, t, least):
+def _int(plan, name, t, least):
     """Address of an int32 tensor of at least `least` entries."""
     if t.dtype is not _I32 or not t.is_contiguous() or t.numel() < least:
         raise _bad(f"{name} must be contiguous int32 with at least {least} entries, got {t.dtype}, {list(t.shape)}")
-    if not t.is_cuda:
-        raise _host(name)
+    if t.get_device() != plan.device:
+        raise _elsewhere(name, t, plan)
     return t.data_ptr()
 
 
 def _pool(plan, block_table, kv_len, free_pages, free_count, B, tokens, stream):
-    return _POOL.pack(B, tokens, _int("block_table", block_table, B * plan.max_blocks), _int("kv_len", kv_len, B),
-                      _int("free_pages", free_pages, plan.num_pages), _int("free_count", free_count, 1), _stream(stream, plan),
+    return _POOL.pack(B, tokens, _int(plan, "block_table", block_table, B * plan.max_blocks), _int(plan, "kv_len", kv_len, B),
+                      _int(plan, "free_pages", free_pages, plan.num_pages), _int(plan, "free_count", free_count, 1), _stream(stream, plan),
                       plan.handle)
 
 
@@ -196,8 +200,8 @@ def ss_kv_append(plan: Plan, block_table, kv_len, free_pages, free_count, cu_new
     entries of slots or positions is not served."""
     B = kv_len.shape[0] if B is None else B
     pool = _pool(plan, block_table, kv_len, free_pages, free_count, B, min(slots.numel(), positions.numel()), stream)
-    code = _lib.ss_kv_append(pool, _int("cu_new", cu_new, B + 1), _int("slots", slots, 0), _int("positions", positions, 0),
-                             _int("seq_len", seq_len, B), _int("row_status", row_status, B))
+    code = _lib.ss_kv_append(pool, _int(plan, "cu_new", cu_new, B + 1), _int(plan, "slots", slots, 0), _int(plan, "positions", positions, 0),
+                             _int(plan, "seq_len", seq_len, B), _int(plan, "row_status", row_status, B))
     if code:
         native._check(code)
 
@@ -207,8 +211,8 @@ def ss_kv_commit(plan: Plan, block_table, kv_len, free_pages, free_count, seq_le
     """ss_kv_commit on int32 tensors: lengths move past what is kept, other pages go back to the pool."""
     B = kv_len.shape[0] if B is None else B
     pool = _pool(plan, block_table, kv_len, free_pages, free_count, B, 0, stream)
-    code = _lib.ss_kv_commit(pool, _int("seq_len", seq_len, B), None if counts is None else _int("counts", counts, B), plus,
-                             None if finished is None else _int("finished", finished, B))
+    code = _lib.ss_kv_commit(pool, _int(plan, "seq_len", seq_len, B), None if counts is None else _int(plan, "counts", counts, B), plus,
+                             None if finished is None else _int(plan, "finished", finished, B))
     if code:
         native._check(code)
 
@@ -226,17 +230,17 @@ def ss_rope_store(plan: Plan, q, k, v, k_cache, v_cache, inv_freq, positions, sl
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None and (w.dtype is not plan.type or w.numel() != plan.head_dim or not w.is_contiguous()):
             raise _bad(f"{name} must be {plan.head_dim} contiguous {plan.type} values")
-        if w is not None and not w.is_cuda:
-            raise _host(name)
+        if w is not None and w.get_device() != plan.device:
+            raise _elsewhere(name, w, plan)
     rot = 0
     if inv_freq is not None:
         if inv_freq.dtype is not torch.float64 or not inv_freq.is_contiguous():
             raise _bad("inv_freq must be contiguous float64")
-        if not inv_freq.is_cuda:
-            raise _host("inv_freq")
+        if inv_freq.get_device() != plan.device:
+            raise _elsewhere("inv_freq", inv_freq, plan)
         rot = 2 * inv_freq.shape[0]
     b = _ROPE.pack(T, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(q_weight), _ptr(k_weight), eps, _ptr(inv_freq),
-                  rot, 1 if interleaved else 0, rope_scale, _int("positions", positions, T), _int("slots", slots, T),
+                  rot, 1 if interleaved else 0, rope_scale, _int(plan, "positions", positions, T), _int(plan, "slots", slots, T),
                   q_out.data_ptr(), os, _stream(stream, plan), plan.handle)
     code = _lib.ss_rope_store(b, cache)
     if code:
@@ -263,11 +267,12 @@ def ss_attend(plan: Plan, q, k_cache, v_cache, block_table, seq_len, cu_new, *, 
         raise _bad("out must have as many tokens as q")
     if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() < q.shape[0] * plan.q_heads):
         raise _bad("lse must be contiguous float32 [tokens, q_heads]")
-    if not workspace.is_cuda or (lse is not None and not lse.is_cuda):
-        raise _host("workspace or lse")
-    b = _ATTEND.pack(B, q.shape[0], q.data_ptr(), qs, _int("cu_new", cu_new, B + 1), _int("seq_len", seq_len, B),
-                    _int("block_table", block_table, B * plan.max_blocks), scale, window, sinks, out.data_ptr(), os, _ptr(lse),
-                    _int("row_status", row_status, B), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+    for name, t in (("workspace", workspace), ("lse", lse)):
+        if t is not None and t.get_device() != plan.device:
+            raise _elsewhere(name, t, plan)
+    b = _ATTEND.pack(B, q.shape[0], q.data_ptr(), qs, _int(plan, "cu_new", cu_new, B + 1), _int(plan, "seq_len", seq_len, B),
+                    _int(plan, "block_table", block_table, B * plan.max_blocks), scale, window, sinks, out.data_ptr(), os, _ptr(lse),
+                    _int(plan, "row_status", row_status, B), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                     _stream(stream, plan), plan.handle)
     code = _lib.ss_attend(b, cache)
     if code:
