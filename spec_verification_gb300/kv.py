@@ -267,6 +267,8 @@ def ss_attend(plan: Plan, q, k_cache, v_cache, block_table, seq_len, cu_new, *, 
         raise _bad("out must have as many tokens as q")
     if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() < q.shape[0] * plan.q_heads):
         raise _bad("lse must be contiguous float32 [tokens, q_heads]")
+    if not workspace.is_contiguous():
+        raise _bad(f"workspace must be contiguous, got strides {list(workspace.stride())}")
     for name, t in (("workspace", workspace), ("lse", lse)):
         if t is not None and t.get_device() != plan.device:
             raise _elsewhere(name, t, plan)

@@ -62,3 +62,18 @@ def test_tensors_of_another_device_are_refused():
             with pytest.raises(native.SSError) as e:
                 call(plan, **args, **others, stream=stream)
             assert e.value.code == -1 and "host" in str(e.value), (call.__name__, name, str(e.value))
+
+
+@pytest.mark.parametrize("workspace", [torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(1 << 12, dtype=torch.uint8)[::2],
+                                       torch.zeros(4, 256, dtype=torch.uint8).T], ids=["expanded", "strided", "turned"])
+def test_workspaces_that_are_not_contiguous_are_refused(workspace):
+    """Their number of elements does not say how many bytes are there from their address on."""
+    from spec_verification_gb300 import build, kv, native
+    build.build()
+    kv.library()
+    plan, calls = _calls(kv)
+    _, tensors, others = calls[-1]
+    args = {n: On(t, 1) for n, t in {**tensors, "workspace": workspace}.items()}
+    with pytest.raises(native.SSError) as e:
+        kv.ss_attend(plan, **args, **others, stream=SimpleNamespace(cuda_stream=0))
+    assert e.value.code == -1 and "contiguous" in str(e.value)
