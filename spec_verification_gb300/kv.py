@@ -174,9 +174,11 @@ def _tokens(name, t, heads, plan):
         raise _bad(f"{name} must be {plan.type}, got {t.dtype}")
     if t.get_device() != plan.device:
         raise _elsewhere(name, t, plan)
+    if shape[0] <= 1:
+        return heads * d  # the stride of one token is of no matter
     if st[0] % 8:
         raise native.SSError(-2, f"{name}: token strides must be multiples of 8 elements, got {st[0]}")
-    return st[0] if shape[0] > 1 else heads * d
+    return st[0]
 
 
 def _int(plan, name, t, least):

@@ -228,3 +228,24 @@ def test_sinks_near_two_to_the_31(cache, page):
         b.run(window=70, sinks=sinks)
         b.check()
     assert b.status.tolist() == [0, 0]
+
+
+def test_one_token_of_any_stride():
+    """One token taken out of rows of an odd length: its stride is of no matter."""
+    kv = _kv()
+    b = Batch([1], [70], 8, 2, 64, "bf16", "bf16", "hnd", 16)
+    wide, out = (torch.zeros(3, 8 * 64 + 5, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    wide[0, :512] = b.q[0].flatten()
+    b.q = wide[:1, :512].view(1, 8, 64)
+    held, b.out = b.out, out[:1, :512].view(1, 8, 64)
+    b.run()
+    held[:1] = b.out
+    b.out = held
+    b.check()
+    assert torch.all(out[:, 512:] == 0) and torch.all(out[1:] == 0)
+    # an unaligned address is still refused
+    from spec_verification_gb300 import native
+    with pytest.raises(native.SSError) as e:
+        b.q = wide[:1, 1:513].view(1, 8, 64)
+        b.run()
+    assert e.value.code == -2
