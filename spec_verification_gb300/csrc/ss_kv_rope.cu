@@ -91,6 +91,11 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | hi << 16;
 }
 
+// Four values of a query or key.  Not __ldg: queries may be overwritten in place, and a read-only load is for what the
+// kernel does not write.  (By way of L2, as each is read once: with plain loads the compiler holds eight registers more over
+// the angles and spills, 16384 tokens 67.6 us where these take 64.7.)
+__device__ __forceinline__ uint2 load_pairs(const void* p) { return __ldcg(static_cast<const uint2*>(p)); }
+
 // Eight values of a head that one thread holds: four pairs (a, b).
 struct Eight {
   float a[4], b[4];
@@ -114,7 +119,7 @@ __device__ __forceinline__ void gathered(const Eight& e, bool halves, float (&y)
 // thread holds both values of each of its pairs, so no lane needs another's; cos and sin of its four pairs are in
 // registers, multiplied with the norm's weights, and a head costs two 8-byte loads, its sum of squares over the
 // lanes, 24 multiplications and additions, and two stores.  Ten CTAs of 128 threads an SM keep enough loads in flight
-// (eight: 71 us where ten take 65): 16384 tokens of 48 heads of 128, with norms, 65.7 us, 6.1 TB/s.
+// (eight: 71 us where ten take 65): 16384 tokens of 48 heads of 128, with norms, 64.7 us, 6.2 TB/s.
 // `Order` says what is known of the pairs at compile time: kNeighbours in every lane, kHalves in every lane (all of
 // the head is rotated), or kMixed ("half" pairs in the first lanes).
 enum Order { kNeighbours, kHalves, kMixed };
@@ -128,7 +133,7 @@ __global__ void __launch_bounds__(kNT, 10) rope_kernel(const RopeParams P) {
   const int tl = group % TB;
   const int t0 = blockIdx.x * TB, t = min(t0 + tl, P.T - 1);
   const bool live = t0 + tl < P.T;
-  const int half = P.rot >> 1;
+  const int half = kOrder == kHalves ? D / 2 : P.rot >> 1;
   const bool turned = kOrder == kHalves || lane * 8 < P.rot;
   const bool halves = kOrder == kHalves || (kOrder == kMixed && turned);
   const int at = halves ? lane * 4 : lane * 8, then = halves ? half + lane * 4 : at + 4;
@@ -146,8 +151,8 @@ __global__ void __launch_bounds__(kNT, 10) rope_kernel(const RopeParams P) {
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) {
       const T* p = src + min(first + n * step, last) * D;
-      r.lo[n] = __ldg(reinterpret_cast<const uint2*>(p + at));
-      r.hi[n] = __ldg(reinterpret_cast<const uint2*>(p + then));
+      r.lo[n] = load_pairs(p + at);
+      r.hi[n] = load_pairs(p + then);
     }
   };
   Raw raw;
@@ -200,7 +205,7 @@ __global__ void __launch_bounds__(kNT, 10) rope_kernel(const RopeParams P) {
           if (std::is_same<T, __nv_bfloat16>::value) {
             // bf16 values whose squares come near the ends of 32 bits, or pass them: once more with the head scaled by a
             // power of two, which the norm takes out.  (Asked before the sum over the lanes, beside which the vote costs
-            // least: 16384 tokens 64.8 -> 65.7 us.  Leaving such heads out for a second pass: 66.3.)
+            // least: 1 us of 65 with 16384 tokens.  Leaving such heads out for a second pass costs 1.5.)
             const bool tiny = P.eps < 0x1p-100f;  // nothing else keeps the root from the small end
             if (__any_sync(0xffffffffu, sum > 0x1p100f || (tiny && sum < 0x1p-100f))) {
 #pragma unroll

@@ -34,3 +34,13 @@ def test_softmax_warps_meet_whatever_one_of_them_has_read():
     partly = code[code.index("bool partly("):]
     assert partly.startswith("bool partly(const AttendParams& P, const Unit& u, int base)")
     assert set(re.findall(r"\b[a-zA-Z]\w*", _body(partly, 0))) <= {"return", "base", "kTile", "u", "pos0", "pos1", "P", "window", "sinks"}
+
+
+def test_queries_that_may_be_overwritten_are_not_read_as_read_only():
+    """ss_rope_store allows q_out to be q; a read-only load is defined only for what the kernel does not write."""
+    code = _code("ss_kv_rope.cu")
+    load = _body(code, code.index("auto load = [&]"))
+    assert "P.q" in load and "__ldg" not in load
+    uses = [m.start() for m in re.finditer(r"__ldg\(", code)]
+    assert [re.search(r"__ldg\(reinterpret_cast<const uint4\*>\(v \+", code[at:at + 60]) is not None for at in uses] == [True]
+    assert "__restrict__" not in code
