@@ -249,3 +249,87 @@ def test_one_token_of_any_stride():
         b.q = wide[:1, 1:513].view(1, 8, 64)
         b.run()
     assert e.value.code == -2
+
+
+# ------------------------------------------------------------------ attention: forms of the kernels that other tests do not reach
+@pytest.mark.parametrize("hq,new,dim,kind", [(16, 4, 128, "bf16"), (16, 8, 128, "f16"), (16, 16, 128, "bf16"), (16, 4, 64, "bf16"),
+                                             (16, 8, 64, "f16"), (24, 16, 64, "bf16"), (8, 2, 256, "f16"), (16, 16, 256, "bf16")])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (80, 5)])
+def test_values_that_are_not_finite_over_8_bits(hq, new, dim, kind, window, sinks):
+    """NaN in a value that some queries see, and in keys and values that none does: the converting kernels."""
+    b = Batch([new, 1, 1], [200, 90, 300], hq, 2, dim, kind, "e4m3", "hnd", 16)
+    nan = 0x7F
+    where = [(0, 200 - new // 2, 1, 7)] + ([(1, 6, 0, 9), (2, 130, 1, dim - 1)] if window else [])
+    for r, t, h, d in where:
+        page, place = int(b.table[r, t // 16]), t % 16
+        b.vc.view(torch.uint8)[page, place, h, d] = nan
+        if r:
+            b.kc.view(torch.uint8)[page, place, h, d] = nan
+    b.run(window, sinks)
+    torch.cuda.synchronize()
+    half = hq // 2
+    wild = torch.zeros(new + 2, hq, dim, dtype=torch.bool, device="cuda")
+    wild[new - new // 2:new, half:, 7] = True  # the queries from that token on, in its head's column
+    got = b.out[:new + 2]
+    assert torch.equal(torch.isnan(got), wild)
+    b.v[0][200 - new // 2, 1, 7] = 0.0
+    at = 0
+    for r, n in enumerate(b.new):
+        want, _, weighted, plain, size = ref.attend(b.q[at:at + n].double(), b.k[r], b.v[r], b.length[r] - n, b.scale, window, sinks)
+        off = (dim * 2.0 ** -23 * size + 2.0 ** -20)[..., None]
+        tol = U[kind] * want.abs() * (1 + 2.0 ** -10) + (U["f16"] + 2 * off) * weighted + 2.0 ** -25 + 2.0 ** -32 * plain
+        assert torch.all(((got[at:at + n].double() - want).abs() <= tol) | wild[at:at + n])
+        at += n
+
+
+@pytest.mark.parametrize("hq,hkv,kind,cache,page", [(4, 1, "bf16", "bf16", 16), (2, 2, "f16", "e4m3", 16), (24, 1, "bf16", "e4m3", 32)])
+def test_as_many_rows_as_a_plan_may_have(hq, hkv, kind, cache, page):
+    """8192 rows, each thread of the search for a CTA's range holds many; some rows are bad, some have nothing new."""
+    rows, dim = 8192, 64
+    rng = np.random.default_rng(hq)
+    new = (rng.random(rows) < 0.9).astype(int)
+    length = 1 + (rng.random(rows) ** 4 * 60).astype(int)
+    length[rng.integers(0, rows, 4)] = 3000
+    b = Batch([1] * 2, [1] * 2, hq, hkv, dim, kind, cache, "hnd", page)  # types, factors
+    g = torch.Generator(device="cuda").manual_seed(hq)
+    used = -(-length // page)
+    blocks, pages = int(used.max()), int(used.sum())
+    first = np.cumsum(used) - used
+    table = torch.full((rows, blocks), -1, dtype=torch.int32)
+    ids = torch.randperm(pages, generator=g, device="cuda")
+    for r in range(rows):
+        table[r, :used[r]] = torch.arange(first[r], first[r] + used[r])
+    table = torch.where(table.cuda() >= 0, ids[table.cuda().clamp(min=0).long()].to(torch.int32), -1).contiguous()
+    kc, vc = (torch.randn(pages, hkv, page, dim, generator=g, device="cuda").to(TYPES[cache]).transpose(1, 2) for _ in range(2))
+    q = torch.randn(int(new.sum()), hq, dim, generator=g, device="cuda").to(TYPES[kind])
+    seq = length.copy()
+    bad = rng.choice(rows, 20, replace=False)
+    seq[bad] = -1
+    plan = _kv().Plan(max_rows=rows, max_tokens=rows, max_new=1, q_heads=hq, kv_heads=hkv, head_dim=dim, page_size=page, num_pages=pages,
+                      max_blocks=blocks, dtype=kind, cache_dtype=cache)
+    out, status = torch.full_like(q, 7.0), _i32([0] * rows)
+    workspace = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    _kv().ss_attend(plan, q, kc, vc, table, _i32(seq.tolist()), _i32([0] + np.cumsum(new).tolist()), out=out, row_status=status,
+                    workspace=workspace, scale=dim ** -0.5, k_scale=b.ks, v_scale=b.vs)
+    torch.cuda.synchronize()
+    want_status = np.zeros(rows, int)
+    want_status[bad] = 1 << 4
+    assert status.tolist() == want_status.tolist()
+    at = np.cumsum(new) - new
+    for some in (np.flatnonzero((new > 0) & (seq > 0))[::7], np.flatnonzero((new > 0) & (seq >= 3000))):
+        for r in some.tolist():
+            t = torch.arange(int(seq[r]), device="cuda")
+            k, v = (c[table[r, t // page].long(), t % page].double() if cache != "e4m3" else
+                    c.view(torch.uint8)[table[r, t // page].long(), t % page].view(TYPES[cache]).double() for c in (kc, vc))
+            if cache == "e4m3":
+                k, v = k * b.ks.double()[:, None], v * b.vs.double()[:, None]
+            k, v = (x.repeat_interleave(hq // hkv, 1) for x in (k, v))
+            w = torch.softmax(torch.einsum("hd,thd->ht", q[at[r]].double(), k) * dim ** -0.5, -1)
+            want, weighted = torch.einsum("ht,thd->hd", w, v), torch.einsum("ht,thd->hd", w, v.abs())
+            product = U["f16" if cache == "e4m3" else kind]
+            # 2^-14: 64 roundings of sums of |q k| below 16, twice, and the 2^x
+            tol = U[kind] * want.abs() * (1 + 2.0 ** -10) + (product + 2.0 ** -14) * weighted + 2.0 ** -24
+            assert torch.all((out[at[r]].double() - want).abs() <= tol), r
+    for r in bad.tolist():
+        if new[r]:
+            assert torch.all(out[at[r]] == 0)
