@@ -53,6 +53,7 @@ struct Pair<__half> {
 __device__ __forceinline__ float2 turn_of(double f, int position) {
   const unsigned long long bits = (unsigned long long)__double_as_longlong(f);
   const int be = (int)(bits >> 52) & 0x7ff;
+  if (be == 0x7ff) return make_float2(NAN, NAN);  // infinite or NaN: so are the angles
   unsigned long long fix = 0;
   if (be != 0) {
     const unsigned long long m64 = ((bits & 0xfffffffffffffull) | 0x10000000000000ull) << 11;

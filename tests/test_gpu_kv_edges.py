@@ -333,3 +333,26 @@ def test_as_many_rows_as_a_plan_may_have(hq, hkv, kind, cache, page):
     for r in bad.tolist():
         if new[r]:
             assert torch.all(out[at[r]] == 0)
+
+
+@pytest.mark.parametrize("wrong", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("inter", [False, True])
+def test_frequencies_that_are_not_finite_show(wrong, inter):
+    """The pairs of such a frequency become NaN, not what they were; the others are as they should be."""
+    kv = _kv()
+    plan = _plan(1, 5, 16, 1, 1, q_heads=2, kv_heads=1, head_dim=64)
+    q, k, v = (torch.randn(5, h, 64, device="cuda").bfloat16() for h in (2, 1, 1))
+    kc, vc = _cache("bf16", "hnd", 1, 16, 1, 64, 0.0), _cache("bf16", "hnd", 1, 16, 1, 64, 0.0)
+    good = torch.tensor(kv.rope_frequencies(32), device="cuda")
+    inv = good.clone()
+    inv[3] = wrong
+    places = torch.arange(5, device="cuda", dtype=torch.int32)
+    outs = []
+    for f in (good, inv):
+        outs.append(torch.empty_like(q))
+        kv.ss_rope_store(plan, q, k, v, kc, vc, f, places, places, q_out=outs[-1], interleaved=inter)
+    torch.cuda.synchronize()
+    nan = torch.zeros(64, dtype=torch.bool, device="cuda")
+    nan[[6, 7] if inter else [3, 19]] = True
+    assert torch.equal(torch.isnan(outs[1]), nan.expand_as(q)) and torch.equal(torch.isnan(kc[0, :5, 0]), nan.expand(5, 64))
+    assert torch.equal(outs[0][..., ~nan], outs[1][..., ~nan]) and torch.equal(vc[0, :5], v)
