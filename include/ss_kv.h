@@ -193,7 +193,9 @@ typedef struct {
  * h / (q_heads / kv_heads).  Scores, softmax sums and outputs are fp32,
  * rounded once at the end (the softmax weights are rounded to the cache's
  * 16-bit type, f16 for SS_E4M3, before the product with the values; the sum
- * that divides is then that of the rounded bf16 weights; f16 weights keep 11
+ * that divides is then that of the rounded bf16 weights; bf16 queries over an
+ * SS_E4M3 cache become f16 by a power of two a row and head, so that values
+ * below 2^-28 of the largest lose bits; f16 weights keep 11
  * bits down to 2^-21 of the row's largest, and below 2^-32 of it may count as 0).  A query
  * that sees no token (a position below 0), or only scores of -inf, gives
  * zeros and lse -inf.  Values of tokens that a query does not see never reach

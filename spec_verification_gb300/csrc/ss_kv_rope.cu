@@ -120,7 +120,9 @@ __device__ __forceinline__ void gathered(const Eight& e, bool halves, float (&y)
 // thread holds both values of each of its pairs, so no lane needs another's; cos and sin of its four pairs are in
 // registers, multiplied with the norm's weights, and a head costs two 8-byte loads, its sum of squares over the
 // lanes, 24 multiplications and additions, and two stores.  Ten CTAs of 128 threads an SM keep enough loads in flight
-// (eight: 71 us where ten take 65): 16384 tokens of 48 heads of 128, with norms, 64.7 us, 6.2 TB/s.
+// (eight: 71 us where ten take 65): 16384 tokens of 48 heads of 128, with norms, 64.7 us, 6.2 TB/s.  That was measured on
+// this form; the 48 registers spill 32 bytes a thread with 8 bits (6000 tokens of 56 heads 32.8 us, 4.9 TB/s) and 64 with
+// "half" pairs on part of the head (6000 of 48 heads, a quarter turned, 39 us, 3.8 TB/s).
 // `Order` says what is known of the pairs at compile time: kNeighbours in every lane, kHalves in every lane (all of
 // the head is rotated), or kMixed ("half" pairs in the first lanes).
 enum Order { kNeighbours, kHalves, kMixed };
