@@ -587,6 +587,38 @@ static __device__ __noinline__ void report_range(const AttendParams& P, const Ra
   while (next_segment(P, k, g)) atomicOr(&P.row_status[g.row], (uint32_t)SS_ST_COPY_TIMEOUT);
 }
 
+// x * scale - m is one operation, which knows more bits of the product than m has.  Where m is beyond 2^20 (a 16th of a
+// power of two, the same for all keys; at 2^24 more than f16 weights can take) the product is rounded as m was, and m is
+// the maximum itself: of scores that large 32 bits tell nothing below it.
+constexpr float kLarge = 0x1p20f;
+
+// A row's weights of one tile where m is large, over its scores: as in softmax_warps.  Returns their sums, that of the
+// rounded ones first.  (Out of line, where it costs the other tiles nothing: as part of their code it did, 256 x 1 short
+// rows 45 -> 49.5 us.)
+template <class S, int KEYS>
+static __device__ __noinline__ float2 large_weights(uint32_t at, int key0, float scale, float z, uint64_t seen) {
+  using E = Elem<typename S::Mul>;
+  float rounded = 0.0f, exact = 0.0f;
+#pragma unroll 1
+  for (int i = key0; i < key0 + KEYS; i += 16) {
+    uint32_t x[16], w[8];
+    tmem_load(x, at + i);
+#pragma unroll
+    for (int n = 0; n < 16; n += 2) {
+      float y[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        y[h] = (seen >> (i + n + h)) & 1 ? ex2(__fsub_rn(__fmul_rn(__uint_as_float(x[n + h]), scale), z)) : 0.0f;
+      w[n / 2] = E::pack(y[0], y[1]);
+      const float2 r = std::is_same<typename S::Mul, __nv_bfloat16>::value ? E::unpack(w[n / 2]) : make_float2(y[0], y[1]);
+      rounded += r.x + r.y;
+      exact += y[0] + y[1];
+    }
+    tmem_store(at + i / 2, w);
+  }
+  return make_float2(rounded, exact);
+}
+
 template <class S, class T, int D, int KEYS>
 __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned char* ring, Control& c) {
   using E = Elem<typename S::Mul>;
@@ -625,6 +657,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
     // NaN.  Products of the held values are below 2^33, so with factors this small every score is 0 either way.
     if (S::kLow) scale = fmaxf(scale, FLT_MIN);
     float mx = -INFINITY, l = 0.0f, exact = 0.0f;  // m, the sum that divides, the sum of the weights
+    bool large = false;  // a row of the warp has an m beyond kLarge
 
     for (int i = 0; i < g.count; ++i, ++it) {
       const int b = it & 1;
@@ -658,11 +691,13 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
 #pragma unroll
           for (int n = 0; n < kChunk; ++n) t[n & 3] = fmaxf(t[n & 3], __uint_as_float(x[n]));
         }
-        const float top = fmaf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), scale, -E::kLift);
-        const bool grow = live && top > (mx == -INFINITY ? mx : mx + 8.0f);
+        const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
+        const bool grow = live && top - mx > 8.0f + E::kLift;
         if (__any_sync(0xffffffffu, grow)) {
-          const float by = grow ? ex2(mx - top) : 1.0f;  // 0 if nothing was seen before
-          if (grow) mx = top;
+          const float now = grow ? (fabsf(top) > kLarge ? top : top - E::kLift) : mx;
+          const float by = grow ? ex2(mx - now) : 1.0f;  // 0 if nothing was seen before
+          mx = now;
+          large = __any_sync(0xffffffffu, mx != -INFINITY && fabsf(mx) > kLarge);
           l *= by;
           exact *= by;
           if (i > 0) {
@@ -680,11 +715,16 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         }
         const float z = mx == -INFINITY ? 0.0f : mx;
         // Weights are rounded to 16 bits for the product (half a step, 2^-9 or 2^-12 of each, random in sign; f16 weights
-        // below 2^-14, 2^-21 of the first tile's largest, by up to 2^-25).  To bf16 the divisor is the sum of the rounded ones, so that the error of a weight that dominates its row cancels; the
-        // log-sum-exp has the sum before rounding.
+        // below 2^-14, 2^-21 of the first tile's largest, by up to 2^-25).  To bf16 the divisor is the sum of the rounded
+        // ones, so that the error of a weight that dominates its row cancels; the log-sum-exp has the sum before rounding.
         constexpr bool kTwo = std::is_same<typename S::Mul, __nv_bfloat16>::value;
+        if (large) {
+          const float2 sums = large_weights<S, KEYS>(lanes + b * kTile, key0, scale, z, seen);
+          l += sums.x;
+          exact += sums.y;
+        }
 #pragma unroll
-        for (int at = 0; at < KEYS; at += kChunk) {
+        for (int at = 0; at < KEYS && !large; at += kChunk) {
           if (KEYS > kChunk) scores(x, at);
           uint32_t w[kChunk / 2];
           float s0 = 0.0f, s1 = 0.0f, e0 = 0.0f, e1 = 0.0f;

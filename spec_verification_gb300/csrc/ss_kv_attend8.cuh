@@ -262,6 +262,20 @@ __device__ __forceinline__ uint32_t place_of(int key, int b) {
   return off ^ ((off >> 3) & (D == 128 ? 0x70 : 0x30));
 }
 
+// Weights of a warp's scores where a row's m is large (see kLarge), out of line for the same reason.
+template <int N>
+struct Scores {
+  float s[N][4];
+};
+template <int N>
+static __device__ __noinline__ Scores<N> large_weights(Scores<N> x, float c0, float z0, float c1, float z1) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x.s[n][e] = ex2(__fsub_rn(__fmul_rn(x.s[n][e], e < 2 ? c0 : c1), e < 2 ? z0 : z1));
+  return x;
+}
+
 template <class S, class T, int D>
 __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsigned char* sq, Control& c) {
   constexpr int kNT = S::kKG * 2;  // 8-key tiles of a warp
@@ -367,6 +381,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
     float mx0 = -INFINITY, mx1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+    bool large = false;  // a row of the warp has an m beyond kLarge
 
     Turn keys, values;
     for (int i = 0; i < count; ++i) {
@@ -430,14 +445,15 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
         t0 = fmaxf(t0, fmaxf(s[n][0], s[n][1]));
         t1 = fmaxf(t1, fmaxf(s[n][2], s[n][3]));
       }
-      t0 = fmaf(t0, c0, -Elem<__half>::kLift);
-      t1 = fmaf(t1, c1, -Elem<__half>::kLift);
-      if (__any_sync(0xffffffffu, t0 > mx0 + 8.0f || t1 > mx1 + 8.0f || (mx0 == -INFINITY && t0 > mx0) || (mx1 == -INFINITY && t1 > mx1))) {
+      t0 *= c0;
+      t1 *= c1;
+      constexpr float kLift = Elem<__half>::kLift;
+      if (__any_sync(0xffffffffu, t0 - mx0 > 8.0f + kLift || t1 - mx1 > 8.0f + kLift)) {
         t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
         t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
-        const float n0 = fmaxf(mx0, t0), n1 = fmaxf(mx1, t1);
+        const float n0 = fmaxf(mx0, fabsf(t0) > kLarge ? t0 : t0 - kLift), n1 = fmaxf(mx1, fabsf(t1) > kLarge ? t1 : t1 - kLift);
         const float a0 = n0 == mx0 ? 1.0f : ex2(mx0 - n0), a1 = n1 == mx1 ? 1.0f : ex2(mx1 - n1);
         l0 *= a0;
         l1 *= a1;
@@ -450,14 +466,31 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
         }
         mx0 = n0;
         mx1 = n1;
+        large = __any_sync(0xffffffffu, (mx0 != -INFINITY && fabsf(mx0) > kLarge) || (mx1 != -INFINITY && fabsf(mx1) > kLarge));
       }
       const float z0 = mx0 == -INFINITY ? 0.0f : mx0, z1 = mx1 == -INFINITY ? 0.0f : mx1;
+      if (large) {
+        Scores<kNT> x;
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x.s[n][e] = s[n][e];
+        x = large_weights(x, c0, z0, c1, z1);
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] = x.s[n][e];
+      } else {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+          s[n][0] = ex2(fmaf(s[n][0], c0, -z0));
+          s[n][1] = ex2(fmaf(s[n][1], c0, -z0));
+          s[n][2] = ex2(fmaf(s[n][2], c1, -z1));
+          s[n][3] = ex2(fmaf(s[n][3], c1, -z1));
+        }
+      }
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
-        s[n][0] = ex2(fmaf(s[n][0], c0, -z0));
-        s[n][1] = ex2(fmaf(s[n][1], c0, -z0));
-        s[n][2] = ex2(fmaf(s[n][2], c1, -z1));
-        s[n][3] = ex2(fmaf(s[n][3], c1, -z1));
         l0 += s[n][0] + s[n][1];
         l1 += s[n][2] + s[n][3];
       }

@@ -356,3 +356,40 @@ def test_frequencies_that_are_not_finite_show(wrong, inter):
     nan[[6, 7] if inter else [3, 19]] = True
     assert torch.equal(torch.isnan(outs[1]), nan.expand_as(q)) and torch.equal(torch.isnan(kc[0, :5, 0]), nan.expand(5, 64))
     assert torch.equal(outs[0][..., ~nan], outs[1][..., ~nan]) and torch.equal(vc[0, :5], v)
+
+
+@pytest.mark.parametrize("rows,dim,kind,cache,spread", [
+    (rows, dim, kind, cache, s) for rows, dim, kind, cache in F16_WEIGHTS + [(4, 64, "bf16", "bf16"), (16, 128, "bf16", "bf16"),
+                                                                              (64, 64, "bf16", "bf16"), (128, 256, "bf16", "bf16")]
+    for s in (1e4, 3e7, 1e9 if kind == "f16" else 1e12, *([1e30] if kind == "bf16" else []))])
+@pytest.mark.parametrize("times", [1, 60])
+def test_scores_of_any_size(rows, dim, kind, cache, spread, times):
+    """Scores spread by up to 1e30: a query's output is the value of its largest score, as far as 32 bits tell which that is."""
+    g = torch.Generator(device="cuda").manual_seed(rows + dim)
+    tokens, hkv, group = 1500, 4, 4
+    n = rows // group
+    a = min(spread ** 0.5, 1e4) if kind == "f16" else spread ** 0.5
+    if cache == "f16" and spread > 1e8:
+        spread = 1e8
+    factors = torch.full((hkv,), spread / a / 50, device="cuda") if cache == "e4m3" else None
+    q = a * torch.randn(n, hkv * group, dim, generator=g, device="cuda")
+    k, v = torch.randn(2, tokens, hkv, dim, generator=g, device="cuda")
+    row = Row(q, k * (spread / a), v, kind, cache, k_scale=factors, v_scale=torch.ones(hkv, device="cuda") if cache == "e4m3" else None, times=times)
+    for kw in ({}, {"window": 700, "sinks": 5}):
+        got, got_lse = row.run(**kw)
+        assert torch.all(torch.isfinite(got)) and torch.all(torch.isfinite(got_lse))
+        t, p = torch.arange(tokens, device="cuda"), torch.arange(tokens - n, tokens, device="cuda")[:, None]
+        seen = (t <= p) & ((t > p - kw["window"]) | (t < kw["sinks"]) if kw else torch.ones_like(t, dtype=torch.bool))
+        kk, vv = row.k.repeat_interleave(group, 1), row.v.repeat_interleave(group, 1)
+        s = torch.einsum("nhd,thd->nht", row.q.double(), kk) * row.scale
+        size = torch.einsum("nhd,thd->nht", row.q.double().abs(), kk.abs()).amax(-1) * row.scale
+        top, at = s.masked_fill(~seen[:, None], -math.inf).topk(2, -1)
+        off = dim * 2.0 ** -23 * size  # of a score
+        sure = top[..., 0] - top[..., 1] > 2 * off + 60
+        assert sure.double().mean() > 0.9
+        want = torch.stack([vv[at[..., 0][:, h], h] for h in range(hkv * group)], 1)
+        # the bound of tests/test_gpu_kv.py where one weight is all there is: the output's rounding and the weight's (the others'
+        # are below 2^-80, whatever the scores are off by); log-sum-exp: the score, rounded with the factors
+        tol = U[kind] * want.abs() * (1 + 2.0 ** -10) + U[row.product] * want.abs() + 2.0 ** -25
+        assert torch.all(((got - want).abs() <= tol)[:, sure])
+        assert torch.all(((got_lse - top[..., 0]).abs() <= off + 2.0 ** -21 * top[..., 0].abs())[:, sure])
