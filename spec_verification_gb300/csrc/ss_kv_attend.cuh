@@ -377,7 +377,7 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
                               fmaxf(fmaxf(fabsf(v2.x), fabsf(v2.y)), fmaxf(fabsf(v3.x), fabsf(v3.y))));
 #pragma unroll
             for (int o = D / 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 240);      // biased exponent
+            const int ex = max((int)(__float_as_uint(top) >> 23), 15);                // biased exponent
             const float up = __uint_as_float((uint32_t)(127 + 14 + 127 - ex) << 23);  // 2^(14 - exponent)
             if (i >= pieces) continue;
             if (i % (D / 8) == 0) c.q_back[sg & 1][i / (D / 8)] = __uint_as_float((uint32_t)(ex - 14) << 23);

@@ -332,7 +332,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
                           fmaxf(fmaxf(fabsf(d.x), fabsf(d.y)), fmaxf(fabsf(e.x), fabsf(e.y))));
 #pragma unroll
         for (int o = D / 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 240);      // biased exponent
+        const int ex = max((int)(__float_as_uint(top) >> 23), 15);                // biased exponent
         const float up = __uint_as_float((uint32_t)(127 + 14 + 127 - ex) << 23);  // 2^(14 - exponent)
         if (piece == 0) c.qinv[m] = __uint_as_float((uint32_t)(ex - 14) << 23);
         x = make_uint4(Pack<__half>::pack(a.x * up, a.y * up), Pack<__half>::pack(b.x * up, b.y * up),

@@ -358,6 +358,30 @@ def test_frequencies_that_are_not_finite_show(wrong, inter):
     assert torch.equal(outs[0][..., ~nan], outs[1][..., ~nan]) and torch.equal(vc[0, :5], v)
 
 
+def _largest_score_wins(row, group, kind):
+    """A query's output is the value of its largest score, wherever 32 bits tell which that is."""
+    n, hq, dim = row.q.shape
+    tokens = row.tokens
+    for kw in ({}, {"window": 700, "sinks": 5}):
+        got, got_lse = row.run(**kw)
+        assert torch.all(torch.isfinite(got)) and torch.all(torch.isfinite(got_lse))
+        t, p = torch.arange(tokens, device="cuda"), torch.arange(tokens - n, tokens, device="cuda")[:, None]
+        seen = (t <= p) & ((t > p - kw["window"]) | (t < kw["sinks"]) if kw else torch.ones_like(t, dtype=torch.bool))
+        kk, vv = row.k.repeat_interleave(group, 1), row.v.repeat_interleave(group, 1)
+        s = torch.einsum("nhd,thd->nht", row.q.double(), kk) * row.scale
+        size = torch.einsum("nhd,thd->nht", row.q.double().abs(), kk.abs()).amax(-1) * row.scale
+        top, at = s.masked_fill(~seen[:, None], -math.inf).topk(2, -1)
+        off = dim * 2.0 ** -23 * size  # of a score
+        sure = top[..., 0] - top[..., 1] > 2 * off + 60
+        assert sure.double().mean() > 0.9
+        want = torch.stack([vv[at[..., 0][:, h], h] for h in range(hq)], 1)
+        # the bound of tests/test_gpu_kv.py where one weight is all there is: the output's rounding and the weight's (the others'
+        # are below 2^-80, whatever the scores are off by); log-sum-exp: the score, rounded with the factors
+        tol = U[kind] * want.abs() * (1 + 2.0 ** -10) + U[row.product] * want.abs() + 2.0 ** -25
+        assert torch.all(((got - want).abs() <= tol)[:, sure])
+        assert torch.all(((got_lse - top[..., 0]).abs() <= off + 2.0 ** -21 * top[..., 0].abs())[:, sure])
+
+
 @pytest.mark.parametrize("rows,dim,kind,cache,spread", [
     (rows, dim, kind, cache, s) for rows, dim, kind, cache in F16_WEIGHTS + [(4, 64, "bf16", "bf16"), (16, 128, "bf16", "bf16"),
                                                                               (64, 64, "bf16", "bf16"), (128, 256, "bf16", "bf16")]
@@ -375,21 +399,22 @@ def test_scores_of_any_size(rows, dim, kind, cache, spread, times):
     q = a * torch.randn(n, hkv * group, dim, generator=g, device="cuda")
     k, v = torch.randn(2, tokens, hkv, dim, generator=g, device="cuda")
     row = Row(q, k * (spread / a), v, kind, cache, k_scale=factors, v_scale=torch.ones(hkv, device="cuda") if cache == "e4m3" else None, times=times)
-    for kw in ({}, {"window": 700, "sinks": 5}):
-        got, got_lse = row.run(**kw)
-        assert torch.all(torch.isfinite(got)) and torch.all(torch.isfinite(got_lse))
-        t, p = torch.arange(tokens, device="cuda"), torch.arange(tokens - n, tokens, device="cuda")[:, None]
-        seen = (t <= p) & ((t > p - kw["window"]) | (t < kw["sinks"]) if kw else torch.ones_like(t, dtype=torch.bool))
-        kk, vv = row.k.repeat_interleave(group, 1), row.v.repeat_interleave(group, 1)
-        s = torch.einsum("nhd,thd->nht", row.q.double(), kk) * row.scale
-        size = torch.einsum("nhd,thd->nht", row.q.double().abs(), kk.abs()).amax(-1) * row.scale
-        top, at = s.masked_fill(~seen[:, None], -math.inf).topk(2, -1)
-        off = dim * 2.0 ** -23 * size  # of a score
-        sure = top[..., 0] - top[..., 1] > 2 * off + 60
-        assert sure.double().mean() > 0.9
-        want = torch.stack([vv[at[..., 0][:, h], h] for h in range(hkv * group)], 1)
-        # the bound of tests/test_gpu_kv.py where one weight is all there is: the output's rounding and the weight's (the others'
-        # are below 2^-80, whatever the scores are off by); log-sum-exp: the score, rounded with the factors
-        tol = U[kind] * want.abs() * (1 + 2.0 ** -10) + U[row.product] * want.abs() + 2.0 ** -25
-        assert torch.all(((got - want).abs() <= tol)[:, sure])
-        assert torch.all(((got_lse - top[..., 0]).abs() <= off + 2.0 ** -21 * top[..., 0].abs())[:, sure])
+    _largest_score_wins(row, group, kind)
+
+
+@pytest.mark.parametrize("rows,dim", [(4, 64), (16, 128), (32, 128), (64, 64), (128, 128), (8, 256)])
+def test_largest_bf16_queries_over_8_bits(rows, dim):
+    """Queries of 3e37: they become f16 by a power of two, however large they are."""
+    g = torch.Generator(device="cuda").manual_seed(rows + dim)
+    tokens, hkv, group = 900, 4, 4
+    q = 3e37 * torch.randn(rows // group, hkv * group, dim, generator=g, device="cuda").clamp(-5, 5)
+    q[:, 1] *= 1e-37
+    k, v = torch.randn(2, tokens, hkv, dim, generator=g, device="cuda")
+    row = Row(q, k * 1e-4, v, "bf16", "e4m3", k_scale=torch.full((hkv,), 2e-6, device="cuda"), v_scale=torch.ones(hkv, device="cuda"))
+    assert 2.0 ** 124 < row.q.abs().max() < math.inf
+    got = row.run()[0][0]
+    assert torch.all(torch.isfinite(got))
+    small = ref.attend(row.q[:, 1:2].double(), row.k[:, :1], row.v[:, :1], tokens - rows // group, row.scale)[0][:, 0]
+    assert torch.all((got[:, 1] - small).abs() <= 2.0 ** -7 * (small.abs() + row.v.abs().mean()))
+    row.q = torch.cat([row.q[:, :1], row.q[:, 2:3], row.q[:, 2:]], 1).contiguous()
+    _largest_score_wins(row, group, "bf16")
