@@ -21,7 +21,7 @@
 // the columns, while the next segment's queries are on their way (256 rows of
 // at most 1000 tokens: 106 us with a join by halves and queries read after it,
 // 94 so).
-// Measured: 32 rows x 4 tokens x 4 query heads over up to 32000 tokens 156 us,
+// Measured: 32 rows x 4 tokens x 4 query heads over up to 32000 tokens 158 us,
 // 4.7 TB/s; what bounds it is the latency of its chains (two warps to a
 // scheduler, 40 % of issue slots, 24 % of the tensor pipe).
 #pragma once
