@@ -86,6 +86,22 @@ typedef struct {
   const float* v_scale;
 } ss_kv_cache;
 
+/* One layer's SS_E4M3 cache with a factor for each block of tokens and key
+ * head (host struct of device pointers): held value 8-bit value * factor.  A
+ * block is block_tokens neighbouring tokens of a page.  Pointers and strides of
+ * k and v as in ss_kv_cache.  The factors are read and written by
+ * ss_kv_store_blocks, which makes them powers of two, 2^-40 to 2^40; the other
+ * calls take any positive ones in that range (what is outside it, or NaN, as
+ * its nearer end, NaN as 2^-40).  They need not be set before the first store. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t page_stride, token_stride, head_stride;
+  float* k_scale;       /* [num_pages, kv_heads, page_size / block_tokens], 16-byte aligned */
+  float* v_scale;
+  int32_t block_tokens; /* a power of two, 16 .. page_size */
+} ss_kv_block_cache;
+
 /* The pool and the rows' tables (host struct of device pointers).
  * Between an append and its commit only block_table entries past a row's
  * held pages are written; an append can be repeated (with other new tokens,
@@ -126,6 +142,55 @@ ss_status ss_kv_append(const ss_kv_pool* pool, const int32_t* cu_new, int32_t* s
  * back and its kv_len is 0.  seq_len: as the append wrote it. */
 ss_status ss_kv_commit(const ss_kv_pool* pool, const int32_t* seq_len, const int32_t* counts, int32_t plus,
                        const int32_t* finished);
+
+/* New tokens' keys and values (rotated, as ss_rope_store writes them) and where they go. */
+typedef struct {
+  int32_t B;              /* rows of this call, 1 .. max_rows */
+  int32_t tokens;         /* that k and v hold (those past max_tokens are not used); 0: nothing is done */
+  const void *k, *v;      /* [tokens, kv_heads, head_dim], heads contiguous; 16-byte aligned */
+  int64_t k_stride, v_stride; /* between tokens, in elements: a multiple of 8 */
+  const int32_t* cu_new;  /* [B+1] prefix sums of the rows' new tokens */
+  const int32_t* kv_len;  /* [B] tokens held before them */
+  const int32_t* seq_len; /* [B] as ss_kv_append wrote it */
+  const int32_t* block_table; /* [B, max_blocks] */
+  uint32_t* row_status;   /* [B]: bits are OR-ed in */
+  void* stream;
+  const ss_kv_plan* plan;
+} ss_store_batch;
+
+/* Stores each row's n_r = cu_new[r+1] - cu_new[r] new tokens at its positions
+ * from kv_len[r] on, as 8-bit values with a factor for each block and key head
+ * (keys and values have their own).  With amax the largest finite |x| that the
+ * call stores of a block and head, and e the least exponent in [-40, 40] with
+ * amax <= 448 * 2^e: a block whose first token the call stores gets the factor
+ * 2^e; one that it goes on in keeps the tokens before, and gets the larger of
+ * 2^e and its old factor (one that is not a power of two counts as the next).
+ * Where that is larger than the old one, the kept values are rounded to it.
+ * A value is held as x / factor, rounded to nearest, all beyond 448 and
+ * infinities as 448 with their sign, NaN as NaN.
+ * A factor does not shrink when tokens are dropped again (ss_kv_commit) until
+ * the block is begun anew.
+ * A row that the append did not serve (seq_len - kv_len is not n_r) stores
+ * nothing.  A row with a negative or decreasing count or a token past tokens or
+ * max_tokens stores nothing (SS_ST_CAPACITY), nor does one with a negative
+ * kv_len or a seq_len past its table row (SS_ST_BAD_PARAM); tokens on a page
+ * id outside the cache are left out (SS_ST_KV_PAGE).  Pages that get new
+ * tokens belong to one row. */
+ss_status ss_kv_store_blocks(const ss_store_batch* batch, const ss_kv_block_cache* cache);
+
+/* Held tokens' way back. */
+typedef struct {
+  int32_t T;              /* >= 0 */
+  const int32_t* slots;   /* [T]; a slot may appear more than once */
+  void *k, *v;            /* [T, kv_heads, head_dim], heads contiguous; 16-byte aligned */
+  int64_t k_stride, v_stride; /* between tokens, in elements: a multiple of 8 */
+  void* stream;
+  const ss_kv_plan* plan;
+} ss_load_batch;
+
+/* Keys and values held at the slots, times their factors, rounded once to the
+ * plan's dtype; a slot outside the cache (-1) gives zeros. */
+ss_status ss_kv_load_blocks(const ss_load_batch* batch, const ss_kv_block_cache* cache);
 
 /* Queries, keys and values of T tokens on their way from the projection. */
 typedef struct {
@@ -207,6 +272,12 @@ typedef struct {
  * report SS_ST_COPY_TIMEOUT, and the workspace is to be zeroed before its next
  * use. */
 ss_status ss_attend(const ss_attend_batch* batch, const ss_kv_cache* cache);
+
+/* ss_attend over a cache with a factor for each block and head, in every other
+ * respect as over an SS_E4M3 cache.  Of a row's keys, those whose weight times
+ * the factor of its values is below 2^-32 of the largest such product may count
+ * as 0 in the output. */
+ss_status ss_attend_blocks(const ss_attend_batch* batch, const ss_kv_block_cache* cache);
 
 #ifdef __cplusplus
 }

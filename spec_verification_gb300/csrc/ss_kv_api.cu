@@ -74,7 +74,7 @@ cudaError_t configure(int device, const ss::AttendKernel& k) {
     size_t smem;
   };
   static std::mutex mu;
-  static Done done[256];  // 16 kernels with at most a few sizes each; past that they are set again each time
+  static Done done[256];  // 26 kernels with at most a few sizes each; past that they are set again each time
   static int count = 0;
   const std::lock_guard<std::mutex> lock(mu);
   bool pages = false;
@@ -92,6 +92,9 @@ cudaError_t configure(int device, const ss::AttendKernel& k) {
   return e;
 }
 
+ss::AttendKernel blocks_kernel(const ss_kv_config& c, int row_tile) {
+  return c.dtype == SS_BF16 ? ss::kv_attend_bf16_blocks(c.head_dim, row_tile) : ss::kv_attend_f16_blocks(c.head_dim, row_tile);
+}
 ss::AttendKernel attend_kernel(const ss_kv_config& c, int row_tile) {
   const bool bf16 = c.dtype == SS_BF16, low = c.cache_dtype == SS_E4M3;
   return bf16 ? (low ? ss::kv_attend_bf16_e4m3(c.head_dim, row_tile) : ss::kv_attend_bf16(c.head_dim, row_tile))
@@ -101,7 +104,8 @@ ss::AttendKernel attend_kernel(const ss_kv_config& c, int row_tile) {
 // A cache as a kernel's copies see it: (part of a head, token, number of the part, head, page).  Swizzled heads come in
 // parts of at most 128 bytes; a copy of 16-bit values has all parts of 64 tokens, or one part of fewer (a smaller page),
 // so that in shared memory a tile is its parts of 64 tokens either way; one of 8-bit values always has all.
-ss_status encode(CUtensorMap* map, const ss_kv_plan* p, const ss_kv_cache* cache, void* base, bool swizzled) {
+template <class Cache>
+ss_status encode(CUtensorMap* map, const ss_kv_plan* p, const Cache* cache, void* base, bool swizzled) {
   const ss_kv_config& c = p->c;
   const bool low = c.cache_dtype == SS_E4M3;
   const cuuint32_t el = low ? 1 : 2, tokens = std::min(c.page_size, 64);
@@ -121,17 +125,41 @@ ss_status encode(CUtensorMap* map, const ss_kv_plan* p, const ss_kv_cache* cache
   return SS_OK;
 }
 
-// Pointers and strides of a cache; e4m3 factors only where the plan has them.
-ss_status check_cache(const ss_kv_plan* p, const ss_kv_cache* cache) {
+// Pointers and strides of a cache.
+ss_status check_layout(const ss_kv_plan* p, const void* k, const void* v, int64_t page_stride, int64_t token_stride, int64_t head_stride) {
   const int64_t per16 = p->c.cache_dtype == SS_E4M3 ? 16 : 8;
-  if (!cache->k || !cache->v) return fail(SS_ERR_ARG, "the cache's keys and values are required");
-  if (!aligned(cache->k, 16) || !aligned(cache->v, 16)) return fail(SS_ERR_ALIGN, "cache pointers must be 16-byte aligned");
-  for (const int64_t s : {cache->page_stride, cache->token_stride, cache->head_stride}) {
+  if (!k || !v) return fail(SS_ERR_ARG, "the cache's keys and values are required");
+  if (!aligned(k, 16) || !aligned(v, 16)) return fail(SS_ERR_ALIGN, "cache pointers must be 16-byte aligned");
+  for (const int64_t s : {page_stride, token_stride, head_stride}) {
     if (s < 1 || s > (1ll << 36)) return fail(SS_ERR_ARG, "cache strides must be in [1, 2^36] elements");
     if (s % per16 != 0) return fail(SS_ERR_ALIGN, "cache strides must be multiples of 16 bytes");
   }
+  return SS_OK;
+}
+
+// A cache with e4m3 factors only where the plan has them.
+ss_status check_cache(const ss_kv_plan* p, const ss_kv_cache* cache) {
+  const ss_status s = check_layout(p, cache->k, cache->v, cache->page_stride, cache->token_stride, cache->head_stride);
+  if (s != SS_OK) return s;
   if (p->c.cache_dtype != SS_E4M3 && (cache->k_scale || cache->v_scale))
     return fail(SS_ERR_ARG, "k_scale and v_scale belong to an SS_E4M3 cache");
+  return SS_OK;
+}
+
+// A cache with a factor for each block.
+ss_status check_blocks(const ss_kv_plan* p, const ss_kv_block_cache* cache) {
+  if (p->c.cache_dtype != SS_E4M3) return fail(SS_ERR_ARG, "factors of blocks belong to a plan with an SS_E4M3 cache");
+  const int32_t n = cache->block_tokens;
+  if (n < 16 || n > p->c.page_size || (n & (n - 1)) != 0) return fail(SS_ERR_UNSUPPORTED, "block_tokens must be a power of two in [16, page_size]");
+  if (!cache->k_scale || !cache->v_scale) return fail(SS_ERR_ARG, "k_scale and v_scale are required");
+  if (!aligned(cache->k_scale, 16) || !aligned(cache->v_scale, 16)) return fail(SS_ERR_ALIGN, "k_scale and v_scale must be 16-byte aligned");
+  return check_layout(p, cache->k, cache->v, cache->page_stride, cache->token_stride, cache->head_stride);
+}
+
+// Stride between tokens of keys or values.
+ss_status check_stride(const ss_kv_config& c, int64_t stride) {
+  if (stride < (int64_t)c.kv_heads * c.head_dim) return fail(SS_ERR_ARG, "a token stride is smaller than its heads");
+  if (stride % 8) return fail(SS_ERR_ALIGN, "token strides must be multiples of 8 elements");
   return SS_OK;
 }
 
@@ -156,6 +184,74 @@ ss::PagesParams pages_params(const ss_kv_pool* pool) {
   P.free_pages = pool->free_pages;
   P.free_count = pool->free_count;
   return P;
+}
+
+// An attention call on a cache of either kind: P has the cache's factors, `pick` gives the kernel.
+template <class Cache>
+ss_status attend(const char* name, const ss_attend_batch* b, const Cache* cache, ss_status (*check)(const ss_kv_plan*, const Cache*),
+                 ss::AttendKernel (*pick)(const ss_kv_config&, int), ss::AttendParams P) {
+  if (!b || !b->plan || !cache) return fail(SS_ERR_ARG, "batch, plan and cache are required");
+  const ss_kv_plan* p = b->plan;
+  const ss_kv_config& c = p->c;
+  if (b->B < 1 || b->B > c.max_rows) return fail(SS_ERR_ARG, "B must be in [1, max_rows]");
+  if (b->tokens < 0) return fail(SS_ERR_ARG, "tokens must be >= 0");
+  if (b->tokens == 0) return SS_OK;
+  if (!b->q || !b->cu_new || !b->seq_len || !b->block_table || !b->out || !b->row_status)
+    return fail(SS_ERR_ARG, "q, cu_new, seq_len, block_table, out and row_status are required");
+  if (!(b->scale > 0.0f) || !std::isfinite(b->scale * 1.4426951f)) return fail(SS_ERR_ARG, "scale must be positive and finite");
+  if (b->window < 0 || b->sinks < 0) return fail(SS_ERR_ARG, "window and sinks must be >= 0");
+  const int64_t wq = (int64_t)c.q_heads * c.head_dim;
+  if (b->q_stride < wq || b->out_stride < wq) return fail(SS_ERR_ARG, "a token stride is smaller than its heads");
+  if (b->q_stride % 8 || b->out_stride % 8) return fail(SS_ERR_ALIGN, "token strides must be multiples of 8 elements");
+  if (!aligned(b->q, 16) || !aligned(b->out, 16)) return fail(SS_ERR_ALIGN, "q and out must be 16-byte aligned");
+  ss_status s = check(p, cache);
+  if (s != SS_OK) return s;
+  if (!b->workspace || b->workspace_bytes < p->ws_bytes)
+    return fail(SS_ERR_WORKSPACE, "workspace missing or smaller than ss_kv_workspace_bytes()");
+  if (!aligned(b->workspace, 256)) return fail(SS_ERR_ALIGN, "workspace must be 256-byte aligned");
+  const OnDevice on(c.device);
+  CUtensorMap mk, mv;
+  const ss::AttendKernel k = pick(c, p->row_tile);
+  s = encode(&mk, p, cache, cache->k, k.swizzled);
+  if (s == SS_OK) s = encode(&mv, p, cache, cache->v, k.swizzled);
+  if (s != SS_OK) return s;
+  const int32_t longest = c.max_blocks * c.page_size;
+  P.q = b->q;
+  P.out = b->out;
+  P.lse = b->lse;
+  P.q_stride = b->q_stride;
+  P.out_stride = b->out_stride;
+  P.cu_new = b->cu_new;
+  P.seq_len = b->seq_len;
+  P.block_table = b->block_table;
+  P.row_status = b->row_status;
+  P.scale_log2 = (float)((double)b->scale * 1.4426950408889634);
+  P.B = b->B;
+  P.hkv = c.kv_heads;
+  P.group = c.q_heads / c.kv_heads;
+  P.max_blocks = c.max_blocks;
+  P.num_pages = c.num_pages;
+  P.page_shift = p->page_shift;
+  P.max_tokens = std::min(b->tokens, c.max_tokens);
+  P.window = b->window >= longest ? 0 : b->window;  // a window that reaches every token is none
+  P.sinks = P.window ? std::min(b->sinks, longest) : 0;
+  char* w = static_cast<char*>(b->workspace);
+  P.counters = reinterpret_cast<uint32_t*>(w);
+  P.part = reinterpret_cast<float*>(w + p->off_part);
+  P.ml = reinterpret_cast<float4*>(w + p->off_ml);
+  P.spin_limit = kSpin;
+  P.rows = p->row_tile;
+  P.slots = k.slots;
+  P.raw_slots = k.raw_slots;
+  P.q_bufs = k.q_bufs;
+  P.unit_cost = k.unit_cost;
+  P.tile_shift = k.tile == 64 ? 6 : 7;
+  while ((1u << P.group_shift) < (uint32_t)P.group) ++P.group_shift;
+  P.group_mul = (uint32_t)(((1ull << 32) * ((1ull << P.group_shift) - P.group)) / P.group + 1);
+  void* args[] = {&P, &mk, &mv};
+  const Range range(name);
+  const cudaError_t e = cudaLaunchKernel(k.fn, dim3(p->attend_grid), dim3(k.threads), args, k.smem, static_cast<cudaStream_t>(b->stream));
+  return e == cudaSuccess ? SS_OK : cuda_fail(e, name);
 }
 
 }  // namespace
@@ -196,6 +292,7 @@ ss_status ss_kv_plan_create(ss_kv_plan** out, const ss_kv_config* config) {
   const int row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   const ss::AttendKernel k = attend_kernel(c, row_tile);
   if (e == cudaSuccess) e = configure(c.device, k);
+  if (e == cudaSuccess && c.cache_dtype == SS_E4M3) e = configure(c.device, blocks_kernel(c, row_tile));
   if (e != cudaSuccess) return cuda_fail(e, "kernel attributes");
   ss_kv_plan* p = new (std::nothrow) ss_kv_plan();
   if (!p) return fail(SS_ERR_ARG, "out of host memory");
@@ -250,6 +347,86 @@ ss_status ss_kv_commit(const ss_kv_pool* pool, const int32_t* seq_len, const int
   const Range range("ss_kv_commit");
   const cudaError_t e = ss::kv_commit_launch(P, static_cast<cudaStream_t>(pool->stream));
   return e == cudaSuccess ? SS_OK : cuda_fail(e, "ss_kv_commit");
+}
+
+ss_status ss_kv_store_blocks(const ss_store_batch* b, const ss_kv_block_cache* cache) {
+  if (!b || !b->plan || !cache) return fail(SS_ERR_ARG, "batch, plan and cache are required");
+  const ss_kv_plan* p = b->plan;
+  const ss_kv_config& c = p->c;
+  if (b->B < 1 || b->B > c.max_rows) return fail(SS_ERR_ARG, "B must be in [1, max_rows]");
+  if (b->tokens < 0) return fail(SS_ERR_ARG, "tokens must be >= 0");
+  if (b->tokens == 0) return SS_OK;
+  if (!b->k || !b->v || !b->cu_new || !b->kv_len || !b->seq_len || !b->block_table || !b->row_status)
+    return fail(SS_ERR_ARG, "k, v, cu_new, kv_len, seq_len, block_table and row_status are required");
+  if (!aligned(b->k, 16) || !aligned(b->v, 16)) return fail(SS_ERR_ALIGN, "k and v must be 16-byte aligned");
+  ss_status s = check_stride(c, b->k_stride);
+  if (s == SS_OK) s = check_stride(c, b->v_stride);
+  if (s == SS_OK) s = check_blocks(p, cache);
+  if (s != SS_OK) return s;
+  ss::StoreParams P = {};
+  P.B = b->B;
+  P.hkv = c.kv_heads;
+  P.max_tokens = std::min(b->tokens, c.max_tokens);
+  P.max_blocks = c.max_blocks;
+  P.num_pages = c.num_pages;
+  P.page_shift = p->page_shift;
+  P.block_shift = __builtin_ctz((unsigned)cache->block_tokens);
+  P.k = b->k;
+  P.v = b->v;
+  P.k_stride = b->k_stride;
+  P.v_stride = b->v_stride;
+  P.cu_new = b->cu_new;
+  P.kv_len = b->kv_len;
+  P.seq_len = b->seq_len;
+  P.block_table = b->block_table;
+  P.row_status = b->row_status;
+  P.k_cache = cache->k;
+  P.v_cache = cache->v;
+  P.page_stride = cache->page_stride;
+  P.token_stride = cache->token_stride;
+  P.head_stride = cache->head_stride;
+  P.k_scale = cache->k_scale;
+  P.v_scale = cache->v_scale;
+  const OnDevice on(c.device);
+  const Range range("ss_kv_store_blocks");
+  const cudaError_t e = ss::kv_store_blocks_launch(P, c.dtype == SS_BF16, c.head_dim, p->sms, static_cast<cudaStream_t>(b->stream));
+  return e == cudaSuccess ? SS_OK : cuda_fail(e, "ss_kv_store_blocks");
+}
+
+ss_status ss_kv_load_blocks(const ss_load_batch* b, const ss_kv_block_cache* cache) {
+  if (!b || !b->plan || !cache) return fail(SS_ERR_ARG, "batch, plan and cache are required");
+  const ss_kv_plan* p = b->plan;
+  const ss_kv_config& c = p->c;
+  if (b->T < 0) return fail(SS_ERR_ARG, "T must be >= 0");
+  if (b->T == 0) return SS_OK;
+  if (!b->slots || !b->k || !b->v) return fail(SS_ERR_ARG, "slots, k and v are required");
+  if (!aligned(b->k, 16) || !aligned(b->v, 16)) return fail(SS_ERR_ALIGN, "k and v must be 16-byte aligned");
+  ss_status s = check_stride(c, b->k_stride);
+  if (s == SS_OK) s = check_stride(c, b->v_stride);
+  if (s == SS_OK) s = check_blocks(p, cache);
+  if (s != SS_OK) return s;
+  ss::LoadParams P = {};
+  P.T = b->T;
+  P.hkv = c.kv_heads;
+  P.page_shift = p->page_shift;
+  P.block_shift = __builtin_ctz((unsigned)cache->block_tokens);
+  P.num_slots = c.num_pages * c.page_size;
+  P.slots = b->slots;
+  P.k_cache = cache->k;
+  P.v_cache = cache->v;
+  P.page_stride = cache->page_stride;
+  P.token_stride = cache->token_stride;
+  P.head_stride = cache->head_stride;
+  P.k_scale = cache->k_scale;
+  P.v_scale = cache->v_scale;
+  P.k_out = b->k;
+  P.v_out = b->v;
+  P.k_stride = b->k_stride;
+  P.v_stride = b->v_stride;
+  const OnDevice on(c.device);
+  const Range range("ss_kv_load_blocks");
+  const cudaError_t e = ss::kv_load_blocks_launch(P, c.dtype == SS_BF16, c.head_dim, p->sms, static_cast<cudaStream_t>(b->stream));
+  return e == cudaSuccess ? SS_OK : cuda_fail(e, "ss_kv_load_blocks");
 }
 
 ss_status ss_rope_store(const ss_rope_batch* b, const ss_kv_cache* cache) {
@@ -332,71 +509,22 @@ ss_status ss_rope_frequencies(double* inv_freq, int32_t rot_dim, double base, do
 }
 
 ss_status ss_attend(const ss_attend_batch* b, const ss_kv_cache* cache) {
-  if (!b || !b->plan || !cache) return fail(SS_ERR_ARG, "batch, plan and cache are required");
-  const ss_kv_plan* p = b->plan;
-  const ss_kv_config& c = p->c;
-  if (b->B < 1 || b->B > c.max_rows) return fail(SS_ERR_ARG, "B must be in [1, max_rows]");
-  if (b->tokens < 0) return fail(SS_ERR_ARG, "tokens must be >= 0");
-  if (b->tokens == 0) return SS_OK;
-  if (!b->q || !b->cu_new || !b->seq_len || !b->block_table || !b->out || !b->row_status)
-    return fail(SS_ERR_ARG, "q, cu_new, seq_len, block_table, out and row_status are required");
-  if (!(b->scale > 0.0f) || !std::isfinite(b->scale * 1.4426951f)) return fail(SS_ERR_ARG, "scale must be positive and finite");
-  if (b->window < 0 || b->sinks < 0) return fail(SS_ERR_ARG, "window and sinks must be >= 0");
-  const int64_t wq = (int64_t)c.q_heads * c.head_dim;
-  if (b->q_stride < wq || b->out_stride < wq) return fail(SS_ERR_ARG, "a token stride is smaller than its heads");
-  if (b->q_stride % 8 || b->out_stride % 8) return fail(SS_ERR_ALIGN, "token strides must be multiples of 8 elements");
-  if (!aligned(b->q, 16) || !aligned(b->out, 16)) return fail(SS_ERR_ALIGN, "q and out must be 16-byte aligned");
-  ss_status s = check_cache(p, cache);
-  if (s != SS_OK) return s;
-  if (!b->workspace || b->workspace_bytes < p->ws_bytes)
-    return fail(SS_ERR_WORKSPACE, "workspace missing or smaller than ss_kv_workspace_bytes()");
-  if (!aligned(b->workspace, 256)) return fail(SS_ERR_ALIGN, "workspace must be 256-byte aligned");
-  const OnDevice on(c.device);
-  CUtensorMap mk, mv;
-  const ss::AttendKernel k = attend_kernel(c, p->row_tile);
-  s = encode(&mk, p, cache, cache->k, k.swizzled);
-  if (s == SS_OK) s = encode(&mv, p, cache, cache->v, k.swizzled);
-  if (s != SS_OK) return s;
-  const int32_t longest = c.max_blocks * c.page_size;
   ss::AttendParams P = {};
-  P.q = b->q;
-  P.out = b->out;
-  P.lse = b->lse;
-  P.q_stride = b->q_stride;
-  P.out_stride = b->out_stride;
-  P.cu_new = b->cu_new;
-  P.seq_len = b->seq_len;
-  P.block_table = b->block_table;
-  P.row_status = b->row_status;
-  P.k_scale = cache->k_scale;
-  P.v_scale = cache->v_scale;
-  P.scale_log2 = (float)((double)b->scale * 1.4426950408889634);
-  P.B = b->B;
-  P.hkv = c.kv_heads;
-  P.group = c.q_heads / c.kv_heads;
-  P.max_blocks = c.max_blocks;
-  P.num_pages = c.num_pages;
-  P.page_shift = p->page_shift;
-  P.max_tokens = std::min(b->tokens, c.max_tokens);
-  P.window = b->window >= longest ? 0 : b->window;  // a window that reaches every token is none
-  P.sinks = P.window ? std::min(b->sinks, longest) : 0;
-  char* w = static_cast<char*>(b->workspace);
-  P.counters = reinterpret_cast<uint32_t*>(w);
-  P.part = reinterpret_cast<float*>(w + p->off_part);
-  P.ml = reinterpret_cast<float4*>(w + p->off_ml);
-  P.spin_limit = kSpin;
-  P.rows = p->row_tile;
-  P.slots = k.slots;
-  P.raw_slots = k.raw_slots;
-  P.q_bufs = k.q_bufs;
-  P.unit_cost = k.unit_cost;
-  P.tile_shift = k.tile == 64 ? 6 : 7;
-  while ((1u << P.group_shift) < (uint32_t)P.group) ++P.group_shift;
-  P.group_mul = (uint32_t)(((1ull << 32) * ((1ull << P.group_shift) - P.group)) / P.group + 1);
-  void* args[] = {&P, &mk, &mv};
-  const Range range("ss_attend");
-  const cudaError_t e = cudaLaunchKernel(k.fn, dim3(p->attend_grid), dim3(k.threads), args, k.smem, static_cast<cudaStream_t>(b->stream));
-  return e == cudaSuccess ? SS_OK : cuda_fail(e, "ss_attend");
+  if (cache) {
+    P.k_scale = cache->k_scale;
+    P.v_scale = cache->v_scale;
+  }
+  return attend("ss_attend", b, cache, check_cache, attend_kernel, P);
+}
+
+ss_status ss_attend_blocks(const ss_attend_batch* b, const ss_kv_block_cache* cache) {
+  ss::AttendParams P = {};
+  if (cache) {
+    P.k_blocks = cache->k_scale;
+    P.v_blocks = cache->v_scale;
+    P.block_shift = cache->block_tokens > 0 ? __builtin_ctz((unsigned)cache->block_tokens) : 0;
+  }
+  return attend("ss_attend_blocks", b, cache, check_blocks, blocks_kernel, P);
 }
 
 }  // extern "C"

@@ -52,6 +52,7 @@
 #include <cfloat>
 #include <type_traits>
 
+#include "ss_kv_blocks.cuh"
 #include "ss_kv_join.cuh"
 #include "ss_stage1.cuh"
 
@@ -114,6 +115,10 @@ __device__ __forceinline__ bool done(unsigned long long* m, uint32_t parity) {
 }
 __device__ __forceinline__ void expect(unsigned long long* m, int bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(m)), "r"(bytes) : "memory");
+}
+// counts bytes that are to come without arriving
+__device__ __forceinline__ void expect_only(unsigned long long* m, int bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(m)), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, unsigned long long* m, int token, int run, int head,
                                          int page) {
@@ -210,8 +215,11 @@ __device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lead) {
 }
 
 // ------------------------------------------------------------------ shape of one instantiation
-template <class T, int D, int KEYS, bool LOW>
+// (BLOCKS: 8-bit values with a factor for each block of tokens.)
+template <class T, int D, int KEYS, bool LOW, bool BLOCKS = false>
 struct Shape {
+  static_assert(LOW || !BLOCKS, "factors belong to 8-bit values");
+  static constexpr bool kBlocks = BLOCKS;
   using Mul = typename std::conditional<LOW, __half, T>::type;  // what is multiplied: 8-bit values become f16
   static constexpr bool kLow = LOW;
   static constexpr bool kScaleQ = LOW && std::is_same<T, __nv_bfloat16>::value;
@@ -254,6 +262,10 @@ static_assert(sizeof(Control) <= kControl, "control block");
 // given back; among them is that of the values of tile t - (places + 2) / 2 at the latest, which took the weights of
 // every softmax warp.
 static_assert((kMaxSlots + kMaxRaw + 2) / 2 <= kBadTiles && (kBadTiles & (kBadTiles - 1)) == 0, "tiles ahead of the softmax");
+
+// Factors of the tiles' keys, kept as the words of `bad` are.
+using TileFactors = Factors<kBadTiles, kTile / 16>;
+static_assert(sizeof(TileFactors) <= 1024, "room for factors");
 
 // Rows of a query buffer: where there are copies, all 128.
 template <class S>
@@ -304,7 +316,7 @@ __device__ __forceinline__ uint64_t visible_keys(const AttendParams& P, int base
 // ------------------------------------------------------------------ load warp
 template <class S, class T, int D>
 __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t sq, uint32_t ring, uint32_t raw,
-                          Control& c) {
+                          Control& c, TileFactors* factors) {
   // the ring that the copies fill
   unsigned long long* const full = S::kLow ? c.raw_full : c.full;
   unsigned long long* const empty = S::kLow ? c.raw_empty : c.empty;
@@ -397,6 +409,9 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
         }
       }
     }
+    CopyFactors mine, after;  // of this lane's copy in the batch and in the next one
+    const int per_copy = 1 << (box_shift - 4);
+    auto place_of = [&](int i0) { return (tile_of(g.u, g.from + i0 + nth) * kTile + (sub << box_shift)) & page_mask; };
     bool published = false;
     auto publish = [&]() {
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -415,6 +430,10 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
         id = P.num_pages;
         atomicOr(&P.row_status[g.row], (uint32_t)SS_ST_KV_PAGE);
       }
+      if constexpr (S::kBlocks) {  // asked for a batch ahead but for a segment's first
+        if (i0 == 0) mine.fetch(P, holds(0) && !is_bad, id, g.h, place_of(0), per_copy);
+        else mine = after;
+      }
       const int n = min(batch, g.count - i0);
       for (int j = 0; j < n && !dead; ++j) {
         const int tok = (tile_of(g.u, g.from + i0 + j) * kTile + (sub << box_shift)) & page_mask;
@@ -429,17 +448,28 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
                 if ((bad_lanes >> ((j << subs_shift) + s)) & 1) bits |= groups << (s << (box_shift - 4));
               c.bad[it++ & (kBadTiles - 1)] = bits;
             }
-            expect(&full[turn.slot], kBytes);
+            if (S::kBlocks && !values) expect_only(&full[turn.slot], kBytes);
+            else expect(&full[turn.slot], kBytes);
           }
           __syncwarp();
           if (nth == j)
             for (int r = 0; r < runs; ++r)
               tma_load(copies + turn.slot * kBytes + r * S::kRun + (sub << box_shift) * (S::kLow ? D : 128), values ? mv : mk,
                        &full[turn.slot], tok, r, g.h, id);
+          if (S::kBlocks && !values) {  // the factors come with the keys
+            const int tile = (__shfl_sync(0xffffffffu, it, 0) - 1) & (kBadTiles - 1);
+            if (nth == j) mine.write(*factors, tile, sub * per_copy, per_copy);
+            __syncwarp();
+            if (lane == 0) arrive(&full[turn.slot]);
+          }
           turn.next(slots);
           asked = min(asked + 1, slots);
         }
         if (!published && !dead) publish();
+        if (S::kBlocks && j == 0) {
+          const bool there = holds(i0 + batch) && (unsigned)next < (unsigned)P.num_pages;
+          after.fetch(P, there, next, g.h, place_of(i0 + batch), per_copy);
+        }
       }
     }
     if (!published) publish();
@@ -619,8 +649,34 @@ static __device__ __noinline__ float2 large_weights(uint32_t at, int key0, float
   return make_float2(rounded, exact);
 }
 
+// The same with factors of blocks.
+template <class S, int KEYS>
+static __device__ __noinline__ float large_weights_blocks(uint32_t at, int key0, float scale, float z, uint64_t seen, const TileFactors& f, int tile) {
+  using E = Elem<typename S::Mul>;
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int i = key0; i < key0 + KEYS; i += 16) {
+    uint32_t x[16], w[8];
+    tmem_load(x, at + i);
+    const float by = factor_of(scale, f.k[tile][i >> 4]), log = f.log[tile][i >> 4];
+    float s = 0.0f;
+#pragma unroll
+    for (int n = 0; n < 16; n += 2) {
+      float y[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        y[h] = (seen >> (i + n + h)) & 1 ? ex2(__fsub_rn(__fadd_rn(__fmul_rn(__uint_as_float(x[n + h]), by), log), z)) : 0.0f;
+      w[n / 2] = E::pack(y[0], y[1]);
+      s += y[0] + y[1];
+    }
+    sum = fmaf(s, f.back[tile][i >> 4], sum);
+    tmem_store(at + i / 2, w);
+  }
+  return sum;
+}
+
 template <class S, class T, int D, int KEYS>
-__device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned char* ring, Control& c) {
+__device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned char* ring, Control& c, const TileFactors* factors) {
   using E = Elem<typename S::Mul>;
   using Out = Elem<T>;
   constexpr int kChunk = S::kLow && KEYS > 32 ? 32 : KEYS;
@@ -685,16 +741,38 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         };
         uint32_t x[kChunk];
         float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        constexpr int kGroups = S::kBlocks ? KEYS / 16 : 1;  // of this thread's keys: their factors
+        float by_k[kGroups], log_v[kGroups], back[kGroups];
+        if constexpr (S::kBlocks) {
+          const int tile = it & (kBadTiles - 1), first = key0 >> 4;
+#pragma unroll
+          for (int n = 0; n < kGroups; ++n) {
+            by_k[n] = factor_of(scale, factors->k[tile][first + n]);
+            log_v[n] = factors->log[tile][first + n];
+            back[n] = factors->back[tile][first + n];
+          }
+        }
+        float top = -INFINITY;
 #pragma unroll
         for (int at = 0; at < KEYS; at += kChunk) {
           scores(x, at);
+          if constexpr (S::kBlocks) {
 #pragma unroll
-          for (int n = 0; n < kChunk; ++n) t[n & 3] = fmaxf(t[n & 3], __uint_as_float(x[n]));
+            for (int g0 = 0; g0 < kChunk; g0 += 16) {
+#pragma unroll
+              for (int n = 0; n < 4; ++n) t[n] = fmaxf(fmaxf(__uint_as_float(x[g0 + n]), __uint_as_float(x[g0 + 4 + n])), fmaxf(__uint_as_float(x[g0 + 8 + n]), __uint_as_float(x[g0 + 12 + n])));
+              const int n = (at + g0) >> 4;
+              top = fmaxf(top, __fadd_rn(__fmul_rn(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), by_k[n]), log_v[n]));
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < kChunk; ++n) t[n & 3] = fmaxf(t[n & 3], __uint_as_float(x[n]));
+          }
         }
-        const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
+        if (!S::kBlocks) top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
         const bool grow = live && top - mx > 8.0f + E::kLift;
         if (__any_sync(0xffffffffu, grow)) {
-          const float now = grow ? (fabsf(top) > kLarge ? top : top - E::kLift) : mx;
+          const float now = grow ? (fabsf(top) > kLarge ? top : S::kBlocks ? rintf(top - E::kLift) : top - E::kLift) : mx;
           const float by = grow ? ex2(mx - now) : 1.0f;  // 0 if nothing was seen before
           mx = now;
           large = __any_sync(0xffffffffu, mx != -INFINITY && fabsf(mx) > kLarge);
@@ -718,7 +796,11 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         // below 2^-14, 2^-21 of the first tile's largest, by up to 2^-25).  To bf16 the divisor is the sum of the rounded
         // ones, so that the error of a weight that dominates its row cancels; the log-sum-exp has the sum before rounding.
         constexpr bool kTwo = std::is_same<typename S::Mul, __nv_bfloat16>::value;
-        if (large) {
+        if (S::kBlocks && large) {
+          const float sum = large_weights_blocks<S, KEYS>(lanes + b * kTile, key0, scale, z, seen, *factors, it & (kBadTiles - 1));
+          l += sum;
+          exact += sum;
+        } else if (large) {
           const float2 sums = large_weights<S, KEYS>(lanes + b * kTile, key0, scale, z, seen);
           l += sums.x;
           exact += sums.y;
@@ -728,6 +810,25 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
           if (KEYS > kChunk) scores(x, at);
           uint32_t w[kChunk / 2];
           float s0 = 0.0f, s1 = 0.0f, e0 = 0.0f, e1 = 0.0f;
+          if constexpr (S::kBlocks) {
+#pragma unroll
+            for (int g0 = 0; g0 < kChunk; g0 += 16) {
+              const int group = (at + g0) >> 4;
+              const float by = by_k[group], less = log_v[group] - z;
+              s0 = s1 = 0.0f;
+#pragma unroll
+              for (int n = g0 / 2; n < g0 / 2 + 8; ++n) {
+                const float a = ex2(fmaf(__uint_as_float(x[2 * n]), by, less)), e = ex2(fmaf(__uint_as_float(x[2 * n + 1]), by, less));
+                w[n] = E::pack(a, e);
+                s0 += a;
+                s1 += e;
+              }
+              l = fmaf(s0 + s1, back[group], l);
+            }
+            exact = l;
+            tmem_store(lanes + b * kTile + (key0 + at) / 2, w);
+            continue;
+          }
 #pragma unroll
           for (int n = 0; n < kChunk / 2; ++n) {
             const float a = ex2(fmaf(__uint_as_float(x[2 * n]), scale, -z)), e = ex2(fmaf(__uint_as_float(x[2 * n + 1]), scale, -z));
@@ -921,12 +1022,17 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
 }
 
 // ------------------------------------------------------------------ kernel
-template <class T, int D, int KEYS, bool LOW>
-__global__ void __launch_bounds__((Shape<T, D, KEYS, LOW>::kThreads), (Shape<T, D, KEYS, LOW>::kCtas))
+template <class T, int D, int KEYS, bool LOW, bool BLOCKS>
+__global__ void __launch_bounds__((Shape<T, D, KEYS, LOW, BLOCKS>::kThreads), (Shape<T, D, KEYS, LOW, BLOCKS>::kCtas))
     attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-  using S = Shape<T, D, KEYS, LOW>;
+  using S = Shape<T, D, KEYS, LOW, BLOCKS>;
   extern __shared__ unsigned char raw[];
   __shared__ Control c;
+  TileFactors* factors = nullptr;
+  if constexpr (BLOCKS) {
+    __shared__ TileFactors f;
+    factors = &f;
+  }
   // query buffers first: products read 128 rows from each of their runs, into the ring where fewer are live
   unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   unsigned char* ring = base + P.q_bufs * q_rows<S>(P) * D * 2;
@@ -967,9 +1073,9 @@ __global__ void __launch_bounds__((Shape<T, D, KEYS, LOW>::kThreads), (Shape<T, 
   if (c.range.cut.ctas == 0) {
     // no work: straight to the end
   } else if (warp < kSoftmaxWarps) {
-    softmax_warps<S, T, D, KEYS>(P, base, ring, c);
+    softmax_warps<S, T, D, KEYS>(P, base, ring, c, factors);
   } else if (warp == kLoadWarp) {
-    load_warp<S, T, D>(P, &mk, &mv, smem_u32(base), smem_u32(ring), smem_u32(raw_ring), c);
+    load_warp<S, T, D>(P, &mk, &mv, smem_u32(base), smem_u32(ring), smem_u32(raw_ring), c, factors);
   } else if (warp == kProductWarp) {
     if (lane == 0) product_thread<S, T, D>(P, smem_u32(base), smem_u32(ring), c);
     __syncwarp();
@@ -985,12 +1091,12 @@ __global__ void __launch_bounds__((Shape<T, D, KEYS, LOW>::kThreads), (Shape<T, 
 }
 
 // The kernel for `rows` query rows of a unit, its rings and shared memory.
-template <class T, int D, int KEYS, bool LOW>
+template <class T, int D, int KEYS, bool LOW, bool BLOCKS>
 AttendKernel entry(int rows) {
-  using S = Shape<T, D, KEYS, LOW>;
-  const int share = (228 * 1024 / S::kCtas - 1024 - kControl - 1024) & ~1023;  // a CTA's, without the control block
+  using S = Shape<T, D, KEYS, LOW, BLOCKS>;
+  const int share = (228 * 1024 / S::kCtas - 1024 - kControl - (BLOCKS ? 1024 : 0) - 1024) & ~1023;  // a CTA's, without the control block
   AttendKernel k;
-  k.fn = reinterpret_cast<const void*>(&attend_kernel<T, D, KEYS, LOW>);
+  k.fn = reinterpret_cast<const void*>(&attend_kernel<T, D, KEYS, LOW, BLOCKS>);
   k.threads = S::kThreads;
   k.ctas = S::kCtas;
   k.tile = kTile;
@@ -1014,11 +1120,14 @@ AttendKernel entry(int rows) {
 // With 64 columns few query rows are copied (see above); so are at most 32 of 128 columns in 8 bits, where the softmax
 // shares its issue slots with the conversion (32 x 4 rows x 8 query heads: 84 us without copies, 76 with four; 64 rows
 // with two: no gain, 98 us; in 16 bits the larger query buffer costs the ring more: 64 x 1 90 -> 103 us).
-template <class T, bool LOW>
+template <class T, bool LOW, bool BLOCKS = false>
 AttendKernel pick(int d, int rows) {
-  if (d == 64) return rows <= 32 ? entry<T, 64, 16, LOW>(rows) : rows == 64 ? entry<T, 64, 32, LOW>(rows) : entry<T, 64, kTile, LOW>(rows);
-  if (LOW && d == 128 && rows <= 32) return entry<T, 128, LOW ? 16 : kTile, LOW>(rows);
-  return d == 128 ? entry<T, 128, kTile, LOW>(rows) : entry<T, 256, kTile, LOW>(rows);
+  if (d == 64)
+    return rows <= 32    ? entry<T, 64, 16, LOW, BLOCKS>(rows)
+           : rows == 64 ? entry<T, 64, 32, LOW, BLOCKS>(rows)
+                        : entry<T, 64, kTile, LOW, BLOCKS>(rows);
+  if (LOW && d == 128 && rows <= 32) return entry<T, 128, LOW ? 16 : kTile, LOW, BLOCKS>(rows);
+  return d == 128 ? entry<T, 128, kTile, LOW, BLOCKS>(rows) : entry<T, 256, kTile, LOW, BLOCKS>(rows);
 }
 
 }  // namespace kv

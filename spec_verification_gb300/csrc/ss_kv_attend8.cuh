@@ -115,8 +115,11 @@ __device__ __forceinline__ bool any_warp(bool x) {
 }
 
 // ------------------------------------------------------------------ shape of one instantiation
-template <class T, int D>
+// (BLOCKS: a factor for each block of tokens.)
+template <class T, int D, bool BLOCKS>
 struct Shape {
+  static constexpr bool kBlocks = BLOCKS;
+  static constexpr int kFactors = BLOCKS ? 2048 : 0;         // bytes for factors
   static constexpr bool kScaleQ = std::is_same<T, __nv_bfloat16>::value;
   static_assert(D <= 128, "a head is one swizzled run");
   static constexpr int kSlot = kTile * D;                    // bytes of a key (or value) tile
@@ -126,7 +129,7 @@ struct Shape {
   static constexpr int kKG = kKeys / 16;                     // their 16-key groups
   static constexpr int kQRow = D * 2 + 16;                   // padded: rows fall into different banks
   // ring of tiles: as many as the room beside the queries and the control block holds
-  static constexpr int kFit = (kSmem - 1024 - kControl - kRows * kQRow) / kSlot;
+  static constexpr int kFit = (kSmem - 1024 - kControl - kFactors - kRows * kQRow) / kSlot;
   static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
 };
 
@@ -145,6 +148,10 @@ struct Control {
 
 static_assert(sizeof(Control) <= kControl, "control block");
 
+// Factors of a tile's keys, by their place in the ring.
+using TileFactors = Factors<kMaxSlots, kTile / 16>;
+static_assert(sizeof(TileFactors) <= 2048, "room for factors");
+
 // A place in the ring: tiles of keys and of values take turns.
 struct Turn {
   int slot = 0;
@@ -160,7 +167,7 @@ struct Turn {
 
 template <class S>
 constexpr size_t smem_bytes() {
-  return 1024 + (size_t)S::kSlots * S::kSlot + (size_t)kRows * S::kQRow + kControl;
+  return 1024 + (size_t)S::kSlots * S::kSlot + (size_t)kRows * S::kQRow + kControl + S::kFactors;
 }
 
 // ------------------------------------------------------------------ loads
@@ -177,7 +184,7 @@ __device__ __forceinline__ void expect(unsigned long long* mbar, int bytes) {
 
 template <class S>
 __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CUtensorMap* mv, unsigned char* ring, Control& c,
-                          Range k) {
+                          TileFactors* factors, Range k) {
   const int lane = threadIdx.x & 31;
   const int box_shift = min(P.page_shift, 6);            // tokens of one copy
   const int subs_shift = 7 - box_shift;                  // copies of a tile
@@ -209,6 +216,9 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
     auto holds = [&](int i0) { return i0 + nth < g.count && block_of(i0) < used; };
     auto fetch = [&](int i0) { return holds(i0) ? __ldg(table + block_of(i0)) : P.num_pages; };
     int next = fetch(0);
+    CopyFactors mine, after;  // of this lane's copy in the batch and in the next one
+    const int per_copy = 1 << (box_shift - 4);
+    auto place_of = [&](int i0) { return (tile_of(g.u, g.from + i0 + nth) * kTile + (sub << box_shift)) & page_mask; };
     for (int i0 = 0; i0 < g.count && !dead; i0 += batch) {
       int id = next;
       next = fetch(i0 + batch);
@@ -217,6 +227,10 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
       if (is_bad) {
         id = P.num_pages;
         atomicOr(&P.row_status[g.row], (uint32_t)SS_ST_KV_PAGE);
+      }
+      if constexpr (S::kBlocks) {  // asked for a batch ahead but for a segment's first
+        if (i0 == 0) mine.fetch(P, holds(0) && !is_bad, id, g.h, place_of(0), per_copy);
+        else mine = after;
       }
       const int n = min(batch, g.count - i0);
       for (int j = 0; j < n && !dead; ++j) {
@@ -232,13 +246,23 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
                 if ((bad_lanes >> ((j << subs_shift) + s)) & 1) bits |= groups << (s << (box_shift - 4));
               c.bad[turn.slot] = bits;
             }
-            expect(&c.full[turn.slot], S::kSlot);
+            if (S::kBlocks && !values) expect_only(&c.full[turn.slot], S::kSlot);
+            else expect(&c.full[turn.slot], S::kSlot);
           }
           __syncwarp();
           if (nth == j)
             tma_load(smem_u32(ring) + turn.slot * S::kSlot + (sub << box_shift) * (S::kSlot / kTile), values ? mv : mk, &c.full[turn.slot], tok, g.h, id);
+          if (S::kBlocks && !values) {  // the factors come with the keys
+            if (nth == j) mine.write(*factors, turn.slot, sub * per_copy, per_copy);
+            __syncwarp();
+            if (lane == 0) arrive(&c.full[turn.slot]);
+          }
           turn.next<S::kSlots>();
           asked = min(asked + 1, S::kSlots);
+        }
+        if (S::kBlocks && j == 0) {
+          const bool there = holds(i0 + batch) && (unsigned)next < (unsigned)P.num_pages;
+          after.fetch(P, there, next, g.h, place_of(i0 + batch), per_copy);
         }
       }
     }
@@ -276,8 +300,23 @@ static __device__ __noinline__ Scores<N> large_weights(Scores<N> x, float c0, fl
   return x;
 }
 
+// The same with factors of blocks: a pair of 8-key tiles has one.
+template <int N>
+struct GroupFactors {
+  float k[N], log[N];
+};
+template <int N>
+static __device__ __noinline__ Scores<N> large_weights_blocks(Scores<N> x, GroupFactors<N / 2> f, float c0, float z0, float c1, float z1) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      x.s[n][e] = ex2(__fsub_rn(__fadd_rn(__fmul_rn(x.s[n][e], factor_of(e < 2 ? c0 : c1, f.k[n / 2])), f.log[n / 2]), e < 2 ? z0 : z1));
+  return x;
+}
+
 template <class S, class T, int D>
-__device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsigned char* sq, Control& c) {
+__device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsigned char* sq, Control& c, const TileFactors* factors) {
   constexpr int kNT = S::kKG * 2;  // 8-key tiles of a warp
   constexpr int kOT = D / 8;       // 8-column tiles of the output
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -424,6 +463,17 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
           }
         }
       }
+      // this warp's factors, before the keys' place is given back
+      constexpr int kGroups = S::kBlocks ? S::kKG : 1;
+      float by_k[kGroups], log_v[kGroups], back[kGroups];
+      if constexpr (S::kBlocks) {
+#pragma unroll
+        for (int n = 0; n < kGroups; ++n) {
+          by_k[n] = factors->k[keys.slot][warp * S::kKG + n];
+          log_v[n] = factors->log[keys.slot][warp * S::kKG + n];
+          back[n] = factors->back[keys.slot][warp * S::kKG + n];
+        }
+      }
       __syncwarp();
       if (!held && lane == 0) arrive(&c.empty[keys.slot]);
       if (part) {
@@ -445,15 +495,27 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
         t0 = fmaxf(t0, fmaxf(s[n][0], s[n][1]));
         t1 = fmaxf(t1, fmaxf(s[n][2], s[n][3]));
       }
-      t0 *= c0;
-      t1 *= c1;
+      if constexpr (S::kBlocks) {
+        t0 = t1 = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < kGroups; ++n) {
+          const float a = fmaxf(fmaxf(s[2 * n][0], s[2 * n][1]), fmaxf(s[2 * n + 1][0], s[2 * n + 1][1]));
+          const float b = fmaxf(fmaxf(s[2 * n][2], s[2 * n][3]), fmaxf(s[2 * n + 1][2], s[2 * n + 1][3]));
+          t0 = fmaxf(t0, __fadd_rn(__fmul_rn(a, factor_of(c0, by_k[n])), log_v[n]));
+          t1 = fmaxf(t1, __fadd_rn(__fmul_rn(b, factor_of(c1, by_k[n])), log_v[n]));
+        }
+      } else {
+        t0 *= c0;
+        t1 *= c1;
+      }
       constexpr float kLift = Elem<__half>::kLift;
       if (__any_sync(0xffffffffu, t0 - mx0 > 8.0f + kLift || t1 - mx1 > 8.0f + kLift)) {
         t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
         t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
-        const float n0 = fmaxf(mx0, fabsf(t0) > kLarge ? t0 : t0 - kLift), n1 = fmaxf(mx1, fabsf(t1) > kLarge ? t1 : t1 - kLift);
+        auto lifted = [&](float t) { return fabsf(t) > kLarge ? t : S::kBlocks ? rintf(t - kLift) : t - kLift; };
+        const float n0 = fmaxf(mx0, lifted(t0)), n1 = fmaxf(mx1, lifted(t1));
         const float a0 = n0 == mx0 ? 1.0f : ex2(mx0 - n0), a1 = n1 == mx1 ? 1.0f : ex2(mx1 - n1);
         l0 *= a0;
         l1 *= a1;
@@ -475,11 +537,30 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x.s[n][e] = s[n][e];
-        x = large_weights(x, c0, z0, c1, z1);
+        if constexpr (S::kBlocks) {
+          GroupFactors<kNT / 2> f;
+#pragma unroll
+          for (int n = 0; n < kGroups; ++n) {
+            f.k[n] = by_k[n];
+            f.log[n] = log_v[n];
+          }
+          x = large_weights_blocks(x, f, c0, z0, c1, z1);
+        } else {
+          x = large_weights(x, c0, z0, c1, z1);
+        }
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][e] = x.s[n][e];
+      } else if constexpr (S::kBlocks) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+          const float a = factor_of(c0, by_k[n / 2]), b = factor_of(c1, by_k[n / 2]), u0 = log_v[n / 2] - z0, u1 = log_v[n / 2] - z1;
+          s[n][0] = ex2(fmaf(s[n][0], a, u0));
+          s[n][1] = ex2(fmaf(s[n][1], a, u0));
+          s[n][2] = ex2(fmaf(s[n][2], b, u1));
+          s[n][3] = ex2(fmaf(s[n][3], b, u1));
+        }
       } else {
 #pragma unroll
         for (int n = 0; n < kNT; ++n) {
@@ -491,8 +572,13 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
       }
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
-        l0 += s[n][0] + s[n][1];
-        l1 += s[n][2] + s[n][3];
+        if constexpr (S::kBlocks) {
+          l0 = fmaf(s[n][0] + s[n][1], back[n / 2], l0);
+          l1 = fmaf(s[n][2] + s[n][3], back[n / 2], l1);
+        } else {
+          l0 += s[n][0] + s[n][1];
+          l1 += s[n][2] + s[n][3];
+        }
       }
 
       // times the values
@@ -644,15 +730,16 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
 }
 
 // ------------------------------------------------------------------ kernel
-template <class T, int D>
-__global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas))
+template <class T, int D, bool BLOCKS>
+__global__ void __launch_bounds__(kThreads, (Shape<T, D, BLOCKS>::kCtas))
     attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-  using S = Shape<T, D>;
+  using S = Shape<T, D, BLOCKS>;
   static_assert(S::kSlots >= 4, "ring length");
   extern __shared__ unsigned char raw[];
   unsigned char* ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   unsigned char* sq = ring + S::kSlots * S::kSlot;
   Control& c = *reinterpret_cast<Control*>(sq + kRows * S::kQRow);
+  TileFactors* factors = BLOCKS ? reinterpret_cast<TileFactors*>(sq + kRows * S::kQRow + kControl) : nullptr;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < S::kSlots; ++i) {
@@ -669,22 +756,22 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas))
 
   find_range<kThreads, kWarps>(P, c.range_sums, &c.range);
   if (c.range.cut.ctas == 0) return;
-  if (warp == kWarps) load_warp<S>(P, &mk, &mv, ring, c, c.range);
-  else compute_warps<S, T, D>(P, ring, sq, c);
+  if (warp == kWarps) load_warp<S>(P, &mk, &mv, ring, c, factors, c.range);
+  else compute_warps<S, T, D>(P, ring, sq, c, factors);
 }
 
-template <class T, int D>
+template <class T, int D, bool BLOCKS>
 AttendKernel entry() {
-  using S = Shape<T, D>;
+  using S = Shape<T, D, BLOCKS>;
   // What starting and ending a unit takes, in tiles.  Measured (us): 128 columns, 128 x 1 rows of at most 3000 tokens with
   // 2, 3, 4, 5: 96, 85.5, 88.5, 91.4; 32 x 4 rows of at most 32000: 176, 154, 152.6, 152.9; 64 columns, 200 x 1 rows of at
   // most 2000 with 1, 2, 3, 4: 38.4, 34.3, 35, 36.3.
   constexpr int kUnitCost = D == 128 ? 3 : 2;
-  return {reinterpret_cast<const void*>(&attend_kernel<T, D>), kThreads, S::kSlots, 0, 1, S::kCtas, kTile, smem_bytes<S>(), kUnitCost, true};
+  return {reinterpret_cast<const void*>(&attend_kernel<T, D, BLOCKS>), kThreads, S::kSlots, 0, 1, S::kCtas, kTile, smem_bytes<S>(), kUnitCost, true};
 }
-template <class T>
+template <class T, bool BLOCKS = false>
 AttendKernel pick(int d) {
-  return d == 64 ? entry<T, 64>() : entry<T, 128>();
+  return d == 64 ? entry<T, 64, BLOCKS>() : entry<T, 128, BLOCKS>();
 }
 
 }  // namespace kv8

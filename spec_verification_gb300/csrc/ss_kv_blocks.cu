@@ -1,0 +1,298 @@
+// ss_kv_store_blocks and ss_kv_load_blocks: new tokens into an 8-bit cache with
+// a factor for each block of tokens and key head, and held tokens back out.
+//
+// A run is what one call writes of one block: consecutive new tokens of a row.
+// Its factor is the least power of two 2^e with max |x| <= 448 * 2^e, or the
+// block's old one where that is larger and tokens before the run are kept; if
+// the factor grows, the kept tokens' bytes are rounded anew.  Powers of two,
+// because the kept bytes then only lose what falls below e4m3's normal range,
+// however often a block grows, and because x / 2^e is exact, so that a value
+// is rounded once.  A whole power of two costs no precision: e4m3 has the same
+// relative step from 2^-6 to 448.
+//
+// Every value is read and written once (a block's kept tokens where its factor
+// grows): HBM bandwidth is the bound, and latency for a step's single tokens.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "ss_kv_blocks.cuh"
+#include "ss_kv_common.cuh"
+
+namespace ss {
+namespace {
+
+constexpr int kNT = 128, kWarps = kNT / 32;
+constexpr int kLoads = 8;  // 16-byte loads of a thread in flight
+
+template <class T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 of(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+  static __device__ __forceinline__ uint32_t to(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+template <>
+struct Pair<__half> {
+  static __device__ __forceinline__ float2 of(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+  static __device__ __forceinline__ uint32_t to(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+// Two values as e4m3, rounded to nearest, what passes 448 (infinities too) as 448 with its sign, NaN as NaN.
+__device__ __forceinline__ uint32_t to8(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 from8(uint32_t w) {  // of the low 16 bits
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+__device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// The least e in range with x <= c * 2^e, c = 1.75 * 2^8 (448), for finite x >= 0; without c: with x <= 2^e.
+__device__ __forceinline__ int exponent_of(float x, bool values) {
+  const uint32_t bits = __float_as_uint(x), part = bits & 0x7fffffu;
+  const int e = (int)(bits >> 23) - 127;  // (numbers below 2^-126 are far below the range)
+  return min(max(values ? e - 8 + (part > 0x600000u) : e + (part != 0u), kLowestBlock), kHighestBlock);
+}
+
+// A row of a call; n == 0: nothing to store.
+struct StoreRow {
+  int q0, n, held;
+  uint32_t status;
+};
+__device__ __forceinline__ StoreRow store_row(const StoreParams& P, int r) {
+  StoreRow w;
+  w.q0 = P.cu_new[r];
+  const int q1 = P.cu_new[r + 1];
+  w.n = q1 - w.q0;
+  w.held = P.kv_len[r];
+  w.status = 0;
+  const int len = P.seq_len[r];
+  if (w.q0 < 0 || q1 < w.q0 || q1 > P.max_tokens) {
+    w.n = 0;
+    w.status = SS_ST_CAPACITY;
+  } else if (w.held < 0 || len < 0 || len > P.max_blocks << P.page_shift) {
+    w.n = 0;
+    w.status = SS_ST_BAD_PARAM;
+  } else if (len < w.held || len - w.held != w.n) {
+    w.n = 0;  // not served by the append
+  }
+  return w;
+}
+__device__ __forceinline__ int runs_of(const StoreParams& P, const StoreRow& w) {
+  return w.n == 0 ? 0 : ((w.held + w.n - 1) >> P.block_shift) - (w.held >> P.block_shift) + 1;
+}
+
+// The group of threads that has a unit: a warp, or (large blocks) the CTA.
+template <bool WIDE>
+struct Group {
+  static constexpr int kSize = WIDE ? kNT : 32;
+  static __device__ __forceinline__ int thread() { return WIDE ? threadIdx.x : threadIdx.x & 31; }
+  static __device__ __forceinline__ float max(float x, float* room) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    if (!WIDE) return x;
+    __syncthreads();  // the last unit's maxima have been read
+    if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = x;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) x = fmaxf(x, room[w]);
+    return x;
+  }
+};
+
+// Units: (run, keys or values, head), runs in order of rows.  Every CTA counts the runs of all rows, a thread those of
+// some neighbouring ones, and its groups take the units in turn.
+template <class T, int D, bool WIDE>
+__global__ void __launch_bounds__(kNT) store_kernel(const StoreParams P) {
+  using G = Group<WIDE>;
+  __shared__ int first[kNT + 1];  // runs before those of each thread's rows
+  __shared__ float room[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (P.B + kNT - 1) / kNT;
+  {
+    int mine = 0;
+    for (int r = min(P.B, tid * per); r < min(P.B, (tid + 1) * per); ++r) {
+      const StoreRow w = store_row(P, r);
+      if (w.status && blockIdx.x == 0) atomicOr(&P.row_status[r], w.status);
+      mine += runs_of(P, w);
+    }
+    int incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += y;
+    }
+    __shared__ int sums[kWarps];
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += sums[w];
+    first[tid + 1] = before + incl;
+    if (tid == 0) first[0] = 0;
+    __syncthreads();
+  }
+  const int kinds = 2 * P.hkv, at = G::thread(), block = 1 << P.block_shift;
+  const long long units = (long long)first[kNT] * kinds, step = (long long)gridDim.x * (kNT / G::kSize);
+  constexpr int kPer = D / 8;  // 16-byte pieces of a new token's head
+  for (long long u = (long long)blockIdx.x * (kNT / G::kSize) + (WIDE ? 0 : warp); u < units; u += step) {
+    const int run = (int)(u / kinds), kind = (int)(u - (long long)run * kinds), h = kind % P.hkv;
+    const bool values = kind >= P.hkv;
+    int owner = 0;
+#pragma unroll
+    for (int s = kNT / 2; s > 0; s >>= 1)
+      if (first[owner + s] <= run) owner += s;
+    int r = owner * per, left = run - first[owner];
+    StoreRow w = store_row(P, r);
+    for (int n = runs_of(P, w); left >= n; n = runs_of(P, w)) {
+      left -= n;
+      w = store_row(P, ++r);
+    }
+    // tokens [p0, p1) of the row, in one block
+    const int blk = (w.held >> P.block_shift) + left;
+    const int p0 = max(w.held, blk << P.block_shift), p1 = min(w.held + w.n, (blk + 1) << P.block_shift);
+    const int page = P.block_table[(long long)r * P.max_blocks + (p0 >> P.page_shift)];
+    if ((unsigned)page >= (unsigned)P.num_pages) {
+      if (at == 0) atomicOr(&P.row_status[r], (uint32_t)SS_ST_KV_PAGE);
+      continue;
+    }
+    const int place = p0 & ((1 << P.page_shift) - 1), kept = place & (block - 1), count = (p1 - p0) * kPer;
+    const T* src = static_cast<const T*>(values ? P.v : P.k) + (w.q0 + p0 - w.held) * (values ? P.v_stride : P.k_stride) + h * D;
+    const long long stride = values ? P.v_stride : P.k_stride;
+    unsigned char* dst = static_cast<unsigned char*>(values ? P.v_cache : P.k_cache) + page * P.page_stride + (place - kept) * P.token_stride +
+                         h * P.head_stride;
+    float* factor = (values ? P.v_scale : P.k_scale) + ((long long)page * P.hkv + h) * (1 << (P.page_shift - P.block_shift)) + (place >> P.block_shift);
+    const float old = kept ? *factor : 0.0f;
+    auto load = [&](uint4 (&x)[kLoads], int i0) {
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) {
+        const int i = i0 + at + n * G::kSize;
+        x[n] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < count) x[n] = __ldg(reinterpret_cast<const uint4*>(src + i / kPer * stride + i % kPer * 8));
+      }
+    };
+    uint4 x[kLoads];
+    float top = 0.0f;
+    for (int i0 = 0; i0 < count; i0 += kLoads * G::kSize) {
+      load(x, i0);
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) {
+        for (const uint32_t y : {x[n].x, x[n].y, x[n].z, x[n].w}) {
+          const float2 v = Pair<T>::of(y);
+          const float a = fabsf(v.x), b = fabsf(v.y);
+          if (a < INFINITY) top = fmaxf(top, a);  // (false for NaN)
+          if (b < INFINITY) top = fmaxf(top, b);
+        }
+      }
+    }
+    top = G::max(top, room);
+    int e = exponent_of(top, true);
+    const float held = block_factor(old);
+    if (kept) e = max(e, exponent_of(held, false));
+    if (kept && held != power(e)) {
+      const float by = held * power(-e);
+      const int pieces = kept * (D / 16);
+      for (int i = at; i < pieces; i += G::kSize) {
+        uint4* line = reinterpret_cast<uint4*>(dst + (long long)(i / (D / 16)) * P.token_stride + i % (D / 16) * 16);
+        uint4 y = *line;
+        uint32_t* ys = &y.x;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const float2 a = from8(ys[n]), b = from8(ys[n] >> 16);
+          ys[n] = to8(a.x * by, a.y * by) | to8(b.x * by, b.y * by) << 16;
+        }
+        *line = y;
+      }
+    }
+    if (at == 0) *factor = power(e);
+    const float down = power(-e);
+    for (int i0 = 0; i0 < count; i0 += kLoads * G::kSize) {
+      if (count > kLoads * G::kSize) load(x, i0);
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) {
+        const int i = i0 + at + n * G::kSize;
+        if (i >= count) break;
+        const float2 a = Pair<T>::of(x[n].x), b = Pair<T>::of(x[n].y), c = Pair<T>::of(x[n].z), d = Pair<T>::of(x[n].w);
+        *reinterpret_cast<uint2*>(dst + (long long)(kept + i / kPer) * P.token_stride + i % kPer * 8) =
+            make_uint2(to8(a.x * down, a.y * down) | to8(b.x * down, b.y * down) << 16, to8(c.x * down, c.y * down) | to8(d.x * down, d.y * down) << 16);
+      }
+    }
+  }
+}
+
+// A thread: 16 values of a token and head.
+template <class T, int D>
+__global__ void __launch_bounds__(256) load_kernel(const LoadParams P) {
+  constexpr int kPer = D / 16;
+  const int per_token = P.hkv * kPer;
+  const long long items = (long long)P.T * per_token;
+  const bool values = blockIdx.y != 0;
+  const unsigned char* cache = static_cast<const unsigned char*>(values ? P.v_cache : P.k_cache);
+  const float* scale = values ? P.v_scale : P.k_scale;
+  T* out = static_cast<T*>(values ? P.v_out : P.k_out);
+  const long long stride = values ? P.v_stride : P.k_stride;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < items; i += (long long)gridDim.x * blockDim.x) {
+    const int t = (int)(i / per_token), rest = (int)(i - (long long)t * per_token), h = rest / kPer, piece = rest % kPer;
+    const int slot = P.slots[t];
+    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+    if (slot >= 0 && slot < P.num_slots) {
+      const int page = slot >> P.page_shift, place = slot & ((1 << P.page_shift) - 1);
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(cache + page * P.page_stride + place * P.token_stride + h * P.head_stride + piece * 16));
+      const float f = block_factor(__ldg(scale + ((long long)page * P.hkv + h) * (1 << (P.page_shift - P.block_shift)) + (place >> P.block_shift)));
+      auto pair = [&](uint32_t w) {
+        const float2 a = from8(w);
+        return Pair<T>::to(a.x * f, a.y * f);
+      };
+      lo = make_uint4(pair(x.x), pair(x.x >> 16), pair(x.y), pair(x.y >> 16));
+      hi = make_uint4(pair(x.z), pair(x.z >> 16), pair(x.w), pair(x.w >> 16));
+    }
+    uint4* to = reinterpret_cast<uint4*>(out + t * stride + h * D + piece * 16);
+    to[0] = lo;
+    to[1] = hi;
+  }
+}
+
+template <class T, int D>
+cudaError_t store(const StoreParams& P, int sms, cudaStream_t st) {
+  // no more CTAs than there can be units, and no more than stay on the GPU
+  const bool wide = (D << P.block_shift) > kLoads * 32 * 8;
+  const long long units = 2ll * P.hkv * (2ll * P.B + ((long long)P.max_tokens >> P.block_shift));
+  const int grid = (int)std::min<long long>(wide ? units : (units + kWarps - 1) / kWarps, 8ll * sms);
+  if (wide) store_kernel<T, D, true><<<grid, kNT, 0, st>>>(P);
+  else store_kernel<T, D, false><<<grid, kNT, 0, st>>>(P);
+  return cudaGetLastError();
+}
+template <class T, int D>
+cudaError_t load(const LoadParams& P, int sms, cudaStream_t st) {
+  const long long items = (long long)P.T * P.hkv * (D / 16);
+  const int grid = (int)std::min<long long>((items + 255) / 256, 16ll * sms);
+  load_kernel<T, D><<<dim3(grid, 2), 256, 0, st>>>(P);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t kv_store_blocks_launch(const StoreParams& P, bool bf16, int head_dim, int sms, cudaStream_t st) {
+  if (bf16)
+    return head_dim == 64    ? store<__nv_bfloat16, 64>(P, sms, st)
+           : head_dim == 128 ? store<__nv_bfloat16, 128>(P, sms, st)
+                             : store<__nv_bfloat16, 256>(P, sms, st);
+  return head_dim == 64 ? store<__half, 64>(P, sms, st) : head_dim == 128 ? store<__half, 128>(P, sms, st) : store<__half, 256>(P, sms, st);
+}
+cudaError_t kv_load_blocks_launch(const LoadParams& P, bool bf16, int head_dim, int sms, cudaStream_t st) {
+  if (bf16)
+    return head_dim == 64    ? load<__nv_bfloat16, 64>(P, sms, st)
+           : head_dim == 128 ? load<__nv_bfloat16, 128>(P, sms, st)
+                             : load<__nv_bfloat16, 256>(P, sms, st);
+  return head_dim == 64 ? load<__half, 64>(P, sms, st) : head_dim == 128 ? load<__half, 128>(P, sms, st) : load<__half, 256>(P, sms, st);
+}
+
+}  // namespace ss

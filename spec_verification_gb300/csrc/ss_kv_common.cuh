@@ -48,6 +48,30 @@ struct RopeParams {
 };
 cudaError_t kv_rope_launch(const RopeParams& P, bool bf16, bool e4m3, int head_dim, int sms, cudaStream_t st);
 
+struct StoreParams {
+  int B, hkv, max_tokens, max_blocks, num_pages, page_shift, block_shift;
+  const void *k, *v;
+  long long k_stride, v_stride;
+  const int32_t *cu_new, *kv_len, *seq_len, *block_table;
+  uint32_t* row_status;
+  void *k_cache, *v_cache;
+  long long page_stride, token_stride, head_stride;
+  float *k_scale, *v_scale;
+};
+cudaError_t kv_store_blocks_launch(const StoreParams& P, bool bf16, int head_dim, int sms, cudaStream_t st);
+
+struct LoadParams {
+  int T, hkv, page_shift, block_shift;
+  int num_slots;
+  const int32_t* slots;
+  const void *k_cache, *v_cache;
+  long long page_stride, token_stride, head_stride;
+  const float *k_scale, *v_scale;
+  void *k_out, *v_out;
+  long long k_stride, v_stride;
+};
+cudaError_t kv_load_blocks_launch(const LoadParams& P, bool bf16, int head_dim, int sms, cudaStream_t st);
+
 struct AttendParams {
   const void* q;
   void* out;
@@ -56,6 +80,8 @@ struct AttendParams {
   const int32_t *cu_new, *seq_len, *block_table;
   uint32_t* row_status;
   const float *k_scale, *v_scale;
+  const float *k_blocks, *v_blocks;  // factors of blocks [num_pages, hkv, blocks of a page] of 2^block_shift tokens, in place of those
+  int block_shift;
   float scale_log2;     // scale * log2(e)
   int B, hkv, group, max_blocks, num_pages, page_shift, max_tokens, window, sinks;
   int rows, slots, raw_slots, q_bufs;  // query rows of a unit, tiles in the rings, query buffers
@@ -79,5 +105,8 @@ AttendKernel kv_attend_bf16(int head_dim, int row_tile);       // bf16 activatio
 AttendKernel kv_attend_f16(int head_dim, int row_tile);        // f16, f16
 AttendKernel kv_attend_bf16_e4m3(int head_dim, int row_tile);  // bf16, e4m3
 AttendKernel kv_attend_f16_e4m3(int head_dim, int row_tile);   // f16, e4m3
+// the same with factors of blocks: tiles, grids and workspaces are those of the kernels above
+AttendKernel kv_attend_bf16_blocks(int head_dim, int row_tile);
+AttendKernel kv_attend_f16_blocks(int head_dim, int row_tile);
 
 }  // namespace ss

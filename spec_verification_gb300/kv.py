@@ -51,15 +51,33 @@ class AttendBatch(C.Structure):
                 ("row_status", _p), ("workspace", _p), ("workspace_bytes", C.c_size_t), ("stream", _p), ("plan", _p)]
 
 
+class BlockCache(C.Structure):
+    _fields_ = [("k", _p), ("v", _p), ("page_stride", _i64), ("token_stride", _i64), ("head_stride", _i64),
+                ("k_scale", _p), ("v_scale", _p), ("block_tokens", _i32)]
+
+
+class StoreBatch(C.Structure):
+    _fields_ = [("B", _i32), ("tokens", _i32), ("k", _p), ("v", _p), ("k_stride", _i64), ("v_stride", _i64), ("cu_new", _p), ("kv_len", _p),
+                ("seq_len", _p), ("block_table", _p), ("row_status", _p), ("stream", _p), ("plan", _p)]
+
+
+class LoadBatch(C.Structure):
+    _fields_ = [("T", _i32), ("slots", _p), ("k", _p), ("v", _p), ("k_stride", _i64), ("v_stride", _i64), ("stream", _p), ("plan", _p)]
+
+
 # The same layouts as native struct formats: packing one takes a fifth of the time that filling a ctypes structure does.
 _CACHE = struct.Struct("@PPqqqPP")
 _POOL = struct.Struct("@iiPPPPPP")
 _ROPE = struct.Struct("@iPPPqqqPPfPiifPPPqPP")
 _ATTEND = struct.Struct("@iiPqPPPfiiPqPPPNPP")
+_BLOCKS = struct.Struct("@PPqqqPPi0q")
+_STORE = struct.Struct("@iiPPqqPPPPPPP")
+_LOAD = struct.Struct("@iPPPqqPP")
 assert [_CACHE.size, _POOL.size, _ROPE.size, _ATTEND.size] == [C.sizeof(c) for c in (Cache, Pool, RopeBatch, AttendBatch)]
+assert [_BLOCKS.size, _STORE.size, _LOAD.size] == [C.sizeof(c) for c in (BlockCache, StoreBatch, LoadBatch)]
 
 EXPORTS = ["ss_kv_plan_create", "ss_kv_plan_destroy", "ss_kv_workspace_bytes", "ss_kv_append", "ss_kv_commit",
-           "ss_rope_store", "ss_rope_frequencies", "ss_attend"]
+           "ss_rope_store", "ss_rope_frequencies", "ss_attend", "ss_kv_store_blocks", "ss_kv_load_blocks", "ss_attend_blocks"]
 
 _lib = None
 
@@ -80,8 +98,10 @@ def library() -> C.CDLL:
     L.ss_kv_commit.argtypes = [_p, _p, _p, _i32, _p]
     L.ss_rope_store.argtypes = [_p, _p]
     L.ss_rope_frequencies.argtypes = [C.POINTER(C.c_double), _i32, C.c_double, C.c_double, _i32, C.c_double, C.c_double]
-    L.ss_attend.argtypes = [_p, _p]
-    for name in ("ss_kv_plan_create", "ss_kv_append", "ss_kv_commit", "ss_rope_store", "ss_rope_frequencies", "ss_attend"):
+    for name in ("ss_attend", "ss_kv_store_blocks", "ss_kv_load_blocks", "ss_attend_blocks"):
+        getattr(L, name).argtypes = [_p, _p]
+    for name in ("ss_kv_plan_create", "ss_kv_append", "ss_kv_commit", "ss_rope_store", "ss_rope_frequencies", "ss_attend",
+                 "ss_kv_store_blocks", "ss_kv_load_blocks", "ss_attend_blocks"):
         getattr(L, name).restype = C.c_int
     _lib = L
     return L
@@ -143,8 +163,8 @@ def _elsewhere(name, t, plan):
     return _bad(f"{name} is on the host: a device tensor is needed")
 
 
-def _cache(plan, k_cache, v_cache, k_scale, v_scale):
-    """k_cache and v_cache seen as [pages, page_size, kv_heads, head_dim], in any memory order of the first three."""
+def _strides(plan, k_cache, v_cache):
+    """Strides of k_cache and v_cache seen as [pages, page_size, kv_heads, head_dim], in any memory order of the first three."""
     if k_cache.shape != plan.cache_shape or v_cache.shape != plan.cache_shape:
         raise _bad(f"caches must be seen as [pages, page_size, kv_heads, head_dim] = {list(plan.cache_shape)}, got "
                    f"{list(k_cache.shape)} and {list(v_cache.shape)}")
@@ -156,6 +176,11 @@ def _cache(plan, k_cache, v_cache, k_scale, v_scale):
     st = k_cache.stride()
     if st != v_cache.stride() or st[3] != 1:
         raise _bad("both caches must have the same strides, and a head's values must be contiguous")
+    return st
+
+
+def _cache(plan, k_cache, v_cache, k_scale, v_scale):
+    st = _strides(plan, k_cache, v_cache)
     if k_scale is not None or v_scale is not None:
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is not None and (t.dtype is not torch.float32 or t.numel() != plan.kv_heads or not t.is_contiguous()):
@@ -163,6 +188,23 @@ def _cache(plan, k_cache, v_cache, k_scale, v_scale):
             if t is not None and t.get_device() != plan.device:
                 raise _elsewhere(name, t, plan)
     return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], _ptr(k_scale), _ptr(v_scale))
+
+
+def _blocks(plan, k_cache, v_cache, k_scale, v_scale):
+    """A cache with factors [pages, kv_heads, blocks of a page]."""
+    if plan.cache_dtype != "e4m3":
+        raise _bad(f"factors of blocks belong to a plan with cache_dtype e4m3, not {plan.cache_dtype}")
+    st = _strides(plan, k_cache, v_cache)
+    shape = k_scale.shape
+    if len(shape) != 3 or shape[0] != plan.num_pages or shape[1] != plan.kv_heads or shape[2] < 1 or plan.page_size % shape[2]:
+        raise _bad(f"k_scale must be [{plan.num_pages}, {plan.kv_heads}, blocks of a page], got {list(shape)}")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous():
+            raise _bad(f"{name} must be contiguous float32 {list(shape)}, got {t.dtype}, {list(t.shape)}")
+        if t.get_device() != plan.device:
+            raise _elsewhere(name, t, plan)
+    return _BLOCKS.pack(k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], k_scale.data_ptr(), v_scale.data_ptr(),
+                        plan.page_size // shape[2])
 
 
 def _tokens(name, t, heads, plan):
@@ -219,6 +261,36 @@ def ss_kv_commit(plan: Plan, block_table, kv_len, free_pages, free_count, seq_le
         native._check(code)
 
 
+def ss_kv_store_blocks(plan: Plan, k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, seq_len, cu_new, *, row_status, B=None,
+                       stream=None):
+    """ss_kv_store_blocks: k, v [tokens, kv_heads, head_dim]; caches seen as [pages, page_size, kv_heads, head_dim]; k_scale, v_scale
+    float32 [pages, kv_heads, page_size / block_tokens]; the lengths before and after the step as ss_kv_append has them."""
+    B = kv_len.shape[0] if B is None else B
+    cache = _blocks(plan, k_cache, v_cache, k_scale, v_scale)
+    ks, vs = _tokens("k", k, plan.kv_heads, plan), _tokens("v", v, plan.kv_heads, plan)
+    if k.shape[0] != v.shape[0]:
+        raise _bad("k and v must have the same number of tokens")
+    b = _STORE.pack(B, k.shape[0], k.data_ptr(), v.data_ptr(), ks, vs, _int(plan, "cu_new", cu_new, B + 1), _int(plan, "kv_len", kv_len, B),
+                    _int(plan, "seq_len", seq_len, B), _int(plan, "block_table", block_table, B * plan.max_blocks),
+                    _int(plan, "row_status", row_status, B), _stream(stream, plan), plan.handle)
+    code = _lib.ss_kv_store_blocks(b, cache)
+    if code:
+        native._check(code)
+
+
+def ss_kv_load_blocks(plan: Plan, k_cache, v_cache, k_scale, v_scale, slots, *, k_out, v_out, stream=None):
+    """ss_kv_load_blocks: the tokens held at slots into k_out, v_out [tokens, kv_heads, head_dim]."""
+    cache = _blocks(plan, k_cache, v_cache, k_scale, v_scale)
+    ks, vs = _tokens("k_out", k_out, plan.kv_heads, plan), _tokens("v_out", v_out, plan.kv_heads, plan)
+    T = slots.shape[0]
+    if k_out.shape[0] != T or v_out.shape[0] != T:
+        raise _bad("slots, k_out and v_out must have the same number of tokens")
+    code = _lib.ss_kv_load_blocks(_LOAD.pack(T, _int(plan, "slots", slots, T), k_out.data_ptr(), v_out.data_ptr(), ks, vs, _stream(stream, plan),
+                                             plan.handle), cache)
+    if code:
+        native._check(code)
+
+
 def ss_rope_store(plan: Plan, q, k, v, k_cache, v_cache, inv_freq, positions, slots, *, q_out, q_weight=None,
                   k_weight=None, eps=1e-6, interleaved=False, rope_scale=1.0, k_scale=None, v_scale=None, stream=None):
     """ss_rope_store: q, k, v, q_out [tokens, heads, head_dim]; caches seen as [pages, page_size, kv_heads, head_dim];
@@ -258,12 +330,9 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, factor: float = 1.0
     return out
 
 
-def ss_attend(plan: Plan, q, k_cache, v_cache, block_table, seq_len, cu_new, *, out, row_status, workspace, scale,
-              window=0, sinks=0, lse=None, k_scale=None, v_scale=None, B=None, stream=None):
-    """ss_attend: q, out [tokens, q_heads, head_dim]; caches seen as [pages, page_size, kv_heads, head_dim]; lse float32
-    [tokens, q_heads] or None.  A row with a token past those of q is left out."""
+def _attend(plan, q, block_table, seq_len, cu_new, out, row_status, workspace, scale, window, sinks, lse, B, stream):
+    """The batch of an attention call."""
     B = seq_len.shape[0] if B is None else B
-    cache = _cache(plan, k_cache, v_cache, k_scale, v_scale)
     qs, os = _tokens("q", q, plan.q_heads, plan), _tokens("out", out, plan.q_heads, plan)
     if out.shape[0] < q.shape[0]:
         raise _bad("out must have as many tokens as q")
@@ -274,10 +343,26 @@ def ss_attend(plan: Plan, q, k_cache, v_cache, block_table, seq_len, cu_new, *, 
     for name, t in (("workspace", workspace), ("lse", lse)):
         if t is not None and t.get_device() != plan.device:
             raise _elsewhere(name, t, plan)
-    b = _ATTEND.pack(B, q.shape[0], q.data_ptr(), qs, _int(plan, "cu_new", cu_new, B + 1), _int(plan, "seq_len", seq_len, B),
-                    _int(plan, "block_table", block_table, B * plan.max_blocks), scale, window, sinks, out.data_ptr(), os, _ptr(lse),
-                    _int(plan, "row_status", row_status, B), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                    _stream(stream, plan), plan.handle)
-    code = _lib.ss_attend(b, cache)
+    return _ATTEND.pack(B, q.shape[0], q.data_ptr(), qs, _int(plan, "cu_new", cu_new, B + 1), _int(plan, "seq_len", seq_len, B),
+                        _int(plan, "block_table", block_table, B * plan.max_blocks), scale, window, sinks, out.data_ptr(), os, _ptr(lse),
+                        _int(plan, "row_status", row_status, B), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                        _stream(stream, plan), plan.handle)
+
+
+def ss_attend(plan: Plan, q, k_cache, v_cache, block_table, seq_len, cu_new, *, out, row_status, workspace, scale,
+              window=0, sinks=0, lse=None, k_scale=None, v_scale=None, B=None, stream=None):
+    """ss_attend: q, out [tokens, q_heads, head_dim]; caches seen as [pages, page_size, kv_heads, head_dim]; lse float32
+    [tokens, q_heads] or None.  A row with a token past those of q is left out."""
+    b = _attend(plan, q, block_table, seq_len, cu_new, out, row_status, workspace, scale, window, sinks, lse, B, stream)
+    code = _lib.ss_attend(b, _cache(plan, k_cache, v_cache, k_scale, v_scale))
+    if code:
+        native._check(code)
+
+
+def ss_attend_blocks(plan: Plan, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len, cu_new, *, out, row_status, workspace, scale,
+                     window=0, sinks=0, lse=None, B=None, stream=None):
+    """ss_attend_blocks: as ss_attend, over a cache with factors k_scale, v_scale float32 [pages, kv_heads, page_size / block_tokens]."""
+    b = _attend(plan, q, block_table, seq_len, cu_new, out, row_status, workspace, scale, window, sinks, lse, B, stream)
+    code = _lib.ss_attend_blocks(b, _blocks(plan, k_cache, v_cache, k_scale, v_scale))
     if code:
         native._check(code)
