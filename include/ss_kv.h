@@ -279,6 +279,38 @@ ss_status ss_attend(const ss_attend_batch* batch, const ss_kv_cache* cache);
  * as 0 in the output. */
 ss_status ss_attend_blocks(const ss_attend_batch* batch, const ss_kv_block_cache* cache);
 
+/* Whole prompts on their way from the projection (queries and keys rotated),
+ * packed one after the other. */
+typedef struct {
+  int32_t B;              /* prompts, 1 .. max_rows */
+  int32_t tokens;         /* that q, k, v, out and lse hold (those past max_tokens are not used); 0: nothing is done */
+  const void* q;          /* [tokens, q_heads, head_dim], heads contiguous; 16-byte aligned */
+  const void *k, *v;      /* [tokens, kv_heads, head_dim] */
+  int64_t q_stride, k_stride, v_stride; /* between tokens, in elements: a multiple of 8 */
+  const int32_t* cu_seq;  /* [B+1] prefix sums of the prompts' tokens */
+  float scale;            /* of the scores, > 0 */
+  int32_t window, sinks;  /* as in ss_attend_batch */
+  void* out;              /* [tokens, q_heads, head_dim]; not q, k or v */
+  int64_t out_stride;
+  float* lse;             /* [tokens, q_heads] ln of the softmax sum, or NULL */
+  uint32_t* row_status;   /* [B]: bits are OR-ed in */
+  void* workspace;        /* as for ss_attend */
+  size_t workspace_bytes;
+  void* stream;
+  const ss_kv_plan* plan;
+} ss_prompt_batch;
+
+/* Causal attention of prompts over themselves, without a cache: a token sees
+ * those of its own prompt up to itself, within the window or among the first
+ * `sinks`; values in the plan's dtype, the rest as in ss_attend (the softmax
+ * weights are rounded to the dtype before the product with the values).  The
+ * plan's cache plays no part.  Keys and values that a token does not see never
+ * reach its result.  A prompt whose cu_seq passes tokens or max_tokens, or
+ * decreases, is left out (SS_ST_CAPACITY).  Should a wait inside the kernel
+ * run out (not expected), all prompts report SS_ST_COPY_TIMEOUT, and the
+ * workspace is to be zeroed before its next use. */
+ss_status ss_attend_prompt(const ss_prompt_batch* batch);
+
 #ifdef __cplusplus
 }
 #endif

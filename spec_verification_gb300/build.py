@@ -20,7 +20,8 @@ LIB = BUILD / "libss.so"
 SOURCES = ["ss_api.cu", "ss_stage1.cu", "ss_stage1_f32.cu", "ss_stage1_bf16.cu", "ss_stage1_exact.cu",
            "ss_stage2.cu", "ss_residual.cu", "ss_noalloc.cu", "ss_kv_api.cu", "ss_kv_pages.cu", "ss_kv_rope.cu", "ss_kv_blocks.cu",
            "ss_kv_attend_bf16.cu", "ss_kv_attend_f16.cu", "ss_kv_attend_bf16_e4m3.cu", "ss_kv_attend_f16_e4m3.cu",
-           "ss_kv_attend_bf16_blocks.cu", "ss_kv_attend_f16_blocks.cu"]
+           "ss_kv_attend_bf16_blocks.cu", "ss_kv_attend_f16_blocks.cu",
+           "ss_kv_prompt_bf16.cu", "ss_kv_prompt_f16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -5,6 +5,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <mutex>
@@ -67,14 +68,14 @@ EncodeTiled encode_tiled() {
 }
 
 // Shared-memory limits of the plans' kernels: set once per device and kernel (and size, for kernels with several).
-cudaError_t configure(int device, const ss::AttendKernel& k) {
+cudaError_t configure(int device, const void* fn, size_t smem) {
   struct Done {
     int device;
     const void* fn;
     size_t smem;
   };
   static std::mutex mu;
-  static Done done[256];  // 26 kernels with at most a few sizes each; past that they are set again each time
+  static Done done[256];  // 32 kernels with at most a few sizes each; past that they are set again each time
   static int count = 0;
   const std::lock_guard<std::mutex> lock(mu);
   bool pages = false;
@@ -82,12 +83,12 @@ cudaError_t configure(int device, const ss::AttendKernel& k) {
   for (const Done* d = done; d != done + count; ++d) {
     if (d->device != device) continue;
     pages = true;
-    if (d->fn == k.fn) most = std::max(most, d->smem);
+    if (d->fn == fn) most = std::max(most, d->smem);
   }
   cudaError_t e = pages ? cudaSuccess : ss::kv_pages_configure();
-  if (e == cudaSuccess && most < k.smem) {
-    e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
-    if (e == cudaSuccess && count < 256) done[count++] = {device, k.fn, k.smem};
+  if (e == cudaSuccess && most < smem) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && count < 256) done[count++] = {device, fn, smem};
   }
   return e;
 }
@@ -99,6 +100,10 @@ ss::AttendKernel attend_kernel(const ss_kv_config& c, int row_tile) {
   const bool bf16 = c.dtype == SS_BF16, low = c.cache_dtype == SS_E4M3;
   return bf16 ? (low ? ss::kv_attend_bf16_e4m3(c.head_dim, row_tile) : ss::kv_attend_bf16(c.head_dim, row_tile))
               : (low ? ss::kv_attend_f16_e4m3(c.head_dim, row_tile) : ss::kv_attend_f16(c.head_dim, row_tile));
+}
+
+ss::PromptKernel prompt_kernel(const ss_kv_config& c) {
+  return c.dtype == SS_BF16 ? ss::kv_prompt_bf16(c.head_dim) : ss::kv_prompt_f16(c.head_dim);
 }
 
 // A cache as a kernel's copies see it: (part of a head, token, number of the part, head, page).  Swizzled heads come in
@@ -123,6 +128,18 @@ ss_status encode(CUtensorMap* map, const ss_kv_plan* p, const Cache* cache, void
                                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SS_ERR_CUDA, "cuTensorMapEncodeTiled refused the cache's layout");
   return SS_OK;
+}
+
+// A tensor of 16-bit values as a kernel's copies see it, in swizzled lines of 64: n dimensions, strides in elements from
+// the second on.
+ss_status encode_lines(CUtensorMap* map, const void* base, int n, const cuuint64_t* dims, const int64_t* strides, const cuuint32_t* box) {
+  cuuint64_t bytes[4];
+  const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i + 1 < n; ++i) bytes[i] = (cuuint64_t)strides[i] * 2;
+  const CUresult r = encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, n, const_cast<void*>(base), dims, bytes, box, step,
+                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SS_OK : fail(SS_ERR_CUDA, "cuTensorMapEncodeTiled refused the tensor's layout");
 }
 
 // Pointers and strides of a cache.
@@ -291,8 +308,15 @@ ss_status ss_kv_plan_create(ss_kv_plan** out, const ss_kv_config* config) {
   const int64_t rows = (int64_t)c.max_new * group;
   const int row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   const ss::AttendKernel k = attend_kernel(c, row_tile);
-  if (e == cudaSuccess) e = configure(c.device, k);
-  if (e == cudaSuccess && c.cache_dtype == SS_E4M3) e = configure(c.device, blocks_kernel(c, row_tile));
+  if (e == cudaSuccess) e = configure(c.device, k.fn, k.smem);
+  if (e == cudaSuccess && c.cache_dtype == SS_E4M3) {
+    const ss::AttendKernel b = blocks_kernel(c, row_tile);
+    e = configure(c.device, b.fn, b.smem);
+  }
+  if (e == cudaSuccess) {
+    const ss::PromptKernel m = prompt_kernel(c);
+    e = configure(c.device, m.fn, m.smem);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "kernel attributes");
   ss_kv_plan* p = new (std::nothrow) ss_kv_plan();
   if (!p) return fail(SS_ERR_ARG, "out of host memory");
@@ -525,6 +549,73 @@ ss_status ss_attend_blocks(const ss_attend_batch* b, const ss_kv_block_cache* ca
     P.block_shift = cache->block_tokens > 0 ? __builtin_ctz((unsigned)cache->block_tokens) : 0;
   }
   return attend("ss_attend_blocks", b, cache, check_blocks, blocks_kernel, P);
+}
+
+ss_status ss_attend_prompt(const ss_prompt_batch* b) {
+  if (!b || !b->plan) return fail(SS_ERR_ARG, "batch and plan are required");
+  const ss_kv_plan* p = b->plan;
+  const ss_kv_config& c = p->c;
+  if (b->B < 1 || b->B > c.max_rows) return fail(SS_ERR_ARG, "B must be in [1, max_rows]");
+  if (b->tokens < 0) return fail(SS_ERR_ARG, "tokens must be >= 0");
+  if (b->tokens == 0) return SS_OK;
+  if (!b->q || !b->k || !b->v || !b->cu_seq || !b->out || !b->row_status)
+    return fail(SS_ERR_ARG, "q, k, v, cu_seq, out and row_status are required");
+  if (!(b->scale > 0.0f) || !std::isfinite(b->scale * 1.4426951f)) return fail(SS_ERR_ARG, "scale must be positive and finite");
+  if (b->window < 0 || b->sinks < 0) return fail(SS_ERR_ARG, "window and sinks must be >= 0");
+  const int64_t wq = (int64_t)c.q_heads * c.head_dim;
+  if (b->q_stride < wq || b->out_stride < wq) return fail(SS_ERR_ARG, "a token stride is smaller than its heads");
+  if (b->q_stride % 8 || b->out_stride % 8) return fail(SS_ERR_ALIGN, "token strides must be multiples of 8 elements");
+  ss_status s = check_stride(c, b->k_stride);
+  if (s == SS_OK) s = check_stride(c, b->v_stride);
+  if (s != SS_OK) return s;
+  for (const int64_t x : {b->q_stride, b->k_stride, b->v_stride})
+    if (x > (1ll << 36)) return fail(SS_ERR_ARG, "token strides must be at most 2^36 elements");
+  for (const void* x : {b->q, b->k, b->v, static_cast<const void*>(b->out)})
+    if (!aligned(x, 16)) return fail(SS_ERR_ALIGN, "q, k, v and out must be 16-byte aligned");
+  if (!b->workspace || b->workspace_bytes < p->ws_bytes)
+    return fail(SS_ERR_WORKSPACE, "workspace missing or smaller than ss_kv_workspace_bytes()");
+  if (!aligned(b->workspace, 256)) return fail(SS_ERR_ALIGN, "workspace must be 256-byte aligned");
+  const ss::PromptKernel k = prompt_kernel(c);
+  const int group = c.q_heads / c.kv_heads, d = c.head_dim;
+  ss::PromptParams P = {};
+  P.out = b->out;
+  P.lse = b->lse;
+  P.out_stride = b->out_stride;
+  P.cu = b->cu_seq;
+  P.row_status = b->row_status;
+  P.scale_log2 = std::max((float)((double)b->scale * 1.4426950408889634), FLT_MIN);
+  P.B = b->B;
+  P.hkv = c.kv_heads;
+  P.group = group;
+  P.max_tokens = std::min(b->tokens, c.max_tokens);
+  P.window = b->window >= P.max_tokens ? 0 : b->window;  // a window that reaches every token is none
+  P.sinks = P.window ? std::min(b->sinks, P.max_tokens) : 0;
+  P.heads = std::min(group, 128);
+  P.tokens = 128 / P.heads;
+  P.chunks = (group + P.heads - 1) / P.heads;
+  P.next = static_cast<unsigned long long*>(b->workspace);
+  P.ended = reinterpret_cast<uint32_t*>(P.next + 1);
+  P.spin_limit = kSpin;
+  const OnDevice on(c.device);
+  CUtensorMap mq, mk, mv;
+  // (a stride is of no matter to one token, but must be a tensor map's: no larger than 2^40 bytes)
+  const cuuint64_t q_dims[3] = {(cuuint64_t)d, (cuuint64_t)c.q_heads, (cuuint64_t)b->tokens};
+  const int64_t q_strides[2] = {d, b->q_stride};
+  const cuuint32_t q_box[3] = {64, (cuuint32_t)P.heads, (cuuint32_t)P.tokens};
+  const cuuint64_t dims[4] = {64, (cuuint64_t)b->tokens, (cuuint64_t)d / 64, (cuuint64_t)c.kv_heads};
+  const int64_t k_strides[3] = {b->k_stride, 64, d}, v_strides[3] = {b->v_stride, 64, d};
+  const cuuint32_t box[4] = {64, 128, (cuuint32_t)std::min(d, 128) / 64, 1};
+  s = encode_lines(&mq, b->q, 3, q_dims, q_strides, q_box);
+  if (s == SS_OK) s = encode_lines(&mk, b->k, 4, dims, k_strides, box);
+  if (s == SS_OK) s = encode_lines(&mv, b->v, 4, dims, v_strides, box);
+  if (s != SS_OK) return s;
+  // a CTA to an SM, but no more than there can be units
+  const int64_t per = (int64_t)k.tiles * P.tokens, units = ((P.max_tokens + per - 1) / per + b->B) * P.hkv * P.chunks;
+  const int grid = (int)std::min<int64_t>(p->sms, units);
+  void* args[] = {&P, &mq, &mk, &mv};
+  const Range range("ss_attend_prompt");
+  const cudaError_t e = cudaLaunchKernel(k.fn, dim3(grid), dim3(k.threads), args, k.smem, static_cast<cudaStream_t>(b->stream));
+  return e == cudaSuccess ? SS_OK : cuda_fail(e, "ss_attend_prompt");
 }
 
 }  // extern "C"

@@ -109,4 +109,25 @@ AttendKernel kv_attend_f16_e4m3(int head_dim, int row_tile);   // f16, e4m3
 AttendKernel kv_attend_bf16_blocks(int head_dim, int row_tile);
 AttendKernel kv_attend_f16_blocks(int head_dim, int row_tile);
 
+struct PromptParams {
+  void* out;
+  float* lse;
+  long long out_stride;
+  const int32_t* cu;
+  uint32_t* row_status;
+  float scale_log2;
+  int B, hkv, group, max_tokens, window, sinks;
+  int heads, tokens, chunks;   // query heads and tokens of a tile of rows, tiles that a key head's query heads take
+  unsigned long long* next;    // units handed out beyond the first of each CTA
+  uint32_t* ended;             // CTAs that have ended
+  uint32_t spin_limit;
+};
+struct PromptKernel {
+  const void* fn;
+  int threads, tiles;  // tiles of query rows of a unit
+  size_t smem;
+};
+PromptKernel kv_prompt_bf16(int head_dim);
+PromptKernel kv_prompt_f16(int head_dim);
+
 }  // namespace ss

@@ -1,0 +1,764 @@
+// ss_attend_prompt: causal attention of packed prompts over themselves, on the
+// 5th-generation tensor cores.
+//
+// Mathematics.  As in ss_kv_attend.cuh: one pass over the keys that a query
+// sees, o = sum_t w_t v_t / sum_t w_t with w_t = 2^(c q.k_t - m), where m is
+// near the row's largest exponent and moves only when a weight would pass 2^8.
+//
+// What bounds it.  4 * head_dim operations for each pair of query and key: at
+// prompts of some thousand tokens the tensor pipe.  A tile of 128 query rows
+// and 128 keys takes it 4 * head_dim * 2 cycles for S = Q K^T and O += P V,
+// and the 128 threads that weigh it about as long, so two tiles of rows take
+// turns: while one is weighed the other is multiplied.
+//
+// Query rows.  The heads that share a key head lie next to each other in a
+// tile: `heads` of them for each of `tokens` tokens (heads * tokens <= 128), so
+// short prompts fill tiles and keys are loaded once for all.  A unit is
+// (prompt, key head, part of its query heads, TILES tiles of tokens) over the
+// keys from the first that its first token sees to its last token.  Units are
+// handed out by a counter, those of a prompt from its end (the longest) on.
+//
+// A CTA's warps:
+//  - load: takes units, publishes them, runs the ring of key and value tiles
+//    (TMA) and brings their queries (TMA; a box of heads by tokens).
+//  - product: one thread issues tcgen05.mma.
+//  - softmax: four warps to a tile of rows; a thread owns a row (a lane of
+//    tensor memory), reads its 128 scores, writes its weights over them.
+//  - guard: two warps look at every tile of values before the products do.  In
+//    one that not every row sees in full, values that no row sees become zeros
+//    (0 x NaN must not reach a sum), and if one that only some rows see is not
+//    finite, the tile is added key by key by the softmax warps.
+// Tensor memory: scores of two tiles at 0 and 128, outputs from 256 on.  With
+// TILES == 1 (256 columns, whose output fills the rest, or little work) the two
+// are tiles of keys in turn.
+#pragma once
+
+#include <algorithm>
+
+#include "ss_kv_attend.cuh"
+
+namespace ss {
+namespace kv {
+namespace prompt {
+
+constexpr int kKeys = 128;       // keys of a tile
+constexpr int kMaxSlots = 8;
+constexpr int kGuardWarps = 2;
+
+template <class T_, int D_, int TILES_>
+struct Shape {
+  using T = T_;
+  static constexpr int D = D_, TILES = TILES_;
+  static constexpr int kSoftmax = 4 * TILES;                  // warps
+  static constexpr int kLoad = kSoftmax, kProduct = kSoftmax + 1, kGuard = kSoftmax + 2;
+  static constexpr int kThreads = 32 * (kGuard + kGuardWarps);
+  static constexpr int kWide = D < 128 ? D : 128;             // columns of a slot
+  static constexpr int kHalves = D / kWide;                   // slots of a tile
+  static constexpr int kRun = kKeys * 128;                    // bytes of 64 columns of 128 rows
+  static constexpr int kSlot = kWide / 64 * kRun;
+  static constexpr int kQ = D / 64 * kRun;                    // bytes of the queries of a tile of rows
+  static constexpr int kOut = 256;
+  // slots: as many as there is room for beside the queries and the control block
+  static constexpr int kFit = (227 * 1024 - 1024 - 2048 - TILES * kQ) / kSlot;
+  static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
+  static constexpr int kSmem = 1024 + TILES * kQ + kSlots * kSlot;
+  static constexpr uint32_t kCommon = 1u << 4 | Elem<T>::kFormat << 7 | Elem<T>::kFormat << 10 | (128u >> 4) << 24;
+  static constexpr uint32_t kScores = kCommon | (kKeys >> 3) << 17;
+  static constexpr uint32_t kValues = kCommon | 1u << 16 | (uint32_t)(kWide >> 3) << 17;
+  static_assert(kSlots >= 2 * kHalves + 1, "ring length");
+  static_assert(kOut + TILES * D <= 512, "tensor memory");
+};
+
+struct Unit {
+  int row, q0, n;            // prompt, its first token and their number
+  int t0, h, chunk;          // first token of the unit in its prompt, key head, part of the query heads
+  int sink, first, tiles;    // key tiles: `sink` from 0, then from `first` on; 0 tiles: the end
+  int live;                  // tiles of rows that have tokens
+  int of_first;              // key tiles of the first tile of rows (the last one has all)
+  int pos1;                  // last token of the unit
+};
+__device__ __forceinline__ int base_of(const Unit& u, int i) { return (i < u.sink ? i : i - u.sink + u.first) * kKeys; }
+__device__ __forceinline__ int tiles_of(const Unit& u, int r) { return r + 1 < u.live ? u.of_first : r < u.live ? u.tiles : 0; }
+// Does some live row of the unit not see all keys of the tile at `base`?
+__device__ __forceinline__ bool cuts(const PromptParams& P, const Unit& u, int base) {
+  return base + kKeys - 1 > u.t0 || (P.window > 0 && base <= u.pos1 - P.window && base > P.sinks - kKeys);
+}
+
+struct Control {
+  unsigned long long full[kMaxSlots], empty[kMaxSlots];  // copies landed; products done
+  // Values looked at, by their number in the CTA's run of slots of values (not by their place in the ring, which may have
+  // held keys before): number n + kMaxSlots is copied only when number n has been multiplied.
+  unsigned long long ready[kMaxSlots];
+  unsigned long long seg_full[2], seg_empty[2];
+  unsigned long long q_full[2], q_free[2];
+  unsigned long long s_full[2], p_full[2], pv_done[2];  // scores there; weights there; added to the output
+  unsigned long long o_free[2];
+  unsigned long long drained;
+  Unit unit[2];
+  int slow[kMaxSlots][kGuardWarps];
+  uint32_t tmem;
+};
+static_assert(sizeof(Control) <= 1024, "control block");
+
+// ------------------------------------------------------------------ units
+// Walks the prompts with a warp: where unit `u` (in order) is.
+struct Cursor {
+  int row = 0;           // first of the 32 prompts looked at
+  long long before = 0;  // units before it
+  // false: past the last one
+  template <class S>
+  __device__ __forceinline__ bool find(const PromptParams& P, long long u, Unit& g) {
+    const int lane = threadIdx.x & 31, per = S::TILES * P.tokens, kinds = P.hkv * P.chunks;
+    for (; row < P.B; row += 32) {
+      int q0 = 0, n = 0;
+      if (row + lane < P.B) {
+        q0 = P.cu[row + lane];
+        const int q1 = P.cu[row + lane + 1];
+        n = q0 < 0 || q1 < q0 || q1 > P.max_tokens ? 0 : q1 - q0;
+      }
+      const long long mine = (long long)((n + per - 1) / per) * kinds;
+      long long incl = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, before + incl > u);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        const long long idx = u - before - __shfl_sync(0xffffffffu, incl - mine, at);
+        g.row = row + at;
+        g.q0 = __shfl_sync(0xffffffffu, q0, at);
+        g.n = __shfl_sync(0xffffffffu, n, at);
+        const int tile = (g.n + per - 1) / per - 1 - (int)(idx / kinds), kind = (int)(idx % kinds);
+        g.t0 = tile * per;
+        g.h = kind / P.chunks;
+        g.chunk = kind % P.chunks;
+        g.pos1 = min(g.n, g.t0 + per) - 1;
+        g.live = (g.pos1 - g.t0) / P.tokens + 1;
+        g.first = P.window > 0 ? max(0, g.t0 - P.window + 1) / kKeys : 0;
+        g.sink = P.window > 0 ? min((P.sinks + kKeys - 1) / kKeys, g.first) : 0;
+        g.tiles = g.sink + g.pos1 / kKeys - g.first + 1;
+        g.of_first = g.sink + min(g.pos1, g.t0 + P.tokens - 1) / kKeys - g.first + 1;
+        return true;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return false;
+  }
+};
+
+// A wait ran out (not expected): which rows it concerns is not known here, so all report it.
+static __device__ __noinline__ void report_all(const PromptParams& P) {
+  for (int r = threadIdx.x & 31; r < P.B; r += 32) atomicOr(&P.row_status[r], (uint32_t)SS_ST_COPY_TIMEOUT);
+}
+
+// ------------------------------------------------------------------ load warp
+template <class S>
+__device__ void load_warp(const PromptParams& P, const CUtensorMap* mq, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t sq, uint32_t ring,
+                          Control& c) {
+  const int lane = threadIdx.x & 31;
+  Turn turn;
+  int asked = 0;
+  uint32_t q_units[2] = {0, 0};  // query tiles brought, by tile of rows
+  bool dead = false;
+  auto wait = [&](unsigned long long* m, uint32_t parity) {
+    if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(m, parity, P.spin_limit, 0u));
+  };
+  Cursor cursor;
+  Unit g;
+  long long u = blockIdx.x;
+  int sg = 0;
+  bool more = true;
+  while (more && !dead) {
+    more = cursor.template find<S>(P, u, g);
+    if (sg >= 2) wait(&c.seg_empty[sg & 1], ((sg >> 1) & 1) ^ 1);
+    if (dead) break;
+    if (!more) g.tiles = g.live = 0;
+    if (lane == 0) {
+      c.unit[sg & 1] = g;
+      arrive(&c.seg_full[sg & 1]);
+    }
+    __syncwarp();
+    if (!more) break;
+    unsigned long long next = 0;
+    if (lane == 0) next = atomicAdd(P.next, 1ull);  // looked at after this unit's loads
+    auto slot = [&](bool values, int i, int half) {
+      wait(&c.empty[turn.slot], turn.parity ^ 1);
+      if (dead) return;
+      if (lane == 0) {
+        expect(&c.full[turn.slot], S::kSlot);
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                ring + turn.slot * S::kSlot),
+            "l"(values ? mv : mk), "r"(0), "r"(g.q0 + base_of(g, i)), "r"(half * (S::kWide / 64)), "r"(g.h), "r"(smem_u32(&c.full[turn.slot]))
+            : "memory");
+      }
+      __syncwarp();
+      turn.next(S::kSlots);
+      asked = min(asked + 1, S::kSlots);
+    };
+    for (int i = 0; i < g.tiles && !dead; ++i) {
+      for (int half = 0; half < S::kHalves; ++half) slot(false, i, half);
+      if (i == 0) {
+#pragma unroll
+        for (int r = 0; r < S::TILES; ++r) {
+          if (r >= g.live || dead) continue;
+          if (q_units[r] > 0) wait(&c.q_free[r], (q_units[r] - 1) & 1);
+          if (dead) continue;
+          ++q_units[r];
+          if (lane == 0) {
+            expect(&c.q_full[r], P.heads * P.tokens * S::D * 2);
+            for (int run = 0; run < S::D / 64; ++run)
+              asm volatile(
+                  "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                      sq + r * S::kQ + run * S::kRun),
+                  "l"(mq), "r"(run * 64), "r"(g.h * P.group + g.chunk * P.heads), "r"(g.q0 + g.t0 + r * P.tokens), "r"(smem_u32(&c.q_full[r]))
+                  : "memory");
+          }
+          __syncwarp();
+        }
+      }
+      for (int half = 0; half < S::kHalves; ++half) slot(true, i, half);
+    }
+    u = (long long)gridDim.x + (long long)__shfl_sync(0xffffffffu, next, 0);
+    ++sg;
+  }
+  // no copy may be in flight when the CTA ends (all have landed unless a wait ran out)
+  for (; asked > 0; --asked) {
+    if (--turn.slot < 0) {
+      turn.slot = S::kSlots - 1;
+      turn.parity ^= 1;
+    }
+    mbar_wait(&c.full[turn.slot], turn.parity, kDrainPolls, 0u);
+  }
+#pragma unroll
+  for (int r = 0; r < S::TILES; ++r)
+    if (q_units[r] > 0) mbar_wait(&c.q_full[r], (q_units[r] - 1) & 1, kDrainPolls, 0u);
+  if (dead) report_all(P);
+}
+
+// ------------------------------------------------------------------ guard warps
+template <class S>
+__device__ void guard_warps(const PromptParams& P, unsigned char* ring, Control& c) {
+  const int tid = threadIdx.x - 32 * S::kGuard, lane = tid & 31;
+  if (blockIdx.x == 0) {  // prompts whose prefix sums are no good
+    for (int r = tid; r < P.B; r += 32 * kGuardWarps) {
+      const int q0 = P.cu[r], q1 = P.cu[r + 1];
+      if (q0 < 0 || q1 < q0 || q1 > P.max_tokens) atomicOr(&P.row_status[r], (uint32_t)SS_ST_CAPACITY);
+    }
+  }
+  using E = Elem<typename S::T>;
+  Turn turn;
+  uint32_t nth = 0;  // slots of values so far
+  bool dead = false;
+  auto wait = [&](unsigned long long* m, uint32_t parity) {
+    if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(m, parity, P.spin_limit, 0u));
+  };
+  bool more = true;
+  for (int sg = 0; more; ++sg) {
+    wait(&c.seg_full[sg & 1], (sg >> 1) & 1);
+    if (dead) break;
+    const Unit u = c.unit[sg & 1];
+    more = u.tiles > 0;
+    for (int i = 0; i < u.tiles && !dead; ++i) {
+      for (int half = 0; half < S::kHalves; ++half) turn.next(S::kSlots);  // the keys
+      const int base = base_of(u, i);
+      const bool cut = cuts(P, u, base);
+      for (int half = 0; half < S::kHalves; ++half, ++nth) {
+        wait(&c.full[turn.slot], turn.parity);
+        if (dead) break;
+        if (cut) {
+          uint32_t wild = 0;  // bits 15 and 31: an exponent of ones, plus one, carries into the sign's place
+          constexpr uint32_t kOnes = E::kExponent * 0x10001u, kOne = kOnes & ~(kOnes << 1);
+          for (int in = tid; in < kKeys; in += 32 * kGuardWarps) {
+            const int key = base + in;
+            const bool some = key <= u.pos1 && (P.window <= 0 || key > u.t0 - P.window || key < P.sinks);
+            const bool all = key <= u.t0 && (P.window <= 0 || key > u.pos1 - P.window || key < P.sinks);
+            if (all) continue;
+#pragma unroll
+            for (int run = 0; run < S::kWide / 64; ++run) {
+              uint4* line = reinterpret_cast<uint4*>(ring + turn.slot * S::kSlot + run * S::kRun + in * 128);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {  // (neighbouring lines in another order: other banks)
+                if (!some) {
+                  line[(x + tid) & 7] = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                  const uint4 y = line[(x + tid) & 7];
+                  for (const uint32_t w : {y.x, y.y, y.z, y.w}) wild |= (w & kOnes) + kOne;
+                }
+              }
+            }
+          }
+          const bool slow = __any_sync(0xffffffffu, (wild & 0x80008000u) != 0);
+          if (lane == 0) c.slow[nth % kMaxSlots][tid >> 5] = slow;
+          proxy_fence();
+        } else if (lane == 0) {
+          c.slow[nth % kMaxSlots][tid >> 5] = 0;
+        }
+        __syncwarp();
+        if (lane == 0) arrive(&c.ready[nth % kMaxSlots]);
+        turn.next(S::kSlots);
+      }
+    }
+    if (lane == 0) arrive(&c.seg_empty[sg & 1]);
+  }
+  if (dead) report_all(P);
+}
+
+// Is the tile with slots of values from number n on one to be added key by key?
+template <class S>
+__device__ __forceinline__ bool is_slow(const Control& c, uint32_t n) {
+  int any = 0;
+#pragma unroll
+  for (int half = 0; half < S::kHalves; ++half) {
+#pragma unroll
+    for (int w = 0; w < kGuardWarps; ++w) any |= c.slow[(n + half) % kMaxSlots][w];
+  }
+  return any != 0;
+}
+__device__ __forceinline__ uint32_t parity_of(uint32_t n) { return (n / kMaxSlots) & 1; }
+
+// ------------------------------------------------------------------ product thread
+template <class S>
+__device__ void product_thread(const PromptParams& P, uint32_t sq, uint32_t ring, Control& c) {
+  const uint32_t tmem = c.tmem;
+  bool dead = false;
+  auto wait = [&](unsigned long long* m, uint32_t parity) {
+    if (!dead) dead = !mbar_wait(m, parity, P.spin_limit, 0u);
+  };
+  Turn at;                                             // slots of the unit's first tile
+  uint32_t nth = 0;                                    // slots of values before the unit
+  uint32_t scored[2] = {0, 0}, added[2] = {0, 0};      // uses of the two score buffers
+  uint32_t q_units[2] = {0, 0}, o_units[2] = {0, 0};   // units by tile of rows
+  bool more = true;
+  for (int sg = 0; more && !dead; ++sg) {
+    wait(&c.seg_full[sg & 1], (sg >> 1) & 1);
+    if (dead) break;
+    const Unit u = c.unit[sg & 1];
+    more = u.tiles > 0;
+    if (!more) break;
+    Turn keys = at, values = at;  // slots of the tile whose scores, and whose products, come next (for the first tile of rows)
+    for (int half = 0; half < S::kHalves; ++half) values.next(S::kSlots);
+    auto skip = [&](Turn& t) {
+      for (int n = 0; n < 2 * S::kHalves; ++n) t.next(S::kSlots);
+    };
+    // scores of tile i of rows r, into the buffer b
+    auto scores = [&](int r, int b, int i, Turn t) {
+      if (i == 0) wait(&c.q_full[r], q_units[r] & 1);
+      if (scored[b] > 0) wait(&c.pv_done[b], (scored[b] - 1) & 1);  // its weights are in the same columns
+      ++scored[b];
+#pragma unroll
+      for (int half = 0; half < S::kHalves; ++half) {
+        wait(&c.full[t.slot], t.parity);
+        if (dead) return;
+        fence_after();
+#pragma unroll
+        for (int k = 0; k < S::kWide / 16; ++k)
+          mma_ss(tmem + b * kKeys, operand(sq + r * S::kQ + (half * (S::kWide / 64) + (k >> 2)) * S::kRun + (k & 3) * 32, 0),
+                 operand(ring + t.slot * S::kSlot + (k >> 2) * S::kRun + (k & 3) * 32, 0), S::kScores, half + k != 0);
+        if (r + 1 == u.live) commit(&c.empty[t.slot]);
+        t.next(S::kSlots);
+      }
+      commit(&c.s_full[b]);
+      if (i + 1 == tiles_of(u, r)) {
+        commit(&c.q_free[r]);
+        ++q_units[r];
+      }
+    };
+    auto products = [&](int r, int b, int i, Turn t) {
+      if (i == 0) {
+        if (o_units[r] > 0) wait(&c.o_free[r], (o_units[r] - 1) & 1);
+        ++o_units[r];
+      }
+      Turn s = t;
+      const uint32_t n = nth + i * S::kHalves;
+#pragma unroll
+      for (int half = 0; half < S::kHalves; ++half) {
+        wait(&c.full[s.slot], s.parity);
+        wait(&c.ready[(n + half) % kMaxSlots], parity_of(n + half));
+        s.next(S::kSlots);
+      }
+      wait(&c.p_full[b], added[b] & 1);
+      ++added[b];
+      if (dead) return;
+      fence_after();
+      const bool slow = cuts(P, u, base_of(u, i)) && is_slow<S>(c, n);
+#pragma unroll
+      for (int half = 0; half < S::kHalves; ++half) {
+        if (!slow) {
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            mma_ts(tmem + S::kOut + r * S::D + half * S::kWide, tmem + b * kKeys + k * 8, operand(ring + t.slot * S::kSlot + k * 2048, S::kRun),
+                   S::kValues, i != 0 || k != 0);
+        }
+        if (r + 1 == u.live) commit(&c.empty[t.slot]);
+        t.next(S::kSlots);
+      }
+      commit(&c.pv_done[b]);
+    };
+    if constexpr (S::TILES == 2) {
+      for (int r = 0; r < u.live; ++r) scores(r, r, 0, keys);
+      skip(keys);
+      for (int i = 0; i < u.tiles && !dead; ++i) {
+        for (int r = 0; r < u.live && !dead; ++r) {
+          const int n = tiles_of(u, r);
+          if (i < n) products(r, r, i, values);
+          if (i + 1 < n && !dead) scores(r, r, i + 1, keys);
+        }
+        skip(keys);
+        skip(values);
+      }
+    } else {
+      uint32_t b = (scored[0] + scored[1]) & 1, d = b;
+      for (int i = 0; i < 2 && i < u.tiles && !dead; ++i) {
+        scores(0, b, i, keys);
+        b ^= 1;
+        skip(keys);
+      }
+      for (int i = 0; i < u.tiles && !dead; ++i) {
+        products(0, d, i, values);
+        d ^= 1;
+        skip(values);
+        if (i + 2 < u.tiles && !dead) {
+          scores(0, b, i + 2, keys);
+          b ^= 1;
+          skip(keys);
+        }
+      }
+    }
+    for (int i = 0; i < u.tiles; ++i) skip(at);
+    nth += u.tiles * S::kHalves;
+    if (!dead) arrive(&c.seg_empty[sg & 1]);
+  }
+  // nothing may be in flight when tensor memory is given back
+  commit(&c.drained);
+  mbar_wait(&c.drained, 0, kDrainPolls, 0u);
+}
+
+// ------------------------------------------------------------------ softmax warps
+__device__ __forceinline__ void tmem_ask(uint32_t (&r)[32], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+        "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at)
+      : "memory");
+}
+
+// Which keys of a tile a row sees, by their number in it: [0, end) but for [sinks, start).
+struct Seen {
+  int end, start, sinks;
+  __device__ __forceinline__ bool operator()(int n) const { return n < end && (n >= start || n < sinks); }
+};
+
+// A row's weights of one tile where m is large (see ss_kv_attend.cuh), over its scores; returns their sum as rounded and as
+// they are.
+template <class E, bool TWO>
+static __device__ __noinline__ float2 large_weights(uint32_t at, float scale, float z, Seen sees) {
+  float rounded = 0.0f, exact = 0.0f;
+#pragma unroll 1
+  for (int i = 0; i < kKeys; i += 16) {
+    uint32_t x[16], w[8];
+    tmem_load(x, at + i);
+#pragma unroll
+    for (int n = 0; n < 16; n += 2) {
+      float y[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) y[h] = sees(i + n + h) ? ex2(__fsub_rn(__fmul_rn(__uint_as_float(x[n + h]), scale), z)) : 0.0f;
+      w[n / 2] = E::pack(y[0], y[1]);
+      const float2 r = TWO ? E::unpack(w[n / 2]) : make_float2(y[0], y[1]);
+      rounded += r.x + r.y;
+      exact += y[0] + y[1];
+    }
+    tmem_store(at + i / 2, w);
+  }
+  return make_float2(rounded, exact);
+}
+
+// Adds a tile whose values are not all finite to the output, key by key and only for the rows that see it.
+template <class S>
+static __device__ __noinline__ void add_by_key(uint32_t scores, uint32_t out, const unsigned char* ring, Turn turn, Seen sees, bool first) {
+  using E = Elem<typename S::T>;
+#pragma unroll 1
+  for (int half = 0; half < S::kHalves; ++half) {
+    const unsigned char* values = ring + turn.slot * S::kSlot;
+    turn.next(S::kSlots);
+#pragma unroll 1
+    for (int d = 0; d < S::kWide; d += 32) {
+      uint32_t o[32];
+      if (!first) tmem_load(o, out + half * S::kWide + d);
+      float acc[32];
+#pragma unroll
+      for (int n = 0; n < 32; ++n) acc[n] = first ? 0.0f : __uint_as_float(o[n]);
+#pragma unroll 1
+      for (int n = 0; n < kKeys; ++n) {
+        uint32_t pair[1];
+        tmem_load(pair, scores + (n >> 1));
+        const float2 ws = E::unpack(pair[0]);
+        const float wt = n & 1 ? ws.y : ws.x;
+        const unsigned char* line = values + (d >> 6) * S::kRun + n * 128;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 y = *reinterpret_cast<const uint4*>(line + ((((d >> 3) & 7) + q) ^ (n & 7)) * 16);
+          const uint32_t ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const float2 v = E::unpack(ys[h]);
+            if (sees(n)) {
+              acc[q * 8 + h * 2] = fmaf(wt, v.x, acc[q * 8 + h * 2]);
+              acc[q * 8 + h * 2 + 1] = fmaf(wt, v.y, acc[q * 8 + h * 2 + 1]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(acc[n]);
+      tmem_store(out + half * S::kWide + d, o);
+    }
+  }
+  store_wait();
+}
+
+template <class S>
+__device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, Control& c) {
+  using T = typename S::T;
+  using E = Elem<T>;
+  constexpr int D = S::D;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = warp >> 2;
+  const int m = threadIdx.x & 127;                                       // row of the tile
+  const uint32_t lanes = c.tmem + ((uint32_t)(warp & 3) << 21);          // this warp's lanes of tensor memory
+  const uint32_t out_at = lanes + S::kOut + r * D;
+  const int token = r * P.tokens + m / P.heads, in_group = m % P.heads;  // of this row: token of the unit, head of the part
+  const float scale = P.scale_log2;
+  bool dead = false;
+  auto wait = [&](unsigned long long* b, uint32_t parity) {
+    if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(b, parity, P.spin_limit, 0u));
+  };
+  Turn at;          // slots of the unit's first tile
+  uint32_t nth = 0; // slots of values before the unit
+  uint32_t it = 0;  // tiles weighed so far
+  // the buffer of tile `tile` and which use of it that is
+  auto buffer = [&](uint32_t tile) { return S::TILES == 2 ? (uint32_t)r : tile & 1; };
+  auto use = [&](uint32_t tile) { return S::TILES == 2 ? tile : tile >> 1; };
+  auto added = [&](uint32_t tile) {  // the output holds everything up to this tile
+    wait(&c.pv_done[buffer(tile)], use(tile) & 1);
+    fence_after();
+  };
+  bool more = true;
+  for (int sg = 0; more; ++sg) {
+    wait(&c.seg_full[sg & 1], (sg >> 1) & 1);
+    if (dead) break;
+    const Unit u = c.unit[sg & 1];
+    more = u.tiles > 0;
+    const int count = tiles_of(u, r);  // 0 at the end
+    const int pos = u.t0 + token, head = u.chunk * P.heads + in_group;
+    const bool live = m < P.heads * P.tokens && pos <= u.pos1 && head < P.group;
+    float mx = -INFINITY, l = 0.0f;
+    bool large = false;
+    Turn turn = at;
+    for (int i = 0; i < u.tiles; ++i)
+      for (int n = 0; n < 2 * S::kHalves; ++n) at.next(S::kSlots);
+    for (int i = 0; i < count && !dead; ++i, ++it) {
+      const uint32_t b = buffer(it), buf = lanes + b * kKeys;
+      const int base = base_of(u, i);
+      const bool cut = cuts(P, u, base);
+      for (int half = 0; half < S::kHalves; ++half) turn.next(S::kSlots);
+      const Turn v_turn = turn;
+      for (int half = 0; half < S::kHalves; ++half) turn.next(S::kSlots);
+      wait(&c.s_full[b], use(it) & 1);
+      if (dead) break;
+      fence_after();
+      Seen sees = {kKeys, 0, 0};
+      if (cut) {
+        sees.end = live ? pos + 1 - base : 0;
+        if (P.window > 0) {
+          sees.start = pos - P.window + 1 - base;
+          sees.sinks = P.sinks - base;
+        }
+      }
+      uint32_t x[4][32];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ask(x[q], buf + 32 * q);
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int n = 0; n < 32; ++n) asm volatile("" : "+r"(x[q][n]));  // not to be read before the wait
+      if (cut) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int n = 0; n < 32; ++n)
+            if (!sees(32 * q + n)) x[q][n] = 0xff800000u;
+      }
+      float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int n = 0; n < 32; n += 8)
+#pragma unroll
+          for (int h = 0; h < 4; ++h) t[h] = fmaxf(t[h], fmaxf(__uint_as_float(x[q][n + h]), __uint_as_float(x[q][n + 4 + h])));
+      const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
+      const bool grow = live && top - mx > 8.0f + E::kLift;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float now = grow ? (fabsf(top) > kLarge ? top : top - E::kLift) : mx;
+        const float by = grow ? ex2(mx - now) : 1.0f;  // 0 if nothing was seen before
+        mx = now;
+        large = __any_sync(0xffffffffu, mx != -INFINITY && fabsf(mx) > kLarge);
+        l *= by;
+        if (i > 0) {
+          added(it - 1);
+#pragma unroll 1
+          for (int d = 0; d < D; d += 16) {
+            uint32_t o[16];
+            tmem_load(o, out_at + d);
+#pragma unroll
+            for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * by);
+            tmem_store(out_at + d, o);
+          }
+          store_wait();
+        }
+      }
+      const float z = mx == -INFINITY ? 0.0f : mx;
+      if (large) {
+        l += large_weights<E, false>(buf, scale, z, sees).y;
+      } else {
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[16];
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            const float a = ex2(fmaf(__uint_as_float(x[q][2 * n]), scale, -z)), e = ex2(fmaf(__uint_as_float(x[q][2 * n + 1]), scale, -z));
+            w[n] = E::pack(a, e);
+            s[n & 1] += a;
+            s[2 + (n & 1)] += e;
+          }
+          tmem_store(buf + 16 * q, w);
+        }
+        l += (s[0] + s[1]) + (s[2] + s[3]);
+      }
+      store_wait();
+      if (cut) {
+        const uint32_t n = nth + i * S::kHalves;
+        for (int half = 0; half < S::kHalves; ++half) wait(&c.ready[(n + half) % kMaxSlots], parity_of(n + half));
+        if (!dead && is_slow<S>(c, n)) {
+          if (i > 0) added(it - 1);
+          add_by_key<S>(buf, out_at, ring, v_turn, sees, i == 0);
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(&c.p_full[b]);
+    }
+    nth += u.tiles * S::kHalves;
+    if (count > 0 && !dead) {
+      added(it - 1);
+      const float f = l == 0.0f ? 0.0f : 1.0f / l;
+      const long long q = u.q0 + pos;
+      const int to_head = u.h * P.group + head;
+      T* to = static_cast<T*>(P.out) + q * P.out_stride + (long long)to_head * D;
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        uint32_t o[32];
+        tmem_load(o, out_at + d);
+        if (!live) continue;
+#pragma unroll
+        for (int n = 0; n < 32; n += 8) {
+          auto val = [&](int k) { return __uint_as_float(o[n + k]) * f; };
+          *reinterpret_cast<uint4*>(to + d + n) =
+              make_uint4(E::pack(val(0), val(1)), E::pack(val(2), val(3)), E::pack(val(4), val(5)), E::pack(val(6), val(7)));
+        }
+      }
+      if (live && P.lse) P.lse[q * (P.group * P.hkv) + to_head] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
+      fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(&c.o_free[r]);
+    }
+    __syncwarp();
+    if (lane == 0 && !dead) arrive(&c.seg_empty[sg & 1]);
+  }
+  if (dead) report_all(P);
+}
+
+// ------------------------------------------------------------------ kernel
+template <class T, int D, int TILES>
+__global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), 1)
+    prompt_kernel(const PromptParams P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv) {
+  using S = Shape<T, D, TILES>;
+  extern __shared__ unsigned char raw[];
+  __shared__ Control c;
+  unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  unsigned char* ring = base + TILES * S::kQ;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < kMaxSlots; ++i) {
+      mbar_init_n(&c.full[i], 1);
+      mbar_init_n(&c.empty[i], 1);
+      mbar_init_n(&c.ready[i], kGuardWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init_n(&c.seg_full[i], 1);
+      mbar_init_n(&c.seg_empty[i], S::kSoftmax + 1 + kGuardWarps);
+      mbar_init_n(&c.q_full[i], 1);
+      mbar_init_n(&c.q_free[i], 1);
+      mbar_init_n(&c.s_full[i], 1);
+      mbar_init_n(&c.p_full[i], 4);
+      mbar_init_n(&c.pv_done[i], 1);
+      mbar_init_n(&c.o_free[i], 4);
+    }
+    mbar_init_n(&c.drained, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == S::kProduct) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&c.tmem)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == S::kLoad && lane < 3) asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &mq : lane == 1 ? &mk : &mv) : "memory");
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp < S::kSoftmax) {
+    softmax_warps<S>(P, ring, c);
+  } else if (warp == S::kLoad) {
+    load_warp<S>(P, &mq, &mk, &mv, smem_u32(base), smem_u32(ring), c);
+  } else if (warp == S::kProduct) {
+    if (lane == 0) product_thread<S>(P, smem_u32(base), smem_u32(ring), c);
+    __syncwarp();
+  } else {
+    guard_warps<S>(P, ring, c);
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == S::kProduct) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(c.tmem), "r"(512) : "memory");
+  }
+  // the counters are left at zero by the last CTA to end: every one has taken its last unit by then
+  if (tid == 0) {
+    __threadfence();
+    if (atomicAdd(P.ended, 1u) + 1 == gridDim.x) {
+      *P.next = 0;
+      *P.ended = 0;
+      __threadfence();
+    }
+  }
+}
+
+template <class T, int D, int TILES>
+PromptKernel entry() {
+  using S = Shape<T, D, TILES>;
+  return {reinterpret_cast<const void*>(&prompt_kernel<T, D, TILES>), S::kThreads, TILES, (size_t)S::kSmem};
+}
+template <class T>
+PromptKernel pick(int d) {
+  return d == 64 ? entry<T, 64, 2>() : d == 128 ? entry<T, 128, 2>() : entry<T, 256, 1>();
+}
+
+}  // namespace prompt
+}  // namespace kv
+}  // namespace ss

@@ -65,6 +65,12 @@ class LoadBatch(C.Structure):
     _fields_ = [("T", _i32), ("slots", _p), ("k", _p), ("v", _p), ("k_stride", _i64), ("v_stride", _i64), ("stream", _p), ("plan", _p)]
 
 
+class PromptBatch(C.Structure):
+    _fields_ = [("B", _i32), ("tokens", _i32), ("q", _p), ("k", _p), ("v", _p), ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64),
+                ("cu_seq", _p), ("scale", _f32), ("window", _i32), ("sinks", _i32), ("out", _p), ("out_stride", _i64), ("lse", _p),
+                ("row_status", _p), ("workspace", _p), ("workspace_bytes", C.c_size_t), ("stream", _p), ("plan", _p)]
+
+
 # The same layouts as native struct formats: packing one takes a fifth of the time that filling a ctypes structure does.
 _CACHE = struct.Struct("@PPqqqPP")
 _POOL = struct.Struct("@iiPPPPPP")
@@ -73,11 +79,13 @@ _ATTEND = struct.Struct("@iiPqPPPfiiPqPPPNPP")
 _BLOCKS = struct.Struct("@PPqqqPPi0q")
 _STORE = struct.Struct("@iiPPqqPPPPPPP")
 _LOAD = struct.Struct("@iPPPqqPP")
+_PROMPT = struct.Struct("@iiPPPqqqPfiiPqPPPNPP")
 assert [_CACHE.size, _POOL.size, _ROPE.size, _ATTEND.size] == [C.sizeof(c) for c in (Cache, Pool, RopeBatch, AttendBatch)]
-assert [_BLOCKS.size, _STORE.size, _LOAD.size] == [C.sizeof(c) for c in (BlockCache, StoreBatch, LoadBatch)]
+assert [_BLOCKS.size, _STORE.size, _LOAD.size, _PROMPT.size] == [C.sizeof(c) for c in (BlockCache, StoreBatch, LoadBatch, PromptBatch)]
 
 EXPORTS = ["ss_kv_plan_create", "ss_kv_plan_destroy", "ss_kv_workspace_bytes", "ss_kv_append", "ss_kv_commit",
-           "ss_rope_store", "ss_rope_frequencies", "ss_attend", "ss_kv_store_blocks", "ss_kv_load_blocks", "ss_attend_blocks"]
+           "ss_rope_store", "ss_rope_frequencies", "ss_attend", "ss_kv_store_blocks", "ss_kv_load_blocks", "ss_attend_blocks",
+           "ss_attend_prompt"]
 
 _lib = None
 
@@ -100,8 +108,9 @@ def library() -> C.CDLL:
     L.ss_rope_frequencies.argtypes = [C.POINTER(C.c_double), _i32, C.c_double, C.c_double, _i32, C.c_double, C.c_double]
     for name in ("ss_attend", "ss_kv_store_blocks", "ss_kv_load_blocks", "ss_attend_blocks"):
         getattr(L, name).argtypes = [_p, _p]
+    L.ss_attend_prompt.argtypes = [_p]
     for name in ("ss_kv_plan_create", "ss_kv_append", "ss_kv_commit", "ss_rope_store", "ss_rope_frequencies", "ss_attend",
-                 "ss_kv_store_blocks", "ss_kv_load_blocks", "ss_attend_blocks"):
+                 "ss_kv_store_blocks", "ss_kv_load_blocks", "ss_attend_blocks", "ss_attend_prompt"):
         getattr(L, name).restype = C.c_int
     _lib = L
     return L
@@ -330,10 +339,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, factor: float = 1.0
     return out
 
 
-def _attend(plan, q, block_table, seq_len, cu_new, out, row_status, workspace, scale, window, sinks, lse, B, stream):
-    """The batch of an attention call."""
-    B = seq_len.shape[0] if B is None else B
-    qs, os = _tokens("q", q, plan.q_heads, plan), _tokens("out", out, plan.q_heads, plan)
+def _outputs(plan, q, out, lse, workspace):
+    """Checks of an attention call's outputs and workspace."""
     if out.shape[0] < q.shape[0]:
         raise _bad("out must have as many tokens as q")
     if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() < q.shape[0] * plan.q_heads):
@@ -343,6 +350,13 @@ def _attend(plan, q, block_table, seq_len, cu_new, out, row_status, workspace, s
     for name, t in (("workspace", workspace), ("lse", lse)):
         if t is not None and t.get_device() != plan.device:
             raise _elsewhere(name, t, plan)
+
+
+def _attend(plan, q, block_table, seq_len, cu_new, out, row_status, workspace, scale, window, sinks, lse, B, stream):
+    """The batch of an attention call."""
+    B = seq_len.shape[0] if B is None else B
+    qs, os = _tokens("q", q, plan.q_heads, plan), _tokens("out", out, plan.q_heads, plan)
+    _outputs(plan, q, out, lse, workspace)
     return _ATTEND.pack(B, q.shape[0], q.data_ptr(), qs, _int(plan, "cu_new", cu_new, B + 1), _int(plan, "seq_len", seq_len, B),
                         _int(plan, "block_table", block_table, B * plan.max_blocks), scale, window, sinks, out.data_ptr(), os, _ptr(lse),
                         _int(plan, "row_status", row_status, B), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
@@ -364,5 +378,22 @@ def ss_attend_blocks(plan: Plan, q, k_cache, v_cache, k_scale, v_scale, block_ta
     """ss_attend_blocks: as ss_attend, over a cache with factors k_scale, v_scale float32 [pages, kv_heads, page_size / block_tokens]."""
     b = _attend(plan, q, block_table, seq_len, cu_new, out, row_status, workspace, scale, window, sinks, lse, B, stream)
     code = _lib.ss_attend_blocks(b, _blocks(plan, k_cache, v_cache, k_scale, v_scale))
+    if code:
+        native._check(code)
+
+
+def ss_attend_prompt(plan: Plan, q, k, v, cu_seq, *, out, row_status, workspace, scale, window=0, sinks=0, lse=None, B=None, stream=None):
+    """ss_attend_prompt: q, out [tokens, q_heads, head_dim], k, v [tokens, kv_heads, head_dim], prompts one after the other; lse float32
+    [tokens, q_heads] or None.  A prompt with a token past those of q is left out."""
+    B = cu_seq.shape[0] - 1 if B is None else B
+    qs, os = _tokens("q", q, plan.q_heads, plan), _tokens("out", out, plan.q_heads, plan)
+    ks, vs = _tokens("k", k, plan.kv_heads, plan), _tokens("v", v, plan.kv_heads, plan)
+    if k.shape[0] != q.shape[0] or v.shape[0] != q.shape[0]:
+        raise _bad("q, k and v must have the same number of tokens")
+    _outputs(plan, q, out, lse, workspace)
+    b = _PROMPT.pack(B, q.shape[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _int(plan, "cu_seq", cu_seq, B + 1), scale, window, sinks,
+                     out.data_ptr(), os, _ptr(lse), _int(plan, "row_status", row_status, B), workspace.data_ptr(),
+                     workspace.numel() * workspace.element_size(), _stream(stream, plan), plan.handle)
+    code = _lib.ss_attend_prompt(b)
     if code:
         native._check(code)

@@ -1,4 +1,4 @@
-"""CPU-side checks of the calls on an 8-bit cache with a factor for each block: struct layouts against include/ss_kv.h,
+"""CPU-side checks of the calls on an 8-bit cache with a factor for each block, and of the attention over prompts: struct layouts against include/ss_kv.h,
 refusals that need no device, tensors of another device than their plan's."""
 import ctypes as C
 import re
@@ -29,7 +29,8 @@ def test_struct_layouts_match_header(kv):
             out += toks[1:]
         return out
 
-    for name, cls in [("ss_kv_block_cache", kv.BlockCache), ("ss_store_batch", kv.StoreBatch), ("ss_load_batch", kv.LoadBatch)]:
+    for name, cls in [("ss_kv_block_cache", kv.BlockCache), ("ss_store_batch", kv.StoreBatch), ("ss_load_batch", kv.LoadBatch),
+                      ("ss_prompt_batch", kv.PromptBatch)]:
         assert fields(name) == [f for f, _ in cls._fields_], name
 
 
@@ -41,6 +42,9 @@ def test_null_arguments_are_refused(kv):
         assert call(C.byref(batch), None) == ERR_ARG
         assert call(C.byref(batch), C.byref(cache)) == ERR_ARG
         assert call(None, C.byref(cache)) == ERR_ARG
+    prompt = kv.PromptBatch()
+    assert L.ss_attend_prompt(None) == ERR_ARG
+    assert L.ss_attend_prompt(C.byref(prompt)) == ERR_ARG
 
 
 def test_tensors_of_another_device_are_refused(kv):
@@ -54,7 +58,9 @@ def test_tensors_of_another_device_are_refused(kv):
     calls = [(kv.ss_kv_store_blocks, dict(cache, **rows, k=bf16(4, 2, 64), v=bf16(4, 2, 64), kv_len=_i32(2)), {}),
              (kv.ss_kv_load_blocks, dict(cache, slots=_i32(4), k_out=bf16(4, 2, 64), v_out=bf16(4, 2, 64)), {}),
              (kv.ss_attend_blocks, dict(cache, **rows, q=bf16(4, 4, 64), out=bf16(4, 4, 64), lse=torch.zeros(4, 4),
-                                        workspace=torch.zeros(256, dtype=torch.uint8)), {"scale": 0.125})]
+                                        workspace=torch.zeros(256, dtype=torch.uint8)), {"scale": 0.125}),
+             (kv.ss_attend_prompt, dict(q=bf16(4, 4, 64), k=bf16(4, 2, 64), v=bf16(4, 2, 64), cu_seq=_i32(3), out=bf16(4, 4, 64), row_status=_i32(2),
+                                        lse=torch.zeros(4, 4), workspace=torch.zeros(256, dtype=torch.uint8)), {"scale": 0.125})]
     stream = SimpleNamespace(cuda_stream=0)
     for call, tensors, others in calls:
         for name in tensors:
@@ -66,6 +72,8 @@ def test_tensors_of_another_device_are_refused(kv):
             with pytest.raises(native.SSError) as e:
                 call(plan, **args, **others, stream=stream)
             assert e.value.code == -1 and "host" in str(e.value), (call.__name__, name, str(e.value))
+        if call is kv.ss_attend_prompt:
+            continue
         with pytest.raises(native.SSError) as e:  # a plan with a 16-bit cache
             call(SimpleNamespace(**{**plan.__dict__, "cache_dtype": "bf16"}), **{n: On(t, 1) for n, t in tensors.items()}, **others, stream=stream)
         assert e.value.code == -1 and "e4m3" in str(e.value)
