@@ -21,7 +21,7 @@
 // A CTA's warps:
 //  - load: takes units, publishes them, runs the ring of key and value tiles
 //    (TMA) and brings their queries (TMA; a box of heads by tokens).
-//  - product: one thread issues tcgen05.mma.
+//  - product: one warp issues tcgen05.mma (by its first lane).
 //  - softmax: four warps to a tile of rows; a thread owns a row (a lane of
 //    tensor memory), reads its 128 scores, writes its weights over them.
 //  - guard: two warps look at every tile of values before the products do.  In
@@ -319,13 +319,43 @@ __device__ __forceinline__ bool is_slow(const Control& c, uint32_t n) {
 }
 __device__ __forceinline__ uint32_t parity_of(uint32_t n) { return (n / kMaxSlots) & 1; }
 
-// ------------------------------------------------------------------ product thread
+// ------------------------------------------------------------------ product warp
+// All lanes go through it together and hold the same numbers, which the reductions below tell the compiler: operands in
+// uniform registers take a product a few cycles to issue, where one thread's own take about a hundred.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+
+// D (+)= A B^T from shared memory, D (+)= A B with A from tensor memory: by the leading lane.  Operands as in operand(), of
+// which the low halves differ from one product to the next.
+constexpr uint32_t kOperandHigh = (uint32_t)(1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t operand_low(uint32_t at, uint32_t lead) { return (at & 0x3ffffu) >> 4 | (lead >> 4) << 16; }
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n mov.b64 a, {%1, %4};\n mov.b64 b, {%2, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"(kOperandHigh), "r"((uint32_t)add), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n mov.b64 b, {%2, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"(kOperandHigh), "r"((uint32_t)add), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, unsigned long long* m) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_u32(m)),
+      "r"(leader)
+      : "memory");
+}
+
 template <class S>
-__device__ void product_thread(const PromptParams& P, uint32_t sq, uint32_t ring, Control& c) {
-  const uint32_t tmem = c.tmem;
+__device__ void product_warp(const PromptParams& P, uint32_t sq, uint32_t ring, Control& c) {
+  const uint32_t tmem = uniform(c.tmem), leader = (threadIdx.x & 31) == 0;
   bool dead = false;
   auto wait = [&](unsigned long long* m, uint32_t parity) {
-    if (!dead) dead = !mbar_wait(m, parity, P.spin_limit, 0u);
+    if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(m, parity, P.spin_limit, 0u));
   };
   Turn at;                                             // slots of the unit's first tile
   uint32_t nth = 0;                                    // slots of values before the unit
@@ -335,7 +365,10 @@ __device__ void product_thread(const PromptParams& P, uint32_t sq, uint32_t ring
   for (int sg = 0; more && !dead; ++sg) {
     wait(&c.seg_full[sg & 1], (sg >> 1) & 1);
     if (dead) break;
-    const Unit u = c.unit[sg & 1];
+    Unit u = c.unit[sg & 1];
+    u.tiles = uniform(u.tiles);
+    u.live = uniform(u.live);
+    u.of_first = uniform(u.of_first);
     more = u.tiles > 0;
     if (!more) break;
     Turn keys = at, values = at;  // slots of the tile whose scores, and whose products, come next (for the first tile of rows)
@@ -353,16 +386,18 @@ __device__ void product_thread(const PromptParams& P, uint32_t sq, uint32_t ring
         wait(&c.full[t.slot], t.parity);
         if (dead) return;
         fence_after();
+        const uint32_t q = operand_low(sq + r * S::kQ + half * (S::kWide / 64) * S::kRun, 0), k = operand_low(ring + t.slot * S::kSlot, 0);
 #pragma unroll
-        for (int k = 0; k < S::kWide / 16; ++k)
-          mma_ss(tmem + b * kKeys, operand(sq + r * S::kQ + (half * (S::kWide / 64) + (k >> 2)) * S::kRun + (k & 3) * 32, 0),
-                 operand(ring + t.slot * S::kSlot + (k >> 2) * S::kRun + (k & 3) * 32, 0), S::kScores, half + k != 0);
-        if (r + 1 == u.live) commit(&c.empty[t.slot]);
+        for (int n = 0; n < S::kWide / 16; ++n) {
+          const uint32_t step = ((n >> 2) * S::kRun + (n & 3) * 32) >> 4;
+          mma_ss(leader, tmem + b * kKeys, q + step, k + step, S::kScores, half + n != 0);
+        }
+        if (r + 1 == u.live) commit(leader, &c.empty[t.slot]);
         t.next(S::kSlots);
       }
-      commit(&c.s_full[b]);
+      commit(leader, &c.s_full[b]);
       if (i + 1 == tiles_of(u, r)) {
-        commit(&c.q_free[r]);
+        commit(leader, &c.q_free[r]);
         ++q_units[r];
       }
     };
@@ -371,39 +406,42 @@ __device__ void product_thread(const PromptParams& P, uint32_t sq, uint32_t ring
         if (o_units[r] > 0) wait(&c.o_free[r], (o_units[r] - 1) & 1);
         ++o_units[r];
       }
-      Turn s = t;
       const uint32_t n = nth + i * S::kHalves;
+      const bool cut = cuts(P, u, base_of(u, i));
+      Turn s = t;
 #pragma unroll
       for (int half = 0; half < S::kHalves; ++half) {
         wait(&c.full[s.slot], s.parity);
-        wait(&c.ready[(n + half) % kMaxSlots], parity_of(n + half));
+        if (cut) wait(&c.ready[(n + half) % kMaxSlots], parity_of(n + half));
         s.next(S::kSlots);
       }
       wait(&c.p_full[b], added[b] & 1);
       ++added[b];
       if (dead) return;
       fence_after();
-      const bool slow = cuts(P, u, base_of(u, i)) && is_slow<S>(c, n);
+      const bool slow = cut && uniform(is_slow<S>(c, n));
 #pragma unroll
       for (int half = 0; half < S::kHalves; ++half) {
         if (!slow) {
+          const uint32_t v = operand_low(ring + t.slot * S::kSlot, S::kRun);
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
-            mma_ts(tmem + S::kOut + r * S::D + half * S::kWide, tmem + b * kKeys + k * 8, operand(ring + t.slot * S::kSlot + k * 2048, S::kRun),
-                   S::kValues, i != 0 || k != 0);
+            mma_ts(leader, tmem + S::kOut + r * S::D + half * S::kWide, tmem + b * kKeys + k * 8, v + k * (2048 >> 4), S::kValues, i != 0 || k != 0);
         }
-        if (r + 1 == u.live) commit(&c.empty[t.slot]);
+        if (r + 1 == u.live) commit(leader, &c.empty[t.slot]);
         t.next(S::kSlots);
       }
-      commit(&c.pv_done[b]);
+      commit(leader, &c.pv_done[b]);
     };
     if constexpr (S::TILES == 2) {
-      for (int r = 0; r < u.live; ++r) scores(r, r, 0, keys);
+      scores(0, 0, 0, keys);
+      if (u.live > 1) scores(1, 1, 0, keys);
       skip(keys);
       for (int i = 0; i < u.tiles && !dead; ++i) {
-        for (int r = 0; r < u.live && !dead; ++r) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
           const int n = tiles_of(u, r);
-          if (i < n) products(r, r, i, values);
+          if (i < n && !dead) products(r, r, i, values);
           if (i + 1 < n && !dead) scores(r, r, i + 1, keys);
         }
         skip(keys);
@@ -429,23 +467,27 @@ __device__ void product_thread(const PromptParams& P, uint32_t sq, uint32_t ring
     }
     for (int i = 0; i < u.tiles; ++i) skip(at);
     nth += u.tiles * S::kHalves;
-    if (!dead) arrive(&c.seg_empty[sg & 1]);
+    __syncwarp();
+    if (leader && !dead) arrive(&c.seg_empty[sg & 1]);
   }
   // nothing may be in flight when tensor memory is given back
-  commit(&c.drained);
+  commit(leader, &c.drained);
   mbar_wait(&c.drained, 0, kDrainPolls, 0u);
 }
 
 // ------------------------------------------------------------------ softmax warps
-__device__ __forceinline__ void tmem_ask(uint32_t (&r)[32], uint32_t at) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-        "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(at)
-      : "memory");
+// Two 32-bit numbers at a time.
+__device__ __forceinline__ uint64_t pair(float a, float b) { return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a); }
+__device__ __forceinline__ float2 halves(uint64_t x) { return make_float2(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32))); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 // Which keys of a tile a row sees, by their number in it: [0, end) but for [sinks, start).
@@ -579,28 +621,26 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
           sees.sinks = P.sinks - base;
         }
       }
-      uint32_t x[4][32];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ask(x[q], buf + 32 * q);
-      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int n = 0; n < 32; ++n) asm volatile("" : "+r"(x[q][n]));  // not to be read before the wait
-      if (cut) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int n = 0; n < 32; ++n)
-            if (!sees(32 * q + n)) x[q][n] = 0xff800000u;
-      }
+      // Scores are read twice, a part at a time: a row's 128 do not stay in registers beside the rest.  Half of them do.
+      uint32_t x[64], y[32];
       float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      auto hide = [&](uint32_t* w, int from, int count) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+        for (int n = 0; n < count; ++n)
+          if (!sees(from + n)) w[n] = 0xff800000u;
+      };
+      auto largest = [&](const uint32_t* w, int count) {
 #pragma unroll
-        for (int n = 0; n < 32; n += 8)
+        for (int n = 0; n < count; n += 8)
 #pragma unroll
-          for (int h = 0; h < 4; ++h) t[h] = fmaxf(t[h], fmaxf(__uint_as_float(x[q][n + h]), __uint_as_float(x[q][n + 4 + h])));
+          for (int h = 0; h < 4; ++h) t[h] = fmaxf(t[h], fmaxf(__uint_as_float(w[n + h]), __uint_as_float(w[n + 4 + h])));
+      };
+      tmem_load(x, buf + 64);
+      if (cut) hide(x, 64, 64);
+      largest(x, 64);
+      tmem_load(x, buf);
+      if (cut) hide(x, 0, 64);
+      largest(x, 64);
       const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
       const bool grow = live && top - mx > 8.0f + E::kLift;
       if (__any_sync(0xffffffffu, grow)) {
@@ -626,20 +666,31 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
       if (large) {
         l += large_weights<E, false>(buf, scale, z, sees).y;
       } else {
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t w[16];
+        uint64_t s0 = 0, s1 = 0;  // sums of even and odd keys
+        const uint64_t by = pair(scale, scale), less = pair(-z, -z);
+        auto weigh = [&](const uint32_t* w, int from) {  // 32 keys
+          uint32_t p[16];
 #pragma unroll
           for (int n = 0; n < 16; ++n) {
-            const float a = ex2(fmaf(__uint_as_float(x[q][2 * n]), scale, -z)), e = ex2(fmaf(__uint_as_float(x[q][2 * n + 1]), scale, -z));
-            w[n] = E::pack(a, e);
-            s[n & 1] += a;
-            s[2 + (n & 1)] += e;
+            const float2 e = halves(fma2(pair(__uint_as_float(w[2 * n]), __uint_as_float(w[2 * n + 1])), by, less));
+            const float a = ex2(e.x), b2 = ex2(e.y);
+            p[n] = E::pack(a, b2);
+            if (n & 1) s1 = add2(s1, pair(a, b2));
+            else s0 = add2(s0, pair(a, b2));
           }
-          tmem_store(buf + 16 * q, w);
+          tmem_store(buf + from / 2, p);
+        };
+        // (weights lie over the scores of the first 64 keys, which have been read)
+        weigh(x, 0);
+        weigh(x + 32, 32);
+#pragma unroll
+        for (int q = 64; q < 128; q += 32) {
+          tmem_load(y, buf + q);
+          if (cut) hide(y, q, 32);
+          weigh(y, q);
         }
-        l += (s[0] + s[1]) + (s[2] + s[3]);
+        const float2 s = halves(add2(s0, s1));
+        l += s.x + s.y;
       }
       store_wait();
       if (cut) {
@@ -727,8 +778,7 @@ __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), 1)
   } else if (warp == S::kLoad) {
     load_warp<S>(P, &mq, &mk, &mv, smem_u32(base), smem_u32(ring), c);
   } else if (warp == S::kProduct) {
-    if (lane == 0) product_thread<S>(P, smem_u32(base), smem_u32(ring), c);
-    __syncwarp();
+    product_warp<S>(P, smem_u32(base), smem_u32(ring), c);
   } else {
     guard_warps<S>(P, ring, c);
   }
