@@ -21,10 +21,10 @@
 // A CTA's warps:
 //  - load: takes units, publishes them, runs the ring of key and value tiles
 //    (TMA) and brings their queries (TMA; a box of heads by tokens).
-//  - product: one warp issues tcgen05.mma (by its first lane).
+//  - product: two warps issue tcgen05.mma.
 //  - softmax: four warps to a tile of rows; a thread owns a row (a lane of
 //    tensor memory), reads its 128 scores, writes its weights over them.
-//  - guard: two warps look at every tile of values before the products do.  In
+//  - guard: a warp looks at every tile of values before the products do.  In
 //    one that not every row sees in full, values that no row sees become zeros
 //    (0 x NaN must not reach a sum), and if one that only some rows see is not
 //    finite, the tile is added key by key by the softmax warps.
@@ -43,14 +43,14 @@ namespace prompt {
 
 constexpr int kKeys = 128;       // keys of a tile
 constexpr int kMaxSlots = 8;
-constexpr int kGuardWarps = 2;
+constexpr int kGuardWarps = 1;
 
 template <class T_, int D_, int TILES_>
 struct Shape {
   using T = T_;
   static constexpr int D = D_, TILES = TILES_;
   static constexpr int kSoftmax = 4 * TILES;                  // warps
-  static constexpr int kLoad = kSoftmax, kProduct = kSoftmax + 1, kGuard = kSoftmax + 2;
+  static constexpr int kLoad = kSoftmax, kProduct = kSoftmax + 1, kGuard = kSoftmax + 3;
   static constexpr int kThreads = 32 * (kGuard + kGuardWarps);
   static constexpr int kWide = D < 128 ? D : 128;             // columns of a slot
   static constexpr int kHalves = D / kWide;                   // slots of a tile
@@ -239,6 +239,14 @@ __device__ void load_warp(const PromptParams& P, const CUtensorMap* mq, const CU
 }
 
 // ------------------------------------------------------------------ guard warps
+template <class T>
+__device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t sum) {
+  uint32_t y;
+  if (std::is_same<T, __half>::value) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0u), "r"(sum));
+  else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0u), "r"(sum));
+  return y;
+}
+
 template <class S>
 __device__ void guard_warps(const PromptParams& P, unsigned char* ring, Control& c) {
   const int tid = threadIdx.x - 32 * S::kGuard, lane = tid & 31;
@@ -248,7 +256,6 @@ __device__ void guard_warps(const PromptParams& P, unsigned char* ring, Control&
       if (q0 < 0 || q1 < q0 || q1 > P.max_tokens) atomicOr(&P.row_status[r], (uint32_t)SS_ST_CAPACITY);
     }
   }
-  using E = Elem<typename S::T>;
   Turn turn;
   uint32_t nth = 0;  // slots of values so far
   bool dead = false;
@@ -269,8 +276,7 @@ __device__ void guard_warps(const PromptParams& P, unsigned char* ring, Control&
         wait(&c.full[turn.slot], turn.parity);
         if (dead) break;
         if (cut) {
-          uint32_t wild = 0;  // bits 15 and 31: an exponent of ones, plus one, carries into the sign's place
-          constexpr uint32_t kOnes = E::kExponent * 0x10001u, kOne = kOnes & ~(kOnes << 1);
+          uint32_t wild = 0;  // x * 0 is 0, or NaN if x is not finite: two values an operation
           for (int in = tid; in < kKeys; in += 32 * kGuardWarps) {
             const int key = base + in;
             const bool some = key <= u.pos1 && (P.window <= 0 || key > u.t0 - P.window || key < P.sinks);
@@ -285,12 +291,12 @@ __device__ void guard_warps(const PromptParams& P, unsigned char* ring, Control&
                   line[(x + tid) & 7] = make_uint4(0u, 0u, 0u, 0u);
                 } else {
                   const uint4 y = line[(x + tid) & 7];
-                  for (const uint32_t w : {y.x, y.y, y.z, y.w}) wild |= (w & kOnes) + kOne;
+                  for (const uint32_t w : {y.x, y.y, y.z, y.w}) wild = times_zero<typename S::T>(w, wild);
                 }
               }
             }
           }
-          const bool slow = __any_sync(0xffffffffu, (wild & 0x80008000u) != 0);
+          const bool slow = __any_sync(0xffffffffu, (wild & 0x7fff7fffu) != 0);
           if (lane == 0) c.slow[nth % kMaxSlots][tid >> 5] = slow;
           proxy_fence();
         } else if (lane == 0) {
@@ -319,49 +325,64 @@ __device__ __forceinline__ bool is_slow(const Control& c, uint32_t n) {
 }
 __device__ __forceinline__ uint32_t parity_of(uint32_t n) { return (n / kMaxSlots) & 1; }
 
-// ------------------------------------------------------------------ product warp
-// All lanes go through it together and hold the same numbers, which the reductions below tell the compiler: operands in
-// uniform registers take a product a few cycles to issue, where one thread's own take about a hundred.
+// ------------------------------------------------------------------ product warps
+// All lanes go through them together and hold the same numbers, which the reductions below tell the compiler, and one of
+// them is elected to issue: with operands in uniform registers a product takes some tens of cycles to issue, where a
+// thread that is alone from the start takes about a hundred.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+__device__ __forceinline__ bool elected() {  // always the same lane
+  uint32_t x;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(x));
+  return x != 0;
+}
 
-// D (+)= A B^T from shared memory, D (+)= A B with A from tensor memory: by the leading lane.  Operands as in operand(), of
-// which the low halves differ from one product to the next.
+// D (+)= A B^T from shared memory, D (+)= A B with A from tensor memory.  Operands as in operand(), of which only the low
+// halves differ from one product to the next.
 constexpr uint32_t kOperandHigh = (uint32_t)(1024 >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint32_t operand_low(uint32_t at, uint32_t lead) { return (at & 0x3ffffu) >> 4 | (lead >> 4) << 16; }
-__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n mov.b64 a, {%1, %4};\n mov.b64 b, {%2, %4};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(desc), "r"(kOperandHigh), "r"((uint32_t)add), "r"(leader)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %4};\n mov.b64 b, {%2, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"(kOperandHigh), "r"((uint32_t)add)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n mov.b64 b, {%2, %4};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(desc), "r"(kOperandHigh), "r"((uint32_t)add), "r"(leader)
-      : "memory");
-}
-__device__ __forceinline__ void commit(uint32_t leader, unsigned long long* m) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-          smem_u32(m)),
-      "r"(leader)
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"(kOperandHigh), "r"((uint32_t)add)
       : "memory");
 }
 
+// Two warps.  TILES == 2: one for each tile of rows, so that one's waits and issuing overlap the other's products;
+// TILES == 1: one for the scores, one for the products with the values.
 template <class S>
-__device__ void product_warp(const PromptParams& P, uint32_t sq, uint32_t ring, Control& c) {
-  const uint32_t tmem = uniform(c.tmem), leader = (threadIdx.x & 31) == 0;
+__device__ void product_warp(const PromptParams& P, int which, uint32_t sq, uint32_t ring, Control& c) {
+  const uint32_t tmem = uniform(c.tmem);
+  const int r = S::TILES == 2 ? which : 0;
+  const bool scores = S::TILES == 2 || which == 0, products = S::TILES == 2 || which == 1;
   bool dead = false;
   auto wait = [&](unsigned long long* m, uint32_t parity) {
     if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(m, parity, P.spin_limit, 0u));
   };
-  Turn at;                                             // slots of the unit's first tile
-  uint32_t nth = 0;                                    // slots of values before the unit
-  uint32_t scored[2] = {0, 0}, added[2] = {0, 0};      // uses of the two score buffers
-  uint32_t q_units[2] = {0, 0}, o_units[2] = {0, 0};   // units by tile of rows
+  Turn keys, values;  // slots of the tile whose scores, and whose products, come next
+  for (int n = 0; n < S::kHalves; ++n) values.next(S::kSlots);
+  auto skip = [&](Turn& t) {
+#pragma unroll
+    for (int n = 0; n < 2 * S::kHalves; ++n) t.next(S::kSlots);
+  };
+  // A slot that this warp has no use for: the other one's release is not to stand for both.
+  auto pass = [&](const Turn& t) {
+    wait(&c.full[t.slot], t.parity);
+    if (!dead && elected()) arrive(&c.empty[t.slot]);
+    __syncwarp();
+  };
+  uint32_t nth = 0;                       // slots of values before the tile
+  uint32_t scored = 0, added = 0;         // tiles so far: scored, multiplied
+  uint32_t q_units = 0, o_units = 0;      // units so far
   bool more = true;
+#pragma unroll 1
   for (int sg = 0; more && !dead; ++sg) {
     wait(&c.seg_full[sg & 1], (sg >> 1) & 1);
     if (dead) break;
@@ -371,107 +392,104 @@ __device__ void product_warp(const PromptParams& P, uint32_t sq, uint32_t ring, 
     u.of_first = uniform(u.of_first);
     more = u.tiles > 0;
     if (!more) break;
-    Turn keys = at, values = at;  // slots of the tile whose scores, and whose products, come next (for the first tile of rows)
-    for (int half = 0; half < S::kHalves; ++half) values.next(S::kSlots);
-    auto skip = [&](Turn& t) {
-      for (int n = 0; n < 2 * S::kHalves; ++n) t.next(S::kSlots);
-    };
-    // scores of tile i of rows r, into the buffer b
-    auto scores = [&](int r, int b, int i, Turn t) {
-      if (i == 0) wait(&c.q_full[r], q_units[r] & 1);
-      if (scored[b] > 0) wait(&c.pv_done[b], (scored[b] - 1) & 1);  // its weights are in the same columns
-      ++scored[b];
+    const int n = tiles_of(u, r);
+#pragma unroll 1
+    for (int i = products && !scores ? 0 : -1; i < u.tiles && !dead; ++i) {
+      if (products && i >= 0) {
+        if (i < n) {
+          const uint32_t b = S::TILES == 2 ? (uint32_t)r : added & 1, use = S::TILES == 2 ? added : added >> 1;
+          if (i == 0) {
+            wait(&c.o_free[r], (o_units & 1) ^ 1);
+            ++o_units;
+          }
+          const bool cut = cuts(P, u, base_of(u, i));
+          Turn t = values;
 #pragma unroll
-      for (int half = 0; half < S::kHalves; ++half) {
-        wait(&c.full[t.slot], t.parity);
-        if (dead) return;
-        fence_after();
-        const uint32_t q = operand_low(sq + r * S::kQ + half * (S::kWide / 64) * S::kRun, 0), k = operand_low(ring + t.slot * S::kSlot, 0);
+          for (int half = 0; half < S::kHalves; ++half) {
+            wait(&c.full[t.slot], t.parity);
+            if (cut) wait(&c.ready[(nth + half) % kMaxSlots], parity_of(nth + half));
+            t.next(S::kSlots);
+          }
+          wait(&c.p_full[b], use & 1);
+          ++added;
+          if (dead) break;
+          fence_after();
+          const bool slow = cut && uniform(is_slow<S>(c, nth)), more_tiles = uniform(i != 0);
+          const uint32_t o = uniform(tmem + S::kOut + r * S::D), w = uniform(tmem + b * kKeys);
+          t = values;
+          const uint32_t v0 = uniform(operand_low(ring + t.slot * S::kSlot, S::kRun));
+          unsigned long long* const e0 = &c.empty[t.slot];
+          t.next(S::kSlots);
+          const uint32_t v1 = S::kHalves == 2 ? uniform(operand_low(ring + t.slot * S::kSlot, S::kRun)) : 0;
+          unsigned long long* const e1 = &c.empty[t.slot];
+          if (elected()) {
+            if (!slow) {
 #pragma unroll
-        for (int n = 0; n < S::kWide / 16; ++n) {
-          const uint32_t step = ((n >> 2) * S::kRun + (n & 3) * 32) >> 4;
-          mma_ss(leader, tmem + b * kKeys, q + step, k + step, S::kScores, half + n != 0);
+              for (int k = 0; k < kKeys / 16; ++k) mma_ts(o, w + k * 8, v0 + k * (2048 >> 4), S::kValues, more_tiles || k != 0);
+            }
+            commit(e0);
+            if constexpr (S::kHalves == 2) {
+              if (!slow) {
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k) mma_ts(o + S::kWide, w + k * 8, v1 + k * (2048 >> 4), S::kValues, more_tiles || k != 0);
+              }
+              commit(e1);
+            }
+            commit(&c.pv_done[b]);
+          }
+          __syncwarp();
+        } else {
+          pass(values);
         }
-        if (r + 1 == u.live) commit(leader, &c.empty[t.slot]);
-        t.next(S::kSlots);
+        skip(values);
+        nth += S::kHalves;
       }
-      commit(leader, &c.s_full[b]);
-      if (i + 1 == tiles_of(u, r)) {
-        commit(leader, &c.q_free[r]);
-        ++q_units[r];
-      }
-    };
-    auto products = [&](int r, int b, int i, Turn t) {
-      if (i == 0) {
-        if (o_units[r] > 0) wait(&c.o_free[r], (o_units[r] - 1) & 1);
-        ++o_units[r];
-      }
-      const uint32_t n = nth + i * S::kHalves;
-      const bool cut = cuts(P, u, base_of(u, i));
-      Turn s = t;
+      const int next = i + 1;
+      if (scores && next < u.tiles && !dead) {
+        if (next < n) {
+          const uint32_t b = S::TILES == 2 ? (uint32_t)r : scored & 1, use = S::TILES == 2 ? scored : scored >> 1;
+          if (next == 0) {
+            wait(&c.q_full[r], q_units & 1);
+            ++q_units;
+          }
+          wait(&c.pv_done[b], (use & 1) ^ 1);  // its last weights are in the same columns
+          ++scored;
+          Turn t = keys;
+          const uint32_t d = uniform(tmem + b * kKeys);
 #pragma unroll
-      for (int half = 0; half < S::kHalves; ++half) {
-        wait(&c.full[s.slot], s.parity);
-        if (cut) wait(&c.ready[(n + half) % kMaxSlots], parity_of(n + half));
-        s.next(S::kSlots);
-      }
-      wait(&c.p_full[b], added[b] & 1);
-      ++added[b];
-      if (dead) return;
-      fence_after();
-      const bool slow = cut && uniform(is_slow<S>(c, n));
+          for (int half = 0; half < S::kHalves; ++half) {
+            wait(&c.full[t.slot], t.parity);
+            if (dead) break;
+            fence_after();
+            const uint32_t q = uniform(operand_low(sq + r * S::kQ + half * (S::kWide / 64) * S::kRun, 0)),
+                           k = uniform(operand_low(ring + t.slot * S::kSlot, 0));
+            if (elected()) {
 #pragma unroll
-      for (int half = 0; half < S::kHalves; ++half) {
-        if (!slow) {
-          const uint32_t v = operand_low(ring + t.slot * S::kSlot, S::kRun);
-#pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            mma_ts(leader, tmem + S::kOut + r * S::D + half * S::kWide, tmem + b * kKeys + k * 8, v + k * (2048 >> 4), S::kValues, i != 0 || k != 0);
-        }
-        if (r + 1 == u.live) commit(leader, &c.empty[t.slot]);
-        t.next(S::kSlots);
-      }
-      commit(leader, &c.pv_done[b]);
-    };
-    if constexpr (S::TILES == 2) {
-      scores(0, 0, 0, keys);
-      if (u.live > 1) scores(1, 1, 0, keys);
-      skip(keys);
-      for (int i = 0; i < u.tiles && !dead; ++i) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int n = tiles_of(u, r);
-          if (i < n && !dead) products(r, r, i, values);
-          if (i + 1 < n && !dead) scores(r, r, i + 1, keys);
+              for (int x = 0; x < S::kWide / 16; ++x) {
+                const uint32_t step = ((x >> 2) * S::kRun + (x & 3) * 32) >> 4;
+                mma_ss(d, q + step, k + step, S::kScores, half + x != 0);
+              }
+              if (half + 1 == S::kHalves) commit(&c.s_full[b]);
+              commit(&c.empty[t.slot]);
+              if (half + 1 == S::kHalves && next + 1 == n) commit(&c.q_free[r]);
+            }
+            __syncwarp();
+            t.next(S::kSlots);
+          }
+          if (dead) break;
+        } else {
+          pass(keys);
         }
         skip(keys);
-        skip(values);
-      }
-    } else {
-      uint32_t b = (scored[0] + scored[1]) & 1, d = b;
-      for (int i = 0; i < 2 && i < u.tiles && !dead; ++i) {
-        scores(0, b, i, keys);
-        b ^= 1;
-        skip(keys);
-      }
-      for (int i = 0; i < u.tiles && !dead; ++i) {
-        products(0, d, i, values);
-        d ^= 1;
-        skip(values);
-        if (i + 2 < u.tiles && !dead) {
-          scores(0, b, i + 2, keys);
-          b ^= 1;
-          skip(keys);
-        }
       }
     }
-    for (int i = 0; i < u.tiles; ++i) skip(at);
-    nth += u.tiles * S::kHalves;
     __syncwarp();
-    if (leader && !dead) arrive(&c.seg_empty[sg & 1]);
+    if (!dead && elected()) arrive(&c.seg_empty[sg & 1]);
+    __syncwarp();
   }
   // nothing may be in flight when tensor memory is given back
-  commit(leader, &c.drained);
+  if (elected()) commit(&c.drained);
+  __syncwarp();
   mbar_wait(&c.drained, 0, kDrainPolls, 0u);
 }
 
@@ -749,12 +767,12 @@ __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), 1)
   if (tid == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init_n(&c.full[i], 1);
-      mbar_init_n(&c.empty[i], 1);
+      mbar_init_n(&c.empty[i], TILES);
       mbar_init_n(&c.ready[i], kGuardWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init_n(&c.seg_full[i], 1);
-      mbar_init_n(&c.seg_empty[i], S::kSoftmax + 1 + kGuardWarps);
+      mbar_init_n(&c.seg_empty[i], S::kSoftmax + 2 + kGuardWarps);
       mbar_init_n(&c.q_full[i], 1);
       mbar_init_n(&c.q_free[i], 1);
       mbar_init_n(&c.s_full[i], 1);
@@ -762,7 +780,7 @@ __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), 1)
       mbar_init_n(&c.pv_done[i], 1);
       mbar_init_n(&c.o_free[i], 4);
     }
-    mbar_init_n(&c.drained, 1);
+    mbar_init_n(&c.drained, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == S::kProduct) {
@@ -778,7 +796,9 @@ __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), 1)
   } else if (warp == S::kLoad) {
     load_warp<S>(P, &mq, &mk, &mv, smem_u32(base), smem_u32(ring), c);
   } else if (warp == S::kProduct) {
-    product_warp<S>(P, smem_u32(base), smem_u32(ring), c);
+    product_warp<S>(P, 0, smem_u32(base), smem_u32(ring), c);
+  } else if (warp == S::kProduct + 1) {
+    product_warp<S>(P, 1, smem_u32(base), smem_u32(ring), c);
   } else {
     guard_warps<S>(P, ring, c);
   }
