@@ -604,7 +604,7 @@ ss_status ss_attend_prompt(const ss_prompt_batch* b) {
   const cuuint32_t q_box[3] = {64, (cuuint32_t)P.heads, (cuuint32_t)P.tokens};
   const cuuint64_t dims[4] = {64, (cuuint64_t)b->tokens, (cuuint64_t)d / 64, (cuuint64_t)c.kv_heads};
   const int64_t k_strides[3] = {b->k_stride, 64, d}, v_strides[3] = {b->v_stride, 64, d};
-  const cuuint32_t box[4] = {64, 128, (cuuint32_t)std::min(d, 128) / 64, 1};
+  const cuuint32_t box[4] = {64, (cuuint32_t)k.keys, (cuuint32_t)std::min(d, 128) / 64, 1};
   s = encode_lines(&mq, b->q, 3, q_dims, q_strides, q_box);
   if (s == SS_OK) s = encode_lines(&mk, b->k, 4, dims, k_strides, box);
   if (s == SS_OK) s = encode_lines(&mv, b->v, 4, dims, v_strides, box);

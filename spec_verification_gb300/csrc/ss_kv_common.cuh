@@ -124,7 +124,7 @@ struct PromptParams {
 };
 struct PromptKernel {
   const void* fn;
-  int threads, tiles;  // tiles of query rows of a unit
+  int threads, tiles, keys;  // tiles of query rows of a unit, keys of a tile
   size_t smem;
 };
 PromptKernel kv_prompt_bf16(int head_dim);

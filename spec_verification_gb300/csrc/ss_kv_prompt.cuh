@@ -28,9 +28,10 @@
 //    one that not every row sees in full, values that no row sees become zeros
 //    (0 x NaN must not reach a sum), and if one that only some rows see is not
 //    finite, the tile is added key by key by the softmax warps.
-// Tensor memory: scores of two tiles at 0 and 128, outputs from 256 on.  With
-// TILES == 1 (256 columns, whose output fills the rest, or little work) the two
-// are tiles of keys in turn.
+// Tensor memory: two buffers of scores for each tile of rows, so that the next
+// tile's scores are there when one has been weighed, in the first 256 columns,
+// outputs in the others.  With two tiles of rows that leaves 64 keys to a tile;
+// 256 columns of output leave room for one tile of rows and 128 keys.
 #pragma once
 
 #include <algorithm>
@@ -41,8 +42,7 @@ namespace ss {
 namespace kv {
 namespace prompt {
 
-constexpr int kKeys = 128;       // keys of a tile
-constexpr int kMaxSlots = 8;
+constexpr int kMaxSlots = 16;
 constexpr int kGuardWarps = 1;
 
 template <class T_, int D_, int TILES_>
@@ -52,11 +52,12 @@ struct Shape {
   static constexpr int kSoftmax = 4 * TILES;                  // warps
   static constexpr int kLoad = kSoftmax, kProduct = kSoftmax + 1, kGuard = kSoftmax + 3;
   static constexpr int kThreads = 32 * (kGuard + kGuardWarps);
+  static constexpr int kKeys = TILES == 2 ? 64 : 128;         // keys of a tile
   static constexpr int kWide = D < 128 ? D : 128;             // columns of a slot
   static constexpr int kHalves = D / kWide;                   // slots of a tile
-  static constexpr int kRun = kKeys * 128;                    // bytes of 64 columns of 128 rows
+  static constexpr int kRun = kKeys * 128, kQRun = 128 * 128; // bytes of 64 columns of a tile, of a tile of rows
   static constexpr int kSlot = kWide / 64 * kRun;
-  static constexpr int kQ = D / 64 * kRun;                    // bytes of the queries of a tile of rows
+  static constexpr int kQ = D / 64 * kQRun;                   // bytes of the queries of a tile of rows
   static constexpr int kOut = 256;
   // slots: as many as there is room for beside the queries and the control block
   static constexpr int kFit = (227 * 1024 - 1024 - 2048 - TILES * kQ) / kSlot;
@@ -66,7 +67,7 @@ struct Shape {
   static constexpr uint32_t kScores = kCommon | (kKeys >> 3) << 17;
   static constexpr uint32_t kValues = kCommon | 1u << 16 | (uint32_t)(kWide >> 3) << 17;
   static_assert(kSlots >= 2 * kHalves + 1, "ring length");
-  static_assert(kOut + TILES * D <= 512, "tensor memory");
+  static_assert(2 * TILES * kKeys == kOut && kOut + TILES * D <= 512, "tensor memory");
 };
 
 struct Unit {
@@ -77,11 +78,15 @@ struct Unit {
   int of_first;              // key tiles of the first tile of rows (the last one has all)
   int pos1;                  // last token of the unit
 };
-__device__ __forceinline__ int base_of(const Unit& u, int i) { return (i < u.sink ? i : i - u.sink + u.first) * kKeys; }
+template <class S>
+__device__ __forceinline__ int base_of(const Unit& u, int i) {
+  return (i < u.sink ? i : i - u.sink + u.first) * S::kKeys;
+}
 __device__ __forceinline__ int tiles_of(const Unit& u, int r) { return r + 1 < u.live ? u.of_first : r < u.live ? u.tiles : 0; }
 // Does some live row of the unit not see all keys of the tile at `base`?
+template <class S>
 __device__ __forceinline__ bool cuts(const PromptParams& P, const Unit& u, int base) {
-  return base + kKeys - 1 > u.t0 || (P.window > 0 && base <= u.pos1 - P.window && base > P.sinks - kKeys);
+  return base + S::kKeys - 1 > u.t0 || (P.window > 0 && base <= u.pos1 - P.window && base > P.sinks - S::kKeys);
 }
 
 struct Control {
@@ -91,7 +96,7 @@ struct Control {
   unsigned long long ready[kMaxSlots];
   unsigned long long seg_full[2], seg_empty[2];
   unsigned long long q_full[2], q_free[2];
-  unsigned long long s_full[2], p_full[2], pv_done[2];  // scores there; weights there; added to the output
+  unsigned long long s_full[4], p_full[4], pv_done[4];  // by buffer: scores there; weights there; added to the output
   unsigned long long o_free[2];
   unsigned long long drained;
   Unit unit[2];
@@ -136,10 +141,10 @@ struct Cursor {
         g.chunk = kind % P.chunks;
         g.pos1 = min(g.n, g.t0 + per) - 1;
         g.live = (g.pos1 - g.t0) / P.tokens + 1;
-        g.first = P.window > 0 ? max(0, g.t0 - P.window + 1) / kKeys : 0;
-        g.sink = P.window > 0 ? min((P.sinks + kKeys - 1) / kKeys, g.first) : 0;
-        g.tiles = g.sink + g.pos1 / kKeys - g.first + 1;
-        g.of_first = g.sink + min(g.pos1, g.t0 + P.tokens - 1) / kKeys - g.first + 1;
+        g.first = P.window > 0 ? max(0, g.t0 - P.window + 1) / S::kKeys : 0;
+        g.sink = P.window > 0 ? min((P.sinks + S::kKeys - 1) / S::kKeys, g.first) : 0;
+        g.tiles = g.sink + g.pos1 / S::kKeys - g.first + 1;
+        g.of_first = g.sink + min(g.pos1, g.t0 + P.tokens - 1) / S::kKeys - g.first + 1;
         return true;
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
@@ -191,7 +196,7 @@ __device__ void load_warp(const PromptParams& P, const CUtensorMap* mq, const CU
         asm volatile(
             "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
                 ring + turn.slot * S::kSlot),
-            "l"(values ? mv : mk), "r"(0), "r"(g.q0 + base_of(g, i)), "r"(half * (S::kWide / 64)), "r"(g.h), "r"(smem_u32(&c.full[turn.slot]))
+            "l"(values ? mv : mk), "r"(0), "r"(g.q0 + base_of<S>(g, i)), "r"(half * (S::kWide / 64)), "r"(g.h), "r"(smem_u32(&c.full[turn.slot]))
             : "memory");
       }
       __syncwarp();
@@ -212,7 +217,7 @@ __device__ void load_warp(const PromptParams& P, const CUtensorMap* mq, const CU
             for (int run = 0; run < S::D / 64; ++run)
               asm volatile(
                   "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-                      sq + r * S::kQ + run * S::kRun),
+                      sq + r * S::kQ + run * S::kQRun),
                   "l"(mq), "r"(run * 64), "r"(g.h * P.group + g.chunk * P.heads), "r"(g.q0 + g.t0 + r * P.tokens), "r"(smem_u32(&c.q_full[r]))
                   : "memory");
           }
@@ -270,14 +275,14 @@ __device__ void guard_warps(const PromptParams& P, unsigned char* ring, Control&
     more = u.tiles > 0;
     for (int i = 0; i < u.tiles && !dead; ++i) {
       for (int half = 0; half < S::kHalves; ++half) turn.next(S::kSlots);  // the keys
-      const int base = base_of(u, i);
-      const bool cut = cuts(P, u, base);
+      const int base = base_of<S>(u, i);
+      const bool cut = cuts<S>(P, u, base);
       for (int half = 0; half < S::kHalves; ++half, ++nth) {
         wait(&c.full[turn.slot], turn.parity);
         if (dead) break;
         if (cut) {
           uint32_t wild = 0;  // x * 0 is 0, or NaN if x is not finite: two values an operation
-          for (int in = tid; in < kKeys; in += 32 * kGuardWarps) {
+          for (int in = tid; in < S::kKeys; in += 32 * kGuardWarps) {
             const int key = base + in;
             const bool some = key <= u.pos1 && (P.window <= 0 || key > u.t0 - P.window || key < P.sinks);
             const bool all = key <= u.t0 && (P.window <= 0 || key > u.pos1 - P.window || key < P.sinks);
@@ -394,15 +399,15 @@ __device__ void product_warp(const PromptParams& P, int which, uint32_t sq, uint
     if (!more) break;
     const int n = tiles_of(u, r);
 #pragma unroll 1
-    for (int i = products && !scores ? 0 : -1; i < u.tiles && !dead; ++i) {
+    for (int i = products ? scores ? -2 : 0 : -1; i < u.tiles && !dead; ++i) {
       if (products && i >= 0) {
         if (i < n) {
-          const uint32_t b = S::TILES == 2 ? (uint32_t)r : added & 1, use = S::TILES == 2 ? added : added >> 1;
+          const uint32_t b = 2 * r + (added & 1), use = added >> 1;
           if (i == 0) {
             wait(&c.o_free[r], (o_units & 1) ^ 1);
             ++o_units;
           }
-          const bool cut = cuts(P, u, base_of(u, i));
+          const bool cut = cuts<S>(P, u, base_of<S>(u, i));
           Turn t = values;
 #pragma unroll
           for (int half = 0; half < S::kHalves; ++half) {
@@ -415,7 +420,7 @@ __device__ void product_warp(const PromptParams& P, int which, uint32_t sq, uint
           if (dead) break;
           fence_after();
           const bool slow = cut && uniform(is_slow<S>(c, nth)), more_tiles = uniform(i != 0);
-          const uint32_t o = uniform(tmem + S::kOut + r * S::D), w = uniform(tmem + b * kKeys);
+          const uint32_t o = uniform(tmem + S::kOut + r * S::D), w = uniform(tmem + b * S::kKeys);
           t = values;
           const uint32_t v0 = uniform(operand_low(ring + t.slot * S::kSlot, S::kRun));
           unsigned long long* const e0 = &c.empty[t.slot];
@@ -425,13 +430,13 @@ __device__ void product_warp(const PromptParams& P, int which, uint32_t sq, uint
           if (elected()) {
             if (!slow) {
 #pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k) mma_ts(o, w + k * 8, v0 + k * (2048 >> 4), S::kValues, more_tiles || k != 0);
+              for (int k = 0; k < S::kKeys / 16; ++k) mma_ts(o, w + k * 8, v0 + k * (2048 >> 4), S::kValues, more_tiles || k != 0);
             }
             commit(e0);
             if constexpr (S::kHalves == 2) {
               if (!slow) {
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k) mma_ts(o + S::kWide, w + k * 8, v1 + k * (2048 >> 4), S::kValues, more_tiles || k != 0);
+                for (int k = 0; k < S::kKeys / 16; ++k) mma_ts(o + S::kWide, w + k * 8, v1 + k * (2048 >> 4), S::kValues, more_tiles || k != 0);
               }
               commit(e1);
             }
@@ -444,10 +449,10 @@ __device__ void product_warp(const PromptParams& P, int which, uint32_t sq, uint
         skip(values);
         nth += S::kHalves;
       }
-      const int next = i + 1;
+      const int next = S::TILES == 2 ? i + 2 : i + 1;
       if (scores && next < u.tiles && !dead) {
         if (next < n) {
-          const uint32_t b = S::TILES == 2 ? (uint32_t)r : scored & 1, use = S::TILES == 2 ? scored : scored >> 1;
+          const uint32_t b = 2 * r + (scored & 1), use = scored >> 1;
           if (next == 0) {
             wait(&c.q_full[r], q_units & 1);
             ++q_units;
@@ -455,19 +460,19 @@ __device__ void product_warp(const PromptParams& P, int which, uint32_t sq, uint
           wait(&c.pv_done[b], (use & 1) ^ 1);  // its last weights are in the same columns
           ++scored;
           Turn t = keys;
-          const uint32_t d = uniform(tmem + b * kKeys);
+          const uint32_t d = uniform(tmem + b * S::kKeys);
 #pragma unroll
           for (int half = 0; half < S::kHalves; ++half) {
             wait(&c.full[t.slot], t.parity);
             if (dead) break;
             fence_after();
-            const uint32_t q = uniform(operand_low(sq + r * S::kQ + half * (S::kWide / 64) * S::kRun, 0)),
+            const uint32_t q = uniform(operand_low(sq + r * S::kQ + half * (S::kWide / 64) * S::kQRun, 0)),
                            k = uniform(operand_low(ring + t.slot * S::kSlot, 0));
             if (elected()) {
 #pragma unroll
               for (int x = 0; x < S::kWide / 16; ++x) {
-                const uint32_t step = ((x >> 2) * S::kRun + (x & 3) * 32) >> 4;
-                mma_ss(d, q + step, k + step, S::kScores, half + x != 0);
+                const uint32_t run = x >> 2, in = (x & 3) * 32 >> 4;
+                mma_ss(d, q + run * (S::kQRun >> 4) + in, k + run * (S::kRun >> 4) + in, S::kScores, half + x != 0);
               }
               if (half + 1 == S::kHalves) commit(&c.s_full[b]);
               commit(&c.empty[t.slot]);
@@ -514,13 +519,12 @@ struct Seen {
   __device__ __forceinline__ bool operator()(int n) const { return n < end && (n >= start || n < sinks); }
 };
 
-// A row's weights of one tile where m is large (see ss_kv_attend.cuh), over its scores; returns their sum as rounded and as
-// they are.
-template <class E, bool TWO>
-static __device__ __noinline__ float2 large_weights(uint32_t at, float scale, float z, Seen sees) {
-  float rounded = 0.0f, exact = 0.0f;
+// A row's weights of one tile where m is large (see ss_kv_attend.cuh), over its scores; returns their sum.
+template <class E, int KEYS>
+static __device__ __noinline__ float large_weights(uint32_t at, float scale, float z, Seen sees) {
+  float sum = 0.0f;
 #pragma unroll 1
-  for (int i = 0; i < kKeys; i += 16) {
+  for (int i = 0; i < KEYS; i += 16) {
     uint32_t x[16], w[8];
     tmem_load(x, at + i);
 #pragma unroll
@@ -529,23 +533,20 @@ static __device__ __noinline__ float2 large_weights(uint32_t at, float scale, fl
 #pragma unroll
       for (int h = 0; h < 2; ++h) y[h] = sees(i + n + h) ? ex2(__fsub_rn(__fmul_rn(__uint_as_float(x[n + h]), scale), z)) : 0.0f;
       w[n / 2] = E::pack(y[0], y[1]);
-      const float2 r = TWO ? E::unpack(w[n / 2]) : make_float2(y[0], y[1]);
-      rounded += r.x + r.y;
-      exact += y[0] + y[1];
+      sum += y[0] + y[1];
     }
     tmem_store(at + i / 2, w);
   }
-  return make_float2(rounded, exact);
+  return sum;
 }
 
 // Adds a tile whose values are not all finite to the output, key by key and only for the rows that see it.
 template <class S>
-static __device__ __noinline__ void add_by_key(uint32_t scores, uint32_t out, const unsigned char* ring, Turn turn, Seen sees, bool first) {
+static __device__ __noinline__ void add_by_key(uint32_t scores, uint32_t out, const unsigned char* ring, uint32_t slot, Seen sees, bool first) {
   using E = Elem<typename S::T>;
 #pragma unroll 1
   for (int half = 0; half < S::kHalves; ++half) {
-    const unsigned char* values = ring + turn.slot * S::kSlot;
-    turn.next(S::kSlots);
+    const unsigned char* values = ring + (slot + half) % S::kSlots * S::kSlot;
 #pragma unroll 1
     for (int d = 0; d < S::kWide; d += 32) {
       uint32_t o[32];
@@ -554,7 +555,7 @@ static __device__ __noinline__ void add_by_key(uint32_t scores, uint32_t out, co
 #pragma unroll
       for (int n = 0; n < 32; ++n) acc[n] = first ? 0.0f : __uint_as_float(o[n]);
 #pragma unroll 1
-      for (int n = 0; n < kKeys; ++n) {
+      for (int n = 0; n < S::kKeys; ++n) {
         uint32_t pair[1];
         tmem_load(pair, scores + (n >> 1));
         const float2 ws = E::unpack(pair[0]);
@@ -597,14 +598,12 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
   auto wait = [&](unsigned long long* b, uint32_t parity) {
     if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(b, parity, P.spin_limit, 0u));
   };
-  Turn at;          // slots of the unit's first tile
-  uint32_t nth = 0; // slots of values before the unit
-  uint32_t it = 0;  // tiles weighed so far
-  // the buffer of tile `tile` and which use of it that is
-  auto buffer = [&](uint32_t tile) { return S::TILES == 2 ? (uint32_t)r : tile & 1; };
-  auto use = [&](uint32_t tile) { return S::TILES == 2 ? tile : tile >> 1; };
+  uint32_t nth = 0;  // slots of values before the unit
+  uint32_t it = 0;   // tiles weighed so far
+  // the slot of values number n: of the CTA's slots every 2 * kHalves bring a tile's keys, then its values
+  auto slot_of = [](uint32_t n) { return (n / S::kHalves * 2 * S::kHalves + S::kHalves + n % S::kHalves) % S::kSlots; };
   auto added = [&](uint32_t tile) {  // the output holds everything up to this tile
-    wait(&c.pv_done[buffer(tile)], use(tile) & 1);
+    wait(&c.pv_done[2 * r + (tile & 1)], (tile >> 1) & 1);
     fence_after();
   };
   bool more = true;
@@ -618,20 +617,14 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
     const bool live = m < P.heads * P.tokens && pos <= u.pos1 && head < P.group;
     float mx = -INFINITY, l = 0.0f;
     bool large = false;
-    Turn turn = at;
-    for (int i = 0; i < u.tiles; ++i)
-      for (int n = 0; n < 2 * S::kHalves; ++n) at.next(S::kSlots);
     for (int i = 0; i < count && !dead; ++i, ++it) {
-      const uint32_t b = buffer(it), buf = lanes + b * kKeys;
-      const int base = base_of(u, i);
-      const bool cut = cuts(P, u, base);
-      for (int half = 0; half < S::kHalves; ++half) turn.next(S::kSlots);
-      const Turn v_turn = turn;
-      for (int half = 0; half < S::kHalves; ++half) turn.next(S::kSlots);
-      wait(&c.s_full[b], use(it) & 1);
+      const uint32_t b = 2 * r + (it & 1), buf = lanes + b * S::kKeys;
+      const int base = base_of<S>(u, i);
+      const bool cut = cuts<S>(P, u, base);
+      wait(&c.s_full[b], (it >> 1) & 1);
       if (dead) break;
       fence_after();
-      Seen sees = {kKeys, 0, 0};
+      Seen sees = {S::kKeys, 0, 0};
       if (cut) {
         sees.end = live ? pos + 1 - base : 0;
         if (P.window > 0) {
@@ -639,8 +632,8 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
           sees.sinks = P.sinks - base;
         }
       }
-      // Scores are read twice, a part at a time: a row's 128 do not stay in registers beside the rest.  Half of them do.
-      uint32_t x[64], y[32];
+      // (128 scores are read twice, a part at a time: they do not stay in registers beside the rest, but half of them do)
+      uint32_t x[64];
       float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       auto hide = [&](uint32_t* w, int from, int count) {
 #pragma unroll
@@ -653,9 +646,11 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
 #pragma unroll
           for (int h = 0; h < 4; ++h) t[h] = fmaxf(t[h], fmaxf(__uint_as_float(w[n + h]), __uint_as_float(w[n + 4 + h])));
       };
-      tmem_load(x, buf + 64);
-      if (cut) hide(x, 64, 64);
-      largest(x, 64);
+      if constexpr (S::kKeys == 128) {
+        tmem_load(x, buf + 64);
+        if (cut) hide(x, 64, 64);
+        largest(x, 64);
+      }
       tmem_load(x, buf);
       if (cut) hide(x, 0, 64);
       largest(x, 64);
@@ -682,7 +677,7 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
       }
       const float z = mx == -INFINITY ? 0.0f : mx;
       if (large) {
-        l += large_weights<E, false>(buf, scale, z, sees).y;
+        l += large_weights<E, S::kKeys>(buf, scale, z, sees);
       } else {
         uint64_t s0 = 0, s1 = 0;  // sums of even and odd keys
         const uint64_t by = pair(scale, scale), less = pair(-z, -z);
@@ -702,7 +697,8 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
         weigh(x, 0);
         weigh(x + 32, 32);
 #pragma unroll
-        for (int q = 64; q < 128; q += 32) {
+        for (int q = 64; q < S::kKeys; q += 32) {
+          uint32_t y[32];
           tmem_load(y, buf + q);
           if (cut) hide(y, q, 32);
           weigh(y, q);
@@ -716,7 +712,7 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
         for (int half = 0; half < S::kHalves; ++half) wait(&c.ready[(n + half) % kMaxSlots], parity_of(n + half));
         if (!dead && is_slow<S>(c, n)) {
           if (i > 0) added(it - 1);
-          add_by_key<S>(buf, out_at, ring, v_turn, sees, i == 0);
+          add_by_key<S>(buf, out_at, ring, slot_of(n), sees, i == 0);
         }
       }
       fence_before();
@@ -770,14 +766,16 @@ __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), 1)
       mbar_init_n(&c.empty[i], TILES);
       mbar_init_n(&c.ready[i], kGuardWarps);
     }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init_n(&c.s_full[i], 1);
+      mbar_init_n(&c.p_full[i], 4);
+      mbar_init_n(&c.pv_done[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init_n(&c.seg_full[i], 1);
       mbar_init_n(&c.seg_empty[i], S::kSoftmax + 2 + kGuardWarps);
       mbar_init_n(&c.q_full[i], 1);
       mbar_init_n(&c.q_free[i], 1);
-      mbar_init_n(&c.s_full[i], 1);
-      mbar_init_n(&c.p_full[i], 4);
-      mbar_init_n(&c.pv_done[i], 1);
       mbar_init_n(&c.o_free[i], 4);
     }
     mbar_init_n(&c.drained, 2);
@@ -822,7 +820,7 @@ __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), 1)
 template <class T, int D, int TILES>
 PromptKernel entry() {
   using S = Shape<T, D, TILES>;
-  return {reinterpret_cast<const void*>(&prompt_kernel<T, D, TILES>), S::kThreads, TILES, (size_t)S::kSmem};
+  return {reinterpret_cast<const void*>(&prompt_kernel<T, D, TILES>), S::kThreads, TILES, S::kKeys, (size_t)S::kSmem};
 }
 template <class T>
 PromptKernel pick(int d) {
