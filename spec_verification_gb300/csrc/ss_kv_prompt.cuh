@@ -21,7 +21,7 @@
 // A CTA's warps:
 //  - load: takes units, publishes them, runs the ring of key and value tiles
 //    (TMA) and brings their queries (TMA; a box of heads by tokens).
-//  - product: two warps issue tcgen05.mma.
+//  - scores and values: two warps for each tile of rows issue tcgen05.mma.
 //  - softmax: four warps to a tile of rows; a thread owns a row (a lane of
 //    tensor memory), reads its 128 scores, writes its weights over them.
 //  - guard: a warp looks at every tile of values before the products do.  In
@@ -50,7 +50,8 @@ struct Shape {
   using T = T_;
   static constexpr int D = D_, TILES = TILES_;
   static constexpr int kSoftmax = 4 * TILES;                  // warps
-  static constexpr int kLoad = kSoftmax, kProduct = kSoftmax + 1, kGuard = kSoftmax + 3;
+  static constexpr int kProducts = 2 * TILES;
+  static constexpr int kLoad = kSoftmax, kProduct = kSoftmax + 1, kGuard = kProduct + kProducts;
   static constexpr int kThreads = 32 * (kGuard + kGuardWarps);
   static constexpr int kKeys = TILES == 2 ? 64 : 128;         // keys of a tile
   static constexpr int kWide = D < 128 ? D : 128;             // columns of a slot
@@ -360,142 +361,166 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
       : "memory");
 }
 
-// Two warps.  TILES == 2: one for each tile of rows, so that one's waits and issuing overlap the other's products;
-// TILES == 1: one for the scores, one for the products with the values.
+// What the product warps have in common: their waits, and the slots that they go through.
 template <class S>
-__device__ void product_warp(const PromptParams& P, int which, uint32_t sq, uint32_t ring, Control& c) {
-  const uint32_t tmem = uniform(c.tmem);
-  const int r = S::TILES == 2 ? which : 0;
-  const bool scores = S::TILES == 2 || which == 0, products = S::TILES == 2 || which == 1;
+struct Issuer {
+  const PromptParams& P;
+  Control& c;
   bool dead = false;
-  auto wait = [&](unsigned long long* m, uint32_t parity) {
+  Turn turn;  // of the next slot
+  __device__ __forceinline__ Issuer(const PromptParams& P_, Control& c_) : P(P_), c(c_) {}
+  __device__ __forceinline__ void wait(unsigned long long* m, uint32_t parity) {
     if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(m, parity, P.spin_limit, 0u));
-  };
-  Turn keys, values;  // slots of the tile whose scores, and whose products, come next
-  for (int n = 0; n < S::kHalves; ++n) values.next(S::kSlots);
-  auto skip = [&](Turn& t) {
+  }
+  // Looks at two barriers overlap; one after the other they take twice the time even if both phases are done.
+  __device__ __forceinline__ void wait(unsigned long long* m, uint32_t m_parity, unsigned long long* n, uint32_t n_parity) {
+    const bool first = done(m, m_parity), second = done(n, n_parity);
+    if (!__all_sync(0xffffffffu, first)) wait(m, m_parity);
+    if (!__all_sync(0xffffffffu, second)) wait(n, n_parity);
+  }
+  // A tile that this warp has no use for: the release by the other tile of rows' warp is not to stand for both.
+  __device__ __forceinline__ void pass() {
+    Turn t = turn;
 #pragma unroll
-    for (int n = 0; n < 2 * S::kHalves; ++n) t.next(S::kSlots);
-  };
-  // A slot that this warp has no use for: the other one's release is not to stand for both.
-  auto pass = [&](const Turn& t) {
-    wait(&c.full[t.slot], t.parity);
-    if (!dead && elected()) arrive(&c.empty[t.slot]);
-    __syncwarp();
-  };
-  uint32_t nth = 0;                       // slots of values before the tile
-  uint32_t scored = 0, added = 0;         // tiles so far: scored, multiplied
-  uint32_t q_units = 0, o_units = 0;      // units so far
-  bool more = true;
-#pragma unroll 1
-  for (int sg = 0; more && !dead; ++sg) {
-    wait(&c.seg_full[sg & 1], (sg >> 1) & 1);
-    if (dead) break;
-    Unit u = c.unit[sg & 1];
-    u.tiles = uniform(u.tiles);
-    u.live = uniform(u.live);
-    u.of_first = uniform(u.of_first);
-    more = u.tiles > 0;
-    if (!more) break;
-    const int n = tiles_of(u, r);
-#pragma unroll 1
-    for (int i = products ? scores ? -2 : 0 : -1; i < u.tiles && !dead; ++i) {
-      if (products && i >= 0) {
-        if (i < n) {
-          const uint32_t b = 2 * r + (added & 1), use = added >> 1;
-          if (i == 0) {
-            wait(&c.o_free[r], (o_units & 1) ^ 1);
-            ++o_units;
-          }
-          const bool cut = cuts<S>(P, u, base_of<S>(u, i));
-          Turn t = values;
-#pragma unroll
-          for (int half = 0; half < S::kHalves; ++half) {
-            wait(&c.full[t.slot], t.parity);
-            if (cut) wait(&c.ready[(nth + half) % kMaxSlots], parity_of(nth + half));
-            t.next(S::kSlots);
-          }
-          wait(&c.p_full[b], use & 1);
-          ++added;
-          if (dead) break;
-          fence_after();
-          const bool slow = cut && uniform(is_slow<S>(c, nth)), more_tiles = uniform(i != 0);
-          const uint32_t o = uniform(tmem + S::kOut + r * S::D), w = uniform(tmem + b * S::kKeys);
-          t = values;
-          const uint32_t v0 = uniform(operand_low(ring + t.slot * S::kSlot, S::kRun));
-          unsigned long long* const e0 = &c.empty[t.slot];
-          t.next(S::kSlots);
-          const uint32_t v1 = S::kHalves == 2 ? uniform(operand_low(ring + t.slot * S::kSlot, S::kRun)) : 0;
-          unsigned long long* const e1 = &c.empty[t.slot];
-          if (elected()) {
-            if (!slow) {
-#pragma unroll
-              for (int k = 0; k < S::kKeys / 16; ++k) mma_ts(o, w + k * 8, v0 + k * (2048 >> 4), S::kValues, more_tiles || k != 0);
-            }
-            commit(e0);
-            if constexpr (S::kHalves == 2) {
-              if (!slow) {
-#pragma unroll
-                for (int k = 0; k < S::kKeys / 16; ++k) mma_ts(o + S::kWide, w + k * 8, v1 + k * (2048 >> 4), S::kValues, more_tiles || k != 0);
-              }
-              commit(e1);
-            }
-            commit(&c.pv_done[b]);
-          }
-          __syncwarp();
-        } else {
-          pass(values);
-        }
-        skip(values);
-        nth += S::kHalves;
-      }
-      const int next = S::TILES == 2 ? i + 2 : i + 1;
-      if (scores && next < u.tiles && !dead) {
-        if (next < n) {
-          const uint32_t b = 2 * r + (scored & 1), use = scored >> 1;
-          if (next == 0) {
-            wait(&c.q_full[r], q_units & 1);
-            ++q_units;
-          }
-          wait(&c.pv_done[b], (use & 1) ^ 1);  // its last weights are in the same columns
-          ++scored;
-          Turn t = keys;
-          const uint32_t d = uniform(tmem + b * S::kKeys);
-#pragma unroll
-          for (int half = 0; half < S::kHalves; ++half) {
-            wait(&c.full[t.slot], t.parity);
-            if (dead) break;
-            fence_after();
-            const uint32_t q = uniform(operand_low(sq + r * S::kQ + half * (S::kWide / 64) * S::kQRun, 0)),
-                           k = uniform(operand_low(ring + t.slot * S::kSlot, 0));
-            if (elected()) {
-#pragma unroll
-              for (int x = 0; x < S::kWide / 16; ++x) {
-                const uint32_t run = x >> 2, in = (x & 3) * 32 >> 4;
-                mma_ss(d, q + run * (S::kQRun >> 4) + in, k + run * (S::kRun >> 4) + in, S::kScores, half + x != 0);
-              }
-              if (half + 1 == S::kHalves) commit(&c.s_full[b]);
-              commit(&c.empty[t.slot]);
-              if (half + 1 == S::kHalves && next + 1 == n) commit(&c.q_free[r]);
-            }
-            __syncwarp();
-            t.next(S::kSlots);
-          }
-          if (dead) break;
-        } else {
-          pass(keys);
-        }
-        skip(keys);
-      }
+    for (int half = 0; half < S::kHalves; ++half) {
+      wait(&c.full[t.slot], t.parity);
+      if (!dead && elected()) arrive(&c.empty[t.slot]);
+      __syncwarp();
+      t.next(S::kSlots);
     }
+  }
+  __device__ __forceinline__ void skip() {  // to the next tile of the same kind
+#pragma unroll
+    for (int n = 0; n < 2 * S::kHalves; ++n) turn.next(S::kSlots);
+  }
+  // The next unit: its tiles, and those of tile of rows r; false at the end.
+  __device__ __forceinline__ bool next(int sg, int r, Unit& u, int& n) {
+    wait(&c.seg_full[sg & 1], (sg >> 1) & 1);
+    if (dead) return false;
+    u = c.unit[sg & 1];
+    n = uniform(tiles_of(u, r));
+    u.tiles = uniform(u.tiles);
+    return u.tiles > 0;
+  }
+  __device__ __forceinline__ void end(int sg) {
     __syncwarp();
     if (!dead && elected()) arrive(&c.seg_empty[sg & 1]);
     __syncwarp();
   }
   // nothing may be in flight when tensor memory is given back
-  if (elected()) commit(&c.drained);
-  __syncwarp();
-  mbar_wait(&c.drained, 0, kDrainPolls, 0u);
+  __device__ __forceinline__ void drain() {
+    if (elected()) commit(&c.drained);
+    __syncwarp();
+    mbar_wait(&c.drained, 0, kDrainPolls, 0u);
+  }
+};
+
+// S = Q K^T of tile of rows r, two tiles of keys ahead of the products with the values.  (A warp for each of the two kinds
+// of products and each tile of rows: what they wait for and the time it takes to issue overlap the others' products.)
+template <class S>
+__device__ void scores_warp(const PromptParams& P, int r, uint32_t sq, uint32_t ring, Control& c) {
+  Issuer<S> w(P, c);
+  const uint32_t tmem = c.tmem + 2 * r * S::kKeys, q = uniform(operand_low(sq + r * S::kQ, 0));
+  uint32_t it = 0, q_units = 0;  // tiles scored, units begun
+  Unit u;
+  int n;
+#pragma unroll 1
+  for (int sg = 0; w.next(sg, r, u, n); ++sg) {
+    if (n > 0) w.wait(&c.q_full[r], q_units++ & 1);
+#pragma unroll 1
+    for (int i = 0; i < u.tiles && !w.dead; ++i) {
+      if (i < n) {
+        const uint32_t b = it & 1;
+        unsigned long long* const there = &c.s_full[2 * r + b];
+        const uint32_t d = uniform(tmem + b * S::kKeys);
+        Turn t = w.turn;
+#pragma unroll
+        for (int half = 0; half < S::kHalves; ++half) {
+          // the keys, and the weights of two tiles ago, which are in the same columns
+          if (half == 0) w.wait(&c.full[t.slot], t.parity, &c.pv_done[2 * r + b], ((it >> 1) & 1) ^ 1);
+          else w.wait(&c.full[t.slot], t.parity);
+          if (w.dead) break;
+          fence_after();
+          const uint32_t k = uniform(operand_low(ring + t.slot * S::kSlot, 0));
+          if (elected()) {
+#pragma unroll
+            for (int x = 0; x < S::kWide / 16; ++x) {
+              const uint32_t run = x >> 2, in = (x & 3) * 32 >> 4;
+              mma_ss(d, q + (half * (S::kWide / 64) + run) * (S::kQRun >> 4) + in, k + run * (S::kRun >> 4) + in, S::kScores, half + x != 0);
+            }
+            if (half + 1 == S::kHalves) commit(there);
+            commit(&c.empty[t.slot]);
+            if (half + 1 == S::kHalves && i + 1 == n) commit(&c.q_free[r]);
+          }
+          __syncwarp();
+          t.next(S::kSlots);
+        }
+        ++it;
+      } else {
+        w.pass();
+      }
+      w.skip();
+    }
+    w.end(sg);
+  }
+  w.drain();
+}
+
+// O += P V of tile of rows r.
+template <class S>
+__device__ void values_warp(const PromptParams& P, int r, uint32_t ring, Control& c) {
+  Issuer<S> w(P, c);
+  for (int half = 0; half < S::kHalves; ++half) w.turn.next(S::kSlots);
+  const uint32_t tmem = c.tmem + 2 * r * S::kKeys, o = uniform(c.tmem + S::kOut + r * S::D);
+  uint32_t it = 0, o_units = 0, nth = 0;  // tiles multiplied, units begun, slots of values passed
+  Unit u;
+  int n;
+#pragma unroll 1
+  for (int sg = 0; w.next(sg, r, u, n); ++sg) {
+    if (n > 0) w.wait(&c.o_free[r], (o_units++ & 1) ^ 1);
+#pragma unroll 1
+    for (int i = 0; i < u.tiles && !w.dead; ++i, nth += S::kHalves) {
+      if (i < n) {
+        const uint32_t b = it & 1;
+        const bool cut = cuts<S>(P, u, base_of<S>(u, i));
+        unsigned long long* const added = &c.pv_done[2 * r + b];
+        const uint32_t weights = uniform(tmem + b * S::kKeys);
+        const bool more = uniform(i);
+        Turn t = w.turn;
+        bool slow = false;
+        if (cut) {
+#pragma unroll
+          for (int half = 0; half < S::kHalves; ++half) w.wait(&c.ready[(nth + half) % kMaxSlots], parity_of(nth + half));
+        }
+#pragma unroll
+        for (int half = 0; half < S::kHalves; ++half) {
+          if (half == 0) w.wait(&c.full[t.slot], t.parity, &c.p_full[2 * r + b], (it >> 1) & 1);
+          else w.wait(&c.full[t.slot], t.parity);
+          if (w.dead) break;
+          fence_after();
+          if (cut && half == 0) slow = uniform(is_slow<S>(c, nth));
+          const uint32_t v = uniform(operand_low(ring + t.slot * S::kSlot, S::kRun));
+          if (elected()) {
+            if (!slow) {
+#pragma unroll
+              for (int k = 0; k < S::kKeys / 16; ++k)
+                mma_ts(o + half * S::kWide, weights + k * 8, v + k * (2048 >> 4), S::kValues, more || k != 0);
+            }
+            if (half + 1 == S::kHalves) commit(added);
+            commit(&c.empty[t.slot]);
+          }
+          __syncwarp();
+          t.next(S::kSlots);
+        }
+        ++it;
+      } else {
+        w.pass();
+      }
+      w.skip();
+    }
+    w.end(sg);
+  }
+  w.drain();
 }
 
 // ------------------------------------------------------------------ softmax warps
@@ -773,12 +798,12 @@ __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init_n(&c.seg_full[i], 1);
-      mbar_init_n(&c.seg_empty[i], S::kSoftmax + 2 + kGuardWarps);
+      mbar_init_n(&c.seg_empty[i], S::kSoftmax + S::kProducts + kGuardWarps);
       mbar_init_n(&c.q_full[i], 1);
       mbar_init_n(&c.q_free[i], 1);
       mbar_init_n(&c.o_free[i], 4);
     }
-    mbar_init_n(&c.drained, 2);
+    mbar_init_n(&c.drained, S::kProducts);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == S::kProduct) {
@@ -793,10 +818,10 @@ __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), 1)
     softmax_warps<S>(P, ring, c);
   } else if (warp == S::kLoad) {
     load_warp<S>(P, &mq, &mk, &mv, smem_u32(base), smem_u32(ring), c);
-  } else if (warp == S::kProduct) {
-    product_warp<S>(P, 0, smem_u32(base), smem_u32(ring), c);
-  } else if (warp == S::kProduct + 1) {
-    product_warp<S>(P, 1, smem_u32(base), smem_u32(ring), c);
+  } else if (warp < S::kGuard) {
+    const int n = warp - S::kProduct;
+    if (n & 1) values_warp<S>(P, n >> 1, smem_u32(ring), c);
+    else scores_warp<S>(P, n >> 1, smem_u32(base), smem_u32(ring), c);
   } else {
     guard_warps<S>(P, ring, c);
   }
