@@ -538,17 +538,29 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Which keys of a tile a row sees, by their number in it: [0, end) but for [sinks, start).
+// Which keys of a tile a row sees, as bits.
+template <int KEYS>
 struct Seen {
-  int end, start, sinks;
-  __device__ __forceinline__ bool operator()(int n) const { return n < end && (n >= start || n < sinks); }
+  uint32_t bits[KEYS / 32];
+  // those in [0, end), but for [start, end_of_sinks) of the earlier ones
+  __device__ __forceinline__ void set(int end, int start, int sinks) {
+#pragma unroll
+    for (int n = 0; n < KEYS / 32; ++n) {
+      auto below = [&](int key) {  // numbers before `key`
+        const int k = key - 32 * n;
+        return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1u;
+      };
+      bits[n] = below(end) & (~below(start) | below(sinks));
+    }
+  }
+  __device__ __forceinline__ bool operator()(int n) const { return bits[n >> 5] >> (n & 31) & 1; }
 };
 
 // A row's weights of one tile where m is large (see ss_kv_attend.cuh), over its scores; returns their sum.
 template <class E, int KEYS>
-static __device__ __noinline__ float large_weights(uint32_t at, float scale, float z, Seen sees) {
+static __device__ __noinline__ float large_weights(uint32_t at, float scale, float z, Seen<KEYS> sees) {
   float sum = 0.0f;
-#pragma unroll 1
+#pragma unroll
   for (int i = 0; i < KEYS; i += 16) {
     uint32_t x[16], w[8];
     tmem_load(x, at + i);
@@ -565,9 +577,10 @@ static __device__ __noinline__ float large_weights(uint32_t at, float scale, flo
   return sum;
 }
 
-// Adds a tile whose values are not all finite to the output, key by key and only for the rows that see it.
+// Adds a tile whose values are not all finite to the output, key by key and only for the rows that see it.  (Not a call:
+// what the loop around it keeps in registers would be spilled for it.)
 template <class S>
-static __device__ __noinline__ void add_by_key(uint32_t scores, uint32_t out, const unsigned char* ring, uint32_t slot, Seen sees, bool first) {
+__device__ __forceinline__ void add_by_key(uint32_t scores, uint32_t out, const unsigned char* ring, uint32_t slot, Seen<S::kKeys> sees, bool first) {
   using E = Elem<typename S::T>;
 #pragma unroll 1
   for (int half = 0; half < S::kHalves; ++half) {
@@ -581,10 +594,13 @@ static __device__ __noinline__ void add_by_key(uint32_t scores, uint32_t out, co
       for (int n = 0; n < 32; ++n) acc[n] = first ? 0.0f : __uint_as_float(o[n]);
 #pragma unroll 1
       for (int n = 0; n < S::kKeys; ++n) {
-        uint32_t pair[1];
+        uint32_t pair[1], word = sees.bits[0];
         tmem_load(pair, scores + (n >> 1));
         const float2 ws = E::unpack(pair[0]);
         const float wt = n & 1 ? ws.y : ws.x;
+#pragma unroll
+        for (int k = 1; k < S::kKeys / 32; ++k) word = n >> 5 == k ? sees.bits[k] : word;
+        const bool seen = word >> (n & 31) & 1;
         const unsigned char* line = values + (d >> 6) * S::kRun + n * 128;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -593,7 +609,7 @@ static __device__ __noinline__ void add_by_key(uint32_t scores, uint32_t out, co
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             const float2 v = E::unpack(ys[h]);
-            if (sees(n)) {
+            if (seen) {
               acc[q * 8 + h * 2] = fmaf(wt, v.x, acc[q * 8 + h * 2]);
               acc[q * 8 + h * 2 + 1] = fmaf(wt, v.y, acc[q * 8 + h * 2 + 1]);
             }
@@ -638,8 +654,7 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
     const Unit u = c.unit[sg & 1];
     more = u.tiles > 0;
     const int count = tiles_of(u, r);  // 0 at the end
-    const int pos = u.t0 + token, head = u.chunk * P.heads + in_group;
-    const bool live = m < P.heads * P.tokens && pos <= u.pos1 && head < P.group;
+    const int pos = u.t0 + token;  // (rows that are none are weighed like others, and not written)
     float mx = -INFINITY, l = 0.0f;
     bool large = false;
     for (int i = 0; i < count && !dead; ++i, ++it) {
@@ -649,18 +664,17 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
       wait(&c.s_full[b], (it >> 1) & 1);
       if (dead) break;
       fence_after();
-      Seen sees = {S::kKeys, 0, 0};
-      if (cut) {
-        sees.end = live ? pos + 1 - base : 0;
-        if (P.window > 0) {
-          sees.start = pos - P.window + 1 - base;
-          sees.sinks = P.sinks - base;
-        }
-      }
+      auto seen = [&]() {  // which keys of the tile this row sees (all, in one that cuts no row)
+        Seen<S::kKeys> sees;
+        if (cut) sees.set(pos + 1 - base, P.window > 0 ? pos - P.window + 1 - base : 0, P.sinks - base);
+        else sees.set(S::kKeys, 0, 0);
+        return sees;
+      };
       // (128 scores are read twice, a part at a time: they do not stay in registers beside the rest, but half of them do)
       uint32_t x[64];
       float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       auto hide = [&](uint32_t* w, int from, int count) {
+        const Seen<S::kKeys> sees = seen();
 #pragma unroll
         for (int n = 0; n < count; ++n)
           if (!sees(from + n)) w[n] = 0xff800000u;
@@ -680,7 +694,7 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
       if (cut) hide(x, 0, 64);
       largest(x, 64);
       const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
-      const bool grow = live && top - mx > 8.0f + E::kLift;
+      const bool grow = top - mx > 8.0f + E::kLift;
       if (__any_sync(0xffffffffu, grow)) {
         const float now = grow ? (fabsf(top) > kLarge ? top : top - E::kLift) : mx;
         const float by = grow ? ex2(mx - now) : 1.0f;  // 0 if nothing was seen before
@@ -702,7 +716,7 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
       }
       const float z = mx == -INFINITY ? 0.0f : mx;
       if (large) {
-        l += large_weights<E, S::kKeys>(buf, scale, z, sees);
+        l += large_weights<E, S::kKeys>(buf, scale, z, seen());
       } else {
         uint64_t s0 = 0, s1 = 0;  // sums of even and odd keys
         const uint64_t by = pair(scale, scale), less = pair(-z, -z);
@@ -737,7 +751,7 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
         for (int half = 0; half < S::kHalves; ++half) wait(&c.ready[(n + half) % kMaxSlots], parity_of(n + half));
         if (!dead && is_slow<S>(c, n)) {
           if (i > 0) added(it - 1);
-          add_by_key<S>(buf, out_at, ring, slot_of(n), sees, i == 0);
+          add_by_key<S>(buf, out_at, ring, slot_of(n), seen(), i == 0);
         }
       }
       fence_before();
@@ -747,23 +761,49 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
     nth += u.tiles * S::kHalves;
     if (count > 0 && !dead) {
       added(it - 1);
+      // Eight lanes write 128 bytes of one row after the other: rows of their own, 16 bytes at a time, kept a warp's stores
+      // 32 lines each (4000 cycles a unit of 128 columns, 900 so).
       const float f = l == 0.0f ? 0.0f : 1.0f / l;
-      const long long q = u.q0 + pos;
-      const int to_head = u.h * P.group + head;
-      T* to = static_cast<T*>(P.out) + q * P.out_stride + (long long)to_head * D;
+      const int head = c.unit[sg & 1].chunk * P.heads + in_group;
+      const bool live = m < P.heads * P.tokens && pos <= c.unit[sg & 1].pos1 && head < P.group;
+      const long long q = c.unit[sg & 1].q0 + pos;
+      const int to_head = c.unit[sg & 1].h * P.group + head;
+      const long long mine = live ? q * P.out_stride + (long long)to_head * D : -1;
+      if (live && P.lse) P.lse[q * (P.group * P.hkv) + to_head] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
 #pragma unroll 1
-      for (int d = 0; d < D; d += 32) {
-        uint32_t o[32];
-        tmem_load(o, out_at + d);
-        if (!live) continue;
+      for (int d = 0; d < D; d += 64) {
+        uint4 o[8];  // eight columns of this lane's row each; then of eight rows, this lane's columns
 #pragma unroll
-        for (int n = 0; n < 32; n += 8) {
-          auto val = [&](int k) { return __uint_as_float(o[n + k]) * f; };
-          *reinterpret_cast<uint4*>(to + d + n) =
-              make_uint4(E::pack(val(0), val(1)), E::pack(val(2), val(3)), E::pack(val(4), val(5)), E::pack(val(6), val(7)));
+        for (int h = 0; h < 2; ++h) {
+          uint32_t y[32];
+          tmem_load(y, out_at + d + 32 * h);
+          auto val = [&](int k) { return __uint_as_float(y[k]) * f; };
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+            o[4 * h + n] = make_uint4(E::pack(val(8 * n), val(8 * n + 1)), E::pack(val(8 * n + 2), val(8 * n + 3)),
+                                      E::pack(val(8 * n + 4), val(8 * n + 5)), E::pack(val(8 * n + 6), val(8 * n + 7)));
+        }
+#pragma unroll
+        for (int m2 = 4; m2 > 0; m2 >>= 1) {
+          const bool high = lane & m2;
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            if (n & m2) continue;
+            uint4& low_piece = o[n];
+            uint4& high_piece = o[n | m2];
+            const uint4 give = high ? low_piece : high_piece;
+            const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, m2), __shfl_xor_sync(0xffffffffu, give.y, m2),
+                                         __shfl_xor_sync(0xffffffffu, give.z, m2), __shfl_xor_sync(0xffffffffu, give.w, m2));
+            if (high) low_piece = got;
+            else high_piece = got;
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const long long at = __shfl_sync(0xffffffffu, mine, (lane & 24) + n);
+          if (at >= 0) *reinterpret_cast<uint4*>(static_cast<T*>(P.out) + at + d + (lane & 7) * 8) = o[n];
         }
       }
-      if (live && P.lse) P.lse[q * (P.group * P.hkv) + to_head] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
       fence_before();
       __syncwarp();
       if (lane == 0) arrive(&c.o_free[r]);
@@ -811,6 +851,11 @@ __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (warp == S::kLoad && lane < 3) asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &mq : lane == 1 ? &mk : &mv) : "memory");
+  // rows of the queries that no copy fills (128 is no multiple of `heads`): zeros, so that their scores are numbers
+  const int filled = P.heads * P.tokens, lines = TILES * (D / 64) * (128 - filled) * 8;
+  for (int i = tid; i < lines; i += S::kThreads)
+    reinterpret_cast<uint4*>(base)[i / ((128 - filled) * 8) * 1024 + filled * 8 + i % ((128 - filled) * 8)] = make_uint4(0u, 0u, 0u, 0u);
+  proxy_fence();
   fence_before();
   __syncthreads();
   fence_after();
