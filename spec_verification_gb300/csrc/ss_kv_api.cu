@@ -75,7 +75,7 @@ cudaError_t configure(int device, const void* fn, size_t smem) {
     size_t smem;
   };
   static std::mutex mu;
-  static Done done[256];  // 32 kernels with at most a few sizes each; past that they are set again each time
+  static Done done[256];  // 36 kernels with at most a few sizes each; past that they are set again each time
   static int count = 0;
   const std::lock_guard<std::mutex> lock(mu);
   bool pages = false;
@@ -102,8 +102,8 @@ ss::AttendKernel attend_kernel(const ss_kv_config& c, int row_tile) {
               : (low ? ss::kv_attend_f16_e4m3(c.head_dim, row_tile) : ss::kv_attend_f16(c.head_dim, row_tile));
 }
 
-ss::PromptKernel prompt_kernel(const ss_kv_config& c) {
-  return c.dtype == SS_BF16 ? ss::kv_prompt_bf16(c.head_dim) : ss::kv_prompt_f16(c.head_dim);
+ss::PromptKernel prompt_kernel(const ss_kv_config& c, int tiles) {
+  return c.dtype == SS_BF16 ? ss::kv_prompt_bf16(c.head_dim, tiles) : ss::kv_prompt_f16(c.head_dim, tiles);
 }
 
 // A cache as a kernel's copies see it: (part of a head, token, number of the part, head, page).  Swizzled heads come in
@@ -313,8 +313,8 @@ ss_status ss_kv_plan_create(ss_kv_plan** out, const ss_kv_config* config) {
     const ss::AttendKernel b = blocks_kernel(c, row_tile);
     e = configure(c.device, b.fn, b.smem);
   }
-  if (e == cudaSuccess) {
-    const ss::PromptKernel m = prompt_kernel(c);
+  for (int tiles = 1; tiles <= 2 && e == cudaSuccess; ++tiles) {
+    const ss::PromptKernel m = prompt_kernel(c, tiles);
     e = configure(c.device, m.fn, m.smem);
   }
   if (e != cudaSuccess) return cuda_fail(e, "kernel attributes");
@@ -575,7 +575,6 @@ ss_status ss_attend_prompt(const ss_prompt_batch* b) {
   if (!b->workspace || b->workspace_bytes < p->ws_bytes)
     return fail(SS_ERR_WORKSPACE, "workspace missing or smaller than ss_kv_workspace_bytes()");
   if (!aligned(b->workspace, 256)) return fail(SS_ERR_ALIGN, "workspace must be 256-byte aligned");
-  const ss::PromptKernel k = prompt_kernel(c);
   const int group = c.q_heads / c.kv_heads, d = c.head_dim;
   ss::PromptParams P = {};
   P.out = b->out;
@@ -590,9 +589,16 @@ ss_status ss_attend_prompt(const ss_prompt_batch* b) {
   P.max_tokens = std::min(b->tokens, c.max_tokens);
   P.window = b->window >= P.max_tokens ? 0 : b->window;  // a window that reaches every token is none
   P.sinks = P.window ? std::min(b->sinks, P.max_tokens) : 0;
+  P.aligned = aligned(b->out, 32) && b->out_stride % 16 == 0;
   P.heads = std::min(group, 128);
   P.tokens = 128 / P.heads;
   P.chunks = (group + P.heads - 1) / P.heads;
+  // Two tiles of query rows to a unit load keys half as often; one, two CTAs to an SM, hides the start and end of a unit
+  // behind the other's products.  Measured (us, 32/8 heads of 128, two / one): 16000 tokens 1222 / 1342, 16 x 2000 409 /
+  // 446, 4000 93.7 / 95.9, 100 of up to 700 129 / 133; 1000 19.9 / 18.6, 300 11.7 / 10.3, 60 9.2 / 7.9, 200 x 60 51.5 /
+  // 48.4.  With 64 columns one was faster throughout (16000 tokens 1047 / 1001), with 256 two do not fit.
+  const bool few = (int64_t)P.max_tokens * c.q_heads <= 256ll * p->sms || P.max_tokens <= 2ll * P.tokens * b->B;
+  const ss::PromptKernel k = prompt_kernel(c, d == 128 && !few ? 2 : 1);
   P.next = static_cast<unsigned long long*>(b->workspace);
   P.ended = reinterpret_cast<uint32_t*>(P.next + 1);
   P.spin_limit = kSpin;
@@ -609,9 +615,9 @@ ss_status ss_attend_prompt(const ss_prompt_batch* b) {
   if (s == SS_OK) s = encode_lines(&mk, b->k, 4, dims, k_strides, box);
   if (s == SS_OK) s = encode_lines(&mv, b->v, 4, dims, v_strides, box);
   if (s != SS_OK) return s;
-  // a CTA to an SM, but no more than there can be units
+  // as many CTAs as stay on the GPU, but no more than there can be units
   const int64_t per = (int64_t)k.tiles * P.tokens, units = ((P.max_tokens + per - 1) / per + b->B) * P.hkv * P.chunks;
-  const int grid = (int)std::min<int64_t>(p->sms, units);
+  const int grid = (int)std::min<int64_t>((int64_t)k.ctas * p->sms, units);
   void* args[] = {&P, &mq, &mk, &mv};
   const Range range("ss_attend_prompt");
   const cudaError_t e = cudaLaunchKernel(k.fn, dim3(grid), dim3(k.threads), args, k.smem, static_cast<cudaStream_t>(b->stream));

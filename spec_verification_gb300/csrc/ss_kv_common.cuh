@@ -117,6 +117,7 @@ struct PromptParams {
   uint32_t* row_status;
   float scale_log2;
   int B, hkv, group, max_tokens, window, sinks;
+  int aligned;                 // are rows of the output 32-byte aligned?
   int heads, tokens, chunks;   // query heads and tokens of a tile of rows, tiles that a key head's query heads take
   unsigned long long* next;    // units handed out beyond the first of each CTA
   uint32_t* ended;             // CTAs that have ended
@@ -124,10 +125,10 @@ struct PromptParams {
 };
 struct PromptKernel {
   const void* fn;
-  int threads, tiles, keys;  // tiles of query rows of a unit, keys of a tile
+  int threads, tiles, keys, ctas;  // tiles of query rows of a unit, keys of a tile, CTAs per SM
   size_t smem;
 };
-PromptKernel kv_prompt_bf16(int head_dim);
-PromptKernel kv_prompt_f16(int head_dim);
+PromptKernel kv_prompt_bf16(int head_dim, int tiles);
+PromptKernel kv_prompt_f16(int head_dim, int tiles);
 
 }  // namespace ss

@@ -53,22 +53,24 @@ struct Shape {
   static constexpr int kProducts = 2 * TILES;
   static constexpr int kLoad = kSoftmax, kProduct = kSoftmax + 1, kGuard = kProduct + kProducts;
   static constexpr int kThreads = 32 * (kGuard + kGuardWarps);
-  static constexpr int kKeys = TILES == 2 ? 64 : 128;         // keys of a tile
+  static constexpr int kKeys = D <= 128 ? 64 : 128;           // keys of a tile
+  static constexpr int kCtas = TILES == 1 && D <= 128 ? 2 : 1;  // CTAs per SM
   static constexpr int kWide = D < 128 ? D : 128;             // columns of a slot
   static constexpr int kHalves = D / kWide;                   // slots of a tile
   static constexpr int kRun = kKeys * 128, kQRun = 128 * 128; // bytes of 64 columns of a tile, of a tile of rows
   static constexpr int kSlot = kWide / 64 * kRun;
   static constexpr int kQ = D / 64 * kQRun;                   // bytes of the queries of a tile of rows
-  static constexpr int kOut = 256;
+  static constexpr int kOut = 2 * TILES * kKeys;              // first column of the outputs in tensor memory
+  static constexpr uint32_t kCols = 512 / kCtas;
   // slots: as many as there is room for beside the queries and the control block
-  static constexpr int kFit = (227 * 1024 - 1024 - 2048 - TILES * kQ) / kSlot;
+  static constexpr int kFit = (228 * 1024 / kCtas - 1024 - 1024 - 2048 - TILES * kQ) / kSlot;
   static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
   static constexpr int kSmem = 1024 + TILES * kQ + kSlots * kSlot;
   static constexpr uint32_t kCommon = 1u << 4 | Elem<T>::kFormat << 7 | Elem<T>::kFormat << 10 | (128u >> 4) << 24;
   static constexpr uint32_t kScores = kCommon | (kKeys >> 3) << 17;
   static constexpr uint32_t kValues = kCommon | 1u << 16 | (uint32_t)(kWide >> 3) << 17;
   static_assert(kSlots >= 2 * kHalves + 1, "ring length");
-  static_assert(2 * TILES * kKeys == kOut && kOut + TILES * D <= 512, "tensor memory");
+  static_assert(kOut + TILES * D <= (int)kCols, "tensor memory");
 };
 
 struct Unit {
@@ -624,6 +626,18 @@ __device__ __forceinline__ void add_by_key(uint32_t scores, uint32_t out, const 
   store_wait();
 }
 
+// 32 bytes of a row: at once where they are aligned.
+__device__ __forceinline__ void store16(void* to, bool aligned, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f, uint32_t g,
+                                        uint32_t h) {
+  if (aligned) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+                 : "memory");
+  } else {
+    static_cast<uint4*>(to)[0] = make_uint4(a, b, c, d);
+    static_cast<uint4*>(to)[1] = make_uint4(e, f, g, h);
+  }
+}
+
 template <class S>
 __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, Control& c) {
   using T = typename S::T;
@@ -761,47 +775,23 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
     nth += u.tiles * S::kHalves;
     if (count > 0 && !dead) {
       added(it - 1);
-      // Eight lanes write 128 bytes of one row after the other: rows of their own, 16 bytes at a time, kept a warp's stores
-      // 32 lines each (4000 cycles a unit of 128 columns, 900 so).
       const float f = l == 0.0f ? 0.0f : 1.0f / l;
       const int head = c.unit[sg & 1].chunk * P.heads + in_group;
       const bool live = m < P.heads * P.tokens && pos <= c.unit[sg & 1].pos1 && head < P.group;
       const long long q = c.unit[sg & 1].q0 + pos;
       const int to_head = c.unit[sg & 1].h * P.group + head;
-      const long long mine = live ? q * P.out_stride + (long long)to_head * D : -1;
+      T* const to = static_cast<T*>(P.out) + q * P.out_stride + (long long)to_head * D;
       if (live && P.lse) P.lse[q * (P.group * P.hkv) + to_head] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
 #pragma unroll 1
       for (int d = 0; d < D; d += 64) {
-        uint4 o[8];  // eight columns of this lane's row each; then of eight rows, this lane's columns
+        uint32_t o[64];
+        tmem_load(o, out_at + d);
+        if (!live) continue;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t y[32];
-          tmem_load(y, out_at + d + 32 * h);
-          auto val = [&](int k) { return __uint_as_float(y[k]) * f; };
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-            o[4 * h + n] = make_uint4(E::pack(val(8 * n), val(8 * n + 1)), E::pack(val(8 * n + 2), val(8 * n + 3)),
-                                      E::pack(val(8 * n + 4), val(8 * n + 5)), E::pack(val(8 * n + 6), val(8 * n + 7)));
-        }
-#pragma unroll
-        for (int m2 = 4; m2 > 0; m2 >>= 1) {
-          const bool high = lane & m2;
-#pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            if (n & m2) continue;
-            uint4& low_piece = o[n];
-            uint4& high_piece = o[n | m2];
-            const uint4 give = high ? low_piece : high_piece;
-            const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, m2), __shfl_xor_sync(0xffffffffu, give.y, m2),
-                                         __shfl_xor_sync(0xffffffffu, give.z, m2), __shfl_xor_sync(0xffffffffu, give.w, m2));
-            if (high) low_piece = got;
-            else high_piece = got;
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const long long at = __shfl_sync(0xffffffffu, mine, (lane & 24) + n);
-          if (at >= 0) *reinterpret_cast<uint4*>(static_cast<T*>(P.out) + at + d + (lane & 7) * 8) = o[n];
+        for (int n = 0; n < 64; n += 16) {
+          auto val = [&](int k) { return __uint_as_float(o[n + k]) * f; };
+          store16(to + d + n, P.aligned, E::pack(val(0), val(1)), E::pack(val(2), val(3)), E::pack(val(4), val(5)), E::pack(val(6), val(7)),
+                  E::pack(val(8), val(9)), E::pack(val(10), val(11)), E::pack(val(12), val(13)), E::pack(val(14), val(15)));
         }
       }
       fence_before();
@@ -816,7 +806,7 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
 
 // ------------------------------------------------------------------ kernel
 template <class T, int D, int TILES>
-__global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), 1)
+__global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), (Shape<T, D, TILES>::kCtas))
     prompt_kernel(const PromptParams P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv) {
   using S = Shape<T, D, TILES>;
@@ -847,7 +837,7 @@ __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == S::kProduct) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&c.tmem)), "r"(512) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&c.tmem)), "r"(S::kCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (warp == S::kLoad && lane < 3) asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &mq : lane == 1 ? &mk : &mv) : "memory");
@@ -874,7 +864,7 @@ __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), 1)
   __syncthreads();
   if (warp == S::kProduct) {
     fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(c.tmem), "r"(512) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(c.tmem), "r"(S::kCols) : "memory");
   }
   // the counters are left at zero by the last CTA to end: every one has taken its last unit by then
   if (tid == 0) {
@@ -890,11 +880,12 @@ __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), 1)
 template <class T, int D, int TILES>
 PromptKernel entry() {
   using S = Shape<T, D, TILES>;
-  return {reinterpret_cast<const void*>(&prompt_kernel<T, D, TILES>), S::kThreads, TILES, S::kKeys, (size_t)S::kSmem};
+  return {reinterpret_cast<const void*>(&prompt_kernel<T, D, TILES>), S::kThreads, TILES, S::kKeys, S::kCtas, (size_t)S::kSmem};
 }
 template <class T>
-PromptKernel pick(int d) {
-  return d == 64 ? entry<T, 64, 2>() : d == 128 ? entry<T, 128, 2>() : entry<T, 256, 1>();
+PromptKernel pick(int d, int tiles) {
+  if (d == 128 && tiles == 2) return entry<T, 128, 2>();
+  return d == 64 ? entry<T, 64, 1>() : d == 128 ? entry<T, 128, 1>() : entry<T, 256, 1>();
 }
 
 }  // namespace prompt
