@@ -89,10 +89,10 @@ typedef struct {
 /* One layer's SS_E4M3 cache with a factor for each block of tokens and key
  * head (host struct of device pointers): held value 8-bit value * factor.  A
  * block is block_tokens neighbouring tokens of a page.  Pointers and strides of
- * k and v as in ss_kv_cache.  The factors are read and written by
- * ss_kv_store_blocks, which makes them powers of two, 2^-40 to 2^40; the other
- * calls take any positive ones in that range (what is outside it, or NaN, as
- * its nearer end, NaN as 2^-40).  They need not be set before the first store. */
+ * k and v as in ss_kv_cache.  The factors are powers of two
+ * from 2^-40 to 2^40, as ss_kv_store_blocks writes them (of another number the
+ * calls take the power of two below it, in that range; of NaN 2^-40).  They
+ * need not be set before the first store. */
 typedef struct {
   void* k;
   void* v;
@@ -164,7 +164,7 @@ typedef struct {
  * call stores of a block and head, and e the least exponent in [-40, 40] with
  * amax <= 448 * 2^e: a block whose first token the call stores gets the factor
  * 2^e; one that it goes on in keeps the tokens before, and gets the larger of
- * 2^e and its old factor (one that is not a power of two counts as the next).
+ * 2^e and its old factor.
  * Where that is larger than the old one, the kept values are rounded to it.
  * A value is held as x / factor, rounded to nearest, all beyond 448 and
  * infinities as 448 with their sign, NaN as NaN.

@@ -409,7 +409,8 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
         }
       }
     }
-    CopyFactors mine, after;  // of this lane's copy in the batch and in the next one
+    CopyFactors mine;   // of this lane's copy in the batch
+    int keys_at = 0;    // place of the tile's keys in the ring
     const int per_copy = 1 << (box_shift - 4);
     auto place_of = [&](int i0) { return (tile_of(g.u, g.from + i0 + nth) * kTile + (sub << box_shift)) & page_mask; };
     bool published = false;
@@ -430,16 +431,14 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
         id = P.num_pages;
         atomicOr(&P.row_status[g.row], (uint32_t)SS_ST_KV_PAGE);
       }
-      if constexpr (S::kBlocks) {  // asked for a batch ahead but for a segment's first
-        if (i0 == 0) mine.fetch(P, holds(0) && !is_bad, id, g.h, place_of(0), per_copy);
-        else mine = after;
-      }
+      if (S::kBlocks && i0 == 0) mine.fetch(P, holds(0) && !is_bad, id, g.h, place_of(0), per_copy);
       const int n = min(batch, g.count - i0);
       for (int j = 0; j < n && !dead; ++j) {
         const int tok = (tile_of(g.u, g.from + i0 + j) * kTile + (sub << box_shift)) & page_mask;
 #pragma unroll(S::kLow ? 1 : 2)
         for (int values = 0; values < 2; ++values) {
           dead = !__all_sync(0xffffffffu, mbar_wait(&empty[turn.slot], turn.parity ^ 1, P.spin_limit, 0u));
+          if (S::kBlocks && dead && values && lane == 0) arrive(&full[keys_at]);  // (its copy is waited for at the end)
           if (dead) break;
           if (lane == 0) {
             if (!values) {
@@ -456,20 +455,24 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
             for (int r = 0; r < runs; ++r)
               tma_load(copies + turn.slot * kBytes + r * S::kRun + (sub << box_shift) * (S::kLow ? D : 128), values ? mv : mk,
                        &full[turn.slot], tok, r, g.h, id);
-          if (S::kBlocks && !values) {  // the factors come with the keys
-            const int tile = (__shfl_sync(0xffffffffu, it, 0) - 1) & (kBadTiles - 1);
-            if (nth == j) mine.write(*factors, tile, sub * per_copy, per_copy);
-            __syncwarp();
-            if (lane == 0) arrive(&full[turn.slot]);
+          if constexpr (S::kBlocks) {
+            if (!values) {
+              keys_at = turn.slot;
+            } else {  // the factors come with the keys, whose barrier waits for them too
+              const int tile = (__shfl_sync(0xffffffffu, it, 0) - 1) & (kBadTiles - 1);
+              if (nth == j) mine.write(*factors, tile, sub * per_copy, per_copy);
+              __syncwarp();
+              if (lane == 0) arrive(&full[keys_at]);
+            }
           }
           turn.next(slots);
           asked = min(asked + 1, slots);
         }
         if (!published && !dead) publish();
-        if (S::kBlocks && j == 0) {
-          const bool there = holds(i0 + batch) && (unsigned)next < (unsigned)P.num_pages;
-          after.fetch(P, there, next, g.h, place_of(i0 + batch), per_copy);
-        }
+      }
+      if (S::kBlocks && i0 + batch < g.count) {  // the next batch's, whose page ids have come meanwhile
+        const bool there = holds(i0 + batch) && (unsigned)next < (unsigned)P.num_pages;
+        mine.fetch(P, there, next, g.h, place_of(i0 + batch), per_copy);
       }
     }
     if (!published) publish();
@@ -658,7 +661,7 @@ static __device__ __noinline__ float large_weights_blocks(uint32_t at, int key0,
   for (int i = key0; i < key0 + KEYS; i += 16) {
     uint32_t x[16], w[8];
     tmem_load(x, at + i);
-    const float by = factor_of(scale, f.k[tile][i >> 4]), log = f.log[tile][i >> 4];
+    const float v = f.v[tile][i >> 4], by = factor_of(scale, f.k[tile][i >> 4]), log = log2_of(v);
     float s = 0.0f;
 #pragma unroll
     for (int n = 0; n < 16; n += 2) {
@@ -669,7 +672,7 @@ static __device__ __noinline__ float large_weights_blocks(uint32_t at, int key0,
       w[n / 2] = E::pack(y[0], y[1]);
       s += y[0] + y[1];
     }
-    sum = fmaf(s, f.back[tile][i >> 4], sum);
+    sum = fmaf(s, back_of(v), sum);
     tmem_store(at + i / 2, w);
   }
   return sum;
@@ -712,6 +715,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
     // A product of factors may vanish (a query of zeros comes with 2^-126), and -inf, the score of a hidden key, times 0 is
     // NaN.  Products of the held values are below 2^33, so with factors this small every score is 0 either way.
     if (S::kLow) scale = fmaxf(scale, FLT_MIN);
+    if (S::kBlocks) scale = scale_of(scale);
     float mx = -INFINITY, l = 0.0f, exact = 0.0f;  // m, the sum that divides, the sum of the weights
     bool large = false;  // a row of the warp has an m beyond kLarge
 
@@ -741,28 +745,28 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         };
         uint32_t x[kChunk];
         float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        constexpr int kGroups = S::kBlocks ? KEYS / 16 : 1;  // of this thread's keys: their factors
-        float by_k[kGroups], log_v[kGroups], back[kGroups];
+        // of this thread's keys, by groups: the factors of the scores; the others are read where they are used
+        constexpr int kGroups = S::kBlocks ? KEYS / 16 : 1;
+        const int tile = it & (kBadTiles - 1), group0 = key0 >> 4;
+        float by_k[kGroups];
         if constexpr (S::kBlocks) {
-          const int tile = it & (kBadTiles - 1), first = key0 >> 4;
+          read_factors(by_k, &factors->k[tile][group0]);
 #pragma unroll
-          for (int n = 0; n < kGroups; ++n) {
-            by_k[n] = factor_of(scale, factors->k[tile][first + n]);
-            log_v[n] = factors->log[tile][first + n];
-            back[n] = factors->back[tile][first + n];
-          }
+          for (int n = 0; n < kGroups; ++n) by_k[n] = factor_of(scale, by_k[n]);
         }
         float top = -INFINITY;
 #pragma unroll
         for (int at = 0; at < KEYS; at += kChunk) {
           scores(x, at);
           if constexpr (S::kBlocks) {
+            float v[kGroups];
+            read_factors(v, &factors->v[tile][group0]);
 #pragma unroll
             for (int g0 = 0; g0 < kChunk; g0 += 16) {
 #pragma unroll
               for (int n = 0; n < 4; ++n) t[n] = fmaxf(fmaxf(__uint_as_float(x[g0 + n]), __uint_as_float(x[g0 + 4 + n])), fmaxf(__uint_as_float(x[g0 + 8 + n]), __uint_as_float(x[g0 + 12 + n])));
               const int n = (at + g0) >> 4;
-              top = fmaxf(top, __fadd_rn(__fmul_rn(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), by_k[n]), log_v[n]));
+              top = fmaxf(top, __fadd_rn(__fmul_rn(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), by_k[n]), log2_of(v[n])));
             }
           } else {
 #pragma unroll
@@ -797,7 +801,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         // ones, so that the error of a weight that dominates its row cancels; the log-sum-exp has the sum before rounding.
         constexpr bool kTwo = std::is_same<typename S::Mul, __nv_bfloat16>::value;
         if (S::kBlocks && large) {
-          const float sum = large_weights_blocks<S, KEYS>(lanes + b * kTile, key0, scale, z, seen, *factors, it & (kBadTiles - 1));
+          const float sum = large_weights_blocks<S, KEYS>(lanes + b * kTile, key0, scale, z, seen, *factors, tile);
           l += sum;
           exact += sum;
         } else if (large) {
@@ -811,10 +815,12 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
           uint32_t w[kChunk / 2];
           float s0 = 0.0f, s1 = 0.0f, e0 = 0.0f, e1 = 0.0f;
           if constexpr (S::kBlocks) {
+            float v[kGroups];
+            read_factors(v, &factors->v[tile][group0]);
 #pragma unroll
             for (int g0 = 0; g0 < kChunk; g0 += 16) {
               const int group = (at + g0) >> 4;
-              const float by = by_k[group], less = log_v[group] - z;
+              const float by = by_k[group], less = log2_of(v[group]) - z;
               s0 = s1 = 0.0f;
 #pragma unroll
               for (int n = g0 / 2; n < g0 / 2 + 8; ++n) {
@@ -823,7 +829,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
                 s0 += a;
                 s1 += e;
               }
-              l = fmaf(s0 + s1, back[group], l);
+              l = fmaf(s0 + s1, back_of(v[group]), l);
             }
             exact = l;
             tmem_store(lanes + b * kTile + (key0 + at) / 2, w);

@@ -216,7 +216,8 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
     auto holds = [&](int i0) { return i0 + nth < g.count && block_of(i0) < used; };
     auto fetch = [&](int i0) { return holds(i0) ? __ldg(table + block_of(i0)) : P.num_pages; };
     int next = fetch(0);
-    CopyFactors mine, after;  // of this lane's copy in the batch and in the next one
+    CopyFactors mine;   // of this lane's copy in the batch
+    int keys_at = 0;    // place of the tile's keys in the ring
     const int per_copy = 1 << (box_shift - 4);
     auto place_of = [&](int i0) { return (tile_of(g.u, g.from + i0 + nth) * kTile + (sub << box_shift)) & page_mask; };
     for (int i0 = 0; i0 < g.count && !dead; i0 += batch) {
@@ -228,16 +229,14 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
         id = P.num_pages;
         atomicOr(&P.row_status[g.row], (uint32_t)SS_ST_KV_PAGE);
       }
-      if constexpr (S::kBlocks) {  // asked for a batch ahead but for a segment's first
-        if (i0 == 0) mine.fetch(P, holds(0) && !is_bad, id, g.h, place_of(0), per_copy);
-        else mine = after;
-      }
+      if (S::kBlocks && i0 == 0) mine.fetch(P, holds(0) && !is_bad, id, g.h, place_of(0), per_copy);
       const int n = min(batch, g.count - i0);
       for (int j = 0; j < n && !dead; ++j) {
         const int tok = (tile_of(g.u, g.from + i0 + j) * kTile + (sub << box_shift)) & page_mask;
 #pragma unroll 1
         for (int values = 0; values < 2; ++values) {
           dead = !__all_sync(0xffffffffu, mbar_wait(&c.empty[turn.slot], turn.parity ^ 1, P.spin_limit, 0u));
+          if (S::kBlocks && dead && values && lane == 0) arrive(&c.full[keys_at]);  // (its copy is waited for at the end)
           if (dead) break;
           if (lane == 0) {
             if (!values) {
@@ -252,18 +251,23 @@ __device__ void load_warp(const AttendParams& P, const CUtensorMap* mk, const CU
           __syncwarp();
           if (nth == j)
             tma_load(smem_u32(ring) + turn.slot * S::kSlot + (sub << box_shift) * (S::kSlot / kTile), values ? mv : mk, &c.full[turn.slot], tok, g.h, id);
-          if (S::kBlocks && !values) {  // the factors come with the keys
-            if (nth == j) mine.write(*factors, turn.slot, sub * per_copy, per_copy);
-            __syncwarp();
-            if (lane == 0) arrive(&c.full[turn.slot]);
+          if constexpr (S::kBlocks) {
+            if (!values) {
+              keys_at = turn.slot;
+            } else {  // the factors come with the keys, whose barrier waits for them too
+              const int tile = keys_at;
+              if (nth == j) mine.write(*factors, tile, sub * per_copy, per_copy);
+              __syncwarp();
+              if (lane == 0) arrive(&c.full[keys_at]);
+            }
           }
           turn.next<S::kSlots>();
           asked = min(asked + 1, S::kSlots);
         }
-        if (S::kBlocks && j == 0) {
-          const bool there = holds(i0 + batch) && (unsigned)next < (unsigned)P.num_pages;
-          after.fetch(P, there, next, g.h, place_of(i0 + batch), per_copy);
-        }
+      }
+      if (S::kBlocks && i0 + batch < g.count) {  // the next batch's, whose page ids have come meanwhile
+        const bool there = holds(i0 + batch) && (unsigned)next < (unsigned)P.num_pages;
+        mine.fetch(P, there, next, g.h, place_of(i0 + batch), per_copy);
       }
     }
   }
@@ -413,6 +417,10 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
     }
     c0 = fmaxf(c0, FLT_MIN);  // see softmax_warps
     c1 = fmaxf(c1, FLT_MIN);
+    if (S::kBlocks) {
+      c0 = scale_of(c0);
+      c1 = scale_of(c1);
+    }
 
     float o[kOT][4];
 #pragma unroll
@@ -465,14 +473,10 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
       }
       // this warp's factors, before the keys' place is given back
       constexpr int kGroups = S::kBlocks ? S::kKG : 1;
-      float by_k[kGroups], log_v[kGroups], back[kGroups];
+      float by_k[kGroups], v_of[kGroups];
       if constexpr (S::kBlocks) {
-#pragma unroll
-        for (int n = 0; n < kGroups; ++n) {
-          by_k[n] = factors->k[keys.slot][warp * S::kKG + n];
-          log_v[n] = factors->log[keys.slot][warp * S::kKG + n];
-          back[n] = factors->back[keys.slot][warp * S::kKG + n];
-        }
+        read_factors(by_k, &factors->k[keys.slot][warp * S::kKG]);
+        read_factors(v_of, &factors->v[keys.slot][warp * S::kKG]);
       }
       __syncwarp();
       if (!held && lane == 0) arrive(&c.empty[keys.slot]);
@@ -501,8 +505,8 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
         for (int n = 0; n < kGroups; ++n) {
           const float a = fmaxf(fmaxf(s[2 * n][0], s[2 * n][1]), fmaxf(s[2 * n + 1][0], s[2 * n + 1][1]));
           const float b = fmaxf(fmaxf(s[2 * n][2], s[2 * n][3]), fmaxf(s[2 * n + 1][2], s[2 * n + 1][3]));
-          t0 = fmaxf(t0, __fadd_rn(__fmul_rn(a, factor_of(c0, by_k[n])), log_v[n]));
-          t1 = fmaxf(t1, __fadd_rn(__fmul_rn(b, factor_of(c1, by_k[n])), log_v[n]));
+          t0 = fmaxf(t0, __fadd_rn(__fmul_rn(a, factor_of(c0, by_k[n])), log2_of(v_of[n])));
+          t1 = fmaxf(t1, __fadd_rn(__fmul_rn(b, factor_of(c1, by_k[n])), log2_of(v_of[n])));
         }
       } else {
         t0 *= c0;
@@ -542,7 +546,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
 #pragma unroll
           for (int n = 0; n < kGroups; ++n) {
             f.k[n] = by_k[n];
-            f.log[n] = log_v[n];
+            f.log[n] = log2_of(v_of[n]);
           }
           x = large_weights_blocks(x, f, c0, z0, c1, z1);
         } else {
@@ -555,7 +559,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
       } else if constexpr (S::kBlocks) {
 #pragma unroll
         for (int n = 0; n < kNT; ++n) {
-          const float a = factor_of(c0, by_k[n / 2]), b = factor_of(c1, by_k[n / 2]), u0 = log_v[n / 2] - z0, u1 = log_v[n / 2] - z1;
+          const float a = factor_of(c0, by_k[n / 2]), b = factor_of(c1, by_k[n / 2]), u0 = log2_of(v_of[n / 2]) - z0, u1 = log2_of(v_of[n / 2]) - z1;
           s[n][0] = ex2(fmaf(s[n][0], a, u0));
           s[n][1] = ex2(fmaf(s[n][1], a, u0));
           s[n][2] = ex2(fmaf(s[n][2], b, u1));
@@ -573,8 +577,8 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
         if constexpr (S::kBlocks) {
-          l0 = fmaf(s[n][0] + s[n][1], back[n / 2], l0);
-          l1 = fmaf(s[n][2] + s[n][3], back[n / 2], l1);
+          l0 = fmaf(s[n][0] + s[n][1], back_of(v_of[n / 2]), l0);
+          l1 = fmaf(s[n][2] + s[n][3], back_of(v_of[n / 2]), l1);
         } else {
           l0 += s[n][0] + s[n][1];
           l1 += s[n][2] + s[n][3];

@@ -56,11 +56,11 @@ __device__ __forceinline__ float2 from8(uint32_t w) {  // of the low 16 bits
 }
 
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-// The least e in range with x <= c * 2^e, c = 1.75 * 2^8 (448), for finite x >= 0; without c: with x <= 2^e.
-__device__ __forceinline__ int exponent_of(float x, bool values) {
-  const uint32_t bits = __float_as_uint(x), part = bits & 0x7fffffu;
+// The least e in range with x <= 448 * 2^e, 448 = 1.75 * 2^8, for finite x >= 0.
+__device__ __forceinline__ int exponent_of(float x) {
+  const uint32_t bits = __float_as_uint(x);
   const int e = (int)(bits >> 23) - 127;  // (numbers below 2^-126 are far below the range)
-  return min(max(values ? e - 8 + (part > 0x600000u) : e + (part != 0u), kLowestBlock), kHighestBlock);
+  return min(max(e - 8 + ((bits & 0x7fffffu) > 0x600000u), kLowestBlock), kHighestBlock);
 }
 
 // A row of a call; n == 0: nothing to store.
@@ -194,11 +194,11 @@ __global__ void __launch_bounds__(kNT) store_kernel(const StoreParams P) {
       }
     }
     top = G::max(top, room);
-    int e = exponent_of(top, true);
-    const float held = block_factor(old);
-    if (kept) e = max(e, exponent_of(held, false));
-    if (kept && held != power(e)) {
-      const float by = held * power(-e);
+    int e = exponent_of(top);
+    const int before = (int)(__float_as_uint(block_factor(old)) >> 23) - 127;
+    if (kept) e = max(e, before);
+    if (kept && e != before) {
+      const float by = power(before - e);
       const int pieces = kept * (D / 16);
       for (int i = at; i < pieces; i += G::kSize) {
         uint4* line = reinterpret_cast<uint4*>(dst + (long long)(i / (D / 16)) * P.token_stride + i % (D / 16) * 16);

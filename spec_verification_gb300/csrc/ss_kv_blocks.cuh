@@ -14,9 +14,11 @@ namespace ss {
 // weight and a value inside 32 bits.
 constexpr int kLowestBlock = -40, kHighestBlock = 40;
 
-// A factor as the kernels take it: inside the range whatever the memory holds (that of a block nothing was stored in
-// may be anything; NaN becomes the lowest).
-__device__ __forceinline__ float block_factor(float x) { return fminf(fmaxf(x, 0x1p-40f), 0x1p40f); }
+// A factor as the kernels take it: a power of two inside the range whatever the memory holds (that of a block nothing was
+// stored in may be anything; NaN becomes the lowest).
+__device__ __forceinline__ float block_factor(float x) {
+  return __uint_as_float(__float_as_uint(fminf(fmaxf(x, 0x1p-40f), 0x1p40f)) & 0x7f800000u);
+}
 
 namespace kv {
 
@@ -24,31 +26,45 @@ namespace kv {
 // w_t = 2^(c ks q.k8_t - m) and o = sum w_t vs v8_t / sum w_t.  The kernels keep u_t = w_t vs instead, as
 // u_t = 2^(c ks q.k8_t + log2 vs - m) with m near the largest exponent of u: the product with the values is then that of
 // their bytes, u fits 16 bits whatever the factors are, and sum w_t is the sum over blocks of sum u_t / vs.  A group of 16
-// keys has one factor each, so that costs nothing a score.  m is a whole number, as log2 vs is where the factor is a
-// power of two, so that the exponent loses no bits.
+// keys has one factor each, so that costs nothing a score.  log2 vs is a whole number, and m is made one, so that the
+// exponent loses no bits.
 //
-// Of the keys of some tiles, by groups of 16: ks, log2 vs, 1 / vs.
+// Of the keys of some tiles, by groups of 16: ks and vs.
 template <int TILES, int GROUPS>
-struct Factors {
-  float k[TILES][GROUPS], log[TILES][GROUPS], back[TILES][GROUPS];
+struct alignas(16) Factors {
+  float k[TILES][GROUPS], v[TILES][GROUPS];
 };
-struct NoFactors {};
-
-__device__ __forceinline__ float log2_of(float x) {  // x normal; exact for powers of two
-  const uint32_t bits = __float_as_uint(x), part = bits & 0x7fffffu;
-  float y = 0.0f;
-  if (part) asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(__uint_as_float(part | 0x3f800000u)));
-  return y + (float)((int)(bits >> 23) - 127);
-}
 
 // The factor of a block's scores.  Held bytes times f16 queries stay below 2^33: factors this small make every score 0, and
-// 0 times a hidden key's -inf, or an infinite factor times 0, must not be NaN.
-__device__ __forceinline__ float factor_of(float scale, float k) { return fminf(fmaxf(scale * k, FLT_MIN), FLT_MAX); }
+// 0 times a hidden key's -inf must not be NaN; nor may 0 times infinity, which scale_of leaves no room for.
+__device__ __forceinline__ float factor_of(float scale, float k) { return fmaxf(scale * k, FLT_MIN); }
+__device__ __forceinline__ float scale_of(float scale) { return fminf(scale, 0x1p80f); }
+// log2 and reciprocal of a power of two
+__device__ __forceinline__ float log2_of(float x) { return (float)((int)(__float_as_uint(x) >> 23) - 127); }
+__device__ __forceinline__ float back_of(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
+
+// N neighbouring factors.
+template <int N>
+__device__ __forceinline__ void read_factors(float (&to)[N], const float* from) {
+  if constexpr (N == 4) {
+    const float4 y = *reinterpret_cast<const float4*>(from);
+    to[0] = y.x;
+    to[1] = y.y;
+    to[2] = y.z;
+    to[3] = y.w;
+  } else if constexpr (N == 2) {
+    const float2 y = *reinterpret_cast<const float2*>(from);
+    to[0] = y.x;
+    to[1] = y.y;
+  } else {
+    to[0] = *from;
+  }
+}
 
 // A load warp's factors of one copy (of up to 64 tokens: 4 groups) of its batch.
 struct CopyFactors {
   float k[4], v[4];
-  // Those of the copy that starts at place `tok` of page `id`; ones where `there` is false.
+  // Asks for those of the copy that starts at place `tok` of page `id`; ones where `there` is false.
   __device__ __forceinline__ void fetch(const AttendParams& P, bool there, int id, int h, int tok, int groups) {
     const long long at = ((long long)id * P.hkv + h) << (P.page_shift - P.block_shift);
 #pragma unroll
@@ -63,13 +79,16 @@ struct CopyFactors {
   }
   template <class F>
   __device__ __forceinline__ void write(F& f, int tile, int first, int groups) const {
+    if (groups == 4) {
+      *reinterpret_cast<float4*>(&f.k[tile][first]) = make_float4(block_factor(k[0]), block_factor(k[1]), block_factor(k[2]), block_factor(k[3]));
+      *reinterpret_cast<float4*>(&f.v[tile][first]) = make_float4(block_factor(v[0]), block_factor(v[1]), block_factor(v[2]), block_factor(v[3]));
+      return;
+    }
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
+    for (int n = 0; n < 2; ++n) {
       if (n >= groups) continue;
-      const float y = block_factor(v[n]);
       f.k[tile][first + n] = block_factor(k[n]);
-      f.log[tile][first + n] = log2_of(y);
-      f.back[tile][first + n] = __frcp_rn(y);
+      f.v[tile][first + n] = block_factor(v[n]);
     }
   }
 };

@@ -40,9 +40,9 @@ def store(held, factor, x, at, block):
         e = exponent_for(float(finite.max()) if finite.numel() else 0.0)
         if p0 > b * block:
             old = min(max(factor[b], 2.0 ** LOWEST), 2.0 ** HIGHEST) if not math.isnan(factor[b]) else 2.0 ** LOWEST
-            e = max(e, math.ceil(math.log2(old)))
-            kept = held[b * block:p0]
-            if old != 2.0 ** e:
-                held[b * block:p0] = rounded(kept * (old / 2.0 ** e))
+            before = math.floor(math.log2(old))
+            e = max(e, before)
+            if e != before:
+                held[b * block:p0] = rounded(held[b * block:p0] * 2.0 ** (before - e))
         factor[b] = 2.0 ** e
         held[p0:p1] = rounded(part / 2.0 ** e)

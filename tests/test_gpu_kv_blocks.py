@@ -5,8 +5,7 @@ Bounds.  Factors are powers of two, so a quotient is exact and a value is rounde
 bit, and so are loads (a product with a power of two, rounded once).  Attention: as for a cache with a factor for each
 head (tests/test_gpu_kv.py), with these changes.  A weight times its values' factor, u, is rounded to f16: half a step
 of it, or 2^-25 where it is below 2^-14; the largest u of a row is at least 2^6 (m is rounded to a whole number, 7 below
-the first tile's largest), so the latter is 2^-31 of the largest.  A factor that is no power of two adds log2 of it, good
-to 2^-22 and rounded with m (at most 2^6 here for scores below 2^5, and rounded to 2^-18): 2^-17 of a weight.
+the first tile's largest), so the latter is 2^-31 of the largest.
 """
 import math
 
@@ -238,7 +237,8 @@ def test_store_on_another_stream_and_in_a_graph():
 # ------------------------------------------------------------------ attention
 class Blocks:
     """Rows with their own keys and values over the pages of a cache whose other bytes are NaN and whose other factors are not
-    numbers to compute with.  `spread`: factors are 2^(-spread .. spread), or any numbers between with exact=False."""
+    numbers to compute with.  `spread`: factors are 2^(-spread .. spread); exact=False: the memory has larger numbers, of which
+    the power of two counts."""
 
     def __init__(self, new, length, hq, hkv, dim, kind, layout, page, block, seed=0, spread=3, exact=True, size=1.5):
         kv = _kv()
@@ -248,7 +248,7 @@ class Blocks:
         used = [-(-n // page) for n in length]
         self.pages = sum(used) + 3
         ids = torch.randperm(self.pages, generator=g, device="cuda").tolist()
-        self.scale, self.kind, self.dim, self.page, self.exact = dim ** -0.5, kind, dim, page, exact
+        self.scale, self.kind, self.dim, self.page = dim ** -0.5, kind, dim, page
         self.cache = [_bytes(layout, self.pages, page, hkv, dim, 0x7F) for _ in range(2)]
         odd = torch.tensor([math.nan, math.inf, -math.inf, 0.0, -3.0, 1e38, 1e-38], device="cuda")
         shape = (self.pages, hkv, page // block)
@@ -264,10 +264,10 @@ class Blocks:
             for which in range(2):
                 wide = spread if which else min(spread, 3)  # (of keys less: it goes into the scores)
                 e = torch.rand(-(-max(n, 1) // block), hkv, generator=g, device="cuda") * 2 * wide - wide
-                f = torch.exp2(e.round() if exact else e)
+                f = torch.exp2(e.round())
                 bits = torch.randn(n, hkv, dim, generator=g, device="cuda").to(E4M3)
                 self.cache[which].view(torch.uint8)[where, token % page] = bits.view(torch.uint8)
-                self.factor[which][where, :, token % page // block] = f[token // block]
+                self.factor[which][where, :, token % page // block] = f[token // block] * (1.0 if exact else 1.75)
                 self.held[which].append(bits.double() * f[token // block].double()[..., None])
         self.table, self.new, self.length = table.cuda(), new, length
         self.tokens = sum(new)
@@ -294,7 +294,7 @@ class Blocks:
             want, lse, weighted, _, size = ref.attend(self.q[at:at + m].double(), k, v, self.length[r] - m, self.scale, window, sinks,
                                                       None if hidden is None else hidden.get(r))
             got, got_lse = self.out[at:at + m].double(), self.lse[at:at + m].double()
-            off = self.dim * 2.0 ** -23 * size + (2.0 ** -20 if self.exact else 2.0 ** -17)  # of a weight, relative
+            off = self.dim * 2.0 ** -23 * size + 2.0 ** -20  # of a weight, relative
             # 2^-31 of the largest weight times factor, of every value in units of its factor (|units| <= 448): `most` of it
             most = self.most(r, at, m, window, sinks, hidden)
             at += m
@@ -317,7 +317,7 @@ class Blocks:
         t = torch.arange(n, device="cuda")
         where = self.table[r, t // self.page].long().clamp(0, self.pages - 1)
         per = self.factor[1].shape[2]
-        f = self.factor[1][where, :, t % self.page * per // self.page].double()  # tokens, heads
+        f = torch.exp2(torch.floor(torch.log2(self.factor[1][where, :, t % self.page * per // self.page].double())))  # tokens, heads
         p = torch.arange(self.length[r] - m, self.length[r], device="cuda")[:, None]
         see = t[None] <= p
         if window:
