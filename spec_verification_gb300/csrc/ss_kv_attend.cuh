@@ -745,12 +745,14 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         };
         uint32_t x[kChunk];
         float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        // of this thread's keys, by groups: the factors of the scores; the others are read where they are used
+        // of this thread's keys, by groups: the factors of the scores and of the values, read once: shared memory is busy with
+        // the conversion, and a look at it takes long
         constexpr int kGroups = S::kBlocks ? KEYS / 16 : 1;
         const int tile = it & (kBadTiles - 1), group0 = key0 >> 4;
-        float by_k[kGroups];
+        float by_k[kGroups], v[kGroups];
         if constexpr (S::kBlocks) {
           read_factors(by_k, &factors->k[tile][group0]);
+          read_factors(v, &factors->v[tile][group0]);
 #pragma unroll
           for (int n = 0; n < kGroups; ++n) by_k[n] = factor_of(scale, by_k[n]);
         }
@@ -759,8 +761,6 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         for (int at = 0; at < KEYS; at += kChunk) {
           scores(x, at);
           if constexpr (S::kBlocks) {
-            float v[kGroups];
-            read_factors(v, &factors->v[tile][group0]);
 #pragma unroll
             for (int g0 = 0; g0 < kChunk; g0 += 16) {
 #pragma unroll
@@ -815,8 +815,6 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
           uint32_t w[kChunk / 2];
           float s0 = 0.0f, s1 = 0.0f, e0 = 0.0f, e1 = 0.0f;
           if constexpr (S::kBlocks) {
-            float v[kGroups];
-            read_factors(v, &factors->v[tile][group0]);
 #pragma unroll
             for (int g0 = 0; g0 < kChunk; g0 += 16) {
               const int group = (at + g0) >> 4;
