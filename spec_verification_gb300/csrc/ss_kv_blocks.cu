@@ -25,7 +25,7 @@ namespace ss {
 namespace {
 
 constexpr int kNT = 128, kWarps = kNT / 32;
-constexpr int kLoads = 8;  // 16-byte loads of a thread in flight
+constexpr int kKept = 1024;  // rows whose numbers a CTA keeps in shared memory
 
 template <class T>
 struct Pair;
@@ -36,6 +36,12 @@ struct Pair<__nv_bfloat16> {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
+  // the larger of each half of two pairs that have no signs; a number rather than NaN
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+  }
 };
 template <>
 struct Pair<__half> {
@@ -43,6 +49,11 @@ struct Pair<__half> {
   static __device__ __forceinline__ uint32_t to(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
   }
 };
 
@@ -110,12 +121,15 @@ struct Group {
 };
 
 // Units: (run, keys or values, head), runs in order of rows.  Every CTA counts the runs of all rows, a thread those of
-// some neighbouring ones, and its groups take the units in turn.
-template <class T, int D, bool WIDE>
+// some neighbouring ones, and its groups take the units in turn.  What a unit waits for, one after the other: its values
+// and its page, asked for together; its old factor, where it has one.
+template <class T, int D, bool WIDE, int LOADS>
 __global__ void __launch_bounds__(kNT) store_kernel(const StoreParams P) {
   using G = Group<WIDE>;
   __shared__ int first[kNT + 1];  // runs before those of each thread's rows
+  __shared__ int kept_q0[kKept], kept_n[kKept], kept_held[kKept];
   __shared__ float room[kWarps];
+  __shared__ int sums[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (P.B + kNT - 1) / kNT;
   {
@@ -124,6 +138,11 @@ __global__ void __launch_bounds__(kNT) store_kernel(const StoreParams P) {
       const StoreRow w = store_row(P, r);
       if (w.status && blockIdx.x == 0) atomicOr(&P.row_status[r], w.status);
       mine += runs_of(P, w);
+      if (r < kKept) {
+        kept_q0[r] = w.q0;
+        kept_n[r] = w.n;
+        kept_held[r] = w.held;
+      }
     }
     int incl = mine;
 #pragma unroll
@@ -131,7 +150,6 @@ __global__ void __launch_bounds__(kNT) store_kernel(const StoreParams P) {
       const int y = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += y;
     }
-    __shared__ int sums[kWarps];
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
     int before = 0;
@@ -140,6 +158,15 @@ __global__ void __launch_bounds__(kNT) store_kernel(const StoreParams P) {
     if (tid == 0) first[0] = 0;
     __syncthreads();
   }
+  auto row_of = [&](int r) {
+    if (r >= kKept) return store_row(P, r);
+    StoreRow w;
+    w.q0 = kept_q0[r];
+    w.n = kept_n[r];
+    w.held = kept_held[r];
+    w.status = 0;
+    return w;
+  };
   const int kinds = 2 * P.hkv, at = G::thread(), block = 1 << P.block_shift;
   const long long units = (long long)first[kNT] * kinds, step = (long long)gridDim.x * (kNT / G::kSize);
   constexpr int kPer = D / 8;  // 16-byte pieces of a new token's head
@@ -151,49 +178,60 @@ __global__ void __launch_bounds__(kNT) store_kernel(const StoreParams P) {
     for (int s = kNT / 2; s > 0; s >>= 1)
       if (first[owner + s] <= run) owner += s;
     int r = owner * per, left = run - first[owner];
-    StoreRow w = store_row(P, r);
+    StoreRow w = row_of(r);
     for (int n = runs_of(P, w); left >= n; n = runs_of(P, w)) {
       left -= n;
-      w = store_row(P, ++r);
+      w = row_of(++r);
     }
     // tokens [p0, p1) of the row, in one block
     const int blk = (w.held >> P.block_shift) + left;
     const int p0 = max(w.held, blk << P.block_shift), p1 = min(w.held + w.n, (blk + 1) << P.block_shift);
     const int page = P.block_table[(long long)r * P.max_blocks + (p0 >> P.page_shift)];
-    if ((unsigned)page >= (unsigned)P.num_pages) {
-      if (at == 0) atomicOr(&P.row_status[r], (uint32_t)SS_ST_KV_PAGE);
-      continue;
-    }
     const int place = p0 & ((1 << P.page_shift) - 1), kept = place & (block - 1), count = (p1 - p0) * kPer;
-    const T* src = static_cast<const T*>(values ? P.v : P.k) + (w.q0 + p0 - w.held) * (values ? P.v_stride : P.k_stride) + h * D;
     const long long stride = values ? P.v_stride : P.k_stride;
-    unsigned char* dst = static_cast<unsigned char*>(values ? P.v_cache : P.k_cache) + page * P.page_stride + (place - kept) * P.token_stride +
-                         h * P.head_stride;
-    float* factor = (values ? P.v_scale : P.k_scale) + ((long long)page * P.hkv + h) * (1 << (P.page_shift - P.block_shift)) + (place >> P.block_shift);
-    const float old = kept ? *factor : 0.0f;
-    auto load = [&](uint4 (&x)[kLoads], int i0) {
+    const T* src = static_cast<const T*>(values ? P.v : P.k) + (w.q0 + p0 - w.held) * stride + h * D;
+    auto load = [&](uint4 (&x)[LOADS], int i0) {
 #pragma unroll
-      for (int n = 0; n < kLoads; ++n) {
+      for (int n = 0; n < LOADS; ++n) {
         const int i = i0 + at + n * G::kSize;
         x[n] = make_uint4(0u, 0u, 0u, 0u);
         if (i < count) x[n] = __ldg(reinterpret_cast<const uint4*>(src + i / kPer * stride + i % kPer * 8));
       }
     };
-    uint4 x[kLoads];
-    float top = 0.0f;
-    for (int i0 = 0; i0 < count; i0 += kLoads * G::kSize) {
-      load(x, i0);
+    uint4 x[LOADS];
+    load(x, 0);
+    if ((unsigned)page >= (unsigned)P.num_pages) {
+      if (at == 0) atomicOr(&P.row_status[r], (uint32_t)SS_ST_KV_PAGE);
+      continue;
+    }
+    unsigned char* dst = static_cast<unsigned char*>(values ? P.v_cache : P.k_cache) + page * P.page_stride + (place - kept) * P.token_stride +
+                         h * P.head_stride;
+    float* factor = (values ? P.v_scale : P.k_scale) + ((long long)page * P.hkv + h) * (1 << (P.page_shift - P.block_shift)) + (place >> P.block_shift);
+    const float old = kept ? *factor : 0.0f;
+    // the largest |x|, of pairs of 16 bits; an infinity among them has it looked for again without
+    uint32_t most = 0;
+    for (int i0 = 0; i0 < count; i0 += LOADS * G::kSize) {
+      if (i0 > 0) load(x, i0);
 #pragma unroll
-      for (int n = 0; n < kLoads; ++n) {
-        for (const uint32_t y : {x[n].x, x[n].y, x[n].z, x[n].w}) {
-          const float2 v = Pair<T>::of(y);
-          const float a = fabsf(v.x), b = fabsf(v.y);
-          if (a < INFINITY) top = fmaxf(top, a);  // (false for NaN)
-          if (b < INFINITY) top = fmaxf(top, b);
+      for (int n = 0; n < LOADS; ++n)
+        for (const uint32_t y : {x[n].x, x[n].y, x[n].z, x[n].w}) most = Pair<T>::larger(most, y & 0x7fff7fffu);
+    }
+    float top = G::max(fmaxf(Pair<T>::of(most).x, Pair<T>::of(most).y), room);
+    if (top == INFINITY) {
+      top = 0.0f;
+      for (int i0 = 0; i0 < count; i0 += LOADS * G::kSize) {
+        if (count > LOADS * G::kSize) load(x, i0);
+#pragma unroll
+        for (int n = 0; n < LOADS; ++n) {
+          for (const uint32_t y : {x[n].x, x[n].y, x[n].z, x[n].w}) {
+            const float2 v = Pair<T>::of(y & 0x7fff7fffu);
+            if (v.x < INFINITY) top = fmaxf(top, v.x);  // (false for NaN)
+            if (v.y < INFINITY) top = fmaxf(top, v.y);
+          }
         }
       }
+      top = G::max(top, room);
     }
-    top = G::max(top, room);
     int e = exponent_of(top);
     const int before = (int)(__float_as_uint(block_factor(old)) >> 23) - 127;
     if (kept) e = max(e, before);
@@ -214,10 +252,10 @@ __global__ void __launch_bounds__(kNT) store_kernel(const StoreParams P) {
     }
     if (at == 0) *factor = power(e);
     const float down = power(-e);
-    for (int i0 = 0; i0 < count; i0 += kLoads * G::kSize) {
-      if (count > kLoads * G::kSize) load(x, i0);
+    for (int i0 = 0; i0 < count; i0 += LOADS * G::kSize) {
+      if (count > LOADS * G::kSize) load(x, i0);
 #pragma unroll
-      for (int n = 0; n < kLoads; ++n) {
+      for (int n = 0; n < LOADS; ++n) {
         const int i = i0 + at + n * G::kSize;
         if (i >= count) break;
         const float2 a = Pair<T>::of(x[n].x), b = Pair<T>::of(x[n].y), c = Pair<T>::of(x[n].z), d = Pair<T>::of(x[n].w);
@@ -263,11 +301,14 @@ __global__ void __launch_bounds__(256) load_kernel(const LoadParams P) {
 template <class T, int D>
 cudaError_t store(const StoreParams& P, int sms, cudaStream_t st) {
   // no more CTAs than there can be units, and no more than stay on the GPU
-  const bool wide = (D << P.block_shift) > kLoads * 32 * 8;
+  // a warp to a unit whose values it can hold, in 8 or 16 loads of 16 bytes a lane; else the CTA
+  const int values = D << P.block_shift;
+  const bool wide = values > 16 * 32 * 8;
   const long long units = 2ll * P.hkv * (2ll * P.B + ((long long)P.max_tokens >> P.block_shift));
   const int grid = (int)std::min<long long>(wide ? units : (units + kWarps - 1) / kWarps, 8ll * sms);
-  if (wide) store_kernel<T, D, true><<<grid, kNT, 0, st>>>(P);
-  else store_kernel<T, D, false><<<grid, kNT, 0, st>>>(P);
+  if (wide) store_kernel<T, D, true, 8><<<grid, kNT, 0, st>>>(P);
+  else if (values > 8 * 32 * 8) store_kernel<T, D, false, 16><<<grid, kNT, 0, st>>>(P);
+  else store_kernel<T, D, false, 8><<<grid, kNT, 0, st>>>(P);
   return cudaGetLastError();
 }
 template <class T, int D>

@@ -204,14 +204,17 @@ def _blocks(plan, k_cache, v_cache, k_scale, v_scale):
     if plan.cache_dtype != "e4m3":
         raise _bad(f"factors of blocks belong to a plan with cache_dtype e4m3, not {plan.cache_dtype}")
     st = _strides(plan, k_cache, v_cache)
-    shape = k_scale.shape
+    shape, f32, device = k_scale.shape, torch.float32, plan.device
     if len(shape) != 3 or shape[0] != plan.num_pages or shape[1] != plan.kv_heads or shape[2] < 1 or plan.page_size % shape[2]:
         raise _bad(f"k_scale must be [{plan.num_pages}, {plan.kv_heads}, blocks of a page], got {list(shape)}")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous():
-            raise _bad(f"{name} must be contiguous float32 {list(shape)}, got {t.dtype}, {list(t.shape)}")
-        if t.get_device() != plan.device:
-            raise _elsewhere(name, t, plan)
+    if k_scale.dtype is not f32 or not k_scale.is_contiguous():
+        raise _bad(f"k_scale must be contiguous float32, got {k_scale.dtype}")
+    if v_scale.dtype is not f32 or v_scale.shape != shape or not v_scale.is_contiguous():
+        raise _bad(f"v_scale must be contiguous float32 {list(shape)}, got {v_scale.dtype}, {list(v_scale.shape)}")
+    if k_scale.get_device() != device:
+        raise _elsewhere("k_scale", k_scale, plan)
+    if v_scale.get_device() != device:
+        raise _elsewhere("v_scale", v_scale, plan)
     return _BLOCKS.pack(k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], k_scale.data_ptr(), v_scale.data_ptr(),
                         plan.page_size // shape[2])
 
