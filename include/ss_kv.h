@@ -97,7 +97,7 @@ typedef struct {
   void* k;
   void* v;
   int64_t page_stride, token_stride, head_stride;
-  float* k_scale;       /* [num_pages, kv_heads, page_size / block_tokens], 16-byte aligned */
+  float* k_scale;       /* [num_pages, kv_heads, page_size / block_tokens] */
   float* v_scale;
   int32_t block_tokens; /* a power of two, 16 .. page_size */
 } ss_kv_block_cache;

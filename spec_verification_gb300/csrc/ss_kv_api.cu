@@ -169,7 +169,7 @@ ss_status check_blocks(const ss_kv_plan* p, const ss_kv_block_cache* cache) {
   const int32_t n = cache->block_tokens;
   if (n < 16 || n > p->c.page_size || (n & (n - 1)) != 0) return fail(SS_ERR_UNSUPPORTED, "block_tokens must be a power of two in [16, page_size]");
   if (!cache->k_scale || !cache->v_scale) return fail(SS_ERR_ARG, "k_scale and v_scale are required");
-  if (!aligned(cache->k_scale, 16) || !aligned(cache->v_scale, 16)) return fail(SS_ERR_ALIGN, "k_scale and v_scale must be 16-byte aligned");
+  if (!aligned(cache->k_scale, 4) || !aligned(cache->v_scale, 4)) return fail(SS_ERR_ALIGN, "k_scale and v_scale must be 4-byte aligned");
   return check_layout(p, cache->k, cache->v, cache->page_stride, cache->token_stride, cache->head_stride);
 }
 

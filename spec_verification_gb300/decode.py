@@ -5,8 +5,11 @@ with a random-weight transformer: prompts go through ss_kv_append,
 ss_rope_store and ss_attend like any other new tokens, drafts come from the
 row's own text (the tokens that followed the last occurrence of its latest
 token), ss_verify accepts a prefix of them and adds a token, and ss_kv_commit
-keeps exactly what was accepted.  Only the matrix products, embeddings and
-activations are torch's.
+keeps exactly what was accepted.  With an 8-bit cache whose blocks have factors
+of their own, prompts are attended as they come from the projection
+(ss_attend_prompt) while their keys and values are quantised into the cache
+(ss_kv_store_blocks), which the steps then read (ss_attend_blocks).  Only the
+matrix products, embeddings and activations are torch's.
 """
 from __future__ import annotations
 
@@ -54,7 +57,8 @@ class Decoder:
     """A batch of requests: their pages and lengths on the device, one cache per layer, the plans and workspaces."""
 
     def __init__(self, model: Model, rows: int, max_tokens: int, max_drafts: int = 4, page_size: int = 16, num_pages: int | None = None,
-                 cache_dtype: str | None = None, greedy: bool = True, seed: int = 0):
+                 cache_dtype: str | None = None, greedy: bool = True, seed: int = 0, block_tokens: int = 0):
+        """block_tokens: of an e4m3 cache, tokens of a block with a factor of its own (0: none, every value is held as it is)."""
         self.model, self.rows, self.max_drafts = model, rows, max_drafts
         dev, i32 = model.device, torch.int32
         blocks = -(-(max_tokens + max_drafts + 1) // page_size)
@@ -65,8 +69,20 @@ class Decoder:
         self.workspace = torch.zeros(self.plan.workspace_bytes, dtype=torch.uint8, device=dev)
         shape = (2, pages, model.kv_heads, page_size, model.head_dim)
         self.caches = [torch.zeros(shape, device=dev).to(self.plan.cache_type).transpose(2, 3) for _ in model.layers]
+        self.factors = None
+        if block_tokens:
+            if self.plan.cache_dtype != "e4m3" or page_size % block_tokens:
+                raise ValueError("blocks with factors belong to an e4m3 cache whose pages they divide")
+            self.factors = [torch.zeros(2, pages, model.kv_heads, page_size // block_tokens, device=dev) for _ in model.layers]
+            # rotated keys (and values) of a step in a row, on their way into the cache: 16-bit pages that follow one another
+            self.most = rows * max_tokens
+            self.rope_plan = kv.Plan(max_rows=1, max_tokens=self.most, q_heads=model.q_heads, kv_heads=model.kv_heads, head_dim=model.head_dim,
+                                     page_size=16, num_pages=-(-self.most // 16), max_blocks=1, dtype=model.dtype, device=dev.index or 0)
+            self.rotated = torch.empty((2,) + tuple(self.rope_plan.cache_shape), dtype=self.rope_plan.type, device=dev)
+            self.in_order = torch.arange(self.most, dtype=i32, device=dev)
         self.block_table = torch.full((rows, blocks), -1, dtype=i32, device=dev)
         self.kv_len = torch.zeros(rows, dtype=i32, device=dev)
+        self.begun = False  # does a row hold tokens?
         self.free_pages = torch.arange(pages, dtype=i32, device=dev)
         self.free_count = torch.tensor([pages], dtype=i32, device=dev)
         self.seq_len = torch.zeros(rows, dtype=i32, device=dev)
@@ -84,8 +100,30 @@ class Decoder:
         self.accepted = torch.zeros(rows, dtype=i32, device=dev)
         self.verify_status = torch.zeros(rows, dtype=i32, device=dev)
 
-    def forward(self, new: list) -> tuple:
-        """Runs the rows' new tokens (a list of token lists) through the model: their hidden states, and cu_new."""
+    def _attention(self, i: int, q, k, v, cu, slots, positions, whole: bool):
+        """Layer i's keys and values into the cache, and its attention of the new tokens."""
+        m, (k_cache, v_cache) = self.model, self.caches[i]
+        layer, n, d = m.layers[i], q.shape[0], m.head_dim
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        norms = dict(q_weight=layer["q_norm"], k_weight=layer["k_norm"])
+        after = dict(out=out, row_status=self.status, workspace=self.workspace, scale=d ** -0.5)
+        if self.factors is None:
+            kv.ss_rope_store(self.plan, q, k, v, k_cache, v_cache, m.inv_freq, positions, slots, q_out=q, **norms)
+            kv.ss_attend(self.plan, q, k_cache, v_cache, self.block_table, self.seq_len, cu, **after)
+            return out
+        kv.ss_rope_store(self.rope_plan, q, k, v, *self.rotated, m.inv_freq, positions, self.in_order[:n], q_out=q, **norms)
+        k, v = (x.view(-1, m.kv_heads, d)[:n] for x in self.rotated)
+        cache = (k_cache, v_cache, *self.factors[i])
+        kv.ss_kv_store_blocks(self.plan, k, v, *cache, self.block_table, self.kv_len, self.seq_len, cu, row_status=self.status)
+        if whole:
+            kv.ss_attend_prompt(self.plan, q, k, v, cu, **after)
+        else:
+            kv.ss_attend_blocks(self.plan, q, *cache, self.block_table, self.seq_len, cu, **after)
+        return out
+
+    def forward(self, new: list, whole: bool = False) -> tuple:
+        """Runs the rows' new tokens (a list of token lists) through the model: their hidden states, and cu_new.  whole: they are
+        all that the rows have, so that nothing is to be read from the cache."""
         m, dev = self.model, self.model.device
         tokens = torch.tensor([t for row in new for t in row], dtype=torch.int64, device=dev)
         cu = torch.tensor(np.concatenate([[0], np.cumsum([len(r) for r in new])]), dtype=torch.int32, device=dev)
@@ -95,14 +133,10 @@ class Decoder:
                         seq_len=self.seq_len, row_status=self.status)
         x = m.embed[tokens]
         hq, hkv, d = m.q_heads, m.kv_heads, m.head_dim
-        for layer, (k_cache, v_cache) in zip(m.layers, self.caches):
+        for i, layer in enumerate(m.layers):
             qkv = m.norm(x) @ layer["qkv"].T
             q, k, v = (part.view(n, heads, d) for part, heads in zip(qkv.split([hq * d, hkv * d, hkv * d], 1), (hq, hkv, hkv)))
-            out = torch.empty(n, hq, d, dtype=x.dtype, device=dev)
-            kv.ss_rope_store(self.plan, q, k, v, k_cache, v_cache, m.inv_freq, positions, slots, q_out=q, q_weight=layer["q_norm"],
-                             k_weight=layer["k_norm"])
-            kv.ss_attend(self.plan, q, k_cache, v_cache, self.block_table, self.seq_len, cu, out=out, row_status=self.status,
-                         workspace=self.workspace, scale=d ** -0.5)
+            out = self._attention(i, q, k, v, cu, slots, positions, whole)
             x = x + out.view(n, hq * d) @ layer["out"].T
             x = m.feed_forward(layer, x)
         return m.norm(x), cu
@@ -116,13 +150,15 @@ class Decoder:
     def prompt(self, prompts: list):
         """Caches all tokens of the prompts but the last of each, which the first step takes.  Where a prompt does not fit
         its table row or the free pages, nothing is kept of any."""
-        self.forward([p[:-1] for p in prompts])
+        self.forward([p[:-1] for p in prompts], whole=not self.begun)
         self._check(self.status)  # the next append writes it anew
         kv.ss_kv_commit(self.plan, self.block_table, self.kv_len, self.free_pages, self.free_count, self.seq_len)
+        self.begun = True
 
     def step(self, last: list, drafts: list, finished=None) -> list:
         """One step: each row's last token and its drafts go in, the tokens it gains come out (accepted drafts and one more)."""
         hidden, cu = self.forward([[t] + d for t, d in zip(last, drafts)])
+        self.begun = True
         logits = torch.nn.functional.pad(hidden @ self.model.embed.T, (0, -self.model.vocab % 8))  # rows on 16-byte boundaries
         if self.model.dtype != "bf16":
             logits = logits.float()
@@ -167,11 +203,12 @@ def main():
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--drafts", type=int, default=4)
     ap.add_argument("--cache", choices=["bf16", "e4m3"], default="bf16")
+    ap.add_argument("--block-tokens", type=int, default=0, help="of an e4m3 cache: tokens of a block with a factor of its own")
     a = ap.parse_args()
     rng = np.random.default_rng(0)
     model = Model()
     prompts = [rng.integers(0, 50, rng.integers(2, a.prompt + 1)).tolist() for _ in range(a.rows)]
-    decoder = Decoder(model, a.rows, a.prompt + a.steps * (a.drafts + 1), a.drafts, cache_dtype=a.cache)
+    decoder = Decoder(model, a.rows, a.prompt + a.steps * (a.drafts + 1), a.drafts, cache_dtype=a.cache, block_tokens=a.block_tokens)
     torch.cuda.synchronize()
     t = time.perf_counter()
     texts, gained = generate(decoder, prompts, a.steps)
