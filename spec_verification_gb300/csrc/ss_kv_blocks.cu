@@ -25,7 +25,7 @@ namespace ss {
 namespace {
 
 constexpr int kNT = 128, kWarps = kNT / 32;
-constexpr int kKept = 1024;  // rows whose numbers a CTA keeps in shared memory
+constexpr int kGroups = 256;  // of 32 rows: 8192
 
 template <class T>
 struct Pair;
@@ -120,69 +120,80 @@ struct Group {
   }
 };
 
-// Units: (run, keys or values, head), runs in order of rows.  Every CTA counts the runs of all rows, a thread those of
-// some neighbouring ones, and its groups take the units in turn.  What a unit waits for, one after the other: its values
-// and its page, asked for together; its old factor, where it has one.
+// Units: (run, keys or values, head), runs in order of rows.  Every CTA counts the runs of all rows, 32 rows at a time, and
+// its groups of threads take the units in turn; a group holds 32 rows, a row to a lane, until a run lies past them.  What a unit waits for, one after the other: its values and its page, asked for together; its old
+// factor, where it has one.
 template <class T, int D, bool WIDE, int LOADS>
 __global__ void __launch_bounds__(kNT) store_kernel(const StoreParams P) {
   using G = Group<WIDE>;
-  __shared__ int first[kNT + 1];  // runs before those of each thread's rows
-  __shared__ int kept_q0[kKept], kept_n[kKept], kept_held[kKept];
+  __shared__ int first[kGroups + 1];  // runs before each 32 rows
   __shared__ float room[kWarps];
-  __shared__ int sums[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (P.B + kNT - 1) / kNT;
-  {
-    int mine = 0;
-    for (int r = min(P.B, tid * per); r < min(P.B, (tid + 1) * per); ++r) {
-      const StoreRow w = store_row(P, r);
-      if (w.status && blockIdx.x == 0) atomicOr(&P.row_status[r], w.status);
-      mine += runs_of(P, w);
-      if (r < kKept) {
-        kept_q0[r] = w.q0;
-        kept_n[r] = w.n;
-        kept_held[r] = w.held;
-      }
+  const int groups = (P.B + 31) / 32;
+  auto row_of = [&](int r) {
+    StoreRow w = {0, 0, 0, 0};
+    return r < P.B ? store_row(P, r) : w;
+  };
+#pragma unroll 4
+  for (int g = warp; g < groups; g += kWarps) {
+    const StoreRow w = row_of(32 * g + lane);
+    if (w.status && blockIdx.x == 0) atomicOr(&P.row_status[32 * g + lane], w.status);
+    const int sum = __reduce_add_sync(0xffffffffu, runs_of(P, w));
+    if (lane == 0) first[g + 1] = sum;
+  }
+  __syncthreads();
+  if (warp == 0) {  // eight groups to a lane
+    int n[kGroups / 32], mine = 0;
+#pragma unroll
+    for (int k = 0; k < kGroups / 32; ++k) {
+      const int g = lane * (kGroups / 32) + k;
+      n[k] = g < groups ? first[g + 1] : 0;
+      mine += n[k];
     }
-    int incl = mine;
+    int sum = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += y;
+      const int y = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += y;
     }
-    if (lane == 31) sums[warp] = incl;
-    __syncthreads();
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += sums[w];
-    first[tid + 1] = before + incl;
-    if (tid == 0) first[0] = 0;
-    __syncthreads();
+    sum -= mine;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kGroups / 32; ++k) {
+      sum += n[k];
+      first[lane * (kGroups / 32) + k + 1] = sum;
+    }
+    if (lane == 0) first[0] = 0;
   }
-  auto row_of = [&](int r) {
-    if (r >= kKept) return store_row(P, r);
-    StoreRow w;
-    w.q0 = kept_q0[r];
-    w.n = kept_n[r];
-    w.held = kept_held[r];
-    w.status = 0;
-    return w;
-  };
+  __syncthreads();
   const int kinds = 2 * P.hkv, at = G::thread(), block = 1 << P.block_shift;
-  const long long units = (long long)first[kNT] * kinds, step = (long long)gridDim.x * (kNT / G::kSize);
+  const long long units = (long long)first[kGroups] * kinds, step = (long long)gridDim.x * (kNT / G::kSize);
   constexpr int kPer = D / 8;  // 16-byte pieces of a new token's head
+  int group = -1, upto = 0, runs = 0;  // the 32 rows that are looked at, runs up to and of this lane's
+  StoreRow mine = {0, 0, 0, 0};
   for (long long u = (long long)blockIdx.x * (kNT / G::kSize) + (WIDE ? 0 : warp); u < units; u += step) {
     const int run = (int)(u / kinds), kind = (int)(u - (long long)run * kinds), h = kind % P.hkv;
     const bool values = kind >= P.hkv;
-    int owner = 0;
+    if (group < 0 || run >= first[group + 1]) {
+      group = 0;
 #pragma unroll
-    for (int s = kNT / 2; s > 0; s >>= 1)
-      if (first[owner + s] <= run) owner += s;
-    int r = owner * per, left = run - first[owner];
-    StoreRow w = row_of(r);
-    for (int n = runs_of(P, w); left >= n; n = runs_of(P, w)) {
-      left -= n;
-      w = row_of(++r);
+      for (int s = kGroups / 2; s > 0; s >>= 1)
+        if (first[group + s] <= run) group += s;
+      mine = row_of(32 * group + lane);
+      runs = upto = runs_of(P, mine);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += y;
+      }
+      upto += first[group];
     }
+    const int owner = __ffs(__ballot_sync(0xffffffffu, upto > run)) - 1;
+    StoreRow w;
+    w.q0 = __shfl_sync(0xffffffffu, mine.q0, owner);
+    w.n = __shfl_sync(0xffffffffu, mine.n, owner);
+    w.held = __shfl_sync(0xffffffffu, mine.held, owner);
+    const int r = 32 * group + owner, left = run - __shfl_sync(0xffffffffu, upto - runs, owner);
     // tokens [p0, p1) of the row, in one block
     const int blk = (w.held >> P.block_shift) + left;
     const int p0 = max(w.held, blk << P.block_shift), p1 = min(w.held + w.n, (blk + 1) << P.block_shift);
@@ -300,12 +311,13 @@ __global__ void __launch_bounds__(256) load_kernel(const LoadParams P) {
 
 template <class T, int D>
 cudaError_t store(const StoreParams& P, int sms, cudaStream_t st) {
-  // no more CTAs than there can be units, and no more than stay on the GPU
+  // no more CTAs than there can be units, and no more than stay on the GPU (measured, 16000 tokens of one row, 5, 6, 8 an SM:
+  // 17.0, 16.6, 18.7 us)
   // a warp to a unit whose values it can hold, in 8 or 16 loads of 16 bytes a lane; else the CTA
   const int values = D << P.block_shift;
   const bool wide = values > 16 * 32 * 8;
   const long long units = 2ll * P.hkv * (2ll * P.B + ((long long)P.max_tokens >> P.block_shift));
-  const int grid = (int)std::min<long long>(wide ? units : (units + kWarps - 1) / kWarps, 8ll * sms);
+  const int grid = (int)std::min<long long>(wide ? units : (units + kWarps - 1) / kWarps, 6ll * sms);
   if (wide) store_kernel<T, D, true, 8><<<grid, kNT, 0, st>>>(P);
   else if (values > 8 * 32 * 8) store_kernel<T, D, false, 16><<<grid, kNT, 0, st>>>(P);
   else store_kernel<T, D, false, 8><<<grid, kNT, 0, st>>>(P);

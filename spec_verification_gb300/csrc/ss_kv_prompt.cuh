@@ -258,11 +258,10 @@ __device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t sum) {
 template <class S>
 __device__ void guard_warps(const PromptParams& P, unsigned char* ring, Control& c) {
   const int tid = threadIdx.x - 32 * S::kGuard, lane = tid & 31;
-  if (blockIdx.x == 0) {  // prompts whose prefix sums are no good
-    for (int r = tid; r < P.B; r += 32 * kGuardWarps) {
-      const int q0 = P.cu[r], q1 = P.cu[r + 1];
-      if (q0 < 0 || q1 < q0 || q1 > P.max_tokens) atomicOr(&P.row_status[r], (uint32_t)SS_ST_CAPACITY);
-    }
+  // prompts whose prefix sums are no good: each CTA looks at its share
+  for (int r = blockIdx.x * 32 * kGuardWarps + tid; r < P.B; r += gridDim.x * 32 * kGuardWarps) {
+    const int q0 = P.cu[r], q1 = P.cu[r + 1];
+    if (q0 < 0 || q1 < q0 || q1 > P.max_tokens) atomicOr(&P.row_status[r], (uint32_t)SS_ST_CAPACITY);
   }
   Turn turn;
   uint32_t nth = 0;  // slots of values so far

@@ -198,6 +198,48 @@ def test_keys_that_are_not_finite_stay_with_who_sees_them():
     assert torch.equal(bad[:200], expect[:200]) and not bad[200:, :2].any()
 
 
+def test_many_prompts():
+    """8192 prompts, most of them of one token or none, and bad ones among them."""
+    lengths = [(0, 1, 2, 1, 5, 1, 40, 1)[i % 8] for i in range(8192)]
+    p = Prompts(lengths, 4, 2, 64, "bf16", spare=5)
+    cu = p.cu.clone()
+    p.cu[4000], p.cu[8192] = -1, p.tokens + 6    # prompts 3999 and 4000, and the last one
+    p.run()
+    torch.cuda.synchronize()
+    bad = [r for r, s in enumerate(p.status.tolist()) if s]
+    assert bad == [3999, 4000, 8191] and set(p.status.tolist()) == {0, 1 << 9}
+    at = cu.tolist()
+    for r in list(range(40)) + list(range(3990, 4010)) + list(range(8150, 8192)):
+        here = slice(at[r], at[r + 1])
+        if r in bad:
+            assert torch.all(p.out[here] == 7.0)
+        elif lengths[r]:
+            want, _, weighted, _, size = reference(p.q[here].double(), p.k[here].double(), p.v[here].double(), p.scale)
+            tol = U["bf16"] * want.abs() * (1 + 2.0 ** -10) + (U["bf16"] + 2 * (64 * 2.0 ** -23 * size + 2.0 ** -20)[..., None]) * weighted + 2.0 ** -25
+            assert torch.all((p.out[here].double() - want).abs() <= tol), r
+    # all others: as if computed with good prefix sums
+    first = p.out.clone()
+    p.cu = cu
+    p.run()
+    torch.cuda.synchronize()
+    good = torch.ones(p.out.shape[0], dtype=torch.bool, device="cuda")
+    for r in bad:
+        good[at[r]:at[r + 1]] = False
+    assert torch.equal(first[good], p.out[good])
+
+
+@pytest.mark.parametrize("dim,hq", [(64, 6), (128, 4), (256, 2)])
+def test_outputs_on_16_byte_boundaries(dim, hq):
+    """Rows that are not 32-byte aligned are written in halves."""
+    p = Prompts([150, 33], hq, 2, dim, "bf16")
+    wide = torch.full((186, hq * dim + 8), 7.0, device="cuda").to(torch.bfloat16)
+    out = wide[:, 8:].view(186, hq, dim)
+    p.run()
+    p.run(out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:183], p.out[:183]) and torch.all(out[183:] == 7.0) and torch.all(wide[:, :8] == 7.0)
+
+
 def test_bad_prefix_sums_are_reported():
     p = Prompts([30, 50, 20, 40], 4, 2, 64, "bf16")
     p.cu = _i32([0, 30, 80, 70, 140])            # the third decreases; the fourth is tokens 70 .. 139
