@@ -594,10 +594,11 @@ ss_status ss_attend_prompt(const ss_prompt_batch* b) {
   P.tokens = 128 / P.heads;
   P.chunks = (group + P.heads - 1) / P.heads;
   // Two tiles of query rows to a unit load keys half as often; one, two CTAs to an SM, hides the start and end of a unit
-  // behind the other's products.  Measured (us, 32/8 heads of 128, two / one): 16000 tokens 1222 / 1342, 16 x 2000 409 /
-  // 446, 4000 93.7 / 95.9, 100 of up to 700 129 / 133; 1000 19.9 / 18.6, 300 11.7 / 10.3, 60 9.2 / 7.9, 200 x 60 51.5 /
-  // 48.4.  With 64 columns one was faster throughout (16000 tokens 1047 / 1001), with 256 two do not fit.
-  const bool few = (int64_t)P.max_tokens * c.q_heads <= 256ll * p->sms || P.max_tokens <= 2ll * P.tokens * b->B;
+  // behind the other's products.  Measured (us, 32/8 heads of 128, two / one): 16000 tokens 1170 / 1312, 16 x 2000 391 /
+  // 412, 50 x 500 141 / 152, 100 x 250 112.5 / 114.5, 4000 91.7 / 95.3; 1000 20.3 / 19.0, 300 11.7 / 10.3, 60 9.2 / 7.9,
+  // 200 x 60 51.5 / 48.4; 100 x 100 with 64/8 heads 89.7 / 80.1, with 16/16 44.4 / 34.6.  With 64 columns one was faster
+  // throughout (16000 tokens 1047 / 1001), with 256 two do not fit.
+  const bool few = (int64_t)P.max_tokens * c.q_heads <= 256ll * p->sms || P.max_tokens <= 200ll * b->B;
   const ss::PromptKernel k = prompt_kernel(c, d == 128 && !few ? 2 : 1);
   P.next = static_cast<unsigned long long*>(b->workspace);
   P.ended = reinterpret_cast<uint32_t*>(P.next + 1);

@@ -80,17 +80,14 @@ struct Unit {
   int live;                  // tiles of rows that have tokens
   int of_first;              // key tiles of the first tile of rows (the last one has all)
   int pos1;                  // last token of the unit
+  int cut, edge0, edge1;     // key tiles that not every row sees in full: from `cut` on, and edge0 .. edge1 - 1
 };
 template <class S>
 __device__ __forceinline__ int base_of(const Unit& u, int i) {
   return (i < u.sink ? i : i - u.sink + u.first) * S::kKeys;
 }
 __device__ __forceinline__ int tiles_of(const Unit& u, int r) { return r + 1 < u.live ? u.of_first : r < u.live ? u.tiles : 0; }
-// Does some live row of the unit not see all keys of the tile at `base`?
-template <class S>
-__device__ __forceinline__ bool cuts(const PromptParams& P, const Unit& u, int base) {
-  return base + S::kKeys - 1 > u.t0 || (P.window > 0 && base <= u.pos1 - P.window && base > P.sinks - S::kKeys);
-}
+__device__ __forceinline__ bool cuts(const Unit& u, int i) { return i >= u.cut || (i >= u.edge0 && i < u.edge1); }
 
 struct Control {
   unsigned long long full[kMaxSlots], empty[kMaxSlots];  // copies landed; products done
@@ -148,6 +145,16 @@ struct Cursor {
         g.sink = P.window > 0 ? min((P.sinks + S::kKeys - 1) / S::kKeys, g.first) : 0;
         g.tiles = g.sink + g.pos1 / S::kKeys - g.first + 1;
         g.of_first = g.sink + min(g.pos1, g.t0 + P.tokens - 1) / S::kKeys - g.first + 1;
+        // the diagonal: tiles that end past the first token; the window's edge: those that start before the last token's
+        // window does, unless they are of sinks alone
+        const int shift = g.sink - g.first;
+        g.cut = (g.t0 + 1) / S::kKeys + shift;
+        g.edge0 = g.edge1 = 0;
+        if (P.window > 0 && g.pos1 >= P.window) {
+          const int all = P.sinks / S::kKeys;
+          g.edge0 = all <= g.sink ? all : all + shift;
+          g.edge1 = (g.pos1 - P.window) / S::kKeys + shift + 1;
+        }
         return true;
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
@@ -278,7 +285,7 @@ __device__ void guard_warps(const PromptParams& P, unsigned char* ring, Control&
     for (int i = 0; i < u.tiles && !dead; ++i) {
       for (int half = 0; half < S::kHalves; ++half) turn.next(S::kSlots);  // the keys
       const int base = base_of<S>(u, i);
-      const bool cut = cuts<S>(P, u, base);
+      const bool cut = cuts(u, i);
       for (int half = 0; half < S::kHalves; ++half, ++nth) {
         wait(&c.full[turn.slot], turn.parity);
         if (dead) break;
@@ -421,7 +428,7 @@ struct Issuer {
 template <class S>
 __device__ void scores_warp(const PromptParams& P, int r, uint32_t sq, uint32_t ring, Control& c) {
   Issuer<S> w(P, c);
-  const uint32_t tmem = c.tmem + 2 * r * S::kKeys, q = uniform(operand_low(sq + r * S::kQ, 0));
+  const uint32_t tmem = uniform(c.tmem + 2 * r * S::kKeys), q = uniform(operand_low(sq + r * S::kQ, 0));
   uint32_t it = 0, q_units = 0;  // tiles scored, units begun
   Unit u;
   int n;
@@ -433,7 +440,7 @@ __device__ void scores_warp(const PromptParams& P, int r, uint32_t sq, uint32_t 
       if (i < n) {
         const uint32_t b = it & 1;
         unsigned long long* const there = &c.s_full[2 * r + b];
-        const uint32_t d = uniform(tmem + b * S::kKeys);
+        const uint32_t d = tmem + b * S::kKeys;
         Turn t = w.turn;
 #pragma unroll
         for (int half = 0; half < S::kHalves; ++half) {
@@ -442,7 +449,7 @@ __device__ void scores_warp(const PromptParams& P, int r, uint32_t sq, uint32_t 
           else w.wait(&c.full[t.slot], t.parity);
           if (w.dead) break;
           fence_after();
-          const uint32_t k = uniform(operand_low(ring + t.slot * S::kSlot, 0));
+          const uint32_t k = operand_low(ring + t.slot * S::kSlot, 0);
           if (elected()) {
 #pragma unroll
             for (int x = 0; x < S::kWide / 16; ++x) {
@@ -472,7 +479,7 @@ template <class S>
 __device__ void values_warp(const PromptParams& P, int r, uint32_t ring, Control& c) {
   Issuer<S> w(P, c);
   for (int half = 0; half < S::kHalves; ++half) w.turn.next(S::kSlots);
-  const uint32_t tmem = c.tmem + 2 * r * S::kKeys, o = uniform(c.tmem + S::kOut + r * S::D);
+  const uint32_t tmem = uniform(c.tmem + 2 * r * S::kKeys), o = uniform(c.tmem + S::kOut + r * S::D);
   uint32_t it = 0, o_units = 0, nth = 0;  // tiles multiplied, units begun, slots of values passed
   Unit u;
   int n;
@@ -483,10 +490,10 @@ __device__ void values_warp(const PromptParams& P, int r, uint32_t ring, Control
     for (int i = 0; i < u.tiles && !w.dead; ++i, nth += S::kHalves) {
       if (i < n) {
         const uint32_t b = it & 1;
-        const bool cut = cuts<S>(P, u, base_of<S>(u, i));
+        const bool cut = cuts(u, i);
         unsigned long long* const added = &c.pv_done[2 * r + b];
-        const uint32_t weights = uniform(tmem + b * S::kKeys);
-        const bool more = uniform(i);
+        const uint32_t weights = tmem + b * S::kKeys;
+        const bool more = i != 0;
         Turn t = w.turn;
         bool slow = false;
         if (cut) {
@@ -500,7 +507,7 @@ __device__ void values_warp(const PromptParams& P, int r, uint32_t ring, Control
           if (w.dead) break;
           fence_after();
           if (cut && half == 0) slow = uniform(is_slow<S>(c, nth));
-          const uint32_t v = uniform(operand_low(ring + t.slot * S::kSlot, S::kRun));
+          const uint32_t v = operand_low(ring + t.slot * S::kSlot, S::kRun);
           if (elected()) {
             if (!slow) {
 #pragma unroll
@@ -673,7 +680,7 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
     for (int i = 0; i < count && !dead; ++i, ++it) {
       const uint32_t b = 2 * r + (it & 1), buf = lanes + b * S::kKeys;
       const int base = base_of<S>(u, i);
-      const bool cut = cuts<S>(P, u, base);
+      const bool cut = cuts(u, i);
       wait(&c.s_full[b], (it >> 1) & 1);
       if (dead) break;
       fence_after();
