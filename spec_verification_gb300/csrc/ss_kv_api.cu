@@ -568,7 +568,7 @@ ss_status ss_attend_prompt(const ss_prompt_batch* b) {
   ss_status s = check_stride(c, b->k_stride);
   if (s == SS_OK) s = check_stride(c, b->v_stride);
   if (s != SS_OK) return s;
-  for (const int64_t x : {b->q_stride, b->k_stride, b->v_stride})
+  for (const int64_t x : {b->q_stride, b->k_stride, b->v_stride, b->out_stride})
     if (x > (1ll << 36)) return fail(SS_ERR_ARG, "token strides must be at most 2^36 elements");
   for (const void* x : {b->q, b->k, b->v, static_cast<const void*>(b->out)})
     if (!aligned(x, 16)) return fail(SS_ERR_ALIGN, "q, k, v and out must be 16-byte aligned");
@@ -593,6 +593,7 @@ ss_status ss_attend_prompt(const ss_prompt_batch* b) {
   P.heads = std::min(group, 128);
   P.tokens = 128 / P.heads;
   P.chunks = (group + P.heads - 1) / P.heads;
+  P.staged = 32 % P.heads == 0;
   // Two tiles of query rows to a unit load keys half as often; one, two CTAs to an SM, hides the start and end of a unit
   // behind the other's products.  Measured (us, 32/8 heads of 128, two / one): 16000 tokens 1170 / 1312, 16 x 2000 391 /
   // 412, 50 x 500 141 / 152, 100 x 250 112.5 / 114.5, 4000 91.7 / 95.3; 1000 20.3 / 19.0, 300 11.7 / 10.3, 60 9.2 / 7.9,
@@ -604,7 +605,7 @@ ss_status ss_attend_prompt(const ss_prompt_batch* b) {
   P.ended = reinterpret_cast<uint32_t*>(P.next + 1);
   P.spin_limit = kSpin;
   const OnDevice on(c.device);
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo = {};
   // (a stride is of no matter to one token, but must be a tensor map's: no larger than 2^40 bytes)
   const cuuint64_t q_dims[3] = {(cuuint64_t)d, (cuuint64_t)c.q_heads, (cuuint64_t)b->tokens};
   const int64_t q_strides[2] = {d, b->q_stride};
@@ -615,11 +616,14 @@ ss_status ss_attend_prompt(const ss_prompt_batch* b) {
   s = encode_lines(&mq, b->q, 3, q_dims, q_strides, q_box);
   if (s == SS_OK) s = encode_lines(&mk, b->k, 4, dims, k_strides, box);
   if (s == SS_OK) s = encode_lines(&mv, b->v, 4, dims, v_strides, box);
+  const int64_t o_strides[2] = {d, b->out_stride};
+  const cuuint32_t o_box[3] = {64, (cuuint32_t)P.heads, (cuuint32_t)(32 / P.heads)};
+  if (s == SS_OK && P.staged) s = encode_lines(&mo, b->out, 3, q_dims, o_strides, o_box);
   if (s != SS_OK) return s;
   // as many CTAs as stay on the GPU, but no more than there can be units
   const int64_t per = (int64_t)k.tiles * P.tokens, units = ((P.max_tokens + per - 1) / per + b->B) * P.hkv * P.chunks;
   const int grid = (int)std::min<int64_t>((int64_t)k.ctas * p->sms, units);
-  void* args[] = {&P, &mq, &mk, &mv};
+  void* args[] = {&P, &mq, &mk, &mv, &mo};
   const Range range("ss_attend_prompt");
   const cudaError_t e = cudaLaunchKernel(k.fn, dim3(grid), dim3(k.threads), args, k.smem, static_cast<cudaStream_t>(b->stream));
   return e == cudaSuccess ? SS_OK : cuda_fail(e, "ss_attend_prompt");

@@ -117,7 +117,7 @@ struct PromptParams {
   uint32_t* row_status;
   float scale_log2;
   int B, hkv, group, max_tokens, window, sinks;
-  int aligned;                 // are rows of the output 32-byte aligned?
+  int aligned, staged;         // are rows of the output 32-byte aligned, does a warp's part of a tile of rows have whole tokens?
   int heads, tokens, chunks;   // query heads and tokens of a tile of rows, tiles that a key head's query heads take
   unsigned long long* next;    // units handed out beyond the first of each CTA
   uint32_t* ended;             // CTAs that have ended

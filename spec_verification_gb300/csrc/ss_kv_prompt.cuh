@@ -62,10 +62,13 @@ struct Shape {
   static constexpr int kQ = D / 64 * kQRun;                   // bytes of the queries of a tile of rows
   static constexpr int kOut = 2 * TILES * kKeys;              // first column of the outputs in tensor memory
   static constexpr uint32_t kCols = 512 / kCtas;
-  // slots: as many as there is room for beside the queries and the control block
-  static constexpr int kFit = (228 * 1024 / kCtas - 1024 - 1024 - 2048 - TILES * kQ) / kSlot;
+  // Outputs on their way out: 64 columns of a softmax warp's 32 rows.  Only where stores from registers are what the end of
+  // a unit waits for (64 KB of rows at about 16 bytes a cycle: 4000 cycles of two tiles of 128 columns) and there is room.
+  static constexpr int kStage = TILES == 2 ? 32 * 128 : 0;
+  // slots: as many as there is room for beside the queries, outputs and the control block
+  static constexpr int kFit = (228 * 1024 / kCtas - 1024 - 1024 - 2048 - TILES * kQ - kSoftmax * kStage) / kSlot;
   static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
-  static constexpr int kSmem = 1024 + TILES * kQ + kSlots * kSlot;
+  static constexpr int kSmem = 1024 + TILES * kQ + kSlots * kSlot + kSoftmax * kStage;
   static constexpr uint32_t kCommon = 1u << 4 | Elem<T>::kFormat << 7 | Elem<T>::kFormat << 10 | (128u >> 4) << 24;
   static constexpr uint32_t kScores = kCommon | (kKeys >> 3) << 17;
   static constexpr uint32_t kValues = kCommon | 1u << 16 | (uint32_t)(kWide >> 3) << 17;
@@ -645,7 +648,7 @@ __device__ __forceinline__ void store16(void* to, bool aligned, uint32_t a, uint
 }
 
 template <class S>
-__device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, Control& c) {
+__device__ void softmax_warps(const PromptParams& P, const CUtensorMap* mo, const unsigned char* ring, unsigned char* stage, Control& c) {
   using T = typename S::T;
   using E = Elem<T>;
   constexpr int D = S::D;
@@ -784,14 +787,36 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
       const float f = l == 0.0f ? 0.0f : 1.0f / l;
       const int head = c.unit[sg & 1].chunk * P.heads + in_group;
       const bool live = m < P.heads * P.tokens && pos <= c.unit[sg & 1].pos1 && head < P.group;
-      const long long q = c.unit[sg & 1].q0 + pos;
-      const int to_head = c.unit[sg & 1].h * P.group + head;
+      const int q0 = c.unit[sg & 1].q0, head0 = c.unit[sg & 1].h * P.group;
+      const long long q = q0 + pos;
+      const int to_head = head0 + head;
       T* const to = static_cast<T*>(P.out) + q * P.out_stride + (long long)to_head * D;
       if (live && P.lse) P.lse[q * (P.group * P.hkv) + to_head] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
+      const bool by_copy = S::kStage > 0 && P.staged && __all_sync(0xffffffffu, live);
 #pragma unroll 1
       for (int d = 0; d < D; d += 64) {
         uint32_t o[64];
         tmem_load(o, out_at + d);
+        if (by_copy) {
+          // the last 64 columns have left the stage
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            auto val = [&](int k) { return __uint_as_float(o[8 * n + k]) * f; };
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((n ^ (lane & 7)) << 4)) =
+                make_uint4(E::pack(val(0), val(1)), E::pack(val(2), val(3)), E::pack(val(4), val(5)), E::pack(val(6), val(7)));
+          }
+          proxy_fence();
+          __syncwarp();
+          if (lane == 0) {  // (this lane's row is the first of the warp's)
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(mo), "r"(d), "r"(to_head),
+                         "r"(q0 + pos), "r"(smem_u32(stage))
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+          continue;
+        }
         if (!live) continue;
 #pragma unroll
         for (int n = 0; n < 64; n += 16) {
@@ -807,6 +832,8 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
     __syncwarp();
     if (lane == 0 && !dead) arrive(&c.seg_empty[sg & 1]);
   }
+  if (S::kStage > 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  __syncwarp();
   if (dead) report_all(P);
 }
 
@@ -814,7 +841,7 @@ __device__ void softmax_warps(const PromptParams& P, const unsigned char* ring, 
 template <class T, int D, int TILES>
 __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), (Shape<T, D, TILES>::kCtas))
     prompt_kernel(const PromptParams P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                  const __grid_constant__ CUtensorMap mv) {
+                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
   using S = Shape<T, D, TILES>;
   extern __shared__ unsigned char raw[];
   __shared__ Control c;
@@ -856,7 +883,7 @@ __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), (Shape<T, D, T
   __syncthreads();
   fence_after();
   if (warp < S::kSoftmax) {
-    softmax_warps<S>(P, ring, c);
+    softmax_warps<S>(P, &mo, ring, ring + S::kSlots * S::kSlot + warp * S::kStage, c);
   } else if (warp == S::kLoad) {
     load_warp<S>(P, &mq, &mk, &mv, smem_u32(base), smem_u32(ring), c);
   } else if (warp < S::kGuard) {

@@ -135,6 +135,65 @@ def test_prompts(lengths, hq, hkv, dim, kind, window, sinks):
     assert torch.equal(first, p.out)
 
 
+# prompts long enough for two tiles of query rows to a unit (more than 200 tokens a prompt, tokens * q_heads above 256 an SM)
+LONG = [
+    ([3000, 1, 500, 0, 1700], 8, 2, "bf16"),   # 32 tokens to a tile of rows: whole ones leave by way of shared memory
+    ([2900, 40], 14, 2, "f16"),                # 18 tokens, 126 rows: stores from registers
+    ([2560, 130], 16, 16, "bf16"),             # 128 tokens: the first tile of rows has fewer key tiles
+    ([700] * 8, 8, 1, "f16"),
+    ([600, 610], 64, 1, "bf16"),               # two tokens
+]
+
+
+@pytest.mark.parametrize("lengths,hq,hkv,kind", LONG)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 0), (700, 70)])
+def test_two_tiles_of_rows(lengths, hq, hkv, kind, window, sinks):
+    p = Prompts(lengths, hq, hkv, 128, kind, seed=hq)
+    p.run(window, sinks)
+    p.check(window, sinks)
+    assert p.status.tolist() == [0] * len(lengths)
+    first = p.out.clone()
+    p.run(window, sinks, lse=None)
+    torch.cuda.synchronize()
+    assert torch.equal(first, p.out)
+
+
+@pytest.mark.parametrize("kind,hq", [("bf16", 8), ("f16", 14)])
+def test_two_tiles_of_rows_with_values_that_are_not_finite(kind, hq):
+    p = Prompts([3000, 1700], hq, 2, 128, kind)
+    p.v[1010, 1, 7], p.v[2999, 0, 3] = math.inf, math.nan
+    p.run(window=300)
+    torch.cuda.synchronize()
+    got, half = p.out[:4700].double(), hq // 2
+    expect = torch.zeros_like(got, dtype=torch.bool)
+    expect[1010:1310, half:, 7] = True
+    expect[2999, :half, 3] = True
+    assert torch.equal(~torch.isfinite(got), expect)
+    p.v[1010, 1, 7] = p.v[2999, 0, 3] = 0.0
+    p.run(window=300)
+    torch.cuda.synchronize()
+    clean = p.out[:4700].double()
+    assert torch.all(((got - clean).abs() <= 2 * U[kind] * clean.abs() + 2.0 ** -16)[~expect])
+
+
+def test_two_tiles_of_rows_in_a_graph_and_on_odd_outputs():
+    p = Prompts([3000, 2200], 8, 2, 128, "bf16")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.run()
+    for lengths in ([5200, 0], [1, 5199], [2600, 2600]):
+        p.out.fill_(7.0)
+        p.lse.fill_(7.0)
+        p.cu.copy_(_i32([0] + np.cumsum(lengths).tolist()))
+        graph.replay()
+        p.check(lengths=lengths)
+    wide = torch.full((5203, 8 * 128 + 8), 7.0, device="cuda").to(torch.bfloat16)
+    out = wide[:, 8:].view(5203, 8, 128)
+    p.run(out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:5200], p.out[:5200]) and torch.all(out[5200:] == 7.0) and torch.all(wide[:, :8] == 7.0)
+
+
 def test_long_prompt():
     """Many units to a CTA; the last rows of a long prompt, and its first, against 64 bits."""
     p = Prompts([5000, 3], 8, 1, 128, "bf16")
