@@ -745,35 +745,33 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         };
         uint32_t x[kChunk];
         float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        // of this thread's keys, by groups: the factors of the scores and of the values, read once: shared memory is busy with
-        // the conversion, and a look at it takes long
-        constexpr int kGroups = S::kBlocks ? KEYS / 16 : 1;
         const int tile = it & (kBadTiles - 1), group0 = key0 >> 4;
-        float by_k[kGroups], v[kGroups];
-        if constexpr (S::kBlocks) {
-          read_factors(by_k, &factors->k[tile][group0]);
-          read_factors(v, &factors->v[tile][group0]);
-#pragma unroll
-          for (int n = 0; n < kGroups; ++n) by_k[n] = factor_of(scale, by_k[n]);
-        }
         float top = -INFINITY;
-#pragma unroll
-        for (int at = 0; at < KEYS; at += kChunk) {
-          scores(x, at);
-          if constexpr (S::kBlocks) {
+        if constexpr (S::kBlocks) {
+          // (not unrolled: with its masks the loop would not stay among the instructions at hand)
+#pragma unroll 1
+          for (int at = 0; at < KEYS; at += kChunk) {
+            float by_k[kChunk / 16], v[kChunk / 16];
+            read_factors(by_k, &factors->k[tile][group0 + (at >> 4)]);
+            read_factors(v, &factors->v[tile][group0 + (at >> 4)]);
+            scores(x, at);
 #pragma unroll
             for (int g0 = 0; g0 < kChunk; g0 += 16) {
 #pragma unroll
-              for (int n = 0; n < 4; ++n) t[n] = fmaxf(fmaxf(__uint_as_float(x[g0 + n]), __uint_as_float(x[g0 + 4 + n])), fmaxf(__uint_as_float(x[g0 + 8 + n]), __uint_as_float(x[g0 + 12 + n])));
-              const int n = (at + g0) >> 4;
-              top = fmaxf(top, __fadd_rn(__fmul_rn(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), by_k[n]), log2_of(v[n])));
+              for (int n = 0; n < 4; ++n)
+                t[n] = fmaxf(fmaxf(__uint_as_float(x[g0 + n]), __uint_as_float(x[g0 + 4 + n])), fmaxf(__uint_as_float(x[g0 + 8 + n]), __uint_as_float(x[g0 + 12 + n])));
+              top = fmaxf(top, __fadd_rn(__fmul_rn(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), factor_of(scale, by_k[g0 / 16])), log2_of(v[g0 / 16])));
             }
-          } else {
+          }
+        } else {
+#pragma unroll
+          for (int at = 0; at < KEYS; at += kChunk) {
+            scores(x, at);
 #pragma unroll
             for (int n = 0; n < kChunk; ++n) t[n & 3] = fmaxf(t[n & 3], __uint_as_float(x[n]));
           }
+          top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
         }
-        if (!S::kBlocks) top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
         const bool grow = live && top - mx > 8.0f + E::kLift;
         if (__any_sync(0xffffffffu, grow)) {
           const float now = grow ? (fabsf(top) > kLarge ? top : S::kBlocks ? rintf(top - E::kLift) : top - E::kLift) : mx;
@@ -809,17 +807,19 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
           l += sums.x;
           exact += sums.y;
         }
-#pragma unroll
-        for (int at = 0; at < KEYS && !large; at += kChunk) {
-          if (KEYS > kChunk) scores(x, at);
-          uint32_t w[kChunk / 2];
-          float s0 = 0.0f, s1 = 0.0f, e0 = 0.0f, e1 = 0.0f;
-          if constexpr (S::kBlocks) {
+        if constexpr (S::kBlocks) {
+#pragma unroll 1
+          for (int at = 0; at < KEYS && !large; at += kChunk) {
+            float by_k[kChunk / 16], v[kChunk / 16];
+            read_factors(by_k, &factors->k[tile][group0 + (at >> 4)]);
+            read_factors(v, &factors->v[tile][group0 + (at >> 4)]);
+            if (KEYS > kChunk) scores(x, at);
+            uint32_t w[kChunk / 2];
 #pragma unroll
             for (int g0 = 0; g0 < kChunk; g0 += 16) {
-              const int group = (at + g0) >> 4;
-              const float by = by_k[group], less = log2_of(v[group]) - z;
-              s0 = s1 = 0.0f;
+              const int group = g0 >> 4;
+              const float by = factor_of(scale, by_k[group]), less = log2_of(v[group]) - z;
+              float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
               for (int n = g0 / 2; n < g0 / 2 + 8; ++n) {
                 const float a = ex2(fmaf(__uint_as_float(x[2 * n]), by, less)), e = ex2(fmaf(__uint_as_float(x[2 * n + 1]), by, less));
@@ -829,10 +829,15 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
               }
               l = fmaf(s0 + s1, back_of(v[group]), l);
             }
-            exact = l;
             tmem_store(lanes + b * kTile + (key0 + at) / 2, w);
-            continue;
           }
+          exact = l;
+        }
+#pragma unroll
+        for (int at = 0; at < (S::kBlocks ? 0 : KEYS) && !large; at += kChunk) {
+          if (KEYS > kChunk) scores(x, at);
+          uint32_t w[kChunk / 2];
+          float s0 = 0.0f, s1 = 0.0f, e0 = 0.0f, e1 = 0.0f;
 #pragma unroll
           for (int n = 0; n < kChunk / 2; ++n) {
             const float a = ex2(fmaf(__uint_as_float(x[2 * n]), scale, -z)), e = ex2(fmaf(__uint_as_float(x[2 * n + 1]), scale, -z));
