@@ -733,11 +733,27 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
       const uint64_t seen = part ? visible_keys(P, base, p, bad) : ~0ull;
       unsigned char* values = ring + v_turn.slot * S::kSlot;
       if (busy) {
+        // Where scores are read twice and have factors, hidden ones are overwritten first: with masks at every read the loops
+        // below would not stay among the instructions at hand (64 query rows 113 us, so 88; 256 columns 110, so 84).
+        constexpr bool kHideFirst = S::kBlocks && KEYS > kChunk;
+        if (kHideFirst && part) {
+#pragma unroll 1
+          for (int at = 0; at < KEYS; at += 32) {
+            uint32_t y[32];
+            tmem_load(y, lanes + b * kTile + key0 + at);
+            const uint32_t word = (uint32_t)(seen >> (key0 + at));
+#pragma unroll
+            for (int n = 0; n < 32; ++n)
+              if (!(word >> n & 1)) y[n] = 0xff800000u;
+            tmem_store(lanes + b * kTile + key0 + at, y);
+          }
+          store_wait();
+        }
         // this thread's scores, kChunk at a time: one chunk where registers allow, else each is read once for the
         // maximum and once for its weights
         auto scores = [&](uint32_t (&x)[kChunk], int at) {
           tmem_load(x, lanes + b * kTile + key0 + at);
-          if (part) {
+          if (part && !kHideFirst) {
 #pragma unroll
             for (int n = 0; n < kChunk; ++n)
               if (!((uint32_t)(seen >> (key0 + at + (n & 32))) >> (n & 31) & 1)) x[n] = 0xff800000u;
@@ -745,13 +761,14 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         };
         uint32_t x[kChunk];
         float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // the factors of this thread's keys, by groups of 16; the loops are not unrolled for the same reason
         const int tile = it & (kBadTiles - 1), group0 = key0 >> 4;
+        constexpr int kGroups = kChunk / 16;
         float top = -INFINITY;
         if constexpr (S::kBlocks) {
-          // (not unrolled: with its masks the loop would not stay among the instructions at hand)
 #pragma unroll 1
           for (int at = 0; at < KEYS; at += kChunk) {
-            float by_k[kChunk / 16], v[kChunk / 16];
+            float by_k[kGroups], v[kGroups];
             read_factors(by_k, &factors->k[tile][group0 + (at >> 4)]);
             read_factors(v, &factors->v[tile][group0 + (at >> 4)]);
             scores(x, at);
@@ -810,15 +827,14 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         if constexpr (S::kBlocks) {
 #pragma unroll 1
           for (int at = 0; at < KEYS && !large; at += kChunk) {
-            float by_k[kChunk / 16], v[kChunk / 16];
+            float by_k[kGroups], v[kGroups];
             read_factors(by_k, &factors->k[tile][group0 + (at >> 4)]);
             read_factors(v, &factors->v[tile][group0 + (at >> 4)]);
             if (KEYS > kChunk) scores(x, at);
             uint32_t w[kChunk / 2];
 #pragma unroll
             for (int g0 = 0; g0 < kChunk; g0 += 16) {
-              const int group = g0 >> 4;
-              const float by = factor_of(scale, by_k[group]), less = log2_of(v[group]) - z;
+              const float by = factor_of(scale, by_k[g0 / 16]), less = log2_of(v[g0 / 16]) - z;
               float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
               for (int n = g0 / 2; n < g0 / 2 + 8; ++n) {
@@ -827,7 +843,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
                 s0 += a;
                 s1 += e;
               }
-              l = fmaf(s0 + s1, back_of(v[group]), l);
+              l = fmaf(s0 + s1, back_of(v[g0 / 16]), l);
             }
             tmem_store(lanes + b * kTile + (key0 + at) / 2, w);
           }
