@@ -6,10 +6,15 @@
 // near the row's largest exponent and moves only when a weight would pass 2^8.
 //
 // What bounds it.  4 * head_dim operations for each pair of query and key: at
-// prompts of some thousand tokens the tensor pipe.  A tile of 128 query rows
-// and 128 keys takes it 4 * head_dim * 2 cycles for S = Q K^T and O += P V,
-// and the 128 threads that weigh it about as long, so two tiles of rows take
-// turns: while one is weighed the other is multiplied.
+// prompts of some thousand tokens the tensor pipe, at 128 columns and more also
+// the power it may draw.  128 query rows and 64 keys of 128 columns take the
+// pipe 640 cycles for S = Q K^T (of which 64 keys use two thirds of it: the
+// queries are read from shared memory for so few) and O += P V, the 128 threads
+// that weigh them about 1300, so two tiles of rows, or two CTAs, share an SM.
+// With 64 columns the weighing is the bound.  Measured (one prompt, causal):
+// 16000 tokens of 32/8 heads of 128 1191 us, 1.76 PFLOP/s (the library's matrix
+// product: 1.93, 1.74 sustained); 28/4 heads of 64 964 us, 0.95; 16/8 of 256
+// 1359 us, 1.54.
 //
 // Query rows.  The heads that share a key head lie next to each other in a
 // tile: `heads` of them for each of `tokens` tokens (heads * tokens <= 128), so
@@ -21,9 +26,16 @@
 // A CTA's warps:
 //  - load: takes units, publishes them, runs the ring of key and value tiles
 //    (TMA) and brings their queries (TMA; a box of heads by tokens).
-//  - scores and values: two warps for each tile of rows issue tcgen05.mma.
+//  - scores and values: two warps for each tile of rows issue tcgen05.mma, one
+//    the scores, two tiles of keys ahead, one the products with the values.  A
+//    warp's waits and issuing take about as long as its products, so they have
+//    to overlap: with one warp for all 16000 tokens took 1977 us, with one for
+//    each tile of rows 1898, with the four 1372.
 //  - softmax: four warps to a tile of rows; a thread owns a row (a lane of
-//    tensor memory), reads its 128 scores, writes its weights over them.
+//    tensor memory), reads its scores, writes its weights over them.  Nothing
+//    of its loop may be spilled: the 28 KB that the SM has left beside its
+//    shared memory hold no stack of 448 threads (1434 us with 100 bytes, 1218
+//    without).
 //  - guard: a warp looks at every tile of values before the products do.  In
 //    one that not every row sees in full, values that no row sees become zeros
 //    (0 x NaN must not reach a sum), and if one that only some rows see is not
@@ -32,6 +44,11 @@
 // tile's scores are there when one has been weighed, in the first 256 columns,
 // outputs in the others.  With two tiles of rows that leaves 64 keys to a tile;
 // 256 columns of output leave room for one tile of rows and 128 keys.
+//
+// The divisor is the sum of the weights before they are rounded for the
+// product.  That of the rounded bf16 weights, as in ss_kv_attend.cuh, costs 10
+// to 18 % of the time here and brings the error from 1.31 to 1.26 of that of
+// the output's own rounding.
 #pragma once
 
 #include <algorithm>
