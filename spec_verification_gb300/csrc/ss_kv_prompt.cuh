@@ -516,17 +516,21 @@ __device__ void values_warp(const PromptParams& P, int r, uint32_t ring, Control
         const bool more = i != 0;
         Turn t = w.turn;
         bool slow = false;
-        if (cut) {
-#pragma unroll
-          for (int half = 0; half < S::kHalves; ++half) w.wait(&c.ready[(nth + half) % kMaxSlots], parity_of(nth + half));
-        }
 #pragma unroll
         for (int half = 0; half < S::kHalves; ++half) {
+          // Every slot is waited for by way of the guard, whether it had to look at it or not: a place in the ring is then
+          // never brought anew before the guard has passed it.
+          const uint32_t number = nth + half;
+          const bool looked = done(&c.ready[number % kMaxSlots], parity_of(number));
           if (half == 0) w.wait(&c.full[t.slot], t.parity, &c.p_full[2 * r + b], (it >> 1) & 1);
           else w.wait(&c.full[t.slot], t.parity);
+          if (!__all_sync(0xffffffffu, looked)) w.wait(&c.ready[number % kMaxSlots], parity_of(number));
+          if (cut && half == 0) {
+            if (S::kHalves == 2) w.wait(&c.ready[(number + 1) % kMaxSlots], parity_of(number + 1));
+            slow = uniform(is_slow<S>(c, nth));
+          }
           if (w.dead) break;
           fence_after();
-          if (cut && half == 0) slow = uniform(is_slow<S>(c, nth));
           const uint32_t v = operand_low(ring + t.slot * S::kSlot, S::kRun);
           if (elected()) {
             if (!slow) {
@@ -682,7 +686,7 @@ __device__ void softmax_warps(const PromptParams& P, const CUtensorMap* mo, cons
   uint32_t nth = 0;  // slots of values before the unit
   uint32_t it = 0;   // tiles weighed so far
   // the slot of values number n: of the CTA's slots every 2 * kHalves bring a tile's keys, then its values
-  auto slot_of = [](uint32_t n) { return (n / S::kHalves * 2 * S::kHalves + S::kHalves + n % S::kHalves) % S::kSlots; };
+  auto slot_of = [](uint64_t n) { return (uint32_t)((n / S::kHalves * 2 * S::kHalves + S::kHalves + n % S::kHalves) % S::kSlots); };
   auto added = [&](uint32_t tile) {  // the output holds everything up to this tile
     wait(&c.pv_done[2 * r + (tile & 1)], (tile >> 1) & 1);
     fence_after();
