@@ -13,8 +13,8 @@
 // that weigh them about 1300, so two tiles of rows, or two CTAs, share an SM.
 // With 64 columns the weighing is the bound.  Measured (one prompt, causal):
 // 16000 tokens of 32/8 heads of 128 1191 us, 1.76 PFLOP/s (the library's matrix
-// product: 1.93, 1.74 sustained); 28/4 heads of 64 964 us, 0.95; 16/8 of 256
-// 1359 us, 1.54.
+// product: 1.93, 1.74 sustained); 28/4 heads of 64 960 us, 0.96; 16/8 of 256
+// 1436 us, 1.46.
 //
 // Query rows.  The heads that share a key head lie next to each other in a
 // tile: `heads` of them for each of `tokens` tokens (heads * tokens <= 128), so
@@ -40,10 +40,15 @@
 //    one that not every row sees in full, values that no row sees become zeros
 //    (0 x NaN must not reach a sum), and if one that only some rows see is not
 //    finite, the tile is added key by key by the softmax warps.
-// Tensor memory: two buffers of scores for each tile of rows, so that the next
-// tile's scores are there when one has been weighed, in the first 256 columns,
-// outputs in the others.  With two tiles of rows that leaves 64 keys to a tile;
-// 256 columns of output leave room for one tile of rows and 128 keys.
+// Tensor memory: two buffers of scores of 64 keys for each tile of rows, so that
+// the next tile's scores are there when one has been weighed, then outputs.
+// 256 columns of output leave room for one tile of rows, and between the two
+// for its queries: the softmax warps bring them there as soon as the last
+// scores of the unit before are taken, the next unit's queries come meanwhile,
+// and outputs leave by way of the room they came to.  (With 128 keys to a tile
+// and queries in shared memory, 5 x 9000 tokens with a window of 1024 took 338
+// us, so 307; 200 x 60 70, so 60; one prompt of 16000 1395, so 1436: there the
+// one tile's softmax is the bound, and it costs less for 128 keys at a time.)
 //
 // The divisor is the sum of the weights before they are rounded for the
 // product.  That of the rounded bf16 weights, as in ss_kv_attend.cuh, costs 10
@@ -70,14 +75,16 @@ struct Shape {
   static constexpr int kProducts = 2 * TILES;
   static constexpr int kLoad = kSoftmax, kProduct = kSoftmax + 1, kGuard = kProduct + kProducts;
   static constexpr int kThreads = 32 * (kGuard + kGuardWarps);
-  static constexpr int kKeys = D <= 128 ? 64 : 128;           // keys of a tile
+  static constexpr int kKeys = 64;                            // keys of a tile
+  static constexpr bool kQTensor = D == 256;                  // queries in tensor memory
   static constexpr int kCtas = TILES == 1 && D <= 128 ? 2 : 1;  // CTAs per SM
   static constexpr int kWide = D < 128 ? D : 128;             // columns of a slot
   static constexpr int kHalves = D / kWide;                   // slots of a tile
   static constexpr int kRun = kKeys * 128, kQRun = 128 * 128; // bytes of 64 columns of a tile, of a tile of rows
   static constexpr int kSlot = kWide / 64 * kRun;
   static constexpr int kQ = D / 64 * kQRun;                   // bytes of the queries of a tile of rows
-  static constexpr int kOut = 2 * TILES * kKeys;              // first column of the outputs in tensor memory
+  static constexpr int kQAt = 2 * TILES * kKeys;              // first column of the queries in tensor memory
+  static constexpr int kOut = kQAt + (kQTensor ? D / 2 : 0);  // and of the outputs
   static constexpr uint32_t kCols = 512 / kCtas;
   // Outputs on their way out: 64 columns of a softmax warp's 32 rows.  Only where stores from registers are what the end of
   // a unit waits for (64 KB of rows at about 16 bytes a cycle: 4000 cycles of two tiles of 128 columns) and there is room.
@@ -115,7 +122,7 @@ struct Control {
   // held keys before): number n + kMaxSlots is copied only when number n has been multiplied.
   unsigned long long ready[kMaxSlots];
   unsigned long long seg_full[2], seg_empty[2];
-  unsigned long long q_full[2], q_free[2];
+  unsigned long long q_full[2], q_free[2], q_ready;
   unsigned long long s_full[4], p_full[4], pv_done[4];  // by buffer: scores there; weights there; added to the output
   unsigned long long o_free[2];
   unsigned long long drained;
@@ -448,13 +455,13 @@ struct Issuer {
 template <class S>
 __device__ void scores_warp(const PromptParams& P, int r, uint32_t sq, uint32_t ring, Control& c) {
   Issuer<S> w(P, c);
-  const uint32_t tmem = uniform(c.tmem + 2 * r * S::kKeys), q = uniform(operand_low(sq + r * S::kQ, 0));
+  const uint32_t tmem = uniform(c.tmem + 2 * r * S::kKeys), q = uniform(S::kQTensor ? c.tmem + S::kQAt : operand_low(sq + r * S::kQ, 0));
   uint32_t it = 0, q_units = 0;  // tiles scored, units begun
   Unit u;
   int n;
 #pragma unroll 1
   for (int sg = 0; w.next(sg, r, u, n); ++sg) {
-    if (n > 0) w.wait(&c.q_full[r], q_units++ & 1);
+    if (n > 0) w.wait(S::kQTensor ? &c.q_ready : &c.q_full[r], q_units++ & 1);
 #pragma unroll 1
     for (int i = 0; i < u.tiles && !w.dead; ++i) {
       if (i < n) {
@@ -474,11 +481,12 @@ __device__ void scores_warp(const PromptParams& P, int r, uint32_t sq, uint32_t 
 #pragma unroll
             for (int x = 0; x < S::kWide / 16; ++x) {
               const uint32_t run = x >> 2, in = (x & 3) * 32 >> 4;
-              mma_ss(d, q + (half * (S::kWide / 64) + run) * (S::kQRun >> 4) + in, k + run * (S::kRun >> 4) + in, S::kScores, half + x != 0);
+              if (S::kQTensor) mma_ts(d, q + half * (S::kWide / 2) + x * 8, k + run * (S::kRun >> 4) + in, S::kScores, half + x != 0);
+              else mma_ss(d, q + (half * (S::kWide / 64) + run) * (S::kQRun >> 4) + in, k + run * (S::kRun >> 4) + in, S::kScores, half + x != 0);
             }
             if (half + 1 == S::kHalves) commit(there);
             commit(&c.empty[t.slot]);
-            if (half + 1 == S::kHalves && i + 1 == n) commit(&c.q_free[r]);
+            if (!S::kQTensor && half + 1 == S::kHalves && i + 1 == n) commit(&c.q_free[r]);
           }
           __syncwarp();
           t.next(S::kSlots);
@@ -669,7 +677,8 @@ __device__ __forceinline__ void store16(void* to, bool aligned, uint32_t a, uint
 }
 
 template <class S>
-__device__ void softmax_warps(const PromptParams& P, const CUtensorMap* mo, const unsigned char* ring, unsigned char* stage, Control& c) {
+__device__ void softmax_warps(const PromptParams& P, const CUtensorMap* mo, unsigned char* sq, const unsigned char* ring, unsigned char* stage,
+                              Control& c) {
   using T = typename S::T;
   using E = Elem<T>;
   constexpr int D = S::D;
@@ -691,10 +700,39 @@ __device__ void softmax_warps(const PromptParams& P, const CUtensorMap* mo, cons
     wait(&c.pv_done[2 * r + (tile & 1)], (tile >> 1) & 1);
     fence_after();
   };
+  // This row's queries of unit sg from shared to tensor memory, once the scores of the unit before are there.
+  auto bring_queries = [&](int sg) {
+    wait(&c.seg_full[sg & 1], (sg >> 1) & 1);
+    if (dead || c.unit[sg & 1].tiles == 0) return;
+    wait(&c.q_full[0], sg & 1);
+    if (dead) return;
+#pragma unroll 1
+    for (int run = 0; run < D / 64; ++run) {
+      uint32_t x[32];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const uint4 y = *reinterpret_cast<const uint4*>(sq + run * S::kQRun + m * 128 + ((n ^ (m & 7)) << 4));
+        x[4 * n] = y.x;
+        x[4 * n + 1] = y.y;
+        x[4 * n + 2] = y.z;
+        x[4 * n + 3] = y.w;
+      }
+      tmem_store(lanes + S::kQAt + run * 32, x);
+    }
+    store_wait();
+    fence_before();
+    __syncwarp();
+    if (lane == 0) arrive(&c.q_ready);
+  };
+  if (S::kQTensor) bring_queries(0);
   bool more = true;
   for (int sg = 0; more; ++sg) {
     wait(&c.seg_full[sg & 1], (sg >> 1) & 1);
     if (dead) break;
+    if (S::kQTensor && lane == 0) {  // the outputs have left the queries' room: the next ones may come
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      arrive(&c.q_free[0]);
+    }
     const Unit u = c.unit[sg & 1];
     more = u.tiles > 0;
     const int count = tiles_of(u, r);  // 0 at the end
@@ -803,6 +841,7 @@ __device__ void softmax_warps(const PromptParams& P, const CUtensorMap* mo, cons
       if (lane == 0) arrive(&c.p_full[b]);
     }
     nth += u.tiles * S::kHalves;
+    if (S::kQTensor && more && !dead) bring_queries(sg + 1);  // its first scores are taken beside this unit's end
     if (count > 0 && !dead) {
       added(it - 1);
       const float f = l == 0.0f ? 0.0f : 1.0f / l;
@@ -813,26 +852,29 @@ __device__ void softmax_warps(const PromptParams& P, const CUtensorMap* mo, cons
       const int to_head = head0 + head;
       T* const to = static_cast<T*>(P.out) + q * P.out_stride + (long long)to_head * D;
       if (live && P.lse) P.lse[q * (P.group * P.hkv) + to_head] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
-      const bool by_copy = S::kStage > 0 && P.staged && __all_sync(0xffffffffu, live);
+      const bool by_copy = (S::kStage > 0 || S::kQTensor) && P.staged && __all_sync(0xffffffffu, live);
 #pragma unroll 1
       for (int d = 0; d < D; d += 64) {
         uint32_t o[64];
         tmem_load(o, out_at + d);
         if (by_copy) {
-          // the last 64 columns have left the stage
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          __syncwarp();
+          // (with queries in tensor memory their room is the stage, of all columns)
+          unsigned char* const to_stage = S::kQTensor ? sq + (d >> 6) * S::kQRun + (warp & 3) * 4096 : stage;
+          if (!S::kQTensor) {  // the last 64 columns have left it
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+          }
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
             auto val = [&](int k) { return __uint_as_float(o[8 * n + k]) * f; };
-            *reinterpret_cast<uint4*>(stage + lane * 128 + ((n ^ (lane & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(to_stage + lane * 128 + ((n ^ (lane & 7)) << 4)) =
                 make_uint4(E::pack(val(0), val(1)), E::pack(val(2), val(3)), E::pack(val(4), val(5)), E::pack(val(6), val(7)));
           }
           proxy_fence();
           __syncwarp();
           if (lane == 0) {  // (this lane's row is the first of the warp's)
             asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(mo), "r"(d), "r"(to_head),
-                         "r"(q0 + pos), "r"(smem_u32(stage))
+                         "r"(q0 + pos), "r"(smem_u32(to_stage))
                          : "memory");
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
@@ -853,7 +895,7 @@ __device__ void softmax_warps(const PromptParams& P, const CUtensorMap* mo, cons
     __syncwarp();
     if (lane == 0 && !dead) arrive(&c.seg_empty[sg & 1]);
   }
-  if (S::kStage > 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  if ((S::kStage > 0 || S::kQTensor) && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   __syncwarp();
   if (dead) report_all(P);
 }
@@ -884,9 +926,10 @@ __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), (Shape<T, D, T
       mbar_init_n(&c.seg_full[i], 1);
       mbar_init_n(&c.seg_empty[i], S::kSoftmax + S::kProducts + kGuardWarps);
       mbar_init_n(&c.q_full[i], 1);
-      mbar_init_n(&c.q_free[i], 1);
+      mbar_init_n(&c.q_free[i], S::kQTensor ? 4 : 1);
       mbar_init_n(&c.o_free[i], 4);
     }
+    mbar_init_n(&c.q_ready, 4);
     mbar_init_n(&c.drained, S::kProducts);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -904,7 +947,7 @@ __global__ void __launch_bounds__((Shape<T, D, TILES>::kThreads), (Shape<T, D, T
   __syncthreads();
   fence_after();
   if (warp < S::kSoftmax) {
-    softmax_warps<S>(P, &mo, ring, ring + S::kSlots * S::kSlot + warp * S::kStage, c);
+    softmax_warps<S>(P, &mo, base, ring, ring + S::kSlots * S::kSlot + warp * S::kStage, c);
   } else if (warp == S::kLoad) {
     load_warp<S>(P, &mq, &mk, &mv, smem_u32(base), smem_u32(ring), c);
   } else if (warp < S::kGuard) {
