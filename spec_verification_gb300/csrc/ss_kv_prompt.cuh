@@ -752,29 +752,19 @@ __device__ void softmax_warps(const PromptParams& P, const CUtensorMap* mo, unsi
         else sees.set(S::kKeys, 0, 0);
         return sees;
       };
-      // (128 scores are read twice, a part at a time: they do not stay in registers beside the rest, but half of them do)
-      uint32_t x[64];
+      uint32_t x[S::kKeys];
       float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      auto hide = [&](uint32_t* w, int from, int count) {
+      tmem_load(x, buf);
+      if (cut) {
         const Seen<S::kKeys> sees = seen();
 #pragma unroll
-        for (int n = 0; n < count; ++n)
-          if (!sees(from + n)) w[n] = 0xff800000u;
-      };
-      auto largest = [&](const uint32_t* w, int count) {
-#pragma unroll
-        for (int n = 0; n < count; n += 8)
-#pragma unroll
-          for (int h = 0; h < 4; ++h) t[h] = fmaxf(t[h], fmaxf(__uint_as_float(w[n + h]), __uint_as_float(w[n + 4 + h])));
-      };
-      if constexpr (S::kKeys == 128) {
-        tmem_load(x, buf + 64);
-        if (cut) hide(x, 64, 64);
-        largest(x, 64);
+        for (int n = 0; n < S::kKeys; ++n)
+          if (!sees(n)) x[n] = 0xff800000u;
       }
-      tmem_load(x, buf);
-      if (cut) hide(x, 0, 64);
-      largest(x, 64);
+#pragma unroll
+      for (int n = 0; n < S::kKeys; n += 8)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) t[h] = fmaxf(t[h], fmaxf(__uint_as_float(x[n + h]), __uint_as_float(x[n + 4 + h])));
       const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
       const bool grow = top - mx > 8.0f + E::kLift;
       if (__any_sync(0xffffffffu, grow)) {
@@ -814,16 +804,9 @@ __device__ void softmax_warps(const PromptParams& P, const CUtensorMap* mo, unsi
           }
           tmem_store(buf + from / 2, p);
         };
-        // (weights lie over the scores of the first 64 keys, which have been read)
+        // (weights lie over scores that have been read)
         weigh(x, 0);
         weigh(x + 32, 32);
-#pragma unroll
-        for (int q = 64; q < S::kKeys; q += 32) {
-          uint32_t y[32];
-          tmem_load(y, buf + q);
-          if (cut) hide(y, q, 32);
-          weigh(y, q);
-        }
         const float2 s = halves(add2(s0, s1));
         l += s.x + s.y;
       }
