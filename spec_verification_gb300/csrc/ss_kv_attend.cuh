@@ -791,7 +791,7 @@ __device__ void softmax_warps(const AttendParams& P, unsigned char* sq, unsigned
         }
         const bool grow = live && top - mx > 8.0f + E::kLift;
         if (__any_sync(0xffffffffu, grow)) {
-          const float now = grow ? (fabsf(top) > kLarge ? top : S::kBlocks ? rintf(top - E::kLift) : top - E::kLift) : mx;
+          const float now = grow ? (fabsf(top) > kLarge ? top : top - E::kLift) : mx;
           const float by = grow ? ex2(mx - now) : 1.0f;  // 0 if nothing was seen before
           mx = now;
           large = __any_sync(0xffffffffu, mx != -INFINITY && fabsf(mx) > kLarge);

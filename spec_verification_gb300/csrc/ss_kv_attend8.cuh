@@ -518,8 +518,7 @@ __device__ void compute_warps(const AttendParams& P, unsigned char* ring, unsign
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
         t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
-        auto lifted = [&](float t) { return fabsf(t) > kLarge ? t : S::kBlocks ? rintf(t - kLift) : t - kLift; };
-        const float n0 = fmaxf(mx0, lifted(t0)), n1 = fmaxf(mx1, lifted(t1));
+        const float n0 = fmaxf(mx0, fabsf(t0) > kLarge ? t0 : t0 - kLift), n1 = fmaxf(mx1, fabsf(t1) > kLarge ? t1 : t1 - kLift);
         const float a0 = n0 == mx0 ? 1.0f : ex2(mx0 - n0), a1 = n1 == mx1 ? 1.0f : ex2(mx1 - n1);
         l0 *= a0;
         l1 *= a1;

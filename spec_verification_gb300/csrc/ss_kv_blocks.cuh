@@ -26,8 +26,9 @@ namespace kv {
 // w_t = 2^(c ks q.k8_t - m) and o = sum w_t vs v8_t / sum w_t.  The kernels keep u_t = w_t vs instead, as
 // u_t = 2^(c ks q.k8_t + log2 vs - m) with m near the largest exponent of u: the product with the values is then that of
 // their bytes, u fits 16 bits whatever the factors are, and sum w_t is the sum over blocks of sum u_t / vs.  A group of 16
-// keys has one factor each, so that costs nothing a score.  log2 vs is a whole number, and m is made one, so that the
-// exponent loses no bits.
+// keys has one factor each, so that costs nothing a score.  log2 vs - m is rounded once for a group, to half a step of 32
+// bits at m, as a score of that size is.  (m is not made a whole number to spare that: the largest weight would then be no
+// power of two, and its rounding to 16 bits the error of every row with one key that dominates.)
 //
 // Of the keys of some tiles, by groups of 16: ks and vs.
 template <int TILES, int GROUPS>

@@ -4,8 +4,9 @@
 Bounds.  Factors are powers of two, so a quotient is exact and a value is rounded once: stores are compared bit for
 bit, and so are loads (a product with a power of two, rounded once).  Attention: as for a cache with a factor for each
 head (tests/test_gpu_kv.py), with these changes.  A weight times its values' factor, u, is rounded to f16: half a step
-of it, or 2^-25 where it is below 2^-14; the largest u of a row is at least 2^6 (m is rounded to a whole number, 7 below
-the first tile's largest), so the latter is 2^-31 of the largest.
+of it, or 2^-25 where it is below 2^-14; the largest u of a row is at least 2^6 (m is 7 below the first tile's largest), so the
+latter is 2^-31 of the largest.  log2 of a factor less m is rounded to 2^-19 at most here (numbers up to 2^6), 2^-20 of a
+weight, as is 2^x.
 """
 import math
 
