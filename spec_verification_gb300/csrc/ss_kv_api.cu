@@ -590,9 +590,17 @@ ss_status ss_attend_prompt(const ss_prompt_batch* b) {
   P.window = b->window >= P.max_tokens ? 0 : b->window;  // a window that reaches every token is none
   P.sinks = P.window ? std::min(b->sinks, P.max_tokens) : 0;
   P.aligned = aligned(b->out, 32) && b->out_stride % 16 == 0;
-  P.heads = std::min(group, 128);
-  P.tokens = 128 / P.heads;
-  P.chunks = (group + P.heads - 1) / P.heads;
+  // The query heads of a key head in as few parts as fill nine tenths of a tile's 128 rows with whole tokens (at most 8; else
+  // in those that fill most): one part for up to 16 heads; 71 heads in three of 24, five tokens each.
+  int most = 0;
+  for (int parts = (group + 127) / 128, last = std::max(8, parts); parts <= last && most < 115; ++parts) {
+    const int heads = (group + parts - 1) / parts, filled = group * (128 / heads) / parts;
+    if (filled <= most) continue;
+    most = filled;
+    P.heads = heads;
+    P.tokens = 128 / heads;
+    P.chunks = parts;
+  }
   P.staged = 32 % P.heads == 0;
   // Two tiles of query rows to a unit load keys half as often; one, two CTAs to an SM, hides the start and end of a unit
   // behind the other's products.  Measured (us, 32/8 heads of 128, two / one): 16000 tokens 1170 / 1312, 16 x 2000 391 /
