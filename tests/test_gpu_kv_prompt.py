@@ -114,7 +114,9 @@ CASES = [
     ([0, 0, 130, 0], 71, 1, 64, "bf16"),
     ([10, 40], 130, 1, 64, "f16"),             # more query heads to a key head than a tile has rows
     ([3, 90], 600, 2, 64, "bf16"),
-    ([200, 75], 66, 2, 128, "bf16"),           # 33 heads in two parts
+    ([200, 75], 66, 2, 128, "bf16"),           # 33 query heads to a key head
+    ([450, 300], 95, 1, 128, "f16"),           # 32, 32 and 31 heads
+    ([40, 70], 76, 2, 256, "bf16"),            # 38 heads in five parts, the last of 6
     ([500, 129, 3], 4, 2, 256, "bf16"),
     ([257, 64], 10, 2, 256, "f16"),
     ([1100, 900], 4, 1, 128, "bf16"),
