@@ -189,7 +189,9 @@ typedef struct {
 } ss_load_batch;
 
 /* Keys and values held at the slots, times their factors, rounded once to the
- * plan's dtype; a slot outside the cache (-1) gives zeros. */
+ * plan's dtype (in SS_F16 all beyond 65504 as 65504 with its sign, NaN as NaN:
+ * a value from 63488 on is held as 65536); a slot outside the cache (-1) gives
+ * zeros. */
 ss_status ss_kv_load_blocks(const ss_load_batch* batch, const ss_kv_block_cache* cache);
 
 /* Queries, keys and values of T tokens on their way from the projection. */
@@ -276,7 +278,8 @@ ss_status ss_attend(const ss_attend_batch* batch, const ss_kv_cache* cache);
 /* ss_attend over a cache with a factor for each block and head, in every other
  * respect as over an SS_E4M3 cache.  Of a row's keys, those whose weight times
  * the factor of its values is below 2^-32 of the largest such product may count
- * as 0 in the output. */
+ * as 0 in the output.  In SS_F16 an output beyond 65504 is infinite, as it is
+ * where held values of 65536 (stored from 63488 on) take nearly all the weight. */
 ss_status ss_attend_blocks(const ss_attend_batch* batch, const ss_kv_block_cache* cache);
 
 /* Whole prompts on their way from the projection (queries and keys rotated),

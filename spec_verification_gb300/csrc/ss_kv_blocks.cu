@@ -49,8 +49,10 @@ struct Pair<__nv_bfloat16> {
 template <>
 struct Pair<__half> {
   static __device__ __forceinline__ float2 of(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+  // Beyond 65504 as 65504 with its sign, NaN as NaN: of f16 values those from 63488 on are held as 65536.
+  static __device__ __forceinline__ float within(float x) { return fabsf(x) > 65504.0f ? copysignf(65504.0f, x) : x; }
   static __device__ __forceinline__ uint32_t to(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
+    const __half2 h = __floats2half2_rn(within(a), within(b));
     return *reinterpret_cast<const uint32_t*>(&h);
   }
   static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
