@@ -126,12 +126,14 @@ struct Group {
 };
 
 // Units: (run, keys or values, head), runs in order of rows.  Every CTA counts the runs of all rows, 32 rows at a time, and
-// its groups of threads take the units in turn; a group holds 32 rows, a row to a lane, until a run lies past them.  What a unit waits for, one after the other: its values and its page, asked for together; its old
-// factor, where it has one.
-template <class T, int D, bool WIDE, int LOADS>
+// its groups of threads take the units in turn; a group holds 32 rows, a row to a lane, until a run lies past them.  What a
+// unit waits for, one after the other: its values and its page, asked for together; its old factor, where it has one.
+// Count: of runs; 64 bits where they could pass 32, as rows that overlap (sums that go up and down) can.  Always 64 bits cost 2 to
+// 5 % (300 rows of 8 tokens 6.2 -> 6.6 us, 8192 of one 120 -> 122).
+template <class T, int D, bool WIDE, int LOADS, class Count>
 __global__ void __launch_bounds__(kNT) store_kernel(const StoreParams P) {
   using G = Group<WIDE>;
-  __shared__ int first[kGroups + 1];  // runs before each 32 rows
+  __shared__ Count first[kGroups + 1];  // runs before each 32 rows
   __shared__ float room[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int groups = (P.B + 31) / 32;
@@ -148,17 +150,17 @@ __global__ void __launch_bounds__(kNT) store_kernel(const StoreParams P) {
   }
   __syncthreads();
   if (warp == 0) {  // eight groups to a lane
-    int n[kGroups / 32], mine = 0;
+    Count n[kGroups / 32], mine = 0;
 #pragma unroll
     for (int k = 0; k < kGroups / 32; ++k) {
       const int g = lane * (kGroups / 32) + k;
       n[k] = g < groups ? first[g + 1] : 0;
       mine += n[k];
     }
-    int sum = mine;
+    Count sum = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, sum, d);
+      const Count y = __shfl_up_sync(0xffffffffu, sum, d);
       if (lane >= d) sum += y;
     }
     sum -= mine;
@@ -174,10 +176,12 @@ __global__ void __launch_bounds__(kNT) store_kernel(const StoreParams P) {
   const int kinds = 2 * P.hkv, at = G::thread(), block = 1 << P.block_shift;
   const long long units = (long long)first[kGroups] * kinds, step = (long long)gridDim.x * (kNT / G::kSize);
   constexpr int kPer = D / 8;  // 16-byte pieces of a new token's head
-  int group = -1, upto = 0, runs = 0;  // the 32 rows that are looked at, runs up to and of this lane's
+  int group = -1, runs = 0;  // the 32 rows that are looked at, runs of this lane's
+  Count upto = 0;            // and up to them
   StoreRow mine = {0, 0, 0, 0};
   for (long long u = (long long)blockIdx.x * (kNT / G::kSize) + (WIDE ? 0 : warp); u < units; u += step) {
-    const int run = (int)(u / kinds), kind = (int)(u - (long long)run * kinds), h = kind % P.hkv;
+    const Count run = (Count)(u / kinds);
+    const int kind = (int)(u - (long long)run * kinds), h = kind % P.hkv;
     const bool values = kind >= P.hkv;
     if (group < 0 || run >= first[group + 1]) {
       group = 0;
@@ -188,7 +192,7 @@ __global__ void __launch_bounds__(kNT) store_kernel(const StoreParams P) {
       runs = upto = runs_of(P, mine);
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, d);
+        const Count y = __shfl_up_sync(0xffffffffu, upto, d);
         if (lane >= d) upto += y;
       }
       upto += first[group];
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(kNT) store_kernel(const StoreParams P) {
     w.q0 = __shfl_sync(0xffffffffu, mine.q0, owner);
     w.n = __shfl_sync(0xffffffffu, mine.n, owner);
     w.held = __shfl_sync(0xffffffffu, mine.held, owner);
-    const int r = 32 * group + owner, left = run - __shfl_sync(0xffffffffu, upto - runs, owner);
+    const int r = 32 * group + owner, left = (int)(run - __shfl_sync(0xffffffffu, upto - runs, owner));
     // tokens [p0, p1) of the row, in one block
     const int blk = (w.held >> P.block_shift) + left;
     const int p0 = max(w.held, blk << P.block_shift), p1 = min(w.held + w.n, (blk + 1) << P.block_shift);
@@ -314,7 +318,7 @@ __global__ void __launch_bounds__(256) load_kernel(const LoadParams P) {
   }
 }
 
-template <class T, int D>
+template <class T, int D, class Count>
 cudaError_t store(const StoreParams& P, int sms, cudaStream_t st) {
   // no more CTAs than there can be units, and no more than stay on the GPU (measured, 16000 tokens of one row, 5, 6, 8 an SM:
   // 17.0, 16.6, 18.7 us)
@@ -323,10 +327,16 @@ cudaError_t store(const StoreParams& P, int sms, cudaStream_t st) {
   const bool wide = values > 16 * 32 * 8;
   const long long units = 2ll * P.hkv * (2ll * P.B + ((long long)P.max_tokens >> P.block_shift));
   const int grid = (int)std::min<long long>(wide ? units : (units + kWarps - 1) / kWarps, 6ll * sms);
-  if (wide) store_kernel<T, D, true, 8><<<grid, kNT, 0, st>>>(P);
-  else if (values > 8 * 32 * 8) store_kernel<T, D, false, 16><<<grid, kNT, 0, st>>>(P);
-  else store_kernel<T, D, false, 8><<<grid, kNT, 0, st>>>(P);
+  if (wide) store_kernel<T, D, true, 8, Count><<<grid, kNT, 0, st>>>(P);
+  else if (values > 8 * 32 * 8) store_kernel<T, D, false, 16, Count><<<grid, kNT, 0, st>>>(P);
+  else store_kernel<T, D, false, 8, Count><<<grid, kNT, 0, st>>>(P);
   return cudaGetLastError();
+}
+template <class T, int D>
+cudaError_t store(const StoreParams& P, int sms, cudaStream_t st) {
+  // a row has at most max_tokens / block + 2 runs, wherever the others are
+  const long long runs = P.B * (((long long)P.max_tokens >> P.block_shift) + 2);
+  return runs < 1ll << 31 ? store<T, D, int>(P, sms, st) : store<T, D, long long>(P, sms, st);
 }
 template <class T, int D>
 cudaError_t load(const LoadParams& P, int sms, cudaStream_t st) {

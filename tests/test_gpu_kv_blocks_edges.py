@@ -46,3 +46,26 @@ def test_large_f16_values_come_back_finite():
         torch.cuda.synchronize()
         held = (8 + (bits & 7)) * 2.0 ** ((bits >> 3) - 10) * factor
         assert torch.all(k_out == min(held, 65504.0)) and torch.all(v_out == min(held, 65504.0))
+
+
+def test_more_runs_than_32_bits_count():
+    """Prefix sums that go up and down: 2050 rows of 2^24 tokens each, on pages that are none, in 2^20 blocks each, between two rows of
+    16 tokens on pages that are some."""
+    rises, n = 2050, 1 << 24
+    rows, blocks = 2 * rises + 3, n // 1024
+    plan = _kv().Plan(max_rows=rows, max_tokens=n, q_heads=1, kv_heads=1, head_dim=64, page_size=1024, num_pages=2, max_blocks=blocks,
+                      dtype="bf16", cache_dtype="e4m3")
+    x = torch.zeros(n, 1, 64, dtype=torch.bfloat16, device="cuda")
+    x[:16] = 3.5
+    cache = torch.zeros(2, 2, 1024, 1, 64, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    factor = torch.full((2, 2, 1, 64), 7.0, device="cuda")
+    table = torch.full((rows, blocks), -1, dtype=torch.int32, device="cuda")
+    table[0, 0], table[-1, 0] = 1, 0
+    held, status = _i32([0] * rows), _i32([0] * rows)
+    seq, cu = _i32([16, 0] + [n, 0] * rises + [16]), _i32([0, 16] + [0, n] * rises + [0, 16])
+    _kv().ss_kv_store_blocks(plan, x, -x, *cache, *factor, table, held, seq, cu, row_status=status)
+    torch.cuda.synchronize()
+    assert status.tolist() == [0, 1 << 9] + [1 << 13, 1 << 9] * rises + [0]
+    for c, f, sign in zip(cache, factor, (1.0, -1.0)):  # 3.5 = 448 * 2^-7
+        assert torch.all(c.float()[:, :16] == sign * 448.0) and torch.all(c.float()[:, 16:] == 0)
+        assert torch.all(f[:, 0, 0] == 2.0 ** -7) and torch.all(f[:, 0, 1:] == 7.0)
