@@ -1,4 +1,5 @@
-"""ss_attend_prompt: what rows that are none leave alone, bit for bit."""
+"""ss_attend_prompt where a CTA takes many units one after the other, and what rows that are none leave alone: against 64
+bits with the bounds of tests/test_gpu_kv_prompt.py, or bit for bit."""
 import math
 
 import pytest
@@ -16,6 +17,62 @@ def _env():
         pytest.skip("needs a CUDA GPU")
     from spec_verification_gb300 import build
     build.build()
+
+
+def units_to_a_cta(lengths, hq, hkv, dim, spare=3):
+    """(units of the call, CTAs, tiles of rows of a unit): the launch of ss_attend_prompt, from its description: a tile of rows has
+    whole tokens of as many query heads as fill 115 of 128 rows, of a key head's heads in as few parts as do."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    group, most = hq // hkv, 0
+    first = -(-group // 128)
+    for parts in range(first, max(8, first) + 1):
+        heads = -(-group // parts)
+        filled = group * (128 // heads) // parts
+        if filled > most:
+            most, tokens, chunks = filled, 128 // heads, parts
+        if most >= 115:
+            break
+    total = sum(lengths) + spare
+    few = total * hq <= 256 * sms or total <= 200 * len(lengths)
+    tiles = 2 if dim == 128 and not few else 1
+    ctas = (2 if tiles == 1 and dim <= 128 else 1) * sms
+    return sum(-(-n // (tiles * tokens)) for n in lengths) * hkv * chunks, ctas, tiles
+
+
+# Lengths are such that a prompt's last tile of rows is partly filled, so that rows that leave by way of shared memory and
+# rows that leave from registers follow one another in a CTA.
+LONG = [1000, 37, 900, 3, 1500, 2100, 450, 333, 129]
+SHORT = [1 + 37 * i % 199 for i in range(110)]
+HANDED = [
+    # lengths, hq, hkv, dim, type, tiles of rows
+    (LONG, 16, 8, 256, "bf16", 1),                     # 64 tokens to a tile: whole ones leave by way of the queries' room
+    (LONG, 40, 8, 256, "f16", 1),                      # 25 tokens of 5 heads: stores from registers
+    ([170] * 40 + [5, 64, 65], 16, 8, 256, "f16", 1),  # short units
+    (SHORT, 16, 8, 128, "bf16", 1),
+    (SHORT, 40, 8, 128, "f16", 1),
+    (LONG + [2600], 32, 8, 128, "bf16", 2),
+    (LONG + [2000], 40, 8, 128, "f16", 2),
+    (LONG + [1800], 28, 4, 64, "bf16", 1),
+    (SHORT, 32, 8, 64, "f16", 1),                      # heads that divide 32
+]
+
+
+@pytest.mark.parametrize("lengths,hq,hkv,dim,kind,tiles", HANDED)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 70)])
+def test_many_units_to_a_cta(lengths, hq, hkv, dim, kind, tiles, window, sinks):
+    """At least five units to a CTA: every barrier between units takes both parities more than once."""
+    units, ctas, of = units_to_a_cta(lengths, hq, hkv, dim)
+    assert units >= 5 * ctas and of == tiles, (units, ctas, of)
+    p = Prompts(lengths, hq, hkv, dim, kind, seed=dim + hq)
+    p.run(window, sinks)
+    p.check(window, sinks)
+    assert p.status.tolist() == [0] * len(lengths)
+    first = p.out.clone()
+    for _ in range(3):  # whichever CTA takes which unit
+        p.out.fill_(7.0)
+        p.run(window, sinks)
+        torch.cuda.synchronize()
+        assert torch.equal(first, p.out)
 
 
 NEIGHBOURS = [
