@@ -1,12 +1,12 @@
 """ss_attend_prompt where a CTA takes many units one after the other, and what rows that are none leave alone: against 64
-bits with the bounds of tests/test_gpu_kv_prompt.py, or bit for bit."""
+bits with the bounds of tests/test_gpu_kv_prompt.py, or bit for bit; and infinite keys."""
 import math
 
 import pytest
 
 torch = pytest.importorskip("torch")
 
-from tests.test_gpu_kv_prompt import Prompts, _i32  # noqa: E402
+from tests.test_gpu_kv_prompt import U, Prompts, _i32, reference  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +119,36 @@ def test_a_key_heads_queries_do_not_depend_on_the_next_ones(hq, dim, kind):
     p.run()
     torch.cuda.synchronize()
     assert torch.equal(out, p.out[:110, :38]) and torch.equal(lse, p.lse[:110, :38])
+
+
+@pytest.mark.parametrize("dim,kind", [(128, "bf16"), (64, "f16"), (256, "bf16")])
+def test_infinite_keys_weigh_nothing_or_everything(dim, kind):
+    """A first key whose scores are all -inf: as if it were not there, and its own token, which sees nothing else, gives zeros
+    and -inf.  Whose scores are +inf: no number for any that sees it."""
+    n0, n = 200, 100
+    p = Prompts([n0, n], 4, 2, dim, kind)
+    q = p.q[n0:n0 + n, 2:]
+    q[..., 5] = -q[..., 5].abs() - 0.1
+    p.k[n0, 1, 5] = math.inf
+    p.run()
+    torch.cuda.synchronize()
+    got, lse = p.out[n0:n0 + n, 2:].double(), p.lse[n0:n0 + n, 2:].double()
+    assert torch.all(got[0] == 0) and torch.all(lse[0] == -math.inf)
+    # without the key: token t of the rest sees the keys 1 .. t
+    k, v = p.k[n0 + 1:n0 + n, 1:].double(), p.v[n0 + 1:n0 + n, 1:].double()
+    want, want_lse, weighted, plain, size = reference(q[1:].double(), k, v, p.scale)
+    off = dim * 2.0 ** -23 * size + 2.0 ** -20
+    tol = U[kind] * want.abs() * (1 + 2.0 ** -10) + (U[kind] + 2 * off[..., None]) * weighted + 2.0 ** -25
+    if kind == "f16":
+        tol = tol + 2.0 ** -25 * plain
+    assert torch.all((got[1:] - want).abs() <= tol)
+    assert torch.all((lse[1:] - want_lse).abs() <= 2 * off + 2.0 ** -22 * want_lse.abs())
+    others = p.out[:n0 + n].clone()
+    q[..., 5] = -q[..., 5]
+    p.run()
+    torch.cuda.synchronize()
+    bad = ~torch.isfinite(p.out[:n0 + n].double())
+    expect = torch.zeros_like(bad)
+    expect[n0:, 2:] = True
+    assert torch.equal(bad, expect)
+    assert torch.equal(others[~expect], p.out[:n0 + n][~expect])
