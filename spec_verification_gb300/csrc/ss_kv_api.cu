@@ -75,7 +75,7 @@ cudaError_t configure(int device, const void* fn, size_t smem) {
     size_t smem;
   };
   static std::mutex mu;
-  static Done done[256];  // 36 kernels with at most a few sizes each; past that they are set again each time
+  static Done done[256];  // 50 kernels with at most a few sizes each; past that they are set again each time
   static int count = 0;
   const std::lock_guard<std::mutex> lock(mu);
   bool pages = false;
@@ -603,11 +603,13 @@ ss_status ss_attend_prompt(const ss_prompt_batch* b) {
   }
   P.staged = 32 % P.heads == 0;
   // Two tiles of query rows to a unit load keys half as often; one, two CTAs to an SM, hides the start and end of a unit
-  // behind the other's products.  Measured (us, 32/8 heads of 128, two / one): 16000 tokens 1170 / 1312, 16 x 2000 391 /
-  // 412, 50 x 500 141 / 152, 100 x 250 112.5 / 114.5, 4000 91.7 / 95.3; 1000 20.3 / 19.0, 300 11.7 / 10.3, 60 9.2 / 7.9,
-  // 200 x 60 51.5 / 48.4; 100 x 100 with 64/8 heads 89.7 / 80.1, with 16/16 44.4 / 34.6.  With 64 columns one was faster
-  // throughout (16000 tokens 1047 / 1001), with 256 two do not fit.
-  const bool few = (int64_t)P.max_tokens * c.q_heads <= 256ll * p->sms || P.max_tokens <= 200ll * b->B;
+  // behind the other's products.  Measured (us, two / one): 32/8 heads of 128, 16000 tokens 1190 / 1328, 16 x 2000 384 / 421,
+  // 4000 90.7 / 96.7; 1000 19.3 / 18.9, 300 12.3 / 11.5, 60 9.1 / 8.6.  200 prompts of 1 to twice as many tokens as stated:
+  // where rows leave by copy it is whole units that count, 32/8 heads 64 tokens 56 / 55, 96 81 / 84, 200 162 / 180; 64/8 20 tokens
+  // 45 / 41, 48 78 / 82; 16/8 200 tokens 105 / 103, 256 133 / 134; 16/16 256 tokens 173 / 161, 384 281 / 274; elsewhere 28/4 heads 128
+  // tokens 99 / 98, 200 154 / 156; 40/8 160 tokens 183 / 181, 256 292 / 299.  With 64 columns one was faster throughout when both were
+  // there (16000 tokens 1047 / 1001), with 256 two do not fit.
+  const bool few = (int64_t)P.max_tokens * c.q_heads <= 256ll * p->sms || P.max_tokens <= (P.staged ? 3ll * P.tokens : 200ll) * b->B;
   const ss::PromptKernel k = prompt_kernel(c, d == 128 && !few ? 2 : 1);
   P.next = static_cast<unsigned long long*>(b->workspace);
   P.ended = reinterpret_cast<uint32_t*>(P.next + 1);

@@ -29,11 +29,11 @@ def units_to_a_cta(lengths, hq, hkv, dim, spare=3):
         heads = -(-group // parts)
         filled = group * (128 // heads) // parts
         if filled > most:
-            most, tokens, chunks = filled, 128 // heads, parts
+            most, tokens, chunks, whole = filled, 128 // heads, parts, 32 % heads == 0
         if most >= 115:
             break
     total = sum(lengths) + spare
-    few = total * hq <= 256 * sms or total <= 200 * len(lengths)
+    few = total * hq <= 256 * sms or total <= (3 * tokens if whole else 200) * len(lengths)
     tiles = 2 if dim == 128 and not few else 1
     ctas = (2 if tiles == 1 and dim <= 128 else 1) * sms
     return sum(-(-n // (tiles * tokens)) for n in lengths) * hkv * chunks, ctas, tiles
