@@ -143,7 +143,10 @@ ss_status ss_kv_append(const ss_kv_pool* pool, const int32_t* cu_new, int32_t* s
 ss_status ss_kv_commit(const ss_kv_pool* pool, const int32_t* seq_len, const int32_t* counts, int32_t plus,
                        const int32_t* finished);
 
-/* New tokens' keys and values (rotated, as ss_rope_store writes them) and where they go. */
+/* New tokens' keys and values and where they go.  ss_rope_store rotates keys
+ * on their way into a cache without factors of blocks: a 16-bit cache of a
+ * second plan, with the slots 0, 1, .. for the call's tokens, gives them in
+ * order. */
 typedef struct {
   int32_t B;              /* rows of this call, 1 .. max_rows */
   int32_t tokens;         /* that k and v hold (those past max_tokens are not used); 0: nothing is done */
@@ -305,9 +308,12 @@ typedef struct {
 
 /* Causal attention of prompts over themselves, without a cache: a token sees
  * those of its own prompt up to itself, within the window or among the first
- * `sinks`; values in the plan's dtype, the rest as in ss_attend (the softmax
- * weights are rounded to the dtype before the product with the values).  The
- * plan's cache plays no part.  Keys and values that a token does not see never
+ * `sinks`; values in the plan's dtype, the rest as in ss_attend, but for the
+ * divisor: the softmax weights are rounded to the dtype before the product with
+ * the values, and the sum that divides is that before the rounding in both
+ * types (so the rounding of a weight that dominates its row stays: up to 2^-8
+ * of the output in bf16, 2^-11 in f16, beside the output's own).  The plan's
+ * cache plays no part.  Keys and values that a token does not see never
  * reach its result.  A prompt whose cu_seq passes tokens or max_tokens, or
  * decreases, is left out (SS_ST_CAPACITY).  Should a wait inside the kernel
  * run out (not expected), all prompts report SS_ST_COPY_TIMEOUT, and the

@@ -12,9 +12,9 @@
 // queries are read from shared memory for so few) and O += P V, the 128 threads
 // that weigh them about 1300, so two tiles of rows, or two CTAs, share an SM.
 // With 64 columns the weighing is the bound.  Measured (one prompt, causal):
-// 16000 tokens of 32/8 heads of 128 1191 us, 1.76 PFLOP/s (the library's matrix
-// product: 1.93, 1.74 sustained); 28/4 heads of 64 960 us, 0.96; 16/8 of 256
-// 1436 us, 1.46.
+// 16000 tokens of 32/8 heads of 128 1333 us, 1.57 PFLOP/s, called again and
+// again, 1190 us, 1.76, in bursts of a few (the library's matrix product: 1.74
+// and 1.93); in bursts 28/4 heads of 64 956 us, 0.96; 16/8 of 256 1440 us, 1.46.
 //
 // Query rows.  The heads that share a key head lie next to each other in a
 // tile: `heads` of them for each of `tokens` tokens (heads * tokens <= 128), so
